@@ -29,7 +29,11 @@
  *     (rx_rope, rx_kv_store_rope);
  *   - FP8 (E4M3) pools and their scatter (rx_kv_store_fp8);
  *   - the compressed finite-state machine of constrained decoding
- *     (rx_fsm_compress on the host, rx_fsm_step on the device).
+ *     (rx_fsm_compress on the host, rx_fsm_step on the device);
+ *   - the verification step of drafted tokens: norm of each q and k head with
+ *     the rotation and the scatter (rx_qk_norm_rope_store), attention of a
+ *     tree of drafted tokens (rx_tree_mask_build, rx_attn_tree), and
+ *     penalties, biases and grammar masks on the logits (rx_logits_process).
  *
  * Attention definition (all attention entry points).  For a query row of
  * request b at absolute position p, q-head h, with G = num_q_heads /
@@ -85,7 +89,10 @@ extern "C" {
 #define RX_DEV_FSM_DONE 8       /* rx_fsm_step: a request's state allows no
                                    token (its constrained text is complete)    */
 #define RX_DEV_BAD_STATE 16     /* rx_fsm_step: a state id outside the machine,
-                                   or a mask bit with no matching edge          */
+                                   or a mask bit with no matching edge;
+                                   rx_logits_process: a mask row that is not there */
+#define RX_DEV_BAD_TOKEN 32     /* rx_logits_process: a token id outside the
+                                   vocabulary, or biases not in ascending order */
 
 /* Message for the last failed call on this thread ("" if none). */
 const char *rx_last_error(void);
@@ -328,6 +335,46 @@ int rx_kv_store_rope_fp8(const rx_kv_pool_fp8 *pool, const void *k_new, const vo
                          const int32_t *slots, const int32_t *pos, int64_t n, double base, int32_t *dev_status,
                          void *stream);
 
+/* ---- norm of each q and k head, rotation and store (device) -------------
+ * Not from the pages.  Many models whose attention shapes the workloads take
+ * normalise every q and k head before the rotation.  One pass over a
+ * token's projected row does both and the slot scatter: for every q and k
+ * head x (head_dim values) of token i,
+ *     y  = x / sqrt(sum_c x[c]^2 / head_dim + eps) * w      (w: q_weight or
+ *          k_weight, one vector for all heads; NULL is all ones),
+ *     y' = y rotated to position pos[i] as rx_rope rotates,
+ * computed in fp32 (the angle as rx_rope reduces it) and rounded once:
+ * q_out[i] = bf16(y') for the q heads, K[slots[i]] = bf16(y') for the k
+ * heads, V[slots[i]] = v_new[i].
+ *   q: device bf16, token i's num_q_heads * head_dim values at q + i *
+ *   q_stride; k_new, v_new: the same at k_new + i * kv_stride, v_new + i *
+ *   kv_stride, num_kv_heads * head_dim values each; strides in elements,
+ *   multiples of 8 and at least the row's length.  So q, k and v may be the
+ *   three parts of one projected row (q_stride = kv_stride = (num_q_heads +
+ *   2 num_kv_heads) head_dim).
+ *   q_out: device bf16 [n, num_q_heads, head_dim]; it may be q itself when
+ *   q_stride = num_q_heads * head_dim, and must not overlap q, k_new or
+ *   v_new otherwise.
+ *   q_weight, k_weight: device bf16 [head_dim] or NULL; pos, slots: device
+ *   int32 [n]; slots distinct as in rx_kv_store.  All tensors 16-byte
+ *   aligned; num_q_heads may be 0 (then q and q_out are not read).
+ * head_dim 64 or 128; base > 1; eps >= 0.  A slot id outside the pool sets
+ * RX_DEV_BAD_SLOT and its K and V rows are not written (its q row is).  The
+ * squares are summed in fp32: a head whose squares sum past 3.4e38 (values
+ * above about 1e18) gives zeros, as a norm held in 32 bits does. */
+int rx_qk_norm_rope_store(const rx_kv_pool *pool, const void *q, int64_t q_stride, void *q_out,
+                          const void *k_new, const void *v_new, int64_t kv_stride, const void *q_weight,
+                          const void *k_weight, const int32_t *slots, const int32_t *pos, int64_t n,
+                          int32_t num_q_heads, double base, float eps, int32_t *dev_status, void *stream);
+
+/* The same into FP8 pools (8-byte aligned): K[slots[i]] = the E4M3 codes
+ * nearest y' / k_scale, straight from the fp32 value (rx_kv_store_rope_fp8
+ * rounds to bf16 first), V[slots[i]] = the codes rx_kv_store_fp8 stores. */
+int rx_qk_norm_rope_store_fp8(const rx_kv_pool_fp8 *pool, const void *q, int64_t q_stride, void *q_out,
+                              const void *k_new, const void *v_new, int64_t kv_stride, const void *q_weight,
+                              const void *k_weight, const int32_t *slots, const int32_t *pos, int64_t n,
+                              int32_t num_q_heads, double base, float eps, int32_t *dev_status, void *stream);
+
 /* Extend attention.  Request b (b < batch) has prefix_len[b] cached tokens and
  * extend_len[b] new ones whose K/V are already in the pool; the slot list is
  * req_to_token row req_idx[b], positions 0 .. prefix_len[b]+extend_len[b]-1.
@@ -548,6 +595,69 @@ int rx_attn_extend_fp8(const rx_kv_pool_fp8 *pool, const void *q, void *o, float
                        int64_t rtt_stride, int32_t batch, int32_t max_extend_len, void *workspace,
                        size_t ws_bytes, float sm_scale, int32_t *dev_status, void *stream);
 
+/* ---- attention of drafted trees (device) ---------------------------------
+ * Not from the pages.  Speculative decoding drafts several tokens per request
+ * and lets the model check all of them in one step: the drafted tokens form
+ * a tree (each follows one earlier drafted token or the text so far), and a
+ * token attends to the whole cached prefix and to its own ancestors.
+ *
+ * rx_tree_mask_build (host): the mask rows of one tree.  parent: host int32
+ * [n], parent[i] in -1 .. i-1 (-1: the token follows the text so far).
+ * out_mask: host uint32 [n][words], words >= ceil(n / 32): bit j % 32 of
+ * word j / 32 of row i is set when j is i or an ancestor of i.  out_depth:
+ * host int32 [n] or NULL, the number of ancestors of i (the token's position
+ * is prefix_len + out_depth[i]).  RX_ERR_INVALID (nothing written) for a
+ * parent out of range. */
+int rx_tree_mask_build(const int32_t *parent, int32_t n, int32_t words, uint32_t *out_mask, int32_t *out_depth);
+
+/* Tree attention.  Request b (b < batch) has prefix_len[b] >= 0 cached
+ * tokens and T_b = qo_indptr[b+1] - qo_indptr[b] drafted ones (0 .. max_tree_len)
+ * whose K/V are already in the pool (rx_qk_norm_rope_store,
+ * rx_kv_store...); the slot list is req_to_token row req_idx[b], the prefix
+ * at positions 0 .. prefix_len[b] - 1 and drafted token i at position
+ * prefix_len[b] + i.  With s and V as in the attention definition above,
+ * drafted token i sees every prefix position, and position prefix_len[b] + j
+ * where bit j of its mask row is set:
+ *     o   = sum over seen j of softmax(s)_j V_j,   lse = log(sum exp(s_j)).
+ * A token that sees nothing (no prefix, an empty mask row) gets o = 0 and
+ * lse = -inf.  A position a token does not see takes no part in its result,
+ * whatever K and V hold there (NaN and infinities among it).
+ *   q, o: device bf16 [qo_indptr[batch], num_q_heads, head_dim]; lse_or_null:
+ *   device fp32 [.., num_q_heads] or NULL; qo_indptr: device int32 [batch+1];
+ *   req_idx, prefix_len: device int32 [batch];
+ *   tree_mask: device uint32 [qo_indptr[batch]][mask_words], bits at or past
+ *   T_b ignored, mask_words >= ceil(max_tree_len / 32); or NULL (mask_words
+ *   ignored): token i sees the drafted tokens 0 .. i (a chain);
+ *   max_tree_len: host bound on T_b, 1 .. 1024;
+ *   workspace: device, >= rx_attn_tree_workspace(...) bytes, 256-byte
+ *   aligned, contents ignored on entry, not used by anything else until the
+ *   call's work on `stream` is done.
+ * Requires head_dim 64 or 128, num_q_heads % num_kv_heads == 0 and
+ * num_q_heads / num_kv_heads <= 128.  A request with T_b > max_tree_len or
+ * prefix_len[b] + T_b past the stride sets RX_DEV_BAD_LEN and its rows stay
+ * unwritten; a bad slot reads as zeros (RX_DEV_BAD_SLOT).  Rows behind
+ * qo_indptr[batch] are left as they were.  The lengths are read on the
+ * device, so a captured call serves later steps. */
+int rx_attn_tree(const rx_kv_pool *pool, const void *q, void *o, float *lse_or_null, int32_t num_q_heads,
+                 const int32_t *qo_indptr, const int32_t *req_idx, const int32_t *prefix_len,
+                 const uint32_t *tree_mask, int32_t mask_words, const int32_t *req_to_token,
+                 int64_t rtt_stride, int32_t batch, int32_t max_tree_len, void *workspace, size_t ws_bytes,
+                 float sm_scale, int32_t *dev_status, void *stream);
+
+/* Tree attention over FP8 pools: the same applied to the values E4M3(code) *
+ * scale, with the same arguments.  A pool's scale times sm_scale multiplies
+ * the scores, V's the output. */
+int rx_attn_tree_fp8(const rx_kv_pool_fp8 *pool, const void *q, void *o, float *lse_or_null,
+                     int32_t num_q_heads, const int32_t *qo_indptr, const int32_t *req_idx,
+                     const int32_t *prefix_len, const uint32_t *tree_mask, int32_t mask_words,
+                     const int32_t *req_to_token, int64_t rtt_stride, int32_t batch, int32_t max_tree_len,
+                     void *workspace, size_t ws_bytes, float sm_scale, int32_t *dev_status, void *stream);
+
+/* Workspace bytes for rx_attn_tree and rx_attn_tree_fp8; 0 on an invalid
+ * argument (rx_last_error says which).  It does not grow with the contexts. */
+size_t rx_attn_tree_workspace(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                              int32_t max_tree_len);
+
 /* ---- compressed finite-state machine (constrained decoding) -------------
  * Source: "SGLang: Efficient Execution of Structured Language Model
  * Programs" (unite.ai, es), "Introducción a SGLang", compressed-FSM bullet.
@@ -630,6 +740,65 @@ typedef struct {
 int rx_fsm_step(const rx_fsm *fsm, const float *logits, int64_t logits_stride, int32_t batch,
                 int32_t *state, int32_t *out_tokens, int32_t *out_count, uint64_t *workspace,
                 int32_t *dev_status, void *stream);
+
+/* ---- penalties, biases and grammar masks on logits (device) --------------
+ * Not from the pages.  What a server applies to the logits before it picks a
+ * token, for every request or, when a drafted tree is verified, for every
+ * drafted token.  Row r belongs to request b; with x = logits[r][t],
+ *     seen  = t is among the request's tokens (or, in a tree, on the row's path),
+ *     count = how often t is among the request's tokens behind its prompt,
+ *             plus, in a tree, on the row's path,
+ *     y = seen ? (x > 0 ? x / repetition[b] : x * repetition[b]) : x
+ *     y = y - frequency[b] * count
+ *     y = count > 0 ? y - presence[b] : y
+ *     y = y + the sum of b's biases of t, added up in list order
+ *     out[r][t] = t allowed by the row's mask ? y : -inf,
+ * every step rounded to fp32.  A row whose mask allows nothing is all -inf.
+ *
+ * Rows: without qo_indptr, row r is request r (n_req rows).  With it, rows
+ * qo_indptr[b] .. qo_indptr[b+1] - 1 are request b's drafted tokens, and the
+ * path of row r is the drafted tokens draft_tok[qo_indptr[b] + j] with bit j
+ * set in tree_mask row r (as rx_attn_tree reads them; at most 1024 a
+ * request, more sets RX_DEV_BAD_LEN and leaves the request's rows
+ * unwritten).  Rows behind the last are left as they were.
+ * All pointers are device memory.  NULL leaves a part out: hist (no request
+ * tokens), repetition (1), frequency and presence (0), bias_ptr, allow,
+ * draft_tok (no paths). */
+typedef struct {
+    int32_t n_req;
+    int32_t vocab;
+    const int32_t *hist;         /* the requests' tokens, prompt first: request b's at     */
+    const int64_t *hist_ptr;     /*   hist[hist_ptr[b] .. hist_ptr[b+1]);  [n_req + 1]     */
+    const int32_t *prompt_len;   /* [n_req] how many of them are the prompt; NULL: none    */
+    const float *repetition;     /* [n_req], > 0                                           */
+    const float *frequency;      /* [n_req]                                                */
+    const float *presence;       /* [n_req]                                                */
+    const int64_t *bias_ptr;     /* [n_req + 1]: request b's biases are entries            */
+    const int32_t *bias_tok;     /*   bias_ptr[b] .. bias_ptr[b+1], token ids ascending    */
+    const float *bias_val;       /*   (the same id may repeat: its values add up)          */
+    const int32_t *qo_indptr;    /* [n_req + 1] rows of each request, or NULL              */
+    const int32_t *draft_tok;    /* [rows] drafted tokens                                  */
+    const uint32_t *tree_mask;   /* [rows][tree_words]; NULL with draft_tok: a chain       */
+    int32_t tree_words;
+    int32_t n_allow;             /* mask rows                                              */
+    const uint32_t *allow;       /* [n_allow][ceil(vocab / 128) * 4], bit t % 32 of word   */
+                                 /*   t / 32: t is allowed (rx_fsm_compress's out_mask)    */
+    const int32_t *allow_row;    /* [rows] mask row of each logits row, -1: all allowed    */
+} rx_logits_rules;
+
+/* logits: device, fp32 (logits_bf16 = 0) or bf16 (1), rows of logits_stride
+ * elements (>= vocab); out: device fp32, rows of out_stride; out may be
+ * logits itself when that is fp32 with the same stride, and must not overlap
+ * it otherwise.  rows: an upper bound of the rows there are (the rows of
+ * logits and out); without qo_indptr exactly n_req.  A token id outside the
+ * vocabulary, in the history, a path or the biases, is left out and sets
+ * RX_DEV_BAD_TOKEN, as does a bias list that is not ascending (the ids out of
+ * order may then be left out); a mask row outside [-1, n_allow) sets
+ * RX_DEV_BAD_STATE and allows nothing.  Rows start at any element; those on
+ * 16-byte boundaries move in 16-byte pieces. */
+int rx_logits_process(const rx_logits_rules *rules, const void *logits, int32_t logits_bf16,
+                      int64_t logits_stride, float *out, int64_t out_stride, int32_t rows,
+                      int32_t *dev_status, void *stream);
 
 /* ---- failure paths, for tests -------------------------------------------
  * Not from the pages.  Two switches that let a test drive the library's

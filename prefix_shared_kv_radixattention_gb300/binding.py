@@ -40,6 +40,7 @@ RX_DEV_BAD_LEN = 2
 RX_DEV_TIMEOUT = 4
 RX_DEV_FSM_DONE = 8
 RX_DEV_BAD_STATE = 16
+RX_DEV_BAD_TOKEN = 32
 RX_PLAN_OPEN_END = -1
 
 
@@ -129,6 +130,24 @@ class FsmStruct(ctypes.Structure):
 _sig("rx_fsm_compress", ctypes.c_int, _I32, _I32, _P, _P, _P, _I32, _P, _P, _P, _P, _P, _P, _I64,
      ctypes.POINTER(FsmInfo))
 _sig("rx_fsm_step", ctypes.c_int, ctypes.POINTER(FsmStruct), _P, _I64, _I32, _P, _P, _P, _P, _P, _P)
+class LogitsRulesStruct(ctypes.Structure):
+    _fields_ = [("n_req", ctypes.c_int32), ("vocab", ctypes.c_int32), ("hist", _P), ("hist_ptr", _P),
+                ("prompt_len", _P), ("repetition", _P), ("frequency", _P), ("presence", _P), ("bias_ptr", _P),
+                ("bias_tok", _P), ("bias_val", _P), ("qo_indptr", _P), ("draft_tok", _P), ("tree_mask", _P),
+                ("tree_words", ctypes.c_int32), ("n_allow", ctypes.c_int32), ("allow", _P), ("allow_row", _P)]
+
+
+_sig("rx_logits_process", ctypes.c_int, ctypes.POINTER(LogitsRulesStruct), _P, _I32, _I64, _P, _I64, _I32, _P, _P)
+_sig("rx_qk_norm_rope_store", ctypes.c_int, ctypes.POINTER(KVPool), _P, _I64, _P, _P, _P, _I64, _P, _P, _P, _P, _I64,
+     _I32, ctypes.c_double, ctypes.c_float, _P, _P)
+_sig("rx_qk_norm_rope_store_fp8", ctypes.c_int, ctypes.POINTER(KVPoolFp8), _P, _I64, _P, _P, _P, _I64, _P, _P, _P, _P,
+     _I64, _I32, ctypes.c_double, ctypes.c_float, _P, _P)
+_sig("rx_tree_mask_build", ctypes.c_int, _P, _I32, _I32, _P, _P)
+_sig("rx_attn_tree", ctypes.c_int, ctypes.POINTER(KVPool), _P, _P, _P, _I32, _P, _P, _P, _P, _I32, _P, _I64, _I32, _I32,
+     _P, ctypes.c_size_t, ctypes.c_float, _P, _P)
+_sig("rx_attn_tree_fp8", ctypes.c_int, ctypes.POINTER(KVPoolFp8), _P, _P, _P, _I32, _P, _P, _P, _P, _I32, _P, _I64,
+     _I32, _I32, _P, ctypes.c_size_t, ctypes.c_float, _P, _P)
+_sig("rx_attn_tree_workspace", ctypes.c_size_t, _I32, _I32, _I32, _I32, _I32)
 _sig("rx_schedule", ctypes.c_int, _P, _P, _P, _I32, _I32, _P, _P)
 _sig("rx_kv_store", ctypes.c_int, ctypes.POINTER(KVPool), _P, _P, _P, _I64, _P, _P)
 _sig("rx_rope", ctypes.c_int, _P, _P, _I64, _I32, _I32, ctypes.c_double, _P)
@@ -750,3 +769,247 @@ def rx_attn_decode_fp8(k_pool, v_pool, k_scale: float, v_scale: float, q, o, lse
                                    _ptr(seq_len), _ptr(req_to_token), req_to_token.shape[1], req_idx.numel(),
                                    int(max_seq_len), pp, _ptr(workspace), ws_bytes, float(sm_scale),
                                    _ptr(dev_status), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# verification of drafted tokens: norm + rotation + store, tree attention,
+# logits
+# ---------------------------------------------------------------------------
+
+
+def _head_rows(t, name):
+    """A CUDA bf16 [n, heads, d] tensor whose rows (all heads of a token) are
+    contiguous; the rows themselves may be strided (a part of a projected
+    row).  Returns the row stride in elements."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name}: expected a CUDA tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
+    n, h, d = t.shape if t.dim() == 3 else (0, 0, 0)
+    if t.dim() != 3 or (n and ((d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d))):
+        raise ValueError(f"{name}: must be [n, heads, head_dim] with contiguous rows")
+    return t.stride(0) if n > 1 else h * d
+
+
+def _norm_args(k_pool, v_pool, q, q_out, k_new, v_new, q_weight, k_weight, slots, pos, dev_status):
+    torch = _torch()
+    qs = _head_rows(q, "q")
+    ks, vs = _head_rows(k_new, "k_new"), _head_rows(v_new, "v_new")
+    _dev(q_out, torch.bfloat16, "q_out")
+    _dev(q_weight, torch.bfloat16, "q_weight")
+    _dev(k_weight, torch.bfloat16, "k_weight")
+    _dev(slots, torch.int32, "slots")
+    _dev(pos, torch.int32, "pos")
+    _dev(dev_status, torch.int32, "dev_status")
+    S, hkv, d, L = _pool_dims(k_pool, v_pool, 0)
+    n = slots.numel()
+    if k_new.shape != (n, hkv, d) or v_new.shape != k_new.shape or pos.numel() != n:
+        raise ValueError("k_new/v_new must be [n, num_kv_heads, head_dim] and pos [n]")
+    if q.shape[0] != n or q.shape[2] != d or q_out.shape != q.shape:
+        raise ValueError("q and q_out must be [n, num_q_heads, head_dim]")
+    if ks != vs:
+        raise ValueError("k_new and v_new must have the same row stride")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None and w.numel() != d:
+            raise ValueError(f"{name} must be [head_dim]")
+    return qs, ks, n, S, hkv, d, L
+
+
+def rx_qk_norm_rope_store(k_pool, v_pool, q, q_out, k_new, v_new, q_weight, k_weight, slots, pos, base: float,
+                          eps: float, dev_status=None, stream=None, layer: int = 0) -> None:
+    """RMS norm of every q and k head (weights bf16 [d] or None), rotation to
+    pos, q into q_out, K and V into the pool.  q, k_new, v_new: bf16 [n,
+    heads, d], for example the three parts of one projected row."""
+    pool = make_pool(k_pool, v_pool, layer)
+    qs, ks, n, *_ = _norm_args(k_pool, v_pool, q, q_out, k_new, v_new, q_weight, k_weight, slots, pos, dev_status)
+    _check(_lib.rx_qk_norm_rope_store(ctypes.byref(pool), _ptr(q), qs, _ptr(q_out), _ptr(k_new), _ptr(v_new), ks,
+                                      _ptr(q_weight), _ptr(k_weight), _ptr(slots), _ptr(pos), n, q.shape[1],
+                                      float(base), float(eps), _ptr(dev_status), _stream(stream)))
+
+
+def rx_qk_norm_rope_store_fp8(k_pool, v_pool, k_scale: float, v_scale: float, q, q_out, k_new, v_new, q_weight,
+                              k_weight, slots, pos, base: float, eps: float, dev_status=None, stream=None,
+                              layer: int = 0) -> None:
+    """rx_qk_norm_rope_store into uint8 E4M3 pools ([L,] S, Hkv, d) with
+    per-pool scales."""
+    torch = _torch()
+    _dev(k_pool, torch.uint8, "k_pool")
+    _dev(v_pool, torch.uint8, "v_pool")
+    qs, ks, n, S, hkv, d, L = _norm_args(k_pool, v_pool, q, q_out, k_new, v_new, q_weight, k_weight, slots, pos,
+                                         dev_status)
+    pool = KVPoolFp8(k_pool.data_ptr(), v_pool.data_ptr(), S, hkv, d, float(k_scale), float(v_scale), L, int(layer))
+    _check(_lib.rx_qk_norm_rope_store_fp8(ctypes.byref(pool), _ptr(q), qs, _ptr(q_out), _ptr(k_new), _ptr(v_new), ks,
+                                          _ptr(q_weight), _ptr(k_weight), _ptr(slots), _ptr(pos), n, q.shape[1],
+                                          float(base), float(eps), _ptr(dev_status), _stream(stream)))
+
+
+def rx_tree_mask_build(parent, words: Optional[int] = None):
+    """(mask int32 [n, words], depth int32 [n]) of one drafted tree from its
+    nodes' parents (-1: the token follows the text so far); host arrays."""
+    p, pp = _np(parent, np.int32)
+    n = len(p)
+    words = (n + 31) // 32 if words is None else int(words)
+    mask = np.zeros((n, max(words, 0)), np.uint32)
+    depth = np.zeros(n, np.int32)
+    _check(_lib.rx_tree_mask_build(pp, n, words, mask.ctypes.data_as(_P), depth.ctypes.data_as(_P)))
+    return mask.view(np.int32), depth
+
+
+def rx_attn_tree_workspace(batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int, max_tree_len: int) -> int:
+    """Workspace bytes for rx_attn_tree and rx_attn_tree_fp8."""
+    n = _lib.rx_attn_tree_workspace(int(batch), int(num_q_heads), int(num_kv_heads), int(head_dim), int(max_tree_len))
+    if n == 0:
+        raise RxError(RX_ERR_INVALID, last_error())
+    return int(n)
+
+
+def _tree_args(q, o, lse, qo_indptr, req_idx, prefix_len, tree_mask, req_to_token, workspace, dev_status):
+    torch = _torch()
+    _dev(q, torch.bfloat16, "q")
+    _dev(o, torch.bfloat16, "o")
+    _dev(lse, torch.float32, "lse")
+    _dev(qo_indptr, torch.int32, "qo_indptr")
+    _dev(req_idx, torch.int32, "req_idx")
+    _dev(prefix_len, torch.int32, "prefix_len")
+    _dev(tree_mask, torch.int32, "tree_mask")
+    _dev(req_to_token, torch.int32, "req_to_token")
+    _dev(workspace, torch.uint8, "workspace")
+    _dev(dev_status, torch.int32, "dev_status")
+    if q.dim() != 3 or q.shape != o.shape:
+        raise ValueError("q and o must be [tokens, num_q_heads, head_dim]")
+    if lse is not None and lse.shape != q.shape[:2]:
+        raise ValueError("lse must be [tokens, num_q_heads]")
+    B = req_idx.numel()
+    if qo_indptr.numel() != B + 1 or prefix_len.numel() != B or req_to_token.dim() != 2:
+        raise ValueError("qo_indptr must be [batch + 1], prefix_len [batch] and req_to_token [requests, stride]")
+    if tree_mask is not None and (tree_mask.dim() != 2 or tree_mask.shape[0] != q.shape[0]):
+        raise ValueError("tree_mask must be [tokens, words]")
+    words = 0 if tree_mask is None else tree_mask.shape[1]
+    return words, B, 0 if workspace is None else workspace.numel()
+
+
+def rx_attn_tree(k_pool, v_pool, q, o, lse, qo_indptr, req_idx, prefix_len, tree_mask, req_to_token,
+                 max_tree_len: int, sm_scale: float, workspace, dev_status=None, stream=None, layer: int = 0) -> None:
+    """Attention of drafted trees: q, o bf16 [tokens, Hq, d], request b's
+    drafted tokens at rows qo_indptr[b] .. qo_indptr[b+1]; tree_mask int32
+    [tokens, words] (rx_tree_mask_build) or None for chains; workspace uint8
+    of rx_attn_tree_workspace(...) bytes."""
+    pool = make_pool(k_pool, v_pool, layer)
+    if q.dim() == 3 and q.shape[2] != pool.head_dim:
+        raise ValueError("q and the pools must have the same head_dim")
+    words, B, ws_bytes = _tree_args(q, o, lse, qo_indptr, req_idx, prefix_len, tree_mask, req_to_token, workspace,
+                                    dev_status)
+    _check(_lib.rx_attn_tree(ctypes.byref(pool), _ptr(q), _ptr(o), _ptr(lse), q.shape[1], _ptr(qo_indptr),
+                             _ptr(req_idx), _ptr(prefix_len), _ptr(tree_mask), words, _ptr(req_to_token),
+                             req_to_token.shape[1], B, int(max_tree_len), _ptr(workspace), ws_bytes, float(sm_scale),
+                             _ptr(dev_status), _stream(stream)))
+
+
+def rx_attn_tree_fp8(k_pool, v_pool, k_scale: float, v_scale: float, q, o, lse, qo_indptr, req_idx, prefix_len,
+                     tree_mask, req_to_token, max_tree_len: int, sm_scale: float, workspace, dev_status=None,
+                     stream=None, layer: int = 0) -> None:
+    """rx_attn_tree over uint8 E4M3 pools ([L,] S, Hkv, d) with per-pool scales."""
+    torch = _torch()
+    _dev(k_pool, torch.uint8, "k_pool")
+    _dev(v_pool, torch.uint8, "v_pool")
+    S, hkv, d, L = _pool_dims(k_pool, v_pool, layer)
+    if q.dim() == 3 and q.shape[2] != d:
+        raise ValueError("q and the pools must have the same head_dim")
+    words, B, ws_bytes = _tree_args(q, o, lse, qo_indptr, req_idx, prefix_len, tree_mask, req_to_token, workspace,
+                                    dev_status)
+    pool = KVPoolFp8(k_pool.data_ptr(), v_pool.data_ptr(), S, hkv, d, float(k_scale), float(v_scale), L, int(layer))
+    _check(_lib.rx_attn_tree_fp8(ctypes.byref(pool), _ptr(q), _ptr(o), _ptr(lse), q.shape[1], _ptr(qo_indptr),
+                                 _ptr(req_idx), _ptr(prefix_len), _ptr(tree_mask), words, _ptr(req_to_token),
+                                 req_to_token.shape[1], B, int(max_tree_len), _ptr(workspace), ws_bytes,
+                                 float(sm_scale), _ptr(dev_status), _stream(stream)))
+
+
+class LogitsRules:
+    """What rx_logits_process applies to a batch's logits (rx_logits_rules):
+    CUDA tensors, each optional, kept alive here.  Their contents may change
+    between calls (a longer history goes into the same tensors); their
+    sizes may not.
+
+    hist int32 [tokens], hist_ptr int64 [n_req + 1], prompt_len int32
+    [n_req]; repetition, frequency, presence fp32 [n_req]; bias_tok int32 and
+    bias_val fp32 [entries], bias_ptr int64 [n_req + 1]; for drafted trees
+    qo_indptr int32 [n_req + 1], draft_tok int32 [rows], tree_mask int32
+    [rows, words]; allow int32 [mask rows, ceil(vocab / 128) * 4] (Fsm.mask),
+    allow_row int32 [rows]."""
+
+    def __init__(self, n_req: int, vocab: int, hist=None, hist_ptr=None, prompt_len=None, repetition=None,
+                 frequency=None, presence=None, bias_tok=None, bias_val=None, bias_ptr=None, qo_indptr=None,
+                 draft_tok=None, tree_mask=None, allow=None, allow_row=None):
+        torch = _torch()
+        self.n_req, self.vocab = int(n_req), int(vocab)
+        i32, i64, f32 = torch.int32, torch.int64, torch.float32
+        want = (("hist", hist, i32, None), ("hist_ptr", hist_ptr, i64, n_req + 1), ("prompt_len", prompt_len, i32, n_req),
+                ("repetition", repetition, f32, n_req), ("frequency", frequency, f32, n_req),
+                ("presence", presence, f32, n_req), ("bias_tok", bias_tok, i32, None),
+                ("bias_val", bias_val, f32, None), ("bias_ptr", bias_ptr, i64, n_req + 1),
+                ("qo_indptr", qo_indptr, i32, n_req + 1), ("draft_tok", draft_tok, i32, None),
+                ("tree_mask", tree_mask, i32, None), ("allow", allow, i32, None), ("allow_row", allow_row, i32, None))
+        self._keep = []
+        for name, t, dt, size in want:
+            _dev(t, dt, name)
+            if t is not None and size is not None and t.numel() != size:
+                raise ValueError(f"LogitsRules: {name} must have {size} entries")
+            self._keep.append(t)
+        if (hist is None) != (hist_ptr is None):
+            raise ValueError("LogitsRules: hist and hist_ptr go together")
+        if len({bias_tok is None, bias_val is None, bias_ptr is None}) != 1 or \
+                (bias_tok is not None and bias_tok.numel() != bias_val.numel()):
+            raise ValueError("LogitsRules: bias_tok, bias_val and bias_ptr go together")
+        if (allow is None) != (allow_row is None):
+            raise ValueError("LogitsRules: allow and allow_row go together")
+        if draft_tok is not None and qo_indptr is None:
+            raise ValueError("LogitsRules: draft_tok needs qo_indptr")
+        if allow is not None and (allow.dim() != 2 or allow.shape[1] != (self.vocab + 127) // 128 * 4):
+            raise ValueError("LogitsRules: allow must be [mask rows, ceil(vocab / 128) * 4]")
+        if tree_mask is not None and tree_mask.dim() != 2:
+            raise ValueError("LogitsRules: tree_mask must be [rows, words]")
+        # rows the per-row tensors hold: rx_logits_process checks them against the logits
+        self.row_tensors = [t for t in (draft_tok, tree_mask, allow_row) if t is not None]
+        self.has_rows = qo_indptr is not None
+
+        def p(t):
+            return None if t is None or t.numel() == 0 else t.data_ptr()
+
+        empty = torch.zeros(1, dtype=i32, device="cuda") if any(t is not None and t.numel() == 0
+                                                                for t in (hist, bias_tok)) else None
+        if empty is not None:  # lists without entries still need an address
+            self._keep.append(empty)
+
+        def q(t):
+            return None if t is None else (t if t.numel() else empty).data_ptr()
+
+        self.struct = LogitsRulesStruct(self.n_req, self.vocab, q(hist), p(hist_ptr), p(prompt_len), p(repetition),
+                                        p(frequency), p(presence), p(bias_ptr), q(bias_tok), q(bias_val),
+                                        p(qo_indptr), p(draft_tok), p(tree_mask),
+                                        0 if tree_mask is None else tree_mask.shape[1],
+                                        0 if allow is None else allow.shape[0], p(allow), p(allow_row))
+
+
+def _logit_rows(t, name, vocab):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name}: expected a CUDA tensor")
+    if t.dim() != 2 or t.shape[1] < vocab or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: must be [rows, >= vocab] with contiguous rows")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), vocab)
+
+
+def rx_logits_process(rules: LogitsRules, logits, out, dev_status=None, stream=None) -> None:
+    """Penalties, biases and grammar masks: logits fp32 or bf16 [rows, >= V],
+    out fp32 [rows, >= V] (may be logits itself)."""
+    torch = _torch()
+    ls, os_ = _logit_rows(logits, "logits", rules.vocab), _logit_rows(out, "out", rules.vocab)
+    if logits.dtype not in (torch.float32, torch.bfloat16) or out.dtype != torch.float32:
+        raise TypeError("rx_logits_process: logits must be float32 or bfloat16, out float32")
+    _dev(dev_status, torch.int32, "dev_status")
+    rows = logits.shape[0]
+    if out.shape[0] != rows or any(t.shape[0] < rows for t in rules.row_tensors):
+        raise ValueError("rx_logits_process: logits, out, draft_tok, tree_mask and allow_row must have the same rows")
+    _check(_lib.rx_logits_process(ctypes.byref(rules.struct), _ptr(logits), int(logits.dtype == torch.bfloat16), ls,
+                                  _ptr(out), os_, rows, _ptr(dev_status), _stream(stream)))

@@ -437,6 +437,28 @@ extern "C" int rx_image_keys(const uint8_t *data, int64_t nbytes, int64_t n_toke
     return RX_OK;
 }
 
+// Mask rows of a drafted tree: a node sees itself and what its parent sees
+// (parents come before their children).
+extern "C" int rx_tree_mask_build(const int32_t *parent, int32_t n, int32_t words, uint32_t *out_mask,
+                                  int32_t *out_depth)
+{
+    if (n < 0 || words < 0 || (n > 0 && (!parent || !out_mask)) || (int64_t)words * 32 < n)
+        return rx_set_error(RX_ERR_INVALID, "rx_tree_mask_build: invalid argument");
+    for (int32_t i = 0; i < n; ++i)
+        if (parent[i] < -1 || parent[i] >= i)
+            return rx_set_error(RX_ERR_INVALID, "rx_tree_mask_build: parent %d of node %d", parent[i], i);
+    for (int32_t i = 0; i < n; ++i) {
+        uint32_t *row = out_mask + (int64_t)i * words;
+        if (parent[i] < 0)
+            std::memset(row, 0, (size_t)words * sizeof(uint32_t));
+        else
+            std::memcpy(row, out_mask + (int64_t)parent[i] * words, (size_t)words * sizeof(uint32_t));
+        row[i / 32] |= 1u << (i % 32);
+        if (out_depth) out_depth[i] = parent[i] < 0 ? 0 : out_depth[parent[i]] + 1;
+    }
+    return RX_OK;
+}
+
 extern "C" int rx_insert(rx_tree *tree, const int64_t *tokens, const int32_t *slots, int64_t n,
                          int64_t *out_already_cached)
 {
