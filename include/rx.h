@@ -645,8 +645,9 @@ int rx_attn_tree(const rx_kv_pool *pool, const void *q, void *o, float *lse_or_n
                  float sm_scale, int32_t *dev_status, void *stream);
 
 /* Tree attention over FP8 pools: the same applied to the values E4M3(code) *
- * scale, with the same arguments.  A pool's scale times sm_scale multiplies
- * the scores, V's the output. */
+ * scale, with the same arguments.  K's scale times sm_scale multiplies the
+ * scores, V's the output.  Pools 16-byte aligned (the other FP8 entry points
+ * take 8). */
 int rx_attn_tree_fp8(const rx_kv_pool_fp8 *pool, const void *q, void *o, float *lse_or_null,
                      int32_t num_q_heads, const int32_t *qo_indptr, const int32_t *req_idx,
                      const int32_t *prefix_len, const uint32_t *tree_mask, int32_t mask_words,

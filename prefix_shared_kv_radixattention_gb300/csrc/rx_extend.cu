@@ -48,10 +48,17 @@
 #include <type_traits>
 
 #include "rx_common.cuh"
+#include "rx_pipe.cuh"
 
 namespace {
 
 using bf16 = __nv_bfloat16;
+
+using rx::drain_wait;
+using rx::sw128;
+using rx::u2f;
+using rx::wait_or_abort;
+using rx::warp_wait;
 
 constexpr int kQT = 2;              // Q tiles per CTA
 constexpr int kRows = 128;          // query rows per Q tile (MMA M)
@@ -139,48 +146,6 @@ struct Tile {
     const int32_t *slots;
     int g;
 };
-
-// Bounded wait of one thread; false when it gave up (or another role did).
-__device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, volatile int *abort_flag,
-                                              int32_t *status)
-{
-    if (rx::mbar_test_wait(bar, parity)) return true;  // already flipped: no suspend
-    const long long t0 = clock64();
-    do {
-        if (rx::mbar_try_wait(bar, parity)) return true;
-        if (*abort_flag) return false;
-    } while (clock64() - t0 < rx::kWaitCycles);
-    *abort_flag = 1;
-    if (status) atomicOr(status, RX_DEV_TIMEOUT);
-    return false;
-}
-// The same for a whole warp, with one answer for all its lanes (the warp-wide
-// tcgen05.ld / st that follow need every lane).
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag,
-                                          int32_t *status)
-{
-    return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag, status));
-}
-
-// byte offset of 16-byte chunk c of row r in a 128-byte-swizzled K-major
-// tile whose 128-byte column blocks are blk bytes apart
-__device__ __forceinline__ uint32_t sw128(int r, int c, int blk)
-{
-    return (uint32_t)((c >> 3) * blk + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-}
-
-__device__ __forceinline__ float u2f(uint32_t u) { return __uint_as_float(u); }
-
-// Bounded wait that ignores the abort flag: used only to let copies already
-// issued finish landing before the CTA exits.
-__device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, int32_t *status)
-{
-    const long long t0 = clock64();
-    do {
-        if (rx::mbar_try_wait(bar, parity)) return;
-    } while (clock64() - t0 < rx::kWaitCycles);
-    if (status) atomicOr(status, RX_DEV_TIMEOUT);
-}
 
 // Eight E4M3 codes (element 0 in the low byte) as eight bf16: every E4M3
 // value, subnormals included, is exact in f16 and in bf16, so the widening

@@ -1,4 +1,5 @@
-// rx_tree.cu -- attention of drafted token trees over the slot pool.
+// rx_tree.cu -- attention of drafted token trees over the slot pool, on the
+// 5th-generation tensor cores (tcgen05.mma, accumulators in TMEM).
 //
 // Drafted token i of request b sees the request's whole prefix (positions
 // 0 .. P_b - 1) and, of the drafted tokens (positions P_b + j), those whose
@@ -6,26 +7,96 @@
 //     s_j = sm_scale q . K[slot_j],  o = sum_seen softmax(s)_j V[slot_j],
 //     lse = log sum_seen exp(s_j);   nothing seen: o = 0, lse = -inf.
 //
-// One warp per (drafted token, q head) walks the positions with a running
-// maximum and sum; each lane holds d / 32 of the head's values.
+// What bounds it: T drafted tokens times the G q heads of a kv head are a few
+// dozen to a few hundred query rows, fewer than the 280 or so flops a byte
+// that this GPU needs to be compute bound: the K and V rows' bytes are the
+// floor.  So:
+//
+//   - the rows of one kv head are one tensor-core tile of 128 rows (M), padded
+//     (an unused row costs nothing but its share of the MMA, which has time to
+//     spare), and every K/V tile of 128 positions is read once for all of them;
+//   - K/V rows are gathered through the slot list by eight producer warps with
+//     16-byte loads into registers and stores into the swizzled tile that the
+//     tensor core reads.  Rows of 256 bytes at random slots stream at 6.6 TB/s
+//     this way with 64 KB in flight an SM (2.9 TB/s as bulk copies, 2.8 TB/s
+//     through three warps of cp.async), so no copy of the context is needed
+//     first;
+//   - the work is cut evenly: the (kv head, request, row tile, position tile)
+//     units are one long list of which every CTA takes a contiguous share; a
+//     (kv head, request, row tile) cut by a CTA's end leaves fp32 partial
+//     results that a second kernel joins by the log-sum-exp identity.  The
+//     heads are outermost, so with 8 heads on 152 SMs nineteen CTAs walk each
+//     head in step and the rows of one slot are read at about the same time;
+//   - S = Q K^T goes to one of two TMEM buffers in turn, so that the tensor
+//     core works on the next tile while four softmax warps (one row a thread)
+//     turn this one into P, written over S and read from there by O += P V.
+//
+// All lengths are read on the device, by every CTA for itself: a scan of the
+// batch's lengths in shared memory finds its share.
 #include <math.h>
 
+#include <algorithm>
+#include <climits>
+
 #include "rx_common.cuh"
+#include "rx_pipe.cuh"
 
 namespace {
 
 using bf16 = __nv_bfloat16;
+using rx::sw128;
+using rx::u2f;
+using rx::wait_or_abort;
+using rx::warp_wait;
 
 constexpr int kMaxTree = 1024;
+constexpr int kCtas = 152;           // CTAs of a call: one an SM
+constexpr int kRows = 128;           // query rows of a tile (MMA M)
+constexpr int kBN = 128;             // positions of a K/V tile
+constexpr int kStages = 2;           // K ring and V ring depth
+constexpr int kProdWarps = 8;
+constexpr int kProdRows = kBN / kProdWarps;  // rows of a tile each producer warp gathers
+constexpr int kSoftWarps = 4;
+constexpr int kWarpQ = kSoftWarps + kProdWarps;      // loads the query rows
+constexpr int kWarpMma = kWarpQ + 1;
+constexpr int kThreads = 32 * (kWarpMma + 1);
+constexpr int kRing = 4;             // per-segment words kept this many segments (see nf, qscale)
+constexpr uint32_t kTmemCols = 512;  // buffer i: S (then P) at 256 i, O at 256 i + 128
+constexpr float kRescale = 8.f;      // log2 units the running max may lag
+constexpr int kMergeRows = 16;       // rows of one merge CTA
+constexpr int kMergeThreads = 128;
+
+template <int D>
+struct TL {
+    static constexpr int NB = D / 64;             // 128-byte column blocks of a row
+    static constexpr int BLK = kRows * 128;       // bytes of one column block of a tile
+    static constexpr int OFF_Q = 0;               // two buffers
+    static constexpr int OFF_K = OFF_Q + 2 * NB * BLK;
+    static constexpr int OFF_V = OFF_K + kStages * NB * BLK;
+    static constexpr int OFF_NF = OFF_V + kStages * NB * BLK;         // kRing x 32 words
+    static constexpr int OFF_QS = OFF_NF + kRing * 32 * 4;            // kRing x 128 floats
+    static constexpr int OFF_SCAN = OFF_QS + kRing * kRows * 4;       // kThreads + 1 int64
+    static constexpr int OFF_BAR = OFF_SCAN + (kThreads + 1) * 8;
+    static constexpr int B_KFULL = 0, B_KEMPTY = B_KFULL + kStages, B_VFULL = B_KEMPTY + kStages,
+                         B_VEMPTY = B_VFULL + kStages, B_QFULL = B_VEMPTY + kStages, B_QEMPTY = B_QFULL + 2,
+                         B_SFULL = B_QEMPTY + 2, B_PFULL = B_SFULL + 2, B_PVDONE = B_PFULL + 2,
+                         B_OEMPTY = B_PVDONE + 1, B_FINAL = B_OEMPTY + 2, N_BAR = B_FINAL + 1;
+    static constexpr int OFF_TMEM = OFF_BAR + N_BAR * 8;
+    static constexpr int OFF_ABORT = OFF_TMEM + 8;
+    static constexpr int OFF_START = OFF_ABORT + 8;                   // Cursor of the CTA's first unit
+    static constexpr int BYTES = OFF_START + 64 + 1024;               // + room to align the base to 1024
+};
+static_assert(TL<128>::BYTES <= 227 * 1024, "shared memory budget");
+static_assert(TL<128>::OFF_SCAN % 8 == 0 && TL<128>::OFF_BAR % 8 == 0, "alignment");
 
 struct TParams {
     const bf16 *q;
     bf16 *o;
     float *lse;
-    const void *k;
-    const void *v;
+    const unsigned char *k;
+    const unsigned char *v;
     int64_t num_slots;
-    int hq, hkv, G;
+    int hq, hkv, G, tb;     // tb: drafted tokens of a row tile, 128 / G
     const int32_t *qo_indptr;
     const int32_t *req_idx;
     const int32_t *prefix_len;
@@ -36,73 +107,759 @@ struct TParams {
     int batch, max_tree;
     float scale_log2;   // sm_scale log2(e), times K's scale for an FP8 pool
     float v_scale;      // V's scale for an FP8 pool; 1 otherwise
+    float *part_o;      // [2 kCtas][128][D] partial results, normalised
+    float *part_l;      // [2 kCtas][128] their log2-sum-exps
     int32_t *status;
 };
 
-template <bool F8>
-__device__ __forceinline__ float value(const void *pool, int64_t at)
+// ---------------------------------------------------------------------------
+// the list of work
+// ---------------------------------------------------------------------------
+
+struct Req {
+    int T, P;
+    int ntiles, nqt;  // 0 where there is nothing to do (no drafted token, or lengths out of range)
+
+    __device__ __forceinline__ int64_t units() const { return (int64_t)ntiles * nqt; }
+};
+
+__device__ __forceinline__ Req load_req(const TParams &p, int b, bool flag = false)
 {
-    if constexpr (F8) {
-        const uint32_t h = rx::e4m3x2_to_f16x2(__ldg(static_cast<const unsigned char *>(pool) + at));
-        return __half2float(__ushort_as_half((unsigned short)(h & 0xFFFFu)));
+    Req r;
+    r.T = __ldg(p.qo_indptr + b + 1) - __ldg(p.qo_indptr + b);
+    r.P = __ldg(p.prefix_len + b);
+    r.ntiles = r.nqt = 0;
+    if (r.T == 0) return r;
+    if (r.T < 0 || r.T > p.max_tree || r.P < 0 || (int64_t)r.P + r.T > p.rtt_stride) {
+        if (flag && p.status) atomicOr(p.status, RX_DEV_BAD_LEN);
+        return r;
+    }
+    r.ntiles = (int)(((int64_t)r.P + r.T + kBN - 1) / kBN);
+    r.nqt = (r.T + p.tb - 1) / p.tb;
+    return r;
+}
+
+// A place in the list: kv head g, request b, row tile qt, position tile j.
+struct Cursor {
+    int left;  // units of this CTA from here on
+    int g, b, qt, j;
+    Req r;
+
+    // position tiles of the segment (g, b, qt) that are this CTA's, from j on
+    __device__ __forceinline__ int end() const { return left < r.ntiles - j ? j + left : r.ntiles; }
+    // to the CTA's next segment; false when there is none
+    __device__ __forceinline__ bool next(const TParams &p)
+    {
+        left -= end() - j;
+        if (left <= 0) return false;
+        j = 0;
+        if (++qt < r.nqt) return true;
+        qt = 0;
+        do {
+            if (++b == p.batch) {
+                b = 0;
+                ++g;
+            }
+            r = load_req(p, b);
+        } while (r.ntiles == 0);
+        return true;
+    }
+};
+
+// Exclusive prefix sums of the requests' units, `per` requests a thread, into
+// pre[0 .. threads]; returns the total.  Whole block.
+template <int THREADS>
+__device__ int64_t scan_units(const TParams &p, int64_t *pre, int per, bool flag)
+{
+    __shared__ int64_t warp_tot[THREADS / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t sum = 0;
+    for (int i = 0; i < per; ++i) {
+        const int64_t b = (int64_t)threadIdx.x * per + i;
+        if (b < p.batch) sum += load_req(p, (int)b, flag).units();
+    }
+    int64_t x = sum;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+    }
+    if (lane == 31) warp_tot[warp] = x;
+    __syncthreads();
+    int64_t base = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) base += warp_tot[w];
+        total += warp_tot[w];
+    }
+    pre[threadIdx.x] = base + x - sum;
+    if (threadIdx.x == THREADS - 1) pre[THREADS] = total;
+    __syncthreads();
+    return total;
+}
+
+// The place of unit u (0 <= u < hkv * per_head).
+template <int THREADS>
+__device__ Cursor locate(const TParams &p, const int64_t *pre, int per, int64_t per_head, int64_t u)
+{
+    Cursor c;
+    c.left = 0;
+    c.g = (int)(u / per_head);
+    int64_t r = u - c.g * per_head;
+    int lo = 0, hi = THREADS - 1;  // the thread whose requests hold unit r
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (pre[mid] <= r) lo = mid; else hi = mid - 1;
+    }
+    r -= pre[lo];
+    c.b = lo * per;
+    for (c.r = load_req(p, c.b); r >= c.r.units(); c.r = load_req(p, c.b)) {
+        r -= c.r.units();
+        ++c.b;
+    }
+    c.qt = (int)(r / c.r.ntiles);
+    c.j = (int)(r - (int64_t)c.qt * c.r.ntiles);
+    return c;
+}
+
+// First unit of CTA c out of `ctas` (no more CTAs than units: none is empty).
+__device__ __forceinline__ int64_t first_unit(int64_t total, int ctas, int c) { return total * c / ctas; }
+
+// ---------------------------------------------------------------------------
+// which drafted tokens a row sees
+// ---------------------------------------------------------------------------
+
+// Word i of drafted token `node`'s mask: prefix positions (i < 0) are seen,
+// bits at and past T are not.
+__device__ __forceinline__ uint32_t mask_word(const TParams &p, const uint32_t *row, int node, int T, int i)
+{
+    if (i < 0) return 0xFFFFFFFFu;
+    int n = T - 32 * i;  // drafted tokens from bit 0 of this word on
+    if (n <= 0) return 0u;
+    uint32_t w;
+    if (row) {
+        w = __ldg(row + i);
     } else {
-        return __bfloat162float(static_cast<const bf16 *>(pool)[at]);
+        w = 0xFFFFFFFFu;
+        n = min(n, node + 1 - 32 * i);
+        if (n <= 0) return 0u;
+    }
+    return n >= 32 ? w : w & ((1u << n) - 1u);
+}
+
+// ---------------------------------------------------------------------------
+// producer warps
+// ---------------------------------------------------------------------------
+
+// Which halves of a word are NaN or infinite (bf16 / f16 pairs): 0xFFFF masks.
+template <bool F8>
+__device__ __forceinline__ uint32_t not_finite(uint32_t w)
+{
+    constexpr uint32_t E = F8 ? 0x7C00u : 0x7F80u;
+    return ((w & E) == E ? 0xFFFFu : 0u) | ((w & (E << 16)) == (E << 16) ? 0xFFFF0000u : 0u);
+}
+template <bool F8>
+__device__ __forceinline__ bool drop_not_finite(uint4 &x)
+{
+    const uint32_t a = not_finite<F8>(x.x), b = not_finite<F8>(x.y), c = not_finite<F8>(x.z), d = not_finite<F8>(x.w);
+    x = make_uint4(x.x & ~a, x.y & ~b, x.z & ~c, x.w & ~d);
+    return (a | b | c | d) != 0u;
+}
+
+// Eight E4M3 codes as eight f16 (exact).
+__device__ __forceinline__ uint4 widen_f16(uint32_t lo, uint32_t hi)
+{
+    return make_uint4(rx::e4m3x2_to_f16x2((uint16_t)lo), rx::e4m3x2_to_f16x2((uint16_t)(lo >> 16)),
+                      rx::e4m3x2_to_f16x2((uint16_t)hi), rx::e4m3x2_to_f16x2((uint16_t)(hi >> 16)));
+}
+
+// A producer warp gathers rows [16 w, 16 w + 16) of every K and V tile: the
+// loads of the next tile's K are issued as soon as this tile's K registers are
+// stored, V alike, so that 32 to 64 KB an SM are always in flight; slot ids
+// run two tiles ahead.
+template <int D, bool F8>
+__device__ void producer(const TParams &p, Cursor c, unsigned char *smem, uint32_t sbase)
+{
+    using L = TL<D>;
+    constexpr int EB = F8 ? 1 : 2;                    // bytes of a value
+    constexpr int CPR = D * EB / 16;                  // 16-byte chunks of a row
+    constexpr int RPI = 32 / CPR;                     // rows of one load instruction
+    constexpr int U = kProdRows / RPI;                // instructions for this warp's rows
+    const uint32_t bar = sbase + L::OFF_BAR;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
+    const int lane = threadIdx.x & 31, pw = (int)(threadIdx.x >> 5) - kSoftWarps;
+    const int r0 = pw * kProdRows;
+    const int sub = lane / CPR, ch = lane % CPR;
+    const int64_t row_bytes = (int64_t)p.hkv * D * EB;
+
+    struct Tile {
+        int32_t slot;  // lane l < 16: slot of row r0 + l, -1 past the end or outside the pool
+        int g, seg;
+        int rel;       // the tile's first position, from the first drafted one
+    };
+    int seg = 0;
+    bool more = true;
+    // the tile at the cursor, with its slot ids (flagged when outside the
+    // pool); then on to the next
+    auto take = [&](Tile &t) -> bool {
+        if (!more) return false;
+        t.g = c.g;
+        t.rel = c.j * kBN - c.r.P;
+        t.seg = seg % kRing;
+        t.slot = -1;
+        const int pos = c.j * kBN + r0 + lane;
+        if (lane < kProdRows && pos < c.r.P + c.r.T) {
+            const int32_t s = __ldg(p.rtt + (int64_t)__ldg(p.req_idx + c.b) * p.rtt_stride + pos);
+            if (s >= 0 && (int64_t)s < p.num_slots) t.slot = s;
+            else if (p.status) atomicOr(p.status, RX_DEV_BAD_SLOT);
+        }
+        ++c.j;
+        if (--c.left <= 0) {
+            more = false;
+        } else if (c.j == c.r.ntiles) {
+            c.j = c.r.ntiles - 1;  // next() counts the tile at j as the segment's last
+            ++c.left;
+            more = c.next(p);
+            ++seg;
+        }
+        return true;
+    };
+    auto load = [&](const unsigned char *pool, const Tile &t, uint4 (&x)[U]) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int32_t s = __shfl_sync(0xffffffffu, t.slot, u * RPI + sub);
+            x[u] = make_uint4(0, 0, 0, 0);
+            if (s >= 0) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(pool + (int64_t)s * row_bytes + (int64_t)t.g * (D * EB)) + ch;
+                x[u] = __ldg(src);
+            }
+        }
+    };
+    auto store = [&](uint32_t off, const Tile &t, uint4 (&x)[U], bool is_v) {
+        // drafted positions' V: a NaN or infinity would reach rows that do
+        // not see the position (0 * inf), so it is dropped here, noted, and
+        // added back to the rows that see it when their result is written
+        const bool check = is_v && t.rel + kBN > 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int r = r0 + u * RPI + sub;
+            unsigned char *tile = smem + off;
+            bool nf = false;
+            if constexpr (F8) {
+                uint4 a = widen_f16(x[u].x, x[u].y), b = widen_f16(x[u].z, x[u].w);
+                if (check && t.rel + r >= 0) {
+                    nf = drop_not_finite<true>(a);
+                    nf |= drop_not_finite<true>(b);
+                }
+                *reinterpret_cast<uint4 *>(tile + sw128(r, 2 * ch, L::BLK)) = a;
+                *reinterpret_cast<uint4 *>(tile + sw128(r, 2 * ch + 1, L::BLK)) = b;
+            } else {
+                if (check && t.rel + r >= 0) nf = drop_not_finite<false>(x[u]);
+                *reinterpret_cast<uint4 *>(tile + sw128(r, ch, L::BLK)) = x[u];
+            }
+            if (nf) {
+                const int e = t.rel + r;
+                atomicOr(reinterpret_cast<uint32_t *>(smem + L::OFF_NF) + t.seg * 32 + (e >> 5), 1u << (e & 31));
+            }
+        }
+        rx::fence_proxy_async_smem();
+        __syncwarp();
+    };
+
+    Tile cur, nxt, nx2;
+    uint4 kx[U], vx[U];
+    take(cur);
+    bool have1 = take(nxt);
+    load(p.k, cur, kx);
+    load(p.v, cur, vx);
+    for (int n = 0;; ++n) {
+        const int st = n % kStages;
+        const bool have2 = have1 && take(nx2);
+        if (n >= kStages && !warp_wait(bar + 8 * (L::B_KEMPTY + st), (n / kStages - 1) & 1, abort_flag, p.status)) return;
+        store(L::OFF_K + st * L::NB * L::BLK, cur, kx, false);
+        if (lane == 0) rx::mbar_arrive(bar + 8 * (L::B_KFULL + st));
+        if (have1) load(p.k, nxt, kx);
+        if (n >= kStages && !warp_wait(bar + 8 * (L::B_VEMPTY + st), (n / kStages - 1) & 1, abort_flag, p.status)) return;
+        store(L::OFF_V + st * L::NB * L::BLK, cur, vx, true);
+        if (lane == 0) rx::mbar_arrive(bar + 8 * (L::B_VFULL + st));
+        if (!have1) return;
+        load(p.v, nxt, vx);
+        cur = nxt;
+        nxt = nx2;
+        have1 = have2;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// query rows
+// ---------------------------------------------------------------------------
+
+// One warp copies each segment's query rows (row r: drafted token r / G of the
+// row tile, q head g G + r % G) into one of two buffers.  bf16 pools: 16-byte
+// async copies.  FP8 pools: the products run in f16, which holds every E4M3
+// value; a query row is brought to f16 times a power of two that puts its
+// largest value just below 2^15 (values 2^-29 of that and above stay exact),
+// and the power goes into the row's score scale.
+template <int D, bool F8>
+__device__ void query_loader(const TParams &p, Cursor c, unsigned char *smem, uint32_t sbase)
+{
+    using L = TL<D>;
+    constexpr int CPR = D / 8;
+    const uint32_t bar = sbase + L::OFF_BAR;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
+    const int lane = threadIdx.x & 31;
+    for (int s = 0;; ++s) {
+        const int buf = s & 1;
+        const int t0 = c.qt * p.tb, M = min(p.tb, c.r.T - t0) * p.G;
+        const int64_t tok0 = (int64_t)__ldg(p.qo_indptr + c.b) + t0;
+        if (s >= 2 && !warp_wait(bar + 8 * (L::B_QEMPTY + buf), ((s >> 1) - 1) & 1, abort_flag, p.status)) break;
+        const uint32_t dst = sbase + L::OFF_Q + buf * L::NB * L::BLK;
+        for (int i0 = 0; i0 < M * CPR; i0 += 32) {
+            const int i = i0 + lane, r = i / CPR, ch = i % CPR;
+            const bool in = i < M * CPR;
+            const bf16 *src = in ? p.q + ((tok0 + r / p.G) * p.hq + (int64_t)c.g * p.G + r % p.G) * D + ch * 8 : p.q;
+            if constexpr (!F8) {
+                if (in) rx::cp_async_16(dst + sw128(r, ch, L::BLK), src, 16);
+            } else {
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (in) x = __ldg(reinterpret_cast<const uint4 *>(src));
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                uint32_t top = 0;  // largest magnitude (bf16 bits) of the row
+#pragma unroll
+                for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
+#pragma unroll
+                for (int d = CPR / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+                const int e = max((int)(top >> 7) - 127, -100);
+                const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);  // 2^(14 - e)
+                uint32_t y[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    y[k] = rx::pack_f16(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xFFFF0000u) * up);
+                if (in) {
+                    *reinterpret_cast<uint4 *>(smem + (dst - sbase) + sw128(r, ch, L::BLK)) = make_uint4(y[0], y[1], y[2], y[3]);
+                    if (ch == 0)
+                        reinterpret_cast<float *>(smem + L::OFF_QS)[(s % kRing) * kRows + r] =
+                            __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+                }
+            }
+        }
+        if constexpr (F8) {
+            rx::fence_proxy_async_smem();
+            rx::mbar_arrive(bar + 8 * (L::B_QFULL + buf));
+        } else {
+            rx::cp_async_mbar_arrive(bar + 8 * (L::B_QFULL + buf));
+        }
+        if (!c.next(p)) break;
+    }
+    rx::cp_async_wait_all();
+}
+
+// ---------------------------------------------------------------------------
+// MMA thread
+// ---------------------------------------------------------------------------
+
+// Over the CTA's tiles n = 0, 1, ... (all segments in a row): S(n) into buffer
+// n & 1, then O += P V of tile n - 1.  P(n - 2) sits in the buffer that S(n)
+// overwrites, so S(n) waits for that product's completion.
+template <int D, bool F8>
+__device__ void mma_issuer(const TParams &p, Cursor c, unsigned char *smem, uint32_t sbase, uint32_t tmem)
+{
+    using L = TL<D>;
+    const uint32_t bar = sbase + L::OFF_BAR;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
+    constexpr uint32_t idesc_qk = F8 ? rx::idesc_f16(kRows, kBN, false, false) : rx::idesc_bf16(kRows, kBN, false, false);
+    constexpr uint32_t idesc_pv = F8 ? rx::idesc_f16(kRows, D, false, true) : rx::idesc_bf16(kRows, D, false, true);
+    auto wait = [&](int b, uint32_t parity) { return wait_or_abort(bar + 8 * b, parity, abort_flag, p.status); };
+    const uint64_t dq = rx::sdesc_sw128(sbase + L::OFF_Q, 16, 1024);
+    const uint64_t dk = rx::sdesc_sw128(sbase + L::OFF_K, 16, 1024);
+    const uint64_t dv = rx::sdesc_sw128(sbase + L::OFF_V, L::BLK, 1024);
+
+    auto issue_s = [&](int n, int s, bool first, bool last) -> bool {
+        const int st = n % kStages, buf = n & 1;
+        if (first && !wait(L::B_QFULL + (s & 1), (s >> 1) & 1)) return false;
+        if (!wait(L::B_KFULL + st, (n / kStages) & 1)) return false;
+        if (n >= 2 && !wait(L::B_PVDONE, n & 1)) return false;  // O += P V of tile n - 2 (same parity)
+        rx::fence_proxy_async_smem();  // query rows landed by cp.async -> async proxy
+        rx::tc_fence_after();
+        const uint64_t dks = dk + (uint64_t)((st * L::NB * L::BLK) >> 4);
+        const uint64_t dqs = dq + (uint64_t)(((s & 1) * L::NB * L::BLK) >> 4);
+#pragma unroll
+        for (int kb = 0; kb < D / 16; ++kb) {
+            const uint64_t off = (uint64_t)(((kb >> 2) * L::BLK + (kb & 3) * 32) >> 4);
+            rx::tc_mma(tmem + buf * 256, dqs + off, dks + off, idesc_qk, kb > 0);
+        }
+        rx::tc_commit(bar + 8 * (L::B_SFULL + buf));
+        rx::tc_commit(bar + 8 * (L::B_KEMPTY + st));
+        if (last) rx::tc_commit(bar + 8 * (L::B_QEMPTY + (s & 1)));
+        return true;
+    };
+    auto issue_pv = [&](int n, int s, bool first) -> bool {
+        const int st = n % kStages, buf = n & 1;
+        if (!wait(L::B_PFULL + buf, (n >> 1) & 1)) return false;
+        if (!wait(L::B_VFULL + st, (n / kStages) & 1)) return false;
+        if (first && s >= 2 && !wait(L::B_OEMPTY + (s & 1), ((s >> 1) - 1) & 1)) return false;
+        rx::tc_fence_after();
+        const uint64_t dvs = dv + (uint64_t)((st * L::NB * L::BLK) >> 4);
+#pragma unroll
+        for (int ks = 0; ks < kBN / 16; ++ks)
+            rx::tc_mma_ts(tmem + (s & 1) * 256 + 128, tmem + buf * 256 + ks * 8, dvs + (uint64_t)((ks * 16 * 128) >> 4),
+                          idesc_pv, (!first || ks > 0) ? 1u : 0u);
+        rx::tc_commit(bar + 8 * L::B_PVDONE);
+        rx::tc_commit(bar + 8 * (L::B_VEMPTY + st));
+        return true;
+    };
+    bool ok = true, prev_first = false;
+    int n = 0, prev_s = 0;
+    for (int s = 0; ok; ++s) {
+        const int j0 = c.j, j1 = c.end();
+        for (int j = j0; j < j1 && ok; ++j, ++n) {
+            ok = issue_s(n, s, j == j0, j == j1 - 1);
+            if (ok && n > 0) ok = issue_pv(n - 1, prev_s, prev_first);
+            prev_s = s;
+            prev_first = j == j0;
+        }
+        if (!ok || !c.next(p)) break;
+    }
+    if (ok) issue_pv(n - 1, prev_s, prev_first);
+    // everything issued has finished before TMEM is released
+    rx::tc_commit(bar + 8 * L::B_FINAL);
+    rx::drain_wait(bar + 8 * L::B_FINAL, 0, p.status);
+}
+
+// ---------------------------------------------------------------------------
+// softmax warps: one query row per thread
+// ---------------------------------------------------------------------------
+
+// The NaN and infinities of V at drafted positions that a row sees, added to
+// its written result: o (part < 0) or the partial row `part`.
+template <int D, bool F8>
+__device__ __noinline__ void add_not_finite(const TParams &p, const uint32_t *nf, const uint32_t *mrow, int node,
+                                            const Cursor &c, int64_t part, int64_t orow)
+{
+    for (int w = 0; w < (c.r.T + 31) / 32; ++w)
+        for (uint32_t bad = nf[w] & mask_word(p, mrow, node, c.r.T, w); bad; bad &= bad - 1) {
+            const int pos = c.r.P + 32 * w + __ffs(bad) - 1;
+            const int64_t slot = __ldg(p.rtt + (int64_t)__ldg(p.req_idx + c.b) * p.rtt_stride + pos);
+            const int64_t at = (slot * p.hkv + c.g) * D;
+            for (int i = 0; i < D; ++i) {
+                float v;
+                if constexpr (F8) {
+                    const uint32_t h = rx::e4m3x2_to_f16x2(__ldg(p.v + at + i));
+                    v = __half2float(__ushort_as_half((unsigned short)(h & 0xFFFFu)));
+                } else {
+                    v = __bfloat162float(reinterpret_cast<const bf16 *>(p.v)[at + i]);
+                }
+                if (isfinite(v)) continue;
+                if (part >= 0) p.part_o[part * D + i] += v;
+                else p.o[orow * D + i] = __float2bfloat16_rn(__bfloat162float(p.o[orow * D + i]) + v);
+            }
+        }
+}
+
+template <int D, bool F8>
+__device__ void softmax_rows(const TParams &p, Cursor c, unsigned char *smem, uint32_t sbase, uint32_t tmem)
+{
+    using L = TL<D>;
+    const uint32_t bar = sbase + L::OFF_BAR;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
+    const int row = threadIdx.x;                       // = TMEM lane
+    const uint32_t lanes = (uint32_t)(row & ~31) << 16;
+    int n = 0;
+    for (int s = 0;; ++s) {
+        const int j0 = c.j, j1 = c.end(), P = c.r.P, T = c.r.T;
+        const int t0 = c.qt * p.tb, M = min(p.tb, T - t0) * p.G;
+        const bool valid = row < M, warp_on = (row & ~31) < M;
+        const int node = t0 + row / p.G;
+        const int64_t tok = (int64_t)__ldg(p.qo_indptr + c.b) + node;
+        const uint32_t *mrow = p.mask && valid ? p.mask + tok * p.words : nullptr;
+        float m_used = -INFINITY, l = 0.f, sl2 = p.scale_log2;
+        for (int j = j0; j < j1; ++j, ++n) {
+            const int buf = n & 1;
+            const uint32_t tS = tmem + buf * 256 + lanes, tO = tmem + (s & 1) * 256 + 128 + lanes;
+            if (!warp_wait(bar + 8 * (L::B_SFULL + buf), (n >> 1) & 1, abort_flag, p.status)) return;
+            rx::tc_fence_after();
+            if (warp_on) {
+                if (F8 && j == j0) sl2 = p.scale_log2 * reinterpret_cast<const float *>(smem + L::OFF_QS)[(s % kRing) * kRows + row];
+                const int kbase = j * kBN;
+                const bool masked = kbase + kBN > P;   // drafted positions, or past the last
+                uint32_t bits[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
+                if (masked) {
+                    const int off = kbase - P, w0 = off >> 5;
+                    uint32_t lo = mask_word(p, mrow, node, T, w0);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t hi = mask_word(p, mrow, node, T, w0 + k + 1);
+                        bits[k] = __funnelshift_r(lo, hi, off & 31);
+                        lo = hi;
+                    }
+                }
+                auto scores = [&](int k, uint32_t (&sv)[32]) {
+                    rx::tmem_ld32(tS + k * 32, sv);
+                    rx::tmem_wait_ld();
+                    if (masked) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!((bits[k] >> i) & 1u)) sv[i] = 0xFF800000u;  // -inf
+                    }
+                };
+                float mx = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < kBN / 32; ++k) {
+                    uint32_t sv[32];
+                    scores(k, sv);
+                    float a0 = mx, a1 = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        a0 = rx::fmax3(a0, u2f(sv[4 * i]), u2f(sv[4 * i + 1]));
+                        a1 = rx::fmax3(a1, u2f(sv[4 * i + 2]), u2f(sv[4 * i + 3]));
+                    }
+                    mx = fmaxf(a0, a1);
+                }
+                const float m_new = fmaxf(m_used, mx * sl2);
+                const bool need = valid && (m_used == -INFINITY || m_new > m_used + kRescale);
+                const bool scale_o = need && m_used != -INFINITY;
+                const float alpha = scale_o ? rx::fast_exp2(m_used - m_new) : 1.f;
+                if (need) {
+                    l *= alpha;
+                    m_used = m_new;
+                }
+                const float mu = m_used == -INFINITY ? 0.f : m_used;
+                const uint64_t scale2 = rx::f2(sl2, sl2), negm2 = rx::f2(-mu, -mu);
+                uint64_t acc0 = 0, acc1 = 0;
+#pragma unroll
+                for (int k = 0; k < kBN / 32; ++k) {
+                    uint32_t sv[32], pk[16];
+                    scores(k, sv);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float x0, x1;
+                        rx::f2_split(rx::f2_fma(rx::f2(u2f(sv[2 * i]), u2f(sv[2 * i + 1])), scale2, negm2), x0, x1);
+                        const float e0 = rx::fast_exp2(x0), e1 = rx::fast_exp2(x1);
+                        if (i & 1) acc1 = rx::f2_add(acc1, rx::f2(e0, e1));
+                        else acc0 = rx::f2_add(acc0, rx::f2(e0, e1));
+                        // the weights are rounded to the type of V's tile for
+                        // the tensor core; their sum is not
+                        pk[i] = F8 ? rx::pack_f16(e0, e1) : rx::pack_bf16(e0, e1);
+                    }
+                    rx::tmem_st16(tS + k * 16, pk);  // over scores already read
+                }
+                float a0, a1;
+                rx::f2_split(rx::f2_add(acc0, acc1), a0, a1);
+                l += a0 + a1;
+                if (__any_sync(0xffffffffu, scale_o)) {
+                    // O += P V of the tile before has to be complete
+                    if (!warp_wait(bar + 8 * L::B_PVDONE, (n - 1) & 1, abort_flag, p.status)) return;
+                    rx::tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < D / 32; ++k) {
+                        uint32_t r[32];
+                        rx::tmem_ld32(tO + k * 32, r);
+                        rx::tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(u2f(r[i]) * alpha);
+                        rx::tmem_st32(tO + k * 32, r);
+                    }
+                }
+                rx::tmem_wait_st();
+            }
+            rx::tc_fence_before();
+            rx::mbar_arrive(bar + 8 * (L::B_PFULL + buf));
+        }
+        // the segment's result
+        const uint32_t tO = tmem + (s & 1) * 256 + 128 + lanes;
+        if (!warp_wait(bar + 8 * L::B_PVDONE, (n - 1) & 1, abort_flag, p.status)) return;
+        rx::tc_fence_after();
+        uint32_t *nf = reinterpret_cast<uint32_t *>(smem + L::OFF_NF) + (s % kRing) * 32;
+        uint32_t any = 0;
+        if (j1 * kBN > P)
+            for (int i = 0; i < (T + 31) / 32; ++i) any |= nf[i];
+        const bool whole = j0 == 0 && j1 == c.r.ntiles;
+        const float inv = l == 0.f ? 0.f : p.v_scale / l;
+        const int64_t orow = tok * p.hq + (int64_t)c.g * p.G + row % p.G;
+        const int64_t prow = (int64_t)(2 * blockIdx.x + (j0 == 0 ? 1 : 0)) * kRows + row;
+        if (warp_on) {
+#pragma unroll
+            for (int k = 0; k < D / 32; ++k) {
+                uint32_t r[32];
+                rx::tmem_ld32(tO + k * 32, r);
+                rx::tmem_wait_ld();
+                if (valid) {
+                    float x[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) x[i] = l == 0.f ? 0.f : u2f(r[i]) * inv;
+                    if (whole) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(p.o + orow * D + k * 32);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            dst[i] = make_uint4(rx::pack_bf16(x[8 * i], x[8 * i + 1]), rx::pack_bf16(x[8 * i + 2], x[8 * i + 3]),
+                                                rx::pack_bf16(x[8 * i + 4], x[8 * i + 5]), rx::pack_bf16(x[8 * i + 6], x[8 * i + 7]));
+                    } else {
+                        float4 *dst = reinterpret_cast<float4 *>(p.part_o + prow * D + k * 32);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                    }
+                }
+                __syncwarp();
+            }
+            if (valid) {
+                const float l2 = l == 0.f ? -INFINITY : m_used + log2f(l);
+                if (!whole) p.part_l[prow] = l2;
+                else if (p.lse) p.lse[orow] = l2 * rx::kLn2;
+            }
+        }
+        if (any) {  // the same for every thread: all have read the words, then they are cleared
+            if (valid) add_not_finite<D, F8>(p, nf, mrow, node, c, whole ? -1 : prow, orow);
+            rx::named_bar_sync(1, 32 * kSoftWarps);
+            if (row < 32) nf[row] = 0;
+        }
+        rx::tc_fence_before();
+        rx::mbar_arrive(bar + 8 * (L::B_OEMPTY + (s & 1)));
+        if (!c.next(p)) return;
     }
 }
 
 template <int D, bool F8>
-__global__ void __launch_bounds__(128) tree_warp_kernel(const TParams p)
+__global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant__ TParams p)
 {
-    constexpr int PER = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int b = blockIdx.y;
-    const int t0 = __ldg(p.qo_indptr + b), T = __ldg(p.qo_indptr + b + 1) - t0;
-    const int64_t P = __ldg(p.prefix_len + b);
-    if (T == 0) return;
-    if (T < 0 || T > p.max_tree || P < 0 || P + T > p.rtt_stride) {
+    using L = TL<D>;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    const uint32_t raw = rx::smem_u32(smem_raw);
+    unsigned char *smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);  // 1024-aligned swizzle atoms
+    const uint32_t sbase = rx::smem_u32(smem);
+    const uint32_t bar = sbase + L::OFF_BAR;
+    const int warp = threadIdx.x >> 5;
+    rx::pdl_launch_dependents();  // the merge kernel may launch and wait on the device
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            rx::mbar_init(bar + 8 * (L::B_KFULL + i), kProdWarps);
+            rx::mbar_init(bar + 8 * (L::B_VFULL + i), kProdWarps);
+            rx::mbar_init(bar + 8 * (L::B_KEMPTY + i), 1);
+            rx::mbar_init(bar + 8 * (L::B_VEMPTY + i), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            rx::mbar_init(bar + 8 * (L::B_QFULL + i), 32);
+            rx::mbar_init(bar + 8 * (L::B_QEMPTY + i), 1);
+            rx::mbar_init(bar + 8 * (L::B_SFULL + i), 1);
+            rx::mbar_init(bar + 8 * (L::B_PFULL + i), 32 * kSoftWarps);
+            rx::mbar_init(bar + 8 * (L::B_OEMPTY + i), 32 * kSoftWarps);
+        }
+        rx::mbar_init(bar + 8 * L::B_PVDONE, 1);
+        rx::mbar_init(bar + 8 * L::B_FINAL, 1);
+        *reinterpret_cast<volatile int *>(smem + L::OFF_ABORT) = 0;
+        rx::fence_mbar_init();
+    }
+    for (int i = threadIdx.x; i < kRing * 32; i += kThreads) reinterpret_cast<uint32_t *>(smem + L::OFF_NF)[i] = 0;
+    int64_t *pre = reinterpret_cast<int64_t *>(smem + L::OFF_SCAN);
+    const int per = (p.batch + kThreads - 1) / kThreads;
+    const int64_t per_head = scan_units<kThreads>(p, pre, per, blockIdx.x == 0);
+    const int64_t total = per_head * p.hkv;
+    const int ctas = (int)min((int64_t)gridDim.x, total);
+    if ((int)blockIdx.x >= ctas) return;
+    if (total / ctas >= INT_MAX) {  // lengths of no real pool
         if (p.status && threadIdx.x == 0) atomicOr(p.status, RX_DEV_BAD_LEN);
         return;
     }
-    const int w = (int)((blockIdx.x * blockDim.x + threadIdx.x) >> 5);
-    const int i = w / p.hq, h = w - i * p.hq;
-    if (i >= T) return;
-    const int g = h / p.G;
-    const int32_t *slots = p.rtt + (int64_t)__ldg(p.req_idx + b) * p.rtt_stride;
-    const int64_t row = ((int64_t)(t0 + i) * p.hq + h) * D;
-    float q[PER], o[PER];
-#pragma unroll
-    for (int c = 0; c < PER; ++c) {
-        q[c] = __bfloat162float(p.q[row + c * 32 + lane]);
-        o[c] = 0.f;
+    static_assert(sizeof(Cursor) <= 64, "the start cursor's room");
+    if (threadIdx.x == 0) {
+        const int64_t u0 = first_unit(total, ctas, blockIdx.x);
+        Cursor c = locate<kThreads>(p, pre, per, per_head, u0);
+        c.left = (int)(first_unit(total, ctas, blockIdx.x + 1) - u0);
+        *reinterpret_cast<Cursor *>(smem + L::OFF_START) = c;
     }
-    float m = -INFINITY, l = 0.f;
-    for (int64_t j = 0; j < P + T; ++j) {
-        if (j >= P) {
-            const int e = (int)(j - P);
-            const bool see = p.mask ? (__ldg(p.mask + (int64_t)(t0 + i) * p.words + (e >> 5)) >> (e & 31)) & 1u : e <= i;
-            if (!see) continue;
-        }
-        const int32_t s = __ldg(slots + j);
-        const bool ok = s >= 0 && (int64_t)s < p.num_slots;
-        if (!ok && p.status && lane == 0) atomicOr(p.status, RX_DEV_BAD_SLOT);
-        const int64_t at = ((int64_t)(ok ? s : 0) * p.hkv + g) * D + lane;
-        float x = 0.f;
-#pragma unroll
-        for (int c = 0; c < PER; ++c) x = fmaf(q[c], ok ? value<F8>(p.k, at + c * 32) : 0.f, x);
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-        x *= p.scale_log2;
-        const float mn = fmaxf(m, x), a = m == -INFINITY ? 0.f : exp2f(m - mn), e = exp2f(x - mn);
-        l = l * a + e;
-#pragma unroll
-        for (int c = 0; c < PER; ++c) o[c] = o[c] * a + e * (ok ? value<F8>(p.v, at + c * 32) : 0.f);
-        m = mn;
+    if (warp == kWarpMma) rx::tmem_alloc(sbase + L::OFF_TMEM, kTmemCols);
+    rx::tc_fence_before();
+    __syncthreads();
+    rx::tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::OFF_TMEM);
+    const Cursor c = *reinterpret_cast<const Cursor *>(smem + L::OFF_START);
+
+    if (warp < kSoftWarps) {
+        softmax_rows<D, F8>(p, c, smem, sbase, tmem);
+    } else if (warp < kWarpQ) {
+        producer<D, F8>(p, c, smem, sbase);
+    } else if (warp == kWarpQ) {
+        query_loader<D, F8>(p, c, smem, sbase);
+    } else {
+        if ((threadIdx.x & 31) == 0) mma_issuer<D, F8>(p, c, smem, sbase, tmem);
+        __syncwarp();
     }
-    const float inv = l == 0.f ? 0.f : p.v_scale / l;
-#pragma unroll
-    for (int c = 0; c < PER; ++c) p.o[row + c * 32 + lane] = __float2bfloat16_rn(o[c] * inv);
-    if (p.lse && lane == 0) p.lse[row / D] = l == 0.f ? -INFINITY : (m + log2f(l)) * rx::kLn2;
+    rx::tc_fence_before();
+    __syncthreads();
+    if (warp == kWarpMma) {
+        rx::tc_fence_after();
+        rx::tmem_dealloc(tmem, kTmemCols);
+    }
 }
+
+// ---------------------------------------------------------------------------
+// joining the partial results
+// ---------------------------------------------------------------------------
+
+// The (kv head, request, row tile) that the boundary between CTAs x and x + 1
+// cuts, x = blockIdx.x, when it is the first boundary inside: its parts are
+// CTA x's last segment (slot 1) and the first segments (slot 0) of the CTAs
+// after it, as far as it reaches.  One warp a row: with m the largest
+// log2-sum-exp, w = 2^(l - m): o = sum w o / sum w.  kMergeRows rows a CTA.
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ TParams p, int main_ctas)
+{
+    __shared__ int64_t pre[kMergeThreads + 1];
+    const int per = (p.batch + kMergeThreads - 1) / kMergeThreads;
+    const int64_t per_head = scan_units<kMergeThreads>(p, pre, per, false);
+    const int64_t total = per_head * p.hkv;
+    const int ctas = (int)min((int64_t)main_ctas, total);
+    const int x0 = (int)blockIdx.x;
+    rx::pdl_wait();  // the partial results are written by the kernel before this one
+    if (x0 + 1 >= ctas || total / ctas >= INT_MAX) return;
+    const int64_t cut = first_unit(total, ctas, x0 + 1);
+    const Cursor c = locate<kMergeThreads>(p, pre, per, per_head, cut);
+    const int64_t begin = cut - c.j, end = begin + c.r.ntiles;
+    if (c.j == 0 || begin < first_unit(total, ctas, x0)) return;
+    int parts = 2;
+    while (x0 + parts < ctas && first_unit(total, ctas, x0 + parts) < end) ++parts;
+
+    constexpr int V = D / 32;  // values of a lane
+    const int lane = threadIdx.x & 31;
+    const int t0 = c.qt * p.tb, M = min(p.tb, c.r.T - t0) * p.G;
+    const int64_t tok0 = (int64_t)__ldg(p.qo_indptr + c.b) + t0;
+    for (int i = threadIdx.x >> 5; i < kMergeRows; i += kMergeThreads / 32) {
+        const int row = (int)blockIdx.y * kMergeRows + i;
+        if (row >= M) break;
+        auto at = [&](int s) { return (int64_t)(2 * (x0 + s) + (s == 0 ? 1 : 0)) * kRows + row; };
+        float m = -INFINITY;
+        for (int s = lane; s < parts; s += 32) m = fmaxf(m, __ldcg(p.part_l + at(s)));
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        const float mu = m == -INFINITY ? 0.f : m;
+        float acc[V] = {}, tot = 0.f;
+#pragma unroll 4
+        for (int s = 0; s < parts; ++s) {
+            const float w = exp2f(__ldcg(p.part_l + at(s)) - mu);
+            const float *src = p.part_o + at(s) * D + lane * V;
+            tot += w;
+            if constexpr (V == 4) {
+                const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
+                acc[0] = fmaf(w, v.x, acc[0]);
+                acc[1] = fmaf(w, v.y, acc[1]);
+                acc[2] = fmaf(w, v.z, acc[2]);
+                acc[3] = fmaf(w, v.w, acc[3]);
+            } else {
+                const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
+                acc[0] = fmaf(w, v.x, acc[0]);
+                acc[1] = fmaf(w, v.y, acc[1]);
+            }
+        }
+        const float inv = tot == 0.f ? 0.f : 1.f / tot;
+        const int64_t orow = (tok0 + row / p.G) * p.hq + (int64_t)c.g * p.G + row % p.G;
+        uint32_t *dst = reinterpret_cast<uint32_t *>(p.o + orow * D + lane * V);
+        dst[0] = rx::pack_bf16(acc[0] * inv, acc[1] * inv);
+        if constexpr (V == 4) dst[1] = rx::pack_bf16(acc[2] * inv, acc[3] * inv);
+        if (p.lse && lane == 0) p.lse[orow] = tot == 0.f ? -INFINITY : (m + log2f(tot)) * rx::kLn2;
+    }
+}
+
+size_t part_bytes(int32_t head_dim) { return (size_t)2 * kCtas * kRows * head_dim * sizeof(float); }
 
 struct TreePool {
     const void *k, *v;
@@ -116,6 +873,27 @@ bool tree_shape_ok(int32_t batch, int32_t hq, int32_t hkv, int32_t D, int32_t ma
 {
     return batch >= 0 && batch <= 65535 && hq > 0 && hkv > 0 && hq % hkv == 0 && hq / hkv <= 128 &&
            (D == 64 || D == 128) && max_tree >= 1 && max_tree <= kMaxTree;
+}
+
+template <int D, bool F8>
+int launch(const TParams &p, cudaStream_t st)
+{
+    // per device; cheap, and right whichever device is current
+    RX_CUDA_CHECK(cudaFuncSetAttribute(tree_kernel<D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, TL<D>::BYTES));
+    tree_kernel<D, F8><<<kCtas, kThreads, TL<D>::BYTES, st>>>(p);
+    RX_CUDA_CHECK(cudaGetLastError());
+    // a programmatic dependent: it finds its part of the work, then waits on the device
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kCtas - 1, (unsigned)((std::min(p.max_tree, p.tb) * p.G + kMergeRows - 1) / kMergeRows));
+    cfg.blockDim = dim3(kMergeThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    RX_CUDA_CHECK(cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, p, (int)kCtas));
+    return RX_OK;
 }
 
 int tree_call(const char *who, const TreePool &pool, const void *q, void *o, float *lse, int32_t hq,
@@ -134,12 +912,9 @@ int tree_call(const char *who, const TreePool &pool, const void *q, void *o, flo
                             who, batch, hq, pool.hkv, max_tree, kMaxTree);
     if (mask && (int64_t)words * 32 < max_tree)
         return rx_set_error(RX_ERR_INVALID, "%s: mask rows of %d words for trees of %d", who, words, max_tree);
-    const uintptr_t pool_align = pool.f8 ? 7 : 15;
-    if (rx_misaligned16(q) || rx_misaligned16(o) || (reinterpret_cast<uintptr_t>(pool.k) & pool_align) != 0 ||
-        (reinterpret_cast<uintptr_t>(pool.v) & pool_align) != 0 || (reinterpret_cast<uintptr_t>(lse) & 3) != 0 ||
-        (reinterpret_cast<uintptr_t>(mask) & 3) != 0)
-        return rx_set_error(RX_ERR_INVALID, "%s: q and o must be 16-byte aligned, the pools %d-byte aligned", who,
-                            (int)pool_align + 1);
+    if (rx_misaligned16(q) || rx_misaligned16(o) || rx_misaligned16(pool.k) || rx_misaligned16(pool.v) ||
+        (reinterpret_cast<uintptr_t>(lse) & 3) != 0 || (reinterpret_cast<uintptr_t>(mask) & 3) != 0)
+        return rx_set_error(RX_ERR_INVALID, "%s: q, o and the pools must be 16-byte aligned", who);
     const size_t need = rx_attn_tree_workspace(batch, hq, pool.hkv, pool.D, max_tree);
     if (!workspace || ws_bytes < need)
         return rx_set_error(RX_ERR_CAPACITY, "%s: workspace of %zu bytes, %zu needed", who, workspace ? ws_bytes : (size_t)0,
@@ -151,12 +926,13 @@ int tree_call(const char *who, const TreePool &pool, const void *q, void *o, flo
     p.q = (const bf16 *)q;
     p.o = (bf16 *)o;
     p.lse = lse;
-    p.k = pool.k;
-    p.v = pool.v;
+    p.k = (const unsigned char *)pool.k;
+    p.v = (const unsigned char *)pool.v;
     p.num_slots = pool.num_slots;
     p.hq = hq;
     p.hkv = pool.hkv;
     p.G = hq / pool.hkv;
+    p.tb = kRows / p.G;
     p.qo_indptr = qo_indptr;
     p.req_idx = req_idx;
     p.prefix_len = prefix_len;
@@ -169,12 +945,11 @@ int tree_call(const char *who, const TreePool &pool, const void *q, void *o, flo
     p.scale_log2 = sm_scale * pool.k_scale * rx::kLog2e;
     p.v_scale = pool.v_scale;
     p.status = dev_status;
-    const dim3 grid((unsigned)(((int64_t)max_tree * hq + 3) / 4), (unsigned)batch);
-    auto kernel = pool.D == 128 ? (pool.f8 ? tree_warp_kernel<128, true> : tree_warp_kernel<128, false>)
-                                : (pool.f8 ? tree_warp_kernel<64, true> : tree_warp_kernel<64, false>);
-    kernel<<<grid, 128, 0, (cudaStream_t)stream>>>(p);
-    RX_CUDA_CHECK(cudaGetLastError());
-    return RX_OK;
+    p.part_o = (float *)workspace;
+    p.part_l = (float *)((char *)workspace + part_bytes(pool.D));
+    cudaStream_t st = (cudaStream_t)stream;
+    if (pool.D == 128) return pool.f8 ? launch<128, true>(p, st) : launch<128, false>(p, st);
+    return pool.f8 ? launch<64, true>(p, st) : launch<64, false>(p, st);
 }
 
 }  // namespace
@@ -185,7 +960,7 @@ extern "C" size_t rx_attn_tree_workspace(int32_t batch, int32_t hq, int32_t hkv,
         rx_set_error(RX_ERR_INVALID, "rx_attn_tree_workspace: invalid argument");
         return 0;
     }
-    return 256;
+    return part_bytes(head_dim) + (size_t)2 * kCtas * kRows * sizeof(float);
 }
 
 extern "C" int rx_attn_tree(const rx_kv_pool *pool_in, const void *q, void *o, float *lse, int32_t hq,
