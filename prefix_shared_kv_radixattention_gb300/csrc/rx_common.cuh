@@ -130,6 +130,17 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return *reinterpret_cast<uint32_t *>(&v);
 }
 
+// 16-byte read-only load that stays where it is written (the compiler may sink
+// a plain load past the waits that it is meant to overlap).
+__device__ __forceinline__ uint4 ld_stream(const void *p)
+{
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
 // Programmatic dependent launch (PTX griddepcontrol).  A kernel launched with
 // programmatic stream serialization may start once every CTA of the kernel
 // before it on the stream has executed launch_dependents (or exited); it

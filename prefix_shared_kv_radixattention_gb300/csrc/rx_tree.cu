@@ -56,38 +56,43 @@ constexpr int kBN = 128;             // positions of a K/V tile
 constexpr int kStages = 2;           // K ring and V ring depth
 constexpr int kProdWarps = 8;
 constexpr int kProdRows = kBN / kProdWarps;  // rows of a tile each producer warp gathers
-constexpr int kSoftWarps = 4;
+constexpr int kSoftWarps = 8;        // two groups of four, one query row a thread
 constexpr int kWarpQ = kSoftWarps + kProdWarps;      // loads the query rows
 constexpr int kWarpMma = kWarpQ + 1;
 constexpr int kThreads = 32 * (kWarpMma + 1);
 constexpr int kRing = 4;             // per-segment words kept this many segments (see nf, qscale)
-constexpr uint32_t kTmemCols = 512;  // buffer i: S (then P) at 256 i, O at 256 i + 128
+constexpr int kCodeBufs = 3;         // FP8: tiles of codes in flight
+constexpr uint32_t kTmemCols = 512;  // group t: S (then P) at 256 t, O at 256 t + 128
 constexpr float kRescale = 8.f;      // log2 units the running max may lag
 constexpr int kMergeRows = 16;       // rows of one merge CTA
 constexpr int kMergeThreads = 128;
 
-template <int D>
+template <int D, bool F8>
 struct TL {
     static constexpr int NB = D / 64;             // 128-byte column blocks of a row
     static constexpr int BLK = kRows * 128;       // bytes of one column block of a tile
-    static constexpr int OFF_Q = 0;               // two buffers
-    static constexpr int OFF_K = OFF_Q + 2 * NB * BLK;
+    static constexpr int QB = F8 ? 1 : 2;         // query buffers (FP8: their room goes to the codes)
+    static constexpr int CODE = F8 ? kBN * D : 0; // bytes of one tile of codes
+    static constexpr int OFF_Q = 0;
+    static constexpr int OFF_K = OFF_Q + QB * NB * BLK;
     static constexpr int OFF_V = OFF_K + kStages * NB * BLK;
-    static constexpr int OFF_NF = OFF_V + kStages * NB * BLK;         // kRing x 32 words
+    static constexpr int OFF_CODE = OFF_V + kStages * NB * BLK;
+    static constexpr int OFF_NF = OFF_CODE + kCodeBufs * CODE;        // kRing x 32 words
     static constexpr int OFF_QS = OFF_NF + kRing * 32 * 4;            // kRing x 128 floats
-    static constexpr int OFF_SCAN = OFF_QS + kRing * kRows * 4;       // kThreads + 1 int64
+    static constexpr int OFF_ML = OFF_QS + kRing * kRows * 4;         // 2 x 2 groups x 128 rows x {max, sum}
+    static constexpr int OFF_SCAN = OFF_ML + 4 * kRows * 8;           // kThreads + 1 int64
     static constexpr int OFF_BAR = OFF_SCAN + (kThreads + 1) * 8;
     static constexpr int B_KFULL = 0, B_KEMPTY = B_KFULL + kStages, B_VFULL = B_KEMPTY + kStages,
-                         B_VEMPTY = B_VFULL + kStages, B_QFULL = B_VEMPTY + kStages, B_QEMPTY = B_QFULL + 2,
-                         B_SFULL = B_QEMPTY + 2, B_PFULL = B_SFULL + 2, B_PVDONE = B_PFULL + 2,
-                         B_OEMPTY = B_PVDONE + 1, B_FINAL = B_OEMPTY + 2, N_BAR = B_FINAL + 1;
+                         B_VEMPTY = B_VFULL + kStages, B_QFULL = B_VEMPTY + kStages, B_QEMPTY = B_QFULL + QB,
+                         B_SFULL = B_QEMPTY + QB, B_PFULL = B_SFULL + 2, B_PVDONE = B_PFULL + 2,
+                         B_OEMPTY = B_PVDONE + 2, B_FINAL = B_OEMPTY + 1, N_BAR = B_FINAL + 1;
     static constexpr int OFF_TMEM = OFF_BAR + N_BAR * 8;
     static constexpr int OFF_ABORT = OFF_TMEM + 8;
     static constexpr int OFF_START = OFF_ABORT + 8;                   // Cursor of the CTA's first unit
     static constexpr int BYTES = OFF_START + 64 + 1024;               // + room to align the base to 1024
 };
-static_assert(TL<128>::BYTES <= 227 * 1024, "shared memory budget");
-static_assert(TL<128>::OFF_SCAN % 8 == 0 && TL<128>::OFF_BAR % 8 == 0, "alignment");
+static_assert(TL<128, false>::BYTES <= 226 * 1024 && TL<128, true>::BYTES <= 226 * 1024, "shared memory budget");
+static_assert(TL<128, false>::OFF_SCAN % 8 == 0 && TL<128, false>::OFF_BAR % 8 == 0, "alignment");
 
 struct TParams {
     const bf16 *q;
@@ -118,6 +123,7 @@ struct TParams {
 
 struct Req {
     int T, P;
+    int row;          // of req_to_token
     int ntiles, nqt;  // 0 where there is nothing to do (no drafted token, or lengths out of range)
 
     __device__ __forceinline__ int64_t units() const { return (int64_t)ntiles * nqt; }
@@ -128,6 +134,7 @@ __device__ __forceinline__ Req load_req(const TParams &p, int b, bool flag = fal
     Req r;
     r.T = __ldg(p.qo_indptr + b + 1) - __ldg(p.qo_indptr + b);
     r.P = __ldg(p.prefix_len + b);
+    r.row = __ldg(p.req_idx + b);
     r.ntiles = r.nqt = 0;
     if (r.T == 0) return r;
     if (r.T < 0 || r.T > p.max_tree || r.P < 0 || (int64_t)r.P + r.T > p.rtt_stride) {
@@ -273,17 +280,26 @@ __device__ __forceinline__ uint4 widen_f16(uint32_t lo, uint32_t hi)
                       rx::e4m3x2_to_f16x2((uint16_t)hi), rx::e4m3x2_to_f16x2((uint16_t)(hi >> 16)));
 }
 
-// A producer warp gathers rows [16 w, 16 w + 16) of every K and V tile: the
-// loads of the next tile's K are issued as soon as this tile's K registers are
-// stored, V alike, so that 32 to 64 KB an SM are always in flight; slot ids
-// run two tiles ahead.
+// A producer warp gathers rows [16 w, 16 w + 16) of every K and V tile with
+// 16-byte async copies, slot ids one tile ahead.  (Loads into registers go
+// through L1, which this kernel's shared memory leaves 28 KB: with 64 KB meant
+// to be in flight they ran at half the rate.)
+//
+// bf16 pools: the copies land in the swizzled tile itself and report to its
+// barrier.  FP8 pools: they land in a ring of three code tiles, K(n), V(n),
+// K(n + 1), ...; each thread widens the chunks that it copied (E4M3 to f16 is
+// exact) and stores them to the tile.
+//
+// V at drafted positions passes through registers in both: a NaN or infinity
+// there would reach rows that do not see the position (0 * inf), so it is
+// dropped, noted, and added back to the rows that see it at the end.
 template <int D, bool F8>
 __device__ void producer(const TParams &p, Cursor c, unsigned char *smem, uint32_t sbase)
 {
-    using L = TL<D>;
+    using L = TL<D, F8>;
     constexpr int EB = F8 ? 1 : 2;                    // bytes of a value
     constexpr int CPR = D * EB / 16;                  // 16-byte chunks of a row
-    constexpr int RPI = 32 / CPR;                     // rows of one load instruction
+    constexpr int RPI = 32 / CPR;                     // rows of one instruction
     constexpr int U = kProdRows / RPI;                // instructions for this warp's rows
     const uint32_t bar = sbase + L::OFF_BAR;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
@@ -293,26 +309,23 @@ __device__ void producer(const TParams &p, Cursor c, unsigned char *smem, uint32
     const int64_t row_bytes = (int64_t)p.hkv * D * EB;
 
     struct Tile {
-        int32_t slot;  // lane l < 16: slot of row r0 + l, -1 past the end or outside the pool
+        int32_t slot;  // lane l < 16: slot of row r0 + l, in flight until check() looks at it
+        bool in;       // ... which is a position of the request
         int g, seg;
         int rel;       // the tile's first position, from the first drafted one
     };
     int seg = 0;
     bool more = true;
-    // the tile at the cursor, with its slot ids (flagged when outside the
-    // pool); then on to the next
+    // the tile at the cursor, with the loads of its slot ids; then on to the next
     auto take = [&](Tile &t) -> bool {
         if (!more) return false;
         t.g = c.g;
         t.rel = c.j * kBN - c.r.P;
         t.seg = seg % kRing;
-        t.slot = -1;
         const int pos = c.j * kBN + r0 + lane;
-        if (lane < kProdRows && pos < c.r.P + c.r.T) {
-            const int32_t s = __ldg(p.rtt + (int64_t)__ldg(p.req_idx + c.b) * p.rtt_stride + pos);
-            if (s >= 0 && (int64_t)s < p.num_slots) t.slot = s;
-            else if (p.status) atomicOr(p.status, RX_DEV_BAD_SLOT);
-        }
+        t.in = lane < kProdRows && pos < c.r.P + c.r.T;
+        t.slot = -1;
+        if (t.in) t.slot = __ldg(p.rtt + (int64_t)c.r.row * p.rtt_stride + pos);
         ++c.j;
         if (--c.left <= 0) {
             more = false;
@@ -324,70 +337,116 @@ __device__ void producer(const TParams &p, Cursor c, unsigned char *smem, uint32
         }
         return true;
     };
-    auto load = [&](const unsigned char *pool, const Tile &t, uint4 (&x)[U]) {
+    // slots past the end or outside the pool (flagged) become -1
+    auto check = [&](Tile &t) {
+        const bool ok = t.in && t.slot >= 0 && (int64_t)t.slot < p.num_slots;
+        if (t.in && !ok && p.status) atomicOr(p.status, RX_DEV_BAD_SLOT);
+        if (!ok) t.slot = -1;
+    };
+    // this thread's chunk of row u * RPI + sub, copied to where dst(u) says
+    auto copy = [&](const unsigned char *pool, const Tile &t, auto dst) {
+        const unsigned char *base = pool + (int64_t)t.g * (D * EB) + ch * 16;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int32_t s = __shfl_sync(0xffffffffu, t.slot, u * RPI + sub);
-            x[u] = make_uint4(0, 0, 0, 0);
-            if (s >= 0) {
-                const uint4 *src = reinterpret_cast<const uint4 *>(pool + (int64_t)s * row_bytes + (int64_t)t.g * (D * EB)) + ch;
-                x[u] = __ldg(src);
-            }
+            rx::cp_async_16(dst(u), base + (s >= 0 ? (int64_t)s * row_bytes : 0), s >= 0 ? 16 : 0);
         }
     };
-    auto store = [&](uint32_t off, const Tile &t, uint4 (&x)[U], bool is_v) {
-        // drafted positions' V: a NaN or infinity would reach rows that do
-        // not see the position (0 * inf), so it is dropped here, noted, and
-        // added back to the rows that see it when their result is written
-        const bool check = is_v && t.rel + kBN > 0;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int r = r0 + u * RPI + sub;
-            unsigned char *tile = smem + off;
-            bool nf = false;
-            if constexpr (F8) {
-                uint4 a = widen_f16(x[u].x, x[u].y), b = widen_f16(x[u].z, x[u].w);
-                if (check && t.rel + r >= 0) {
-                    nf = drop_not_finite<true>(a);
-                    nf |= drop_not_finite<true>(b);
-                }
-                *reinterpret_cast<uint4 *>(tile + sw128(r, 2 * ch, L::BLK)) = a;
-                *reinterpret_cast<uint4 *>(tile + sw128(r, 2 * ch + 1, L::BLK)) = b;
-            } else {
-                if (check && t.rel + r >= 0) nf = drop_not_finite<false>(x[u]);
-                *reinterpret_cast<uint4 *>(tile + sw128(r, ch, L::BLK)) = x[u];
-            }
-            if (nf) {
-                const int e = t.rel + r;
-                atomicOr(reinterpret_cast<uint32_t *>(smem + L::OFF_NF) + t.seg * 32 + (e >> 5), 1u << (e & 31));
-            }
-        }
-        rx::fence_proxy_async_smem();
-        __syncwarp();
+    auto note = [&](const Tile &t, int r) {
+        const int e = t.rel + r;
+        atomicOr(reinterpret_cast<uint32_t *>(smem + L::OFF_NF) + t.seg * 32 + (e >> 5), 1u << (e & 31));
     };
 
-    Tile cur, nxt, nx2;
-    uint4 kx[U], vx[U];
+    Tile cur, nxt;
     take(cur);
-    bool have1 = take(nxt);
-    load(p.k, cur, kx);
-    load(p.v, cur, vx);
-    for (int n = 0;; ++n) {
-        const int st = n % kStages;
-        const bool have2 = have1 && take(nx2);
-        if (n >= kStages && !warp_wait(bar + 8 * (L::B_KEMPTY + st), (n / kStages - 1) & 1, abort_flag, p.status)) return;
-        store(L::OFF_K + st * L::NB * L::BLK, cur, kx, false);
-        if (lane == 0) rx::mbar_arrive(bar + 8 * (L::B_KFULL + st));
-        if (have1) load(p.k, nxt, kx);
-        if (n >= kStages && !warp_wait(bar + 8 * (L::B_VEMPTY + st), (n / kStages - 1) & 1, abort_flag, p.status)) return;
-        store(L::OFF_V + st * L::NB * L::BLK, cur, vx, true);
-        if (lane == 0) rx::mbar_arrive(bar + 8 * (L::B_VFULL + st));
-        if (!have1) return;
-        load(p.v, nxt, vx);
-        cur = nxt;
-        nxt = nx2;
-        have1 = have2;
+    if constexpr (!F8) {
+        for (int n = 0;; ++n) {
+            const int st = n % kStages;
+            const bool have1 = take(nxt);
+            check(cur);
+            const uint32_t kd = sbase + L::OFF_K + st * L::NB * L::BLK, vd = sbase + L::OFF_V + st * L::NB * L::BLK;
+            if (n >= kStages && !warp_wait(bar + 8 * (L::B_KEMPTY + st), (n / kStages - 1) & 1, abort_flag, p.status)) break;
+            copy(p.k, cur, [&](int u) { return kd + sw128(r0 + u * RPI + sub, ch, L::BLK); });
+            rx::cp_async_mbar_arrive(bar + 8 * (L::B_KFULL + st));
+            if (n >= kStages && !warp_wait(bar + 8 * (L::B_VEMPTY + st), (n / kStages - 1) & 1, abort_flag, p.status)) break;
+            if (cur.rel + kBN <= 0) {
+                copy(p.v, cur, [&](int u) { return vd + sw128(r0 + u * RPI + sub, ch, L::BLK); });
+                rx::cp_async_mbar_arrive(bar + 8 * (L::B_VFULL + st));
+            } else {
+                uint4 x[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int32_t s = __shfl_sync(0xffffffffu, cur.slot, u * RPI + sub);
+                    x[u] = make_uint4(0, 0, 0, 0);
+                    if (s >= 0) x[u] = rx::ld_stream(p.v + (int64_t)s * row_bytes + (int64_t)cur.g * (D * EB) + ch * 16);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const int r = r0 + u * RPI + sub;
+                    if (cur.rel + r >= 0 && drop_not_finite<false>(x[u])) note(cur, r);
+                    *reinterpret_cast<uint4 *>(smem + (vd - sbase) + sw128(r, ch, L::BLK)) = x[u];
+                }
+                rx::fence_proxy_async_smem();
+                rx::mbar_arrive(bar + 8 * (L::B_VFULL + st));
+            }
+            if (!have1) break;
+            cur = nxt;
+        }
+    } else {
+        const uint32_t mine = L::OFF_CODE + (uint32_t)(pw * U * 32 + lane) * 16;  // chunk u of buffer b: + b CODE + 512 u
+        auto fetch = [&](const unsigned char *pool, const Tile &t, int item) {
+            copy(pool, t, [&](int u) { return sbase + mine + (item % kCodeBufs) * L::CODE + u * 512; });
+            rx::cp_async_commit();
+        };
+        // this thread's chunks of a landed item into the tile at `off`
+        auto widen = [&](uint32_t off, const Tile &t, int item, bool is_v) {
+            const bool drafted = is_v && t.rel + kBN > 0;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(smem + mine + (item % kCodeBufs) * L::CODE + u * 512);
+                uint4 a = widen_f16(x.x, x.y), b = widen_f16(x.z, x.w);
+                const int r = r0 + u * RPI + sub;
+                if (drafted && t.rel + r >= 0) {
+                    bool nf = drop_not_finite<true>(a);
+                    nf |= drop_not_finite<true>(b);
+                    if (nf) note(t, r);
+                }
+                *reinterpret_cast<uint4 *>(smem + off + sw128(r, 2 * ch, L::BLK)) = a;
+                *reinterpret_cast<uint4 *>(smem + off + sw128(r, 2 * ch + 1, L::BLK)) = b;
+            }
+            rx::fence_proxy_async_smem();
+        };
+        check(cur);
+        fetch(p.k, cur, 0);
+        fetch(p.v, cur, 1);
+        bool have1 = take(nxt);
+        for (int n = 0;; ++n) {
+            const int st = n % kStages;
+            Tile nx2;
+            if (have1) {
+                check(nxt);
+                fetch(p.k, nxt, 2 * n + 2);
+            } else {
+                rx::cp_async_commit();  // an empty group keeps the count
+            }
+            const bool have2 = have1 && take(nx2);
+            rx::cp_async_wait<2>();     // K(n)
+            if (n >= kStages && !warp_wait(bar + 8 * (L::B_KEMPTY + st), (n / kStages - 1) & 1, abort_flag, p.status)) break;
+            widen(L::OFF_K + st * L::NB * L::BLK, cur, 2 * n, false);
+            rx::mbar_arrive(bar + 8 * (L::B_KFULL + st));
+            if (have1) fetch(p.v, nxt, 2 * n + 3);
+            else rx::cp_async_commit();
+            rx::cp_async_wait<2>();     // V(n)
+            if (n >= kStages && !warp_wait(bar + 8 * (L::B_VEMPTY + st), (n / kStages - 1) & 1, abort_flag, p.status)) break;
+            widen(L::OFF_V + st * L::NB * L::BLK, cur, 2 * n + 1, true);
+            rx::mbar_arrive(bar + 8 * (L::B_VFULL + st));
+            if (!have1) break;
+            cur = nxt;
+            nxt = nx2;
+            have1 = have2;
+        }
     }
+    rx::cp_async_wait_all();  // nothing may still be landing when the CTA exits
 }
 
 // ---------------------------------------------------------------------------
@@ -395,7 +454,7 @@ __device__ void producer(const TParams &p, Cursor c, unsigned char *smem, uint32
 // ---------------------------------------------------------------------------
 
 // One warp copies each segment's query rows (row r: drafted token r / G of the
-// row tile, q head g G + r % G) into one of two buffers.  bf16 pools: 16-byte
+// row tile, q head g G + r % G) into a query buffer.  bf16 pools: 16-byte
 // async copies.  FP8 pools: the products run in f16, which holds every E4M3
 // value; a query row is brought to f16 times a power of two that puts its
 // largest value just below 2^15 (values 2^-29 of that and above stay exact),
@@ -403,16 +462,16 @@ __device__ void producer(const TParams &p, Cursor c, unsigned char *smem, uint32
 template <int D, bool F8>
 __device__ void query_loader(const TParams &p, Cursor c, unsigned char *smem, uint32_t sbase)
 {
-    using L = TL<D>;
+    using L = TL<D, F8>;
     constexpr int CPR = D / 8;
     const uint32_t bar = sbase + L::OFF_BAR;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
     const int lane = threadIdx.x & 31;
     for (int s = 0;; ++s) {
-        const int buf = s & 1;
+        const int buf = s % L::QB;
         const int t0 = c.qt * p.tb, M = min(p.tb, c.r.T - t0) * p.G;
         const int64_t tok0 = (int64_t)__ldg(p.qo_indptr + c.b) + t0;
-        if (s >= 2 && !warp_wait(bar + 8 * (L::B_QEMPTY + buf), ((s >> 1) - 1) & 1, abort_flag, p.status)) break;
+        if (s >= L::QB && !warp_wait(bar + 8 * (L::B_QEMPTY + buf), (s / L::QB - 1) & 1, abort_flag, p.status)) break;
         const uint32_t dst = sbase + L::OFF_Q + buf * L::NB * L::BLK;
         for (int i0 = 0; i0 < M * CPR; i0 += 32) {
             const int i = i0 + lane, r = i / CPR, ch = i % CPR;
@@ -458,13 +517,14 @@ __device__ void query_loader(const TParams &p, Cursor c, unsigned char *smem, ui
 // MMA thread
 // ---------------------------------------------------------------------------
 
-// Over the CTA's tiles n = 0, 1, ... (all segments in a row): S(n) into buffer
-// n & 1, then O += P V of tile n - 1.  P(n - 2) sits in the buffer that S(n)
-// overwrites, so S(n) waits for that product's completion.
+// Over the CTA's tiles n = 0, 1, ... (all segments in a row), tile n belonging
+// to softmax group n & 1: S(n) into the group's columns, then O += P V of tile
+// n - 1.  P(n - 2) sits in the columns that S(n) overwrites, so S(n) waits for
+// that product's completion.
 template <int D, bool F8>
 __device__ void mma_issuer(const TParams &p, Cursor c, unsigned char *smem, uint32_t sbase, uint32_t tmem)
 {
-    using L = TL<D>;
+    using L = TL<D, F8>;
     const uint32_t bar = sbase + L::OFF_BAR;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
     constexpr uint32_t idesc_qk = F8 ? rx::idesc_f16(kRows, kBN, false, false) : rx::idesc_bf16(kRows, kBN, false, false);
@@ -476,13 +536,13 @@ __device__ void mma_issuer(const TParams &p, Cursor c, unsigned char *smem, uint
 
     auto issue_s = [&](int n, int s, bool first, bool last) -> bool {
         const int st = n % kStages, buf = n & 1;
-        if (first && !wait(L::B_QFULL + (s & 1), (s >> 1) & 1)) return false;
+        if (first && !wait(L::B_QFULL + s % L::QB, (s / L::QB) & 1)) return false;
         if (!wait(L::B_KFULL + st, (n / kStages) & 1)) return false;
-        if (n >= 2 && !wait(L::B_PVDONE, n & 1)) return false;  // O += P V of tile n - 2 (same parity)
-        rx::fence_proxy_async_smem();  // query rows landed by cp.async -> async proxy
+        if (n >= 2 && !wait(L::B_PVDONE + buf, ((n >> 1) - 1) & 1)) return false;  // O += P V of tile n - 2
+        rx::fence_proxy_async_smem();  // rows landed by cp.async -> async proxy
         rx::tc_fence_after();
         const uint64_t dks = dk + (uint64_t)((st * L::NB * L::BLK) >> 4);
-        const uint64_t dqs = dq + (uint64_t)(((s & 1) * L::NB * L::BLK) >> 4);
+        const uint64_t dqs = dq + (uint64_t)(((s % L::QB) * L::NB * L::BLK) >> 4);
 #pragma unroll
         for (int kb = 0; kb < D / 16; ++kb) {
             const uint64_t off = (uint64_t)(((kb >> 2) * L::BLK + (kb & 3) * 32) >> 4);
@@ -490,21 +550,22 @@ __device__ void mma_issuer(const TParams &p, Cursor c, unsigned char *smem, uint
         }
         rx::tc_commit(bar + 8 * (L::B_SFULL + buf));
         rx::tc_commit(bar + 8 * (L::B_KEMPTY + st));
-        if (last) rx::tc_commit(bar + 8 * (L::B_QEMPTY + (s & 1)));
+        if (last) rx::tc_commit(bar + 8 * (L::B_QEMPTY + s % L::QB));
         return true;
     };
-    auto issue_pv = [&](int n, int s, bool first) -> bool {
+    auto issue_pv = [&](int n, int s, bool first) -> bool {  // first: the group's first tile of the segment
         const int st = n % kStages, buf = n & 1;
         if (!wait(L::B_PFULL + buf, (n >> 1) & 1)) return false;
         if (!wait(L::B_VFULL + st, (n / kStages) & 1)) return false;
-        if (first && s >= 2 && !wait(L::B_OEMPTY + (s & 1), ((s >> 1) - 1) & 1)) return false;
+        if (first && s >= 1 && !wait(L::B_OEMPTY, (s - 1) & 1)) return false;
+        rx::fence_proxy_async_smem();  // V rows landed by cp.async
         rx::tc_fence_after();
         const uint64_t dvs = dv + (uint64_t)((st * L::NB * L::BLK) >> 4);
 #pragma unroll
         for (int ks = 0; ks < kBN / 16; ++ks)
-            rx::tc_mma_ts(tmem + (s & 1) * 256 + 128, tmem + buf * 256 + ks * 8, dvs + (uint64_t)((ks * 16 * 128) >> 4),
+            rx::tc_mma_ts(tmem + buf * 256 + 128, tmem + buf * 256 + ks * 8, dvs + (uint64_t)((ks * 16 * 128) >> 4),
                           idesc_pv, (!first || ks > 0) ? 1u : 0u);
-        rx::tc_commit(bar + 8 * L::B_PVDONE);
+        rx::tc_commit(bar + 8 * (L::B_PVDONE + buf));
         rx::tc_commit(bar + 8 * (L::B_VEMPTY + st));
         return true;
     };
@@ -516,7 +577,7 @@ __device__ void mma_issuer(const TParams &p, Cursor c, unsigned char *smem, uint
             ok = issue_s(n, s, j == j0, j == j1 - 1);
             if (ok && n > 0) ok = issue_pv(n - 1, prev_s, prev_first);
             prev_s = s;
-            prev_first = j == j0;
+            prev_first = j < j0 + 2;
         }
         if (!ok || !c.next(p)) break;
     }
@@ -531,17 +592,18 @@ __device__ void mma_issuer(const TParams &p, Cursor c, unsigned char *smem, uint
 // ---------------------------------------------------------------------------
 
 // The NaN and infinities of V at drafted positions that a row sees, added to
-// its written result: o (part < 0) or the partial row `part`.
+// its written result: o (part < 0) or the partial row `part`, values
+// [col, col + D / 2).
 template <int D, bool F8>
 __device__ __noinline__ void add_not_finite(const TParams &p, const uint32_t *nf, const uint32_t *mrow, int node,
-                                            const Cursor &c, int64_t part, int64_t orow)
+                                            const Cursor &c, int64_t part, int64_t orow, int col)
 {
     for (int w = 0; w < (c.r.T + 31) / 32; ++w)
         for (uint32_t bad = nf[w] & mask_word(p, mrow, node, c.r.T, w); bad; bad &= bad - 1) {
             const int pos = c.r.P + 32 * w + __ffs(bad) - 1;
-            const int64_t slot = __ldg(p.rtt + (int64_t)__ldg(p.req_idx + c.b) * p.rtt_stride + pos);
+            const int64_t slot = __ldg(p.rtt + (int64_t)c.r.row * p.rtt_stride + pos);
             const int64_t at = (slot * p.hkv + c.g) * D;
-            for (int i = 0; i < D; ++i) {
+            for (int i = col; i < col + D / 2; ++i) {
                 float v;
                 if constexpr (F8) {
                     const uint32_t h = rx::e4m3x2_to_f16x2(__ldg(p.v + at + i));
@@ -556,15 +618,22 @@ __device__ __noinline__ void add_not_finite(const TParams &p, const uint32_t *nf
         }
 }
 
+// Group t (four warps) takes the CTA's tiles n with n & 1 == t, with a running
+// maximum and sum and an O of its own; at a segment's end the two are joined:
+// with m the larger maximum and a_t = 2^(m_t - m),
+//     o = (a_0 O_0 + a_1 O_1) / (a_0 l_0 + a_1 l_1),
+// each group writing half of the row.
 template <int D, bool F8>
 __device__ void softmax_rows(const TParams &p, Cursor c, unsigned char *smem, uint32_t sbase, uint32_t tmem)
 {
-    using L = TL<D>;
+    using L = TL<D, F8>;
     const uint32_t bar = sbase + L::OFF_BAR;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
-    const int row = threadIdx.x;                       // = TMEM lane
+    const int t = threadIdx.x >> 7;                    // group
+    const int row = threadIdx.x & (kRows - 1);         // = TMEM lane
     const uint32_t lanes = (uint32_t)(row & ~31) << 16;
-    int n = 0;
+    const uint32_t tS = tmem + t * 256 + lanes, tO = tS + 128;
+    int n0 = 0;                                        // tiles of the segments before
     for (int s = 0;; ++s) {
         const int j0 = c.j, j1 = c.end(), P = c.r.P, T = c.r.T;
         const int t0 = c.qt * p.tb, M = min(p.tb, T - t0) * p.G;
@@ -573,13 +642,14 @@ __device__ void softmax_rows(const TParams &p, Cursor c, unsigned char *smem, ui
         const int64_t tok = (int64_t)__ldg(p.qo_indptr + c.b) + node;
         const uint32_t *mrow = p.mask && valid ? p.mask + tok * p.words : nullptr;
         float m_used = -INFINITY, l = 0.f, sl2 = p.scale_log2;
-        for (int j = j0; j < j1; ++j, ++n) {
-            const int buf = n & 1;
-            const uint32_t tS = tmem + buf * 256 + lanes, tO = tmem + (s & 1) * 256 + 128 + lanes;
-            if (!warp_wait(bar + 8 * (L::B_SFULL + buf), (n >> 1) & 1, abort_flag, p.status)) return;
+        const int first = (n0 & 1) == t ? j0 : j0 + 1;  // the group's first tile
+        int n = n0 + first - j0;
+        for (int j = first; j < j1; j += 2, n += 2) {
+            if (!warp_wait(bar + 8 * (L::B_SFULL + t), (n >> 1) & 1, abort_flag, p.status)) return;
             rx::tc_fence_after();
             if (warp_on) {
-                if (F8 && j == j0) sl2 = p.scale_log2 * reinterpret_cast<const float *>(smem + L::OFF_QS)[(s % kRing) * kRows + row];
+                if (F8 && j == first)
+                    sl2 = p.scale_log2 * reinterpret_cast<const float *>(smem + L::OFF_QS)[(s % kRing) * kRows + row];
                 const int kbase = j * kBN;
                 const bool masked = kbase + kBN > P;   // drafted positions, or past the last
                 uint32_t bits[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
@@ -593,25 +663,28 @@ __device__ void softmax_rows(const TParams &p, Cursor c, unsigned char *smem, ui
                         lo = hi;
                     }
                 }
-                auto scores = [&](int k, uint32_t (&sv)[32]) {
-                    rx::tmem_ld32(tS + k * 32, sv);
-                    rx::tmem_wait_ld();
+                auto hide = [&](int k, uint32_t (&sv)[32]) {
                     if (masked) {
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             if (!((bits[k] >> i) & 1u)) sv[i] = 0xFF800000u;  // -inf
                     }
                 };
+                // two passes over the scores, 32 columns at a time (128 at once
+                // do not fit in registers); the other group's warps fill the
+                // load latency
                 float mx = -INFINITY;
+                uint32_t x[32];
 #pragma unroll
                 for (int k = 0; k < kBN / 32; ++k) {
-                    uint32_t sv[32];
-                    scores(k, sv);
+                    rx::tmem_ld32(tS + k * 32, x);
+                    rx::tmem_wait_ld();
+                    hide(k, x);
                     float a0 = mx, a1 = -INFINITY;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        a0 = rx::fmax3(a0, u2f(sv[4 * i]), u2f(sv[4 * i + 1]));
-                        a1 = rx::fmax3(a1, u2f(sv[4 * i + 2]), u2f(sv[4 * i + 3]));
+                        a0 = rx::fmax3(a0, u2f(x[4 * i]), u2f(x[4 * i + 1]));
+                        a1 = rx::fmax3(a1, u2f(x[4 * i + 2]), u2f(x[4 * i + 3]));
                     }
                     mx = fmaxf(a0, a1);
                 }
@@ -628,12 +701,14 @@ __device__ void softmax_rows(const TParams &p, Cursor c, unsigned char *smem, ui
                 uint64_t acc0 = 0, acc1 = 0;
 #pragma unroll
                 for (int k = 0; k < kBN / 32; ++k) {
-                    uint32_t sv[32], pk[16];
-                    scores(k, sv);
+                    rx::tmem_ld32(tS + k * 32, x);
+                    rx::tmem_wait_ld();
+                    hide(k, x);
+                    uint32_t pk[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         float x0, x1;
-                        rx::f2_split(rx::f2_fma(rx::f2(u2f(sv[2 * i]), u2f(sv[2 * i + 1])), scale2, negm2), x0, x1);
+                        rx::f2_split(rx::f2_fma(rx::f2(u2f(x[2 * i]), u2f(x[2 * i + 1])), scale2, negm2), x0, x1);
                         const float e0 = rx::fast_exp2(x0), e1 = rx::fast_exp2(x1);
                         if (i & 1) acc1 = rx::f2_add(acc1, rx::f2(e0, e1));
                         else acc0 = rx::f2_add(acc0, rx::f2(e0, e1));
@@ -647,73 +722,87 @@ __device__ void softmax_rows(const TParams &p, Cursor c, unsigned char *smem, ui
                 rx::f2_split(rx::f2_add(acc0, acc1), a0, a1);
                 l += a0 + a1;
                 if (__any_sync(0xffffffffu, scale_o)) {
-                    // O += P V of the tile before has to be complete
-                    if (!warp_wait(bar + 8 * L::B_PVDONE, (n - 1) & 1, abort_flag, p.status)) return;
-                    rx::tc_fence_after();
+                    // the group's product before (tile n - 2) has completed: S(n) waited for it
 #pragma unroll
                     for (int k = 0; k < D / 32; ++k) {
-                        uint32_t r[32];
-                        rx::tmem_ld32(tO + k * 32, r);
+                        rx::tmem_ld32(tO + k * 32, x);
                         rx::tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(u2f(r[i]) * alpha);
-                        rx::tmem_st32(tO + k * 32, r);
+                        for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(u2f(x[i]) * alpha);
+                        rx::tmem_st32(tO + k * 32, x);
                     }
                 }
                 rx::tmem_wait_st();
             }
             rx::tc_fence_before();
-            rx::mbar_arrive(bar + 8 * (L::B_PFULL + buf));
+            rx::mbar_arrive(bar + 8 * (L::B_PFULL + t));
         }
-        // the segment's result
-        const uint32_t tO = tmem + (s & 1) * 256 + 128 + lanes;
-        if (!warp_wait(bar + 8 * L::B_PVDONE, (n - 1) & 1, abort_flag, p.status)) return;
+        n0 += j1 - j0;
+        // the segment's result: both groups' products are complete
+        if (first < j1 && !warp_wait(bar + 8 * (L::B_PVDONE + t), ((n - 2) >> 1) & 1, abort_flag, p.status)) return;
+        // two buffers in turn: a group without a tile in the next segment is
+        // at its end while the other still reads this one's
+        float2 *ml = reinterpret_cast<float2 *>(smem + L::OFF_ML) + (s & 1) * 2 * kRows;
+        ml[t * kRows + row] = make_float2(m_used, l);
+        rx::tc_fence_before();
+        rx::named_bar_sync(1, 32 * kSoftWarps);
         rx::tc_fence_after();
+        const float2 other = ml[(1 - t) * kRows + row];
+        const float m0 = t ? other.x : m_used, l0 = t ? other.y : l, m1 = t ? m_used : other.x, l1 = t ? l : other.y;
+        const float m = fmaxf(m0, m1);
+        // a group without a seen key has no O (its columns hold anything)
+        float f0 = l0 == 0.f ? 0.f : rx::fast_exp2(m0 - m), f1 = l1 == 0.f ? 0.f : rx::fast_exp2(m1 - m);
+        const float ls = f0 * l0 + f1 * l1;
+        const float inv = ls == 0.f ? 0.f : p.v_scale / ls;
+        f0 *= inv;
+        f1 *= inv;
         uint32_t *nf = reinterpret_cast<uint32_t *>(smem + L::OFF_NF) + (s % kRing) * 32;
         uint32_t any = 0;
         if (j1 * kBN > P)
             for (int i = 0; i < (T + 31) / 32; ++i) any |= nf[i];
         const bool whole = j0 == 0 && j1 == c.r.ntiles;
-        const float inv = l == 0.f ? 0.f : p.v_scale / l;
         const int64_t orow = tok * p.hq + (int64_t)c.g * p.G + row % p.G;
         const int64_t prow = (int64_t)(2 * blockIdx.x + (j0 == 0 ? 1 : 0)) * kRows + row;
         if (warp_on) {
 #pragma unroll
-            for (int k = 0; k < D / 32; ++k) {
-                uint32_t r[32];
-                rx::tmem_ld32(tO + k * 32, r);
+            for (int k = 0; k < D / 64; ++k) {
+                const int col = t * (D / 2) + k * 32;
+                uint32_t a[32], b[32];
+                rx::tmem_ld32(tmem + lanes + 128 + col, a);
+                rx::tmem_ld32(tmem + lanes + 256 + 128 + col, b);
                 rx::tmem_wait_ld();
                 if (valid) {
                     float x[32];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) x[i] = l == 0.f ? 0.f : u2f(r[i]) * inv;
+                    for (int i = 0; i < 32; ++i)
+                        x[i] = (l0 == 0.f ? 0.f : u2f(a[i]) * f0) + (l1 == 0.f ? 0.f : u2f(b[i]) * f1);
                     if (whole) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(p.o + orow * D + k * 32);
+                        uint4 *dst = reinterpret_cast<uint4 *>(p.o + orow * D + col);
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             dst[i] = make_uint4(rx::pack_bf16(x[8 * i], x[8 * i + 1]), rx::pack_bf16(x[8 * i + 2], x[8 * i + 3]),
                                                 rx::pack_bf16(x[8 * i + 4], x[8 * i + 5]), rx::pack_bf16(x[8 * i + 6], x[8 * i + 7]));
                     } else {
-                        float4 *dst = reinterpret_cast<float4 *>(p.part_o + prow * D + k * 32);
+                        float4 *dst = reinterpret_cast<float4 *>(p.part_o + prow * D + col);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
                     }
                 }
                 __syncwarp();
             }
-            if (valid) {
-                const float l2 = l == 0.f ? -INFINITY : m_used + log2f(l);
+            if (valid && t == 0) {
+                const float l2 = ls == 0.f ? -INFINITY : m + log2f(ls);
                 if (!whole) p.part_l[prow] = l2;
                 else if (p.lse) p.lse[orow] = l2 * rx::kLn2;
             }
         }
         if (any) {  // the same for every thread: all have read the words, then they are cleared
-            if (valid) add_not_finite<D, F8>(p, nf, mrow, node, c, whole ? -1 : prow, orow);
+            if (valid) add_not_finite<D, F8>(p, nf, mrow, node, c, whole ? -1 : prow, orow, t * (D / 2));
             rx::named_bar_sync(1, 32 * kSoftWarps);
-            if (row < 32) nf[row] = 0;
+            if (threadIdx.x < 32) nf[threadIdx.x] = 0;
         }
         rx::tc_fence_before();
-        rx::mbar_arrive(bar + 8 * (L::B_OEMPTY + (s & 1)));
+        rx::mbar_arrive(bar + 8 * L::B_OEMPTY);
         if (!c.next(p)) return;
     }
 }
@@ -721,7 +810,7 @@ __device__ void softmax_rows(const TParams &p, Cursor c, unsigned char *smem, ui
 template <int D, bool F8>
 __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant__ TParams p)
 {
-    using L = TL<D>;
+    using L = TL<D, F8>;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const uint32_t raw = rx::smem_u32(smem_raw);
     unsigned char *smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);  // 1024-aligned swizzle atoms
@@ -732,19 +821,21 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            rx::mbar_init(bar + 8 * (L::B_KFULL + i), kProdWarps);
-            rx::mbar_init(bar + 8 * (L::B_VFULL + i), kProdWarps);
+            rx::mbar_init(bar + 8 * (L::B_KFULL + i), 32 * kProdWarps);
+            rx::mbar_init(bar + 8 * (L::B_VFULL + i), 32 * kProdWarps);
             rx::mbar_init(bar + 8 * (L::B_KEMPTY + i), 1);
             rx::mbar_init(bar + 8 * (L::B_VEMPTY + i), 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < L::QB; ++i) {
             rx::mbar_init(bar + 8 * (L::B_QFULL + i), 32);
             rx::mbar_init(bar + 8 * (L::B_QEMPTY + i), 1);
-            rx::mbar_init(bar + 8 * (L::B_SFULL + i), 1);
-            rx::mbar_init(bar + 8 * (L::B_PFULL + i), 32 * kSoftWarps);
-            rx::mbar_init(bar + 8 * (L::B_OEMPTY + i), 32 * kSoftWarps);
         }
-        rx::mbar_init(bar + 8 * L::B_PVDONE, 1);
+        for (int i = 0; i < 2; ++i) {
+            rx::mbar_init(bar + 8 * (L::B_SFULL + i), 1);
+            rx::mbar_init(bar + 8 * (L::B_PFULL + i), kRows);
+            rx::mbar_init(bar + 8 * (L::B_PVDONE + i), 1);
+        }
+        rx::mbar_init(bar + 8 * L::B_OEMPTY, 32 * kSoftWarps);
         rx::mbar_init(bar + 8 * L::B_FINAL, 1);
         *reinterpret_cast<volatile int *>(smem + L::OFF_ABORT) = 0;
         rx::fence_mbar_init();
@@ -879,8 +970,8 @@ template <int D, bool F8>
 int launch(const TParams &p, cudaStream_t st)
 {
     // per device; cheap, and right whichever device is current
-    RX_CUDA_CHECK(cudaFuncSetAttribute(tree_kernel<D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, TL<D>::BYTES));
-    tree_kernel<D, F8><<<kCtas, kThreads, TL<D>::BYTES, st>>>(p);
+    RX_CUDA_CHECK(cudaFuncSetAttribute(tree_kernel<D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (TL<D, F8>::BYTES)));
+    tree_kernel<D, F8><<<kCtas, kThreads, (TL<D, F8>::BYTES), st>>>(p);
     RX_CUDA_CHECK(cudaGetLastError());
     // a programmatic dependent: it finds its part of the work, then waits on the device
     cudaLaunchConfig_t cfg = {};
