@@ -141,6 +141,26 @@ __device__ __forceinline__ uint4 ld_stream(const void *p)
     return v;
 }
 
+__device__ __forceinline__ int32_t ld_stream_b32(const int32_t *p)
+{
+    int32_t v;
+    asm volatile("ld.global.nc.b32 %0, [%1];\n" : "=r"(v) : "l"(p));
+    return v;
+}
+
+// Registers a thread of this warpgroup from here on (all four warps): more,
+// granted once others of the block have given theirs back, or fewer.
+template <int N>
+__device__ __forceinline__ void reg_inc()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_dec()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+
 // Programmatic dependent launch (PTX griddepcontrol).  A kernel launched with
 // programmatic stream serialization may start once every CTA of the kernel
 // before it on the stream has executed launch_dependents (or exited); it

@@ -59,7 +59,11 @@ constexpr int kProdRows = kBN / kProdWarps;  // rows of a tile each producer war
 constexpr int kSoftWarps = 8;        // two groups of four, one query row a thread
 constexpr int kWarpQ = kSoftWarps + kProdWarps;      // loads the query rows
 constexpr int kWarpMma = kWarpQ + 1;
-constexpr int kThreads = 32 * (kWarpMma + 1);
+constexpr int kThreads = 32 * (kWarpQ + 4);          // two warps idle: register shares go by warpgroup
+// registers a thread, by role: 256 (136 + 72) + 128 56 of the 640 96 launched
+constexpr int kRegsSoft = 136, kRegsProd = 72, kRegsMisc = 56;
+static_assert(32 * (kSoftWarps * kRegsSoft + kProdWarps * kRegsProd + 4 * kRegsMisc) <= kThreads * 96,
+              "a share is granted out of the launched registers only");
 constexpr int kRing = 4;             // per-segment words kept this many segments (see nf, qscale)
 constexpr int kCodeBufs = 3;         // FP8: tiles of codes in flight
 constexpr uint32_t kTmemCols = 512;  // group t: S (then P) at 256 t, O at 256 t + 128
@@ -229,6 +233,18 @@ __device__ Cursor locate(const TParams &p, const int64_t *pre, int per, int64_t 
     return c;
 }
 
+// The CTA's first place, as thread 0 left it in shared memory.
+template <typename L>
+__device__ __forceinline__ Cursor start_of(const unsigned char *smem)
+{
+    const volatile int *w = reinterpret_cast<const volatile int *>(smem + L::OFF_START);
+    Cursor c;
+    int *d = reinterpret_cast<int *>(&c);
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(Cursor) / 4); ++i) d[i] = w[i];
+    return c;
+}
+
 // First unit of CTA c out of `ctas` (no more CTAs than units: none is empty).
 __device__ __forceinline__ int64_t first_unit(int64_t total, int ctas, int c) { return total * c / ctas; }
 
@@ -237,21 +253,16 @@ __device__ __forceinline__ int64_t first_unit(int64_t total, int ctas, int c) { 
 // ---------------------------------------------------------------------------
 
 // Word i of drafted token `node`'s mask: prefix positions (i < 0) are seen,
-// bits at and past T are not.
+// bits at and past T are not.  Without branches around the load, so that the
+// loads of several words go out together.
 __device__ __forceinline__ uint32_t mask_word(const TParams &p, const uint32_t *row, int node, int T, int i)
 {
-    if (i < 0) return 0xFFFFFFFFu;
+    uint32_t w = 0xFFFFFFFFu;
     int n = T - 32 * i;  // drafted tokens from bit 0 of this word on
-    if (n <= 0) return 0u;
-    uint32_t w;
-    if (row) {
-        w = __ldg(row + i);
-    } else {
-        w = 0xFFFFFFFFu;
-        n = min(n, node + 1 - 32 * i);
-        if (n <= 0) return 0u;
-    }
-    return n >= 32 ? w : w & ((1u << n) - 1u);
+    if (row) w = __ldg(row + min(max(i, 0), p.words - 1));
+    else n = min(n, node + 1 - 32 * i);
+    w = n >= 32 ? w : n <= 0 ? 0u : w & ((1u << (n & 31)) - 1u);
+    return i < 0 ? 0xFFFFFFFFu : w;
 }
 
 // ---------------------------------------------------------------------------
@@ -294,9 +305,10 @@ __device__ __forceinline__ uint4 widen_f16(uint32_t lo, uint32_t hi)
 // there would reach rows that do not see the position (0 * inf), so it is
 // dropped, noted, and added back to the rows that see it at the end.
 template <int D, bool F8>
-__device__ void producer(const TParams &p, Cursor c, unsigned char *smem, uint32_t sbase)
+__device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
 {
     using L = TL<D, F8>;
+    Cursor c = start_of<L>(smem);
     constexpr int EB = F8 ? 1 : 2;                    // bytes of a value
     constexpr int CPR = D * EB / 16;                  // 16-byte chunks of a row
     constexpr int RPI = 32 / CPR;                     // rows of one instruction
@@ -325,7 +337,7 @@ __device__ void producer(const TParams &p, Cursor c, unsigned char *smem, uint32
         const int pos = c.j * kBN + r0 + lane;
         t.in = lane < kProdRows && pos < c.r.P + c.r.T;
         t.slot = -1;
-        if (t.in) t.slot = __ldg(p.rtt + (int64_t)c.r.row * p.rtt_stride + pos);
+        if (t.in) t.slot = rx::ld_stream_b32(p.rtt + (int64_t)c.r.row * p.rtt_stride + pos);
         ++c.j;
         if (--c.left <= 0) {
             more = false;
@@ -460,9 +472,10 @@ __device__ void producer(const TParams &p, Cursor c, unsigned char *smem, uint32
 // largest value just below 2^15 (values 2^-29 of that and above stay exact),
 // and the power goes into the row's score scale.
 template <int D, bool F8>
-__device__ void query_loader(const TParams &p, Cursor c, unsigned char *smem, uint32_t sbase)
+__device__ void query_loader(const TParams &p, unsigned char *smem, uint32_t sbase)
 {
     using L = TL<D, F8>;
+    Cursor c = start_of<L>(smem);
     constexpr int CPR = D / 8;
     const uint32_t bar = sbase + L::OFF_BAR;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
@@ -522,9 +535,11 @@ __device__ void query_loader(const TParams &p, Cursor c, unsigned char *smem, ui
 // n - 1.  P(n - 2) sits in the columns that S(n) overwrites, so S(n) waits for
 // that product's completion.
 template <int D, bool F8>
-__device__ void mma_issuer(const TParams &p, Cursor c, unsigned char *smem, uint32_t sbase, uint32_t tmem)
+__device__ void mma_issuer(const TParams &p, unsigned char *smem, uint32_t sbase)
 {
     using L = TL<D, F8>;
+    Cursor c = start_of<L>(smem);
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::OFF_TMEM);
     const uint32_t bar = sbase + L::OFF_BAR;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
     constexpr uint32_t idesc_qk = F8 ? rx::idesc_f16(kRows, kBN, false, false) : rx::idesc_bf16(kRows, kBN, false, false);
@@ -595,14 +610,14 @@ __device__ void mma_issuer(const TParams &p, Cursor c, unsigned char *smem, uint
 // its written result: o (part < 0) or the partial row `part`, values
 // [col, col + D / 2).
 template <int D, bool F8>
-__device__ __noinline__ void add_not_finite(const TParams &p, const uint32_t *nf, const uint32_t *mrow, int node,
-                                            const Cursor &c, int64_t part, int64_t orow, int col)
+__device__ __noinline__ void add_not_finite(const TParams &p, const uint32_t *nf, const uint32_t *mrow, int node, int b,
+                                            int g, int P, int T, int64_t part, int64_t orow, int col)
 {
-    for (int w = 0; w < (c.r.T + 31) / 32; ++w)
-        for (uint32_t bad = nf[w] & mask_word(p, mrow, node, c.r.T, w); bad; bad &= bad - 1) {
-            const int pos = c.r.P + 32 * w + __ffs(bad) - 1;
-            const int64_t slot = __ldg(p.rtt + (int64_t)c.r.row * p.rtt_stride + pos);
-            const int64_t at = (slot * p.hkv + c.g) * D;
+    for (int w = 0; w < (T + 31) / 32; ++w)
+        for (uint32_t bad = nf[w] & mask_word(p, mrow, node, T, w); bad; bad &= bad - 1) {
+            const int pos = P + 32 * w + __ffs(bad) - 1;
+            const int64_t slot = __ldg(p.rtt + (int64_t)__ldg(p.req_idx + b) * p.rtt_stride + pos);
+            const int64_t at = (slot * p.hkv + g) * D;
             for (int i = col; i < col + D / 2; ++i) {
                 float v;
                 if constexpr (F8) {
@@ -624,9 +639,11 @@ __device__ __noinline__ void add_not_finite(const TParams &p, const uint32_t *nf
 //     o = (a_0 O_0 + a_1 O_1) / (a_0 l_0 + a_1 l_1),
 // each group writing half of the row.
 template <int D, bool F8>
-__device__ void softmax_rows(const TParams &p, Cursor c, unsigned char *smem, uint32_t sbase, uint32_t tmem)
+__device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sbase)
 {
     using L = TL<D, F8>;
+    Cursor c = start_of<L>(smem);
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::OFF_TMEM);
     const uint32_t bar = sbase + L::OFF_BAR;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
     const int t = threadIdx.x >> 7;                    // group
@@ -655,13 +672,11 @@ __device__ void softmax_rows(const TParams &p, Cursor c, unsigned char *smem, ui
                 uint32_t bits[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
                 if (masked) {
                     const int off = kbase - P, w0 = off >> 5;
-                    uint32_t lo = mask_word(p, mrow, node, T, w0);
+                    uint32_t w[5];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t hi = mask_word(p, mrow, node, T, w0 + k + 1);
-                        bits[k] = __funnelshift_r(lo, hi, off & 31);
-                        lo = hi;
-                    }
+                    for (int k = 0; k < 5; ++k) w[k] = mask_word(p, mrow, node, T, w0 + k);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) bits[k] = __funnelshift_r(w[k], w[k + 1], off & 31);
                 }
                 auto hide = [&](int k, uint32_t (&sv)[32]) {
                     if (masked) {
@@ -797,7 +812,7 @@ __device__ void softmax_rows(const TParams &p, Cursor c, unsigned char *smem, ui
             }
         }
         if (any) {  // the same for every thread: all have read the words, then they are cleared
-            if (valid) add_not_finite<D, F8>(p, nf, mrow, node, c, whole ? -1 : prow, orow, t * (D / 2));
+            if (valid) add_not_finite<D, F8>(p, nf, mrow, node, c.b, c.g, P, T, whole ? -1 : prow, orow, t * (D / 2));
             rx::named_bar_sync(1, 32 * kSoftWarps);
             if (threadIdx.x < 32) nf[threadIdx.x] = 0;
         }
@@ -862,24 +877,27 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     rx::tc_fence_before();
     __syncthreads();
     rx::tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::OFF_TMEM);
-    const Cursor c = *reinterpret_cast<const Cursor *>(smem + L::OFF_START);
 
     if (warp < kSoftWarps) {
-        softmax_rows<D, F8>(p, c, smem, sbase, tmem);
+        rx::reg_inc<kRegsSoft>();
+        softmax_rows<D, F8>(p, smem, sbase);
     } else if (warp < kWarpQ) {
-        producer<D, F8>(p, c, smem, sbase);
-    } else if (warp == kWarpQ) {
-        query_loader<D, F8>(p, c, smem, sbase);
+        rx::reg_dec<kRegsProd>();
+        producer<D, F8>(p, smem, sbase);
     } else {
-        if ((threadIdx.x & 31) == 0) mma_issuer<D, F8>(p, c, smem, sbase, tmem);
-        __syncwarp();
+        rx::reg_dec<kRegsMisc>();
+        if (warp == kWarpQ) {
+            query_loader<D, F8>(p, smem, sbase);
+        } else if (warp == kWarpMma) {
+            if ((threadIdx.x & 31) == 0) mma_issuer<D, F8>(p, smem, sbase);
+            __syncwarp();
+        }
     }
     rx::tc_fence_before();
     __syncthreads();
     if (warp == kWarpMma) {
         rx::tc_fence_after();
-        rx::tmem_dealloc(tmem, kTmemCols);
+        rx::tmem_dealloc(*reinterpret_cast<volatile uint32_t *>(smem + L::OFF_TMEM), kTmemCols);
     }
 }
 
