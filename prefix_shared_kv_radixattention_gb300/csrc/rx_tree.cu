@@ -54,19 +54,21 @@ constexpr int kCtas = 152;           // CTAs of a call: one an SM
 constexpr int kRows = 128;           // query rows of a tile (MMA M)
 constexpr int kBN = 128;             // positions of a K/V tile
 constexpr int kStages = 2;           // K ring and V ring depth
-constexpr int kProdWarps = 8;
+constexpr int kProdWarps = 8;        // for K, and as many for V
 constexpr int kProdRows = kBN / kProdWarps;  // rows of a tile each producer warp gathers
-constexpr int kSoftWarps = 8;        // two groups of four, one query row a thread
-constexpr int kWarpQ = kSoftWarps + kProdWarps;      // loads the query rows
+constexpr int kSoftWarps = 4;        // one query row a thread
+constexpr int kWarpQ = kSoftWarps + 2 * kProdWarps;  // loads the query rows
 constexpr int kWarpMma = kWarpQ + 1;
 constexpr int kThreads = 32 * (kWarpQ + 4);          // two warps idle: register shares go by warpgroup
-// registers a thread, by role: 256 (136 + 72) + 128 56 of the 640 96 launched
-constexpr int kRegsSoft = 136, kRegsProd = 72, kRegsMisc = 56;
-static_assert(32 * (kSoftWarps * kRegsSoft + kProdWarps * kRegsProd + 4 * kRegsMisc) <= kThreads * 96,
+// registers a thread, by role (a softmax thread holds a row's 128 scores):
+// 128 x 192 + 512 x 56 + 128 x 56 of the 768 x 80 launched
+constexpr int kRegsSoft = 192, kRegsProd = 56, kRegsMisc = 56, kRegsLaunch = 80;
+static_assert(32 * (kSoftWarps * kRegsSoft + 2 * kProdWarps * kRegsProd + 4 * kRegsMisc) <= kThreads * kRegsLaunch,
               "a share is granted out of the launched registers only");
+static_assert(kThreads * kRegsLaunch <= 65536, "registers of an SM");
 constexpr int kRing = 4;             // per-segment words kept this many segments (see nf, qscale)
-constexpr int kCodeBufs = 3;         // FP8: tiles of codes in flight
-constexpr uint32_t kTmemCols = 512;  // group t: S (then P) at 256 t, O at 256 t + 128
+constexpr int kCodeBufs = 3;         // FP8: half tiles of codes in flight, for K and for V
+constexpr uint32_t kTmemCols = 512;  // buffer i: S (then P) at 256 i, O at 256 i + 128
 constexpr float kRescale = 8.f;      // log2 units the running max may lag
 constexpr int kMergeRows = 16;       // rows of one merge CTA
 constexpr int kMergeThreads = 128;
@@ -76,20 +78,19 @@ struct TL {
     static constexpr int NB = D / 64;             // 128-byte column blocks of a row
     static constexpr int BLK = kRows * 128;       // bytes of one column block of a tile
     static constexpr int QB = F8 ? 1 : 2;         // query buffers (FP8: their room goes to the codes)
-    static constexpr int CODE = F8 ? kBN * D : 0; // bytes of one tile of codes
+    static constexpr int CODE = F8 ? kBN * D / 2 : 0;  // bytes of half a tile of codes
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_K = OFF_Q + QB * NB * BLK;
     static constexpr int OFF_V = OFF_K + kStages * NB * BLK;
     static constexpr int OFF_CODE = OFF_V + kStages * NB * BLK;
-    static constexpr int OFF_NF = OFF_CODE + kCodeBufs * CODE;        // kRing x 32 words
+    static constexpr int OFF_NF = OFF_CODE + 2 * kCodeBufs * CODE;        // kRing x 32 words
     static constexpr int OFF_QS = OFF_NF + kRing * 32 * 4;            // kRing x 128 floats
-    static constexpr int OFF_ML = OFF_QS + kRing * kRows * 4;         // 2 x 2 groups x 128 rows x {max, sum}
-    static constexpr int OFF_SCAN = OFF_ML + 4 * kRows * 8;           // kThreads + 1 int64
+    static constexpr int OFF_SCAN = OFF_QS + kRing * kRows * 4;       // kThreads + 1 int64
     static constexpr int OFF_BAR = OFF_SCAN + (kThreads + 1) * 8;
     static constexpr int B_KFULL = 0, B_KEMPTY = B_KFULL + kStages, B_VFULL = B_KEMPTY + kStages,
                          B_VEMPTY = B_VFULL + kStages, B_QFULL = B_VEMPTY + kStages, B_QEMPTY = B_QFULL + QB,
                          B_SFULL = B_QEMPTY + QB, B_PFULL = B_SFULL + 2, B_PVDONE = B_PFULL + 2,
-                         B_OEMPTY = B_PVDONE + 2, B_FINAL = B_OEMPTY + 1, N_BAR = B_FINAL + 1;
+                         B_OEMPTY = B_PVDONE + 1, B_FINAL = B_OEMPTY + 2, N_BAR = B_FINAL + 1;
     static constexpr int OFF_TMEM = OFF_BAR + N_BAR * 8;
     static constexpr int OFF_ABORT = OFF_TMEM + 8;
     static constexpr int OFF_START = OFF_ABORT + 8;                   // Cursor of the CTA's first unit
@@ -291,20 +292,21 @@ __device__ __forceinline__ uint4 widen_f16(uint32_t lo, uint32_t hi)
                       rx::e4m3x2_to_f16x2((uint16_t)hi), rx::e4m3x2_to_f16x2((uint16_t)(hi >> 16)));
 }
 
-// A producer warp gathers rows [16 w, 16 w + 16) of every K and V tile with
-// 16-byte async copies, slot ids one tile ahead.  (Loads into registers go
+// Eight producer warps for K and eight for V (V's wait for the softmax does
+// not hold up K); warp w gathers rows [16 w, 16 w + 16) of every tile with
+// 16-byte async copies, slot ids two tiles ahead.  (Loads into registers go
 // through L1, which this kernel's shared memory leaves 28 KB: with 64 KB meant
 // to be in flight they ran at half the rate.)
 //
 // bf16 pools: the copies land in the swizzled tile itself and report to its
-// barrier.  FP8 pools: they land in a ring of three code tiles, K(n), V(n),
-// K(n + 1), ...; each thread widens the chunks that it copied (E4M3 to f16 is
-// exact) and stores them to the tile.
+// barrier.  FP8 pools: they land in a ring of three half tiles of codes; each
+// thread widens the chunks that it copied (E4M3 to f16 is exact) and stores
+// them to the tile.
 //
 // V at drafted positions passes through registers in both: a NaN or infinity
 // there would reach rows that do not see the position (0 * inf), so it is
 // dropped, noted, and added back to the rows that see it at the end.
-template <int D, bool F8>
+template <int D, bool F8, bool IS_V>
 __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
 {
     using L = TL<D, F8>;
@@ -313,41 +315,42 @@ __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
     constexpr int CPR = D * EB / 16;                  // 16-byte chunks of a row
     constexpr int RPI = 32 / CPR;                     // rows of one instruction
     constexpr int U = kProdRows / RPI;                // instructions for this warp's rows
-    const uint32_t bar = sbase + L::OFF_BAR;
+    const uint32_t bar_full = sbase + L::OFF_BAR + 8 * (IS_V ? L::B_VFULL : L::B_KFULL);
+    const uint32_t bar_empty = sbase + L::OFF_BAR + 8 * (IS_V ? L::B_VEMPTY : L::B_KEMPTY);
+    const unsigned char *pool = IS_V ? p.v : p.k;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
-    const int lane = threadIdx.x & 31, pw = (int)(threadIdx.x >> 5) - kSoftWarps;
+    const int lane = threadIdx.x & 31, pw = ((int)(threadIdx.x >> 5) - kSoftWarps) % kProdWarps;
     const int r0 = pw * kProdRows;
     const int sub = lane / CPR, ch = lane % CPR;
-    const int64_t row_bytes = (int64_t)p.hkv * D * EB;
+    const int row_bytes = p.hkv * D * EB;             // at most 2^15 heads (host check)
 
     struct Tile {
         int32_t slot;  // lane l < 16: slot of row r0 + l, in flight until check() looks at it
-        bool in;       // ... which is a position of the request
-        int g, seg;
+        int g;
         int rel;       // the tile's first position, from the first drafted one
+        int seg;       // segment mod kRing; -1: no tile
+        bool in;       // row r0 + l is a position of the request
     };
     int seg = 0;
-    bool more = true;
     // the tile at the cursor, with the loads of its slot ids; then on to the next
-    auto take = [&](Tile &t) -> bool {
-        if (!more) return false;
+    auto take = [&](Tile &t) {
+        t.seg = t.slot = -1;
+        t.g = t.rel = 0;
+        t.in = false;
+        if (c.left <= 0) return;
         t.g = c.g;
         t.rel = c.j * kBN - c.r.P;
         t.seg = seg % kRing;
         const int pos = c.j * kBN + r0 + lane;
         t.in = lane < kProdRows && pos < c.r.P + c.r.T;
-        t.slot = -1;
         if (t.in) t.slot = rx::ld_stream_b32(p.rtt + (int64_t)c.r.row * p.rtt_stride + pos);
-        ++c.j;
-        if (--c.left <= 0) {
-            more = false;
-        } else if (c.j == c.r.ntiles) {
-            c.j = c.r.ntiles - 1;  // next() counts the tile at j as the segment's last
-            ++c.left;
-            more = c.next(p);
+        if (c.j + 1 < c.r.ntiles) {
+            ++c.j;
+            --c.left;
+        } else {
             ++seg;
+            c.next(p);  // the tile at j is the segment's last
         }
-        return true;
     };
     // slots past the end or outside the pool (flagged) become -1
     auto check = [&](Tile &t) {
@@ -355,107 +358,113 @@ __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
         if (t.in && !ok && p.status) atomicOr(p.status, RX_DEV_BAD_SLOT);
         if (!ok) t.slot = -1;
     };
-    // this thread's chunk of row u * RPI + sub, copied to where dst(u) says
-    auto copy = [&](const unsigned char *pool, const Tile &t, auto dst) {
-        const unsigned char *base = pool + (int64_t)t.g * (D * EB) + ch * 16;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int32_t s = __shfl_sync(0xffffffffu, t.slot, u * RPI + sub);
-            rx::cp_async_16(dst(u), base + (s >= 0 ? (int64_t)s * row_bytes : 0), s >= 0 ? 16 : 0);
-        }
+    auto source = [&](const Tile &t, int u, bool &ok) {
+        const int32_t s = __shfl_sync(0xffffffffu, t.slot, u * RPI + sub);
+        ok = s >= 0;
+        return pool + (ok ? (int64_t)s * row_bytes : 0) + (t.g * (D * EB) + ch * 16);
     };
     auto note = [&](const Tile &t, int r) {
         const int e = t.rel + r;
         atomicOr(reinterpret_cast<uint32_t *>(smem + L::OFF_NF) + t.seg * 32 + (e >> 5), 1u << (e & 31));
     };
 
-    Tile cur, nxt;
+    Tile cur, nxt, nx2;
     take(cur);
+    take(nxt);
     if constexpr (!F8) {
-        for (int n = 0;; ++n) {
+        for (int n = 0; cur.seg >= 0; ++n) {
             const int st = n % kStages;
-            const bool have1 = take(nxt);
+            take(nx2);
             check(cur);
-            const uint32_t kd = sbase + L::OFF_K + st * L::NB * L::BLK, vd = sbase + L::OFF_V + st * L::NB * L::BLK;
-            if (n >= kStages && !warp_wait(bar + 8 * (L::B_KEMPTY + st), (n / kStages - 1) & 1, abort_flag, p.status)) break;
-            copy(p.k, cur, [&](int u) { return kd + sw128(r0 + u * RPI + sub, ch, L::BLK); });
-            rx::cp_async_mbar_arrive(bar + 8 * (L::B_KFULL + st));
-            if (n >= kStages && !warp_wait(bar + 8 * (L::B_VEMPTY + st), (n / kStages - 1) & 1, abort_flag, p.status)) break;
-            if (cur.rel + kBN <= 0) {
-                copy(p.v, cur, [&](int u) { return vd + sw128(r0 + u * RPI + sub, ch, L::BLK); });
-                rx::cp_async_mbar_arrive(bar + 8 * (L::B_VFULL + st));
-            } else {
-                uint4 x[U];
+            const uint32_t off = (IS_V ? L::OFF_V : L::OFF_K) + st * L::NB * L::BLK;
+            if (n >= kStages && !warp_wait(bar_empty + 8 * st, (n / kStages - 1) & 1, abort_flag, p.status)) break;
+            if (!IS_V || cur.rel + kBN <= 0) {
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
-                    const int32_t s = __shfl_sync(0xffffffffu, cur.slot, u * RPI + sub);
-                    x[u] = make_uint4(0, 0, 0, 0);
-                    if (s >= 0) x[u] = rx::ld_stream(p.v + (int64_t)s * row_bytes + (int64_t)cur.g * (D * EB) + ch * 16);
+                    bool ok;
+                    const unsigned char *src = source(cur, u, ok);
+                    rx::cp_async_16(sbase + off + sw128(r0 + u * RPI + sub, ch, L::BLK), src, ok ? 16 : 0);
                 }
+                rx::cp_async_mbar_arrive(bar_full + 8 * st);
+            } else {
+                constexpr int H = U / 2;  // half the rows at a time
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const int r = r0 + u * RPI + sub;
-                    if (cur.rel + r >= 0 && drop_not_finite<false>(x[u])) note(cur, r);
-                    *reinterpret_cast<uint4 *>(smem + (vd - sbase) + sw128(r, ch, L::BLK)) = x[u];
+                for (int h = 0; h < 2; ++h) {
+                    uint4 x[H];
+#pragma unroll
+                    for (int u = 0; u < H; ++u) {
+                        bool ok;
+                        const unsigned char *src = source(cur, h * H + u, ok);
+                        x[u] = make_uint4(0, 0, 0, 0);
+                        if (ok) x[u] = rx::ld_stream(src);
+                    }
+#pragma unroll
+                    for (int u = 0; u < H; ++u) {
+                        const int r = r0 + (h * H + u) * RPI + sub;
+                        if (cur.rel + r >= 0 && drop_not_finite<false>(x[u])) note(cur, r);
+                        *reinterpret_cast<uint4 *>(smem + off + sw128(r, ch, L::BLK)) = x[u];
+                    }
                 }
                 rx::fence_proxy_async_smem();
-                rx::mbar_arrive(bar + 8 * (L::B_VFULL + st));
+                rx::mbar_arrive(bar_full + 8 * st);
             }
-            if (!have1) break;
             cur = nxt;
+            nxt = nx2;
         }
     } else {
-        const uint32_t mine = L::OFF_CODE + (uint32_t)(pw * U * 32 + lane) * 16;  // chunk u of buffer b: + b CODE + 512 u
-        auto fetch = [&](const unsigned char *pool, const Tile &t, int item) {
-            copy(pool, t, [&](int u) { return sbase + mine + (item % kCodeBufs) * L::CODE + u * 512; });
+        constexpr int H = U / 2;  // instructions of half a tile
+        // chunk u of half-tile buffer b: + b CODE + 512 u
+        const uint32_t mine = L::OFF_CODE + (IS_V ? kCodeBufs * L::CODE : 0) + (uint32_t)(pw * H * 32 + lane) * 16;
+        auto fetch = [&](const Tile &t, int item) {  // item = 2 n + half
+#pragma unroll
+            for (int u = 0; u < H; ++u) {
+                bool ok;
+                const unsigned char *src = source(t, (item & 1) * H + u, ok);
+                rx::cp_async_16(sbase + mine + (item % kCodeBufs) * L::CODE + u * 512, src, ok ? 16 : 0);
+            }
             rx::cp_async_commit();
         };
-        // this thread's chunks of a landed item into the tile at `off`
-        auto widen = [&](uint32_t off, const Tile &t, int item, bool is_v) {
-            const bool drafted = is_v && t.rel + kBN > 0;
+        // this thread's chunks of a landed half into the tile at `off`
+        auto widen = [&](uint32_t off, const Tile &t, int item) {
+            const bool drafted = IS_V && t.rel + kBN > 0;
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
+            for (int u = 0; u < H; ++u) {
                 const uint4 x = *reinterpret_cast<const uint4 *>(smem + mine + (item % kCodeBufs) * L::CODE + u * 512);
                 uint4 a = widen_f16(x.x, x.y), b = widen_f16(x.z, x.w);
-                const int r = r0 + u * RPI + sub;
+                const int r = r0 + ((item & 1) * H + u) * RPI + sub;
                 if (drafted && t.rel + r >= 0) {
                     bool nf = drop_not_finite<true>(a);
                     nf |= drop_not_finite<true>(b);
                     if (nf) note(t, r);
                 }
-                *reinterpret_cast<uint4 *>(smem + off + sw128(r, 2 * ch, L::BLK)) = a;
-                *reinterpret_cast<uint4 *>(smem + off + sw128(r, 2 * ch + 1, L::BLK)) = b;
+                // the upper lanes of a row store their second chunk first: the
+                // two column blocks of a row lie on the same banks
+                const int swap = D == 128 ? (ch >> 2) & 1 : 0;
+                *reinterpret_cast<uint4 *>(smem + off + sw128(r, 2 * ch + swap, L::BLK)) = swap ? b : a;
+                *reinterpret_cast<uint4 *>(smem + off + sw128(r, 2 * ch + 1 - swap, L::BLK)) = swap ? a : b;
             }
-            rx::fence_proxy_async_smem();
         };
         check(cur);
-        fetch(p.k, cur, 0);
-        fetch(p.v, cur, 1);
-        bool have1 = take(nxt);
-        for (int n = 0;; ++n) {
+        check(nxt);
+        fetch(cur, 0);
+        fetch(cur, 1);
+        fetch(nxt, 2);
+        for (int n = 0; cur.seg >= 0; ++n) {
             const int st = n % kStages;
-            Tile nx2;
-            if (have1) {
-                check(nxt);
-                fetch(p.k, nxt, 2 * n + 2);
-            } else {
-                rx::cp_async_commit();  // an empty group keeps the count
-            }
-            const bool have2 = have1 && take(nx2);
-            rx::cp_async_wait<2>();     // K(n)
-            if (n >= kStages && !warp_wait(bar + 8 * (L::B_KEMPTY + st), (n / kStages - 1) & 1, abort_flag, p.status)) break;
-            widen(L::OFF_K + st * L::NB * L::BLK, cur, 2 * n, false);
-            rx::mbar_arrive(bar + 8 * (L::B_KFULL + st));
-            if (have1) fetch(p.v, nxt, 2 * n + 3);
-            else rx::cp_async_commit();
-            rx::cp_async_wait<2>();     // V(n)
-            if (n >= kStages && !warp_wait(bar + 8 * (L::B_VEMPTY + st), (n / kStages - 1) & 1, abort_flag, p.status)) break;
-            widen(L::OFF_V + st * L::NB * L::BLK, cur, 2 * n + 1, true);
-            rx::mbar_arrive(bar + 8 * (L::B_VFULL + st));
-            if (!have1) break;
+            const uint32_t off = (IS_V ? L::OFF_V : L::OFF_K) + st * L::NB * L::BLK;
+            take(nx2);
+            rx::cp_async_wait<2>();     // the first half of tile n
+            if (n >= kStages && !warp_wait(bar_empty + 8 * st, (n / kStages - 1) & 1, abort_flag, p.status)) break;
+            widen(off, cur, 2 * n);
+            fetch(nxt, 2 * n + 3);
+            rx::cp_async_wait<2>();     // the second
+            widen(off, cur, 2 * n + 1);
+            rx::fence_proxy_async_smem();
+            rx::mbar_arrive(bar_full + 8 * st);
+            check(nx2);
+            fetch(nx2, 2 * n + 4);
             cur = nxt;
             nxt = nx2;
-            have1 = have2;
         }
     }
     rx::cp_async_wait_all();  // nothing may still be landing when the CTA exits
@@ -530,10 +539,10 @@ __device__ void query_loader(const TParams &p, unsigned char *smem, uint32_t sba
 // MMA thread
 // ---------------------------------------------------------------------------
 
-// Over the CTA's tiles n = 0, 1, ... (all segments in a row), tile n belonging
-// to softmax group n & 1: S(n) into the group's columns, then O += P V of tile
-// n - 1.  P(n - 2) sits in the columns that S(n) overwrites, so S(n) waits for
-// that product's completion.
+// Over the CTA's tiles n = 0, 1, ... (all segments in a row): S(n) into buffer
+// n & 1, then O += P V of tile n - 1, O of segment s in buffer s & 1.  P(n - 2)
+// sits in the columns that S(n) overwrites, so S(n) waits for that product's
+// completion.
 template <int D, bool F8>
 __device__ void mma_issuer(const TParams &p, unsigned char *smem, uint32_t sbase)
 {
@@ -553,7 +562,7 @@ __device__ void mma_issuer(const TParams &p, unsigned char *smem, uint32_t sbase
         const int st = n % kStages, buf = n & 1;
         if (first && !wait(L::B_QFULL + s % L::QB, (s / L::QB) & 1)) return false;
         if (!wait(L::B_KFULL + st, (n / kStages) & 1)) return false;
-        if (n >= 2 && !wait(L::B_PVDONE + buf, ((n >> 1) - 1) & 1)) return false;  // O += P V of tile n - 2
+        if (n >= 2 && !wait(L::B_PVDONE, n & 1)) return false;  // O += P V of tile n - 2 (the same parity)
         rx::fence_proxy_async_smem();  // rows landed by cp.async -> async proxy
         rx::tc_fence_after();
         const uint64_t dks = dk + (uint64_t)((st * L::NB * L::BLK) >> 4);
@@ -568,19 +577,19 @@ __device__ void mma_issuer(const TParams &p, unsigned char *smem, uint32_t sbase
         if (last) rx::tc_commit(bar + 8 * (L::B_QEMPTY + s % L::QB));
         return true;
     };
-    auto issue_pv = [&](int n, int s, bool first) -> bool {  // first: the group's first tile of the segment
+    auto issue_pv = [&](int n, int s, bool first) -> bool {
         const int st = n % kStages, buf = n & 1;
         if (!wait(L::B_PFULL + buf, (n >> 1) & 1)) return false;
         if (!wait(L::B_VFULL + st, (n / kStages) & 1)) return false;
-        if (first && s >= 1 && !wait(L::B_OEMPTY, (s - 1) & 1)) return false;
+        if (first && s >= 2 && !wait(L::B_OEMPTY + (s & 1), ((s >> 1) - 1) & 1)) return false;
         rx::fence_proxy_async_smem();  // V rows landed by cp.async
         rx::tc_fence_after();
         const uint64_t dvs = dv + (uint64_t)((st * L::NB * L::BLK) >> 4);
 #pragma unroll
         for (int ks = 0; ks < kBN / 16; ++ks)
-            rx::tc_mma_ts(tmem + buf * 256 + 128, tmem + buf * 256 + ks * 8, dvs + (uint64_t)((ks * 16 * 128) >> 4),
+            rx::tc_mma_ts(tmem + (s & 1) * 256 + 128, tmem + buf * 256 + ks * 8, dvs + (uint64_t)((ks * 16 * 128) >> 4),
                           idesc_pv, (!first || ks > 0) ? 1u : 0u);
-        rx::tc_commit(bar + 8 * (L::B_PVDONE + buf));
+        rx::tc_commit(bar + 8 * L::B_PVDONE);
         rx::tc_commit(bar + 8 * (L::B_VEMPTY + st));
         return true;
     };
@@ -592,7 +601,7 @@ __device__ void mma_issuer(const TParams &p, unsigned char *smem, uint32_t sbase
             ok = issue_s(n, s, j == j0, j == j1 - 1);
             if (ok && n > 0) ok = issue_pv(n - 1, prev_s, prev_first);
             prev_s = s;
-            prev_first = j < j0 + 2;
+            prev_first = j == j0;
         }
         if (!ok || !c.next(p)) break;
     }
@@ -607,18 +616,17 @@ __device__ void mma_issuer(const TParams &p, unsigned char *smem, uint32_t sbase
 // ---------------------------------------------------------------------------
 
 // The NaN and infinities of V at drafted positions that a row sees, added to
-// its written result: o (part < 0) or the partial row `part`, values
-// [col, col + D / 2).
+// its written result: o (part < 0) or the partial row `part`.
 template <int D, bool F8>
 __device__ __noinline__ void add_not_finite(const TParams &p, const uint32_t *nf, const uint32_t *mrow, int node, int b,
-                                            int g, int P, int T, int64_t part, int64_t orow, int col)
+                                            int g, int P, int T, int64_t part, int64_t orow)
 {
     for (int w = 0; w < (T + 31) / 32; ++w)
         for (uint32_t bad = nf[w] & mask_word(p, mrow, node, T, w); bad; bad &= bad - 1) {
             const int pos = P + 32 * w + __ffs(bad) - 1;
             const int64_t slot = __ldg(p.rtt + (int64_t)__ldg(p.req_idx + b) * p.rtt_stride + pos);
             const int64_t at = (slot * p.hkv + g) * D;
-            for (int i = col; i < col + D / 2; ++i) {
+            for (int i = 0; i < D; ++i) {
                 float v;
                 if constexpr (F8) {
                     const uint32_t h = rx::e4m3x2_to_f16x2(__ldg(p.v + at + i));
@@ -633,11 +641,6 @@ __device__ __noinline__ void add_not_finite(const TParams &p, const uint32_t *nf
         }
 }
 
-// Group t (four warps) takes the CTA's tiles n with n & 1 == t, with a running
-// maximum and sum and an O of its own; at a segment's end the two are joined:
-// with m the larger maximum and a_t = 2^(m_t - m),
-//     o = (a_0 O_0 + a_1 O_1) / (a_0 l_0 + a_1 l_1),
-// each group writing half of the row.
 template <int D, bool F8>
 __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sbase)
 {
@@ -646,11 +649,9 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::OFF_TMEM);
     const uint32_t bar = sbase + L::OFF_BAR;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
-    const int t = threadIdx.x >> 7;                    // group
-    const int row = threadIdx.x & (kRows - 1);         // = TMEM lane
+    const int row = threadIdx.x;                       // = TMEM lane
     const uint32_t lanes = (uint32_t)(row & ~31) << 16;
-    const uint32_t tS = tmem + t * 256 + lanes, tO = tS + 128;
-    int n0 = 0;                                        // tiles of the segments before
+    int n = 0;
     for (int s = 0;; ++s) {
         const int j0 = c.j, j1 = c.end(), P = c.r.P, T = c.r.T;
         const int t0 = c.qt * p.tb, M = min(p.tb, T - t0) * p.G;
@@ -658,50 +659,48 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
         const int node = t0 + row / p.G;
         const int64_t tok = (int64_t)__ldg(p.qo_indptr + c.b) + node;
         const uint32_t *mrow = p.mask && valid ? p.mask + tok * p.words : nullptr;
+        const uint32_t tO = tmem + (s & 1) * 256 + 128 + lanes;
         float m_used = -INFINITY, l = 0.f, sl2 = p.scale_log2;
-        const int first = (n0 & 1) == t ? j0 : j0 + 1;  // the group's first tile
-        int n = n0 + first - j0;
-        for (int j = first; j < j1; j += 2, n += 2) {
-            if (!warp_wait(bar + 8 * (L::B_SFULL + t), (n >> 1) & 1, abort_flag, p.status)) return;
+        for (int j = j0; j < j1; ++j, ++n) {
+            const int buf = n & 1;
+            const uint32_t tS = tmem + buf * 256 + lanes;
+            if (!warp_wait(bar + 8 * (L::B_SFULL + buf), (n >> 1) & 1, abort_flag, p.status)) return;
             rx::tc_fence_after();
             if (warp_on) {
-                if (F8 && j == first)
-                    sl2 = p.scale_log2 * reinterpret_cast<const float *>(smem + L::OFF_QS)[(s % kRing) * kRows + row];
+                // the row's scores of this tile, loaded once (four loads in
+                // flight): a load takes about 200 cycles to come back
+                uint32_t sv[kBN];
+#pragma unroll
+                for (int k = 0; k < kBN / 32; ++k) rx::tmem_ld32(tS + k * 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * k));
+                if (F8 && j == j0) sl2 = p.scale_log2 * reinterpret_cast<const float *>(smem + L::OFF_QS)[(s % kRing) * kRows + row];
                 const int kbase = j * kBN;
-                const bool masked = kbase + kBN > P;   // drafted positions, or past the last
-                uint32_t bits[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};
-                if (masked) {
+                if (kbase + kBN > P) {   // drafted positions, or past the last
                     const int off = kbase - P, w0 = off >> 5;
                     uint32_t w[5];
 #pragma unroll
                     for (int k = 0; k < 5; ++k) w[k] = mask_word(p, mrow, node, T, w0 + k);
+                    rx::tmem_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) bits[k] = __funnelshift_r(w[k], w[k + 1], off & 31);
-                }
-                auto hide = [&](int k, uint32_t (&sv)[32]) {
-                    if (masked) {
+                    for (int k = 0; k < kBN / 32; ++k) {
+                        const uint32_t bits = __funnelshift_r(w[k], w[k + 1], off & 31);
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            if (!((bits[k] >> i) & 1u)) sv[i] = 0xFF800000u;  // -inf
+                            if (!((bits >> i) & 1u)) sv[32 * k + i] = 0xFF800000u;  // -inf
                     }
-                };
-                // two passes over the scores, 32 columns at a time (128 at once
-                // do not fit in registers); the other group's warps fill the
-                // load latency
-                float mx = -INFINITY;
-                uint32_t x[32];
-#pragma unroll
-                for (int k = 0; k < kBN / 32; ++k) {
-                    rx::tmem_ld32(tS + k * 32, x);
+                } else {
                     rx::tmem_wait_ld();
-                    hide(k, x);
-                    float a0 = mx, a1 = -INFINITY;
+                }
+                float mx;
+                {
+                    float a0 = -INFINITY, a1 = -INFINITY, a2 = -INFINITY, a3 = -INFINITY;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        a0 = rx::fmax3(a0, u2f(x[4 * i]), u2f(x[4 * i + 1]));
-                        a1 = rx::fmax3(a1, u2f(x[4 * i + 2]), u2f(x[4 * i + 3]));
+                    for (int k = 0; k < kBN / 8; ++k) {
+                        a0 = rx::fmax3(a0, u2f(sv[8 * k]), u2f(sv[8 * k + 1]));
+                        a1 = rx::fmax3(a1, u2f(sv[8 * k + 2]), u2f(sv[8 * k + 3]));
+                        a2 = rx::fmax3(a2, u2f(sv[8 * k + 4]), u2f(sv[8 * k + 5]));
+                        a3 = rx::fmax3(a3, u2f(sv[8 * k + 6]), u2f(sv[8 * k + 7]));
                     }
-                    mx = fmaxf(a0, a1);
+                    mx = rx::fmax3(fmaxf(a0, a1), a2, a3);
                 }
                 const float m_new = fmaxf(m_used, mx * sl2);
                 const bool need = valid && (m_used == -INFINITY || m_new > m_used + kRescale);
@@ -713,33 +712,32 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
                 }
                 const float mu = m_used == -INFINITY ? 0.f : m_used;
                 const uint64_t scale2 = rx::f2(sl2, sl2), negm2 = rx::f2(-mu, -mu);
-                uint64_t acc0 = 0, acc1 = 0;
+                uint64_t acc[4] = {0, 0, 0, 0};
 #pragma unroll
-                for (int k = 0; k < kBN / 32; ++k) {
-                    rx::tmem_ld32(tS + k * 32, x);
-                    rx::tmem_wait_ld();
-                    hide(k, x);
-                    uint32_t pk[16];
+                for (int k = 0; k < kBN / 64; ++k) {
+                    uint32_t pk[32];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
+                    for (int i = 0; i < 32; ++i) {
                         float x0, x1;
-                        rx::f2_split(rx::f2_fma(rx::f2(u2f(x[2 * i]), u2f(x[2 * i + 1])), scale2, negm2), x0, x1);
+                        rx::f2_split(rx::f2_fma(rx::f2(u2f(sv[64 * k + 2 * i]), u2f(sv[64 * k + 2 * i + 1])), scale2, negm2), x0, x1);
                         const float e0 = rx::fast_exp2(x0), e1 = rx::fast_exp2(x1);
-                        if (i & 1) acc1 = rx::f2_add(acc1, rx::f2(e0, e1));
-                        else acc0 = rx::f2_add(acc0, rx::f2(e0, e1));
+                        acc[i & 3] = rx::f2_add(acc[i & 3], rx::f2(e0, e1));
                         // the weights are rounded to the type of V's tile for
                         // the tensor core; their sum is not
                         pk[i] = F8 ? rx::pack_f16(e0, e1) : rx::pack_bf16(e0, e1);
                     }
-                    rx::tmem_st16(tS + k * 16, pk);  // over scores already read
+                    rx::tmem_st32(tS + k * 32, pk);  // over scores already read
                 }
                 float a0, a1;
-                rx::f2_split(rx::f2_add(acc0, acc1), a0, a1);
+                rx::f2_split(rx::f2_add(rx::f2_add(acc[0], acc[1]), rx::f2_add(acc[2], acc[3])), a0, a1);
                 l += a0 + a1;
                 if (__any_sync(0xffffffffu, scale_o)) {
-                    // the group's product before (tile n - 2) has completed: S(n) waited for it
+                    // O += P V of the tile before has to be complete
+                    if (!warp_wait(bar + 8 * L::B_PVDONE, (n - 1) & 1, abort_flag, p.status)) return;
+                    rx::tc_fence_after();
 #pragma unroll
                     for (int k = 0; k < D / 32; ++k) {
+                        uint32_t x[32];
                         rx::tmem_ld32(tO + k * 32, x);
                         rx::tmem_wait_ld();
 #pragma unroll
@@ -750,74 +748,55 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
                 rx::tmem_wait_st();
             }
             rx::tc_fence_before();
-            rx::mbar_arrive(bar + 8 * (L::B_PFULL + t));
+            rx::mbar_arrive(bar + 8 * (L::B_PFULL + buf));
         }
-        n0 += j1 - j0;
-        // the segment's result: both groups' products are complete
-        if (first < j1 && !warp_wait(bar + 8 * (L::B_PVDONE + t), ((n - 2) >> 1) & 1, abort_flag, p.status)) return;
-        // two buffers in turn: a group without a tile in the next segment is
-        // at its end while the other still reads this one's
-        float2 *ml = reinterpret_cast<float2 *>(smem + L::OFF_ML) + (s & 1) * 2 * kRows;
-        ml[t * kRows + row] = make_float2(m_used, l);
-        rx::tc_fence_before();
-        rx::named_bar_sync(1, 32 * kSoftWarps);
+        // the segment's result
+        if (!warp_wait(bar + 8 * L::B_PVDONE, (n - 1) & 1, abort_flag, p.status)) return;
         rx::tc_fence_after();
-        const float2 other = ml[(1 - t) * kRows + row];
-        const float m0 = t ? other.x : m_used, l0 = t ? other.y : l, m1 = t ? m_used : other.x, l1 = t ? l : other.y;
-        const float m = fmaxf(m0, m1);
-        // a group without a seen key has no O (its columns hold anything)
-        float f0 = l0 == 0.f ? 0.f : rx::fast_exp2(m0 - m), f1 = l1 == 0.f ? 0.f : rx::fast_exp2(m1 - m);
-        const float ls = f0 * l0 + f1 * l1;
-        const float inv = ls == 0.f ? 0.f : p.v_scale / ls;
-        f0 *= inv;
-        f1 *= inv;
         uint32_t *nf = reinterpret_cast<uint32_t *>(smem + L::OFF_NF) + (s % kRing) * 32;
         uint32_t any = 0;
         if (j1 * kBN > P)
             for (int i = 0; i < (T + 31) / 32; ++i) any |= nf[i];
         const bool whole = j0 == 0 && j1 == c.r.ntiles;
+        const float inv = l == 0.f ? 0.f : p.v_scale / l;
         const int64_t orow = tok * p.hq + (int64_t)c.g * p.G + row % p.G;
         const int64_t prow = (int64_t)(2 * blockIdx.x + (j0 == 0 ? 1 : 0)) * kRows + row;
         if (warp_on) {
+            uint32_t r[D];
 #pragma unroll
-            for (int k = 0; k < D / 64; ++k) {
-                const int col = t * (D / 2) + k * 32;
-                uint32_t a[32], b[32];
-                rx::tmem_ld32(tmem + lanes + 128 + col, a);
-                rx::tmem_ld32(tmem + lanes + 256 + 128 + col, b);
-                rx::tmem_wait_ld();
-                if (valid) {
-                    float x[32];
+            for (int k = 0; k < D / 32; ++k) rx::tmem_ld32(tO + k * 32, *reinterpret_cast<uint32_t(*)[32]>(r + 32 * k));
+            rx::tmem_wait_ld();
+            if (valid) {
+                if (whole) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(p.o + orow * D);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        x[i] = (l0 == 0.f ? 0.f : u2f(a[i]) * f0) + (l1 == 0.f ? 0.f : u2f(b[i]) * f1);
-                    if (whole) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(p.o + orow * D + col);
+                    for (int i = 0; i < D / 8; ++i) {
+                        uint32_t w[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            dst[i] = make_uint4(rx::pack_bf16(x[8 * i], x[8 * i + 1]), rx::pack_bf16(x[8 * i + 2], x[8 * i + 3]),
-                                                rx::pack_bf16(x[8 * i + 4], x[8 * i + 5]), rx::pack_bf16(x[8 * i + 6], x[8 * i + 7]));
-                    } else {
-                        float4 *dst = reinterpret_cast<float4 *>(p.part_o + prow * D + col);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) dst[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                        for (int k = 0; k < 4; ++k) w[k] = rx::pack_bf16(u2f(r[8 * i + 2 * k]) * inv, u2f(r[8 * i + 2 * k + 1]) * inv);
+                        dst[i] = l == 0.f ? make_uint4(0, 0, 0, 0) : make_uint4(w[0], w[1], w[2], w[3]);
                     }
+                } else {
+                    float4 *dst = reinterpret_cast<float4 *>(p.part_o + prow * D);
+#pragma unroll
+                    for (int i = 0; i < D / 4; ++i)
+                        dst[i] = l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                          : make_float4(u2f(r[4 * i]) * inv, u2f(r[4 * i + 1]) * inv,
+                                                        u2f(r[4 * i + 2]) * inv, u2f(r[4 * i + 3]) * inv);
                 }
-                __syncwarp();
-            }
-            if (valid && t == 0) {
-                const float l2 = ls == 0.f ? -INFINITY : m + log2f(ls);
+                const float l2 = l == 0.f ? -INFINITY : m_used + log2f(l);
                 if (!whole) p.part_l[prow] = l2;
                 else if (p.lse) p.lse[orow] = l2 * rx::kLn2;
             }
-        }
-        if (any) {  // the same for every thread: all have read the words, then they are cleared
-            if (valid) add_not_finite<D, F8>(p, nf, mrow, node, c.b, c.g, P, T, whole ? -1 : prow, orow, t * (D / 2));
-            rx::named_bar_sync(1, 32 * kSoftWarps);
-            if (threadIdx.x < 32) nf[threadIdx.x] = 0;
+            __syncwarp();
         }
         rx::tc_fence_before();
-        rx::mbar_arrive(bar + 8 * L::B_OEMPTY);
+        rx::mbar_arrive(bar + 8 * (L::B_OEMPTY + (s & 1)));
+        if (any) {  // the same for every thread: all have read the words, then they are cleared
+            if (valid) add_not_finite<D, F8>(p, nf, mrow, node, c.b, c.g, P, T, whole ? -1 : prow, orow);
+            rx::named_bar_sync(1, 32 * kSoftWarps);
+            if (row < 32) nf[row] = 0;
+        }
         if (!c.next(p)) return;
     }
 }
@@ -848,9 +827,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         for (int i = 0; i < 2; ++i) {
             rx::mbar_init(bar + 8 * (L::B_SFULL + i), 1);
             rx::mbar_init(bar + 8 * (L::B_PFULL + i), kRows);
-            rx::mbar_init(bar + 8 * (L::B_PVDONE + i), 1);
+            rx::mbar_init(bar + 8 * (L::B_OEMPTY + i), kRows);
         }
-        rx::mbar_init(bar + 8 * L::B_OEMPTY, 32 * kSoftWarps);
+        rx::mbar_init(bar + 8 * L::B_PVDONE, 1);
         rx::mbar_init(bar + 8 * L::B_FINAL, 1);
         *reinterpret_cast<volatile int *>(smem + L::OFF_ABORT) = 0;
         rx::fence_mbar_init();
@@ -883,7 +862,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         softmax_rows<D, F8>(p, smem, sbase);
     } else if (warp < kWarpQ) {
         rx::reg_dec<kRegsProd>();
-        producer<D, F8>(p, smem, sbase);
+        if (warp < kSoftWarps + kProdWarps) producer<D, F8, false>(p, smem, sbase);
+        else producer<D, F8, true>(p, smem, sbase);
     } else {
         rx::reg_dec<kRegsMisc>();
         if (warp == kWarpQ) {
@@ -980,7 +960,7 @@ struct TreePool {
 
 bool tree_shape_ok(int32_t batch, int32_t hq, int32_t hkv, int32_t D, int32_t max_tree)
 {
-    return batch >= 0 && batch <= 65535 && hq > 0 && hkv > 0 && hq % hkv == 0 && hq / hkv <= 128 &&
+    return batch >= 0 && batch <= 65535 && hq > 0 && hkv > 0 && hkv <= 8192 && hq % hkv == 0 && hq / hkv <= 128 &&
            (D == 64 || D == 128) && max_tree >= 1 && max_tree <= kMaxTree;
 }
 
