@@ -51,7 +51,8 @@ using rx::warp_wait;
 
 constexpr int kMaxTree = 1024;
 constexpr int kCtas = 152;           // CTAs of a call: one an SM
-constexpr int kRows = 128;           // query rows of a tile (MMA M)
+constexpr int kRows = 128;           // query rows of a row tile (MMA M)
+constexpr int kMaxNt = 2;            // row tiles that share a K/V tile
 constexpr int kBN = 128;             // positions of a K/V tile
 constexpr int kStages = 2;           // K ring and V ring depth
 constexpr int kProdWarps = 8;        // for K, and as many for V
@@ -59,45 +60,66 @@ constexpr int kProdRows = kBN / kProdWarps;  // rows of a tile each producer war
 constexpr int kSoftWarps = 4;        // one query row a thread
 constexpr int kWarpQ = kSoftWarps + 2 * kProdWarps;  // loads the query rows
 constexpr int kWarpMma = kWarpQ + 1;
-constexpr int kThreads = 32 * (kWarpQ + 4);          // two warps idle: register shares go by warpgroup
+constexpr int kWarpSched = kWarpQ + 2;               // hands out the segments
+constexpr int kThreads = 32 * (kWarpQ + 4);          // a warp idle: register shares go by warpgroup
 // registers a thread, by role (a softmax thread holds a row's 128 scores):
 // 128 x 192 + 512 x 56 + 128 x 56 of the 768 x 80 launched
 constexpr int kRegsSoft = 192, kRegsProd = 56, kRegsMisc = 56, kRegsLaunch = 80;
 static_assert(32 * (kSoftWarps * kRegsSoft + 2 * kProdWarps * kRegsProd + 4 * kRegsMisc) <= kThreads * kRegsLaunch,
               "a share is granted out of the launched registers only");
 static_assert(kThreads * kRegsLaunch <= 65536, "registers of an SM");
-constexpr int kRing = 4;             // per-segment words kept this many segments (see nf, qscale)
-constexpr int kCodeBufs = 3;         // FP8: half tiles of codes in flight, for K and for V
+constexpr int kSegs = 4;             // segments handed out ahead
+constexpr int kMaskT = 128;          // trees up to this size have their mask words in shared memory
+constexpr int kRing = 4;             // score scales kept (see query_loader)
 constexpr uint32_t kTmemCols = 512;  // buffer i: S (then P) at 256 i, O at 256 i + 128
 constexpr float kRescale = 8.f;      // log2 units the running max may lag
 constexpr int kMergeRows = 16;       // rows of one merge CTA
 constexpr int kMergeThreads = 128;
 
+// A segment: the position tiles [j0, j1) of a (kv head g, request, row tiles)
+// that are this CTA's.
+struct Seg {
+    int g, j0, j1;
+    int P, T;        // the request's prefix and drafted tokens
+    int row;         // of req_to_token
+    int node, ntok;  // the rows' drafted tokens: node .. node + ntok - 1 of the tree,
+    int tok;         //   the first of them at this query row
+    int nt;          // row tiles: 1 or 2
+    int whole;       // every tile of the context: the result is final
+    int last;        // the CTA's last segment
+};
+
 template <int D, bool F8>
 struct TL {
     static constexpr int NB = D / 64;             // 128-byte column blocks of a row
     static constexpr int BLK = kRows * 128;       // bytes of one column block of a tile
-    static constexpr int QB = F8 ? 1 : 2;         // query buffers (FP8: their room goes to the codes)
-    static constexpr int CODE = F8 ? kBN * D / 2 : 0;  // bytes of half a tile of codes
+    // query buffers: two for bf16 pools; one for FP8 pools, whose loads go
+    // through L1 and need the room there
+    static constexpr int QB = F8 ? 1 : 2;
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_K = OFF_Q + QB * NB * BLK;
     static constexpr int OFF_V = OFF_K + kStages * NB * BLK;
-    static constexpr int OFF_CODE = OFF_V + kStages * NB * BLK;
-    static constexpr int OFF_NF = OFF_CODE + 2 * kCodeBufs * CODE;        // kRing x 32 words
-    static constexpr int OFF_QS = OFF_NF + kRing * 32 * 4;            // kRing x 128 floats
-    static constexpr int OFF_SCAN = OFF_QS + kRing * kRows * 4;       // kThreads + 1 int64
-    static constexpr int OFF_BAR = OFF_SCAN + (kThreads + 1) * 8;
+    static constexpr int OFF_NF = OFF_V + kStages * NB * BLK;         // kSegs x 32 words
+    static constexpr int OFF_QS = OFF_NF + kSegs * 32 * 4;            // kRing x 128 floats
+    static constexpr int OFF_MASK = OFF_QS + kRing * kRows * 4;       // kSegs x 128 tokens x 4 words;
+    static constexpr int MASK = kSegs * kMaskT * (kMaskT / 32) * 4;   //   before them, the scan of the lengths
+    static_assert((kThreads + 1) * 8 <= MASK, "room for the scan");
+    static constexpr int OFF_SEG = OFF_MASK + MASK;
+    static constexpr int OFF_BAR = OFF_SEG + kSegs * 64;
     static constexpr int B_KFULL = 0, B_KEMPTY = B_KFULL + kStages, B_VFULL = B_KEMPTY + kStages,
                          B_VEMPTY = B_VFULL + kStages, B_QFULL = B_VEMPTY + kStages, B_QEMPTY = B_QFULL + QB,
                          B_SFULL = B_QEMPTY + QB, B_PFULL = B_SFULL + 2, B_PVDONE = B_PFULL + 2,
-                         B_OEMPTY = B_PVDONE + 1, B_FINAL = B_OEMPTY + 2, N_BAR = B_FINAL + 1;
+                         B_OEMPTY = B_PVDONE + 2, B_SEGFULL = B_OEMPTY + 2, B_SEGEMPTY = B_SEGFULL + kSegs,
+                         B_FINAL = B_SEGEMPTY + kSegs, N_BAR = B_FINAL + 1;
     static constexpr int OFF_TMEM = OFF_BAR + N_BAR * 8;
     static constexpr int OFF_ABORT = OFF_TMEM + 8;
-    static constexpr int OFF_START = OFF_ABORT + 8;                   // Cursor of the CTA's first unit
-    static constexpr int BYTES = OFF_START + 64 + 1024;               // + room to align the base to 1024
+    static constexpr int OFF_START = OFF_ABORT + 8;                   // Start
+    static constexpr int BYTES = OFF_START + 32 + 1024;               // + room to align the base to 1024
 };
-static_assert(TL<128, false>::BYTES <= 226 * 1024 && TL<128, true>::BYTES <= 226 * 1024, "shared memory budget");
-static_assert(TL<128, false>::OFF_SCAN % 8 == 0 && TL<128, false>::OFF_BAR % 8 == 0, "alignment");
+static_assert(sizeof(Seg) <= 64, "room of a segment");
+static_assert(TL<128, false>::BYTES <= 226 * 1024, "shared memory budget");
+static_assert(TL<128, true>::BYTES <= 194 * 1024, "leaves 60 KB of L1");
+static_assert(TL<128, false>::OFF_MASK % 16 == 0 && TL<128, false>::OFF_BAR % 8 == 0, "alignment");
 
 struct TParams {
     const bf16 *q;
@@ -106,7 +128,9 @@ struct TParams {
     const unsigned char *k;
     const unsigned char *v;
     int64_t num_slots;
-    int hq, hkv, G, tb;     // tb: drafted tokens of a row tile, 128 / G
+    int hq, hkv, G;
+    int tb;                 // drafted tokens of a row tile: 128 / G
+    int nt;                 // row tiles that share a K/V tile
     const int32_t *qo_indptr;
     const int32_t *req_idx;
     const int32_t *prefix_len;
@@ -117,8 +141,8 @@ struct TParams {
     int batch, max_tree;
     float scale_log2;   // sm_scale log2(e), times K's scale for an FP8 pool
     float v_scale;      // V's scale for an FP8 pool; 1 otherwise
-    float *part_o;      // [2 kCtas][128][D] partial results, normalised
-    float *part_l;      // [2 kCtas][128] their log2-sum-exps
+    float *part_o;      // [2 kCtas][128 nt][D] partial results, normalised
+    float *part_l;      // [2 kCtas][128 nt] their log2-sum-exps
     int32_t *status;
 };
 
@@ -126,9 +150,12 @@ struct TParams {
 // the list of work
 // ---------------------------------------------------------------------------
 
+// The list is (kv head g, request b, group qt of nt row tiles, position tile
+// j), j innermost; a unit is one entry.
 struct Req {
     int T, P;
     int row;          // of req_to_token
+    int tok;          // its first query row
     int ntiles, nqt;  // 0 where there is nothing to do (no drafted token, or lengths out of range)
 
     __device__ __forceinline__ int64_t units() const { return (int64_t)ntiles * nqt; }
@@ -137,7 +164,8 @@ struct Req {
 __device__ __forceinline__ Req load_req(const TParams &p, int b, bool flag = false)
 {
     Req r;
-    r.T = __ldg(p.qo_indptr + b + 1) - __ldg(p.qo_indptr + b);
+    r.tok = __ldg(p.qo_indptr + b);
+    r.T = __ldg(p.qo_indptr + b + 1) - r.tok;
     r.P = __ldg(p.prefix_len + b);
     r.row = __ldg(p.req_idx + b);
     r.ntiles = r.nqt = 0;
@@ -147,35 +175,13 @@ __device__ __forceinline__ Req load_req(const TParams &p, int b, bool flag = fal
         return r;
     }
     r.ntiles = (int)(((int64_t)r.P + r.T + kBN - 1) / kBN);
-    r.nqt = (r.T + p.tb - 1) / p.tb;
+    r.nqt = (r.T + p.tb * p.nt - 1) / (p.tb * p.nt);
     return r;
 }
 
-// A place in the list: kv head g, request b, row tile qt, position tile j.
-struct Cursor {
-    int left;  // units of this CTA from here on
-    int g, b, qt, j;
-    Req r;
-
-    // position tiles of the segment (g, b, qt) that are this CTA's, from j on
-    __device__ __forceinline__ int end() const { return left < r.ntiles - j ? j + left : r.ntiles; }
-    // to the CTA's next segment; false when there is none
-    __device__ __forceinline__ bool next(const TParams &p)
-    {
-        left -= end() - j;
-        if (left <= 0) return false;
-        j = 0;
-        if (++qt < r.nqt) return true;
-        qt = 0;
-        do {
-            if (++b == p.batch) {
-                b = 0;
-                ++g;
-            }
-            r = load_req(p, b);
-        } while (r.ntiles == 0);
-        return true;
-    }
+// A place in the list, and how many units of it from there on.
+struct Start {
+    int g, b, qt, j, left;
 };
 
 // Exclusive prefix sums of the requests' units, `per` requests a thread, into
@@ -210,57 +216,136 @@ __device__ int64_t scan_units(const TParams &p, int64_t *pre, int per, bool flag
     return total;
 }
 
-// The place of unit u (0 <= u < hkv * per_head).
+// The place of unit u (0 <= u < hkv * per_head); r: its request.
 template <int THREADS>
-__device__ Cursor locate(const TParams &p, const int64_t *pre, int per, int64_t per_head, int64_t u)
+__device__ Start locate(const TParams &p, const int64_t *pre, int per, int64_t per_head, int64_t u, Req &r)
 {
-    Cursor c;
+    Start c;
     c.left = 0;
     c.g = (int)(u / per_head);
-    int64_t r = u - c.g * per_head;
-    int lo = 0, hi = THREADS - 1;  // the thread whose requests hold unit r
+    int64_t x = u - c.g * per_head;
+    int lo = 0, hi = THREADS - 1;  // the thread whose requests hold unit x
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (pre[mid] <= r) lo = mid; else hi = mid - 1;
+        if (pre[mid] <= x) lo = mid; else hi = mid - 1;
     }
-    r -= pre[lo];
+    x -= pre[lo];
     c.b = lo * per;
-    for (c.r = load_req(p, c.b); r >= c.r.units(); c.r = load_req(p, c.b)) {
-        r -= c.r.units();
+    for (r = load_req(p, c.b); x >= r.units(); r = load_req(p, c.b)) {
+        x -= r.units();
         ++c.b;
     }
-    c.qt = (int)(r / c.r.ntiles);
-    c.j = (int)(r - (int64_t)c.qt * c.r.ntiles);
-    return c;
-}
-
-// The CTA's first place, as thread 0 left it in shared memory.
-template <typename L>
-__device__ __forceinline__ Cursor start_of(const unsigned char *smem)
-{
-    const volatile int *w = reinterpret_cast<const volatile int *>(smem + L::OFF_START);
-    Cursor c;
-    int *d = reinterpret_cast<int *>(&c);
-#pragma unroll
-    for (int i = 0; i < (int)(sizeof(Cursor) / 4); ++i) d[i] = w[i];
+    c.qt = (int)(x / r.ntiles);
+    c.j = (int)(x - (int64_t)c.qt * r.ntiles);
     return c;
 }
 
 // First unit of CTA c out of `ctas` (no more CTAs than units: none is empty).
 __device__ __forceinline__ int64_t first_unit(int64_t total, int ctas, int c) { return total * c / ctas; }
 
+// One warp walks the CTA's share and hands its segments to the other roles,
+// up to kSegs ahead, each with its tree's mask words where positions of the
+// tree are among its tiles: under load a read of global memory takes
+// microseconds, which no other role then waits for.  The lanes hold the
+// lengths of 32 requests at a time.
+template <int D, bool F8>
+__device__ void scheduler(const TParams &p, unsigned char *smem, uint32_t sbase)
+{
+    using L = TL<D, F8>;
+    const uint32_t bar = sbase + L::OFF_BAR;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
+    const int lane = threadIdx.x & 31;
+    Start c = *reinterpret_cast<const Start *>(smem + L::OFF_START);
+    int base = c.b;
+    Req mine;  // of request base + lane
+    auto fill = [&]() {
+        mine.ntiles = 0;
+        if (base + lane < p.batch) mine = load_req(p, base + lane);
+    };
+    fill();
+    for (int s = 0;; ++s) {
+        const int slot = s % kSegs, l = c.b - base;
+        if (s >= kSegs && !warp_wait(bar + 8 * (L::B_SEGEMPTY + slot), (s / kSegs - 1) & 1, abort_flag, p.status)) break;
+        Seg g;
+        const int ntiles = __shfl_sync(0xffffffffu, mine.ntiles, l), nqt = __shfl_sync(0xffffffffu, mine.nqt, l);
+        g.g = c.g;
+        g.P = __shfl_sync(0xffffffffu, mine.P, l);
+        g.T = __shfl_sync(0xffffffffu, mine.T, l);
+        g.row = __shfl_sync(0xffffffffu, mine.row, l);
+        g.j0 = c.j;
+        g.j1 = c.left < ntiles - c.j ? c.j + c.left : ntiles;
+        g.node = c.qt * p.tb * p.nt;
+        g.ntok = min(p.tb * p.nt, g.T - g.node);
+        g.tok = __shfl_sync(0xffffffffu, mine.tok, l) + g.node;
+        g.nt = g.ntok > p.tb ? 2 : 1;
+        g.whole = g.j0 == 0 && g.j1 == ntiles;
+        c.left -= g.j1 - g.j0;
+        g.last = c.left <= 0;
+        if (lane == 0) *reinterpret_cast<Seg *>(smem + L::OFF_SEG + slot * 64) = g;
+        if (p.mask && g.T <= kMaskT && g.j1 * kBN > g.P) {
+            const int W = (g.T + 31) / 32;
+            const uint32_t dst = sbase + L::OFF_MASK + slot * (kMaskT * (kMaskT / 32) * 4);
+            for (int i = lane; i < g.ntok * W; i += 32) {
+                const int t = i / W, w = i - t * W;
+                rx::cp_async_4(dst + (t * (kMaskT / 32) + w) * 4, p.mask + (int64_t)(g.tok + t) * p.words + w, 4);
+            }
+        }
+        rx::cp_async_mbar_arrive(bar + 8 * (L::B_SEGFULL + slot));  // the words, as they land
+        __syncwarp();
+        if (lane == 0) rx::mbar_arrive(bar + 8 * (L::B_SEGFULL + slot));  // the segment
+        if (g.last) break;
+        c.j = 0;
+        if (++c.qt < nqt) continue;
+        c.qt = 0;
+        unsigned next;  // the next request with anything to do: there is one
+        do {
+            const int from = c.b - base;
+            next = __ballot_sync(0xffffffffu, mine.ntiles > 0) & (from >= 31 ? 0u : 0xFFFFFFFEu << (from < 0 ? 0 : from));
+            if (from < 0) next = __ballot_sync(0xffffffffu, mine.ntiles > 0);
+            if (!next) {
+                base += 32;
+                if (base >= p.batch) {
+                    base = 0;
+                    ++c.g;
+                }
+                c.b = base - 1;
+                fill();
+            }
+        } while (!next);
+        c.b = base + __ffs(next) - 1;
+    }
+    rx::cp_async_wait_all();
+}
+
+// The CTA's segment s for another role; false when a wait gave up.  The role
+// arrives on the segment's empty barrier once it needs it no more.
+template <typename L>
+__device__ __forceinline__ bool get_seg(int s, Seg &g, unsigned char *smem, uint32_t sbase, int32_t *status)
+{
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
+    if (!wait_or_abort(sbase + L::OFF_BAR + 8 * (L::B_SEGFULL + s % kSegs), (s / kSegs) & 1, abort_flag, status)) return false;
+    const int4 *w = reinterpret_cast<const int4 *>(smem + L::OFF_SEG + (s % kSegs) * 64);
+    const int4 a = w[0], b = w[1], c = w[2];
+    g = Seg{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
+    return true;
+}
+template <typename L>
+__device__ __forceinline__ void free_seg(int s, uint32_t sbase)
+{
+    rx::mbar_arrive(sbase + L::OFF_BAR + 8 * (L::B_SEGEMPTY + s % kSegs));
+}
+
 // ---------------------------------------------------------------------------
 // which drafted tokens a row sees
 // ---------------------------------------------------------------------------
 
 // Word i of drafted token `node`'s mask: prefix positions (i < 0) are seen,
-// bits at and past T are not.  Without branches around the load, so that the
-// loads of several words go out together.
-__device__ __forceinline__ uint32_t mask_word(const TParams &p, const uint32_t *row, int node, int T, int i)
+// bits at and past T are not.  row: its words, or null for a chain.
+__device__ __forceinline__ uint32_t mask_word(const uint32_t *row, int words, int node, int T, int i)
 {
     uint32_t w = 0xFFFFFFFFu;
     int n = T - 32 * i;  // drafted tokens from bit 0 of this word on
-    if (row) w = __ldg(row + min(max(i, 0), p.words - 1));
+    if (row) w = row[min(max(i, 0), words - 1)];
     else n = min(n, node + 1 - 32 * i);
     w = n >= 32 ? w : n <= 0 ? 0u : w & ((1u << (n & 31)) - 1u);
     return i < 0 ? 0xFFFFFFFFu : w;
@@ -293,24 +378,24 @@ __device__ __forceinline__ uint4 widen_f16(uint32_t lo, uint32_t hi)
 }
 
 // Eight producer warps for K and eight for V (V's wait for the softmax does
-// not hold up K); warp w gathers rows [16 w, 16 w + 16) of every tile with
-// 16-byte async copies, slot ids two tiles ahead.  (Loads into registers go
-// through L1, which this kernel's shared memory leaves 28 KB: with 64 KB meant
-// to be in flight they ran at half the rate.)
+// not hold up K); warp w gathers rows [16 w, 16 w + 16) of every tile in
+// 16-byte pieces, slot ids two tiles ahead.
 //
-// bf16 pools: the copies land in the swizzled tile itself and report to its
-// barrier.  FP8 pools: they land in a ring of three half tiles of codes; each
-// thread widens the chunks that it copied (E4M3 to f16 is exact) and stores
-// them to the tile.
+// bf16 pools: async copies that land in the swizzled tile itself and report to
+// its barrier (loads into registers go through L1, which this much shared
+// memory leaves 28 KB: they ran at half the rate).  FP8 pools: loads into
+// registers, a tile ahead, widened (E4M3 to f16 is exact) and stored to the
+// tile; half the bytes and one query buffer less leave 60 KB of L1 for them,
+// and codes copied to shared memory first would cost two more passes through
+// it, which the tensor core's operands keep busy.
 //
-// V at drafted positions passes through registers in both: a NaN or infinity
-// there would reach rows that do not see the position (0 * inf), so it is
-// dropped, noted, and added back to the rows that see it at the end.
+// V at drafted positions is looked at before it is handed over: a NaN or
+// infinity there would reach rows that do not see the position (0 * inf), so it
+// is dropped, noted, and added back to the rows that see it at the end.
 template <int D, bool F8, bool IS_V>
 __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
 {
     using L = TL<D, F8>;
-    Cursor c = start_of<L>(smem);
     constexpr int EB = F8 ? 1 : 2;                    // bytes of a value
     constexpr int CPR = D * EB / 16;                  // 16-byte chunks of a row
     constexpr int RPI = 32 / CPR;                     // rows of one instruction
@@ -322,121 +407,122 @@ __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
     const int lane = threadIdx.x & 31, pw = ((int)(threadIdx.x >> 5) - kSoftWarps) % kProdWarps;
     const int r0 = pw * kProdRows;
     const int sub = lane / CPR, ch = lane % CPR;
-    const int row_bytes = p.hkv * D * EB;             // at most 2^15 heads (host check)
+    const int row_bytes = p.hkv * D * EB;             // at most 2^21 (the heads are bounded)
 
     struct Tile {
         int32_t slot;  // lane l < 16: slot of row r0 + l, in flight until check() looks at it
-        int g;
-        int rel;       // the tile's first position, from the first drafted one
-        int seg;       // segment mod kRing; -1: no tile
-        bool in;       // row r0 + l is a position of the request
+        int lim;       // positions of the request from the tile's first on; 0: no tile
+        int meta;      // kv head, T, segment mod kSegs: bits 0, 13 and 24 on
+
+        __device__ __forceinline__ int g() const { return meta & 0x1FFF; }
+        __device__ __forceinline__ int rel() const { return ((meta >> 13) & 0x7FF) - lim; }  // first position, from the first drafted one
+        __device__ __forceinline__ int seg() const { return meta >> 24; }
     };
-    int seg = 0;
-    // the tile at the cursor, with the loads of its slot ids; then on to the next
+    static_assert(kMaxTree < 2048 && kSegs <= 64, "the fields of meta");
+    // the segment being handed out: its next tile, and how many it still has
+    int s = -1, left = 0, lim = 0, meta = 0;
+    bool last = false;
+    const int32_t *slots = nullptr;  // of this lane's row in that tile
+    // the next tile, with the loads of its slot ids
     auto take = [&](Tile &t) {
-        t.seg = t.slot = -1;
-        t.g = t.rel = 0;
-        t.in = false;
-        if (c.left <= 0) return;
-        t.g = c.g;
-        t.rel = c.j * kBN - c.r.P;
-        t.seg = seg % kRing;
-        const int pos = c.j * kBN + r0 + lane;
-        t.in = lane < kProdRows && pos < c.r.P + c.r.T;
-        if (t.in) t.slot = rx::ld_stream_b32(p.rtt + (int64_t)c.r.row * p.rtt_stride + pos);
-        if (c.j + 1 < c.r.ntiles) {
-            ++c.j;
-            --c.left;
-        } else {
-            ++seg;
-            c.next(p);  // the tile at j is the segment's last
+        t.slot = -1;
+        t.lim = 0;
+        if (left == 0) {
+            if (last) return;
+            Seg q;
+            if (!__all_sync(0xffffffffu, get_seg<L>(s + 1, q, smem, sbase, p.status))) {
+                last = true;  // gave up
+                return;
+            }
+            __syncwarp();
+            ++s;
+            if (lane == 0) free_seg<L>(s, sbase);
+            left = q.j1 - q.j0;
+            lim = q.P + q.T - q.j0 * kBN;
+            meta = q.g | (q.T << 13) | ((s % kSegs) << 24);
+            last = q.last;
+            slots = p.rtt + (int64_t)q.row * p.rtt_stride + (int64_t)q.j0 * kBN + r0 + lane;
         }
+        t.lim = lim;
+        t.meta = meta;
+        if (lane < kProdRows && r0 + lane < lim) t.slot = rx::ld_stream_b32(slots);
+        --left;
+        lim -= kBN;
+        slots += kBN;
     };
     // slots past the end or outside the pool (flagged) become -1
     auto check = [&](Tile &t) {
-        const bool ok = t.in && t.slot >= 0 && (int64_t)t.slot < p.num_slots;
-        if (t.in && !ok && p.status) atomicOr(p.status, RX_DEV_BAD_SLOT);
-        if (!ok) t.slot = -1;
+        if (t.slot >= 0 && (int64_t)t.slot < p.num_slots) return;
+        if (lane < kProdRows && r0 + lane < t.lim && p.status) atomicOr(p.status, RX_DEV_BAD_SLOT);
+        t.slot = -1;
     };
     auto source = [&](const Tile &t, int u, bool &ok) {
-        const int32_t s = __shfl_sync(0xffffffffu, t.slot, u * RPI + sub);
-        ok = s >= 0;
-        return pool + (ok ? (int64_t)s * row_bytes : 0) + (t.g * (D * EB) + ch * 16);
+        const int32_t id = __shfl_sync(0xffffffffu, t.slot, u * RPI + sub);
+        ok = id >= 0;
+        return pool + (ok ? (int64_t)id * row_bytes : 0) + (t.g() * (D * EB) + ch * 16);
     };
-    auto note = [&](const Tile &t, int r) {
-        const int e = t.rel + r;
-        atomicOr(reinterpret_cast<uint32_t *>(smem + L::OFF_NF) + t.seg * 32 + (e >> 5), 1u << (e & 31));
+    auto load = [&](const Tile &t, int u) {
+        bool ok;
+        const unsigned char *src = source(t, u, ok);
+        return ok ? rx::ld_stream(src) : make_uint4(0, 0, 0, 0);
+    };
+    // this thread's chunks of V at drafted positions, once they are in the tile
+    auto scrub = [&](uint32_t off, const Tile &t) {
+        constexpr int CH = F8 ? 2 : 1;  // 16-byte chunks of the tile for one of the row
+#pragma unroll 1
+        for (int u = 0; u < U * CH; ++u) {
+            const int r = r0 + u / CH * RPI + sub, e = t.rel() + r;
+            uint4 *at = reinterpret_cast<uint4 *>(smem + off + sw128(r, CH * ch + u % CH, L::BLK));
+            uint4 x = *at;
+            if (e >= 0 && drop_not_finite<F8>(x)) {
+                *at = x;
+                atomicOr(reinterpret_cast<uint32_t *>(smem + L::OFF_NF) + t.seg() * 32 + (e >> 5), 1u << (e & 31));
+            }
+        }
     };
 
-    Tile cur, nxt, nx2;
-    take(cur);
-    take(nxt);
     if constexpr (!F8) {
-        for (int n = 0; cur.seg >= 0; ++n) {
+        Tile cur, nxt, nx2;
+        take(cur);
+        take(nxt);
+        for (int n = 0; cur.lim > 0; ++n) {
             const int st = n % kStages;
             take(nx2);
             check(cur);
             const uint32_t off = (IS_V ? L::OFF_V : L::OFF_K) + st * L::NB * L::BLK;
             if (n >= kStages && !warp_wait(bar_empty + 8 * st, (n / kStages - 1) & 1, abort_flag, p.status)) break;
-            if (!IS_V || cur.rel + kBN <= 0) {
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    bool ok;
-                    const unsigned char *src = source(cur, u, ok);
-                    rx::cp_async_16(sbase + off + sw128(r0 + u * RPI + sub, ch, L::BLK), src, ok ? 16 : 0);
-                }
-                rx::cp_async_mbar_arrive(bar_full + 8 * st);
-            } else {
-                constexpr int H = U / 2;  // half the rows at a time
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint4 x[H];
-#pragma unroll
-                    for (int u = 0; u < H; ++u) {
-                        bool ok;
-                        const unsigned char *src = source(cur, h * H + u, ok);
-                        x[u] = make_uint4(0, 0, 0, 0);
-                        if (ok) x[u] = rx::ld_stream(src);
-                    }
-#pragma unroll
-                    for (int u = 0; u < H; ++u) {
-                        const int r = r0 + (h * H + u) * RPI + sub;
-                        if (cur.rel + r >= 0 && drop_not_finite<false>(x[u])) note(cur, r);
-                        *reinterpret_cast<uint4 *>(smem + off + sw128(r, ch, L::BLK)) = x[u];
-                    }
-                }
+#pragma unroll 2
+            for (int u = 0; u < U; ++u) {
+                bool ok;
+                const unsigned char *src = source(cur, u, ok);
+                rx::cp_async_16(sbase + off + sw128(r0 + u * RPI + sub, ch, L::BLK), src, ok ? 16 : 0);
+            }
+            if (IS_V && cur.rel() + kBN > 0) {  // the tile has drafted positions
+                rx::cp_async_wait_all();
+                scrub(off, cur);
                 rx::fence_proxy_async_smem();
                 rx::mbar_arrive(bar_full + 8 * st);
+            } else {
+                rx::cp_async_mbar_arrive(bar_full + 8 * st);
             }
             cur = nxt;
             nxt = nx2;
         }
+        rx::cp_async_wait_all();  // nothing may still be landing when the CTA exits
     } else {
-        constexpr int H = U / 2;  // instructions of half a tile
-        // chunk u of half-tile buffer b: + b CODE + 512 u
-        const uint32_t mine = L::OFF_CODE + (IS_V ? kCodeBufs * L::CODE : 0) + (uint32_t)(pw * H * 32 + lane) * 16;
-        auto fetch = [&](const Tile &t, int item) {  // item = 2 n + half
+        // the rows in two halves: a half's registers take the next tile's codes
+        // as soon as they are stored
+        constexpr int H = U / 2;
+        uint4 x[U];
+        auto fetch = [&](const Tile &t, int h) {
 #pragma unroll
-            for (int u = 0; u < H; ++u) {
-                bool ok;
-                const unsigned char *src = source(t, (item & 1) * H + u, ok);
-                rx::cp_async_16(sbase + mine + (item % kCodeBufs) * L::CODE + u * 512, src, ok ? 16 : 0);
-            }
-            rx::cp_async_commit();
+            for (int u = h * H; u < (h + 1) * H; ++u) x[u] = load(t, u);
         };
-        // this thread's chunks of a landed half into the tile at `off`
-        auto widen = [&](uint32_t off, const Tile &t, int item) {
-            const bool drafted = IS_V && t.rel + kBN > 0;
+        auto widen = [&](uint32_t off, int h) {
 #pragma unroll
-            for (int u = 0; u < H; ++u) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(smem + mine + (item % kCodeBufs) * L::CODE + u * 512);
-                uint4 a = widen_f16(x.x, x.y), b = widen_f16(x.z, x.w);
-                const int r = r0 + ((item & 1) * H + u) * RPI + sub;
-                if (drafted && t.rel + r >= 0) {
-                    bool nf = drop_not_finite<true>(a);
-                    nf |= drop_not_finite<true>(b);
-                    if (nf) note(t, r);
-                }
+            for (int u = h * H; u < (h + 1) * H; ++u) {
+                const uint4 a = widen_f16(x[u].x, x[u].y), b = widen_f16(x[u].z, x[u].w);
+                const int r = r0 + u * RPI + sub;
                 // the upper lanes of a row store their second chunk first: the
                 // two column blocks of a row lie on the same banks
                 const int swap = D == 128 ? (ch >> 2) & 1 : 0;
@@ -444,30 +530,28 @@ __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
                 *reinterpret_cast<uint4 *>(smem + off + sw128(r, 2 * ch + 1 - swap, L::BLK)) = swap ? a : b;
             }
         };
+        Tile cur, nxt;
+        take(cur);
+        take(nxt);
         check(cur);
-        check(nxt);
         fetch(cur, 0);
         fetch(cur, 1);
-        fetch(nxt, 2);
-        for (int n = 0; cur.seg >= 0; ++n) {
+        for (int n = 0; cur.lim > 0; ++n) {
             const int st = n % kStages;
             const uint32_t off = (IS_V ? L::OFF_V : L::OFF_K) + st * L::NB * L::BLK;
-            take(nx2);
-            rx::cp_async_wait<2>();     // the first half of tile n
+            check(nxt);
             if (n >= kStages && !warp_wait(bar_empty + 8 * st, (n / kStages - 1) & 1, abort_flag, p.status)) break;
-            widen(off, cur, 2 * n);
-            fetch(nxt, 2 * n + 3);
-            rx::cp_async_wait<2>();     // the second
-            widen(off, cur, 2 * n + 1);
+            widen(off, 0);
+            fetch(nxt, 0);
+            widen(off, 1);
+            fetch(nxt, 1);
+            if (IS_V && cur.rel() + kBN > 0) scrub(off, cur);  // the tile has drafted positions
             rx::fence_proxy_async_smem();
             rx::mbar_arrive(bar_full + 8 * st);
-            check(nx2);
-            fetch(nx2, 2 * n + 4);
             cur = nxt;
-            nxt = nx2;
+            take(nxt);
         }
     }
-    rx::cp_async_wait_all();  // nothing may still be landing when the CTA exits
 }
 
 // ---------------------------------------------------------------------------
@@ -484,21 +568,27 @@ template <int D, bool F8>
 __device__ void query_loader(const TParams &p, unsigned char *smem, uint32_t sbase)
 {
     using L = TL<D, F8>;
-    Cursor c = start_of<L>(smem);
     constexpr int CPR = D / 8;
     const uint32_t bar = sbase + L::OFF_BAR;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
     const int lane = threadIdx.x & 31;
+    int qi = 0;  // row tiles so far
     for (int s = 0;; ++s) {
-        const int buf = s % L::QB;
-        const int t0 = c.qt * p.tb, M = min(p.tb, c.r.T - t0) * p.G;
-        const int64_t tok0 = (int64_t)__ldg(p.qo_indptr + c.b) + t0;
-        if (s >= L::QB && !warp_wait(bar + 8 * (L::B_QEMPTY + buf), (s / L::QB - 1) & 1, abort_flag, p.status)) break;
+        Seg g;
+        if (!__all_sync(0xffffffffu, get_seg<L>(s, g, smem, sbase, p.status))) break;
+        __syncwarp();
+        if (lane == 0) free_seg<L>(s, sbase);
+        bool ok = true;
+        for (int t = 0; t < g.nt && ok; ++t, ++qi) {
+        const int buf = qi % L::QB;
+        const int M = min(p.tb, g.ntok - t * p.tb) * p.G;
+        const int64_t tok0 = (int64_t)g.tok + t * p.tb;
+        if (qi >= L::QB && !(ok = warp_wait(bar + 8 * (L::B_QEMPTY + buf), (qi / L::QB - 1) & 1, abort_flag, p.status))) break;
         const uint32_t dst = sbase + L::OFF_Q + buf * L::NB * L::BLK;
         for (int i0 = 0; i0 < M * CPR; i0 += 32) {
             const int i = i0 + lane, r = i / CPR, ch = i % CPR;
             const bool in = i < M * CPR;
-            const bf16 *src = in ? p.q + ((tok0 + r / p.G) * p.hq + (int64_t)c.g * p.G + r % p.G) * D + ch * 8 : p.q;
+            const bf16 *src = in ? p.q + ((tok0 + r / p.G) * p.hq + (int64_t)g.g * p.G + r % p.G) * D + ch * 8 : p.q;
             if constexpr (!F8) {
                 if (in) rx::cp_async_16(dst + sw128(r, ch, L::BLK), src, 16);
             } else {
@@ -519,7 +609,7 @@ __device__ void query_loader(const TParams &p, unsigned char *smem, uint32_t sba
                 if (in) {
                     *reinterpret_cast<uint4 *>(smem + (dst - sbase) + sw128(r, ch, L::BLK)) = make_uint4(y[0], y[1], y[2], y[3]);
                     if (ch == 0)
-                        reinterpret_cast<float *>(smem + L::OFF_QS)[(s % kRing) * kRows + r] =
+                        reinterpret_cast<float *>(smem + L::OFF_QS)[(qi % kRing) * kRows + r] =
                             __uint_as_float((uint32_t)(127 - 14 + e) << 23);
                 }
             }
@@ -530,7 +620,8 @@ __device__ void query_loader(const TParams &p, unsigned char *smem, uint32_t sba
         } else {
             rx::cp_async_mbar_arrive(bar + 8 * (L::B_QFULL + buf));
         }
-        if (!c.next(p)) break;
+        }
+        if (!ok || g.last) break;
     }
     rx::cp_async_wait_all();
 }
@@ -539,15 +630,17 @@ __device__ void query_loader(const TParams &p, unsigned char *smem, uint32_t sba
 // MMA thread
 // ---------------------------------------------------------------------------
 
-// Over the CTA's tiles n = 0, 1, ... (all segments in a row): S(n) into buffer
-// n & 1, then O += P V of tile n - 1, O of segment s in buffer s & 1.  P(n - 2)
-// sits in the columns that S(n) overwrites, so S(n) waits for that product's
-// completion.
-template <int D, bool F8>
+// Over the CTA's items i = 0, 1, ...: for every position tile n (all segments
+// in a row) the segment's row tiles t.  S(i) = Q_t K_n^T into buffer i & 1, then
+// O_t += P V of item i - 1; the O (and Q) of the q-th row tile of the CTA in
+// buffer q & 1.  P(i - 2) sits in the columns that S(i) overwrites, so S(i)
+// waits for that product's completion.  The products of odd and even items
+// complete on barriers of their own: whoever waits for one knows that the one
+// two items before has completed, so a phase's parity is never ambiguous.
+template <int D, bool F8, int NT>
 __device__ void mma_issuer(const TParams &p, unsigned char *smem, uint32_t sbase)
 {
     using L = TL<D, F8>;
-    Cursor c = start_of<L>(smem);
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::OFF_TMEM);
     const uint32_t bar = sbase + L::OFF_BAR;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
@@ -558,54 +651,65 @@ __device__ void mma_issuer(const TParams &p, unsigned char *smem, uint32_t sbase
     const uint64_t dk = rx::sdesc_sw128(sbase + L::OFF_K, 16, 1024);
     const uint64_t dv = rx::sdesc_sw128(sbase + L::OFF_V, L::BLK, 1024);
 
-    auto issue_s = [&](int n, int s, bool first, bool last) -> bool {
-        const int st = n % kStages, buf = n & 1;
-        if (first && !wait(L::B_QFULL + s % L::QB, (s / L::QB) & 1)) return false;
-        if (!wait(L::B_KFULL + st, (n / kStages) & 1)) return false;
-        if (n >= 2 && !wait(L::B_PVDONE, n & 1)) return false;  // O += P V of tile n - 2 (the same parity)
+    struct Item {
+        int i, n, q;                   // item, position tile, row tile
+        bool t0, t1;                   // the first, the last row tile of the position tile
+        bool first, last;              // the row tile's first, last position tile
+    };
+    auto issue_s = [&](const Item &m) -> bool {
+        const int st = m.n % kStages, buf = m.i & 1, qb = m.q % L::QB;
+        if (m.first && !wait(L::B_QFULL + qb, (m.q / L::QB) & 1)) return false;
+        if (m.t0 && !wait(L::B_KFULL + st, (m.n / kStages) & 1)) return false;
+        if (m.i >= 2 && !wait(L::B_PVDONE + buf, ((m.i >> 1) - 1) & 1)) return false;  // O += P V of item i - 2
         rx::fence_proxy_async_smem();  // rows landed by cp.async -> async proxy
         rx::tc_fence_after();
         const uint64_t dks = dk + (uint64_t)((st * L::NB * L::BLK) >> 4);
-        const uint64_t dqs = dq + (uint64_t)(((s % L::QB) * L::NB * L::BLK) >> 4);
+        const uint64_t dqs = dq + (uint64_t)((qb * L::NB * L::BLK) >> 4);
 #pragma unroll
         for (int kb = 0; kb < D / 16; ++kb) {
             const uint64_t off = (uint64_t)(((kb >> 2) * L::BLK + (kb & 3) * 32) >> 4);
             rx::tc_mma(tmem + buf * 256, dqs + off, dks + off, idesc_qk, kb > 0);
         }
         rx::tc_commit(bar + 8 * (L::B_SFULL + buf));
-        rx::tc_commit(bar + 8 * (L::B_KEMPTY + st));
-        if (last) rx::tc_commit(bar + 8 * (L::B_QEMPTY + s % L::QB));
+        if (m.t1) rx::tc_commit(bar + 8 * (L::B_KEMPTY + st));
+        if (m.last) rx::tc_commit(bar + 8 * (L::B_QEMPTY + qb));
         return true;
     };
-    auto issue_pv = [&](int n, int s, bool first) -> bool {
-        const int st = n % kStages, buf = n & 1;
-        if (!wait(L::B_PFULL + buf, (n >> 1) & 1)) return false;
-        if (!wait(L::B_VFULL + st, (n / kStages) & 1)) return false;
-        if (first && s >= 2 && !wait(L::B_OEMPTY + (s & 1), ((s >> 1) - 1) & 1)) return false;
+    auto issue_pv = [&](const Item &m) -> bool {
+        const int st = m.n % kStages, buf = m.i & 1, ob = m.q & 1;
+        if (!wait(L::B_PFULL + buf, (m.i >> 1) & 1)) return false;
+        if (m.t0 && !wait(L::B_VFULL + st, (m.n / kStages) & 1)) return false;
+        if (m.first && m.q >= 2 && !wait(L::B_OEMPTY + ob, ((m.q >> 1) - 1) & 1)) return false;
         rx::fence_proxy_async_smem();  // V rows landed by cp.async
         rx::tc_fence_after();
         const uint64_t dvs = dv + (uint64_t)((st * L::NB * L::BLK) >> 4);
 #pragma unroll
         for (int ks = 0; ks < kBN / 16; ++ks)
-            rx::tc_mma_ts(tmem + (s & 1) * 256 + 128, tmem + buf * 256 + ks * 8, dvs + (uint64_t)((ks * 16 * 128) >> 4),
-                          idesc_pv, (!first || ks > 0) ? 1u : 0u);
-        rx::tc_commit(bar + 8 * L::B_PVDONE);
-        rx::tc_commit(bar + 8 * (L::B_VEMPTY + st));
+            rx::tc_mma_ts(tmem + ob * 256 + 128, tmem + buf * 256 + ks * 8, dvs + (uint64_t)((ks * 16 * 128) >> 4),
+                          idesc_pv, (!m.first || ks > 0) ? 1u : 0u);
+        rx::tc_commit(bar + 8 * (L::B_PVDONE + buf));
+        if (m.t1) rx::tc_commit(bar + 8 * (L::B_VEMPTY + st));
         return true;
     };
-    bool ok = true, prev_first = false;
-    int n = 0, prev_s = 0;
+    bool ok = true;
+    Item prev{};
+    int i = 0, n = 0, q0 = 0;
     for (int s = 0; ok; ++s) {
-        const int j0 = c.j, j1 = c.end();
-        for (int j = j0; j < j1 && ok; ++j, ++n) {
-            ok = issue_s(n, s, j == j0, j == j1 - 1);
-            if (ok && n > 0) ok = issue_pv(n - 1, prev_s, prev_first);
-            prev_s = s;
-            prev_first = j == j0;
-        }
-        if (!ok || !c.next(p)) break;
+        Seg g;
+        if (!(ok = get_seg<L>(s, g, smem, sbase, p.status))) break;
+        free_seg<L>(s, sbase);
+        const int nt = NT == 1 ? 1 : g.nt;
+        for (int j = g.j0; j < g.j1 && ok; ++j, ++n)
+            for (int t = 0; t < nt && ok; ++t, ++i) {
+                const Item m{i, n, q0 + t, NT == 1 || t == 0, NT == 1 || t == nt - 1, j == g.j0, j == g.j1 - 1};
+                ok = issue_s(m);
+                if (ok && i > 0) ok = issue_pv(prev);
+                prev = m;
+            }
+        q0 += nt;
+        if (g.last) break;
     }
-    if (ok) issue_pv(n - 1, prev_s, prev_first);
+    if (ok) issue_pv(prev);
     // everything issued has finished before TMEM is released
     rx::tc_commit(bar + 8 * L::B_FINAL);
     rx::drain_wait(bar + 8 * L::B_FINAL, 0, p.status);
@@ -618,13 +722,13 @@ __device__ void mma_issuer(const TParams &p, unsigned char *smem, uint32_t sbase
 // The NaN and infinities of V at drafted positions that a row sees, added to
 // its written result: o (part < 0) or the partial row `part`.
 template <int D, bool F8>
-__device__ __noinline__ void add_not_finite(const TParams &p, const uint32_t *nf, const uint32_t *mrow, int node, int b,
-                                            int g, int P, int T, int64_t part, int64_t orow)
+__device__ __noinline__ void add_not_finite(const TParams &p, const uint32_t *nf, const uint32_t *mrow, int words, int node,
+                                            int row, int g, int P, int T, int64_t part, int64_t orow)
 {
     for (int w = 0; w < (T + 31) / 32; ++w)
-        for (uint32_t bad = nf[w] & mask_word(p, mrow, node, T, w); bad; bad &= bad - 1) {
+        for (uint32_t bad = nf[w] & mask_word(mrow, words, node, T, w); bad; bad &= bad - 1) {
             const int pos = P + 32 * w + __ffs(bad) - 1;
-            const int64_t slot = __ldg(p.rtt + (int64_t)__ldg(p.req_idx + b) * p.rtt_stride + pos);
+            const int64_t slot = __ldg(p.rtt + (int64_t)row * p.rtt_stride + pos);
             const int64_t at = (slot * p.hkv + g) * D;
             for (int i = 0; i < D; ++i) {
                 float v;
@@ -641,167 +745,200 @@ __device__ __noinline__ void add_not_finite(const TParams &p, const uint32_t *nf
         }
 }
 
-template <int D, bool F8>
+// What a thread keeps of its row of one row tile.
+struct RowState {
+    float m, l;    // running maximum (log2 units) and sum
+    float sl2;     // log2 units of a score
+};
+
+template <int D, bool F8, int NT>
 __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sbase)
 {
     using L = TL<D, F8>;
-    Cursor c = start_of<L>(smem);
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::OFF_TMEM);
     const uint32_t bar = sbase + L::OFF_BAR;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
     const int row = threadIdx.x;                       // = TMEM lane
     const uint32_t lanes = (uint32_t)(row & ~31) << 16;
-    int n = 0;
+    const int rt = row / p.G, rh = row - rt * p.G;     // drafted token of the row tile, q head of the kv head
+    int i = 0, q0 = 0;                                 // items and row tiles of the segments before
     for (int s = 0;; ++s) {
-        const int j0 = c.j, j1 = c.end(), P = c.r.P, T = c.r.T;
-        const int t0 = c.qt * p.tb, M = min(p.tb, T - t0) * p.G;
-        const bool valid = row < M, warp_on = (row & ~31) < M;
-        const int node = t0 + row / p.G;
-        const int64_t tok = (int64_t)__ldg(p.qo_indptr + c.b) + node;
-        const uint32_t *mrow = p.mask && valid ? p.mask + tok * p.words : nullptr;
-        const uint32_t tO = tmem + (s & 1) * 256 + 128 + lanes;
-        float m_used = -INFINITY, l = 0.f, sl2 = p.scale_log2;
-        for (int j = j0; j < j1; ++j, ++n) {
-            const int buf = n & 1;
-            const uint32_t tS = tmem + buf * 256 + lanes;
-            if (!warp_wait(bar + 8 * (L::B_SFULL + buf), (n >> 1) & 1, abort_flag, p.status)) return;
-            rx::tc_fence_after();
-            if (warp_on) {
-                // the row's scores of this tile, loaded once (four loads in
-                // flight): a load takes about 200 cycles to come back
-                uint32_t sv[kBN];
+        Seg g;
+        if (!__all_sync(0xffffffffu, get_seg<L>(s, g, smem, sbase, p.status))) return;
+        const int nt = NT == 1 ? 1 : g.nt;
+        // the mask row of drafted token rt + t * tb of the segment
+        const uint32_t *masks = !p.mask ? nullptr
+                                : g.T <= kMaskT ? reinterpret_cast<const uint32_t *>(smem + L::OFF_MASK) + (s % kSegs) * (kMaskT * (kMaskT / 32))
+                                                : p.mask + (int64_t)g.tok * p.words;
+        const int words = g.T <= kMaskT ? kMaskT / 32 : p.words;
+        RowState a{-INFINITY, 0.f, p.scale_log2}, b = a;   // the item's row tile, and the other one
+        for (int j = g.j0; j < g.j1; ++j)
+            for (int t = 0; t < nt; ++t, ++i) {
+                const int buf = i & 1;
+                const uint32_t tS = tmem + buf * 256 + lanes, tO = tmem + ((q0 + t) & 1) * 256 + 128 + lanes;
+                const int M = min(p.tb, g.ntok - t * p.tb) * p.G;
+                const bool valid = row < M, warp_on = (row & ~31) < M;
+                if (!warp_wait(bar + 8 * (L::B_SFULL + buf), (i >> 1) & 1, abort_flag, p.status)) return;
+                rx::tc_fence_after();
+                if (warp_on) {
+                    // the row's scores of this tile, loaded once (four loads in
+                    // flight): a load takes about 200 cycles to come back
+                    uint32_t sv[kBN];
 #pragma unroll
-                for (int k = 0; k < kBN / 32; ++k) rx::tmem_ld32(tS + k * 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * k));
-                if (F8 && j == j0) sl2 = p.scale_log2 * reinterpret_cast<const float *>(smem + L::OFF_QS)[(s % kRing) * kRows + row];
-                const int kbase = j * kBN;
-                if (kbase + kBN > P) {   // drafted positions, or past the last
-                    const int off = kbase - P, w0 = off >> 5;
-                    uint32_t w[5];
+                    for (int k = 0; k < kBN / 32; ++k) rx::tmem_ld32(tS + k * 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * k));
+                    if (F8 && j == g.j0)
+                        a.sl2 = p.scale_log2 * reinterpret_cast<const float *>(smem + L::OFF_QS)[((q0 + t) % kRing) * kRows + row];
+                    const int kbase = j * kBN;
+                    if (kbase + kBN > g.P) {   // drafted positions, or past the last
+                        const int off = kbase - g.P, w0 = off >> 5, node = rt + t * p.tb;
+                        const uint32_t *mrow = masks && valid ? masks + (int64_t)node * words : nullptr;
+                        uint32_t w[5];
 #pragma unroll
-                    for (int k = 0; k < 5; ++k) w[k] = mask_word(p, mrow, node, T, w0 + k);
-                    rx::tmem_wait_ld();
-#pragma unroll
-                    for (int k = 0; k < kBN / 32; ++k) {
-                        const uint32_t bits = __funnelshift_r(w[k], w[k + 1], off & 31);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (!((bits >> i) & 1u)) sv[32 * k + i] = 0xFF800000u;  // -inf
-                    }
-                } else {
-                    rx::tmem_wait_ld();
-                }
-                float mx;
-                {
-                    float a0 = -INFINITY, a1 = -INFINITY, a2 = -INFINITY, a3 = -INFINITY;
-#pragma unroll
-                    for (int k = 0; k < kBN / 8; ++k) {
-                        a0 = rx::fmax3(a0, u2f(sv[8 * k]), u2f(sv[8 * k + 1]));
-                        a1 = rx::fmax3(a1, u2f(sv[8 * k + 2]), u2f(sv[8 * k + 3]));
-                        a2 = rx::fmax3(a2, u2f(sv[8 * k + 4]), u2f(sv[8 * k + 5]));
-                        a3 = rx::fmax3(a3, u2f(sv[8 * k + 6]), u2f(sv[8 * k + 7]));
-                    }
-                    mx = rx::fmax3(fmaxf(a0, a1), a2, a3);
-                }
-                const float m_new = fmaxf(m_used, mx * sl2);
-                const bool need = valid && (m_used == -INFINITY || m_new > m_used + kRescale);
-                const bool scale_o = need && m_used != -INFINITY;
-                const float alpha = scale_o ? rx::fast_exp2(m_used - m_new) : 1.f;
-                if (need) {
-                    l *= alpha;
-                    m_used = m_new;
-                }
-                const float mu = m_used == -INFINITY ? 0.f : m_used;
-                const uint64_t scale2 = rx::f2(sl2, sl2), negm2 = rx::f2(-mu, -mu);
-                uint64_t acc[4] = {0, 0, 0, 0};
-#pragma unroll
-                for (int k = 0; k < kBN / 64; ++k) {
-                    uint32_t pk[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        float x0, x1;
-                        rx::f2_split(rx::f2_fma(rx::f2(u2f(sv[64 * k + 2 * i]), u2f(sv[64 * k + 2 * i + 1])), scale2, negm2), x0, x1);
-                        const float e0 = rx::fast_exp2(x0), e1 = rx::fast_exp2(x1);
-                        acc[i & 3] = rx::f2_add(acc[i & 3], rx::f2(e0, e1));
-                        // the weights are rounded to the type of V's tile for
-                        // the tensor core; their sum is not
-                        pk[i] = F8 ? rx::pack_f16(e0, e1) : rx::pack_bf16(e0, e1);
-                    }
-                    rx::tmem_st32(tS + k * 32, pk);  // over scores already read
-                }
-                float a0, a1;
-                rx::f2_split(rx::f2_add(rx::f2_add(acc[0], acc[1]), rx::f2_add(acc[2], acc[3])), a0, a1);
-                l += a0 + a1;
-                if (__any_sync(0xffffffffu, scale_o)) {
-                    // O += P V of the tile before has to be complete
-                    if (!warp_wait(bar + 8 * L::B_PVDONE, (n - 1) & 1, abort_flag, p.status)) return;
-                    rx::tc_fence_after();
-#pragma unroll
-                    for (int k = 0; k < D / 32; ++k) {
-                        uint32_t x[32];
-                        rx::tmem_ld32(tO + k * 32, x);
+                        for (int k = 0; k < 5; ++k) w[k] = mask_word(mrow, words, g.node + node, g.T, w0 + k);
                         rx::tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(u2f(x[i]) * alpha);
-                        rx::tmem_st32(tO + k * 32, x);
+                        for (int k = 0; k < kBN / 32; ++k) {
+                            const uint32_t bits = __funnelshift_r(w[k], w[k + 1], off & 31);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (!((bits >> e) & 1u)) sv[32 * k + e] = 0xFF800000u;  // -inf
+                        }
+                    } else {
+                        rx::tmem_wait_ld();
                     }
+                    float mx;
+                    {
+                        float a0 = -INFINITY, a1 = -INFINITY, a2 = -INFINITY, a3 = -INFINITY;
+#pragma unroll
+                        for (int k = 0; k < kBN / 8; ++k) {
+                            a0 = rx::fmax3(a0, u2f(sv[8 * k]), u2f(sv[8 * k + 1]));
+                            a1 = rx::fmax3(a1, u2f(sv[8 * k + 2]), u2f(sv[8 * k + 3]));
+                            a2 = rx::fmax3(a2, u2f(sv[8 * k + 4]), u2f(sv[8 * k + 5]));
+                            a3 = rx::fmax3(a3, u2f(sv[8 * k + 6]), u2f(sv[8 * k + 7]));
+                        }
+                        mx = rx::fmax3(fmaxf(a0, a1), a2, a3);
+                    }
+                    const float m_new = fmaxf(a.m, mx * a.sl2);
+                    const bool need = valid && (a.m == -INFINITY || m_new > a.m + kRescale);
+                    const bool scale_o = need && a.m != -INFINITY;
+                    const float alpha = scale_o ? rx::fast_exp2(a.m - m_new) : 1.f;
+                    if (need) {
+                        a.l *= alpha;
+                        a.m = m_new;
+                    }
+                    const float mu = a.m == -INFINITY ? 0.f : a.m;
+                    const uint64_t scale2 = rx::f2(a.sl2, a.sl2), negm2 = rx::f2(-mu, -mu);
+                    uint64_t acc[4] = {0, 0, 0, 0};
+#pragma unroll
+                    for (int k = 0; k < kBN / 64; ++k) {
+                        uint32_t pk[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            float x0, x1;
+                            rx::f2_split(rx::f2_fma(rx::f2(u2f(sv[64 * k + 2 * e]), u2f(sv[64 * k + 2 * e + 1])), scale2, negm2), x0, x1);
+                            const float e0 = rx::fast_exp2(x0), e1 = rx::fast_exp2(x1);
+                            acc[e & 3] = rx::f2_add(acc[e & 3], rx::f2(e0, e1));
+                            // the weights are rounded to the type of V's tile for
+                            // the tensor core; their sum is not
+                            pk[e] = F8 ? rx::pack_f16(e0, e1) : rx::pack_bf16(e0, e1);
+                        }
+                        rx::tmem_st32(tS + k * 32, pk);  // over scores already read
+                    }
+                    float a0, a1;
+                    rx::f2_split(rx::f2_add(rx::f2_add(acc[0], acc[1]), rx::f2_add(acc[2], acc[3])), a0, a1);
+                    a.l += a0 + a1;
+                    if (__any_sync(0xffffffffu, scale_o)) {
+                        // this row tile's O += P V before has to be complete: item
+                        // i - nt; i - 2 is (S(i) waited for it)
+                        if (nt == 1 && !warp_wait(bar + 8 * (L::B_PVDONE + ((i - 1) & 1)), ((i - 1) >> 1) & 1, abort_flag, p.status))
+                            return;
+                        rx::tc_fence_after();
+#pragma unroll
+                        for (int k = 0; k < D / 32; ++k) {
+                            uint32_t x[32];
+                            rx::tmem_ld32(tO + k * 32, x);
+                            rx::tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) x[e] = __float_as_uint(u2f(x[e]) * alpha);
+                            rx::tmem_st32(tO + k * 32, x);
+                        }
+                    }
+                    rx::tmem_wait_st();
                 }
-                rx::tmem_wait_st();
+                rx::tc_fence_before();
+                rx::mbar_arrive(bar + 8 * (L::B_PFULL + buf));
+                if (nt == 2) {
+                    const RowState x = a;
+                    a = b;
+                    b = x;
+                }
+            }
+        // the segment's results
+        uint32_t any = 0;
+        const uint32_t *nf = reinterpret_cast<const uint32_t *>(smem + L::OFF_NF) + (s % kSegs) * 32;
+        for (int t = 0; t < nt; ++t) {
+            // the row tile's last product, item i - nt + t
+            const int e = i - nt + t;
+            if (!warp_wait(bar + 8 * (L::B_PVDONE + (e & 1)), (e >> 1) & 1, abort_flag, p.status)) return;
+            rx::tc_fence_after();
+            const RowState &r = t == 0 ? a : b;
+            const int M = min(p.tb, g.ntok - t * p.tb) * p.G, node = rt + t * p.tb;
+            const bool valid = row < M, warp_on = (row & ~31) < M;
+            const uint32_t tO = tmem + ((q0 + t) & 1) * 256 + 128 + lanes;
+            const float inv = r.l == 0.f ? 0.f : p.v_scale / r.l;
+            const int64_t orow = (int64_t)(g.tok + node) * p.hq + (int64_t)g.g * p.G + rh;
+            const int64_t prow = ((int64_t)(2 * blockIdx.x + (g.j0 == 0 ? 1 : 0)) * NT + t) * kRows + row;
+            if (warp_on) {
+                uint32_t x[D];
+#pragma unroll
+                for (int k = 0; k < D / 32; ++k) rx::tmem_ld32(tO + k * 32, *reinterpret_cast<uint32_t(*)[32]>(x + 32 * k));
+                rx::tmem_wait_ld();
+                if (valid) {
+                    if (g.whole) {
+                        uint4 *dst = reinterpret_cast<uint4 *>(p.o + orow * D);
+#pragma unroll
+                        for (int e = 0; e < D / 8; ++e) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) w[k] = rx::pack_bf16(u2f(x[8 * e + 2 * k]) * inv, u2f(x[8 * e + 2 * k + 1]) * inv);
+                            dst[e] = r.l == 0.f ? make_uint4(0, 0, 0, 0) : make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    } else {
+                        float4 *dst = reinterpret_cast<float4 *>(p.part_o + prow * D);
+#pragma unroll
+                        for (int e = 0; e < D / 4; ++e)
+                            dst[e] = r.l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                                : make_float4(u2f(x[4 * e]) * inv, u2f(x[4 * e + 1]) * inv,
+                                                              u2f(x[4 * e + 2]) * inv, u2f(x[4 * e + 3]) * inv);
+                    }
+                    const float l2 = r.l == 0.f ? -INFINITY : r.m + log2f(r.l);
+                    if (!g.whole) p.part_l[prow] = l2;
+                    else if (p.lse) p.lse[orow] = l2 * rx::kLn2;
+                }
+                __syncwarp();
             }
             rx::tc_fence_before();
-            rx::mbar_arrive(bar + 8 * (L::B_PFULL + buf));
-        }
-        // the segment's result
-        if (!warp_wait(bar + 8 * L::B_PVDONE, (n - 1) & 1, abort_flag, p.status)) return;
-        rx::tc_fence_after();
-        uint32_t *nf = reinterpret_cast<uint32_t *>(smem + L::OFF_NF) + (s % kRing) * 32;
-        uint32_t any = 0;
-        if (j1 * kBN > P)
-            for (int i = 0; i < (T + 31) / 32; ++i) any |= nf[i];
-        const bool whole = j0 == 0 && j1 == c.r.ntiles;
-        const float inv = l == 0.f ? 0.f : p.v_scale / l;
-        const int64_t orow = tok * p.hq + (int64_t)c.g * p.G + row % p.G;
-        const int64_t prow = (int64_t)(2 * blockIdx.x + (j0 == 0 ? 1 : 0)) * kRows + row;
-        if (warp_on) {
-            uint32_t r[D];
-#pragma unroll
-            for (int k = 0; k < D / 32; ++k) rx::tmem_ld32(tO + k * 32, *reinterpret_cast<uint32_t(*)[32]>(r + 32 * k));
-            rx::tmem_wait_ld();
-            if (valid) {
-                if (whole) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(p.o + orow * D);
-#pragma unroll
-                    for (int i = 0; i < D / 8; ++i) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) w[k] = rx::pack_bf16(u2f(r[8 * i + 2 * k]) * inv, u2f(r[8 * i + 2 * k + 1]) * inv);
-                        dst[i] = l == 0.f ? make_uint4(0, 0, 0, 0) : make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                } else {
-                    float4 *dst = reinterpret_cast<float4 *>(p.part_o + prow * D);
-#pragma unroll
-                    for (int i = 0; i < D / 4; ++i)
-                        dst[i] = l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                          : make_float4(u2f(r[4 * i]) * inv, u2f(r[4 * i + 1]) * inv,
-                                                        u2f(r[4 * i + 2]) * inv, u2f(r[4 * i + 3]) * inv);
-                }
-                const float l2 = l == 0.f ? -INFINITY : m_used + log2f(l);
-                if (!whole) p.part_l[prow] = l2;
-                else if (p.lse) p.lse[orow] = l2 * rx::kLn2;
+            rx::mbar_arrive(bar + 8 * (L::B_OEMPTY + ((q0 + t) & 1)));
+            if (g.j1 * kBN > g.P) {
+                if (t == 0)
+                    for (int w = 0; w < (g.T + 31) / 32; ++w) any |= nf[w];
+                if (any && valid)
+                    add_not_finite<D, F8>(p, nf, masks ? masks + (int64_t)node * words : nullptr, words, g.node + node, g.row, g.g,
+                                          g.P, g.T, g.whole ? -1 : prow, orow);
             }
-            __syncwarp();
         }
-        rx::tc_fence_before();
-        rx::mbar_arrive(bar + 8 * (L::B_OEMPTY + (s & 1)));
+        q0 += nt;
         if (any) {  // the same for every thread: all have read the words, then they are cleared
-            if (valid) add_not_finite<D, F8>(p, nf, mrow, node, c.b, c.g, P, T, whole ? -1 : prow, orow);
             rx::named_bar_sync(1, 32 * kSoftWarps);
-            if (row < 32) nf[row] = 0;
+            if (row < 32) const_cast<uint32_t *>(nf)[row] = 0;
         }
-        if (!c.next(p)) return;
+        __syncwarp();
+        if ((row & 31) == 0) free_seg<L>(s, sbase);
+        if (g.last) return;
     }
 }
 
-template <int D, bool F8>
+template <int D, bool F8, int NT>
 __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant__ TParams p)
 {
     using L = TL<D, F8>;
@@ -827,15 +964,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         for (int i = 0; i < 2; ++i) {
             rx::mbar_init(bar + 8 * (L::B_SFULL + i), 1);
             rx::mbar_init(bar + 8 * (L::B_PFULL + i), kRows);
+            rx::mbar_init(bar + 8 * (L::B_PVDONE + i), 1);
             rx::mbar_init(bar + 8 * (L::B_OEMPTY + i), kRows);
         }
-        rx::mbar_init(bar + 8 * L::B_PVDONE, 1);
+        for (int i = 0; i < kSegs; ++i) {
+            rx::mbar_init(bar + 8 * (L::B_SEGFULL + i), 32 + 1);  // the scheduler's lanes' copies, and the segment
+            rx::mbar_init(bar + 8 * (L::B_SEGEMPTY + i), kSoftWarps + 2 * kProdWarps + 2);
+        }
         rx::mbar_init(bar + 8 * L::B_FINAL, 1);
         *reinterpret_cast<volatile int *>(smem + L::OFF_ABORT) = 0;
         rx::fence_mbar_init();
     }
-    for (int i = threadIdx.x; i < kRing * 32; i += kThreads) reinterpret_cast<uint32_t *>(smem + L::OFF_NF)[i] = 0;
-    int64_t *pre = reinterpret_cast<int64_t *>(smem + L::OFF_SCAN);
+    for (int i = threadIdx.x; i < kSegs * 32; i += kThreads) reinterpret_cast<uint32_t *>(smem + L::OFF_NF)[i] = 0;
+    int64_t *pre = reinterpret_cast<int64_t *>(smem + L::OFF_MASK);
     const int per = (p.batch + kThreads - 1) / kThreads;
     const int64_t per_head = scan_units<kThreads>(p, pre, per, blockIdx.x == 0);
     const int64_t total = per_head * p.hkv;
@@ -845,21 +986,22 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         if (p.status && threadIdx.x == 0) atomicOr(p.status, RX_DEV_BAD_LEN);
         return;
     }
-    static_assert(sizeof(Cursor) <= 64, "the start cursor's room");
+    static_assert(sizeof(Start) <= 32, "the start's room");
     if (threadIdx.x == 0) {
         const int64_t u0 = first_unit(total, ctas, blockIdx.x);
-        Cursor c = locate<kThreads>(p, pre, per, per_head, u0);
+        Req r;
+        Start c = locate<kThreads>(p, pre, per, per_head, u0, r);
         c.left = (int)(first_unit(total, ctas, blockIdx.x + 1) - u0);
-        *reinterpret_cast<Cursor *>(smem + L::OFF_START) = c;
+        *reinterpret_cast<Start *>(smem + L::OFF_START) = c;
     }
     if (warp == kWarpMma) rx::tmem_alloc(sbase + L::OFF_TMEM, kTmemCols);
     rx::tc_fence_before();
-    __syncthreads();
+    __syncthreads();  // from here on the scan's room holds masks
     rx::tc_fence_after();
 
     if (warp < kSoftWarps) {
         rx::reg_inc<kRegsSoft>();
-        softmax_rows<D, F8>(p, smem, sbase);
+        softmax_rows<D, F8, NT>(p, smem, sbase);
     } else if (warp < kWarpQ) {
         rx::reg_dec<kRegsProd>();
         if (warp < kSoftWarps + kProdWarps) producer<D, F8, false>(p, smem, sbase);
@@ -869,8 +1011,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         if (warp == kWarpQ) {
             query_loader<D, F8>(p, smem, sbase);
         } else if (warp == kWarpMma) {
-            if ((threadIdx.x & 31) == 0) mma_issuer<D, F8>(p, smem, sbase);
+            if ((threadIdx.x & 31) == 0) mma_issuer<D, F8, NT>(p, smem, sbase);
             __syncwarp();
+        } else if (warp == kWarpSched) {
+            scheduler<D, F8>(p, smem, sbase);
         }
     }
     rx::tc_fence_before();
@@ -885,7 +1029,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
 // joining the partial results
 // ---------------------------------------------------------------------------
 
-// The (kv head, request, row tile) that the boundary between CTAs x and x + 1
+// The (kv head, request, row tiles) that the boundary between CTAs x and x + 1
 // cuts, x = blockIdx.x, when it is the first boundary inside: its parts are
 // CTA x's last segment (slot 1) and the first segments (slot 0) of the CTAs
 // after it, as far as it reaches.  One warp a row: with m the largest
@@ -902,20 +1046,21 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
     rx::pdl_wait();  // the partial results are written by the kernel before this one
     if (x0 + 1 >= ctas || total / ctas >= INT_MAX) return;
     const int64_t cut = first_unit(total, ctas, x0 + 1);
-    const Cursor c = locate<kMergeThreads>(p, pre, per, per_head, cut);
-    const int64_t begin = cut - c.j, end = begin + c.r.ntiles;
+    Req req;
+    const Start c = locate<kMergeThreads>(p, pre, per, per_head, cut, req);
+    const int64_t begin = cut - c.j, end = begin + req.ntiles;
     if (c.j == 0 || begin < first_unit(total, ctas, x0)) return;
     int parts = 2;
     while (x0 + parts < ctas && first_unit(total, ctas, x0 + parts) < end) ++parts;
 
     constexpr int V = D / 32;  // values of a lane
     const int lane = threadIdx.x & 31;
-    const int t0 = c.qt * p.tb, M = min(p.tb, c.r.T - t0) * p.G;
-    const int64_t tok0 = (int64_t)__ldg(p.qo_indptr + c.b) + t0;
+    const int node = c.qt * p.tb * p.nt, ntok = min(p.tb * p.nt, req.T - node);
     for (int i = threadIdx.x >> 5; i < kMergeRows; i += kMergeThreads / 32) {
-        const int row = (int)blockIdx.y * kMergeRows + i;
-        if (row >= M) break;
-        auto at = [&](int s) { return (int64_t)(2 * (x0 + s) + (s == 0 ? 1 : 0)) * kRows + row; };
+        const int row = (int)blockIdx.y * kMergeRows + i;      // of the group's nt * 128
+        const int t = row / kRows, r = row % kRows;
+        if (t >= p.nt || r >= min(p.tb, ntok - t * p.tb) * p.G) continue;
+        auto at = [&](int s) { return (int64_t)(2 * (x0 + s) + (s == 0 ? 1 : 0)) * p.nt * kRows + row; };
         float m = -INFINITY;
         for (int s = lane; s < parts; s += 32) m = fmaxf(m, __ldcg(p.part_l + at(s)));
 #pragma unroll
@@ -940,7 +1085,7 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
             }
         }
         const float inv = tot == 0.f ? 0.f : 1.f / tot;
-        const int64_t orow = (tok0 + row / p.G) * p.hq + (int64_t)c.g * p.G + row % p.G;
+        const int64_t orow = ((int64_t)req.tok + node + t * p.tb + r / p.G) * p.hq + (int64_t)c.g * p.G + r % p.G;
         uint32_t *dst = reinterpret_cast<uint32_t *>(p.o + orow * D + lane * V);
         dst[0] = rx::pack_bf16(acc[0] * inv, acc[1] * inv);
         if constexpr (V == 4) dst[1] = rx::pack_bf16(acc[2] * inv, acc[3] * inv);
@@ -948,7 +1093,12 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
     }
 }
 
-size_t part_bytes(int32_t head_dim) { return (size_t)2 * kCtas * kRows * head_dim * sizeof(float); }
+size_t part_bytes(int32_t nt, int32_t head_dim) { return (size_t)2 * kCtas * nt * kRows * head_dim * sizeof(float); }
+
+// Row tiles that share a K/V tile: two where some tree may have more than one
+// (64-token trees over 64/8 heads, 8k contexts: @NT@), and bf16
+// pools only (an FP8 tile has one query buffer).
+int row_tiles(int32_t hq, int32_t hkv, int32_t max_tree) { return (int64_t)max_tree > kRows / (hq / hkv) ? kMaxNt : 1; }
 
 struct TreePool {
     const void *k, *v;
@@ -964,16 +1114,19 @@ bool tree_shape_ok(int32_t batch, int32_t hq, int32_t hkv, int32_t D, int32_t ma
            (D == 64 || D == 128) && max_tree >= 1 && max_tree <= kMaxTree;
 }
 
-template <int D, bool F8>
+template <int D, bool F8, int NT = 1>
 int launch(const TParams &p, cudaStream_t st)
 {
     // per device; cheap, and right whichever device is current
-    RX_CUDA_CHECK(cudaFuncSetAttribute(tree_kernel<D, F8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (TL<D, F8>::BYTES)));
-    tree_kernel<D, F8><<<kCtas, kThreads, (TL<D, F8>::BYTES), st>>>(p);
+    RX_CUDA_CHECK(cudaFuncSetAttribute(tree_kernel<D, F8, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (TL<D, F8>::BYTES)));
+    if (F8)  // no more shared memory than it needs: the rest is L1
+        RX_CUDA_CHECK(cudaFuncSetAttribute(tree_kernel<D, F8, NT>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                           ((TL<D, F8>::BYTES) + 2048) * 100 / (228 * 1024) + 1));
+    tree_kernel<D, F8, NT><<<kCtas, kThreads, (TL<D, F8>::BYTES), st>>>(p);
     RX_CUDA_CHECK(cudaGetLastError());
     // a programmatic dependent: it finds its part of the work, then waits on the device
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kCtas - 1, (unsigned)((std::min(p.max_tree, p.tb) * p.G + kMergeRows - 1) / kMergeRows));
+    cfg.gridDim = dim3(kCtas - 1, (unsigned)(p.nt == 1 ? (std::min(p.max_tree, p.tb) * p.G + kMergeRows - 1) / kMergeRows : p.nt * kRows / kMergeRows));
     cfg.blockDim = dim3(kMergeThreads);
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
@@ -1022,6 +1175,7 @@ int tree_call(const char *who, const TreePool &pool, const void *q, void *o, flo
     p.hkv = pool.hkv;
     p.G = hq / pool.hkv;
     p.tb = kRows / p.G;
+    p.nt = pool.f8 ? 1 : row_tiles(hq, pool.hkv, max_tree);
     p.qo_indptr = qo_indptr;
     p.req_idx = req_idx;
     p.prefix_len = prefix_len;
@@ -1035,10 +1189,11 @@ int tree_call(const char *who, const TreePool &pool, const void *q, void *o, flo
     p.v_scale = pool.v_scale;
     p.status = dev_status;
     p.part_o = (float *)workspace;
-    p.part_l = (float *)((char *)workspace + part_bytes(pool.D));
+    p.part_l = (float *)((char *)workspace + part_bytes(p.nt, pool.D));
     cudaStream_t st = (cudaStream_t)stream;
-    if (pool.D == 128) return pool.f8 ? launch<128, true>(p, st) : launch<128, false>(p, st);
-    return pool.f8 ? launch<64, true>(p, st) : launch<64, false>(p, st);
+    if (pool.D == 128)
+        return pool.f8 ? launch<128, true>(p, st) : p.nt == 1 ? launch<128, false>(p, st) : launch<128, false, kMaxNt>(p, st);
+    return pool.f8 ? launch<64, true>(p, st) : p.nt == 1 ? launch<64, false>(p, st) : launch<64, false, kMaxNt>(p, st);
 }
 
 }  // namespace
@@ -1049,7 +1204,8 @@ extern "C" size_t rx_attn_tree_workspace(int32_t batch, int32_t hq, int32_t hkv,
         rx_set_error(RX_ERR_INVALID, "rx_attn_tree_workspace: invalid argument");
         return 0;
     }
-    return part_bytes(head_dim) + (size_t)2 * kCtas * kRows * sizeof(float);
+    const int nt = row_tiles(hq, hkv, max_tree);
+    return part_bytes(nt, head_dim) + (size_t)2 * kCtas * nt * kRows * sizeof(float);
 }
 
 extern "C" int rx_attn_tree(const rx_kv_pool *pool_in, const void *q, void *o, float *lse, int32_t hq,
