@@ -59,9 +59,10 @@ constexpr int kProdWarps = 8;        // for K, and as many for V
 constexpr int kProdRows = kBN / kProdWarps;  // rows of a tile each producer warp gathers
 constexpr int kSoftWarps = 4;        // one query row a thread
 constexpr int kWarpQ = kSoftWarps + 2 * kProdWarps;  // loads the query rows
-constexpr int kWarpMma = kWarpQ + 1;
+constexpr int kWarpMma = kWarpQ + 1;                 // issues S = Q K^T; kWarpPv the other product
 constexpr int kWarpSched = kWarpQ + 2;               // hands out the segments
-constexpr int kThreads = 32 * (kWarpQ + 4);          // a warp idle: register shares go by warpgroup
+constexpr int kWarpPv = kWarpQ + 3;
+constexpr int kThreads = 32 * (kWarpQ + 4);
 // registers a thread, by role (a softmax thread holds a row's 128 scores):
 // 128 x 192 + 512 x 56 + 128 x 56 of the 768 x 80 launched
 constexpr int kRegsSoft = 192, kRegsProd = 56, kRegsMisc = 56, kRegsLaunch = 80;
@@ -110,7 +111,7 @@ struct TL {
                          B_VEMPTY = B_VFULL + kStages, B_QFULL = B_VEMPTY + kStages, B_QEMPTY = B_QFULL + QB,
                          B_SFULL = B_QEMPTY + QB, B_PFULL = B_SFULL + 2, B_PVDONE = B_PFULL + 2,
                          B_OEMPTY = B_PVDONE + 2, B_SEGFULL = B_OEMPTY + 2, B_SEGEMPTY = B_SEGFULL + kSegs,
-                         B_FINAL = B_SEGEMPTY + kSegs, N_BAR = B_FINAL + 1;
+                         B_FINAL = B_SEGEMPTY + kSegs, N_BAR = B_FINAL + 2;
     static constexpr int OFF_TMEM = OFF_BAR + N_BAR * 8;
     static constexpr int OFF_ABORT = OFF_TMEM + 8;
     static constexpr int OFF_START = OFF_ABORT + 8;                   // Start
@@ -627,36 +628,56 @@ __device__ void query_loader(const TParams &p, unsigned char *smem, uint32_t sba
 }
 
 // ---------------------------------------------------------------------------
-// MMA thread
+// the two MMA threads
 // ---------------------------------------------------------------------------
 
-// Over the CTA's items i = 0, 1, ...: for every position tile n (all segments
-// in a row) the segment's row tiles t.  S(i) = Q_t K_n^T into buffer i & 1, then
-// O_t += P V of item i - 1; the O (and Q) of the q-th row tile of the CTA in
-// buffer q & 1.  P(i - 2) sits in the columns that S(i) overwrites, so S(i)
-// waits for that product's completion.  The products of odd and even items
-// complete on barriers of their own: whoever waits for one knows that the one
-// two items before has completed, so a phase's parity is never ambiguous.
+// The CTA's items i = 0, 1, ...: for every position tile n (all segments in a
+// row) the segment's row tiles t.  S(i) = Q_t K_n^T goes into buffer i & 1; the O
+// (and Q) of the q-th row tile of the CTA into buffer q & 1.  P(i - 2) sits in
+// the columns that S(i) overwrites, so S(i) waits for that product's
+// completion.  The products of odd and even items complete on barriers of their
+// own: whoever waits for one knows that the one two items before has completed,
+// so a phase's parity is never ambiguous.
+//
+// S and P V are issued by a thread each: a thread spends as long on the waits
+// and commits around an operation's eight MMAs as on the MMAs, and with one
+// thread for both the tensor core idled meanwhile (@TWO@).
+struct Item {
+    int i, n, q;                   // item, position tile, row tile
+    bool t0, t1;                   // the first, the last row tile of the position tile
+    bool first, last;              // the row tile's first, last position tile
+};
+
+// f(item) for every item, until it or a wait gives up.
+template <typename L, int NT, typename F>
+__device__ __forceinline__ void for_items(const TParams &p, unsigned char *smem, uint32_t sbase, F f)
+{
+    int i = 0, n = 0, q0 = 0;
+    for (int s = 0;; ++s) {
+        Seg g;
+        if (!get_seg<L>(s, g, smem, sbase, p.status)) return;
+        free_seg<L>(s, sbase);
+        const int nt = NT == 1 ? 1 : g.nt;
+        for (int j = g.j0; j < g.j1; ++j, ++n)
+            for (int t = 0; t < nt; ++t, ++i)
+                if (!f(Item{i, n, q0 + t, NT == 1 || t == 0, NT == 1 || t == nt - 1, j == g.j0, j == g.j1 - 1})) return;
+        q0 += nt;
+        if (g.last) return;
+    }
+}
+
 template <int D, bool F8, int NT>
-__device__ void mma_issuer(const TParams &p, unsigned char *smem, uint32_t sbase)
+__device__ void issue_qk(const TParams &p, unsigned char *smem, uint32_t sbase)
 {
     using L = TL<D, F8>;
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::OFF_TMEM);
     const uint32_t bar = sbase + L::OFF_BAR;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
-    constexpr uint32_t idesc_qk = F8 ? rx::idesc_f16(kRows, kBN, false, false) : rx::idesc_bf16(kRows, kBN, false, false);
-    constexpr uint32_t idesc_pv = F8 ? rx::idesc_f16(kRows, D, false, true) : rx::idesc_bf16(kRows, D, false, true);
+    constexpr uint32_t idesc = F8 ? rx::idesc_f16(kRows, kBN, false, false) : rx::idesc_bf16(kRows, kBN, false, false);
     auto wait = [&](int b, uint32_t parity) { return wait_or_abort(bar + 8 * b, parity, abort_flag, p.status); };
     const uint64_t dq = rx::sdesc_sw128(sbase + L::OFF_Q, 16, 1024);
     const uint64_t dk = rx::sdesc_sw128(sbase + L::OFF_K, 16, 1024);
-    const uint64_t dv = rx::sdesc_sw128(sbase + L::OFF_V, L::BLK, 1024);
-
-    struct Item {
-        int i, n, q;                   // item, position tile, row tile
-        bool t0, t1;                   // the first, the last row tile of the position tile
-        bool first, last;              // the row tile's first, last position tile
-    };
-    auto issue_s = [&](const Item &m) -> bool {
+    for_items<L, NT>(p, smem, sbase, [&](const Item &m) -> bool {
         const int st = m.n % kStages, buf = m.i & 1, qb = m.q % L::QB;
         if (m.first && !wait(L::B_QFULL + qb, (m.q / L::QB) & 1)) return false;
         if (m.t0 && !wait(L::B_KFULL + st, (m.n / kStages) & 1)) return false;
@@ -668,51 +689,46 @@ __device__ void mma_issuer(const TParams &p, unsigned char *smem, uint32_t sbase
 #pragma unroll
         for (int kb = 0; kb < D / 16; ++kb) {
             const uint64_t off = (uint64_t)(((kb >> 2) * L::BLK + (kb & 3) * 32) >> 4);
-            rx::tc_mma(tmem + buf * 256, dqs + off, dks + off, idesc_qk, kb > 0);
+            rx::tc_mma(tmem + buf * 256, dqs + off, dks + off, idesc, kb > 0);
         }
         rx::tc_commit(bar + 8 * (L::B_SFULL + buf));
         if (m.t1) rx::tc_commit(bar + 8 * (L::B_KEMPTY + st));
         if (m.last) rx::tc_commit(bar + 8 * (L::B_QEMPTY + qb));
         return true;
-    };
-    auto issue_pv = [&](const Item &m) -> bool {
+    });
+    // everything issued has finished before TMEM is released
+    rx::tc_commit(bar + 8 * L::B_FINAL);
+    rx::drain_wait(bar + 8 * L::B_FINAL, 0, p.status);
+}
+
+template <int D, bool F8, int NT>
+__device__ void issue_pv(const TParams &p, unsigned char *smem, uint32_t sbase)
+{
+    using L = TL<D, F8>;
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::OFF_TMEM);
+    const uint32_t bar = sbase + L::OFF_BAR;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
+    constexpr uint32_t idesc = F8 ? rx::idesc_f16(kRows, D, false, true) : rx::idesc_bf16(kRows, D, false, true);
+    auto wait = [&](int b, uint32_t parity) { return wait_or_abort(bar + 8 * b, parity, abort_flag, p.status); };
+    const uint64_t dv = rx::sdesc_sw128(sbase + L::OFF_V, L::BLK, 1024);
+    for_items<L, NT>(p, smem, sbase, [&](const Item &m) -> bool {
         const int st = m.n % kStages, buf = m.i & 1, ob = m.q & 1;
-        if (!wait(L::B_PFULL + buf, (m.i >> 1) & 1)) return false;
         if (m.t0 && !wait(L::B_VFULL + st, (m.n / kStages) & 1)) return false;
         if (m.first && m.q >= 2 && !wait(L::B_OEMPTY + ob, ((m.q >> 1) - 1) & 1)) return false;
+        if (!wait(L::B_PFULL + buf, (m.i >> 1) & 1)) return false;
         rx::fence_proxy_async_smem();  // V rows landed by cp.async
         rx::tc_fence_after();
         const uint64_t dvs = dv + (uint64_t)((st * L::NB * L::BLK) >> 4);
 #pragma unroll
         for (int ks = 0; ks < kBN / 16; ++ks)
-            rx::tc_mma_ts(tmem + ob * 256 + 128, tmem + buf * 256 + ks * 8, dvs + (uint64_t)((ks * 16 * 128) >> 4),
-                          idesc_pv, (!m.first || ks > 0) ? 1u : 0u);
+            rx::tc_mma_ts(tmem + ob * 256 + 128, tmem + buf * 256 + ks * 8, dvs + (uint64_t)((ks * 16 * 128) >> 4), idesc,
+                          (!m.first || ks > 0) ? 1u : 0u);
         rx::tc_commit(bar + 8 * (L::B_PVDONE + buf));
         if (m.t1) rx::tc_commit(bar + 8 * (L::B_VEMPTY + st));
         return true;
-    };
-    bool ok = true;
-    Item prev{};
-    int i = 0, n = 0, q0 = 0;
-    for (int s = 0; ok; ++s) {
-        Seg g;
-        if (!(ok = get_seg<L>(s, g, smem, sbase, p.status))) break;
-        free_seg<L>(s, sbase);
-        const int nt = NT == 1 ? 1 : g.nt;
-        for (int j = g.j0; j < g.j1 && ok; ++j, ++n)
-            for (int t = 0; t < nt && ok; ++t, ++i) {
-                const Item m{i, n, q0 + t, NT == 1 || t == 0, NT == 1 || t == nt - 1, j == g.j0, j == g.j1 - 1};
-                ok = issue_s(m);
-                if (ok && i > 0) ok = issue_pv(prev);
-                prev = m;
-            }
-        q0 += nt;
-        if (g.last) break;
-    }
-    if (ok) issue_pv(prev);
-    // everything issued has finished before TMEM is released
-    rx::tc_commit(bar + 8 * L::B_FINAL);
-    rx::drain_wait(bar + 8 * L::B_FINAL, 0, p.status);
+    });
+    rx::tc_commit(bar + 8 * (L::B_FINAL + 1));
+    rx::drain_wait(bar + 8 * (L::B_FINAL + 1), 0, p.status);
 }
 
 // ---------------------------------------------------------------------------
@@ -969,9 +985,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         }
         for (int i = 0; i < kSegs; ++i) {
             rx::mbar_init(bar + 8 * (L::B_SEGFULL + i), 32 + 1);  // the scheduler's lanes' copies, and the segment
-            rx::mbar_init(bar + 8 * (L::B_SEGEMPTY + i), kSoftWarps + 2 * kProdWarps + 2);
+            rx::mbar_init(bar + 8 * (L::B_SEGEMPTY + i), kSoftWarps + 2 * kProdWarps + 3);
         }
         rx::mbar_init(bar + 8 * L::B_FINAL, 1);
+        rx::mbar_init(bar + 8 * (L::B_FINAL + 1), 1);
         *reinterpret_cast<volatile int *>(smem + L::OFF_ABORT) = 0;
         rx::fence_mbar_init();
     }
@@ -1011,7 +1028,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         if (warp == kWarpQ) {
             query_loader<D, F8>(p, smem, sbase);
         } else if (warp == kWarpMma) {
-            if ((threadIdx.x & 31) == 0) mma_issuer<D, F8, NT>(p, smem, sbase);
+            if ((threadIdx.x & 31) == 0) issue_qk<D, F8, NT>(p, smem, sbase);
+            __syncwarp();
+        } else if (warp == kWarpPv) {
+            if ((threadIdx.x & 31) == 0) issue_pv<D, F8, NT>(p, smem, sbase);
             __syncwarp();
         } else if (warp == kWarpSched) {
             scheduler<D, F8>(p, smem, sbase);
