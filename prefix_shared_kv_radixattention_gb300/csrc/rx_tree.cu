@@ -27,9 +27,10 @@
 //     results that a second kernel joins by the log-sum-exp identity.  The
 //     heads are outermost, so with 8 heads on 152 SMs nineteen CTAs walk each
 //     head in step and the rows of one slot are read at about the same time;
-//   - S = Q K^T goes to one of two TMEM buffers in turn, so that the tensor
-//     core works on the next tile while four softmax warps (one row a thread)
-//     turn this one into P, written over S and read from there by O += P V.
+//   - four softmax warps (one row a thread) take the scores S = Q K^T of a tile
+//     from TMEM into registers at once, which frees S for the next tile's, and
+//     write P to a TMEM buffer of its own, from where O += P V reads it: the
+//     tensor core works on the tiles before and after meanwhile.
 //
 // All lengths are read on the device, by every CTA for itself: a scan of the
 // batch's lengths in shared memory finds its share.
@@ -72,7 +73,17 @@ static_assert(kThreads * kRegsLaunch <= 65536, "registers of an SM");
 constexpr int kSegs = 4;             // segments handed out ahead
 constexpr int kMaskT = 128;          // trees up to this size have their mask words in shared memory
 constexpr int kRing = 4;             // score scales kept (see query_loader)
-constexpr uint32_t kTmemCols = 512;  // buffer i: S (then P) at 256 i, O at 256 i + 128
+constexpr int kCodeBufs = 3;         // FP8: half tiles of codes in flight, for K and for V
+// TMEM: an O for each row tile, then S buffers (two; one beside two O), then
+// two P of 64 columns (16-bit pairs)
+constexpr uint32_t kTmemCols = 512;
+template <int NT>
+struct Tm {
+    static constexpr int NS = NT == 1 ? 2 : 1;
+    static __device__ __forceinline__ uint32_t o(int t) { return t * 128; }
+    static __device__ __forceinline__ uint32_t s(int b) { return NT * 128 + b * 128; }
+    static __device__ __forceinline__ uint32_t p(int b) { return 384 + b * 64; }
+};
 constexpr float kRescale = 8.f;      // log2 units the running max may lag
 constexpr int kMergeRows = 16;       // rows of one merge CTA
 constexpr int kMergeThreads = 128;
@@ -94,13 +105,15 @@ template <int D, bool F8>
 struct TL {
     static constexpr int NB = D / 64;             // 128-byte column blocks of a row
     static constexpr int BLK = kRows * 128;       // bytes of one column block of a tile
-    // query buffers: two for bf16 pools; one for FP8 pools, whose loads go
-    // through L1 and need the room there
+    // query buffers: two for bf16 pools (of segments in turn, or of a segment's
+    // row tiles); one for FP8 pools, whose codes need the room
     static constexpr int QB = F8 ? 1 : 2;
+    static constexpr int CODE = F8 ? kBN * D / 2 : 0;  // bytes of half a tile of codes
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_K = OFF_Q + QB * NB * BLK;
     static constexpr int OFF_V = OFF_K + kStages * NB * BLK;
-    static constexpr int OFF_NF = OFF_V + kStages * NB * BLK;         // kSegs x 32 words
+    static constexpr int OFF_CODE = OFF_V + kStages * NB * BLK;
+    static constexpr int OFF_NF = OFF_CODE + 2 * kCodeBufs * CODE;    // kSegs x 32 words
     static constexpr int OFF_QS = OFF_NF + kSegs * 32 * 4;            // kRing x 128 floats
     static constexpr int OFF_MASK = OFF_QS + kRing * kRows * 4;       // kSegs x 128 tokens x 4 words;
     static constexpr int MASK = kSegs * kMaskT * (kMaskT / 32) * 4;   //   before them, the scan of the lengths
@@ -109,7 +122,7 @@ struct TL {
     static constexpr int OFF_BAR = OFF_SEG + kSegs * 64;
     static constexpr int B_KFULL = 0, B_KEMPTY = B_KFULL + kStages, B_VFULL = B_KEMPTY + kStages,
                          B_VEMPTY = B_VFULL + kStages, B_QFULL = B_VEMPTY + kStages, B_QEMPTY = B_QFULL + QB,
-                         B_SFULL = B_QEMPTY + QB, B_PFULL = B_SFULL + 2, B_PVDONE = B_PFULL + 2,
+                         B_SFULL = B_QEMPTY + QB, B_SEMPTY = B_SFULL + 2, B_PFULL = B_SEMPTY + 2, B_PVDONE = B_PFULL + 2,
                          B_OEMPTY = B_PVDONE + 2, B_SEGFULL = B_OEMPTY + 2, B_SEGEMPTY = B_SEGFULL + kSegs,
                          B_FINAL = B_SEGEMPTY + kSegs, N_BAR = B_FINAL + 2;
     static constexpr int OFF_TMEM = OFF_BAR + N_BAR * 8;
@@ -118,8 +131,7 @@ struct TL {
     static constexpr int BYTES = OFF_START + 32 + 1024;               // + room to align the base to 1024
 };
 static_assert(sizeof(Seg) <= 64, "room of a segment");
-static_assert(TL<128, false>::BYTES <= 226 * 1024, "shared memory budget");
-static_assert(TL<128, true>::BYTES <= 194 * 1024, "leaves 60 KB of L1");
+static_assert(TL<128, false>::BYTES <= 226 * 1024 && TL<128, true>::BYTES <= 226 * 1024, "shared memory budget");
 static_assert(TL<128, false>::OFF_MASK % 16 == 0 && TL<128, false>::OFF_BAR % 8 == 0, "alignment");
 
 struct TParams {
@@ -380,15 +392,14 @@ __device__ __forceinline__ uint4 widen_f16(uint32_t lo, uint32_t hi)
 
 // Eight producer warps for K and eight for V (V's wait for the softmax does
 // not hold up K); warp w gathers rows [16 w, 16 w + 16) of every tile in
-// 16-byte pieces, slot ids two tiles ahead.
+// 16-byte async copies, slot ids two tiles ahead.  (Loads into registers go
+// through L1, which this kernel's shared memory leaves 28 KB: they ran at half
+// the rate.)
 //
-// bf16 pools: async copies that land in the swizzled tile itself and report to
-// its barrier (loads into registers go through L1, which this much shared
-// memory leaves 28 KB: they ran at half the rate).  FP8 pools: loads into
-// registers, a tile ahead, widened (E4M3 to f16 is exact) and stored to the
-// tile; half the bytes and one query buffer less leave 60 KB of L1 for them,
-// and codes copied to shared memory first would cost two more passes through
-// it, which the tensor core's operands keep busy.
+// bf16 pools: the copies land in the swizzled tile itself and report to its
+// barrier.  FP8 pools: they land in a ring of three half tiles of codes; each
+// thread widens the chunks that it copied (E4M3 to f16 is exact) and stores
+// them to the tile.
 //
 // V at drafted positions is looked at before it is handed over: a NaN or
 // infinity there would reach rows that do not see the position (0 * inf), so it
@@ -427,7 +438,7 @@ __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
     // the next tile, with the loads of its slot ids
     auto take = [&](Tile &t) {
         t.slot = -1;
-        t.lim = 0;
+        t.lim = t.meta = 0;
         if (left == 0) {
             if (last) return;
             Seg q;
@@ -461,11 +472,6 @@ __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
         const int32_t id = __shfl_sync(0xffffffffu, t.slot, u * RPI + sub);
         ok = id >= 0;
         return pool + (ok ? (int64_t)id * row_bytes : 0) + (t.g() * (D * EB) + ch * 16);
-    };
-    auto load = [&](const Tile &t, int u) {
-        bool ok;
-        const unsigned char *src = source(t, u, ok);
-        return ok ? rx::ld_stream(src) : make_uint4(0, 0, 0, 0);
     };
     // this thread's chunks of V at drafted positions, once they are in the tile
     auto scrub = [&](uint32_t off, const Tile &t) {
@@ -511,19 +517,25 @@ __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
         }
         rx::cp_async_wait_all();  // nothing may still be landing when the CTA exits
     } else {
-        // the rows in two halves: a half's registers take the next tile's codes
-        // as soon as they are stored
-        constexpr int H = U / 2;
-        uint4 x[U];
-        auto fetch = [&](const Tile &t, int h) {
+        constexpr int H = U / 2;  // instructions of half a tile
+        // chunk u of half-tile buffer b: + b CODE + 512 u
+        const uint32_t mine = L::OFF_CODE + (IS_V ? kCodeBufs * L::CODE : 0) + (uint32_t)(pw * H * 32 + lane) * 16;
+        auto fetch = [&](const Tile &t, int h, int buf) {
 #pragma unroll
-            for (int u = h * H; u < (h + 1) * H; ++u) x[u] = load(t, u);
+            for (int u = 0; u < H; ++u) {
+                bool ok;
+                const unsigned char *src = source(t, h * H + u, ok);
+                rx::cp_async_16(sbase + mine + buf * L::CODE + u * 512, src, ok ? 16 : 0);
+            }
+            rx::cp_async_commit();
         };
-        auto widen = [&](uint32_t off, int h) {
+        // this thread's chunks of a landed half into the tile at `off`
+        auto widen = [&](uint32_t off, int h, int buf) {
 #pragma unroll
-            for (int u = h * H; u < (h + 1) * H; ++u) {
-                const uint4 a = widen_f16(x[u].x, x[u].y), b = widen_f16(x[u].z, x[u].w);
-                const int r = r0 + u * RPI + sub;
+            for (int u = 0; u < H; ++u) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(smem + mine + buf * L::CODE + u * 512);
+                const uint4 a = widen_f16(x.x, x.y), b = widen_f16(x.z, x.w);
+                const int r = r0 + (h * H + u) * RPI + sub;
                 // the upper lanes of a row store their second chunk first: the
                 // two column blocks of a row lie on the same banks
                 const int swap = D == 128 ? (ch >> 2) & 1 : 0;
@@ -531,27 +543,35 @@ __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
                 *reinterpret_cast<uint4 *>(smem + off + sw128(r, 2 * ch + 1 - swap, L::BLK)) = swap ? a : b;
             }
         };
-        Tile cur, nxt;
+        Tile cur, nxt, nx2;
         take(cur);
         take(nxt);
         check(cur);
-        fetch(cur, 0);
-        fetch(cur, 1);
+        check(nxt);
+        fetch(cur, 0, 0);
+        fetch(cur, 1, 1);
+        fetch(nxt, 0, 2);
+        int buf = 0;  // of the tile's first half; three halves are in flight
         for (int n = 0; cur.lim > 0; ++n) {
-            const int st = n % kStages;
+            const int st = n % kStages, buf1 = buf == 2 ? 0 : buf + 1, buf2 = buf1 == 2 ? 0 : buf1 + 1;
             const uint32_t off = (IS_V ? L::OFF_V : L::OFF_K) + st * L::NB * L::BLK;
-            check(nxt);
+            take(nx2);
+            rx::cp_async_wait<2>();     // the first half
             if (n >= kStages && !warp_wait(bar_empty + 8 * st, (n / kStages - 1) & 1, abort_flag, p.status)) break;
-            widen(off, 0);
-            fetch(nxt, 0);
-            widen(off, 1);
-            fetch(nxt, 1);
+            widen(off, 0, buf);
+            fetch(nxt, 1, buf);
+            rx::cp_async_wait<2>();     // the second
+            widen(off, 1, buf1);
             if (IS_V && cur.rel() + kBN > 0) scrub(off, cur);  // the tile has drafted positions
             rx::fence_proxy_async_smem();
             rx::mbar_arrive(bar_full + 8 * st);
+            check(nx2);
+            fetch(nx2, 0, buf1);
+            buf = buf2;
             cur = nxt;
-            take(nxt);
+            nxt = nx2;
         }
+        rx::cp_async_wait_all();
     }
 }
 
@@ -559,68 +579,95 @@ __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
 // query rows
 // ---------------------------------------------------------------------------
 
-// One warp copies each segment's query rows (row r: drafted token r / G of the
-// row tile, q head g G + r % G) into a query buffer.  bf16 pools: 16-byte
-// async copies.  FP8 pools: the products run in f16, which holds every E4M3
-// value; a query row is brought to f16 times a power of two that puts its
-// largest value just below 2^15 (values 2^-29 of that and above stay exact),
-// and the power goes into the row's score scale.
-template <int D, bool F8>
+// One warp copies each segment's query rows (row r of row tile t: drafted token
+// t tb + r / G of the segment, q head g G + r % G).  bf16 pools: 16-byte async
+// copies.  FP8 pools: the products run in f16, which holds every E4M3 value; a
+// query row is brought to f16 times a power of two that puts its largest value
+// just below 2^15 (values 2^-29 of that and above stay exact), and the power
+// goes into the row's score scale.
+//
+// Buffers: with one row tile a segment, of the segments in turn; with two, one
+// for each row tile.
+template <int D, bool F8, int NT>
 __device__ void query_loader(const TParams &p, unsigned char *smem, uint32_t sbase)
 {
     using L = TL<D, F8>;
-    constexpr int CPR = D / 8;
+    constexpr int CPR = D / 8, RPI = 32 / CPR;   // chunks of a row, rows of one instruction
+    constexpr int UQ = 4;                        // FP8: instructions in flight
     const uint32_t bar = sbase + L::OFF_BAR;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
-    const int lane = threadIdx.x & 31;
-    int qi = 0;  // row tiles so far
+    const int lane = threadIdx.x & 31, sub = lane / CPR, ch = lane % CPR;
+    int uses[2] = {0, 0};  // of each buffer
     for (int s = 0;; ++s) {
         Seg g;
         if (!__all_sync(0xffffffffu, get_seg<L>(s, g, smem, sbase, p.status))) break;
         __syncwarp();
         if (lane == 0) free_seg<L>(s, sbase);
         bool ok = true;
-        for (int t = 0; t < g.nt && ok; ++t, ++qi) {
-        const int buf = qi % L::QB;
-        const int M = min(p.tb, g.ntok - t * p.tb) * p.G;
-        const int64_t tok0 = (int64_t)g.tok + t * p.tb;
-        if (qi >= L::QB && !(ok = warp_wait(bar + 8 * (L::B_QEMPTY + buf), (qi / L::QB - 1) & 1, abort_flag, p.status))) break;
-        const uint32_t dst = sbase + L::OFF_Q + buf * L::NB * L::BLK;
-        for (int i0 = 0; i0 < M * CPR; i0 += 32) {
-            const int i = i0 + lane, r = i / CPR, ch = i % CPR;
-            const bool in = i < M * CPR;
-            const bf16 *src = in ? p.q + ((tok0 + r / p.G) * p.hq + (int64_t)g.g * p.G + r % p.G) * D + ch * 8 : p.q;
-            if constexpr (!F8) {
-                if (in) rx::cp_async_16(dst + sw128(r, ch, L::BLK), src, 16);
-            } else {
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (in) x = __ldg(reinterpret_cast<const uint4 *>(src));
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                uint32_t top = 0;  // largest magnitude (bf16 bits) of the row
 #pragma unroll
-                for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
+        for (int t = 0; t < NT; ++t) {
+            if (t >= g.nt || !ok) break;
+            const int buf = NT == 1 ? s % L::QB : t, use = NT == 1 ? s / L::QB : uses[t]++;
+            const int M = min(p.tb, g.ntok - t * p.tb) * p.G;
+            if (use >= 1 && !(ok = warp_wait(bar + 8 * (L::B_QEMPTY + buf), (use - 1) & 1, abort_flag, p.status))) break;
+            const uint32_t dst = L::OFF_Q + buf * L::NB * L::BLK;
+            // this lane's row, its drafted token's query row and its head
+            int r = sub;
+            const int step_t = RPI / p.G, step_h = RPI - step_t * p.G;
+            int h = r % p.G;
+            int64_t src = ((int64_t)(g.tok + t * p.tb + r / p.G) * p.hq + (int64_t)g.g * p.G + h) * D + ch * 8;
+            auto advance = [&]() {  // RPI rows on
+                r += RPI;
+                h += step_h;
+                src += ((int64_t)step_t * p.hq + step_h) * D;
+                if (h >= p.G) {     // the next drafted token's first heads
+                    h -= p.G;
+                    src += (int64_t)(p.hq - p.G) * D;
+                }
+            };
+            while (r - sub < M) {
+                if constexpr (!F8) {
+                    if (r < M) rx::cp_async_16(sbase + dst + sw128(r, ch, L::BLK), p.q + src, 16);
+                    advance();
+                } else {
+                    const int rbase = r;
+                    uint4 x[UQ];
 #pragma unroll
-                for (int d = CPR / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-                const int e = max((int)(top >> 7) - 127, -100);
-                const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);  // 2^(14 - e)
-                uint32_t y[4];
+                    for (int u = 0; u < UQ; ++u) {
+                        x[u] = make_uint4(0, 0, 0, 0);
+                        if (r < M) x[u] = rx::ld_stream(p.q + src);
+                        advance();
+                    }
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    y[k] = rx::pack_f16(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xFFFF0000u) * up);
-                if (in) {
-                    *reinterpret_cast<uint4 *>(smem + (dst - sbase) + sw128(r, ch, L::BLK)) = make_uint4(y[0], y[1], y[2], y[3]);
-                    if (ch == 0)
-                        reinterpret_cast<float *>(smem + L::OFF_QS)[(qi % kRing) * kRows + r] =
-                            __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+                    for (int u = 0; u < UQ; ++u) {
+                        const int ru = rbase + u * RPI;
+                        const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+                        uint32_t top = 0;  // largest magnitude (bf16 bits) of the row
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) top = max(top, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
+#pragma unroll
+                        for (int d = CPR / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+                        const int e = max((int)(top >> 7) - 127, -100);
+                        const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);  // 2^(14 - e)
+                        uint32_t y[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            y[k] = rx::pack_f16(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xFFFF0000u) * up);
+                        if (ru < M) {
+                            *reinterpret_cast<uint4 *>(smem + dst + sw128(ru, ch, L::BLK)) = make_uint4(y[0], y[1], y[2], y[3]);
+                            if (ch == 0)
+                                reinterpret_cast<float *>(smem + L::OFF_QS)[(s % kRing) * kRows + ru] =
+                                    __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+                        }
+                    }
                 }
             }
-        }
-        if constexpr (F8) {
-            rx::fence_proxy_async_smem();
-            rx::mbar_arrive(bar + 8 * (L::B_QFULL + buf));
-        } else {
-            rx::cp_async_mbar_arrive(bar + 8 * (L::B_QFULL + buf));
-        }
+            if constexpr (F8) {
+                rx::fence_proxy_async_smem();
+                rx::mbar_arrive(bar + 8 * (L::B_QFULL + buf));
+            } else {
+                rx::cp_async_mbar_arrive(bar + 8 * (L::B_QFULL + buf));
+            }
         }
         if (!ok || g.last) break;
     }
@@ -632,18 +679,21 @@ __device__ void query_loader(const TParams &p, unsigned char *smem, uint32_t sba
 // ---------------------------------------------------------------------------
 
 // The CTA's items i = 0, 1, ...: for every position tile n (all segments in a
-// row) the segment's row tiles t.  S(i) = Q_t K_n^T goes into buffer i & 1; the O
-// (and Q) of the q-th row tile of the CTA into buffer q & 1.  P(i - 2) sits in
-// the columns that S(i) overwrites, so S(i) waits for that product's
-// completion.  The products of odd and even items complete on barriers of their
-// own: whoever waits for one knows that the one two items before has completed,
-// so a phase's parity is never ambiguous.
+// row) the segment's row tiles t.  S(i) = Q_t K_n^T waits for an S buffer whose
+// scores the softmax has in registers, O_t += P(i) V_n for P(i).  P(i), in
+// buffer i & 1, is stored once the product of item i - 2 has completed; the
+// products of odd and even items complete on barriers of their own, so that
+// whoever waits for one knows that the one two items before has completed and
+// a phase's parity is never ambiguous.
 //
 // S and P V are issued by a thread each: a thread spends as long on the waits
 // and commits around an operation's eight MMAs as on the MMAs, and with one
-// thread for both the tensor core idled meanwhile (@TWO@).
+// thread for both the tensor core idled meanwhile (long chat 0.252 against
+// 0.242 ms).
 struct Item {
-    int i, n, q;                   // item, position tile, row tile
+    int i, n, t;
+    int use;                       // row tiles before this one in its O (and Q) buffer
+    int seg;
     bool t0, t1;                   // the first, the last row tile of the position tile
     bool first, last;              // the row tile's first, last position tile
 };
@@ -652,7 +702,7 @@ struct Item {
 template <typename L, int NT, typename F>
 __device__ __forceinline__ void for_items(const TParams &p, unsigned char *smem, uint32_t sbase, F f)
 {
-    int i = 0, n = 0, q0 = 0;
+    int i = 0, n = 0, s2 = 0;  // s2: segments with two row tiles
     for (int s = 0;; ++s) {
         Seg g;
         if (!get_seg<L>(s, g, smem, sbase, p.status)) return;
@@ -660,8 +710,9 @@ __device__ __forceinline__ void for_items(const TParams &p, unsigned char *smem,
         const int nt = NT == 1 ? 1 : g.nt;
         for (int j = g.j0; j < g.j1; ++j, ++n)
             for (int t = 0; t < nt; ++t, ++i)
-                if (!f(Item{i, n, q0 + t, NT == 1 || t == 0, NT == 1 || t == nt - 1, j == g.j0, j == g.j1 - 1})) return;
-        q0 += nt;
+                if (!f(Item{i, n, t, t == 0 ? s : s2, s, NT == 1 || t == 0, NT == 1 || t == nt - 1, j == g.j0, j == g.j1 - 1}))
+                    return;
+        s2 += nt == 2;
         if (g.last) return;
     }
 }
@@ -670,6 +721,7 @@ template <int D, bool F8, int NT>
 __device__ void issue_qk(const TParams &p, unsigned char *smem, uint32_t sbase)
 {
     using L = TL<D, F8>;
+    using M = Tm<NT>;
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::OFF_TMEM);
     const uint32_t bar = sbase + L::OFF_BAR;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
@@ -678,10 +730,11 @@ __device__ void issue_qk(const TParams &p, unsigned char *smem, uint32_t sbase)
     const uint64_t dq = rx::sdesc_sw128(sbase + L::OFF_Q, 16, 1024);
     const uint64_t dk = rx::sdesc_sw128(sbase + L::OFF_K, 16, 1024);
     for_items<L, NT>(p, smem, sbase, [&](const Item &m) -> bool {
-        const int st = m.n % kStages, buf = m.i & 1, qb = m.q % L::QB;
-        if (m.first && !wait(L::B_QFULL + qb, (m.q / L::QB) & 1)) return false;
+        const int st = m.n % kStages, b = m.i % M::NS;
+        const int qb = NT == 1 ? m.seg % L::QB : m.t, quse = NT == 1 ? m.seg / L::QB : m.use;
+        if (m.first && !wait(L::B_QFULL + qb, quse & 1)) return false;
         if (m.t0 && !wait(L::B_KFULL + st, (m.n / kStages) & 1)) return false;
-        if (m.i >= 2 && !wait(L::B_PVDONE + buf, ((m.i >> 1) - 1) & 1)) return false;  // O += P V of item i - 2
+        if (m.i >= M::NS && !wait(L::B_SEMPTY + b, (m.i / M::NS - 1) & 1)) return false;
         rx::fence_proxy_async_smem();  // rows landed by cp.async -> async proxy
         rx::tc_fence_after();
         const uint64_t dks = dk + (uint64_t)((st * L::NB * L::BLK) >> 4);
@@ -689,9 +742,9 @@ __device__ void issue_qk(const TParams &p, unsigned char *smem, uint32_t sbase)
 #pragma unroll
         for (int kb = 0; kb < D / 16; ++kb) {
             const uint64_t off = (uint64_t)(((kb >> 2) * L::BLK + (kb & 3) * 32) >> 4);
-            rx::tc_mma(tmem + buf * 256, dqs + off, dks + off, idesc, kb > 0);
+            rx::tc_mma(tmem + M::s(b), dqs + off, dks + off, idesc, kb > 0);
         }
-        rx::tc_commit(bar + 8 * (L::B_SFULL + buf));
+        rx::tc_commit(bar + 8 * (L::B_SFULL + b));
         if (m.t1) rx::tc_commit(bar + 8 * (L::B_KEMPTY + st));
         if (m.last) rx::tc_commit(bar + 8 * (L::B_QEMPTY + qb));
         return true;
@@ -705,6 +758,7 @@ template <int D, bool F8, int NT>
 __device__ void issue_pv(const TParams &p, unsigned char *smem, uint32_t sbase)
 {
     using L = TL<D, F8>;
+    using M = Tm<NT>;
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::OFF_TMEM);
     const uint32_t bar = sbase + L::OFF_BAR;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
@@ -712,18 +766,18 @@ __device__ void issue_pv(const TParams &p, unsigned char *smem, uint32_t sbase)
     auto wait = [&](int b, uint32_t parity) { return wait_or_abort(bar + 8 * b, parity, abort_flag, p.status); };
     const uint64_t dv = rx::sdesc_sw128(sbase + L::OFF_V, L::BLK, 1024);
     for_items<L, NT>(p, smem, sbase, [&](const Item &m) -> bool {
-        const int st = m.n % kStages, buf = m.i & 1, ob = m.q & 1;
+        const int st = m.n % kStages, b = m.i & 1;
         if (m.t0 && !wait(L::B_VFULL + st, (m.n / kStages) & 1)) return false;
-        if (m.first && m.q >= 2 && !wait(L::B_OEMPTY + ob, ((m.q >> 1) - 1) & 1)) return false;
-        if (!wait(L::B_PFULL + buf, (m.i >> 1) & 1)) return false;
+        if (m.first && m.use >= 1 && !wait(L::B_OEMPTY + m.t, (m.use - 1) & 1)) return false;
+        if (!wait(L::B_PFULL + b, (m.i >> 1) & 1)) return false;
         rx::fence_proxy_async_smem();  // V rows landed by cp.async
         rx::tc_fence_after();
         const uint64_t dvs = dv + (uint64_t)((st * L::NB * L::BLK) >> 4);
 #pragma unroll
         for (int ks = 0; ks < kBN / 16; ++ks)
-            rx::tc_mma_ts(tmem + ob * 256 + 128, tmem + buf * 256 + ks * 8, dvs + (uint64_t)((ks * 16 * 128) >> 4), idesc,
+            rx::tc_mma_ts(tmem + M::o(m.t), tmem + M::p(b) + ks * 8, dvs + (uint64_t)((ks * 16 * 128) >> 4), idesc,
                           (!m.first || ks > 0) ? 1u : 0u);
-        rx::tc_commit(bar + 8 * (L::B_PVDONE + buf));
+        rx::tc_commit(bar + 8 * (L::B_PVDONE + b));
         if (m.t1) rx::tc_commit(bar + 8 * (L::B_VEMPTY + st));
         return true;
     });
@@ -771,13 +825,14 @@ template <int D, bool F8, int NT>
 __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sbase)
 {
     using L = TL<D, F8>;
+    using TM = Tm<NT>;
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::OFF_TMEM);
     const uint32_t bar = sbase + L::OFF_BAR;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
     const int row = threadIdx.x;                       // = TMEM lane
     const uint32_t lanes = (uint32_t)(row & ~31) << 16;
     const int rt = row / p.G, rh = row - rt * p.G;     // drafted token of the row tile, q head of the kv head
-    int i = 0, q0 = 0;                                 // items and row tiles of the segments before
+    int i = 0;                                         // items so far
     for (int s = 0;; ++s) {
         Seg g;
         if (!__all_sync(0xffffffffu, get_seg<L>(s, g, smem, sbase, p.status))) return;
@@ -790,20 +845,34 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
         RowState a{-INFINITY, 0.f, p.scale_log2}, b = a;   // the item's row tile, and the other one
         for (int j = g.j0; j < g.j1; ++j)
             for (int t = 0; t < nt; ++t, ++i) {
-                const int buf = i & 1;
-                const uint32_t tS = tmem + buf * 256 + lanes, tO = tmem + ((q0 + t) & 1) * 256 + 128 + lanes;
+                const int sb = i % TM::NS;
+                const uint32_t tS = tmem + TM::s(sb) + lanes, tO = tmem + TM::o(t) + lanes, tP = tmem + TM::p(i & 1) + lanes;
                 const int M = min(p.tb, g.ntok - t * p.tb) * p.G;
                 const bool valid = row < M, warp_on = (row & ~31) < M;
-                if (!warp_wait(bar + 8 * (L::B_SFULL + buf), (i >> 1) & 1, abort_flag, p.status)) return;
+                if (!warp_wait(bar + 8 * (L::B_SFULL + sb), (i / TM::NS) & 1, abort_flag, p.status)) return;
                 rx::tc_fence_after();
-                if (warp_on) {
+                auto release_s = [&]() {
+                    rx::tc_fence_before();
+                    rx::mbar_arrive(bar + 8 * (L::B_SEMPTY + sb));
+                };
+                // the product two items before has read P's columns (a warp
+                // without rows waits too, or it could arrive twice in a phase)
+                auto p_free = [&]() {
+                    const bool ok = i < 2 || warp_wait(bar + 8 * (L::B_PVDONE + (i & 1)), ((i >> 1) - 1) & 1, abort_flag, p.status);
+                    rx::tc_fence_after();
+                    return ok;
+                };
+                if (!warp_on) {
+                    release_s();
+                    if (!p_free()) return;
+                } else {
                     // the row's scores of this tile, loaded once (four loads in
                     // flight): a load takes about 200 cycles to come back
                     uint32_t sv[kBN];
 #pragma unroll
                     for (int k = 0; k < kBN / 32; ++k) rx::tmem_ld32(tS + k * 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * k));
                     if (F8 && j == g.j0)
-                        a.sl2 = p.scale_log2 * reinterpret_cast<const float *>(smem + L::OFF_QS)[((q0 + t) % kRing) * kRows + row];
+                        a.sl2 = p.scale_log2 * reinterpret_cast<const float *>(smem + L::OFF_QS)[(s % kRing) * kRows + row];
                     const int kbase = j * kBN;
                     if (kbase + kBN > g.P) {   // drafted positions, or past the last
                         const int off = kbase - g.P, w0 = off >> 5, node = rt + t * p.tb;
@@ -812,6 +881,7 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
 #pragma unroll
                         for (int k = 0; k < 5; ++k) w[k] = mask_word(mrow, words, g.node + node, g.T, w0 + k);
                         rx::tmem_wait_ld();
+                        release_s();
 #pragma unroll
                         for (int k = 0; k < kBN / 32; ++k) {
                             const uint32_t bits = __funnelshift_r(w[k], w[k + 1], off & 31);
@@ -821,6 +891,7 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
                         }
                     } else {
                         rx::tmem_wait_ld();
+                        release_s();
                     }
                     float mx;
                     {
@@ -845,6 +916,7 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
                     const float mu = a.m == -INFINITY ? 0.f : a.m;
                     const uint64_t scale2 = rx::f2(a.sl2, a.sl2), negm2 = rx::f2(-mu, -mu);
                     uint64_t acc[4] = {0, 0, 0, 0};
+                    if (!p_free()) return;
 #pragma unroll
                     for (int k = 0; k < kBN / 64; ++k) {
                         uint32_t pk[32];
@@ -858,14 +930,14 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
                             // the tensor core; their sum is not
                             pk[e] = F8 ? rx::pack_f16(e0, e1) : rx::pack_bf16(e0, e1);
                         }
-                        rx::tmem_st32(tS + k * 32, pk);  // over scores already read
+                        rx::tmem_st32(tP + k * 32, pk);
                     }
                     float a0, a1;
                     rx::f2_split(rx::f2_add(rx::f2_add(acc[0], acc[1]), rx::f2_add(acc[2], acc[3])), a0, a1);
                     a.l += a0 + a1;
                     if (__any_sync(0xffffffffu, scale_o)) {
-                        // this row tile's O += P V before has to be complete: item
-                        // i - nt; i - 2 is (S(i) waited for it)
+                        // this row tile's product before, item i - nt, has to be
+                        // complete; i - 2 is
                         if (nt == 1 && !warp_wait(bar + 8 * (L::B_PVDONE + ((i - 1) & 1)), ((i - 1) >> 1) & 1, abort_flag, p.status))
                             return;
                         rx::tc_fence_after();
@@ -882,7 +954,7 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
                     rx::tmem_wait_st();
                 }
                 rx::tc_fence_before();
-                rx::mbar_arrive(bar + 8 * (L::B_PFULL + buf));
+                rx::mbar_arrive(bar + 8 * (L::B_PFULL + (i & 1)));
                 if (nt == 2) {
                     const RowState x = a;
                     a = b;
@@ -900,33 +972,38 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
             const RowState &r = t == 0 ? a : b;
             const int M = min(p.tb, g.ntok - t * p.tb) * p.G, node = rt + t * p.tb;
             const bool valid = row < M, warp_on = (row & ~31) < M;
-            const uint32_t tO = tmem + ((q0 + t) & 1) * 256 + 128 + lanes;
+            const uint32_t tO = tmem + TM::o(t) + lanes;
             const float inv = r.l == 0.f ? 0.f : p.v_scale / r.l;
             const int64_t orow = (int64_t)(g.tok + node) * p.hq + (int64_t)g.g * p.G + rh;
             const int64_t prow = ((int64_t)(2 * blockIdx.x + (g.j0 == 0 ? 1 : 0)) * NT + t) * kRows + row;
             if (warp_on) {
-                uint32_t x[D];
+                // not unrolled: straight-line code that runs once a segment is
+                // fetched more slowly than it runs
+#pragma unroll 1
+                for (int k = 0; k < D / 32; ++k) {
+                    uint32_t x[32];
+                    rx::tmem_ld32(tO + k * 32, x);
+                    rx::tmem_wait_ld();
+                    if (valid) {
 #pragma unroll
-                for (int k = 0; k < D / 32; ++k) rx::tmem_ld32(tO + k * 32, *reinterpret_cast<uint32_t(*)[32]>(x + 32 * k));
-                rx::tmem_wait_ld();
-                if (valid) {
+                    for (int e = 0; e < 32; ++e) x[e] = r.l == 0.f ? 0u : __float_as_uint(u2f(x[e]) * inv);
                     if (g.whole) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(p.o + orow * D);
+                        uint4 *dst = reinterpret_cast<uint4 *>(p.o + orow * D + k * 32);
 #pragma unroll
-                        for (int e = 0; e < D / 8; ++e) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) w[k] = rx::pack_bf16(u2f(x[8 * e + 2 * k]) * inv, u2f(x[8 * e + 2 * k + 1]) * inv);
-                            dst[e] = r.l == 0.f ? make_uint4(0, 0, 0, 0) : make_uint4(w[0], w[1], w[2], w[3]);
-                        }
+                        for (int e = 0; e < 4; ++e)
+                            dst[e] = make_uint4(rx::pack_bf16(u2f(x[8 * e]), u2f(x[8 * e + 1])),
+                                                rx::pack_bf16(u2f(x[8 * e + 2]), u2f(x[8 * e + 3])),
+                                                rx::pack_bf16(u2f(x[8 * e + 4]), u2f(x[8 * e + 5])),
+                                                rx::pack_bf16(u2f(x[8 * e + 6]), u2f(x[8 * e + 7])));
                     } else {
-                        float4 *dst = reinterpret_cast<float4 *>(p.part_o + prow * D);
+                        uint4 *dst = reinterpret_cast<uint4 *>(p.part_o + prow * D + k * 32);
 #pragma unroll
-                        for (int e = 0; e < D / 4; ++e)
-                            dst[e] = r.l == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                                : make_float4(u2f(x[4 * e]) * inv, u2f(x[4 * e + 1]) * inv,
-                                                              u2f(x[4 * e + 2]) * inv, u2f(x[4 * e + 3]) * inv);
+                        for (int e = 0; e < 8; ++e) dst[e] = make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
                     }
+                    }
+                    __syncwarp();
+                }
+                if (valid) {
                     const float l2 = r.l == 0.f ? -INFINITY : r.m + log2f(r.l);
                     if (!g.whole) p.part_l[prow] = l2;
                     else if (p.lse) p.lse[orow] = l2 * rx::kLn2;
@@ -934,7 +1011,7 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
                 __syncwarp();
             }
             rx::tc_fence_before();
-            rx::mbar_arrive(bar + 8 * (L::B_OEMPTY + ((q0 + t) & 1)));
+            rx::mbar_arrive(bar + 8 * (L::B_OEMPTY + t));
             if (g.j1 * kBN > g.P) {
                 if (t == 0)
                     for (int w = 0; w < (g.T + 31) / 32; ++w) any |= nf[w];
@@ -943,7 +1020,6 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
                                           g.P, g.T, g.whole ? -1 : prow, orow);
             }
         }
-        q0 += nt;
         if (any) {  // the same for every thread: all have read the words, then they are cleared
             rx::named_bar_sync(1, 32 * kSoftWarps);
             if (row < 32) const_cast<uint32_t *>(nf)[row] = 0;
@@ -979,6 +1055,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         }
         for (int i = 0; i < 2; ++i) {
             rx::mbar_init(bar + 8 * (L::B_SFULL + i), 1);
+            rx::mbar_init(bar + 8 * (L::B_SEMPTY + i), kRows);
             rx::mbar_init(bar + 8 * (L::B_PFULL + i), kRows);
             rx::mbar_init(bar + 8 * (L::B_PVDONE + i), 1);
             rx::mbar_init(bar + 8 * (L::B_OEMPTY + i), kRows);
@@ -1026,7 +1103,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     } else {
         rx::reg_dec<kRegsMisc>();
         if (warp == kWarpQ) {
-            query_loader<D, F8>(p, smem, sbase);
+            query_loader<D, F8, NT>(p, smem, sbase);
         } else if (warp == kWarpMma) {
             if ((threadIdx.x & 31) == 0) issue_qk<D, F8, NT>(p, smem, sbase);
             __syncwarp();
@@ -1139,9 +1216,6 @@ int launch(const TParams &p, cudaStream_t st)
 {
     // per device; cheap, and right whichever device is current
     RX_CUDA_CHECK(cudaFuncSetAttribute(tree_kernel<D, F8, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (TL<D, F8>::BYTES)));
-    if (F8)  // no more shared memory than it needs: the rest is L1
-        RX_CUDA_CHECK(cudaFuncSetAttribute(tree_kernel<D, F8, NT>, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                           ((TL<D, F8>::BYTES) + 2048) * 100 / (228 * 1024) + 1));
     tree_kernel<D, F8, NT><<<kCtas, kThreads, (TL<D, F8>::BYTES), st>>>(p);
     RX_CUDA_CHECK(cudaGetLastError());
     // a programmatic dependent: it finds its part of the work, then waits on the device
