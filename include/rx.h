@@ -750,7 +750,7 @@ int rx_fsm_step(const rx_fsm *fsm, const float *logits, int64_t logits_stride, i
  *     count = how often t is among the request's tokens behind its prompt,
  *             plus, in a tree, on the row's path,
  *     y = seen ? (x > 0 ? x / repetition[b] : x * repetition[b]) : x
- *     y = y - frequency[b] * count
+ *     y = count > 0 ? y - frequency[b] * count : y
  *     y = count > 0 ? y - presence[b] : y
  *     y = y + the sum of b's biases of t, added up in list order
  *     out[r][t] = t allowed by the row's mask ? y : -inf,
@@ -759,9 +759,9 @@ int rx_fsm_step(const rx_fsm *fsm, const float *logits, int64_t logits_stride, i
  * Rows: without qo_indptr, row r is request r (n_req rows).  With it, rows
  * qo_indptr[b] .. qo_indptr[b+1] - 1 are request b's drafted tokens, and the
  * path of row r is the drafted tokens draft_tok[qo_indptr[b] + j] with bit j
- * set in tree_mask row r (as rx_attn_tree reads them; at most 1024 a
- * request, more sets RX_DEV_BAD_LEN and leaves the request's rows
- * unwritten).  Rows behind the last are left as they were.
+ * set in tree_mask row r (as rx_attn_tree reads them; a request with more
+ * than 1024 of them, or than the mask's bits, sets RX_DEV_BAD_LEN and gets
+ * its mask only).  Rows behind the last are left as they were.
  * All pointers are device memory.  NULL leaves a part out: hist (no request
  * tokens), repetition (1), frequency and presence (0), bias_ptr, allow,
  * draft_tok (no paths). */

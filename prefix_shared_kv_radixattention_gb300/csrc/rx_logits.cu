@@ -3,23 +3,39 @@
 //
 // For every id t of a logits row of request b, x = logits[t]:
 //     y = seen ? (x > 0 ? x / repetition : x repetition) : x
-//     y = y - frequency count;  y = count > 0 ? y - presence : y
+//     y = count > 0 ? (y - frequency count) - presence : y
 //     y = y + sum of the request's biases of t;  out = allowed ? y : -inf
 // with seen / count over the request's token list and, for a drafted tree,
 // the drafted tokens on the row's path.
 //
 // The floor is one write of the fp32 row and one read of the logits that the
-// mask allows: an element needs a handful of operations, so the work is a
-// stream.  Few ids are touched by a penalty or a bias; the rest are copied
-// (or become -inf).  A CTA takes a tile of consecutive ids for some rows of
-// one request: it first counts the request's tokens that fall into its tile
-// in shared memory (32-bit words: the count, a bit "in the prompt", a bit
-// "has a bias"), with a bit map of the touched groups of four ids, then
-// streams the rows through that table.  A group of four ids without an
-// allowed one is not read at all.  A row's path is added to the table before
-// the row and taken out after it.
+// mask allows.  A CTA takes a tile of the ids of one request and all of its rows
+// (with few requests, some of them):
+//
+//   - the request's words for the tile's ids (the count, a bit "in the prompt",
+//     "has a bias", "is drafted") are made in shared memory: each CTA reads all
+//     of the request's tokens and counts those of its tile, the others cost a few
+//     instructions;
+//   - row by row, a thread takes groups of four ids: the logits (not read where
+//     the mask allows none of the four), their words, the values.  The next
+//     row's logits are on their way meanwhile.
+//
+// So the rows move once, in whole sectors.  What bounds it is partly that, partly
+// the counting (a request's 32,768 tokens are read by every tile's CTA), partly
+// the 70 instructions for four touched ids: 192 drafted rows of 128,256 bf16
+// logits take 60 us (3.3 times their 133 MB), 64 rows of fp32 logits 33 us, one
+// row of 32,000 ids 6.7 us.  A copy of the rows followed by a kernel for the
+// listed touched ids alone took 92, 37 and 5.6 us: partial sectors, and the
+// common tokens in a few CTAs.  The list spread over a cluster through its shared
+// memory, 82, 38 and 6.8 us; through global memory, a third kernel, 61, 45 and
+// 14 us.
+//
+// In place, only forbidden and listed ids are written.
 #include <algorithm>
+#include <climits>
 #include <math.h>
+
+#include <type_traits>
 
 #include "rx_common.cuh"
 
@@ -28,10 +44,12 @@ namespace {
 using bf16 = __nv_bfloat16;
 
 constexpr int kThreads = 512;
-constexpr int kUnroll = 4;                  // groups of four ids a thread has in flight
+constexpr int kVecs = 4;                    // groups of four ids of a thread
+constexpr int kTile = kThreads * kVecs * 4; // ids of a CTA, at most
 constexpr uint32_t kPrompt = 0x80000000u;   // the id is in the prompt
 constexpr uint32_t kBias = 0x40000000u;     // the id has a bias
-constexpr uint32_t kCount = 0x3FFFFFFFu;
+constexpr uint32_t kDraft = 0x20000000u;    // the id is a drafted token
+constexpr uint32_t kCount = 0x1FFFFFFFu;
 constexpr int kMaxPath = 1024;              // drafted tokens of one request
 
 struct LParams {
@@ -40,199 +58,367 @@ struct LParams {
     int64_t stride;
     float *out;
     int64_t out_stride;
-    int32_t rows, tile, words;
+    int32_t rows, words;
     int32_t *status;
 };
 
-// y of one touched id: c is its table word.
-struct Penalty {
-    float rep, freq, pres;
-    const int32_t *btok;   // the request's biases, nb of them
-    const float *bval;
-    int64_t nb;
+// One request's rules; false where it is flagged (those of its rows that there
+// are then get their mask only).
+struct Request {
+    int row0, tree;          // its rows
+    float rep, freq, pres, inv;   // inv: 1 / rep
+    bool plain_rep;               // rep is in divide's range
+    bool penal;              // any of them does anything
+    int64_t bias0, nbias;
+    int64_t hist0, nhist;
 
-    __device__ float apply(float x, uint32_t c, int id) const
+    __device__ __forceinline__ bool load(const LParams &p, int b)
+    {
+        const rx_logits_rules &r = p.r;
+        int row1 = b + 1;
+        row0 = b;
+        if (r.qo_indptr) {
+            row0 = __ldg(r.qo_indptr + b);
+            row1 = __ldg(r.qo_indptr + b + 1);
+        }
+        rep = r.repetition ? __ldg(r.repetition + b) : 1.f;
+        freq = r.frequency ? __ldg(r.frequency + b) : 0.f;
+        pres = r.presence ? __ldg(r.presence + b) : 0.f;
+        inv = __frcp_rn(rep);
+        plain_rep = rep >= 0x1p-60f && rep <= 0x1p60f;
+        bias0 = r.bias_ptr ? __ldg(r.bias_ptr + b) : 0;
+        nbias = r.bias_ptr ? __ldg(r.bias_ptr + b + 1) - bias0 : 0;
+        hist0 = r.hist ? __ldg(r.hist_ptr + b) : 0;
+        nhist = r.hist ? __ldg(r.hist_ptr + b + 1) - hist0 : 0;
+        penal = rep != 1.f || freq != 0.f || pres != 0.f;
+        tree = row1 - row0;
+        if (row0 >= 0 && tree >= 0 && row1 <= p.rows && nhist <= (int64_t)kCount - kMaxPath &&
+            !(r.draft_tok && (tree > kMaxPath || (r.tree_mask && (int64_t)tree > 32ll * r.tree_words))))
+            return true;
+        if (p.status && threadIdx.x == 0) atomicOr(p.status, RX_DEV_BAD_LEN);
+        row0 = max(row0, 0);
+        tree = max(min(row1, p.rows) - row0, 0);
+        return false;
+    }
+    // y of an id whose word is c, biases apart, from x / repetition
+    __device__ __forceinline__ float penalised(float x, float quotient, uint32_t c) const
     {
         const uint32_t n = c & kCount;
-        if (n || (c & kPrompt)) x = x > 0.f ? __fdiv_rn(x, rep) : __fmul_rn(x, rep);
+        float y = x > 0.f ? quotient : __fmul_rn(x, rep);
+        y = (c & (kPrompt | kCount)) ? y : x;
         // the product is rounded before the difference, as the formula's steps are
-        x = __fsub_rn(x, __fmul_rn(freq, (float)n));
-        if (n) x = __fsub_rn(x, pres);
-        if (c & kBias) {
-            int64_t lo = 0, hi = nb;  // first entry at or above id
-            while (lo < hi) {
-                const int64_t mid = (lo + hi) >> 1;
-                if (__ldg(btok + mid) < id) lo = mid + 1; else hi = mid;
-            }
-            if (lo < nb && __ldg(btok + lo) == id) {
-                float s = __ldg(bval + lo);
-                for (++lo; lo < nb && __ldg(btok + lo) == id; ++lo) s = __fadd_rn(s, __ldg(bval + lo));
-                x = __fadd_rn(x, s);
-            }
-        }
-        return x;
+        const float z = __fsub_rn(__fsub_rn(y, __fmul_rn(freq, (float)n)), pres);
+        return n ? z : y;
+    }
+    // x / rep, correctly rounded, for 2^-60 <= rep <= 2^60 and x <= 0 (any
+    // value: unused) or 2^-40 <= x <= 2^40: with 1 / rep correctly rounded, the
+    // first step is within one place of the quotient and the second rounds it
+    // correctly (Markstein, IBM J. Res. Dev. 34, 1990).  Four multiply-adds for
+    // a quotient, where the general division takes three times as many
+    // instructions.
+    __device__ __forceinline__ float divide(float x) const
+    {
+        float y = __fmul_rn(x, inv);
+        y = __fmaf_rn(__fmaf_rn(-rep, y, x), inv, y);
+        return __fmaf_rn(__fmaf_rn(-rep, y, x), inv, y);
     }
 };
 
-template <bool BF16>
-__device__ __forceinline__ float logit(const void *row, int id)
+// Out of line: hardly ever called.
+__device__ __noinline__ float4 divide_any(float4 x, float rep)
 {
-    if constexpr (BF16) return __bfloat162float(static_cast<const bf16 *>(row)[id]);
-    else return static_cast<const float *>(row)[id];
+    return make_float4(__fdiv_rn(x.x, rep), __fdiv_rn(x.y, rep), __fdiv_rn(x.z, rep), __fdiv_rn(x.w, rep));
 }
 
-template <bool BF16>
-__global__ void __launch_bounds__(kThreads) logits_kernel(const __grid_constant__ LParams p)
+// The sum of the biases of id in an ascending list, in list order.
+__device__ float bias_sum(int id, const int32_t *tok, const float *val, int64_t n)
 {
-    extern __shared__ uint32_t sm[];
-    uint32_t *table = sm;                       // [tile]
-    uint32_t *touched = sm + p.tile;            // a bit for each group of four ids
-    const rx_logits_rules &r = p.r;
-    const int b = blockIdx.y;
-    const int lo = (int)blockIdx.x * p.tile, hi = min(r.vocab, lo + p.tile), n = hi - lo;
-    int row0 = b, row1 = b + 1;
-    if (r.qo_indptr) {
-        row0 = __ldg(r.qo_indptr + b);
-        row1 = __ldg(r.qo_indptr + b + 1);
+    int64_t lo = 0, hi = n;  // first entry at or above id
+    while (lo < hi) {
+        const int64_t mid = (lo + hi) >> 1;
+        if (__ldg(tok + mid) < id) lo = mid + 1; else hi = mid;
     }
-    const int tree = row1 - row0;
-    if (tree == 0) return;
-    if (row0 < 0 || tree < 0 || row1 > p.rows || (r.draft_tok && tree > kMaxPath) ||
-        (r.draft_tok && r.tree_mask && (int64_t)tree > 32ll * r.tree_words)) {
-        if (p.status && threadIdx.x == 0) atomicOr(p.status, RX_DEV_BAD_LEN);
-        return;
-    }
-    if (row0 + (int)blockIdx.z >= row1) return;
+    if (lo >= n || __ldg(tok + lo) != id) return 0.f;
+    float s = __ldg(val + lo);
+    for (++lo; lo < n && __ldg(tok + lo) == id; ++lo) s = __fadd_rn(s, __ldg(val + lo));
+    return s;
+}
 
-    Penalty pen;
-    pen.rep = r.repetition ? __ldg(r.repetition + b) : 1.f;
-    pen.freq = r.frequency ? __ldg(r.frequency + b) : 0.f;
-    pen.pres = r.presence ? __ldg(r.presence + b) : 0.f;
-    const bool penal = pen.rep != 1.f || pen.freq != 0.f || pen.pres != 0.f;
-    const int64_t b0 = r.bias_ptr ? __ldg(r.bias_ptr + b) : 0;
-    pen.nb = r.bias_ptr ? __ldg(r.bias_ptr + b + 1) - b0 : 0;
-    pen.btok = r.bias_tok + b0;
-    pen.bval = r.bias_val + b0;
+// The values of ids id .. id + 3 with their biases added.
+__device__ __noinline__ float4 add_biases(float4 y, uint4 c, int id, const int32_t *tok, const float *val, int64_t n)
+{
+    if (c.x & kBias) y.x = __fadd_rn(y.x, bias_sum(id, tok, val, n));
+    if (c.y & kBias) y.y = __fadd_rn(y.y, bias_sum(id + 1, tok, val, n));
+    if (c.z & kBias) y.z = __fadd_rn(y.z, bias_sum(id + 2, tok, val, n));
+    if (c.w & kBias) y.w = __fadd_rn(y.w, bias_sum(id + 3, tok, val, n));
+    return y;
+}
 
-    for (int i = threadIdx.x; i < p.tile + p.tile / 128; i += kThreads) sm[i] = 0;
-    __syncthreads();
-    auto touch = [&](int t) { atomicOr(touched + (t >> 7), 1u << ((t >> 2) & 31)); };
-    bool bad = false;
-    // an id outside the vocabulary is reported by the CTAs of the first tile
-    auto outside = [&](int t) {
-        if (t >= 0 && t < r.vocab) return false;
-        bad = true;
-        return true;
-    };
-    if (r.hist) {
-        const int64_t h0 = __ldg(r.hist_ptr + b), h1 = __ldg(r.hist_ptr + b + 1);
-        const int64_t hp = h0 + (r.prompt_len ? __ldg(r.prompt_len + b) : 0);
-        if (penal || lo == 0)  // neutral penalties: only the check of the ids
-            for (int64_t i = h0 + threadIdx.x; i < h1; i += kThreads) {
-                const int t = __ldg(r.hist + i);
-                if (outside(t) || !penal || t < lo || t >= hi) continue;
-                if (i < hp) atomicOr(table + (t - lo), kPrompt);
-                else atomicAdd(table + (t - lo), 1u);
-                touch(t - lo);
-            }
-    }
-    for (int64_t i = threadIdx.x; i < pen.nb; i += kThreads) {
-        const int t = __ldg(pen.btok + i);
-        if (i > 0 && __ldg(pen.btok + i - 1) > t) bad = true;
-        if (outside(t) || t < lo || t >= hi) continue;
-        atomicOr(table + (t - lo), kBias);
-        touch(t - lo);
-    }
+// One row's tile: where it is and what its mask is.
+template <bool BF16> struct Row {
+    const unsigned char *in;  // its ids from lo on
+    float *out;
+    const uint32_t *mask;     // the word of id lo (lo is a multiple of 32), or null: all allowed
+    bool none;                // no id allowed
+    bool vec;                 // groups of four ids on 16 bytes (8 of bf16)
 
-    for (int row = row0 + (int)blockIdx.z; row < row1; row += (int)gridDim.z) {
-        // the drafted tokens on the row's path (sign +1: in, -1: out again)
-        auto path = [&](uint32_t add) {
-            if (!r.draft_tok || (!penal && lo != 0)) return;  // neutral penalties: only the check of the ids
-            for (int j = threadIdx.x; j < tree; j += kThreads) {
-                const bool on = r.tree_mask
-                                    ? (__ldg(r.tree_mask + (int64_t)row * r.tree_words + (j >> 5)) >> (j & 31)) & 1u
-                                    : j <= row - row0;
-                if (!on) continue;
-                const int t = __ldg(r.draft_tok + row0 + j);
-                if (outside(t) || !penal || t < lo || t >= hi) continue;
-                atomicAdd(table + (t - lo), add);
-                touch(t - lo);
-            }
-        };
-        path(1u);
-        __syncthreads();
-        const unsigned char *in = static_cast<const unsigned char *>(p.logits) + (int64_t)row * p.stride * (BF16 ? 2 : 4);
-        float *out = p.out + (int64_t)row * p.out_stride;
-        // the row's mask: null allows all; a row that is not there, nothing
-        const uint32_t *allow = nullptr;
-        bool none = false;
-        if (r.allow) {
-            const int a = __ldg(r.allow_row + row);
-            if (a >= 0 && a < r.n_allow) {
-                allow = r.allow + (int64_t)a * p.words;
-            } else if (a != -1) {
+    // a: the row's entry of allow_row
+    __device__ __forceinline__ Row(const LParams &p, int64_t row, int lo, int a)
+    {
+        in = static_cast<const unsigned char *>(p.logits) + (row * p.stride + lo) * (BF16 ? 2 : 4);
+        out = p.out + row * p.out_stride + lo;
+        mask = nullptr;
+        none = false;
+        if (p.r.allow) {
+            if (a >= 0 && a < p.r.n_allow) {
+                mask = p.r.allow + (int64_t)a * p.words + (lo >> 5);
+            } else if (a != -1) {  // a mask row that is not there allows nothing
                 none = true;
                 if (p.status && threadIdx.x == 0) atomicOr(p.status, RX_DEV_BAD_STATE);
             }
         }
-        // groups of four ids; a row that does not start on 16 bytes (8 for
-        // bf16) goes element by element
-        const bool vec = (reinterpret_cast<uintptr_t>(in) & (BF16 ? 7 : 15)) == 0 &&
-                         (reinterpret_cast<uintptr_t>(out) & 15) == 0;
-        const int groups = vec ? n / 4 : 0;
-        for (int g0 = threadIdx.x; g0 < groups; g0 += kThreads * kUnroll) {
-            float4 x[kUnroll];
-            uint32_t ok[kUnroll];
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int g = g0 + u * kThreads;
-                ok[u] = 0u;
-                if (g >= groups) continue;
-                const int id = lo + 4 * g;
-                ok[u] = none ? 0u : allow ? (__ldg(allow + (id >> 5)) >> (id & 31)) & 15u : 15u;
-                if (!ok[u]) continue;
-                if constexpr (BF16) {
-                    const uint2 w = *reinterpret_cast<const uint2 *>(in + 2 * (int64_t)id);
-                    x[u] = make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
-                                       __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u));
-                } else {
-                    x[u] = *reinterpret_cast<const float4 *>(in + 4 * (int64_t)id);
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < kUnroll; ++u) {
-                const int g = g0 + u * kThreads;
-                if (g >= groups) continue;
-                const int id = lo + 4 * g;
-                float y[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-                if (ok[u] && (touched[g >> 5] >> (g & 31)) & 1u) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t c = table[4 * g + k];
-                        if (c) y[k] = pen.apply(y[k], c, id + k);
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (!((ok[u] >> k) & 1u)) y[k] = -INFINITY;
-                *reinterpret_cast<float4 *>(out + id) = make_float4(y[0], y[1], y[2], y[3]);
-            }
-        }
-        for (int i = groups * 4 + (int)threadIdx.x; i < n; i += kThreads) {
-            const int id = lo + i;
-            const bool ok = !none && (!allow || ((__ldg(allow + (id >> 5)) >> (id & 31)) & 1u));
-            float y = -INFINITY;
-            if (ok) {
-                y = logit<BF16>(in, id);
-                const uint32_t c = table[i];
-                if (c) y = pen.apply(y, c, id);
-            }
-            out[id] = y;
-        }
-        __syncthreads();
-        path(0xFFFFFFFFu);
+        vec = (reinterpret_cast<uintptr_t>(in) & (BF16 ? 7 : 15)) == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
     }
-    if (bad && lo == 0 && p.status) atomicOr(p.status, RX_DEV_BAD_TOKEN);
+    // bit k: id i + k is allowed (i a multiple of four, or one id)
+    __device__ __forceinline__ uint32_t allowed(int i) const
+    {
+        if (none) return 0u;
+        return mask ? __ldg(mask + (i >> 5)) >> (i & 31) : 15u;
+    }
+    // plain loads: out may be logits
+    __device__ __forceinline__ float one(int i) const
+    {
+        return BF16 ? __bfloat162float(reinterpret_cast<const bf16 *>(in)[i]) : reinterpret_cast<const float *>(in)[i];
+    }
+};
+
+// Grid: x = tiles, y = requests, z = shares of a request's rows.  IN_PLACE: out
+// is logits.
+template <bool BF16, bool IN_PLACE>
+__global__ void __launch_bounds__(kThreads, 2) logits_kernel(const __grid_constant__ LParams p, int tile, bool touched)
+{
+    extern __shared__ __align__(16) uint32_t table[];                // [tile] words
+    uint8_t *prompt = reinterpret_cast<uint8_t *>(table + tile);    // [tile] the id is in the prompt
+    const rx_logits_rules &r = p.r;
+    const int b = blockIdx.y, lo = (int)blockIdx.x * tile, n = min(r.vocab - lo, tile);
+    Request q;
+    const bool listed = q.load(p, b) && touched;
+
+    // a thread's groups of four are 4 (threadIdx.x + u kThreads) of the tile
+    const int i0 = 4 * threadIdx.x, step = (int)gridDim.z;
+    using Raw = std::conditional_t<BF16, uint2, float4>;
+    Raw x[kVecs];
+    uint32_t m = 0;      // bits 4 u ..: the allowed ids of group u
+    uint32_t hot = 0;    // bit u: group u has an id whose word is not 0
+    auto masks = [&](const Row<BF16> &w) {
+        uint32_t word[kVecs], to = 0;
+#pragma unroll
+        for (int u = 0; u < kVecs; ++u) {
+            const int i = i0 + 4 * kThreads * u;
+            word[u] = i + 4 <= n ? w.allowed(i) & 15u : 0u;
+        }
+#pragma unroll
+        for (int u = 0; u < kVecs; ++u) to |= word[u] << (4 * u);
+        return to;
+    };
+    auto fetch = [&](const Row<BF16> &w, uint32_t to, int u) {
+        to = to >> (4 * u) & 15u;
+        x[u] = {};
+        if (w.vec && to != 0u && (!IN_PLACE || to != 15u || ((hot >> u) & 1u)))
+            x[u] = *reinterpret_cast<const Raw *>(w.in + (BF16 ? 2 : 4) * (i0 + 4 * kThreads * u));
+    };
+    auto mask_row = [&](int k) { return r.allow && k < q.tree ? __ldg(r.allow_row + q.row0 + k) : -1; };
+    int k = blockIdx.z;
+    if (k >= q.tree) return;
+    Row<BF16> w(p, (int64_t)q.row0 + k, lo, mask_row(k));
+    m = masks(w);
+    if (!IN_PLACE) {
+#pragma unroll
+        for (int u = 0; u < kVecs; ++u) fetch(w, m, u);
+    }
+    int a = mask_row(k + step);  // of the row after this one
+
+    // this thread's drafted tokens (threadIdx.x and the one kThreads behind): their places in the tile
+    static_assert(kMaxPath <= 2 * kThreads, "drafted tokens of a thread");
+    int drafted[2] = {-1, -1};
+    bool paths = false;
+    if (listed) {
+        for (int i = threadIdx.x; i < tile / 4; i += kThreads) reinterpret_cast<uint4 *>(table)[i] = make_uint4(0, 0, 0, 0);
+        for (int i = threadIdx.x; i < tile / 16; i += kThreads) reinterpret_cast<uint4 *>(prompt)[i] = make_uint4(0, 0, 0, 0);
+        __syncthreads();
+        // ids outside the vocabulary are reported by the first tile
+        const bool first = lo == 0 && blockIdx.z == 0;
+        bool bad = false;
+        // f(t) for the tokens [from, to) of the request: single ones up to a
+        // 16-byte boundary, four at a time, the rest
+        auto tokens = [&](int from, int to, auto f) {
+            const int32_t *h = r.hist + q.hist0 + from;
+            const int len = to - from;
+            if (len <= 0) return;
+            const int head = min(len, (int)((16 - (reinterpret_cast<uintptr_t>(h) & 15)) >> 2 & 3)), n4 = (len - head) / 4;
+            const int4 *h4 = reinterpret_cast<const int4 *>(h + head);
+            constexpr int U = 4;
+            int i = threadIdx.x;
+            for (; i + (U - 1) * kThreads < n4; i += U * kThreads) {
+                int4 t[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u) t[u] = __ldg(h4 + i + u * kThreads);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    f(t[u].x);
+                    f(t[u].y);
+                    f(t[u].z);
+                    f(t[u].w);
+                }
+            }
+            for (; i < n4; i += kThreads) {
+                const int4 t = __ldg(h4 + i);
+                f(t.x);
+                f(t.y);
+                f(t.z);
+                f(t.w);
+            }
+            // at most three before the first four and three behind the last
+            const int at = (int)threadIdx.x < head ? threadIdx.x : 4 * n4 + (int)threadIdx.x;
+            if (threadIdx.x < 8 && at < len) f(__ldg(h + at));
+        };
+        const int len = (int)q.nhist, np = r.prompt_len && r.hist ? min(max(__ldg(r.prompt_len + b), 0), len) : 0;
+        if (first) tokens(0, len, [&](int t) { bad |= (uint32_t)t >= (uint32_t)r.vocab; });
+        if (q.penal) {
+            tokens(0, np, [&](int t) {
+                const uint32_t d = (uint32_t)t - (uint32_t)lo;
+                if (d < (uint32_t)n) prompt[d] = 1;
+            });
+            tokens(np, len, [&](int t) {
+                const uint32_t d = (uint32_t)t - (uint32_t)lo;
+                if (d < (uint32_t)n) atomicAdd(table + d, 1u);
+            });
+        }
+        auto mark = [&](int t, uint32_t bit) {
+            const uint32_t d = (uint32_t)t - (uint32_t)lo;
+            if (d < (uint32_t)n) atomicOr(table + d, bit);
+            bad |= (uint32_t)t >= (uint32_t)r.vocab;
+        };
+        for (int64_t i = threadIdx.x; i < q.nbias; i += kThreads) {
+            const int t = __ldg(r.bias_tok + q.bias0 + i);
+            bad |= i > 0 && __ldg(r.bias_tok + q.bias0 + i - 1) > t;
+            mark(t, kBias);
+        }
+        if (r.draft_tok) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int node = (int)threadIdx.x + j * kThreads;
+                if (node >= q.tree) break;
+                const int t = __ldg(r.draft_tok + q.row0 + node);
+                bad |= (uint32_t)t >= (uint32_t)r.vocab;
+                if (q.penal && (uint32_t)t - (uint32_t)lo < (uint32_t)n) {
+                    drafted[j] = t - lo;
+                    atomicOr(table + drafted[j], kDraft);
+                }
+            }
+        }
+        if (bad && first && p.status) atomicOr(p.status, RX_DEV_BAD_TOKEN);
+        // drafted tokens in this tile: the rows' paths count
+        paths = __syncthreads_or(drafted[0] >= 0 || drafted[1] >= 0);
+        uint4 *words = reinterpret_cast<uint4 *>(table);
+#pragma unroll
+        for (int u = 0; u < kVecs; ++u) {
+            const int g = threadIdx.x + kThreads * u;
+            if (4 * g >= tile) break;
+            uint4 v = words[g];
+            const uint32_t seen = reinterpret_cast<const uint32_t *>(prompt)[g];
+            if (seen) {
+                v.x |= seen << 31;
+                v.y |= (seen & 0x100u) << 23;
+                v.z |= (seen & 0x10000u) << 15;
+                v.w |= (seen & 0x1000000u) << 7;
+                words[g] = v;
+            }
+            if (v.x | v.y | v.z | v.w) hot |= 1u << u;
+        }
+        if (paths || !w.vec || (n & 3)) __syncthreads();  // single ids' words are read by other threads
+    }
+    if (IN_PLACE) {
+#pragma unroll
+        for (int u = 0; u < kVecs; ++u) fetch(w, m, u);
+    }
+    // the values of ids i .. i + 3 of the tile with words c
+    auto process = [&](float4 v, uint4 c, int i) {
+        // the quotients' range: of the positive values the largest and the smallest
+        const float top = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
+        const float low = fminf(fminf(v.x > 0.f ? v.x : 1.f, v.y > 0.f ? v.y : 1.f),
+                                fminf(v.z > 0.f ? v.z : 1.f, v.w > 0.f ? v.w : 1.f));
+        float4 d = make_float4(q.divide(v.x), q.divide(v.y), q.divide(v.z), q.divide(v.w));
+        if (!(q.plain_rep && top <= 0x1p40f && low >= 0x1p-40f)) d = divide_any(v, q.rep);
+        v = make_float4(q.penalised(v.x, d.x, c.x), q.penalised(v.y, d.y, c.y), q.penalised(v.z, d.z, c.z),
+                        q.penalised(v.w, d.w, c.w));
+        if ((c.x | c.y | c.z | c.w) & kBias) v = add_biases(v, c, lo + i, r.bias_tok + q.bias0, r.bias_val + q.bias0, q.nbias);
+        return v;
+    };
+    // the drafted tokens on node k's path, counted in (1) or out (-1) of the words
+    auto path = [&](int node, uint32_t by) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int at = (int)threadIdx.x + j * kThreads;
+            if (drafted[j] < 0) continue;
+            const bool on = r.tree_mask ? (__ldg(r.tree_mask + (int64_t)(q.row0 + node) * r.tree_words + (at >> 5)) >> (at & 31)) & 1u
+                                        : at <= node;
+            if (on) atomicAdd(table + drafted[j], by);
+        }
+    };
+    for (;;) {
+        const Row<BF16> now = w;
+        const int node = k;
+        if (paths) {
+            path(node, 1u);
+            __syncthreads();
+        }
+        k += step;
+        const bool more = k < q.tree;
+        uint32_t ahead = 0;
+        if (more) {
+            w = Row<BF16>(p, (int64_t)q.row0 + k, lo, a);
+            a = mask_row(k + step);
+            ahead = masks(w);
+        }
+#pragma unroll
+        for (int u = 0; u < kVecs; ++u) {
+            const int i = i0 + 4 * kThreads * u;
+            float4 v;
+            if constexpr (BF16)
+                v = make_float4(__uint_as_float(x[u].x << 16), __uint_as_float(x[u].x & 0xFFFF0000u),
+                                __uint_as_float(x[u].y << 16), __uint_as_float(x[u].y & 0xFFFF0000u));
+            else
+                v = x[u];
+            const uint32_t mu = m >> (4 * u) & 15u;
+            if (mu != 0u && ((hot >> u) & 1u)) {
+                const uint4 c = reinterpret_cast<const uint4 *>(table)[threadIdx.x + kThreads * u];
+                v = process(v, c, i);
+            }
+            if (now.vec && i + 4 <= n && (!IN_PLACE || mu != 15u || ((hot >> u) & 1u)))
+                *reinterpret_cast<float4 *>(now.out + i) =
+                    make_float4(mu & 1u ? v.x : -INFINITY, mu & 2u ? v.y : -INFINITY, mu & 4u ? v.z : -INFINITY,
+                                mu & 8u ? v.w : -INFINITY);
+            if (more) fetch(w, ahead, u);
+        }
+        m = ahead;
+        // single ids: the rest behind the last four, or the whole of a row that is not aligned
+        for (int i = (now.vec ? n / 4 * 4 : 0) + (int)threadIdx.x; i < n; i += kThreads) {
+            const bool ok = now.allowed(i) & 1u;
+            const uint32_t c = listed ? table[i] : 0u;
+            float y = -INFINITY;
+            if (ok && (!IN_PLACE || c)) {
+                y = now.one(i);
+                if (c) y = process(make_float4(y, 1.f, 1.f, 1.f), make_uint4(c, 0u, 0u, 0u), i).x;
+            }
+            if (!IN_PLACE || c || !ok) now.out[i] = y;
+        }
+        if (paths) {
+            __syncthreads();
+            path(node, ~0u);
+        }
+        if (!more) return;
+    }
 }
 
 int logits_num_sms()
@@ -271,6 +457,7 @@ extern "C" int rx_logits_process(const rx_logits_rules *rules, const void *logit
         (r.allow && (!r.allow_row || r.n_allow < 1)) || (r.draft_tok && !r.qo_indptr) ||
         (r.draft_tok && r.tree_mask && r.tree_words < 1))
         return rx_set_error(RX_ERR_INVALID, "rx_logits_process: a part of the rules is missing");
+    if (r.vocab > (1 << 30)) return rx_set_error(RX_ERR_UNSUPPORTED, "rx_logits_process: vocabulary of %d ids", r.vocab);
     if (r.n_req > 65535) return rx_set_error(RX_ERR_UNSUPPORTED, "rx_logits_process: %d requests (up to 65535)", r.n_req);
     LParams p{};
     p.r = r;
@@ -281,26 +468,20 @@ extern "C" int rx_logits_process(const rx_logits_rules *rules, const void *logit
     p.rows = rows;
     p.words = (r.vocab + 127) / 128 * 4;
     p.status = dev_status;
-    // the largest tile (its list of tokens is read once a tile) that still
-    // gives two CTAs an SM over all requests
-    const int64_t want = 2 * (int64_t)logits_num_sms();
-    int tile = 16384;
-    while (tile > 2048 && (int64_t)((r.vocab + tile - 1) / tile) * r.n_req < want) tile /= 2;
-    p.tile = tile;
-    const int tiles = (r.vocab + tile - 1) / tile;
-    // few requests with several rows each: the rows of one are shared out
-    int64_t slices = 1;
-    if (r.qo_indptr) {
-        const int64_t per = (rows + r.n_req - 1) / r.n_req;
-        slices = std::min<int64_t>(per, (want + (int64_t)tiles * r.n_req - 1) / ((int64_t)tiles * r.n_req));
-        slices = std::max<int64_t>(1, std::min<int64_t>(slices, 65535));
-    }
-    const size_t smem = (size_t)(tile + tile / 128) * sizeof(uint32_t);
-    auto kernel = logits_bf16 ? logits_kernel<true> : logits_kernel<false>;
+    cudaStream_t st = (cudaStream_t)stream;
+    const bool in_place = out == logits, touched = r.hist || r.bias_ptr || r.draft_tok;
+    if (in_place && !touched && !r.allow) return RX_OK;
+    const int tile = kTile;
+    const int64_t tiles = (r.vocab + (int64_t)tile - 1) / tile;
+    // four CTAs an SM (two at a time): with fewer, a request's rows are dealt out
+    // to several, which all count.  16 requests of 8 to 16 rows of 128,256 ids:
+    // 66 us with 1 share, 60 with 2, 62 with 3 and with 4
+    const int64_t shares = std::max<int64_t>(1, std::min<int64_t>(4 * logits_num_sms() / (tiles * r.n_req), rows));
+    const size_t smem = (size_t)tile * (touched ? 5 : 0);
+    auto kernel = in_place ? logits_kernel<false, true> : logits_bf16 ? logits_kernel<true, false> : logits_kernel<false, false>;
     // per device and function; cheap, and right whichever device is current
-    RX_CUDA_CHECK(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)((16384 + 128) * sizeof(uint32_t))));
-    kernel<<<dim3((unsigned)tiles, (unsigned)r.n_req, (unsigned)slices), kThreads, smem, (cudaStream_t)stream>>>(p);
+    RX_CUDA_CHECK(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTile * 5));
+    kernel<<<dim3((unsigned)tiles, (unsigned)r.n_req, (unsigned)shares), kThreads, smem, st>>>(p, tile, touched);
     RX_CUDA_CHECK(cudaGetLastError());
     return RX_OK;
 }
