@@ -47,39 +47,91 @@ struct NormParams {
     void *k_pool;
     void *v_pool;
     int64_t num_slots;
-    float k_scale, v_scale;
+    float k_scale, v_scale, k_inv, v_inv;  // the inverses correctly rounded
     int32_t *status;
     rx::RopeTab tab;
 };
 
-__device__ __forceinline__ void widen(const uint4 &v, float (&x)[8])
+// Two fp32 values in one 64-bit register: this GPU's packed multiply-adds take
+// one instruction for both, each rounded as the plain one.
+struct F2 {
+    uint64_t v;
+    __device__ __forceinline__ F2() {}
+    __device__ __forceinline__ F2(float a, float b) { asm("mov.b64 %0, {%1, %2};\n" : "=l"(v) : "f"(a), "f"(b)); }
+    __device__ __forceinline__ void split(float &a, float &b) const { asm("mov.b64 {%0, %1}, %2;\n" : "=f"(a), "=f"(b) : "l"(v)); }
+};
+
+__device__ __forceinline__ F2 mul(F2 a, F2 b)
+{
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c)
+{
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
+__device__ __forceinline__ void widen(const uint4 &v, F2 (&x)[4])
 {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w[k]));
-        x[2 * k] = f.x;
-        x[2 * k + 1] = f.y;
-    }
+    for (int k = 0; k < 4; ++k) x[k] = F2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
 }
 
-__device__ __forceinline__ uint4 narrow(const float (&x)[8])
+__device__ __forceinline__ uint4 narrow(const F2 (&x)[4])
 {
-    return make_uint4(rx::pack_bf16(x[0], x[1]), rx::pack_bf16(x[2], x[3]), rx::pack_bf16(x[4], x[5]),
-                      rx::pack_bf16(x[6], x[7]));
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        float a, b;
+        x[k].split(a, b);
+        w[k] = rx::pack_bf16(a, b);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
 }
+
+// Out of line: hardly ever called.
+__device__ __noinline__ float divide_any(float x, float y) { return __fdiv_rn(x, y); }
 
 // Eight fp32 values as E4M3 codes of value / scale: a correctly rounded
 // division, then the nearest code, magnitudes past 448 saturated.
-__device__ __forceinline__ uint2 codes(const float (&x)[8], float scale)
+//
+// plain: 2^-60 <= scale <= 2^60 and no magnitude above 2^40.  Then with inv,
+// 1 / scale correctly rounded, the first step's quotient is within one place
+// and the second rounds it correctly (Markstein, IBM J. Res. Dev. 34, 1990):
+// nothing overflows, and what underflows is far below the least code.
+__device__ __forceinline__ uint2 codes(F2 (&x)[4], float scale, float inv, bool plain)
 {
+    const F2 s(scale, scale), i(inv, inv), minus(-1.f, -1.f), ni(-inv, -inv);
     uint16_t pair[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        const float lo = __fdiv_rn(x[2 * k], scale), hi = __fdiv_rn(x[2 * k + 1], scale);
+        float lo, hi;
+        if (plain) {
+            const F2 nx = mul(x[k], minus);
+            F2 y = mul(x[k], i);
+            y = fma(fma(y, s, nx), ni, y);
+            y = fma(fma(y, s, nx), ni, y);
+            y.split(lo, hi);
+        } else {
+            x[k].split(lo, hi);
+            lo = divide_any(lo, scale);
+            hi = divide_any(hi, scale);
+        }
         asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(pair[k]) : "f"(hi), "f"(lo));
     }
     return make_uint2((uint32_t)pair[0] | ((uint32_t)pair[1] << 16), (uint32_t)pair[2] | ((uint32_t)pair[3] << 16));
+}
+
+// 1 / sqrt(v): the hardware's approximation and a Newton step.
+__device__ __forceinline__ float inverse_root(float v)
+{
+    const float r = rsqrtf(v);
+    return r > 0.f && r < INFINITY ? r * fmaf(-0.5f * v * r, r, 1.5f) : r;
 }
 
 template <int D, bool F8>
@@ -89,106 +141,122 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_store_kernel(const __gr
     constexpr int RPP = kThreads / LPR;     // heads of one pass of the CTA
     constexpr int HALF = D / 2;
     using Chunk = std::conditional_t<F8, uint2, uint4>;  // 8 values of the pool
-    // pair 2j, 2j + 1 of lane gi: {cos, sin, cos, sin} at [token][j][gi], so
+    // columns 2j, 2j + 1 of lane gi: {cos, cos, sin, sin} at [token][j][gi], and
+    // the weights of q and k, of columns 4j .. 4j + 3 of a lane's two octets, so
     // that the lanes of a head read consecutive 16-byte words
     __shared__ float4 cs[kMaxTok][4][LPR];
+    __shared__ float4 weight[2][2][2][LPR];
     const int gi = threadIdx.x % LPR, sub = threadIdx.x / LPR;
     const int64_t t0 = (int64_t)blockIdx.x * p.tok;
     const int ntok = (int)min((int64_t)p.tok, p.n - t0);
     const int R = p.hq + 2 * p.hkv;
-    const int total = ntok * R;
+    const int step_t = RPP / R, step_h = RPP - step_t * R;  // token and head of the next row of a thread
+    auto advance = [&](int &tt, int &h) {
+        tt += step_t;
+        h += step_h;
+        if (h >= R) {
+            h -= R;
+            ++tt;
+        }
+    };
 
     uint4 lo[kUnroll], hi[kUnroll];
-    auto load = [&](int base) {
+    int lt = sub / R, lh = sub - lt * R;  // of the next row to load
+    auto load = [&]() {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const int idx = base + u * RPP + sub;
             lo[u] = hi[u] = make_uint4(0, 0, 0, 0);
-            if (idx < total) {
-                const int tt = idx / R, h = idx - tt * R;
-                const bf16 *src = h < p.hq            ? p.q + (t0 + tt) * p.q_stride + (int64_t)h * D
-                                  : h < p.hq + p.hkv ? p.k_new + (t0 + tt) * p.kv_stride + (int64_t)(h - p.hq) * D
-                                                     : p.v_new + (t0 + tt) * p.kv_stride +
-                                                           (int64_t)(h - p.hq - p.hkv) * D;
+            if (lt < ntok) {
+                const bf16 *src = lh < p.hq            ? p.q + (t0 + lt) * p.q_stride + lh * D
+                                  : lh < p.hq + p.hkv ? p.k_new + (t0 + lt) * p.kv_stride + (lh - p.hq) * D
+                                                      : p.v_new + (t0 + lt) * p.kv_stride + (lh - p.hq - p.hkv) * D;
                 // plain loads: q_out may be q
                 lo[u] = *reinterpret_cast<const uint4 *>(src + gi * 8);
                 hi[u] = *reinterpret_cast<const uint4 *>(src + HALF + gi * 8);
             }
+            advance(lt, lh);
         }
     };
-    load(0);
+    int tt = lt, h = lh;  // of the next row to work off
+    load();
 
     for (int i = threadIdx.x; i < ntok * HALF; i += kThreads) {
-        const int tt = i / HALF, c = i % HALF;
-        const int32_t pos = __ldg(p.pos + t0 + tt);
+        const int t = i / HALF, c = i % HALF;
+        const int32_t pos = __ldg(p.pos + t0 + t);
         const uint32_t up = pos < 0 ? 0u - (uint32_t)pos : (uint32_t)pos;
         float sn, cn;
-        rx::sincos_at(p.tab, up, c, sn, cn);
-        float *dst = reinterpret_cast<float *>(&cs[tt][(c % 8) / 2][c / 8]) + 2 * (c % 2);
+        rx::sincos_exact(p.tab, up, c, sn, cn);
+        float *dst = reinterpret_cast<float *>(&cs[t][(c % 8) / 2][c / 8]) + c % 2;
         dst[0] = cn;
-        dst[1] = pos < 0 ? -sn : sn;
+        dst[2] = pos < 0 ? -sn : sn;
     }
-    __syncthreads();
+    bool small = true;
+    if (threadIdx.x < 2 * D) {
+        const int c = threadIdx.x % D;
+        const bf16 *w = threadIdx.x < D ? p.qw : p.kw;
+        const float f = w ? __bfloat162float(w[c]) : 1.f;
+        small = fabsf(f) <= 0x1p30f;
+        reinterpret_cast<float *>(&weight[threadIdx.x / D][c / HALF][c % 8 / 4][c % HALF / 8])[c % 4] = f;
+    }
+    // a normalised value is at most sqrt(D), a rotated one sqrt(2) times that:
+    // below 2^40 with weights up to 2^30
+    small = __syncthreads_and(small);
 
-    for (int base = 0; base < total; base += RPP * kUnroll) {
-        if (base > 0) load(base);
+    for (int left = ntok * R; left > 0; left -= RPP * kUnroll) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const int idx = base + u * RPP + sub;
-            const bool in = idx < total;
-            const int tt = in ? idx / R : 0, h = in ? idx - tt * R : 0;
-            float a[8], b[8];
+            F2 a[4], b[4];
             widen(lo[u], a);
             widen(hi[u], b);
-            float ss = 0.f;
+            F2 sq(0.f, 0.f);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) ss = fmaf(a[k], a[k], fmaf(b[k], b[k], ss));
+            for (int k = 0; k < 4; ++k) sq = fma(a[k], a[k], fma(b[k], b[k], sq));
+            float ss, odd;
+            sq.split(ss, odd);
+            ss += odd;
 #pragma unroll
             for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            if (!in) continue;
-            const bool is_q = h < p.hq, is_v = h >= p.hq + p.hkv;
+            const int t = tt, hh = h;
+            advance(tt, h);
+            if (t >= ntok) continue;
+            const bool is_q = hh < p.hq, is_v = hh >= p.hq + p.hkv;
             if (!is_v) {
-                const float r = 1.f / sqrtf(ss * (1.f / D) + p.eps);
-                const bf16 *w = is_q ? p.qw : p.kw;
-                float wa[8], wb[8];
-#pragma unroll
-                for (int k = 0; k < 8; ++k) wa[k] = wb[k] = 1.f;
-                if (w) {
-                    widen(__ldg(reinterpret_cast<const uint4 *>(w + gi * 8)), wa);
-                    widen(__ldg(reinterpret_cast<const uint4 *>(w + HALF + gi * 8)), wb);
-                }
+                const float r = inverse_root(ss * (1.f / D) + p.eps);
+                const F2 rr(r, r), minus(-1.f, -1.f);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float4 q = cs[tt][j][gi];
-                    const float a0 = a[2 * j] * r * wa[2 * j], b0 = b[2 * j] * r * wb[2 * j];
-                    const float a1 = a[2 * j + 1] * r * wa[2 * j + 1], b1 = b[2 * j + 1] * r * wb[2 * j + 1];
-                    a[2 * j] = a0 * q.x - b0 * q.y;
-                    b[2 * j] = b0 * q.x + a0 * q.y;
-                    a[2 * j + 1] = a1 * q.z - b1 * q.w;
-                    b[2 * j + 1] = b1 * q.z + a1 * q.w;
+                    const float4 q = cs[t][j][gi], wa = weight[is_q ? 0 : 1][0][j / 2][gi], wb = weight[is_q ? 0 : 1][1][j / 2][gi];
+                    const F2 c(q.x, q.y), s(q.z, q.w);
+                    const F2 x = mul(mul(a[j], rr), j % 2 ? F2(wa.z, wa.w) : F2(wa.x, wa.y));
+                    const F2 y = mul(mul(b[j], rr), j % 2 ? F2(wb.z, wb.w) : F2(wb.x, wb.y));
+                    a[j] = fma(x, c, mul(mul(y, s), minus));
+                    b[j] = fma(y, c, mul(x, s));
                 }
             }
             if (is_q) {
-                bf16 *dst = p.q_out + ((t0 + tt) * p.hq + h) * D;
+                bf16 *dst = p.q_out + ((t0 + t) * p.hq + hh) * D;
                 *reinterpret_cast<uint4 *>(dst + gi * 8) = narrow(a);
                 *reinterpret_cast<uint4 *>(dst + HALF + gi * 8) = narrow(b);
                 continue;
             }
-            const int32_t s = __ldg(p.slots + t0 + tt);
-            if (s < 0 || (int64_t)s >= p.num_slots) {
-                if (p.status && h == p.hq && gi == 0) atomicOr(p.status, RX_DEV_BAD_SLOT);
+            const int32_t slot = __ldg(p.slots + t0 + t);
+            if (slot < 0 || (int64_t)slot >= p.num_slots) {
+                if (p.status && hh == p.hq && gi == 0) atomicOr(p.status, RX_DEV_BAD_SLOT);
                 continue;
             }
-            const int g = h - p.hq - (is_v ? p.hkv : 0);
-            Chunk *dst = static_cast<Chunk *>(is_v ? p.v_pool : p.k_pool) + ((int64_t)s * p.hkv + g) * (D / 8);
+            const int g = hh - p.hq - (is_v ? p.hkv : 0);
+            Chunk *dst = static_cast<Chunk *>(is_v ? p.v_pool : p.k_pool) + ((int64_t)slot * p.hkv + g) * (D / 8);
             if constexpr (F8) {
-                dst[gi] = codes(a, is_v ? p.v_scale : p.k_scale);
-                dst[LPR + gi] = codes(b, is_v ? p.v_scale : p.k_scale);
+                const float scale = is_v ? p.v_scale : p.k_scale, inv = is_v ? p.v_inv : p.k_inv;
+                const bool plain = scale >= 0x1p-60f && scale <= 0x1p60f && (is_v ? ss <= 0x1p80f : small);
+                dst[gi] = codes(a, scale, inv, plain);
+                dst[LPR + gi] = codes(b, scale, inv, plain);
             } else {
                 dst[gi] = is_v ? lo[u] : narrow(a);
                 dst[LPR + gi] = is_v ? hi[u] : narrow(b);
             }
         }
+        if (left > RPP * kUnroll) load();
     }
 }
 
@@ -254,6 +322,8 @@ int norm_call(const char *who, const Pool &pool, const void *q, int64_t q_stride
     p.num_slots = pool.num_slots;
     p.k_scale = pool.k_scale;
     p.v_scale = pool.v_scale;
+    p.k_inv = 1.f / pool.k_scale;
+    p.v_inv = 1.f / pool.v_scale;
     p.status = dev_status;
     p.tab = tab;
     // tokens of a CTA: enough for kUnroll rows a thread, fewer while that

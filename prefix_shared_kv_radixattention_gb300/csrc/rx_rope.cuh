@@ -40,6 +40,31 @@ __device__ __forceinline__ void sincos_at(const RopeTab &tab, uint32_t up, int c
     sincosf(ar, &sn, &cs);
 }
 
+// The same, reduced to an eighth of a turn in the integers, so that the angle
+// keeps all its fp32 digits (sincos_at's has up to 2^-23 of absolute error near
+// half a turn), then by the Taylor series: on [-pi/4, pi/4] the first term left
+// out is below 2^-29.
+__device__ __forceinline__ void sincos_exact(const RopeTab &tab, uint32_t up, int c, float &sn, float &cs)
+{
+    constexpr float kTurn = 1.4629180792671596e-9f;  // 2 pi / 2^32
+    const uint32_t t = __umulhi(up, tab.f_lo[c]) + up * tab.f_hi[c];
+    const uint32_t quarter = (t + 0x20000000u) >> 30;  // nearest quarter turn
+    const float x = (float)(int32_t)(t - (quarter << 30)) * kTurn, x2 = x * x;
+    float s = fmaf(x2, 1.f / 362880.f, -1.f / 5040.f);
+    s = fmaf(x2, s, 1.f / 120.f);
+    s = fmaf(x2, s, -1.f / 6.f);
+    s = fmaf(x * x2, s, x);
+    float k = fmaf(x2, -1.f / 3628800.f, 1.f / 40320.f);
+    k = fmaf(x2, k, -1.f / 720.f);
+    k = fmaf(x2, k, 1.f / 24.f);
+    k = fmaf(x2, k, -.5f);
+    k = fmaf(x2, k, 1.f);
+    // a quarter turn: (cos, sin) -> (-sin, cos)
+    const float a = quarter & 1u ? k : s, b = quarter & 1u ? s : k;
+    sn = quarter & 2u ? -a : a;
+    cs = (quarter + 1u) & 2u ? -b : b;
+}
+
 __device__ __forceinline__ Rot8 angles(const RopeTab &tab, int32_t pos, int c0)
 {
     // |p|, and the sine's sign: a rotation by -a is the one by a with sin negated
