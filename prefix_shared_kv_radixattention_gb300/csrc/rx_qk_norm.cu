@@ -17,6 +17,16 @@
 // CTA takes `tok` tokens; their angles are formed once, one sine and cosine
 // a thread, into shared memory (a head's own lanes forming them would
 // compute each for every head), while the first rows are in flight.
+//
+// Bound by memory where the batch is long: 16,384 tokens of 64 q and 8 kv
+// heads of 128, 671 MB, take 105 us (6.4 TB/s), 4,099 of 32/8 into an FP8
+// pool 22 us (92 MB in less than two waves of CTAs).  It was bound by
+// instructions before that: 397 a row of a warp, of which the general
+// division, sincosf and the unpacked arithmetic were two thirds.  Two rows a
+// thread in flight at four CTAs an SM; four rows and two CTAs take 115 and
+// 28 us, one row and four 117 and 23.  Rows that do not fill a CTA's passes
+// (two tokens of 80 rows on passes of 128) took 156 us.
+#include <numeric>
 #include <type_traits>
 
 #include "rx_common.cuh"
@@ -28,7 +38,7 @@ using bf16 = __nv_bfloat16;
 
 constexpr int kThreads = 256;
 constexpr int kMaxTok = 16;   // tokens of one CTA
-constexpr int kUnroll = 4;    // rows a thread has in flight
+constexpr int kUnroll = 2;    // rows a thread has in flight
 
 struct NormParams {
     const bf16 *q;
@@ -135,7 +145,7 @@ __device__ __forceinline__ float inverse_root(float v)
 }
 
 template <int D, bool F8>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_store_kernel(const __grid_constant__ NormParams p)
+__global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_store_kernel(const __grid_constant__ NormParams p)
 {
     constexpr int LPR = D / 16;             // lanes of one head
     constexpr int RPP = kThreads / LPR;     // heads of one pass of the CTA
@@ -326,12 +336,12 @@ int norm_call(const char *who, const Pool &pool, const void *q, int64_t q_stride
     p.v_inv = 1.f / pool.v_scale;
     p.status = dev_status;
     p.tab = tab;
-    // tokens of a CTA: enough for kUnroll rows a thread, fewer while that
-    // would leave less than two CTAs an SM
-    const int R = hq + 2 * pool.hkv, rpp = kThreads / (pool.D / 16);
-    int64_t tok = (kUnroll * rpp + R - 1) / R;
+    // tokens of a CTA: rows that fill its passes, fewer while that would leave
+    // less than four CTAs an SM
+    const int R = hq + 2 * pool.hkv, pass = kUnroll * kThreads / (pool.D / 16);
+    int64_t tok = pass / std::gcd(R, pass);
     if (tok > kMaxTok) tok = kMaxTok;
-    if (tok > n / 304) tok = n / 304;
+    if (tok > n / 608) tok = n / 608;
     if (tok < 1) tok = 1;
     p.tok = (int)tok;
     const int64_t grid = (n + tok - 1) / tok;
