@@ -137,11 +137,14 @@ __device__ __forceinline__ uint2 codes(F2 (&x)[4], float scale, float inv, bool 
     return make_uint2((uint32_t)pair[0] | ((uint32_t)pair[1] << 16), (uint32_t)pair[2] | ((uint32_t)pair[3] << 16));
 }
 
-// 1 / sqrt(v): the hardware's approximation and a Newton step.
+// 1 / sqrt(v): the hardware's approximation and a Newton step, whose v r^2 is
+// held to more than 32 bits.
 __device__ __forceinline__ float inverse_root(float v)
 {
     const float r = rsqrtf(v);
-    return r > 0.f && r < INFINITY ? r * fmaf(-0.5f * v * r, r, 1.5f) : r;
+    if (!(r > 0.f && r < INFINITY)) return r;
+    const float p = __fmul_rn(v, r), low = __fmaf_rn(v, r, -p);
+    return fmaf(.5f * r, fmaf(-low, r, __fmaf_rn(-p, r, 1.f)), r);
 }
 
 template <int D, bool F8>

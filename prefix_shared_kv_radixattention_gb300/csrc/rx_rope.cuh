@@ -40,25 +40,31 @@ __device__ __forceinline__ void sincos_at(const RopeTab &tab, uint32_t up, int c
     sincosf(ar, &sn, &cs);
 }
 
-// The same, reduced to an eighth of a turn in the integers, so that the angle
-// keeps all its fp32 digits (sincos_at's has up to 2^-23 of absolute error near
-// half a turn), then by the Taylor series: on [-pi/4, pi/4] the first term left
-// out is below 2^-29.
+// The same to about half a place of the result: reduced to an eighth of a turn
+// in the integers, the angle held as the sum of two fp32 values (sincos_at's
+// has up to 2^-23 of absolute error near half a turn), then by the Taylor
+// series: on [-pi/4, pi/4] the first term left out is below 2^-29.
 __device__ __forceinline__ void sincos_exact(const RopeTab &tab, uint32_t up, int c, float &sn, float &cs)
 {
-    constexpr float kTurn = 1.4629180792671596e-9f;  // 2 pi / 2^32
+    constexpr float kTurn = 1.4629180792671596e-9f;  // 2 pi / 2^32, and what its rounding left
+    constexpr float kTurnLow = (float)(1.4629180792671596e-9 - (double)1.4629180792671596e-9f);
     const uint32_t t = __umulhi(up, tab.f_lo[c]) + up * tab.f_hi[c];
     const uint32_t quarter = (t + 0x20000000u) >> 30;  // nearest quarter turn
-    const float x = (float)(int32_t)(t - (quarter << 30)) * kTurn, x2 = x * x;
+    const int32_t rest = (int32_t)(t - (quarter << 30));
+    const float top = (float)rest, low = (float)(rest - (int32_t)top);
+    const float x = __fmul_rn(top, kTurn);
+    const float e = fmaf(low, kTurn, fmaf(top, kTurnLow, fmaf(top, kTurn, -x)));  // the angle is x + e
+    const float x2 = x * x;
     float s = fmaf(x2, 1.f / 362880.f, -1.f / 5040.f);
     s = fmaf(x2, s, 1.f / 120.f);
     s = fmaf(x2, s, -1.f / 6.f);
-    s = fmaf(x * x2, s, x);
+    s = x + fmaf(x * x2, s, fmaf(-.5f * x2, e, e));
     float k = fmaf(x2, -1.f / 3628800.f, 1.f / 40320.f);
     k = fmaf(x2, k, -1.f / 720.f);
     k = fmaf(x2, k, 1.f / 24.f);
-    k = fmaf(x2, k, -.5f);
-    k = fmaf(x2, k, 1.f);
+    // 1 - x^2 / 2 and what its rounding left
+    const float h = fmaf(-.5f, x2, 1.f), left = fmaf(-.5f, x2, 1.f - h);
+    k = h + fmaf(x2 * x2, k, fmaf(-x, e, left));
     // a quarter turn: (cos, sin) -> (-sin, cos)
     const float a = quarter & 1u ? k : s, b = quarter & 1u ? s : k;
     sn = quarter & 2u ? -a : a;
