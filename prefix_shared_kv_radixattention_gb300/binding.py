@@ -368,9 +368,15 @@ def rx_schedule(tree: RadixTree, requests: Sequence[Sequence[int]], policy: int)
 # ---------------------------------------------------------------------------
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dev(t, dtype, name):
@@ -387,13 +393,16 @@ def _dev(t, dtype, name):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
-    torch = _torch()
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    # the current stream's handle without the Python object around it, which
+    # takes 3 us to make: a sixth of a call on a small batch
+    c = _torch()._C
+    return c._cuda_getCurrentRawStream(c._cuda_getDevice())
 
 
 def _pool_dims(k_pool, v_pool, layer: int):
@@ -786,10 +795,12 @@ def _head_rows(t, name):
         raise TypeError(f"{name}: expected a CUDA tensor")
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name}: expected {torch.bfloat16}, got {t.dtype}")
-    n, h, d = t.shape if t.dim() == 3 else (0, 0, 0)
-    if t.dim() != 3 or (n and ((d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d))):
+    if t.dim() != 3:
         raise ValueError(f"{name}: must be [n, heads, head_dim] with contiguous rows")
-    return t.stride(0) if n > 1 else h * d
+    (n, h, d), (row, head, one) = t.shape, t.stride()
+    if n and ((d > 1 and one != 1) or (h > 1 and head != d)):
+        raise ValueError(f"{name}: must be [n, heads, head_dim] with contiguous rows")
+    return row if n > 1 else h * d
 
 
 def _norm_args(k_pool, v_pool, q, q_out, k_new, v_new, q_weight, k_weight, slots, pos, dev_status):
