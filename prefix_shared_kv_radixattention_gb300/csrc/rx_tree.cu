@@ -156,6 +156,7 @@ struct TParams {
     float v_scale;      // V's scale for an FP8 pool; 1 otherwise
     float *part_o;      // [2 kCtas][128 nt][D] partial results, normalised
     float *part_l;      // [2 kCtas][128 nt] their log2-sum-exps
+    struct Cut *cuts;   // [kCtas] what the merge has to do
     int32_t *status;
 };
 
@@ -195,6 +196,16 @@ __device__ __forceinline__ Req load_req(const TParams &p, int b, bool flag = fal
 // A place in the list, and how many units of it from there on.
 struct Start {
     int g, b, qt, j, left;
+    int64_t total;  // units of the list
+};
+
+// The (kv head g, request, row tiles) that the end of a CTA's share cuts, when
+// it also begins in that share: its parts are the CTA's last segment (slot 1)
+// and the first segments (slot 0) of the CTAs after it.
+struct __align__(16) Cut {
+    int parts;      // 0: there is none
+    int g;
+    int tok, ntok;  // first query row, drafted tokens
 };
 
 // Exclusive prefix sums of the requests' units, `per` requests a thread, into
@@ -235,6 +246,7 @@ __device__ Start locate(const TParams &p, const int64_t *pre, int per, int64_t p
 {
     Start c;
     c.left = 0;
+    c.total = per_head * p.hkv;
     c.g = (int)(u / per_head);
     int64_t x = u - c.g * per_head;
     int lo = 0, hi = THREADS - 1;  // the thread whose requests hold unit x
@@ -276,6 +288,7 @@ __device__ void scheduler(const TParams &p, unsigned char *smem, uint32_t sbase)
         if (base + lane < p.batch) mine = load_req(p, base + lane);
     };
     fill();
+    Cut cut{0, 0, 0, 0};
     for (int s = 0;; ++s) {
         const int slot = s % kSegs, l = c.b - base;
         if (s >= kSegs && !warp_wait(bar + 8 * (L::B_SEGEMPTY + slot), (s / kSegs - 1) & 1, abort_flag, p.status)) break;
@@ -306,7 +319,19 @@ __device__ void scheduler(const TParams &p, unsigned char *smem, uint32_t sbase)
         rx::cp_async_mbar_arrive(bar + 8 * (L::B_SEGFULL + slot));  // the words, as they land
         __syncwarp();
         if (lane == 0) rx::mbar_arrive(bar + 8 * (L::B_SEGFULL + slot));  // the segment
-        if (g.last) break;
+        if (g.last) {
+            if (g.j0 == 0 && g.j1 < ntiles) {
+                const int ctas = (int)min((int64_t)gridDim.x, c.total), x = (int)blockIdx.x;
+                const int64_t end = first_unit(c.total, ctas, x + 1) + (ntiles - g.j1);
+                cut = Cut{2, g.g, g.tok, g.ntok};
+                for (int n = 32; n == 32;) {  // the CTAs behind the next whose share begins inside
+                    const int y = x + cut.parts + lane;
+                    n = __popc(__ballot_sync(0xffffffffu, y < ctas && first_unit(c.total, ctas, y) < end));
+                    cut.parts += n;
+                }
+            }
+            break;
+        }
         c.j = 0;
         if (++c.qt < nqt) continue;
         c.qt = 0;
@@ -327,6 +352,7 @@ __device__ void scheduler(const TParams &p, unsigned char *smem, uint32_t sbase)
         } while (!next);
         c.b = base + __ffs(next) - 1;
     }
+    if (lane == 0) p.cuts[blockIdx.x] = cut;
     rx::cp_async_wait_all();
 }
 
@@ -1075,9 +1101,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
     const int64_t per_head = scan_units<kThreads>(p, pre, per, blockIdx.x == 0);
     const int64_t total = per_head * p.hkv;
     const int ctas = (int)min((int64_t)gridDim.x, total);
-    if ((int)blockIdx.x >= ctas) return;
-    if (total / ctas >= INT_MAX) {  // lengths of no real pool
-        if (p.status && threadIdx.x == 0) atomicOr(p.status, RX_DEV_BAD_LEN);
+    if ((int)blockIdx.x >= ctas || total / ctas >= INT_MAX) {  // nothing to do, or lengths of no real pool
+        if (threadIdx.x == 0) {
+            p.cuts[blockIdx.x] = Cut{0, 0, 0, 0};
+            if (ctas > 0 && total / ctas >= INT_MAX && p.status) atomicOr(p.status, RX_DEV_BAD_LEN);
+        }
         return;
     }
     static_assert(sizeof(Start) <= 32, "the start's room");
@@ -1126,37 +1154,26 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
 // joining the partial results
 // ---------------------------------------------------------------------------
 
-// The (kv head, request, row tiles) that the boundary between CTAs x and x + 1
-// cuts, x = blockIdx.x, when it is the first boundary inside: its parts are
-// CTA x's last segment (slot 1) and the first segments (slot 0) of the CTAs
-// after it, as far as it reaches.  One warp a row: with m the largest
+// The parts of cut x = blockIdx.x, one warp a row: with m the largest
 // log2-sum-exp, w = 2^(l - m): o = sum w o / sum w.  kMergeRows rows a CTA.
+// Finding the cuts here, by a scan of the lengths in every CTA, took longer than
+// joining them: 5 us more for eight trees of 64 tokens, 2.5 of 18.7 for one of 5.
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ TParams p, int main_ctas)
+__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ TParams p)
 {
-    __shared__ int64_t pre[kMergeThreads + 1];
-    const int per = (p.batch + kMergeThreads - 1) / kMergeThreads;
-    const int64_t per_head = scan_units<kMergeThreads>(p, pre, per, false);
-    const int64_t total = per_head * p.hkv;
-    const int ctas = (int)min((int64_t)main_ctas, total);
     const int x0 = (int)blockIdx.x;
-    rx::pdl_wait();  // the partial results are written by the kernel before this one
-    if (x0 + 1 >= ctas || total / ctas >= INT_MAX) return;
-    const int64_t cut = first_unit(total, ctas, x0 + 1);
-    Req req;
-    const Start c = locate<kMergeThreads>(p, pre, per, per_head, cut, req);
-    const int64_t begin = cut - c.j, end = begin + req.ntiles;
-    if (c.j == 0 || begin < first_unit(total, ctas, x0)) return;
-    int parts = 2;
-    while (x0 + parts < ctas && first_unit(total, ctas, x0 + parts) < end) ++parts;
+    rx::pdl_wait();  // the cuts and the partial results are written by the kernel before this one
+    const int4 raw = __ldcg(reinterpret_cast<const int4 *>(p.cuts + x0));
+    const Cut c{raw.x, raw.y, raw.z, raw.w};
+    const int parts = c.parts;
+    if (parts == 0) return;
 
     constexpr int V = D / 32;  // values of a lane
     const int lane = threadIdx.x & 31;
-    const int node = c.qt * p.tb * p.nt, ntok = min(p.tb * p.nt, req.T - node);
     for (int i = threadIdx.x >> 5; i < kMergeRows; i += kMergeThreads / 32) {
         const int row = (int)blockIdx.y * kMergeRows + i;      // of the group's nt * 128
         const int t = row / kRows, r = row % kRows;
-        if (t >= p.nt || r >= min(p.tb, ntok - t * p.tb) * p.G) continue;
+        if (t >= p.nt || r >= min(p.tb, c.ntok - t * p.tb) * p.G) continue;
         auto at = [&](int s) { return (int64_t)(2 * (x0 + s) + (s == 0 ? 1 : 0)) * p.nt * kRows + row; };
         float m = -INFINITY;
         for (int s = lane; s < parts; s += 32) m = fmaxf(m, __ldcg(p.part_l + at(s)));
@@ -1182,7 +1199,7 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
             }
         }
         const float inv = tot == 0.f ? 0.f : 1.f / tot;
-        const int64_t orow = ((int64_t)req.tok + node + t * p.tb + r / p.G) * p.hq + (int64_t)c.g * p.G + r % p.G;
+        const int64_t orow = ((int64_t)c.tok + t * p.tb + r / p.G) * p.hq + (int64_t)c.g * p.G + r % p.G;
         uint32_t *dst = reinterpret_cast<uint32_t *>(p.o + orow * D + lane * V);
         dst[0] = rx::pack_bf16(acc[0] * inv, acc[1] * inv);
         if constexpr (V == 4) dst[1] = rx::pack_bf16(acc[2] * inv, acc[3] * inv);
@@ -1218,7 +1235,7 @@ int launch(const TParams &p, cudaStream_t st)
     RX_CUDA_CHECK(cudaFuncSetAttribute(tree_kernel<D, F8, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (TL<D, F8>::BYTES)));
     tree_kernel<D, F8, NT><<<kCtas, kThreads, (TL<D, F8>::BYTES), st>>>(p);
     RX_CUDA_CHECK(cudaGetLastError());
-    // a programmatic dependent: it finds its part of the work, then waits on the device
+    // a programmatic dependent: it is launched meanwhile and waits on the device
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(kCtas - 1, (unsigned)(p.nt == 1 ? (std::min(p.max_tree, p.tb) * p.G + kMergeRows - 1) / kMergeRows : p.nt * kRows / kMergeRows));
     cfg.blockDim = dim3(kMergeThreads);
@@ -1228,7 +1245,7 @@ int launch(const TParams &p, cudaStream_t st)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    RX_CUDA_CHECK(cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, p, (int)kCtas));
+    RX_CUDA_CHECK(cudaLaunchKernelEx(&cfg, tree_merge_kernel<D>, p));
     return RX_OK;
 }
 
@@ -1284,6 +1301,7 @@ int tree_call(const char *who, const TreePool &pool, const void *q, void *o, flo
     p.status = dev_status;
     p.part_o = (float *)workspace;
     p.part_l = (float *)((char *)workspace + part_bytes(p.nt, pool.D));
+    p.cuts = (Cut *)(p.part_l + (size_t)2 * kCtas * p.nt * kRows);
     cudaStream_t st = (cudaStream_t)stream;
     if (pool.D == 128)
         return pool.f8 ? launch<128, true>(p, st) : p.nt == 1 ? launch<128, false>(p, st) : launch<128, false, kMaxNt>(p, st);
@@ -1299,7 +1317,8 @@ extern "C" size_t rx_attn_tree_workspace(int32_t batch, int32_t hq, int32_t hkv,
         return 0;
     }
     const int nt = row_tiles(hq, hkv, max_tree);
-    return part_bytes(nt, head_dim) + (size_t)2 * kCtas * nt * kRows * sizeof(float);
+    return part_bytes(nt, head_dim) + (size_t)2 * kCtas * nt * kRows * sizeof(float) +
+           kCtas * sizeof(Cut);
 }
 
 extern "C" int rx_attn_tree(const rx_kv_pool *pool_in, const void *q, void *o, float *lse, int32_t hq,
