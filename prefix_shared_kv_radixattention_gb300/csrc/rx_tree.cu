@@ -15,25 +15,36 @@
 //   - the rows of one kv head are one tensor-core tile of 128 rows (M), padded
 //     (an unused row costs nothing but its share of the MMA, which has time to
 //     spare), and every K/V tile of 128 positions is read once for all of them;
-//   - K/V rows are gathered through the slot list by eight producer warps with
-//     16-byte loads into registers and stores into the swizzled tile that the
-//     tensor core reads.  Rows of 256 bytes at random slots stream at 6.6 TB/s
-//     this way with 64 KB in flight an SM (2.9 TB/s as bulk copies, 2.8 TB/s
-//     through three warps of cp.async), so no copy of the context is needed
-//     first;
+//   - K/V rows are gathered through the slot list by producer warps in 16-byte
+//     asynchronous copies that land in the swizzled tile that the tensor core
+//     reads (see producer()).  Rows of 256 bytes at random slots stream at 6.7
+//     TB/s this way with 64 KB in flight an SM (2.9 TB/s as bulk copies, 2.8
+//     TB/s through three warps), so no copy of the context is needed first;
 //   - the work is cut evenly: the (kv head, request, row tile, position tile)
 //     units are one long list of which every CTA takes a contiguous share; a
 //     (kv head, request, row tile) cut by a CTA's end leaves fp32 partial
 //     results that a second kernel joins by the log-sum-exp identity.  The
 //     heads are outermost, so with 8 heads on 152 SMs nineteen CTAs walk each
 //     head in step and the rows of one slot are read at about the same time;
-//   - four softmax warps (one row a thread) take the scores S = Q K^T of a tile
+//   - four softmax warps a row tile (one row a thread) take the scores S = Q K^T of a tile
 //     from TMEM into registers at once, which frees S for the next tile's, and
 //     write P to a TMEM buffer of its own, from where O += P V reads it: the
 //     tensor core works on the tiles before and after meanwhile.
 //
 // All lengths are read on the device, by every CTA for itself: a scan of the
 // batch's lengths in shared memory finds its share.
+//
+// Measured, with what is left: 16 requests of up to 32,768 positions, 64/8
+// heads of 128, 234 us, 6.7 TB/s of the rows read (a shared prefix is read once
+// a request; read once in all it would be 164 us); 64 of 1,281, 32/32 heads,
+// 212 us (149 us of bytes; four of a tile's 128 rows are used, and a softmax
+// warp takes 2,300 cycles for a tile however few rows it has); E4M3 pools, 16 of
+// up to 32,768, 32/8 heads, 301 us (119 us of bytes: the softmax warps' 3,500
+// cycles a tile, in which the codes' conversions share their exp unit); trees of
+// 64 tokens, 64/8 heads, 8 requests, 123 us (42 us of tensor-core time: 4,000
+// cycles for two row tiles, half of them the softmax, a quarter its waits for
+// S); one request of 333 positions 16.5 us, of it 2 x 2 us of launches, 3,500
+// cycles until the first scores, 3,000 at the segment's end, the merge.
 #include <math.h>
 
 #include <algorithm>
@@ -56,33 +67,43 @@ constexpr int kRows = 128;           // query rows of a row tile (MMA M)
 constexpr int kMaxNt = 2;            // row tiles that share a K/V tile
 constexpr int kBN = 128;             // positions of a K/V tile
 constexpr int kStages = 2;           // K ring and V ring depth
-constexpr int kProdWarps = 8;        // for K, and as many for V
-constexpr int kProdRows = kBN / kProdWarps;  // rows of a tile each producer warp gathers
-constexpr int kSoftWarps = 4;        // one query row a thread
-constexpr int kWarpQ = kSoftWarps + 2 * kProdWarps;  // loads the query rows
-constexpr int kWarpMma = kWarpQ + 1;                 // issues S = Q K^T; kWarpPv the other product
-constexpr int kWarpSched = kWarpQ + 2;               // hands out the segments
-constexpr int kWarpPv = kWarpQ + 3;
-constexpr int kThreads = 32 * (kWarpQ + 4);
-// registers a thread, by role (a softmax thread holds a row's 128 scores):
-// 128 x 192 + 512 x 56 + 128 x 56 of the 768 x 80 launched
-constexpr int kRegsSoft = 192, kRegsProd = 56, kRegsMisc = 56, kRegsLaunch = 80;
-static_assert(32 * (kSoftWarps * kRegsSoft + 2 * kProdWarps * kRegsProd + 4 * kRegsMisc) <= kThreads * kRegsLaunch,
-              "a share is granted out of the launched registers only");
-static_assert(kThreads * kRegsLaunch <= 65536, "registers of an SM");
 constexpr int kSegs = 4;             // segments handed out ahead
 constexpr int kMaskT = 128;          // trees up to this size have their mask words in shared memory
 constexpr int kRing = 4;             // score scales kept (see query_loader)
 constexpr int kCodeBufs = 3;         // FP8: half tiles of codes in flight, for K and for V
+// The roles of the warps: for each row tile four softmax warps, one query row a
+// thread; producers for K and as many for V; one each that loads the query rows,
+// issues S = Q K^T, hands out the segments, issues the other product.
+template <int NT>
+struct Ro {
+    static constexpr int SOFT = 4 * NT, PROD = NT == 1 ? 8 : 4;
+    static constexpr int ROWS = kBN / PROD;              // rows of a tile each producer warp gathers
+    static constexpr int Q = SOFT + 2 * PROD, MMA = Q + 1, SCHED = Q + 2, PV = Q + 3;
+    static constexpr int THREADS = 32 * (Q + 4);
+    // registers a thread, by role (a softmax thread holds a row's 128 scores):
+    // 128 x 192 + 640 x 56 of the 768 x 80 launched; with two row tiles
+    // 256 x 168 + 384 x 48 of 640 x 96
+    static constexpr int R_SOFT = NT == 1 ? 192 : 168, R_REST = NT == 1 ? 56 : 48, R_LAUNCH = NT == 1 ? 80 : 96;
+    static_assert(32 * (SOFT * R_SOFT + (2 * PROD + 4) * R_REST) <= THREADS * R_LAUNCH,
+                  "a share is granted out of the launched registers only");
+    static_assert(THREADS * R_LAUNCH <= 65536, "registers of an SM");
+};
 // TMEM: an O for each row tile, then S buffers (two; one beside two O), then
 // two P of 64 columns (16-bit pairs)
 constexpr uint32_t kTmemCols = 512;
 template <int NT>
 struct Tm {
-    static constexpr int NS = NT == 1 ? 2 : 1;
     static __device__ __forceinline__ uint32_t o(int t) { return t * 128; }
-    static __device__ __forceinline__ uint32_t s(int b) { return NT * 128 + b * 128; }
+    static __device__ __forceinline__ uint32_t s(int b) { return NT * 128 + (NT == 1 ? b * 128 : 0); }
     static __device__ __forceinline__ uint32_t p(int b) { return 384 + b * 64; }
+};
+// An item's S, P and product barriers and buffers: with one row tile the items
+// take turns at two; with two row tiles each has its own (but one S for both).
+// c: which item of its row tile it is.
+template <int NT>
+struct Turn {
+    int b, phase;
+    __device__ __forceinline__ Turn(int t, int c) : b(NT == 1 ? c & 1 : t), phase(NT == 1 ? c >> 1 : c) {}
 };
 constexpr float kRescale = 8.f;      // log2 units the running max may lag
 constexpr int kMergeRows = 16;       // rows of one merge CTA
@@ -117,7 +138,7 @@ struct TL {
     static constexpr int OFF_QS = OFF_NF + kSegs * 32 * 4;            // kRing x 128 floats
     static constexpr int OFF_MASK = OFF_QS + kRing * kRows * 4;       // kSegs x 128 tokens x 4 words;
     static constexpr int MASK = kSegs * kMaskT * (kMaskT / 32) * 4;   //   before them, the scan of the lengths
-    static_assert((kThreads + 1) * 8 <= MASK, "room for the scan");
+    static_assert((Ro<1>::THREADS + 1) * 8 <= MASK && (Ro<2>::THREADS + 1) * 8 <= MASK, "room for the scan");
     static constexpr int OFF_SEG = OFF_MASK + MASK;
     static constexpr int OFF_BAR = OFF_SEG + kSegs * 64;
     static constexpr int B_KFULL = 0, B_KEMPTY = B_KFULL + kStages, B_VFULL = B_KEMPTY + kStages,
@@ -292,6 +313,8 @@ __device__ void scheduler(const TParams &p, unsigned char *smem, uint32_t sbase)
     for (int s = 0;; ++s) {
         const int slot = s % kSegs, l = c.b - base;
         if (s >= kSegs && !warp_wait(bar + 8 * (L::B_SEGEMPTY + slot), (s / kSegs - 1) & 1, abort_flag, p.status)) break;
+        // no drafted position of the new segment noted yet (see the V producers)
+        if (s >= kSegs) reinterpret_cast<uint32_t *>(smem + L::OFF_NF)[slot * 32 + lane] = 0;
         Seg g;
         const int ntiles = __shfl_sync(0xffffffffu, mine.ntiles, l), nqt = __shfl_sync(0xffffffffu, mine.nqt, l);
         g.g = c.g;
@@ -416,8 +439,8 @@ __device__ __forceinline__ uint4 widen_f16(uint32_t lo, uint32_t hi)
                       rx::e4m3x2_to_f16x2((uint16_t)hi), rx::e4m3x2_to_f16x2((uint16_t)(hi >> 16)));
 }
 
-// Eight producer warps for K and eight for V (V's wait for the softmax does
-// not hold up K); warp w gathers rows [16 w, 16 w + 16) of every tile in
+// Eight producer warps for K and eight for V, four with two row tiles (V's wait for the softmax does
+// not hold up K); each gathers the same rows of every tile in
 // 16-byte async copies, slot ids two tiles ahead.  (Loads into registers go
 // through L1, which this kernel's shared memory leaves 28 KB: they ran at half
 // the rate.)
@@ -430,25 +453,26 @@ __device__ __forceinline__ uint4 widen_f16(uint32_t lo, uint32_t hi)
 // V at drafted positions is looked at before it is handed over: a NaN or
 // infinity there would reach rows that do not see the position (0 * inf), so it
 // is dropped, noted, and added back to the rows that see it at the end.
-template <int D, bool F8, bool IS_V>
+template <int D, bool F8, int NT, bool IS_V>
 __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
 {
     using L = TL<D, F8>;
+    constexpr int ROWS = Ro<NT>::ROWS;
     constexpr int EB = F8 ? 1 : 2;                    // bytes of a value
     constexpr int CPR = D * EB / 16;                  // 16-byte chunks of a row
     constexpr int RPI = 32 / CPR;                     // rows of one instruction
-    constexpr int U = kProdRows / RPI;                // instructions for this warp's rows
+    constexpr int U = ROWS / RPI;                     // instructions for this warp's rows
     const uint32_t bar_full = sbase + L::OFF_BAR + 8 * (IS_V ? L::B_VFULL : L::B_KFULL);
     const uint32_t bar_empty = sbase + L::OFF_BAR + 8 * (IS_V ? L::B_VEMPTY : L::B_KEMPTY);
     const unsigned char *pool = IS_V ? p.v : p.k;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
-    const int lane = threadIdx.x & 31, pw = ((int)(threadIdx.x >> 5) - kSoftWarps) % kProdWarps;
-    const int r0 = pw * kProdRows;
+    const int lane = threadIdx.x & 31, pw = ((int)(threadIdx.x >> 5) - Ro<NT>::SOFT) % Ro<NT>::PROD;
+    const int r0 = pw * ROWS;
     const int sub = lane / CPR, ch = lane % CPR;
     const int row_bytes = p.hkv * D * EB;             // at most 2^21 (the heads are bounded)
 
     struct Tile {
-        int32_t slot;  // lane l < 16: slot of row r0 + l, in flight until check() looks at it
+        int32_t slot;  // lane l < ROWS: slot of row r0 + l, in flight until check() looks at it
         int lim;       // positions of the request from the tile's first on; 0: no tile
         int meta;      // kv head, T, segment mod kSegs: bits 0, 13 and 24 on
 
@@ -483,7 +507,7 @@ __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
         }
         t.lim = lim;
         t.meta = meta;
-        if (lane < kProdRows && r0 + lane < lim) t.slot = rx::ld_stream_b32(slots);
+        if (lane < ROWS && r0 + lane < lim) t.slot = rx::ld_stream_b32(slots);
         --left;
         lim -= kBN;
         slots += kBN;
@@ -491,7 +515,7 @@ __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
     // slots past the end or outside the pool (flagged) become -1
     auto check = [&](Tile &t) {
         if (t.slot >= 0 && (int64_t)t.slot < p.num_slots) return;
-        if (lane < kProdRows && r0 + lane < t.lim && p.status) atomicOr(p.status, RX_DEV_BAD_SLOT);
+        if (lane < ROWS && r0 + lane < t.lim && p.status) atomicOr(p.status, RX_DEV_BAD_SLOT);
         t.slot = -1;
     };
     auto source = [&](const Tile &t, int u, bool &ok) {
@@ -704,20 +728,24 @@ __device__ void query_loader(const TParams &p, unsigned char *smem, uint32_t sba
 // the two MMA threads
 // ---------------------------------------------------------------------------
 
-// The CTA's items i = 0, 1, ...: for every position tile n (all segments in a
-// row) the segment's row tiles t.  S(i) = Q_t K_n^T waits for an S buffer whose
-// scores the softmax has in registers, O_t += P(i) V_n for P(i).  P(i), in
-// buffer i & 1, is stored once the product of item i - 2 has completed; the
-// products of odd and even items complete on barriers of their own, so that
-// whoever waits for one knows that the one two items before has completed and
-// a phase's parity is never ambiguous.
+// The CTA's items: for every position tile n (all segments in a row) the
+// segment's row tiles t.  S = Q_t K_n^T waits for an S buffer whose scores the
+// softmax has in registers, O_t += P V_n for P.
+//
+// One row tile: S and P have two buffers each, which the items take in turn, and
+// barriers for each: whoever waits for one product knows that the one two items
+// before has completed, and a phase's parity is never ambiguous.  Two row tiles:
+// a P and barriers for each, so again each barrier is waited for phase by phase
+// by one group of warps; TMEM has room for one S, which the next item of either
+// takes once the last one's scores are in registers.
 //
 // S and P V are issued by a thread each: a thread spends as long on the waits
 // and commits around an operation's eight MMAs as on the MMAs, and with one
 // thread for both the tensor core idled meanwhile (long chat 0.252 against
 // 0.242 ms).
 struct Item {
-    int i, n, t;
+    int c, n, t;                   // c: of its row tile; before: the item before it, if any
+    int before_t, before_c;
     int use;                       // row tiles before this one in its O (and Q) buffer
     int seg;
     bool t0, t1;                   // the first, the last row tile of the position tile
@@ -728,16 +756,22 @@ struct Item {
 template <typename L, int NT, typename F>
 __device__ __forceinline__ void for_items(const TParams &p, unsigned char *smem, uint32_t sbase, F f)
 {
-    int i = 0, n = 0, s2 = 0;  // s2: segments with two row tiles
+    int c0 = 0, c1 = 0, n = 0, s2 = 0;  // s2: segments with two row tiles
+    int before_t = 0, before_c = -1;
     for (int s = 0;; ++s) {
         Seg g;
         if (!get_seg<L>(s, g, smem, sbase, p.status)) return;
         free_seg<L>(s, sbase);
         const int nt = NT == 1 ? 1 : g.nt;
         for (int j = g.j0; j < g.j1; ++j, ++n)
-            for (int t = 0; t < nt; ++t, ++i)
-                if (!f(Item{i, n, t, t == 0 ? s : s2, s, NT == 1 || t == 0, NT == 1 || t == nt - 1, j == g.j0, j == g.j1 - 1}))
+            for (int t = 0; t < nt; ++t) {
+                const int c = t == 0 ? c0++ : c1++;
+                if (!f(Item{c, n, t, before_t, before_c, t == 0 ? s : s2, s, NT == 1 || t == 0, NT == 1 || t == nt - 1, j == g.j0,
+                            j == g.j1 - 1}))
                     return;
+                before_t = t;
+                before_c = c;
+            }
         s2 += nt == 2;
         if (g.last) return;
     }
@@ -756,11 +790,17 @@ __device__ void issue_qk(const TParams &p, unsigned char *smem, uint32_t sbase)
     const uint64_t dq = rx::sdesc_sw128(sbase + L::OFF_Q, 16, 1024);
     const uint64_t dk = rx::sdesc_sw128(sbase + L::OFF_K, 16, 1024);
     for_items<L, NT>(p, smem, sbase, [&](const Item &m) -> bool {
-        const int st = m.n % kStages, b = m.i % M::NS;
+        const int st = m.n % kStages;
+        const Turn<NT> turn(m.t, m.c);
         const int qb = NT == 1 ? m.seg % L::QB : m.t, quse = NT == 1 ? m.seg / L::QB : m.use;
         if (m.first && !wait(L::B_QFULL + qb, quse & 1)) return false;
         if (m.t0 && !wait(L::B_KFULL + st, (m.n / kStages) & 1)) return false;
-        if (m.i >= M::NS && !wait(L::B_SEMPTY + b, (m.i / M::NS - 1) & 1)) return false;
+        // its S: of the item two before, or with one for both row tiles of the item before
+        if constexpr (NT == 1) {
+            if (m.c >= 2 && !wait(L::B_SEMPTY + turn.b, (turn.phase - 1) & 1)) return false;
+        } else {
+            if (m.before_c >= 0 && !wait(L::B_SEMPTY + m.before_t, m.before_c & 1)) return false;
+        }
         rx::fence_proxy_async_smem();  // rows landed by cp.async -> async proxy
         rx::tc_fence_after();
         const uint64_t dks = dk + (uint64_t)((st * L::NB * L::BLK) >> 4);
@@ -768,9 +808,9 @@ __device__ void issue_qk(const TParams &p, unsigned char *smem, uint32_t sbase)
 #pragma unroll
         for (int kb = 0; kb < D / 16; ++kb) {
             const uint64_t off = (uint64_t)(((kb >> 2) * L::BLK + (kb & 3) * 32) >> 4);
-            rx::tc_mma(tmem + M::s(b), dqs + off, dks + off, idesc, kb > 0);
+            rx::tc_mma(tmem + M::s(turn.b), dqs + off, dks + off, idesc, kb > 0);
         }
-        rx::tc_commit(bar + 8 * (L::B_SFULL + b));
+        rx::tc_commit(bar + 8 * (L::B_SFULL + turn.b));
         if (m.t1) rx::tc_commit(bar + 8 * (L::B_KEMPTY + st));
         if (m.last) rx::tc_commit(bar + 8 * (L::B_QEMPTY + qb));
         return true;
@@ -792,18 +832,19 @@ __device__ void issue_pv(const TParams &p, unsigned char *smem, uint32_t sbase)
     auto wait = [&](int b, uint32_t parity) { return wait_or_abort(bar + 8 * b, parity, abort_flag, p.status); };
     const uint64_t dv = rx::sdesc_sw128(sbase + L::OFF_V, L::BLK, 1024);
     for_items<L, NT>(p, smem, sbase, [&](const Item &m) -> bool {
-        const int st = m.n % kStages, b = m.i & 1;
+        const int st = m.n % kStages;
+        const Turn<NT> turn(m.t, m.c);
         if (m.t0 && !wait(L::B_VFULL + st, (m.n / kStages) & 1)) return false;
         if (m.first && m.use >= 1 && !wait(L::B_OEMPTY + m.t, (m.use - 1) & 1)) return false;
-        if (!wait(L::B_PFULL + b, (m.i >> 1) & 1)) return false;
+        if (!wait(L::B_PFULL + turn.b, turn.phase & 1)) return false;
         rx::fence_proxy_async_smem();  // V rows landed by cp.async
         rx::tc_fence_after();
         const uint64_t dvs = dv + (uint64_t)((st * L::NB * L::BLK) >> 4);
 #pragma unroll
         for (int ks = 0; ks < kBN / 16; ++ks)
-            rx::tc_mma_ts(tmem + M::o(m.t), tmem + M::p(b) + ks * 8, dvs + (uint64_t)((ks * 16 * 128) >> 4), idesc,
+            rx::tc_mma_ts(tmem + M::o(m.t), tmem + M::p(turn.b) + ks * 8, dvs + (uint64_t)((ks * 16 * 128) >> 4), idesc,
                           (!m.first || ks > 0) ? 1u : 0u);
-        rx::tc_commit(bar + 8 * (L::B_PVDONE + b));
+        rx::tc_commit(bar + 8 * (L::B_PVDONE + turn.b));
         if (m.t1) rx::tc_commit(bar + 8 * (L::B_VEMPTY + st));
         return true;
     });
@@ -855,36 +896,42 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::OFF_TMEM);
     const uint32_t bar = sbase + L::OFF_BAR;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
-    const int row = threadIdx.x;                       // = TMEM lane
+    const int row = threadIdx.x & (kRows - 1);         // = TMEM lane
+    const int t = NT == 1 ? 0 : threadIdx.x / kRows;   // the warps' row tile
     const uint32_t lanes = (uint32_t)(row & ~31) << 16;
     const int rt = row / p.G, rh = row - rt * p.G;     // drafted token of the row tile, q head of the kv head
-    int i = 0;                                         // items so far
+    int c = 0;                                         // the row tile's items so far
     for (int s = 0;; ++s) {
         Seg g;
         if (!__all_sync(0xffffffffu, get_seg<L>(s, g, smem, sbase, p.status))) return;
-        const int nt = NT == 1 ? 1 : g.nt;
+        if (NT == 2 && t >= g.nt) {  // the segment has one row tile
+            __syncwarp();
+            if ((row & 31) == 0) free_seg<L>(s, sbase);
+            if (g.last) return;
+            continue;
+        }
         // the mask row of drafted token rt + t * tb of the segment
         const uint32_t *masks = !p.mask ? nullptr
                                 : g.T <= kMaskT ? reinterpret_cast<const uint32_t *>(smem + L::OFF_MASK) + (s % kSegs) * (kMaskT * (kMaskT / 32))
                                                 : p.mask + (int64_t)g.tok * p.words;
         const int words = g.T <= kMaskT ? kMaskT / 32 : p.words;
-        RowState a{-INFINITY, 0.f, p.scale_log2}, b = a;   // the item's row tile, and the other one
-        for (int j = g.j0; j < g.j1; ++j)
-            for (int t = 0; t < nt; ++t, ++i) {
-                const int sb = i % TM::NS;
-                const uint32_t tS = tmem + TM::s(sb) + lanes, tO = tmem + TM::o(t) + lanes, tP = tmem + TM::p(i & 1) + lanes;
-                const int M = min(p.tb, g.ntok - t * p.tb) * p.G;
+        RowState a{-INFINITY, 0.f, p.scale_log2};
+        for (int j = g.j0; j < g.j1; ++j, ++c) {
+                const int M = min(p.tb, g.ntok - t * p.tb) * p.G, node = rt + t * p.tb;
                 const bool valid = row < M, warp_on = (row & ~31) < M;
-                if (!warp_wait(bar + 8 * (L::B_SFULL + sb), (i / TM::NS) & 1, abort_flag, p.status)) return;
+                const uint32_t tO = tmem + TM::o(t) + lanes;
+                const Turn<NT> turn(t, c);
+                const uint32_t tS = tmem + TM::s(turn.b) + lanes, tP = tmem + TM::p(turn.b) + lanes;
+                if (!warp_wait(bar + 8 * (L::B_SFULL + turn.b), turn.phase & 1, abort_flag, p.status)) return;
                 rx::tc_fence_after();
                 auto release_s = [&]() {
                     rx::tc_fence_before();
-                    rx::mbar_arrive(bar + 8 * (L::B_SEMPTY + sb));
+                    rx::mbar_arrive(bar + 8 * (L::B_SEMPTY + turn.b));
                 };
-                // the product two items before has read P's columns (a warp
-                // without rows waits too, or it could arrive twice in a phase)
+                // the product before in these columns has read P (a warp without
+                // rows waits too, or it could arrive twice in a phase)
                 auto p_free = [&]() {
-                    const bool ok = i < 2 || warp_wait(bar + 8 * (L::B_PVDONE + (i & 1)), ((i >> 1) - 1) & 1, abort_flag, p.status);
+                    const bool ok = turn.phase < 1 || warp_wait(bar + 8 * (L::B_PVDONE + turn.b), (turn.phase - 1) & 1, abort_flag, p.status);
                     rx::tc_fence_after();
                     return ok;
                 };
@@ -901,7 +948,7 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
                         a.sl2 = p.scale_log2 * reinterpret_cast<const float *>(smem + L::OFF_QS)[(s % kRing) * kRows + row];
                     const int kbase = j * kBN;
                     if (kbase + kBN > g.P) {   // drafted positions, or past the last
-                        const int off = kbase - g.P, w0 = off >> 5, node = rt + t * p.tb;
+                        const int off = kbase - g.P, w0 = off >> 5;
                         const uint32_t *mrow = masks && valid ? masks + (int64_t)node * words : nullptr;
                         uint32_t w[5];
 #pragma unroll
@@ -962,9 +1009,9 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
                     rx::f2_split(rx::f2_add(rx::f2_add(acc[0], acc[1]), rx::f2_add(acc[2], acc[3])), a0, a1);
                     a.l += a0 + a1;
                     if (__any_sync(0xffffffffu, scale_o)) {
-                        // this row tile's product before, item i - nt, has to be
-                        // complete; i - 2 is
-                        if (nt == 1 && !warp_wait(bar + 8 * (L::B_PVDONE + ((i - 1) & 1)), ((i - 1) >> 1) & 1, abort_flag, p.status))
+                        // the row tile's product before has to be complete; that
+                        // of the item two before is
+                        if (NT == 1 && !warp_wait(bar + 8 * (L::B_PVDONE + ((c - 1) & 1)), ((c - 1) >> 1) & 1, abort_flag, p.status))
                             return;
                         rx::tc_fence_after();
 #pragma unroll
@@ -980,26 +1027,18 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
                     rx::tmem_wait_st();
                 }
                 rx::tc_fence_before();
-                rx::mbar_arrive(bar + 8 * (L::B_PFULL + (i & 1)));
-                if (nt == 2) {
-                    const RowState x = a;
-                    a = b;
-                    b = x;
-                }
+                rx::mbar_arrive(bar + 8 * (L::B_PFULL + turn.b));
             }
-        // the segment's results
-        uint32_t any = 0;
+        // the segment's results, once the row tile's last product is complete
         const uint32_t *nf = reinterpret_cast<const uint32_t *>(smem + L::OFF_NF) + (s % kSegs) * 32;
-        for (int t = 0; t < nt; ++t) {
-            // the row tile's last product, item i - nt + t
-            const int e = i - nt + t;
-            if (!warp_wait(bar + 8 * (L::B_PVDONE + (e & 1)), (e >> 1) & 1, abort_flag, p.status)) return;
-            rx::tc_fence_after();
-            const RowState &r = t == 0 ? a : b;
+        {
+            const Turn<NT> end(t, c - 1);
             const int M = min(p.tb, g.ntok - t * p.tb) * p.G, node = rt + t * p.tb;
             const bool valid = row < M, warp_on = (row & ~31) < M;
             const uint32_t tO = tmem + TM::o(t) + lanes;
-            const float inv = r.l == 0.f ? 0.f : p.v_scale / r.l;
+            if (!warp_wait(bar + 8 * (L::B_PVDONE + end.b), end.phase & 1, abort_flag, p.status)) return;
+            rx::tc_fence_after();
+            const float inv = a.l == 0.f ? 0.f : p.v_scale / a.l;
             const int64_t orow = (int64_t)(g.tok + node) * p.hq + (int64_t)g.g * p.G + rh;
             const int64_t prow = ((int64_t)(2 * blockIdx.x + (g.j0 == 0 ? 1 : 0)) * NT + t) * kRows + row;
             if (warp_on) {
@@ -1012,7 +1051,7 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
                     rx::tmem_wait_ld();
                     if (valid) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) x[e] = r.l == 0.f ? 0u : __float_as_uint(u2f(x[e]) * inv);
+                    for (int e = 0; e < 32; ++e) x[e] = a.l == 0.f ? 0u : __float_as_uint(u2f(x[e]) * inv);
                     if (g.whole) {
                         uint4 *dst = reinterpret_cast<uint4 *>(p.o + orow * D + k * 32);
 #pragma unroll
@@ -1030,7 +1069,7 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
                     __syncwarp();
                 }
                 if (valid) {
-                    const float l2 = r.l == 0.f ? -INFINITY : r.m + log2f(r.l);
+                    const float l2 = a.l == 0.f ? -INFINITY : a.m + log2f(a.l);
                     if (!g.whole) p.part_l[prow] = l2;
                     else if (p.lse) p.lse[orow] = l2 * rx::kLn2;
                 }
@@ -1039,16 +1078,12 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
             rx::tc_fence_before();
             rx::mbar_arrive(bar + 8 * (L::B_OEMPTY + t));
             if (g.j1 * kBN > g.P) {
-                if (t == 0)
-                    for (int w = 0; w < (g.T + 31) / 32; ++w) any |= nf[w];
+                uint32_t any = 0;
+                for (int w = 0; w < (g.T + 31) / 32; ++w) any |= nf[w];
                 if (any && valid)
                     add_not_finite<D, F8>(p, nf, masks ? masks + (int64_t)node * words : nullptr, words, g.node + node, g.row, g.g,
                                           g.P, g.T, g.whole ? -1 : prow, orow);
             }
-        }
-        if (any) {  // the same for every thread: all have read the words, then they are cleared
-            rx::named_bar_sync(1, 32 * kSoftWarps);
-            if (row < 32) const_cast<uint32_t *>(nf)[row] = 0;
         }
         __syncwarp();
         if ((row & 31) == 0) free_seg<L>(s, sbase);
@@ -1057,9 +1092,11 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
 }
 
 template <int D, bool F8, int NT>
-__global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant__ TParams p)
+__global__ void __launch_bounds__(Ro<NT>::THREADS, 1) tree_kernel(const __grid_constant__ TParams p)
 {
     using L = TL<D, F8>;
+    using W = Ro<NT>;
+    constexpr int kThreads = W::THREADS;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const uint32_t raw = rx::smem_u32(smem_raw);
     unsigned char *smem = smem_raw + (((raw + 1023u) & ~1023u) - raw);  // 1024-aligned swizzle atoms
@@ -1070,8 +1107,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            rx::mbar_init(bar + 8 * (L::B_KFULL + i), 32 * kProdWarps);
-            rx::mbar_init(bar + 8 * (L::B_VFULL + i), 32 * kProdWarps);
+            rx::mbar_init(bar + 8 * (L::B_KFULL + i), 32 * W::PROD);
+            rx::mbar_init(bar + 8 * (L::B_VFULL + i), 32 * W::PROD);
             rx::mbar_init(bar + 8 * (L::B_KEMPTY + i), 1);
             rx::mbar_init(bar + 8 * (L::B_VEMPTY + i), 1);
         }
@@ -1088,7 +1125,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         }
         for (int i = 0; i < kSegs; ++i) {
             rx::mbar_init(bar + 8 * (L::B_SEGFULL + i), 32 + 1);  // the scheduler's lanes' copies, and the segment
-            rx::mbar_init(bar + 8 * (L::B_SEGEMPTY + i), kSoftWarps + 2 * kProdWarps + 3);
+            rx::mbar_init(bar + 8 * (L::B_SEGEMPTY + i), W::SOFT + 2 * W::PROD + 3);
         }
         rx::mbar_init(bar + 8 * L::B_FINAL, 1);
         rx::mbar_init(bar + 8 * (L::B_FINAL + 1), 1);
@@ -1116,35 +1153,35 @@ __global__ void __launch_bounds__(kThreads, 1) tree_kernel(const __grid_constant
         c.left = (int)(first_unit(total, ctas, blockIdx.x + 1) - u0);
         *reinterpret_cast<Start *>(smem + L::OFF_START) = c;
     }
-    if (warp == kWarpMma) rx::tmem_alloc(sbase + L::OFF_TMEM, kTmemCols);
+    if (warp == W::MMA) rx::tmem_alloc(sbase + L::OFF_TMEM, kTmemCols);
     rx::tc_fence_before();
     __syncthreads();  // from here on the scan's room holds masks
     rx::tc_fence_after();
 
-    if (warp < kSoftWarps) {
-        rx::reg_inc<kRegsSoft>();
+    if (warp < W::SOFT) {
+        rx::reg_inc<W::R_SOFT>();
         softmax_rows<D, F8, NT>(p, smem, sbase);
-    } else if (warp < kWarpQ) {
-        rx::reg_dec<kRegsProd>();
-        if (warp < kSoftWarps + kProdWarps) producer<D, F8, false>(p, smem, sbase);
-        else producer<D, F8, true>(p, smem, sbase);
+    } else if (warp < W::Q) {
+        rx::reg_dec<W::R_REST>();
+        if (warp < W::SOFT + W::PROD) producer<D, F8, NT, false>(p, smem, sbase);
+        else producer<D, F8, NT, true>(p, smem, sbase);
     } else {
-        rx::reg_dec<kRegsMisc>();
-        if (warp == kWarpQ) {
+        rx::reg_dec<W::R_REST>();
+        if (warp == W::Q) {
             query_loader<D, F8, NT>(p, smem, sbase);
-        } else if (warp == kWarpMma) {
+        } else if (warp == W::MMA) {
             if ((threadIdx.x & 31) == 0) issue_qk<D, F8, NT>(p, smem, sbase);
             __syncwarp();
-        } else if (warp == kWarpPv) {
+        } else if (warp == W::PV) {
             if ((threadIdx.x & 31) == 0) issue_pv<D, F8, NT>(p, smem, sbase);
             __syncwarp();
-        } else if (warp == kWarpSched) {
+        } else if (warp == W::SCHED) {
             scheduler<D, F8>(p, smem, sbase);
         }
     }
     rx::tc_fence_before();
     __syncthreads();
-    if (warp == kWarpMma) {
+    if (warp == W::MMA) {
         rx::tc_fence_after();
         rx::tmem_dealloc(*reinterpret_cast<volatile uint32_t *>(smem + L::OFF_TMEM), kTmemCols);
     }
@@ -1210,8 +1247,9 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
 size_t part_bytes(int32_t nt, int32_t head_dim) { return (size_t)2 * kCtas * nt * kRows * head_dim * sizeof(float); }
 
 // Row tiles that share a K/V tile: two where some tree may have more than one
-// (64-token trees over 64/8 heads, 8k contexts: @NT@), and bf16
-// pools only (an FP8 tile has one query buffer).
+// (64-token trees over 64/8 heads, 8k contexts: 123 us, one at a time 134 us),
+// and bf16 pools only (an FP8 tile has one query buffer).  The second brings
+// softmax warps of its own; one group for both took 133 us.
 int row_tiles(int32_t hq, int32_t hkv, int32_t max_tree) { return (int64_t)max_tree > kRows / (hq / hkv) ? kMaxNt : 1; }
 
 struct TreePool {
@@ -1233,7 +1271,7 @@ int launch(const TParams &p, cudaStream_t st)
 {
     // per device; cheap, and right whichever device is current
     RX_CUDA_CHECK(cudaFuncSetAttribute(tree_kernel<D, F8, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (TL<D, F8>::BYTES)));
-    tree_kernel<D, F8, NT><<<kCtas, kThreads, (TL<D, F8>::BYTES), st>>>(p);
+    tree_kernel<D, F8, NT><<<kCtas, Ro<NT>::THREADS, (TL<D, F8>::BYTES), st>>>(p);
     RX_CUDA_CHECK(cudaGetLastError());
     // a programmatic dependent: it is launched meanwhile and waits on the device
     cudaLaunchConfig_t cfg = {};
