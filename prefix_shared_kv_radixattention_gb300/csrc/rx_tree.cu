@@ -40,7 +40,9 @@
 // 212 us (149 us of bytes; four of a tile's 128 rows are used, and a softmax
 // warp takes 2,300 cycles for a tile however few rows it has); E4M3 pools, 16 of
 // up to 32,768, 32/8 heads, 301 us (119 us of bytes: the softmax warps' 3,500
-// cycles a tile, in which the codes' conversions share their exp unit); trees of
+// cycles a tile, two of the four with rows; a part of the exponentials on the
+// multiply-add units made the tile slower, 368 us: it is their issue, not the
+// exp unit, that counts); trees of
 // 64 tokens, 64/8 heads, 8 requests, 123 us (42 us of tensor-core time: 4,000
 // cycles for two row tiles, half of them the softmax, a quarter its waits for
 // S); one request of 333 positions 16.5 us, of it 2 x 2 us of launches, 3,500
@@ -439,9 +441,9 @@ __device__ __forceinline__ uint4 widen_f16(uint32_t lo, uint32_t hi)
                       rx::e4m3x2_to_f16x2((uint16_t)hi), rx::e4m3x2_to_f16x2((uint16_t)(hi >> 16)));
 }
 
-// Eight producer warps for K and eight for V, four with two row tiles (V's wait for the softmax does
-// not hold up K); each gathers the same rows of every tile in
-// 16-byte async copies, slot ids two tiles ahead.  (Loads into registers go
+// Eight producer warps for K and eight for V, four with two row tiles (V's wait
+// for the softmax does not hold up K); each gathers the same rows of every tile
+// in 16-byte async copies, slot ids two tiles ahead.  (Loads into registers go
 // through L1, which this kernel's shared memory leaves 28 KB: they ran at half
 // the rate.)
 //
