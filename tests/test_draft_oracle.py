@@ -112,7 +112,7 @@ def test_tree_refuses_invalid_arguments(bad):
 
 
 @pytest.mark.parametrize("bad", [dict(d=96), dict(d=256), dict(hq=5), dict(hq=258, hkv=2), dict(max_tree=1025, words=40),
-                                 dict(batch=65536)], ids=str)
+                                 dict(batch=65536), dict(hq=8193, hkv=8193)], ids=str)
 def test_tree_refuses_unsupported_shapes(bad):
     assert set(_tree(rx.library(), **bad)) == {rx.RX_ERR_UNSUPPORTED}
 
@@ -186,5 +186,6 @@ def test_logits_refuses_invalid_arguments(bad):
 def test_logits_other_answers_without_a_launch():
     lib = rx.library()
     assert _logits(lib, n_req=70000, rows=70000) == rx.RX_ERR_UNSUPPORTED
+    assert _logits(lib, vocab=(1 << 30) + 1, ls=1 << 31, os=1 << 31) == rx.RX_ERR_UNSUPPORTED
     assert _logits(lib, n_req=0, rows=0, logits=None, out=None) == rx.RX_OK
     assert _logits(lib, n_req=3, rows=0, qo_indptr=FAKE, logits=None, out=None) == rx.RX_OK
