@@ -632,8 +632,9 @@ int rx_tree_mask_build(const int32_t *parent, int32_t n, int32_t words, uint32_t
  *   workspace: device, >= rx_attn_tree_workspace(...) bytes, 256-byte
  *   aligned, contents ignored on entry, not used by anything else until the
  *   call's work on `stream` is done.
- * Requires head_dim 64 or 128, num_q_heads % num_kv_heads == 0 and
- * num_q_heads / num_kv_heads <= 128.  A request with T_b > max_tree_len or
+ * Requires head_dim 64 or 128, num_q_heads % num_kv_heads == 0,
+ * num_q_heads / num_kv_heads <= 128, num_kv_heads <= 8192 and batch <= 65535.
+ * A prefix that several requests share is read for each of them.  A request with T_b > max_tree_len or
  * prefix_len[b] + T_b past the stride sets RX_DEV_BAD_LEN and its rows stay
  * unwritten; a bad slot reads as zeros (RX_DEV_BAD_SLOT).  Rows behind
  * qo_indptr[batch] are left as they were.  The lengths are read on the
@@ -759,9 +760,11 @@ int rx_fsm_step(const rx_fsm *fsm, const float *logits, int64_t logits_stride, i
  * Rows: without qo_indptr, row r is request r (n_req rows).  With it, rows
  * qo_indptr[b] .. qo_indptr[b+1] - 1 are request b's drafted tokens, and the
  * path of row r is the drafted tokens draft_tok[qo_indptr[b] + j] with bit j
- * set in tree_mask row r (as rx_attn_tree reads them; a request with more
- * than 1024 of them, or than the mask's bits, sets RX_DEV_BAD_LEN and gets
- * its mask only).  Rows behind the last are left as they were.
+ * set in tree_mask row r (as rx_attn_tree reads them).  Rows behind the last
+ * are left as they were.  A request with more than 1024 drafted tokens, or
+ * more than the mask has bits, or more than 2^29 - 1025 tokens in hist, or
+ * whose pointers descend or pass the last row sets RX_DEV_BAD_LEN, and the
+ * rows that it has get their mask only.
  * All pointers are device memory.  NULL leaves a part out: hist (no request
  * tokens), repetition (1), frequency and presence (0), bias_ptr, allow,
  * draft_tok (no paths). */
@@ -796,7 +799,9 @@ typedef struct {
  * RX_DEV_BAD_TOKEN, as does a bias list that is not ascending (the ids out of
  * order may then be left out); a mask row outside [-1, n_allow) sets
  * RX_DEV_BAD_STATE and allows nothing.  Rows start at any element; those on
- * 16-byte boundaries move in 16-byte pieces. */
+ * 16-byte boundaries move in 16-byte pieces.  n_req <= 65535, vocab <= 2^30
+ * (RX_ERR_UNSUPPORTED otherwise).  No workspace: calls on several streams, or
+ * captured ones, may share the rules. */
 int rx_logits_process(const rx_logits_rules *rules, const void *logits, int32_t logits_bf16,
                       int64_t logits_stride, float *out, int64_t out_stride, int32_t rows,
                       int32_t *dev_status, void *stream);

@@ -30,7 +30,7 @@
 // memory, 82, 38 and 6.8 us; through global memory, a third kernel, 61, 45 and
 // 14 us.
 //
-// In place, only forbidden and listed ids are written.
+// In place, only groups with a forbidden or a touched id are read and written.
 #include <algorithm>
 #include <climits>
 #include <math.h>
@@ -92,7 +92,7 @@ struct Request {
         nhist = r.hist ? __ldg(r.hist_ptr + b + 1) - hist0 : 0;
         penal = rep != 1.f || freq != 0.f || pres != 0.f;
         tree = row1 - row0;
-        if (row0 >= 0 && tree >= 0 && row1 <= p.rows && nhist <= (int64_t)kCount - kMaxPath &&
+        if (row0 >= 0 && tree >= 0 && row1 <= p.rows && nhist >= 0 && nhist <= (int64_t)kCount - kMaxPath && nbias >= 0 &&
             !(r.draft_tok && (tree > kMaxPath || (r.tree_mask && (int64_t)tree > 32ll * r.tree_words))))
             return true;
         if (p.status && threadIdx.x == 0) atomicOr(p.status, RX_DEV_BAD_LEN);
@@ -479,8 +479,7 @@ extern "C" int rx_logits_process(const rx_logits_rules *rules, const void *logit
     const int64_t shares = std::max<int64_t>(1, std::min<int64_t>(4 * logits_num_sms() / (tiles * r.n_req), rows));
     const size_t smem = (size_t)tile * (touched ? 5 : 0);
     auto kernel = in_place ? logits_kernel<false, true> : logits_bf16 ? logits_kernel<true, false> : logits_kernel<false, false>;
-    // per device and function; cheap, and right whichever device is current
-    RX_CUDA_CHECK(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTile * 5));
+    static_assert(kTile * 5 <= 48 * 1024, "shared memory of an ordinary launch");
     kernel<<<dim3((unsigned)tiles, (unsigned)r.n_req, (unsigned)shares), kThreads, smem, st>>>(p, tile, touched);
     RX_CUDA_CHECK(cudaGetLastError());
     return RX_OK;

@@ -203,6 +203,29 @@ def test_trees_too_large_for_the_rules_get_their_mask_only():
         _same(out.cpu().numpy(), c.reference())
 
 
+def test_lists_that_descend_and_drafts_without_penalties():
+    """A request whose list pointers descend is flagged and gets its mask only;
+    a drafted token outside the vocabulary is reported although no penalty
+    asks for it."""
+    from prefix_shared_kv_radixattention_gb300 import binding as rx
+    c = Case(15, 3, 500, hist=60, states=3)
+    rules, status = c.rules(), torch.zeros(1, dtype=torch.int32, device="cuda")
+    at = [0, len(c.hist[0]), 0, 0]                               # request 1 from the end of 0's back to its start
+    rules._keep[1].copy_(torch.tensor(at))
+    out = torch.zeros(3, 500, device="cuda")
+    rx.rx_logits_process(rules, c.logits(), out, status)
+    assert int(status.item()) == rx.RX_DEV_BAD_LEN
+    c.hist[1] = c.hist[2] = np.zeros(0, np.int32)
+    _same(out.cpu().numpy(), c.reference())
+    c = Case(16, 2, 500, trees=[4, 3], penalties=False)
+    c.draft[1][2] = 500
+    out = torch.zeros(7, 500, device="cuda")
+    status.zero_()
+    rx.rx_logits_process(c.rules(), c.logits(), out, status)
+    assert int(status.item()) == rx.RX_DEV_BAD_TOKEN
+    _same(out.cpu().numpy(), c.reference())
+
+
 @pytest.mark.parametrize("in_place", [False, True])
 def test_quotients_of_every_size(in_place):
     """Repetition factors and logits of every exponent: the quotient is the
