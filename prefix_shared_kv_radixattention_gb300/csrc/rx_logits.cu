@@ -20,15 +20,18 @@
 //     the mask allows none of the four), their words, the values.  The next
 //     row's logits are on their way meanwhile.
 //
-// So the rows move once, in whole sectors.  What bounds it is partly that, partly
-// the counting (a request's 32,768 tokens are read by every tile's CTA), partly
-// the 70 instructions for four touched ids: 192 drafted rows of 128,256 bf16
-// logits take 60 us (3.3 times their 133 MB), 64 rows of fp32 logits 33 us, one
-// row of 32,000 ids 6.7 us.  A copy of the rows followed by a kernel for the
-// listed touched ids alone took 92, 37 and 5.6 us: partial sectors, and the
-// common tokens in a few CTAs.  The list spread over a cluster through its shared
-// memory, 82, 38 and 6.8 us; through global memory, a third kernel, 61, 45 and
-// 14 us.
+// So the rows move once, in whole sectors.  What bounds it is the instructions:
+// 192 drafted rows of 128,256 bf16 logits over 32,768 tokens a request take 56
+// us (2.9 times the 20 us of their bytes) and 32 million warp instructions at
+// 2.4 a cycle, a quarter of them the counting, which every tile's CTA does for
+// all of the tokens, the rest some 90 for a warp's 128 ids.  64 rows of fp32
+// logits take 34 us, where the chain of loads and barriers before the first
+// row (14,000 cycles of a CTA's 18,000) counts, one row of 32,000 ids 6.7 us.
+//
+// A copy of the rows followed by a kernel for the listed touched ids alone took
+// 92, 37 and 5.6 us: partial sectors, and the common tokens in a few CTAs.  The
+// list spread over a cluster through its shared memory, 82, 38 and 6.8 us;
+// through global memory, a third kernel, 61, 45 and 14 us.
 //
 // In place, only groups with a forbidden or a touched id are read and written.
 #include <algorithm>
@@ -100,27 +103,36 @@ struct Request {
         tree = max(min(row1, p.rows) - row0, 0);
         return false;
     }
-    // y of an id whose word is c, biases apart, from x / repetition
-    __device__ __forceinline__ float penalised(float x, float quotient, uint32_t c) const
+    // x / rep of two values, correctly rounded, for 2^-60 <= rep <= 2^60 and x
+    // <= 0 (any value: unused) or 2^-40 <= x <= 2^40: with 1 / rep correctly
+    // rounded, the first step is within one place of the quotient and the
+    // second rounds it correctly (Markstein, IBM J. Res. Dev. 34, 1990).  Five
+    // packed operations for two quotients, where the general division takes
+    // some ten for one.
+    __device__ __forceinline__ uint64_t divide(uint64_t x) const
     {
-        const uint32_t n = c & kCount;
-        float y = x > 0.f ? quotient : __fmul_rn(x, rep);
-        y = (c & (kPrompt | kCount)) ? y : x;
-        // the product is rounded before the difference, as the formula's steps are
-        const float z = __fsub_rn(__fsub_rn(y, __fmul_rn(freq, (float)n)), pres);
-        return n ? z : y;
+        const uint64_t i = rx::f2(inv, inv), m = rx::f2(-rep, -rep);
+        uint64_t y = rx::f2_mul(x, i);
+        y = rx::f2_fma(rx::f2_fma(m, y, x), i, y);
+        return rx::f2_fma(rx::f2_fma(m, y, x), i, y);
     }
-    // x / rep, correctly rounded, for 2^-60 <= rep <= 2^60 and x <= 0 (any
-    // value: unused) or 2^-40 <= x <= 2^40: with 1 / rep correctly rounded, the
-    // first step is within one place of the quotient and the second rounds it
-    // correctly (Markstein, IBM J. Res. Dev. 34, 1990).  Four multiply-adds for
-    // a quotient, where the general division takes three times as many
-    // instructions.
-    __device__ __forceinline__ float divide(float x) const
+    // the values of two ids with words c0 and c1, biases apart, from their
+    // logits x and quotients d
+    __device__ __forceinline__ void penalise(float &x0, float &x1, float d0, float d1, uint32_t c0, uint32_t c1) const
     {
-        float y = __fmul_rn(x, inv);
-        y = __fmaf_rn(__fmaf_rn(-rep, y, x), inv, y);
-        return __fmaf_rn(__fmaf_rn(-rep, y, x), inv, y);
+        float y0, y1, z0, z1;
+        rx::f2_split(rx::f2_mul(rx::f2(x0, x1), rx::f2(rep, rep)), y0, y1);
+        y0 = x0 > 0.f ? d0 : y0;
+        y1 = x1 > 0.f ? d1 : y1;
+        y0 = (c0 & (kPrompt | kCount)) ? y0 : x0;
+        y1 = (c1 & (kPrompt | kCount)) ? y1 : x1;
+        const uint32_t n0 = c0 & kCount, n1 = c1 & kCount;
+        // the product is rounded before the difference, as the formula's steps
+        // are (a packed product would be joined with the packed difference)
+        const uint64_t fn = rx::f2(__fmul_rn(-freq, (float)n0), __fmul_rn(-freq, (float)n1));
+        rx::f2_split(rx::f2_add(rx::f2_add(rx::f2(y0, y1), fn), rx::f2(-pres, -pres)), z0, z1);
+        x0 = n0 ? z0 : y0;
+        x1 = n1 ? z1 : y1;
     }
 };
 
@@ -130,68 +142,6 @@ __device__ __noinline__ float4 divide_any(float4 x, float rep)
     return make_float4(__fdiv_rn(x.x, rep), __fdiv_rn(x.y, rep), __fdiv_rn(x.z, rep), __fdiv_rn(x.w, rep));
 }
 
-// The sum of the biases of id in an ascending list, in list order.
-__device__ float bias_sum(int id, const int32_t *tok, const float *val, int64_t n)
-{
-    int64_t lo = 0, hi = n;  // first entry at or above id
-    while (lo < hi) {
-        const int64_t mid = (lo + hi) >> 1;
-        if (__ldg(tok + mid) < id) lo = mid + 1; else hi = mid;
-    }
-    if (lo >= n || __ldg(tok + lo) != id) return 0.f;
-    float s = __ldg(val + lo);
-    for (++lo; lo < n && __ldg(tok + lo) == id; ++lo) s = __fadd_rn(s, __ldg(val + lo));
-    return s;
-}
-
-// The values of ids id .. id + 3 with their biases added.
-__device__ __noinline__ float4 add_biases(float4 y, uint4 c, int id, const int32_t *tok, const float *val, int64_t n)
-{
-    if (c.x & kBias) y.x = __fadd_rn(y.x, bias_sum(id, tok, val, n));
-    if (c.y & kBias) y.y = __fadd_rn(y.y, bias_sum(id + 1, tok, val, n));
-    if (c.z & kBias) y.z = __fadd_rn(y.z, bias_sum(id + 2, tok, val, n));
-    if (c.w & kBias) y.w = __fadd_rn(y.w, bias_sum(id + 3, tok, val, n));
-    return y;
-}
-
-// One row's tile: where it is and what its mask is.
-template <bool BF16> struct Row {
-    const unsigned char *in;  // its ids from lo on
-    float *out;
-    const uint32_t *mask;     // the word of id lo (lo is a multiple of 32), or null: all allowed
-    bool none;                // no id allowed
-    bool vec;                 // groups of four ids on 16 bytes (8 of bf16)
-
-    // a: the row's entry of allow_row
-    __device__ __forceinline__ Row(const LParams &p, int64_t row, int lo, int a)
-    {
-        in = static_cast<const unsigned char *>(p.logits) + (row * p.stride + lo) * (BF16 ? 2 : 4);
-        out = p.out + row * p.out_stride + lo;
-        mask = nullptr;
-        none = false;
-        if (p.r.allow) {
-            if (a >= 0 && a < p.r.n_allow) {
-                mask = p.r.allow + (int64_t)a * p.words + (lo >> 5);
-            } else if (a != -1) {  // a mask row that is not there allows nothing
-                none = true;
-                if (p.status && threadIdx.x == 0) atomicOr(p.status, RX_DEV_BAD_STATE);
-            }
-        }
-        vec = (reinterpret_cast<uintptr_t>(in) & (BF16 ? 7 : 15)) == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
-    }
-    // bit k: id i + k is allowed (i a multiple of four, or one id)
-    __device__ __forceinline__ uint32_t allowed(int i) const
-    {
-        if (none) return 0u;
-        return mask ? __ldg(mask + (i >> 5)) >> (i & 31) : 15u;
-    }
-    // plain loads: out may be logits
-    __device__ __forceinline__ float one(int i) const
-    {
-        return BF16 ? __bfloat162float(reinterpret_cast<const bf16 *>(in)[i]) : reinterpret_cast<const float *>(in)[i];
-    }
-};
-
 // Grid: x = tiles, y = requests, z = shares of a request's rows.  IN_PLACE: out
 // is logits.
 template <bool BF16, bool IN_PLACE>
@@ -199,6 +149,7 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const __grid_consta
 {
     extern __shared__ __align__(16) uint32_t table[];                // [tile] words
     uint8_t *prompt = reinterpret_cast<uint8_t *>(table + tile);    // [tile] the id is in the prompt
+    float *bias = reinterpret_cast<float *>(prompt + tile);         // [tile] the sum of its biases, where it has some
     const rx_logits_rules &r = p.r;
     const int b = blockIdx.y, lo = (int)blockIdx.x * tile, n = min(r.vocab - lo, tile);
     Request q;
@@ -208,35 +159,59 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const __grid_consta
     const int i0 = 4 * threadIdx.x, step = (int)gridDim.z;
     using Raw = std::conditional_t<BF16, uint2, float4>;
     Raw x[kVecs];
-    uint32_t m = 0;      // bits 4 u ..: the allowed ids of group u
     uint32_t hot = 0;    // bit u: group u has an id whose word is not 0
-    auto masks = [&](const Row<BF16> &w) {
-        uint32_t word[kVecs], to = 0;
+    // the tile of the request's row k
+    auto in = [&](int k) {
+        return static_cast<const unsigned char *>(p.logits) + ((int64_t)(q.row0 + k) * p.stride + lo) * (BF16 ? 2 : 4);
+    };
+    auto out = [&](int k) { return p.out + (int64_t)(q.row0 + k) * p.out_stride + lo; };
+    // its groups of four start on 16 bytes (8 of bf16)
+    auto aligned = [&](int k) {
+        return (reinterpret_cast<uintptr_t>(in(k)) & (BF16 ? 7 : 15)) == 0 && (reinterpret_cast<uintptr_t>(out(k)) & 15) == 0;
+    };
+    auto one = [&](int k, int i) {  // a plain load: out may be logits
+        return BF16 ? __bfloat162float(reinterpret_cast<const bf16 *>(in(k))[i]) : reinterpret_cast<const float *>(in(k))[i];
+    };
+    // row k's mask: its entry of allow_row (-1: all ids; a row that is not there
+    // allows none), from which the words of this thread's groups, from which
+    // bits 4 u ..: the allowed ids of group u
+    auto mask_row = [&](int k) { return r.allow && k < q.tree ? __ldg(r.allow_row + q.row0 + k) : -1; };
+    auto mask_word = [&](int a, int i) {
+        if (a >= 0 && a < r.n_allow) return __ldg(r.allow + (int64_t)a * p.words + ((lo + i) >> 5));
+        return a == -1 ? ~0u : 0u;
+    };
+    auto mask_words = [&](int a, uint32_t (&w)[kVecs]) {
 #pragma unroll
         for (int u = 0; u < kVecs; ++u) {
             const int i = i0 + 4 * kThreads * u;
-            word[u] = i + 4 <= n ? w.allowed(i) & 15u : 0u;
+            w[u] = i + 4 <= n ? mask_word(a, i) : 0u;
         }
+    };
+    auto pack = [&](const uint32_t (&w)[kVecs]) {
+        uint32_t m = 0;
 #pragma unroll
-        for (int u = 0; u < kVecs; ++u) to |= word[u] << (4 * u);
-        return to;
+        for (int u = 0; u < kVecs; ++u) m |= (w[u] >> (i0 & 31) & 15u) << (4 * u);
+        return m;
     };
-    auto fetch = [&](const Row<BF16> &w, uint32_t to, int u) {
-        to = to >> (4 * u) & 15u;
+    auto fetch = [&](int k, bool vec, uint32_t m, int u) {
+        m = m >> (4 * u) & 15u;
         x[u] = {};
-        if (w.vec && to != 0u && (!IN_PLACE || to != 15u || ((hot >> u) & 1u)))
-            x[u] = *reinterpret_cast<const Raw *>(w.in + (BF16 ? 2 : 4) * (i0 + 4 * kThreads * u));
+        if (vec && m != 0u && (!IN_PLACE || m != 15u || ((hot >> u) & 1u)))
+            x[u] = *reinterpret_cast<const Raw *>(in(k) + (BF16 ? 2 : 4) * (i0 + 4 * kThreads * u));
     };
-    auto mask_row = [&](int k) { return r.allow && k < q.tree ? __ldg(r.allow_row + q.row0 + k) : -1; };
     int k = blockIdx.z;
     if (k >= q.tree) return;
-    Row<BF16> w(p, (int64_t)q.row0 + k, lo, mask_row(k));
-    m = masks(w);
+    // rows ahead: entries of allow_row three, mask words two, logits one
+    int a0 = mask_row(k), a1 = mask_row(k + step), a2 = mask_row(k + 2 * step);
+    uint32_t word[kVecs];
+    mask_words(a0, word);
+    uint32_t m = pack(word);
+    bool vec = aligned(k);
     if (!IN_PLACE) {
 #pragma unroll
-        for (int u = 0; u < kVecs; ++u) fetch(w, m, u);
+        for (int u = 0; u < kVecs; ++u) fetch(k, vec, m, u);
     }
-    int a = mask_row(k + step);  // of the row after this one
+    mask_words(a1, word);
 
     // this thread's drafted tokens (threadIdx.x and the one kThreads behind): their places in the tile
     static_assert(kMaxPath <= 2 * kThreads, "drafted tokens of a thread");
@@ -246,6 +221,9 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const __grid_consta
         for (int i = threadIdx.x; i < tile / 4; i += kThreads) reinterpret_cast<uint4 *>(table)[i] = make_uint4(0, 0, 0, 0);
         for (int i = threadIdx.x; i < tile / 16; i += kThreads) reinterpret_cast<uint4 *>(prompt)[i] = make_uint4(0, 0, 0, 0);
         __syncthreads();
+        // the biases' ids, this one's and its neighbours' (-1: there is none)
+        auto id_at = [&](int64_t i) { return i >= 0 && i < q.nbias ? __ldg(r.bias_tok + q.bias0 + i) : -1; };
+        int t = id_at(threadIdx.x), before = id_at((int64_t)threadIdx.x - 1), next = id_at((int64_t)threadIdx.x + 1);
         // ids outside the vocabulary are reported by the first tile
         const bool first = lo == 0 && blockIdx.z == 0;
         bool bad = false;
@@ -294,15 +272,22 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const __grid_consta
                 if (d < (uint32_t)n) atomicAdd(table + d, 1u);
             });
         }
-        auto mark = [&](int t, uint32_t bit) {
-            const uint32_t d = (uint32_t)t - (uint32_t)lo;
-            if (d < (uint32_t)n) atomicOr(table + d, bit);
-            bad |= (uint32_t)t >= (uint32_t)r.vocab;
-        };
         for (int64_t i = threadIdx.x; i < q.nbias; i += kThreads) {
-            const int t = __ldg(r.bias_tok + q.bias0 + i);
-            bad |= i > 0 && __ldg(r.bias_tok + q.bias0 + i - 1) > t;
-            mark(t, kBias);
+            if (i >= kThreads) {
+                t = id_at(i);
+                before = id_at(i - 1);
+                next = id_at(i + 1);
+            }
+            bad |= (i > 0 && before > t) || (uint32_t)t >= (uint32_t)r.vocab;
+            const uint32_t d = (uint32_t)t - (uint32_t)lo;
+            if (d >= (uint32_t)n || (i > 0 && before == t)) continue;
+            float sum = __ldg(r.bias_val + q.bias0 + i);
+            for (int64_t j = i + 1; next == t; ++j) {  // the same id again
+                sum = __fadd_rn(sum, __ldg(r.bias_val + q.bias0 + j));
+                next = id_at(j + 1);
+            }
+            bias[d] = sum;
+            atomicOr(table + d, kBias);
         }
         if (r.draft_tok) {
 #pragma unroll
@@ -336,51 +321,64 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const __grid_consta
             }
             if (v.x | v.y | v.z | v.w) hot |= 1u << u;
         }
-        if (paths || !w.vec || (n & 3)) __syncthreads();  // single ids' words are read by other threads
+        __syncthreads();  // single ids' words are read by other threads
     }
     if (IN_PLACE) {
 #pragma unroll
-        for (int u = 0; u < kVecs; ++u) fetch(w, m, u);
+        for (int u = 0; u < kVecs; ++u) fetch(k, vec, m, u);
     }
+    uint32_t ahead = pack(word);
     // the values of ids i .. i + 3 of the tile with words c
     auto process = [&](float4 v, uint4 c, int i) {
-        // the quotients' range: of the positive values the largest and the smallest
+        // the quotients' range: the largest value, and the least bits (the
+        // positive values'; a zero takes the general division)
         const float top = fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w));
-        const float low = fminf(fminf(v.x > 0.f ? v.x : 1.f, v.y > 0.f ? v.y : 1.f),
-                                fminf(v.z > 0.f ? v.z : 1.f, v.w > 0.f ? v.w : 1.f));
-        float4 d = make_float4(q.divide(v.x), q.divide(v.y), q.divide(v.z), q.divide(v.w));
-        if (!(q.plain_rep && top <= 0x1p40f && low >= 0x1p-40f)) d = divide_any(v, q.rep);
-        v = make_float4(q.penalised(v.x, d.x, c.x), q.penalised(v.y, d.y, c.y), q.penalised(v.z, d.z, c.z),
-                        q.penalised(v.w, d.w, c.w));
-        if ((c.x | c.y | c.z | c.w) & kBias) v = add_biases(v, c, lo + i, r.bias_tok + q.bias0, r.bias_val + q.bias0, q.nbias);
+        const uint32_t low = min(min(__float_as_uint(v.x), __float_as_uint(v.y)), min(__float_as_uint(v.z), __float_as_uint(v.w)));
+        float4 d;
+        rx::f2_split(q.divide(rx::f2(v.x, v.y)), d.x, d.y);
+        rx::f2_split(q.divide(rx::f2(v.z, v.w)), d.z, d.w);
+        if (!(q.plain_rep && top <= 0x1p40f && low >= 0x2B800000u)) d = divide_any(v, q.rep);  // 2^-40
+        q.penalise(v.x, v.y, d.x, d.y, c.x, c.y);
+        q.penalise(v.z, v.w, d.z, d.w, c.z, c.w);
+        if ((c.x | c.y | c.z | c.w) & kBias) {
+            if (c.x & kBias) v.x = __fadd_rn(v.x, bias[i]);
+            if (c.y & kBias) v.y = __fadd_rn(v.y, bias[i + 1]);
+            if (c.z & kBias) v.z = __fadd_rn(v.z, bias[i + 2]);
+            if (c.w & kBias) v.w = __fadd_rn(v.w, bias[i + 3]);
+        }
         return v;
     };
-    // the drafted tokens on node k's path, counted in (1) or out (-1) of the words
-    auto path = [&](int node, uint32_t by) {
+    // which of this thread's drafted tokens are on row k's path: its mask words
+    // (of the row after the one at hand, so that nobody waits for them)
+    uint32_t path[2];
+    auto path_words = [&](int k) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int at = (int)threadIdx.x + j * kThreads;
-            if (drafted[j] < 0) continue;
-            const bool on = r.tree_mask ? (__ldg(r.tree_mask + (int64_t)(q.row0 + node) * r.tree_words + (at >> 5)) >> (at & 31)) & 1u
-                                        : at <= node;
-            if (on) atomicAdd(table + drafted[j], by);
+            path[j] = 0;
+            if (drafted[j] < 0 || k >= q.tree) continue;
+            if (r.tree_mask) path[j] = __ldg(r.tree_mask + (int64_t)(q.row0 + k) * r.tree_words + (at >> 5));
+            else path[j] = at <= k ? ~0u : 0u;
         }
     };
+    bool counted[2] = {false, false};  // the token is counted in its word
+    if (paths) path_words(k);
     for (;;) {
-        const Row<BF16> now = w;
-        const int node = k;
-        if (paths) {
-            path(node, 1u);
+        if (a0 != -1 && (a0 < 0 || a0 >= r.n_allow) && threadIdx.x == 0 && p.status) atomicOr(p.status, RX_DEV_BAD_STATE);
+        if (paths) {  // the words of the path's tokens
+            __syncthreads();  // the row before has been worked off
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const bool on = (path[j] >> (threadIdx.x & 31)) & 1u;
+                if (on != counted[j]) atomicAdd(table + drafted[j], on ? 1u : ~0u);
+                counted[j] = on;
+            }
             __syncthreads();
+            path_words(k + step);
         }
-        k += step;
-        const bool more = k < q.tree;
-        uint32_t ahead = 0;
-        if (more) {
-            w = Row<BF16>(p, (int64_t)q.row0 + k, lo, a);
-            a = mask_row(k + step);
-            ahead = masks(w);
-        }
+        const bool more = k + step < q.tree, vec1 = more && aligned(k + step);
+        mask_words(a2, word);
+        const int a3 = mask_row(k + 3 * step);
 #pragma unroll
         for (int u = 0; u < kVecs; ++u) {
             const int i = i0 + 4 * kThreads * u;
@@ -391,33 +389,33 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const __grid_consta
             else
                 v = x[u];
             const uint32_t mu = m >> (4 * u) & 15u;
-            if (mu != 0u && ((hot >> u) & 1u)) {
-                const uint4 c = reinterpret_cast<const uint4 *>(table)[threadIdx.x + kThreads * u];
-                v = process(v, c, i);
-            }
-            if (now.vec && i + 4 <= n && (!IN_PLACE || mu != 15u || ((hot >> u) & 1u)))
-                *reinterpret_cast<float4 *>(now.out + i) =
+            const bool touches = (hot >> u) & 1u;
+            if (mu != 0u && touches) v = process(v, reinterpret_cast<const uint4 *>(table)[threadIdx.x + kThreads * u], i);
+            if (vec && i + 4 <= n && (!IN_PLACE || mu != 15u || touches))
+                *reinterpret_cast<float4 *>(out(k) + i) =
                     make_float4(mu & 1u ? v.x : -INFINITY, mu & 2u ? v.y : -INFINITY, mu & 4u ? v.z : -INFINITY,
                                 mu & 8u ? v.w : -INFINITY);
-            if (more) fetch(w, ahead, u);
+            fetch(k + step, vec1, ahead, u);
         }
-        m = ahead;
         // single ids: the rest behind the last four, or the whole of a row that is not aligned
-        for (int i = (now.vec ? n / 4 * 4 : 0) + (int)threadIdx.x; i < n; i += kThreads) {
-            const bool ok = now.allowed(i) & 1u;
+        for (int i = (vec ? n / 4 * 4 : 0) + (int)threadIdx.x; i < n; i += kThreads) {
+            const bool ok = mask_word(a0, i) >> (i & 31) & 1u;
             const uint32_t c = listed ? table[i] : 0u;
             float y = -INFINITY;
             if (ok && (!IN_PLACE || c)) {
-                y = now.one(i);
+                y = one(k, i);
                 if (c) y = process(make_float4(y, 1.f, 1.f, 1.f), make_uint4(c, 0u, 0u, 0u), i).x;
             }
-            if (!IN_PLACE || c || !ok) now.out[i] = y;
-        }
-        if (paths) {
-            __syncthreads();
-            path(node, ~0u);
+            if (!IN_PLACE || c || !ok) out(k)[i] = y;
         }
         if (!more) return;
+        k += step;
+        vec = vec1;
+        m = ahead;
+        ahead = pack(word);
+        a0 = a1;
+        a1 = a2;
+        a2 = a3;
     }
 }
 
@@ -475,11 +473,12 @@ extern "C" int rx_logits_process(const rx_logits_rules *rules, const void *logit
     const int64_t tiles = (r.vocab + (int64_t)tile - 1) / tile;
     // four CTAs an SM (two at a time): with fewer, a request's rows are dealt out
     // to several, which all count.  16 requests of 8 to 16 rows of 128,256 ids:
-    // 66 us with 1 share, 60 with 2, 62 with 3 and with 4
+    // 60 us with 1 share, 57 with 2, 59 with 3, 61 with 4
     const int64_t shares = std::max<int64_t>(1, std::min<int64_t>(4 * logits_num_sms() / (tiles * r.n_req), rows));
-    const size_t smem = (size_t)tile * (touched ? 5 : 0);
+    const size_t smem = (size_t)tile * (r.bias_ptr ? 9 : touched ? 5 : 0);
     auto kernel = in_place ? logits_kernel<false, true> : logits_bf16 ? logits_kernel<true, false> : logits_kernel<false, false>;
-    static_assert(kTile * 5 <= 48 * 1024, "shared memory of an ordinary launch");
+    // per device and function; cheap, and right whichever device is current
+    if (smem > 48 * 1024) RX_CUDA_CHECK(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
     kernel<<<dim3((unsigned)tiles, (unsigned)r.n_req, (unsigned)shares), kThreads, smem, st>>>(p, tile, touched);
     RX_CUDA_CHECK(cudaGetLastError());
     return RX_OK;
