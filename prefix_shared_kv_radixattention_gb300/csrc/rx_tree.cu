@@ -40,9 +40,10 @@
 // 212 us (149 us of bytes; four of a tile's 128 rows are used, and a softmax
 // warp takes 2,300 cycles for a tile however few rows it has); E4M3 pools, 16 of
 // up to 32,768, 32/8 heads, 301 us (119 us of bytes: the softmax warps' 3,500
-// cycles a tile, two of the four with rows; a part of the exponentials on the
-// multiply-add units made the tile slower, 368 us: it is their issue, not the
-// exp unit, that counts); trees of
+// cycles a tile, two of the four with rows, with the producers' 2,500 close
+// behind; a part of the exponentials on the multiply-add units, 368 us, or the
+// rows put in twice and a tile's positions shared between the copies, 382 us,
+// were no faster: the SM's issue slots are what they share); trees of
 // 64 tokens, 64/8 heads, 8 requests, 123 us (42 us of tensor-core time: 4,000
 // cycles for two row tiles, half of them the softmax, a quarter its waits for
 // S); one request of 333 positions 16.5 us, of it 2 x 2 us of launches, 3,500
