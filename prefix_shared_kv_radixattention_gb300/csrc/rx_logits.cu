@@ -22,9 +22,10 @@
 //
 // So the rows move once, in whole sectors.  What bounds it is the instructions:
 // 192 drafted rows of 128,256 bf16 logits over 32,768 tokens a request take 56
-// us (2.9 times the 20 us of their bytes) and 32 million warp instructions at
+// us (2.9 times the 20 us of their bytes) and 34 million warp instructions at
 // 2.4 a cycle, a quarter of them the counting, which every tile's CTA does for
-// all of the tokens, the rest some 90 for a warp's 128 ids.  64 rows of fp32
+// all of the tokens, the rest some 130 for a warp's 128 ids (the touched ones of
+// a group one after the other: 69 us).  64 rows of fp32
 // logits take 34 us, where the chain of loads and barriers before the first
 // row (14,000 cycles of a CTA's 18,000) counts, one row of 32,000 ids 6.7 us.
 //
