@@ -982,7 +982,6 @@ class LogitsRules:
             raise ValueError("LogitsRules: tree_mask must be [rows, words]")
         # rows the per-row tensors hold: rx_logits_process checks them against the logits
         self.row_tensors = [t for t in (draft_tok, tree_mask, allow_row) if t is not None]
-        self.has_rows = qo_indptr is not None
 
         def p(t):
             return None if t is None or t.numel() == 0 else t.data_ptr()

@@ -1269,9 +1269,20 @@ bool tree_shape_ok(int32_t batch, int32_t hq, int32_t hkv, int32_t D, int32_t ma
            (D == 64 || D == 128) && max_tree >= 1 && max_tree <= kMaxTree;
 }
 
+// The registers that the kernel is launched with: the shares of the roles are
+// granted out of them, and a share that is not there would be waited for.
+template <int D, bool F8, int NT>
+bool registers_ok()
+{
+    cudaFuncAttributes a;
+    return cudaFuncGetAttributes(&a, tree_kernel<D, F8, NT>) == cudaSuccess && a.numRegs >= Ro<NT>::R_LAUNCH;
+}
+
 template <int D, bool F8, int NT = 1>
 int launch(const TParams &p, cudaStream_t st)
 {
+    static const bool ok = registers_ok<D, F8, NT>();
+    if (!ok) return rx_set_error(RX_ERR_UNSUPPORTED, "tree attention: the kernel was built with too few registers");
     // per device; cheap, and right whichever device is current
     RX_CUDA_CHECK(cudaFuncSetAttribute(tree_kernel<D, F8, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (TL<D, F8>::BYTES)));
     tree_kernel<D, F8, NT><<<kCtas, Ro<NT>::THREADS, (TL<D, F8>::BYTES), st>>>(p);
