@@ -380,10 +380,9 @@ def _torch():
 
 
 def _dev(t, dtype, name):
-    torch = _torch()
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, _torch().Tensor) or not t.is_cuda:
         raise TypeError(f"{name}: expected a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
@@ -789,7 +788,7 @@ def rx_attn_decode_fp8(k_pool, v_pool, k_scale: float, v_scale: float, q, o, lse
 def _head_rows(t, name):
     """A CUDA bf16 [n, heads, d] tensor whose rows (all heads of a token) are
     contiguous; the rows themselves may be strided (a part of a projected
-    row).  Returns the row stride in elements."""
+    row).  Returns n, heads, d and the row stride in elements."""
     torch = _torch()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name}: expected a CUDA tensor")
@@ -800,31 +799,31 @@ def _head_rows(t, name):
     (n, h, d), (row, head, one) = t.shape, t.stride()
     if n and ((d > 1 and one != 1) or (h > 1 and head != d)):
         raise ValueError(f"{name}: must be [n, heads, head_dim] with contiguous rows")
-    return row if n > 1 else h * d
+    return n, h, d, row if n > 1 else h * d
 
 
 def _norm_args(k_pool, v_pool, q, q_out, k_new, v_new, q_weight, k_weight, slots, pos, dev_status):
     torch = _torch()
-    qs = _head_rows(q, "q")
-    ks, vs = _head_rows(k_new, "k_new"), _head_rows(v_new, "v_new")
-    _dev(q_out, torch.bfloat16, "q_out")
-    _dev(q_weight, torch.bfloat16, "q_weight")
-    _dev(k_weight, torch.bfloat16, "k_weight")
-    _dev(slots, torch.int32, "slots")
-    _dev(pos, torch.int32, "pos")
-    _dev(dev_status, torch.int32, "dev_status")
-    S, hkv, d, L = _pool_dims(k_pool, v_pool, 0)
-    n = slots.numel()
-    if k_new.shape != (n, hkv, d) or v_new.shape != k_new.shape or pos.numel() != n:
+    bf16, i32 = torch.bfloat16, torch.int32
+    n, hq, d, qs = _head_rows(q, "q")
+    new, v_row = _head_rows(k_new, "k_new"), _head_rows(v_new, "v_new")
+    _dev(q_out, bf16, "q_out")
+    _dev(q_weight, bf16, "q_weight")
+    _dev(k_weight, bf16, "k_weight")
+    _dev(slots, i32, "slots")
+    _dev(pos, i32, "pos")
+    _dev(dev_status, i32, "dev_status")
+    S, hkv, dim, L = _pool_dims(k_pool, v_pool, 0)
+    if new[:3] != (slots.numel(), hkv, dim) or v_row[:3] != new[:3] or pos.numel() != new[0]:
         raise ValueError("k_new/v_new must be [n, num_kv_heads, head_dim] and pos [n]")
-    if q.shape[0] != n or q.shape[2] != d or q_out.shape != q.shape:
+    if n != new[0] or d != dim or q_out.shape != q.shape:
         raise ValueError("q and q_out must be [n, num_q_heads, head_dim]")
-    if ks != vs:
+    if new[3] != v_row[3]:
         raise ValueError("k_new and v_new must have the same row stride")
     for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if w is not None and w.numel() != d:
             raise ValueError(f"{name} must be [head_dim]")
-    return qs, ks, n, S, hkv, d, L
+    return qs, new[3], n, hq, S, hkv, d, L
 
 
 def rx_qk_norm_rope_store(k_pool, v_pool, q, q_out, k_new, v_new, q_weight, k_weight, slots, pos, base: float,
@@ -832,10 +831,14 @@ def rx_qk_norm_rope_store(k_pool, v_pool, q, q_out, k_new, v_new, q_weight, k_we
     """RMS norm of every q and k head (weights bf16 [d] or None), rotation to
     pos, q into q_out, K and V into the pool.  q, k_new, v_new: bf16 [n,
     heads, d], for example the three parts of one projected row."""
-    pool = make_pool(k_pool, v_pool, layer)
-    qs, ks, n, *_ = _norm_args(k_pool, v_pool, q, q_out, k_new, v_new, q_weight, k_weight, slots, pos, dev_status)
+    torch = _torch()
+    _dev(k_pool, torch.bfloat16, "k_pool")
+    _dev(v_pool, torch.bfloat16, "v_pool")
+    qs, ks, n, hq, S, hkv, d, L = _norm_args(k_pool, v_pool, q, q_out, k_new, v_new, q_weight, k_weight, slots, pos,
+                                             dev_status)
+    pool = KVPool(k_pool.data_ptr(), v_pool.data_ptr(), S, hkv, d, L, int(layer))
     _check(_lib.rx_qk_norm_rope_store(ctypes.byref(pool), _ptr(q), qs, _ptr(q_out), _ptr(k_new), _ptr(v_new), ks,
-                                      _ptr(q_weight), _ptr(k_weight), _ptr(slots), _ptr(pos), n, q.shape[1],
+                                      _ptr(q_weight), _ptr(k_weight), _ptr(slots), _ptr(pos), n, hq,
                                       float(base), float(eps), _ptr(dev_status), _stream(stream)))
 
 
@@ -847,11 +850,11 @@ def rx_qk_norm_rope_store_fp8(k_pool, v_pool, k_scale: float, v_scale: float, q,
     torch = _torch()
     _dev(k_pool, torch.uint8, "k_pool")
     _dev(v_pool, torch.uint8, "v_pool")
-    qs, ks, n, S, hkv, d, L = _norm_args(k_pool, v_pool, q, q_out, k_new, v_new, q_weight, k_weight, slots, pos,
-                                         dev_status)
+    qs, ks, n, hq, S, hkv, d, L = _norm_args(k_pool, v_pool, q, q_out, k_new, v_new, q_weight, k_weight, slots, pos,
+                                             dev_status)
     pool = KVPoolFp8(k_pool.data_ptr(), v_pool.data_ptr(), S, hkv, d, float(k_scale), float(v_scale), L, int(layer))
     _check(_lib.rx_qk_norm_rope_store_fp8(ctypes.byref(pool), _ptr(q), qs, _ptr(q_out), _ptr(k_new), _ptr(v_new), ks,
-                                          _ptr(q_weight), _ptr(k_weight), _ptr(slots), _ptr(pos), n, q.shape[1],
+                                          _ptr(q_weight), _ptr(k_weight), _ptr(slots), _ptr(pos), n, hq,
                                           float(base), float(eps), _ptr(dev_status), _stream(stream)))
 
 
@@ -877,16 +880,17 @@ def rx_attn_tree_workspace(batch: int, num_q_heads: int, num_kv_heads: int, head
 
 def _tree_args(q, o, lse, qo_indptr, req_idx, prefix_len, tree_mask, req_to_token, workspace, dev_status):
     torch = _torch()
+    i32 = torch.int32
     _dev(q, torch.bfloat16, "q")
     _dev(o, torch.bfloat16, "o")
     _dev(lse, torch.float32, "lse")
-    _dev(qo_indptr, torch.int32, "qo_indptr")
-    _dev(req_idx, torch.int32, "req_idx")
-    _dev(prefix_len, torch.int32, "prefix_len")
-    _dev(tree_mask, torch.int32, "tree_mask")
-    _dev(req_to_token, torch.int32, "req_to_token")
+    _dev(qo_indptr, i32, "qo_indptr")
+    _dev(req_idx, i32, "req_idx")
+    _dev(prefix_len, i32, "prefix_len")
+    _dev(tree_mask, i32, "tree_mask")
+    _dev(req_to_token, i32, "req_to_token")
     _dev(workspace, torch.uint8, "workspace")
-    _dev(dev_status, torch.int32, "dev_status")
+    _dev(dev_status, i32, "dev_status")
     if q.dim() != 3 or q.shape != o.shape:
         raise ValueError("q and o must be [tokens, num_q_heads, head_dim]")
     if lse is not None and lse.shape != q.shape[:2]:
