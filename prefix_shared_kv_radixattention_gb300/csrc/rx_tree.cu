@@ -52,6 +52,7 @@
 
 #include <algorithm>
 #include <climits>
+#include <type_traits>
 
 #include "rx_common.cuh"
 #include "rx_pipe.cuh"
@@ -109,8 +110,8 @@ struct Turn {
     __device__ __forceinline__ Turn(int t, int c) : b(NT == 1 ? c & 1 : t), phase(NT == 1 ? c >> 1 : c) {}
 };
 constexpr float kRescale = 8.f;      // log2 units the running max may lag
-constexpr int kMergeRows = 16;       // rows of one merge CTA
 constexpr int kMergeThreads = 128;
+constexpr int kMergeRows = kMergeThreads / 32;  // rows of one merge CTA
 
 // A segment: the position tiles [j0, j1) of a (kv head g, request, row tiles)
 // that are this CTA's.
@@ -1194,10 +1195,11 @@ __global__ void __launch_bounds__(Ro<NT>::THREADS, 1) tree_kernel(const __grid_c
 // joining the partial results
 // ---------------------------------------------------------------------------
 
-// The parts of cut x = blockIdx.x, one warp a row: with m the largest
-// log2-sum-exp, w = 2^(l - m): o = sum w o / sum w.  kMergeRows rows a CTA.
-// Finding the cuts here, by a scan of the lengths in every CTA, took longer than
-// joining them: 5 us more for eight trees of 64 tokens, 2.5 of 18.7 for one of 5.
+// The parts of cut x = blockIdx.x, a warp a row: with m the largest
+// log2-sum-exp, w = 2^(l - m): o = sum w o / sum w.  The first two parts'
+// results are on their way before it has their weights; with four rows a warp,
+// one after the other, the call for one small request took 17.5 us, with four
+// rows' loads together 16, with one row 13.
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_constant__ TParams p)
 {
@@ -1210,41 +1212,40 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
 
     constexpr int V = D / 32;  // values of a lane
     const int lane = threadIdx.x & 31;
-    for (int i = threadIdx.x >> 5; i < kMergeRows; i += kMergeThreads / 32) {
-        const int row = (int)blockIdx.y * kMergeRows + i;      // of the group's nt * 128
-        const int t = row / kRows, r = row % kRows;
-        if (t >= p.nt || r >= min(p.tb, c.ntok - t * p.tb) * p.G) continue;
-        auto at = [&](int s) { return (int64_t)(2 * (x0 + s) + (s == 0 ? 1 : 0)) * p.nt * kRows + row; };
-        float m = -INFINITY;
-        for (int s = lane; s < parts; s += 32) m = fmaxf(m, __ldcg(p.part_l + at(s)));
+    const int row = (int)blockIdx.y * kMergeRows + (int)(threadIdx.x >> 5);  // of the group's nt * 128
+    const int t = row / kRows, r = row % kRows;
+    if (t >= p.nt || r >= min(p.tb, c.ntok - t * p.tb) * p.G) return;
+    using Vec = std::conditional_t<V == 4, float4, float2>;
+    auto at = [&](int s) { return (int64_t)(2 * (x0 + s) + (s == 0 ? 1 : 0)) * p.nt * kRows + row; };
+    auto part = [&](int s) { return __ldcg(reinterpret_cast<const Vec *>(p.part_o + at(s) * D) + lane); };
+    const float l = lane < parts ? __ldcg(p.part_l + at(lane)) : -INFINITY;
+    const Vec v0 = part(0), v1 = part(1);
+    float m = l;
+    for (int s = lane + 32; s < parts; s += 32) m = fmaxf(m, __ldcg(p.part_l + at(s)));
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-        const float mu = m == -INFINITY ? 0.f : m;
-        float acc[V] = {}, tot = 0.f;
-#pragma unroll 4
-        for (int s = 0; s < parts; ++s) {
-            const float w = exp2f(__ldcg(p.part_l + at(s)) - mu);
-            const float *src = p.part_o + at(s) * D + lane * V;
-            tot += w;
-            if constexpr (V == 4) {
-                const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
-                acc[0] = fmaf(w, v.x, acc[0]);
-                acc[1] = fmaf(w, v.y, acc[1]);
-                acc[2] = fmaf(w, v.z, acc[2]);
-                acc[3] = fmaf(w, v.w, acc[3]);
-            } else {
-                const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
-                acc[0] = fmaf(w, v.x, acc[0]);
-                acc[1] = fmaf(w, v.y, acc[1]);
-            }
+    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    const float mu = m == -INFINITY ? 0.f : m;
+    float acc[V] = {}, tot = 0.f;
+    auto add = [&](float ls, const Vec &x) {
+        const float w = rx::fast_exp2(ls - mu);
+        tot += w;
+        acc[0] = fmaf(w, x.x, acc[0]);
+        acc[1] = fmaf(w, x.y, acc[1]);
+        if constexpr (V == 4) {
+            acc[2] = fmaf(w, x.z, acc[2]);
+            acc[3] = fmaf(w, x.w, acc[3]);
         }
-        const float inv = tot == 0.f ? 0.f : 1.f / tot;
-        const int64_t orow = ((int64_t)c.tok + t * p.tb + r / p.G) * p.hq + (int64_t)c.g * p.G + r % p.G;
-        uint32_t *dst = reinterpret_cast<uint32_t *>(p.o + orow * D + lane * V);
-        dst[0] = rx::pack_bf16(acc[0] * inv, acc[1] * inv);
-        if constexpr (V == 4) dst[1] = rx::pack_bf16(acc[2] * inv, acc[3] * inv);
-        if (p.lse && lane == 0) p.lse[orow] = tot == 0.f ? -INFINITY : (m + log2f(tot)) * rx::kLn2;
-    }
+    };
+    add(__shfl_sync(0xffffffffu, l, 0), v0);
+    add(__shfl_sync(0xffffffffu, l, 1), v1);
+#pragma unroll 4
+    for (int s = 2; s < parts; ++s) add(s < 32 ? __shfl_sync(0xffffffffu, l, s) : __ldcg(p.part_l + at(s)), part(s));
+    const float inv = tot == 0.f ? 0.f : 1.f / tot;
+    const int64_t orow = ((int64_t)c.tok + t * p.tb + r / p.G) * p.hq + (int64_t)c.g * p.G + r % p.G;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(p.o + orow * D + lane * V);
+    dst[0] = rx::pack_bf16(acc[0] * inv, acc[1] * inv);
+    if constexpr (V == 4) dst[1] = rx::pack_bf16(acc[2] * inv, acc[3] * inv);
+    if (p.lse && lane == 0) p.lse[orow] = tot == 0.f ? -INFINITY : (m + log2f(tot)) * rx::kLn2;
 }
 
 size_t part_bytes(int32_t nt, int32_t head_dim) { return (size_t)2 * kCtas * nt * kRows * head_dim * sizeof(float); }
