@@ -35,19 +35,19 @@
 // batch's lengths in shared memory finds its share.
 //
 // Measured, with what is left: 16 requests of up to 32,768 positions, 64/8
-// heads of 128, 234 us, 6.7 TB/s of the rows read (a shared prefix is read once
+// heads of 128, 229 us, 6.8 TB/s of the rows read (a shared prefix is read once
 // a request; read once in all it would be 164 us); 64 of 1,281, 32/32 heads,
-// 212 us (149 us of bytes; four of a tile's 128 rows are used, and a softmax
+// 211 us (149 us of bytes; four of a tile's 128 rows are used, and a softmax
 // warp takes 2,300 cycles for a tile however few rows it has); E4M3 pools, 16 of
-// up to 32,768, 32/8 heads, 301 us (119 us of bytes: the softmax warps' 3,500
+// up to 32,768, 32/8 heads, 295 us (119 us of bytes: the softmax warps' 3,500
 // cycles a tile, two of the four with rows, with the producers' 2,500 close
 // behind; a part of the exponentials on the multiply-add units, 368 us, or the
 // rows put in twice and a tile's positions shared between the copies, 382 us,
 // were no faster: the SM's issue slots are what they share); trees of
-// 64 tokens, 64/8 heads, 8 requests, 123 us (42 us of tensor-core time: 4,000
+// 64 tokens, 64/8 heads, 8 requests, 121 us (42 us of tensor-core time: 4,000
 // cycles for two row tiles, half of them the softmax, a quarter its waits for
-// S); one request of 333 positions 16.5 us, of it 2 x 2 us of launches, 3,500
-// cycles until the first scores, 3,000 at the segment's end, the merge.
+// S); one request of 333 positions 13 us: 3 until the roles start, 3.5 until the
+// first scores, 4 until the segment's end, 2 for the merge.
 #include <math.h>
 
 #include <algorithm>
@@ -1251,7 +1251,7 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
 size_t part_bytes(int32_t nt, int32_t head_dim) { return (size_t)2 * kCtas * nt * kRows * head_dim * sizeof(float); }
 
 // Row tiles that share a K/V tile: two where some tree may have more than one
-// (64-token trees over 64/8 heads, 8k contexts: 123 us, one at a time 134 us),
+// (64-token trees over 64/8 heads, 8k contexts: 121 us, one at a time 134 us),
 // and bf16 pools only (an FP8 tile has one query buffer).  The second brings
 // softmax warps of its own; one group for both took 133 us.
 int row_tiles(int32_t hq, int32_t hkv, int32_t max_tree) { return (int64_t)max_tree > kRows / (hq / hkv) ? kMaxNt : 1; }
