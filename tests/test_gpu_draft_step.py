@@ -291,3 +291,27 @@ def test_codes_are_those_of_the_slot_scatter(scale):
     rx.rx_qk_norm_rope_store_fp8(*pools[0], 1.0, scale, q, torch.empty_like(q), k, v, None, None, slots, slots, BASE, EPS)
     rx.rx_kv_store_fp8(*pools[1], 1.0, scale, k, v, slots)
     assert torch.equal(pools[0][1], pools[1][1])
+
+
+@pytest.mark.parametrize("f8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("hq,hkv,most", [(16, 1, 20), (4, 2, 6)], ids=["two_row_tiles", "one_row_tile"])
+def test_a_request_with_a_nan_value_leaves_the_next_ones_alone(hq, hkv, most, f8):
+    """Many requests a CTA, every third with a NaN V at its last drafted token,
+    which only that token sees."""
+    from tests.test_gpu_draft_tree import Run
+    rng = np.random.default_rng(8)
+    B = 700
+    trees = [int(t) for t in rng.integers(1, most + 1, B)]
+    prefixes = [int(p) for p in rng.integers(0, 150, B)]
+    b = _draft.TreeBatch(9, hq, hkv, 64, prefixes, trees, masks="chain")
+    ref = Run(b, f8).reference()
+    last = b.indptr[1:] - 1
+    bad = last[::3]
+    for i in range(0, B, 3):
+        b.v[b.rtt[b.req_idx[i], prefixes[i] + trees[i] - 1]] = np.nan
+    r = Run(b, f8)
+    o, lse = r()
+    assert int(r.status.item()) == 0
+    keep = np.setdiff1d(np.arange(int(b.indptr[-1])), bad)
+    _draft.check_tree(o[keep], lse[keep], tuple(x[keep] for x in ref), "the others")
+    assert np.isnan(o[bad]).all()
