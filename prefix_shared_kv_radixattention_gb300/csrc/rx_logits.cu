@@ -75,6 +75,7 @@ struct Request {
     bool penal;              // any of them does anything
     int64_t bias0, nbias;
     int64_t hist0, nhist;
+    int prompt;              // of them the prompt's
 
     __device__ __forceinline__ bool load(const LParams &p, int b)
     {
@@ -94,6 +95,7 @@ struct Request {
         nbias = r.bias_ptr ? __ldg(r.bias_ptr + b + 1) - bias0 : 0;
         hist0 = r.hist ? __ldg(r.hist_ptr + b) : 0;
         nhist = r.hist ? __ldg(r.hist_ptr + b + 1) - hist0 : 0;
+        prompt = r.prompt_len ? __ldg(r.prompt_len + b) : 0;
         penal = rep != 1.f || freq != 0.f || pres != 0.f;
         tree = row1 - row0;
         if (row0 >= 0 && tree >= 0 && row1 <= p.rows && nhist >= 0 && nhist <= (int64_t)kCount - kMaxPath && nbias >= 0 &&
@@ -205,74 +207,88 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const __grid_consta
     // rows ahead: entries of allow_row three, mask words two, logits one
     int a0 = mask_row(k), a1 = mask_row(k + step), a2 = mask_row(k + 2 * step);
     uint32_t word[kVecs];
-    mask_words(a0, word);
-    uint32_t m = pack(word);
-    bool vec = aligned(k);
-    if (!IN_PLACE) {
-#pragma unroll
-        for (int u = 0; u < kVecs; ++u) fetch(k, vec, m, u);
-    }
-    mask_words(a1, word);
+    const bool vec0 = aligned(k);
 
     // this thread's drafted tokens (threadIdx.x and the one kThreads behind): their places in the tile
     static_assert(kMaxPath <= 2 * kThreads, "drafted tokens of a thread");
     int drafted[2] = {-1, -1};
     bool paths = false;
+    // the biases' ids: this thread's first and its neighbours' (-1: there is none)
+    auto id_at = [&](int64_t i) { return i >= 0 && i < q.nbias ? __ldg(r.bias_tok + q.bias0 + i) : -1; };
+    int t = -1, before = -1, next = -1;
     if (listed) {
         for (int i = threadIdx.x; i < tile / 4; i += kThreads) reinterpret_cast<uint4 *>(table)[i] = make_uint4(0, 0, 0, 0);
         for (int i = threadIdx.x; i < tile / 16; i += kThreads) reinterpret_cast<uint4 *>(prompt)[i] = make_uint4(0, 0, 0, 0);
+        t = id_at(threadIdx.x);
+        before = id_at((int64_t)threadIdx.x - 1);
+        next = id_at((int64_t)threadIdx.x + 1);
+    }
+    mask_words(a0, word);
+    // ids outside the vocabulary are reported by the first tile
+    const bool first = lo == 0 && blockIdx.z == 0;
+    bool bad = false;
+    if (listed) {
         __syncthreads();
-        // the biases' ids, this one's and its neighbours' (-1: there is none)
-        auto id_at = [&](int64_t i) { return i >= 0 && i < q.nbias ? __ldg(r.bias_tok + q.bias0 + i) : -1; };
-        int t = id_at(threadIdx.x), before = id_at((int64_t)threadIdx.x - 1), next = id_at((int64_t)threadIdx.x + 1);
-        // ids outside the vocabulary are reported by the first tile
-        const bool first = lo == 0 && blockIdx.z == 0;
-        bool bad = false;
-        // f(t) for the tokens [from, to) of the request: single ones up to a
-        // 16-byte boundary, four at a time, the rest
-        auto tokens = [&](int from, int to, auto f) {
-            const int32_t *h = r.hist + q.hist0 + from;
-            const int len = to - from;
-            if (len <= 0) return;
-            const int head = min(len, (int)((16 - (reinterpret_cast<uintptr_t>(h) & 15)) >> 2 & 3)), n4 = (len - head) / 4;
-            const int4 *h4 = reinterpret_cast<const int4 *>(h + head);
-            constexpr int U = 4;
-            int i = threadIdx.x;
-            for (; i + (U - 1) * kThreads < n4; i += U * kThreads) {
-                int4 t[U];
+        const int32_t *h = r.hist + q.hist0;
+        const uint32_t ids = q.penal ? (uint32_t)n : 0u;
+        const int len = q.penal || first ? (int)q.nhist : 0;  // neutral penalties: only the check of the ids
+        // a prompt's token needs no more than a mark
+        auto mark = [&](int t) {
+            const uint32_t d = (uint32_t)t - (uint32_t)lo;
+            if (d < ids) prompt[d] = 1;
+        };
+        auto count = [&](int t) {
+            const uint32_t d = (uint32_t)t - (uint32_t)lo;
+            if (d < ids) atomicAdd(table + d, 1u);
+        };
+        auto token = [&](int t, int i) {
+            if (first) bad |= (uint32_t)t >= (uint32_t)r.vocab;
+            if (i < q.prompt) mark(t);
+            else count(t);
+        };
+        // single tokens up to a 16-byte boundary, four at a time, the rest
+        const int head = min(len, (int)((16 - (reinterpret_cast<uintptr_t>(h) & 15)) >> 2 & 3)), n4 = (len - head) / 4;
+        const int4 *h4 = reinterpret_cast<const int4 *>(h + head);
+        constexpr int U = 4;
+        for (int i = threadIdx.x; i < n4; i += U * kThreads) {
+            int4 x[U];
 #pragma unroll
-                for (int u = 0; u < U; ++u) t[u] = __ldg(h4 + i + u * kThreads);
+            for (int u = 0; u < U; ++u)
+                if (i + u * kThreads < n4) x[u] = __ldg(h4 + i + u * kThreads);
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    f(t[u].x);
-                    f(t[u].y);
-                    f(t[u].z);
-                    f(t[u].w);
+            for (int u = 0; u < U; ++u) {
+                if (i + u * kThreads >= n4) break;
+                const int at = head + 4 * (i + u * kThreads);
+                if (!first && at + 3 < q.prompt) {
+                    mark(x[u].x);
+                    mark(x[u].y);
+                    mark(x[u].z);
+                    mark(x[u].w);
+                } else if (!first && at >= q.prompt) {
+                    count(x[u].x);
+                    count(x[u].y);
+                    count(x[u].z);
+                    count(x[u].w);
+                } else {
+                    token(x[u].x, at);
+                    token(x[u].y, at + 1);
+                    token(x[u].z, at + 2);
+                    token(x[u].w, at + 3);
                 }
             }
-            for (; i < n4; i += kThreads) {
-                const int4 t = __ldg(h4 + i);
-                f(t.x);
-                f(t.y);
-                f(t.z);
-                f(t.w);
-            }
-            // at most three before the first four and three behind the last
-            const int at = (int)threadIdx.x < head ? threadIdx.x : 4 * n4 + (int)threadIdx.x;
-            if (threadIdx.x < 8 && at < len) f(__ldg(h + at));
-        };
-        const int len = (int)q.nhist, np = r.prompt_len && r.hist ? min(max(__ldg(r.prompt_len + b), 0), len) : 0;
-        if (first) tokens(0, len, [&](int t) { bad |= (uint32_t)t >= (uint32_t)r.vocab; });
-        if (q.penal) {
-            tokens(0, np, [&](int t) {
-                const uint32_t d = (uint32_t)t - (uint32_t)lo;
-                if (d < (uint32_t)n) prompt[d] = 1;
-            });
-            tokens(np, len, [&](int t) {
-                const uint32_t d = (uint32_t)t - (uint32_t)lo;
-                if (d < (uint32_t)n) atomicAdd(table + d, 1u);
-            });
         }
+        // at most three before the first four and three behind the last
+        const int at = (int)threadIdx.x < head ? threadIdx.x : 4 * n4 + (int)threadIdx.x;
+        if (threadIdx.x < 8 && at < len) token(__ldg(h + at), at);
+    }
+    uint32_t m = pack(word);
+    bool vec = vec0;
+    if (!IN_PLACE) {
+#pragma unroll
+        for (int u = 0; u < kVecs; ++u) fetch(k, vec, m, u);
+    }
+    mask_words(a1, word);
+    if (listed) {
         for (int64_t i = threadIdx.x; i < q.nbias; i += kThreads) {
             if (i >= kThreads) {
                 t = id_at(i);
