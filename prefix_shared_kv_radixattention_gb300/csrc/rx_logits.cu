@@ -21,13 +21,13 @@
 //     row's logits are on their way meanwhile.
 //
 // So the rows move once, in whole sectors.  What bounds it is the instructions:
-// 192 drafted rows of 128,256 bf16 logits over 32,768 tokens a request take 56
-// us (2.9 times the 20 us of their bytes) and 34 million warp instructions at
+// 192 drafted rows of 128,256 bf16 logits over 32,768 tokens a request take 55
+// us (2.8 times the 20 us of their bytes) and 34 million warp instructions at
 // 2.4 a cycle, a quarter of them the counting, which every tile's CTA does for
 // all of the tokens, the rest some 130 for a warp's 128 ids (the touched ones of
-// a group one after the other: 69 us).  64 rows of fp32
-// logits take 34 us, where the chain of loads and barriers before the first
-// row (14,000 cycles of a CTA's 18,000) counts, one row of 32,000 ids 6.7 us.
+// a group one after the other: 69 us).  64 rows of fp32 logits take 31 us, where
+// the chain of loads and barriers before the first row (two thirds of a CTA's
+// time) counts, one row of 32,000 ids 5.8 us.
 //
 // A copy of the rows followed by a kernel for the listed touched ids alone took
 // 92, 37 and 5.6 us: partial sectors, and the common tokens in a few CTAs.  The
@@ -490,7 +490,7 @@ extern "C" int rx_logits_process(const rx_logits_rules *rules, const void *logit
     const int64_t tiles = (r.vocab + (int64_t)tile - 1) / tile;
     // four CTAs an SM (two at a time): with fewer, a request's rows are dealt out
     // to several, which all count.  16 requests of 8 to 16 rows of 128,256 ids:
-    // 60 us with 1 share, 57 with 2, 59 with 3, 61 with 4
+    // 60 us with 1 share, 57 with 2, 59 with 3, 61 with 4 (55 with 2 since)
     const int64_t shares = std::max<int64_t>(1, std::min<int64_t>(4 * logits_num_sms() / (tiles * r.n_req), rows));
     const size_t smem = (size_t)tile * (r.bias_ptr ? 9 : touched ? 5 : 0);
     auto kernel = in_place ? logits_kernel<false, true> : logits_bf16 ? logits_kernel<true, false> : logits_kernel<false, false>;
