@@ -382,9 +382,9 @@ def _torch():
 def _dev(t, dtype, name):
     if t is None:
         return None
-    if not isinstance(t, _torch().Tensor) or not t.is_cuda:
+    if not isinstance(t, (_torch_module or _torch()).Tensor) or not t.is_cuda:
         raise TypeError(f"{name}: expected a CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
