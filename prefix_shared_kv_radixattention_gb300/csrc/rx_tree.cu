@@ -42,8 +42,9 @@
 // up to 32,768, 32/8 heads, 295 us (119 us of bytes: the softmax warps' 3,500
 // cycles a tile, two of the four with rows, with the producers' 2,500 close
 // behind; a part of the exponentials on the multiply-add units, 368 us, or the
-// rows put in twice and a tile's positions shared between the copies, 382 us,
-// were no faster: the SM's issue slots are what they share); trees of
+// rows put in twice and the tiles' positions, 382 us, or the tiles, 325 us,
+// shared between the copies were no faster: the warps that got less to do took
+// as much longer for it, so it is the SM's units that are shared); trees of
 // 64 tokens, 64/8 heads, 8 requests, 121 us (42 us of tensor-core time: 4,000
 // cycles for two row tiles, half of them the softmax, a quarter its waits for
 // S); one request of 333 positions 13 us: 3 until the roles start, 3.5 until the
