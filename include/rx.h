@@ -620,7 +620,10 @@ int rx_tree_mask_build(const int32_t *parent, int32_t n, int32_t words, uint32_t
  * where bit j of its mask row is set:
  *     o   = sum over seen j of softmax(s)_j V_j,   lse = log(sum exp(s_j)).
  * A token that sees nothing (no prefix, an empty mask row) gets o = 0 and
- * lse = -inf.  A position a token does not see takes no part in its result,
+ * lse = -inf.  Scores, maxima, sums and the output's accumulator are fp32; the
+ * softmax weights are rounded to bf16 for the product with V (as rx_attn_extend
+ * does, and over FP8 pools too), which is off by at most 2^-8 sum p |V|, and o
+ * is rounded once more.  A position a token does not see takes no part in its result,
  * whatever K and V hold there (NaN and infinities among it).
  *   q, o: device bf16 [qo_indptr[batch], num_q_heads, head_dim]; lse_or_null:
  *   device fp32 [.., num_q_heads] or NULL; qo_indptr: device int32 [batch+1];

@@ -130,6 +130,22 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
     return *reinterpret_cast<uint32_t *>(&v);
 }
 
+// Eight E4M3 codes (element 0 in the low byte) as eight bf16: every E4M3
+// value, subnormals included, is exact in f16 and in bf16, so the widening
+// through f16 is exact.
+__device__ __forceinline__ uint4 e4m3x8_to_bf16x8(uint2 c)
+{
+    const uint32_t w[2] = {c.x, c.y};
+    uint32_t r[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t h = e4m3x2_to_f16x2((uint16_t)(w[k >> 1] >> (16 * (k & 1))));
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+        r[k] = pack_bf16(f.x, f.y);
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
 // 16-byte read-only load that stays where it is written (the compiler may sink
 // a plain load past the waits that it is meant to overlap).
 __device__ __forceinline__ uint4 ld_stream(const void *p)

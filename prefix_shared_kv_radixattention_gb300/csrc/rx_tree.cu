@@ -422,17 +422,15 @@ __device__ __forceinline__ uint32_t mask_word(const uint32_t *row, int words, in
 // producer warps
 // ---------------------------------------------------------------------------
 
-// Which halves of a word are NaN or infinite (bf16 / f16 pairs): 0xFFFF masks.
-template <bool F8>
+// Which halves of a word are NaN or infinite (bf16 pairs): 0xFFFF masks.
 __device__ __forceinline__ uint32_t not_finite(uint32_t w)
 {
-    constexpr uint32_t E = F8 ? 0x7C00u : 0x7F80u;
+    constexpr uint32_t E = 0x7F80u;
     return ((w & E) == E ? 0xFFFFu : 0u) | ((w & (E << 16)) == (E << 16) ? 0xFFFF0000u : 0u);
 }
-template <bool F8>
 __device__ __forceinline__ bool drop_not_finite(uint4 &x)
 {
-    const uint32_t a = not_finite<F8>(x.x), b = not_finite<F8>(x.y), c = not_finite<F8>(x.z), d = not_finite<F8>(x.w);
+    const uint32_t a = not_finite(x.x), b = not_finite(x.y), c = not_finite(x.z), d = not_finite(x.w);
     x = make_uint4(x.x & ~a, x.y & ~b, x.z & ~c, x.w & ~d);
     return (a | b | c | d) != 0u;
 }
@@ -452,8 +450,8 @@ __device__ __forceinline__ uint4 widen_f16(uint32_t lo, uint32_t hi)
 //
 // bf16 pools: the copies land in the swizzled tile itself and report to its
 // barrier.  FP8 pools: they land in a ring of three half tiles of codes; each
-// thread widens the chunks that it copied (E4M3 to f16 is exact) and stores
-// them to the tile.
+// thread widens the chunks that it copied and stores them to the tile: K to
+// f16, V to bf16, as the weights are (both hold every E4M3 value).
 //
 // V at drafted positions is looked at before it is handed over: a NaN or
 // infinity there would reach rows that do not see the position (0 * inf), so it
@@ -536,7 +534,7 @@ __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
             const int r = r0 + u / CH * RPI + sub, e = t.rel() + r;
             uint4 *at = reinterpret_cast<uint4 *>(smem + off + sw128(r, CH * ch + u % CH, L::BLK));
             uint4 x = *at;
-            if (e >= 0 && drop_not_finite<F8>(x)) {
+            if (e >= 0 && drop_not_finite(x)) {
                 *at = x;
                 atomicOr(reinterpret_cast<uint32_t *>(smem + L::OFF_NF) + t.seg() * 32 + (e >> 5), 1u << (e & 31));
             }
@@ -589,7 +587,8 @@ __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
 #pragma unroll
             for (int u = 0; u < H; ++u) {
                 const uint4 x = *reinterpret_cast<const uint4 *>(smem + mine + buf * L::CODE + u * 512);
-                const uint4 a = widen_f16(x.x, x.y), b = widen_f16(x.z, x.w);
+                const uint4 a = IS_V ? rx::e4m3x8_to_bf16x8(make_uint2(x.x, x.y)) : widen_f16(x.x, x.y);
+                const uint4 b = IS_V ? rx::e4m3x8_to_bf16x8(make_uint2(x.z, x.w)) : widen_f16(x.z, x.w);
                 const int r = r0 + (h * H + u) * RPI + sub;
                 // the upper lanes of a row store their second chunk first: the
                 // two column blocks of a row lie on the same banks
@@ -636,7 +635,7 @@ __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
 
 // One warp copies each segment's query rows (row r of row tile t: drafted token
 // t tb + r / G of the segment, q head g G + r % G).  bf16 pools: 16-byte async
-// copies.  FP8 pools: the products run in f16, which holds every E4M3 value; a
+// copies.  FP8 pools: S = Q K^T runs in f16, which holds every E4M3 value; a
 // query row is brought to f16 times a power of two that puts its largest value
 // just below 2^15 (values 2^-29 of that and above stay exact), and the power
 // goes into the row's score scale.
@@ -833,7 +832,7 @@ __device__ void issue_pv(const TParams &p, unsigned char *smem, uint32_t sbase)
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::OFF_TMEM);
     const uint32_t bar = sbase + L::OFF_BAR;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
-    constexpr uint32_t idesc = F8 ? rx::idesc_f16(kRows, D, false, true) : rx::idesc_bf16(kRows, D, false, true);
+    constexpr uint32_t idesc = rx::idesc_bf16(kRows, D, false, true);
     auto wait = [&](int b, uint32_t parity) { return wait_or_abort(bar + 8 * b, parity, abort_flag, p.status); };
     const uint64_t dv = rx::sdesc_sw128(sbase + L::OFF_V, L::BLK, 1024);
     for_items<L, NT>(p, smem, sbase, [&](const Item &m) -> bool {
@@ -1004,9 +1003,11 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
                             rx::f2_split(rx::f2_fma(rx::f2(u2f(sv[64 * k + 2 * e]), u2f(sv[64 * k + 2 * e + 1])), scale2, negm2), x0, x1);
                             const float e0 = rx::fast_exp2(x0), e1 = rx::fast_exp2(x1);
                             acc[e & 3] = rx::f2_add(acc[e & 3], rx::f2(e0, e1));
-                            // the weights are rounded to the type of V's tile for
-                            // the tensor core; their sum is not
-                            pk[e] = F8 ? rx::pack_f16(e0, e1) : rx::pack_bf16(e0, e1);
+                            // the weights are rounded to bf16 for the tensor core
+                            // (their sum is not), over FP8 pools too: f16 would keep
+                            // three more bits of weights near the largest, but none of
+                            // those 17 nats below it, which a long context adds up
+                            pk[e] = rx::pack_bf16(e0, e1);
                         }
                         rx::tmem_st32(tP + k * 32, pk);
                     }
