@@ -650,7 +650,8 @@ int rx_attn_tree(const rx_kv_pool *pool, const void *q, void *o, float *lse_or_n
 
 /* Tree attention over FP8 pools: the same applied to the values E4M3(code) *
  * scale, with the same arguments.  K's scale times sm_scale multiplies the
- * scores, V's the output.  Pools 16-byte aligned (the other FP8 entry points
+ * scores, V's the output.  RX_ERR_INVALID where that product times log2(e) (for
+ * rx_attn_tree, sm_scale times it) is not a normal fp32 number.  Pools 16-byte aligned (the other FP8 entry points
  * take 8). */
 int rx_attn_tree_fp8(const rx_kv_pool_fp8 *pool, const void *q, void *o, float *lse_or_null,
                      int32_t num_q_heads, const int32_t *qo_indptr, const int32_t *req_idx,

@@ -709,9 +709,12 @@ __device__ void query_loader(const TParams &p, unsigned char *smem, uint32_t sba
                             y[k] = rx::pack_f16(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xFFFF0000u) * up);
                         if (ru < M) {
                             *reinterpret_cast<uint4 *>(smem + dst + sw128(ru, ch, L::BLK)) = make_uint4(y[0], y[1], y[2], y[3]);
+                            // never 0 or infinite: a masked place's score is
+                            // -inf times it (a finite one is below 2^31)
                             if (ch == 0)
                                 reinterpret_cast<float *>(smem + L::OFF_QS)[(s % kRing) * kRows + ru] =
-                                    __uint_as_float((uint32_t)(127 - 14 + e) << 23);
+                                    fminf(fmaxf(p.scale_log2 * __uint_as_float((uint32_t)(127 - 14 + e) << 23), 0x1p-126f),
+                                          0x1.fffffep127f);
                         }
                     }
                 }
@@ -948,8 +951,7 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
                     uint32_t sv[kBN];
 #pragma unroll
                     for (int k = 0; k < kBN / 32; ++k) rx::tmem_ld32(tS + k * 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * k));
-                    if (F8 && j == g.j0)
-                        a.sl2 = p.scale_log2 * reinterpret_cast<const float *>(smem + L::OFF_QS)[(s % kRing) * kRows + row];
+                    if (F8 && j == g.j0) a.sl2 = reinterpret_cast<const float *>(smem + L::OFF_QS)[(s % kRing) * kRows + row];
                     const int kbase = j * kBN;
                     if (kbase + kBN > g.P) {   // drafted positions, or past the last
                         const int off = kbase - g.P, w0 = off >> 5;
@@ -1323,6 +1325,10 @@ int tree_call(const char *who, const TreePool &pool, const void *q, void *o, flo
     if (rx_misaligned16(q) || rx_misaligned16(o) || rx_misaligned16(pool.k) || rx_misaligned16(pool.v) ||
         (reinterpret_cast<uintptr_t>(lse) & 3) != 0 || (reinterpret_cast<uintptr_t>(mask) & 3) != 0)
         return rx_set_error(RX_ERR_INVALID, "%s: q, o and the pools must be 16-byte aligned", who);
+    const float scale_log2 = sm_scale * pool.k_scale * rx::kLog2e;
+    if (!(scale_log2 >= 0x1p-126f && scale_log2 < INFINITY))
+        return rx_set_error(RX_ERR_INVALID, "%s: sm_scale %g (times K's scale %g) outside fp32's normal range", who, sm_scale,
+                            pool.k_scale);
     const size_t need = rx_attn_tree_workspace(batch, hq, pool.hkv, pool.D, max_tree);
     if (!workspace || ws_bytes < need)
         return rx_set_error(RX_ERR_CAPACITY, "%s: workspace of %zu bytes, %zu needed", who, workspace ? ws_bytes : (size_t)0,
@@ -1351,7 +1357,7 @@ int tree_call(const char *who, const TreePool &pool, const void *q, void *o, flo
     p.rtt_stride = rtt_stride;
     p.batch = batch;
     p.max_tree = max_tree;
-    p.scale_log2 = sm_scale * pool.k_scale * rx::kLog2e;
+    p.scale_log2 = scale_log2;
     p.v_scale = pool.v_scale;
     p.status = dev_status;
     p.part_o = (float *)workspace;
