@@ -898,8 +898,9 @@ def _tree_args(q, o, lse, qo_indptr, req_idx, prefix_len, tree_mask, req_to_toke
     B = req_idx.numel()
     if qo_indptr.numel() != B + 1 or prefix_len.numel() != B or req_to_token.dim() != 2:
         raise ValueError("qo_indptr must be [batch + 1], prefix_len [batch] and req_to_token [requests, stride]")
-    if tree_mask is not None and (tree_mask.dim() != 2 or tree_mask.shape[0] != q.shape[0]):
-        raise ValueError("tree_mask must be [tokens, words]")
+    # an empty tensor has no address, and without one the call is that of chains
+    if tree_mask is not None and (tree_mask.dim() != 2 or tree_mask.shape[0] != q.shape[0] or tree_mask.shape[1] == 0):
+        raise ValueError("tree_mask must be [tokens, words], words at least 1")
     words = 0 if tree_mask is None else tree_mask.shape[1]
     return words, B, 0 if workspace is None else workspace.numel()
 
@@ -982,8 +983,10 @@ class LogitsRules:
             raise ValueError("LogitsRules: draft_tok needs qo_indptr")
         if allow is not None and (allow.dim() != 2 or allow.shape[1] != (self.vocab + 127) // 128 * 4):
             raise ValueError("LogitsRules: allow must be [mask rows, ceil(vocab / 128) * 4]")
-        if tree_mask is not None and tree_mask.dim() != 2:
-            raise ValueError("LogitsRules: tree_mask must be [rows, words]")
+        if allow is not None and allow.shape[0] == 0:
+            raise ValueError("LogitsRules: allow must have a mask row")
+        if tree_mask is not None and (tree_mask.dim() != 2 or tree_mask.shape[1] == 0):
+            raise ValueError("LogitsRules: tree_mask must be [rows, words], words at least 1")
         # rows the per-row tensors hold: rx_logits_process checks them against the logits
         self.row_tensors = [t for t in (draft_tok, tree_mask, allow_row) if t is not None]
 

@@ -1,5 +1,5 @@
-"""Arguments at the edge of what the draft-verification calls take: scales near
-the ends of fp32."""
+"""Arguments at the edge of what the draft-verification calls take: tensors
+without a word or a row, and scales near the ends of fp32."""
 import numpy as np
 import pytest
 
@@ -9,6 +9,37 @@ from tests.test_gpu_draft_tree import Run
 pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
+
+
+def _rx():
+    from prefix_shared_kv_radixattention_gb300 import binding as rx
+    return rx
+
+
+def _i32(*shape):
+    return torch.zeros(*shape, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("f8", [False, True], ids=["bf16", "fp8"])
+def test_mask_rows_without_words_are_not_a_chain(f8):
+    """A mask tensor of no words is too narrow for any tree; only None is a chain."""
+    b = _draft.TreeBatch(61, 4, 2, 64, [10, 3], [3, 1])
+    r = Run(b, f8)
+    o, lse = torch.empty_like(r.q), torch.empty(r.q.shape[:2], device="cuda")
+    r.mask = _i32(4, 0)
+    with pytest.raises(ValueError):
+        r.launch(o, lse)
+
+
+def test_rules_without_words_or_mask_rows():
+    """No words of a tree mask, no row of an allow table: refused, neither a
+    chain nor rows without a grammar."""
+    rx = _rx()
+    indptr = torch.tensor([0, 2, 3], dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        rx.LogitsRules(2, 400, qo_indptr=indptr, draft_tok=_i32(3), tree_mask=_i32(3, 0))
+    with pytest.raises(ValueError):
+        rx.LogitsRules(3, 400, allow=_i32(0, 16), allow_row=_i32(3))
 
 
 @pytest.mark.parametrize("ks", [1e-13, 1e-30, 1e25])
