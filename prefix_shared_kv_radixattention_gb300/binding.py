@@ -902,7 +902,8 @@ def _tree_args(q, o, lse, qo_indptr, req_idx, prefix_len, tree_mask, req_to_toke
     if tree_mask is not None and (tree_mask.dim() != 2 or tree_mask.shape[0] != q.shape[0] or tree_mask.shape[1] == 0):
         raise ValueError("tree_mask must be [tokens, words], words at least 1")
     words = 0 if tree_mask is None else tree_mask.shape[1]
-    return words, B, 0 if workspace is None else workspace.numel()
+    # empty tensors have no address; without tokens or requests there is nothing to do
+    return words, B, 0 if workspace is None else workspace.numel(), B > 0 and q.shape[0] > 0
 
 
 def rx_attn_tree(k_pool, v_pool, q, o, lse, qo_indptr, req_idx, prefix_len, tree_mask, req_to_token,
@@ -910,12 +911,15 @@ def rx_attn_tree(k_pool, v_pool, q, o, lse, qo_indptr, req_idx, prefix_len, tree
     """Attention of drafted trees: q, o bf16 [tokens, Hq, d], request b's
     drafted tokens at rows qo_indptr[b] .. qo_indptr[b+1]; tree_mask int32
     [tokens, words] (rx_tree_mask_build) or None for chains; workspace uint8
-    of rx_attn_tree_workspace(...) bytes."""
+    of rx_attn_tree_workspace(...) bytes.  Without drafted tokens (no rows of q)
+    or requests the call does nothing."""
     pool = make_pool(k_pool, v_pool, layer)
     if q.dim() == 3 and q.shape[2] != pool.head_dim:
         raise ValueError("q and the pools must have the same head_dim")
-    words, B, ws_bytes = _tree_args(q, o, lse, qo_indptr, req_idx, prefix_len, tree_mask, req_to_token, workspace,
-                                    dev_status)
+    words, B, ws_bytes, any_work = _tree_args(q, o, lse, qo_indptr, req_idx, prefix_len, tree_mask, req_to_token,
+                                              workspace, dev_status)
+    if not any_work:
+        return
     _check(_lib.rx_attn_tree(ctypes.byref(pool), _ptr(q), _ptr(o), _ptr(lse), q.shape[1], _ptr(qo_indptr),
                              _ptr(req_idx), _ptr(prefix_len), _ptr(tree_mask), words, _ptr(req_to_token),
                              req_to_token.shape[1], B, int(max_tree_len), _ptr(workspace), ws_bytes, float(sm_scale),
@@ -932,8 +936,10 @@ def rx_attn_tree_fp8(k_pool, v_pool, k_scale: float, v_scale: float, q, o, lse, 
     S, hkv, d, L = _pool_dims(k_pool, v_pool, layer)
     if q.dim() == 3 and q.shape[2] != d:
         raise ValueError("q and the pools must have the same head_dim")
-    words, B, ws_bytes = _tree_args(q, o, lse, qo_indptr, req_idx, prefix_len, tree_mask, req_to_token, workspace,
-                                    dev_status)
+    words, B, ws_bytes, any_work = _tree_args(q, o, lse, qo_indptr, req_idx, prefix_len, tree_mask, req_to_token,
+                                              workspace, dev_status)
+    if not any_work:
+        return
     pool = KVPoolFp8(k_pool.data_ptr(), v_pool.data_ptr(), S, hkv, d, float(k_scale), float(v_scale), L, int(layer))
     _check(_lib.rx_attn_tree_fp8(ctypes.byref(pool), _ptr(q), _ptr(o), _ptr(lse), q.shape[1], _ptr(qo_indptr),
                                  _ptr(req_idx), _ptr(prefix_len), _ptr(tree_mask), words, _ptr(req_to_token),

@@ -1,5 +1,5 @@
 """Arguments at the edge of what the draft-verification calls take: tensors
-without a word or a row, and scales near the ends of fp32."""
+without a word, a row or a token, and scales near the ends of fp32."""
 import numpy as np
 import pytest
 
@@ -40,6 +40,19 @@ def test_rules_without_words_or_mask_rows():
         rx.LogitsRules(2, 400, qo_indptr=indptr, draft_tok=_i32(3), tree_mask=_i32(3, 0))
     with pytest.raises(ValueError):
         rx.LogitsRules(3, 400, allow=_i32(0, 16), allow_row=_i32(3))
+
+
+@pytest.mark.parametrize("f8", [False, True], ids=["bf16", "fp8"])
+def test_nothing_drafted(f8):
+    """No request has a drafted token, or there is no request: nothing to do."""
+    b = _draft.TreeBatch(62, 4, 2, 64, [10, 3], [1, 1])
+    r = Run(b, f8)
+    r.q, r.mask, r.indptr = r.q[:0], r.mask[:0], _i32(3)
+    r.launch(torch.empty_like(r.q), None)
+    r.indptr, r.req, r.plen = _i32(1), r.req[:0], r.plen[:0]
+    r.launch(torch.empty_like(r.q), torch.empty(0, 4, device="cuda"))
+    torch.cuda.synchronize()
+    assert int(r.status.item()) == 0
 
 
 @pytest.mark.parametrize("ks", [1e-13, 1e-30, 1e25])
