@@ -18,6 +18,21 @@
                                 cudaGetErrorString(e_));                               \
     } while (0)
 
+// SMs of the current device.  Kept a thread: threads that launch at once share
+// nothing here.
+inline int rx_num_sms()
+{
+    static thread_local int of = -1, sms = 0;
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+    if (dev != of) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 152;
+        of = dev;
+        sms = n;
+    }
+    return sms;
+}
+
 inline bool rx_misaligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) != 0; }
 
 namespace rx {

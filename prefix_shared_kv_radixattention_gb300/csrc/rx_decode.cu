@@ -929,18 +929,6 @@ __global__ void __launch_bounds__(128) merge_kernel(const Params p, int use_plan
     if (p.lse && lane == 0) p.lse[row] = (m + log2f(wsum)) * rx::kLn2;
 }
 
-int num_sms()
-{
-    static int sms = 0;
-    if (sms == 0) {
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-            sms = 148;
-    }
-    return sms;
-}
-
 // ---------------------------------------------------------------------------
 // wide items: one request, every kv head at once
 // ---------------------------------------------------------------------------
@@ -1816,7 +1804,7 @@ int launch_decode_gqa(const Params &p, cudaStream_t st, bool dependent)
                                            bytes));
         configured = true;
     }
-    const int grid = p.n_wide < num_sms() ? p.n_wide : num_sms();
+    const int grid = p.n_wide < rx_num_sms() ? p.n_wide : rx_num_sms();
     return launch_on(decode_gqa_kernel<D, F8>, grid, 32 * (1 + kGqaCopyWarps + kGqaWarps), bytes, st, dependent, p);
 }
 
@@ -1829,7 +1817,7 @@ int launch_decode_wide_cfg(const Params &p, cudaStream_t st, bool dependent)
                                            cudaFuncAttributeMaxDynamicSharedMemorySize, WideLayout::BYTES));
         configured = true;
     }
-    const int grid = p.n_wide < num_sms() ? p.n_wide : num_sms();
+    const int grid = p.n_wide < rx_num_sms() ? p.n_wide : rx_num_sms();
     return launch_on(decode_wide_kernel<D, LOG_NP, HPW, CW, F8>, grid, 32 * (1 + kWideCopyWarps + CW),
                      WideLayout::BYTES, st, dependent, p);
 }
@@ -1879,7 +1867,7 @@ int launch_decode(const Params &p, cudaStream_t st)
                                            Layout<D, F8>::BYTES));
         configured = true;
     }
-    const int grid = p.total_work < num_sms() ? p.total_work : num_sms();
+    const int grid = p.total_work < rx_num_sms() ? p.total_work : rx_num_sms();
     return launch_on(decode_kernel<D, PLAN, F8>, grid, kThreads, Layout<D, F8>::BYTES, st, false, p);
 }
 

@@ -263,18 +263,6 @@ __global__ void __launch_bounds__(kFinishThreads) fsm_finish_kernel(const FsmPar
     }
 }
 
-int fsm_num_sms()
-{
-    static int sms = 0;
-    if (sms == 0) {
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-            sms = 148;
-    }
-    return sms;
-}
-
 }  // namespace
 
 extern "C" int rx_fsm_compress(int32_t n_states, int32_t vocab, const int64_t *row_ptr, const int32_t *tok,
@@ -410,7 +398,7 @@ extern "C" int rx_fsm_step(const rx_fsm *fsm, const float *logits, int64_t logit
     p.fused = batch <= kScanThreads;
     cudaStream_t st = (cudaStream_t)stream;
     // scan: one resident wave of CTAs walking the (request, tile) pairs
-    const int64_t resident = (int64_t)kScanCtasPerSm * fsm_num_sms();
+    const int64_t resident = (int64_t)kScanCtasPerSm * rx_num_sms();
     const unsigned grid = (unsigned)std::min<int64_t>(tiles, resident);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);

@@ -67,18 +67,6 @@ __global__ void __launch_bounds__(256) kv_store_fp8_kernel(const uint4 *__restri
     }
 }
 
-int num_sms()
-{
-    static int sms = 0;
-    if (sms == 0) {
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-            sms = 148;
-    }
-    return sms;
-}
-
 }  // namespace
 
 extern "C" int rx_kv_store(const rx_kv_pool *pool_in, const void *k_new, const void *v_new,
@@ -102,7 +90,7 @@ extern "C" int rx_kv_store(const rx_kv_pool *pool_in, const void *k_new, const v
     const int64_t work = 2 * n * cpr;
     const int threads = 256;
     int64_t blocks = (work + threads - 1) / threads;
-    const int64_t cap = (int64_t)num_sms() * 8;
+    const int64_t cap = (int64_t)rx_num_sms() * 8;
     if (blocks > cap) blocks = cap;
     kv_store_kernel<<<(unsigned)blocks, threads, 0, (cudaStream_t)stream>>>(
         (const uint4 *)k_new, (const uint4 *)v_new, slots, n, cpr, (uint4 *)pool->k,
@@ -133,7 +121,7 @@ extern "C" int rx_kv_store_fp8(const rx_kv_pool_fp8 *pool_in, const void *k_new,
     const int64_t work = 2 * n * cpr;
     const int threads = 256;
     int64_t blocks = (work + threads - 1) / threads;
-    const int64_t cap = (int64_t)num_sms() * 8;
+    const int64_t cap = (int64_t)rx_num_sms() * 8;
     if (blocks > cap) blocks = cap;
     kv_store_fp8_kernel<<<(unsigned)blocks, threads, 0, (cudaStream_t)stream>>>(
         (const uint4 *)k_new, (const uint4 *)v_new, slots, n, cpr, (uint2 *)pool->k, (uint2 *)pool->v,

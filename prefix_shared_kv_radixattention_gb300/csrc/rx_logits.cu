@@ -436,18 +436,6 @@ __global__ void __launch_bounds__(kThreads, 2) logits_kernel(const __grid_consta
     }
 }
 
-int logits_num_sms()
-{
-    static int sms = 0;
-    if (sms == 0) {
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-            sms = 152;
-    }
-    return sms;
-}
-
 }  // namespace
 
 extern "C" int rx_logits_process(const rx_logits_rules *rules, const void *logits, int32_t logits_bf16,
@@ -491,7 +479,7 @@ extern "C" int rx_logits_process(const rx_logits_rules *rules, const void *logit
     // four CTAs an SM (two at a time): with fewer, a request's rows are dealt out
     // to several, which all count.  16 requests of 8 to 16 rows of 128,256 ids:
     // 60 us with 1 share, 57 with 2, 59 with 3, 61 with 4 (55 with 2 since)
-    const int64_t shares = std::max<int64_t>(1, std::min<int64_t>(4 * logits_num_sms() / (tiles * r.n_req), rows));
+    const int64_t shares = std::max<int64_t>(1, std::min<int64_t>(4 * rx_num_sms() / (tiles * r.n_req), rows));
     const size_t smem = (size_t)tile * (r.bias_ptr ? 9 : touched ? 5 : 0);
     auto kernel = in_place ? logits_kernel<false, true> : logits_bf16 ? logits_kernel<true, false> : logits_kernel<false, false>;
     // per device and function; cheap, and right whichever device is current

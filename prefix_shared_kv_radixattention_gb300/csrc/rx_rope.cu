@@ -158,22 +158,10 @@ __global__ void __launch_bounds__(256) kv_store_rope_kernel(const uint4 *__restr
     }
 }
 
-int num_sms()
-{
-    static int sms = 0;
-    if (sms == 0) {
-        int dev = 0;
-        if (cudaGetDevice(&dev) != cudaSuccess ||
-            cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-            sms = 148;
-    }
-    return sms;
-}
-
 unsigned grid_for(int64_t work)
 {
     int64_t blocks = (work + 255) / 256;
-    const int64_t cap = (int64_t)num_sms() * 8;
+    const int64_t cap = (int64_t)rx_num_sms() * 8;
     return (unsigned)(blocks > cap ? cap : (blocks < 1 ? 1 : blocks));
 }
 
@@ -184,7 +172,7 @@ bool misaligned(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) !=
 int chunks_per_thread(int64_t n, int heads, int D)
 {
     const int hchunks = (heads + kHeadsPerThread - 1) / kHeadsPerThread;
-    const int64_t target = (int64_t)num_sms() * 1024;
+    const int64_t target = (int64_t)rx_num_sms() * 1024;
     const int64_t one = n * (D / 16) * hchunks;  // threads at one chunk each
     int64_t cpt = (one + target - 1) / target;
     if (cpt < 1) cpt = 1;

@@ -73,3 +73,49 @@ def test_query_rows_of_zeros_and_scales_near_the_ends(ks):
     assert int(r.status.item()) == 0
     keep = slice(None) if ks < 1 else slice(0, None, 2)
     _draft.check_tree(o[keep], lse[keep], tuple(x[keep] for x in r.reference()), f"scale {ks}")
+
+
+def test_calls_of_several_threads_at_once():
+    """Every thread with a stream and outputs of its own: the results are those
+    of the same calls one after the other."""
+    import threading
+
+    from tests.test_gpu_draft_logits import Case
+    rx = _rx()
+    c = Case(64, 5, 9001, hist=500, bias=20, states=3)
+    rules, x = c.rules(), c.logits()
+    runs = [Run(_draft.TreeBatch(65, 8, 2, 64, [300, 7, 129], [9, 4, 17]), f8) for f8 in (False, True)]
+
+    def step(out, stream):
+        for r, (o, lse, ws) in zip(runs, out[1:]):
+            r.launch(o, lse, stream=stream, ws=ws)
+        rx.rx_logits_process(rules, x, out[0], stream=stream)
+
+    def outputs():
+        return [torch.zeros(5, 9001, device="cuda")] + [
+            (torch.zeros_like(r.q), torch.zeros(r.q.shape[:2], device="cuda"), torch.empty_like(r.ws)) for r in runs]
+
+    want, outs = outputs(), [outputs() for _ in range(8)]
+    step(want, None)
+    torch.cuda.synchronize()
+    streams, gate, bad = [torch.cuda.Stream() for _ in outs], threading.Barrier(len(outs)), []
+
+    def work(out, stream):
+        try:
+            gate.wait(60)
+            for _ in range(10):
+                step(out, stream)
+        except Exception as e:  # noqa: BLE001 -- reported by the test's thread
+            bad.append(e)
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(outs, streams)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not bad
+    for out in outs:
+        assert torch.equal(out[0], want[0])
+        for (o, lse, _), (wo, wl, _) in zip(out[1:], want[1:]):
+            assert torch.equal(o, wo) and torch.equal(lse, wl)
