@@ -1255,9 +1255,11 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const __grid_
 size_t part_bytes(int32_t nt, int32_t head_dim) { return (size_t)2 * kCtas * nt * kRows * head_dim * sizeof(float); }
 
 // Row tiles that share a K/V tile: two where some tree may have more than one
-// (64-token trees over 64/8 heads, 8k contexts: 121 us, one at a time 134 us),
-// and bf16 pools only (an FP8 tile has one query buffer).  The second brings
-// softmax warps of its own; one group for both took 133 us.
+// (64-token trees over 64/8 heads, 8k contexts: 121 us, one at a time 134 us).
+// The second brings softmax warps of its own; one group for both took 133 us.
+// The call takes it for bf16 pools only: an FP8 tile has one query buffer, and
+// the same trees over E4M3 pools gather every K/V tile once a row tile, 213 us.
+// The workspace has room for either.
 int row_tiles(int32_t hq, int32_t hkv, int32_t max_tree) { return (int64_t)max_tree > kRows / (hq / hkv) ? kMaxNt : 1; }
 
 struct TreePool {
