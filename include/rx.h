@@ -343,7 +343,9 @@ int rx_kv_store_rope_fp8(const rx_kv_pool_fp8 *pool, const void *k_new, const vo
  *     y  = x / sqrt(sum_c x[c]^2 / head_dim + eps) * w      (w: q_weight or
  *          k_weight, one vector for all heads; NULL is all ones),
  *     y' = y rotated to position pos[i] as rx_rope rotates,
- * computed in fp32 (the angle as rx_rope reduces it) and rounded once:
+ * computed in fp32 and rounded once (the angle is reduced as in rx_rope, but its
+ * sine and cosine are those of two fp32 words where rx_rope takes one, so a K
+ * row written by the two paths can differ in its last place):
  * q_out[i] = bf16(y') for the q heads, K[slots[i]] = bf16(y') for the k
  * heads, V[slots[i]] = v_new[i].
  *   q: device bf16, token i's num_q_heads * head_dim values at q + i *
@@ -361,7 +363,10 @@ int rx_kv_store_rope_fp8(const rx_kv_pool_fp8 *pool, const void *k_new, const vo
  * head_dim 64 or 128; base > 1; eps >= 0.  A slot id outside the pool sets
  * RX_DEV_BAD_SLOT and its K and V rows are not written (its q row is).  The
  * squares are summed in fp32: a head whose squares sum past 3.4e38 (values
- * above about 1e18) gives zeros, as a norm held in 32 bits does. */
+ * above about 1e18) gives zeros, as a norm held in 32 bits does.  With eps
+ * below fp32's normal range (0 among it), a head whose mean square is below
+ * 1.2e-38 (values under about 1e-19) loses bits, and one whose squares all
+ * vanish (under about 1e-23; a head of zeros) gives infinities or NaN. */
 int rx_qk_norm_rope_store(const rx_kv_pool *pool, const void *q, int64_t q_stride, void *q_out,
                           const void *k_new, const void *v_new, int64_t kv_stride, const void *q_weight,
                           const void *k_weight, const int32_t *slots, const int32_t *pos, int64_t n,
@@ -635,13 +640,21 @@ int rx_tree_mask_build(const int32_t *parent, int32_t n, int32_t words, uint32_t
  *   workspace: device, >= rx_attn_tree_workspace(...) bytes, 256-byte
  *   aligned, contents ignored on entry, not used by anything else until the
  *   call's work on `stream` is done.
+ * For one chain a request rx_attn_extend computes the same (extend_len = T_b).
+ * This call is made for few tokens over long contexts and reads a request's K
+ * and V once for every 256 / G drafted tokens (G = num_q_heads / num_kv_heads;
+ * over FP8 pools for every 128 / G): it is the faster of the two for chains of
+ * up to 256 tokens (FP8: some 50), the staged rx_attn_extend for longer ones (8
+ * requests of up to 8,192, 64/8 heads of 128: 16 tokens 55 against 166 us, 256
+ * tokens 424 against 429, 1,024 1,979 against 1,451; FP8 16 tokens 84 against
+ * 150, 64 tokens 219 against 168).
  * Requires head_dim 64 or 128, num_q_heads % num_kv_heads == 0,
  * num_q_heads / num_kv_heads <= 128, num_kv_heads <= 8192 and batch <= 65535.
- * A prefix that several requests share is read for each of them.  A request with T_b > max_tree_len or
- * prefix_len[b] + T_b past the stride sets RX_DEV_BAD_LEN and its rows stay
- * unwritten; a bad slot reads as zeros (RX_DEV_BAD_SLOT).  Rows behind
- * qo_indptr[batch] are left as they were.  The lengths are read on the
- * device, so a captured call serves later steps. */
+ * A prefix that several requests share is read for each of them.  A request
+ * with T_b > max_tree_len or prefix_len[b] + T_b past the stride sets
+ * RX_DEV_BAD_LEN and its rows stay unwritten; a bad slot reads as zeros
+ * (RX_DEV_BAD_SLOT).  Rows behind qo_indptr[batch] are left as they were.  The
+ * lengths are read on the device, so a captured call serves later steps. */
 int rx_attn_tree(const rx_kv_pool *pool, const void *q, void *o, float *lse_or_null, int32_t num_q_heads,
                  const int32_t *qo_indptr, const int32_t *req_idx, const int32_t *prefix_len,
                  const uint32_t *tree_mask, int32_t mask_words, const int32_t *req_to_token,
@@ -651,8 +664,8 @@ int rx_attn_tree(const rx_kv_pool *pool, const void *q, void *o, float *lse_or_n
 /* Tree attention over FP8 pools: the same applied to the values E4M3(code) *
  * scale, with the same arguments.  K's scale times sm_scale multiplies the
  * scores, V's the output.  RX_ERR_INVALID where that product times log2(e) (for
- * rx_attn_tree, sm_scale times it) is not a normal fp32 number.  Pools 16-byte aligned (the other FP8 entry points
- * take 8). */
+ * rx_attn_tree, sm_scale times it) is not a normal fp32 number.  Pools 16-byte
+ * aligned (the other FP8 entry points take 8). */
 int rx_attn_tree_fp8(const rx_kv_pool_fp8 *pool, const void *q, void *o, float *lse_or_null,
                      int32_t num_q_heads, const int32_t *qo_indptr, const int32_t *req_idx,
                      const int32_t *prefix_len, const uint32_t *tree_mask, int32_t mask_words,
@@ -802,9 +815,11 @@ typedef struct {
  * vocabulary, in the history, a path or the biases, is left out and sets
  * RX_DEV_BAD_TOKEN, as does a bias list that is not ascending (the ids out of
  * order may then be left out); a mask row outside [-1, n_allow) sets
- * RX_DEV_BAD_STATE and allows nothing.  Rows start at any element; those on
- * 16-byte boundaries move in 16-byte pieces.  n_req <= 65535, vocab <= 2^30
- * (RX_ERR_UNSUPPORTED otherwise).  No workspace: calls on several streams, or
+ * RX_DEV_BAD_STATE and allows nothing.  Rows start at any element; those of out
+ * (and of fp32 logits) on 16-byte boundaries, and of bf16 logits on 8-byte ones,
+ * move in such pieces, others id by id (64 fp32 rows of 50,257 ids 29 us, of
+ * 50,256 15): strides that are multiples of 4 are worth their padding.
+ * n_req <= 65535, vocab <= 2^30 (RX_ERR_UNSUPPORTED otherwise).  No workspace: calls on several streams, or
  * captured ones, may share the rules. */
 int rx_logits_process(const rx_logits_rules *rules, const void *logits, int32_t logits_bf16,
                       int64_t logits_stride, float *out, int64_t out_stride, int32_t rows,

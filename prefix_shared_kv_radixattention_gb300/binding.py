@@ -950,8 +950,10 @@ def rx_attn_tree_fp8(k_pool, v_pool, k_scale: float, v_scale: float, q, o, lse, 
 class LogitsRules:
     """What rx_logits_process applies to a batch's logits (rx_logits_rules):
     CUDA tensors, each optional, kept alive here.  Their contents may change
-    between calls (a longer history goes into the same tensors); their
-    sizes may not.
+    between calls; their sizes may not.  They are checked here, once, not at
+    each call.  hist may be longer than its lists, so that they can grow in
+    place, but request b's list ends where that of b + 1 starts: a list that
+    grows moves those behind it.
 
     hist int32 [tokens], hist_ptr int64 [n_req + 1], prompt_len int32
     [n_req]; repetition, frequency, presence fp32 [n_req]; bias_tok int32 and

@@ -39,9 +39,9 @@
 // a request; read once in all it would be 164 us); 64 of 1,281, 32/32 heads,
 // 211 us (149 us of bytes; four of a tile's 128 rows are used, and a softmax
 // warp takes 2,300 cycles for a tile however few rows it has); E4M3 pools, 16 of
-// up to 32,768, 32/8 heads, 295 us (119 us of bytes: the softmax warps' 3,500
-// cycles a tile, two of the four with rows, with the producers' 2,500 close
-// behind; a part of the exponentials on the multiply-add units, 368 us, or the
+// up to 32,768, 32/8 heads, 295 us (119 us of bytes: the softmax warps' 3,300
+// cycles a tile, two of the four with rows, with the producers' 2,500 for K and
+// 2,900 for V close behind; a part of the exponentials on the multiply-add units, 368 us, or the
 // rows put in twice and the tiles' positions, 382 us, or the tiles, 325 us,
 // shared between the copies were no faster: the warps that got less to do took
 // as much longer for it, so it is the SM's units that are shared); trees of
