@@ -576,7 +576,8 @@ int rx_attn_decode_static(const rx_kv_pool *pool, const void *q, void *o, float 
  * in f16 with fp32 sums: codes widen to f16 exactly, q is converted to f16
  * (exact for |q| within f16's range, which q must respect; values below
  * 2^-14 round to f16 subnormals), and the softmax weights are rounded to f16
- * rather than bf16.  K's scale multiplies the scores, V's the output. */
+ * rather than bf16 (those 17 nats and more below an item's largest vanish from
+ * o, though not from lse).  K's scale multiplies the scores, V's the output. */
 int rx_attn_decode_fp8(const rx_kv_pool_fp8 *pool, const void *q, void *o, float *lse, int32_t num_q_heads,
                        const int32_t *req_idx, const int32_t *seq_len, const int32_t *req_to_token,
                        int64_t rtt_stride, int32_t batch, int32_t max_seq_len, const rx_decode_plan *plan,

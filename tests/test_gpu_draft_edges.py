@@ -119,3 +119,55 @@ def test_calls_of_several_threads_at_once():
         assert torch.equal(out[0], want[0])
         for (o, lse, _), (wo, wl, _) in zip(out[1:], want[1:]):
             assert torch.equal(o, wo) and torch.equal(lse, wl)
+
+
+@pytest.mark.parametrize("f8", [False, True], ids=["bf16", "fp8"])
+def test_pools_past_32_bits_of_offset(f8):
+    """The same rows in slots whose byte offset passes 2^32: the same bits.  The
+    norm, rotation and store writes there too."""
+    rx = _rx()
+    b = _draft.TreeBatch(66, 32, 16, 128, [300, 0, 129], [9, 4, 17])
+    r = Run(b, f8)
+    want = r()
+    rows = (2 ** 32 + 2 ** 28) // (16 * 128 * r.k.element_size())
+    first = rows - b.num_slots
+    k, v = (torch.zeros(rows, 16, 128, dtype=r.k.dtype, device="cuda") for _ in range(2))
+    k[first:], v[first:] = r.k, r.v
+    small = r.k, r.v
+    r.k, r.v, r.rtt = k, v, torch.where(r.rtt < 0, r.rtt, r.rtt + first)
+    got = r()
+    assert int(r.status.item()) == 0
+    assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
+
+    n = 40
+    x = torch.randn(n, 64, 128, generator=torch.Generator().manual_seed(5)).cuda().bfloat16()
+    slots = torch.randperm(b.num_slots, generator=torch.Generator().manual_seed(6))[:n].int().cuda()
+    pos, q = torch.arange(n, dtype=torch.int32, device="cuda"), torch.empty(n, 32, 128, dtype=torch.bfloat16, device="cuda")
+    for pools, at in ((small, slots), ((k, v), slots + first)):
+        args = (x[:, :32], q, x[:, 32:48], x[:, 48:], None, None, at, pos, 10000.0, 1e-6, r.status)
+        if f8:
+            rx.rx_qk_norm_rope_store_fp8(*pools, 0.05, 0.05, *args)
+        else:
+            rx.rx_qk_norm_rope_store(*pools, *args)
+    assert int(r.status.item()) == 0
+    for big, little in zip((k, v), small):
+        assert torch.equal(big[first:], little) and not big[:first].any()
+
+
+def test_logits_past_32_bits_of_offset():
+    """17,000 rows of 128,256 ids (2^31 elements and more): the last rows as
+    those of a call of their own."""
+    rx = _rx()
+    n, V, m = 17000, 128256, 3
+    x = torch.zeros(n, V, dtype=torch.bfloat16, device="cuda")
+    x[-m:] = torch.randn(m, V, generator=torch.Generator().manual_seed(7)).cuda()
+    out = torch.empty(n, V, device="cuda")
+    pres = torch.linspace(0, 1, n, device="cuda")
+    hist = torch.arange(n, dtype=torch.int32, device="cuda") % V
+    ptr = torch.arange(n + 1, device="cuda")
+    rx.rx_logits_process(rx.LogitsRules(n, V, hist=hist, hist_ptr=ptr, presence=pres), x, out)
+    few = torch.empty(m, V, device="cuda")
+    rx.rx_logits_process(rx.LogitsRules(m, V, hist=hist[-m:].contiguous(), hist_ptr=ptr[:m + 1].contiguous(),
+                                        presence=pres[-m:].contiguous()), x[-m:], few)
+    assert torch.equal(out[-m:], few)
+    assert (few != x[-m:].float()).sum() == m and (out[:-m] != 0).sum() == n - m - 1   # the first row's presence is 0
