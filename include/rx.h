@@ -678,6 +678,146 @@ int rx_attn_tree_fp8(const rx_kv_pool_fp8 *pool, const void *q, void *o, float *
 size_t rx_attn_tree_workspace(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                               int32_t max_tree_len);
 
+/* ---- attention with rules on the scores (device) ---------------------------
+ * Not from the pages, which do not reach inside the model.  Models cap their
+ * attention scores, let them fall with the distance, look back over a window
+ * only, and let the tokens of an image or of a prefix see one another; texts
+ * packed into one request must not see each other.  With s_j = sm_scale q . k_j
+ * as in the attention definition above, a query token at position p and the
+ * key at position j, head h:
+ *     x_j = c(s_j) - slope[h] |p - j|,   c(s) = cap tanh(s / cap), or s without
+ *           a cap,
+ *     lo  = max(0, p - window + 1, see_from[i]),  hi = max(p + 1, min(see_to[i], n)),
+ *     o   = sum_{lo <= j < hi} softmax(x)_j V_j,  lse = log(sum_{lo <= j < hi} exp(x_j)),
+ * n being the request's context (its cached and new tokens) and i the query
+ * token's row of q.  A token that sees nothing (lo >= hi) gets o = 0 and lse =
+ * -inf.  So see_from holds the start of the token's document, see_to the end of
+ * the image or prefix that the token belongs to (0: it sees what is before it);
+ * the window bounds only what lies behind the token.
+ *
+ * Scores, sums and the output's accumulator are fp32; the weights are rounded to
+ * bf16 for the product with V (off by at most 2^-8 sum p |V|) and o once more,
+ * as in rx_attn_extend and rx_attn_tree.  The cap's tanh comes from the
+ * hardware's exponential and reciprocal: off by a few 2^-23 cap.  With a cap of
+ * up to 50 and no slopes, V values above 2^57 may overflow o.
+ *
+ * What a token does not see takes no part in its result, whatever K and V hold
+ * there (NaN and infinities among it).  Positions that no token of a request
+ * sees may be read or not: their slot ids must be in the pool or are flagged if
+ * they are read (a window's call skips whole tiles of 128 positions before it,
+ * and rx_attn_decode_rules reads no position before its token's lo). */
+typedef struct {
+    float cap;                /* > 0 (1e-3 to 1e6): scores are capped; 0: they are not        */
+    int32_t window;           /* > 0: positions a token sees, itself among them; 0: all of them */
+    const float *slope;       /* device fp32 [num_q_heads], finite, or NULL: none             */
+    const int32_t *see_from;  /* device int32 [query tokens] or NULL: 0                       */
+    const int32_t *see_to;    /* device int32 [query tokens] or NULL: 0                       */
+} rx_attn_rules;
+
+/* Extend attention with rules: rx_attn_extend's arguments, requirements and
+ * errors, with a workspace of rx_attn_rules_workspace(...) bytes, which every
+ * call needs (RX_ERR_CAPACITY).  Calls with few query rows (max_extend_len of at
+ * most 1024, and less work than fills the GPU) share each context among CTAs;
+ * the others copy the contexts into the workspace, as rx_attn_extend does with
+ * one.  Contexts that sum to more rows than the workspace was sized for set
+ * RX_DEV_BAD_LEN and leave every output row unwritten there. */
+int rx_attn_extend_rules(const rx_kv_pool *pool, const void *q, void *o, float *lse_or_null, int32_t num_q_heads,
+                         const int32_t *qo_indptr, const int32_t *req_idx, const int32_t *prefix_len,
+                         const int32_t *extend_len, const int32_t *req_to_token, int64_t rtt_stride, int32_t batch,
+                         int32_t max_extend_len, const rx_attn_rules *rules, void *workspace, size_t ws_bytes,
+                         float sm_scale, int32_t *dev_status, void *stream);
+
+/* The same over FP8 pools (16-byte aligned). */
+int rx_attn_extend_rules_fp8(const rx_kv_pool_fp8 *pool, const void *q, void *o, float *lse_or_null, int32_t num_q_heads,
+                             const int32_t *qo_indptr, const int32_t *req_idx, const int32_t *prefix_len,
+                             const int32_t *extend_len, const int32_t *req_to_token, int64_t rtt_stride, int32_t batch,
+                             int32_t max_extend_len, const rx_attn_rules *rules, void *workspace, size_t ws_bytes,
+                             float sm_scale, int32_t *dev_status, void *stream);
+
+/* Decode attention with rules: one query per request b at position seq_len[b] -
+ * 1 over its seq_len[b] positions (its own K/V already in the pool), see_from
+ * [batch], no see_to (RX_ERR_INVALID).  A request with seq_len 0 is left out:
+ * its rows of o and lse stay as they were.  A seq_len below 0 or above the
+ * stride sets RX_DEV_BAD_LEN and leaves the row out as well.  There is no plan:
+ * a prefix that several requests share is read once for each.  Up to 128 q
+ * heads a kv head.  Workspace: rx_attn_rules_workspace(0, batch, ..., 1). */
+int rx_attn_decode_rules(const rx_kv_pool *pool, const void *q, void *o, float *lse_or_null, int32_t num_q_heads,
+                         const int32_t *req_idx, const int32_t *seq_len, const int32_t *req_to_token, int64_t rtt_stride,
+                         int32_t batch, const rx_attn_rules *rules, void *workspace, size_t ws_bytes, float sm_scale,
+                         int32_t *dev_status, void *stream);
+
+/* The same over FP8 pools (16-byte aligned). */
+int rx_attn_decode_rules_fp8(const rx_kv_pool_fp8 *pool, const void *q, void *o, float *lse_or_null, int32_t num_q_heads,
+                             const int32_t *req_idx, const int32_t *seq_len, const int32_t *req_to_token,
+                             int64_t rtt_stride, int32_t batch, const rx_attn_rules *rules, void *workspace,
+                             size_t ws_bytes, float sm_scale, int32_t *dev_status, void *stream);
+
+/* Workspace bytes for the calls with rules (256-byte aligned; contents ignored
+ * on entry and undefined after the call; not used by anything else until the
+ * call's work on its stream is done): `batch` requests whose contexts sum to at
+ * most total_ctx_tokens (0 for decode) with up to max_extend_len new tokens each
+ * (1 for decode).  With a window only the last window + max_extend_len + 128
+ * positions of a context count.  0 on an invalid argument. */
+size_t rx_attn_rules_workspace(int64_t total_ctx_tokens, int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                               int32_t head_dim, int32_t max_extend_len);
+
+/* ---- rotation with positions on several axes, and store (device) -----------
+ * Not from the pages.  Models that read images and video give a token a position
+ * on each of several axes (time, height, width) and turn each pair of a head's
+ * values by the position on one of them.  For every q and k head x of token i,
+ * c < head_dim / 2 and theta_c = base^(-2c / head_dim):
+ *     a     = pos[pair_axis[c]][i] theta_c,
+ *     y'[c] = y[c] cos a - y[c + head_dim/2] sin a,
+ *     y'[c + head_dim/2] = y[c + head_dim/2] cos a + y[c] sin a,
+ * with y = x, or with norm != 0 the RMS norm of rx_qk_norm_rope_store (q_weight,
+ * k_weight and eps as there).  Everything else is as in rx_qk_norm_rope_store:
+ * fp32, one rounding, q into q_out, K and V into the pool at slots[i].
+ *   pos: device int32, the positions on axis a at pos + a * pos_stride (n each);
+ *   num_axes: 1 .. 8; pair_axis: host uint8 [head_dim / 2], each below num_axes
+ *   (sections of consecutive pairs, the axes in turn, or any other order).
+ * Without norm the weights must be NULL and eps is not looked at; a value times
+ * sine or cosine that overflows bf16 is infinite. */
+int rx_qk_rope_axes_store(const rx_kv_pool *pool, const void *q, int64_t q_stride, void *q_out, const void *k_new,
+                          const void *v_new, int64_t kv_stride, int32_t norm, const void *q_weight, const void *k_weight,
+                          const int32_t *slots, const int32_t *pos, int64_t pos_stride, int32_t num_axes,
+                          const uint8_t *pair_axis, int64_t n, int32_t num_q_heads, double base, float eps,
+                          int32_t *dev_status, void *stream);
+
+/* The same into FP8 pools, as rx_qk_norm_rope_store_fp8. */
+int rx_qk_rope_axes_store_fp8(const rx_kv_pool_fp8 *pool, const void *q, int64_t q_stride, void *q_out, const void *k_new,
+                              const void *v_new, int64_t kv_stride, int32_t norm, const void *q_weight,
+                              const void *k_weight, const int32_t *slots, const int32_t *pos, int64_t pos_stride,
+                              int32_t num_axes, const uint8_t *pair_axis, int64_t n, int32_t num_q_heads, double base,
+                              float eps, int32_t *dev_status, void *stream);
+
+/* ---- the lists of a step (device) ------------------------------------------
+ * Not from the pages.  What the other calls take for a ragged batch, from the
+ * requests' lengths and without the host: request b (b < batch) has prefix_len[b]
+ * tokens in the pool and new_len[b] new ones, at positions prefix_len[b] + i:
+ *     qo_indptr[b] = sum of new_len before b, qo_indptr[batch] = all of them,
+ *     seq_len[b]   = prefix_len[b] + new_len[b],
+ *     pos[qo_indptr[b] + i]   = prefix_len[b] + i,
+ *     slots[qo_indptr[b] + i] = the slot of that position: from req_to_token row
+ *         req_idx[b], or, with pages, pages[req_idx[b]][position / page_size] *
+ *         page_size + position % page_size, which is then also written to
+ *         req_to_token (a pool handed out in pages of page_size slots).
+ * Entries of pos and slots past the last token stay as they were.
+ *   req_idx (distinct where pages are given), prefix_len, new_len: device int32
+ *   [batch]; req_to_token: device int32, row stride rtt_stride; pages: device
+ *   int32, row stride pages_stride, page ids in [0, num_slots / page_size), or
+ *   NULL; qo_indptr: device int32 [batch + 1]; seq_len: device int32 [batch] or
+ *   NULL; pos, slots: device int32 [max_tokens].  The outputs must not overlap the
+ *   inputs or one another.
+ * A negative length, or one past rtt_stride (or the pages' positions), sets
+ * RX_DEV_BAD_LEN and counts as a request without new tokens, seq_len 0.  More
+ * new tokens than max_tokens set RX_DEV_BAD_LEN: qo_indptr ends at max_tokens
+ * and the tokens behind it are left out.  A slot or page outside the pool sets
+ * RX_DEV_BAD_SLOT and its slot is -1 (in req_to_token too). */
+int rx_step_maps(const int32_t *req_idx, const int32_t *prefix_len, const int32_t *new_len, int32_t batch,
+                 int32_t *req_to_token, int64_t rtt_stride, const int32_t *pages, int64_t pages_stride, int32_t page_size,
+                 int64_t num_slots, int32_t *qo_indptr, int32_t *seq_len, int32_t *pos, int32_t *slots, int64_t max_tokens,
+                 int32_t *dev_status, void *stream);
+
 /* ---- compressed finite-state machine (constrained decoding) -------------
  * Source: "SGLang: Efficient Execution of Structured Language Model
  * Programs" (unite.ai, es), "Introducción a SGLang", compressed-FSM bullet.

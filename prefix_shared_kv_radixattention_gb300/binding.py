@@ -149,6 +149,26 @@ _sig("rx_attn_tree_fp8", ctypes.c_int, ctypes.POINTER(KVPoolFp8), _P, _P, _P, _I
      _I32, _I32, _P, ctypes.c_size_t, ctypes.c_float, _P, _P)
 _sig("rx_attn_tree_workspace", ctypes.c_size_t, _I32, _I32, _I32, _I32, _I32)
 _sig("rx_schedule", ctypes.c_int, _P, _P, _P, _I32, _I32, _P, _P)
+
+
+class AttnRulesStruct(ctypes.Structure):
+    _fields_ = [("cap", ctypes.c_float), ("window", ctypes.c_int32), ("slope", _P), ("see_from", _P), ("see_to", _P)]
+
+
+_sig("rx_attn_extend_rules", ctypes.c_int, ctypes.POINTER(KVPool), _P, _P, _P, _I32, _P, _P, _P, _P, _P, _I64, _I32, _I32,
+     ctypes.POINTER(AttnRulesStruct), _P, ctypes.c_size_t, ctypes.c_float, _P, _P)
+_sig("rx_attn_extend_rules_fp8", ctypes.c_int, ctypes.POINTER(KVPoolFp8), _P, _P, _P, _I32, _P, _P, _P, _P, _P, _I64, _I32,
+     _I32, ctypes.POINTER(AttnRulesStruct), _P, ctypes.c_size_t, ctypes.c_float, _P, _P)
+_sig("rx_attn_decode_rules", ctypes.c_int, ctypes.POINTER(KVPool), _P, _P, _P, _I32, _P, _P, _P, _I64, _I32,
+     ctypes.POINTER(AttnRulesStruct), _P, ctypes.c_size_t, ctypes.c_float, _P, _P)
+_sig("rx_attn_decode_rules_fp8", ctypes.c_int, ctypes.POINTER(KVPoolFp8), _P, _P, _P, _I32, _P, _P, _P, _I64, _I32,
+     ctypes.POINTER(AttnRulesStruct), _P, ctypes.c_size_t, ctypes.c_float, _P, _P)
+_sig("rx_attn_rules_workspace", ctypes.c_size_t, _I64, _I32, _I32, _I32, _I32, _I32)
+_sig("rx_qk_rope_axes_store", ctypes.c_int, ctypes.POINTER(KVPool), _P, _I64, _P, _P, _P, _I64, _I32, _P, _P, _P, _P, _I64,
+     _I32, _P, _I64, _I32, ctypes.c_double, ctypes.c_float, _P, _P)
+_sig("rx_qk_rope_axes_store_fp8", ctypes.c_int, ctypes.POINTER(KVPoolFp8), _P, _I64, _P, _P, _P, _I64, _I32, _P, _P, _P, _P,
+     _I64, _I32, _P, _I64, _I32, ctypes.c_double, ctypes.c_float, _P, _P)
+_sig("rx_step_maps", ctypes.c_int, _P, _P, _P, _I32, _P, _I64, _P, _I64, _I32, _I64, _P, _P, _P, _P, _I64, _P, _P)
 _sig("rx_kv_store", ctypes.c_int, ctypes.POINTER(KVPool), _P, _P, _P, _I64, _P, _P)
 _sig("rx_rope", ctypes.c_int, _P, _P, _I64, _I32, _I32, ctypes.c_double, _P)
 _sig("rx_kv_store_rope", ctypes.c_int, ctypes.POINTER(KVPool), _P, _P, _P, _P, _I64, ctypes.c_double, _P, _P)
@@ -1038,3 +1058,244 @@ def rx_logits_process(rules: LogitsRules, logits, out, dev_status=None, stream=N
         raise ValueError("rx_logits_process: logits, out, draft_tok, tree_mask and allow_row must have the same rows")
     _check(_lib.rx_logits_process(ctypes.byref(rules.struct), _ptr(logits), int(logits.dtype == torch.bfloat16), ls,
                                   _ptr(out), os_, rows, _ptr(dev_status), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# attention with rules on the scores, rotation on several axes, the lists of a
+# step
+# ---------------------------------------------------------------------------
+
+
+def _here(t, name):
+    """The launch goes to the current device: its tensors have to be there."""
+    if t.get_device() != _torch()._C._cuda_getDevice():
+        raise ValueError(f"{name}: must be on the current CUDA device")
+
+
+class AttnRules:
+    """What the calls with rules apply to the scores (rx_attn_rules): cap > 0
+    caps them (cap * tanh(s / cap)), window > 0 bounds how far back a token sees,
+    slopes fp32 [num_q_heads] lower them by slopes[h] a position of distance,
+    see_from and see_to int32 [query tokens] bound what a token sees.  CUDA
+    tensors, each optional, kept alive here; their contents may change between
+    calls, their sizes may not."""
+
+    def __init__(self, cap: float = 0.0, window: int = 0, slopes=None, see_from=None, see_to=None):
+        torch = _torch()
+        _dev(slopes, torch.float32, "slopes")
+        _dev(see_from, torch.int32, "see_from")
+        _dev(see_to, torch.int32, "see_to")
+        if not 0 <= int(window) <= 0x7FFFFFFF:
+            raise ValueError("AttnRules: window must be in 0 .. 2^31 - 1")
+        self.cap, self.window = float(cap), int(window)
+        self.slopes, self.see_from, self.see_to = slopes, see_from, see_to
+        self.struct = AttnRulesStruct(self.cap, self.window, _ptr(slopes), _ptr(see_from), _ptr(see_to))
+        self._ref = ctypes.byref(self.struct)
+
+    def _check(self, tokens: int, heads: int):
+        if self.slopes is not None and self.slopes.numel() != heads:
+            raise ValueError("AttnRules: slopes must have an entry for each q head")
+        for t in (self.see_from, self.see_to):
+            if t is not None and t.numel() < tokens:
+                raise ValueError("AttnRules: see_from and see_to must have an entry for each query token")
+        return self._ref
+
+
+def rx_attn_rules_workspace(total_ctx_tokens: int, batch: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
+                            max_extend_len: int = 1) -> int:
+    """Workspace bytes for the calls with rules: contexts that sum to at most
+    total_ctx_tokens (0 for decode), up to max_extend_len new tokens a request."""
+    n = _lib.rx_attn_rules_workspace(int(total_ctx_tokens), int(batch), int(num_q_heads), int(num_kv_heads), int(head_dim),
+                                     int(max_extend_len))
+    if n == 0:
+        raise RxError(RX_ERR_INVALID, last_error())
+    return int(n)
+
+
+def _rules_args(q, o, lse, lists, req_to_token, rules, workspace, dev_status, head_dim):
+    torch = _torch()
+    i32 = torch.int32
+    _dev(q, torch.bfloat16, "q")
+    _dev(o, torch.bfloat16, "o")
+    _dev(lse, torch.float32, "lse")
+    for name, t in lists:
+        _dev(t, i32, name)
+    _dev(req_to_token, i32, "req_to_token")
+    _dev(workspace, torch.uint8, "workspace")
+    _dev(dev_status, i32, "dev_status")
+    _here(q, "q")
+    if not isinstance(rules, AttnRules):
+        raise TypeError("rules: expected an AttnRules")
+    if q.dim() != 3 or q.shape != o.shape or q.shape[2] != head_dim:
+        raise ValueError("q and o must be [tokens, num_q_heads, head_dim], head_dim that of the pools")
+    if lse is not None and lse.shape != q.shape[:2]:
+        raise ValueError("lse must be [tokens, num_q_heads]")
+    if req_to_token.dim() != 2:
+        raise ValueError("req_to_token must be [requests, stride]")
+    return rules._check(q.shape[0], q.shape[1]), 0 if workspace is None else workspace.numel()
+
+
+def _bf16_pool(k_pool, v_pool, layer):
+    pool = make_pool(k_pool, v_pool, layer)
+    return ctypes.byref(pool), pool.head_dim
+
+
+def _fp8_pool(k_pool, v_pool, k_scale, v_scale, layer):
+    torch = _torch()
+    _dev(k_pool, torch.uint8, "k_pool")
+    _dev(v_pool, torch.uint8, "v_pool")
+    S, hkv, d, L = _pool_dims(k_pool, v_pool, layer)
+    return ctypes.byref(KVPoolFp8(k_pool.data_ptr(), v_pool.data_ptr(), S, hkv, d, float(k_scale), float(v_scale), L,
+                                  int(layer))), d
+
+
+def _extend_rules(call, pool, d, q, o, lse, qo_indptr, req_idx, prefix_len, extend_len, req_to_token, max_extend_len,
+                  sm_scale, rules, workspace, dev_status, stream):
+    ref, ws_bytes = _rules_args(q, o, lse, (("qo_indptr", qo_indptr), ("req_idx", req_idx), ("prefix_len", prefix_len),
+                                            ("extend_len", extend_len)), req_to_token, rules, workspace, dev_status, d)
+    B = req_idx.numel()
+    if qo_indptr.numel() != B + 1 or prefix_len.numel() != B or extend_len.numel() != B:
+        raise ValueError("qo_indptr must be [batch + 1], prefix_len and extend_len [batch]")
+    if B == 0 or q.shape[0] == 0:
+        return  # empty tensors have no address; there is nothing to do
+    _check(call(pool, _ptr(q), _ptr(o), _ptr(lse), q.shape[1], _ptr(qo_indptr), _ptr(req_idx), _ptr(prefix_len),
+                _ptr(extend_len), _ptr(req_to_token), req_to_token.shape[1], B, int(max_extend_len), ref, _ptr(workspace),
+                ws_bytes, float(sm_scale), _ptr(dev_status), _stream(stream)))
+
+
+def rx_attn_extend_rules(k_pool, v_pool, q, o, lse, qo_indptr, req_idx, prefix_len, extend_len, req_to_token,
+                         max_extend_len: int, sm_scale: float, rules: AttnRules, workspace, dev_status=None, stream=None,
+                         layer: int = 0) -> None:
+    """rx_attn_extend with rules on the scores; workspace: uint8, at least
+    rx_attn_rules_workspace(...) bytes.  Without query tokens (no rows of q) or
+    requests the call does nothing."""
+    pool, d = _bf16_pool(k_pool, v_pool, layer)
+    _extend_rules(_lib.rx_attn_extend_rules, pool, d, q, o, lse, qo_indptr, req_idx, prefix_len, extend_len, req_to_token,
+                  max_extend_len, sm_scale, rules, workspace, dev_status, stream)
+
+
+def rx_attn_extend_rules_fp8(k_pool, v_pool, k_scale: float, v_scale: float, q, o, lse, qo_indptr, req_idx, prefix_len,
+                             extend_len, req_to_token, max_extend_len: int, sm_scale: float, rules: AttnRules, workspace,
+                             dev_status=None, stream=None, layer: int = 0) -> None:
+    """rx_attn_extend_rules over uint8 E4M3 pools ([L,] S, Hkv, d) with per-pool scales."""
+    pool, d = _fp8_pool(k_pool, v_pool, k_scale, v_scale, layer)
+    _extend_rules(_lib.rx_attn_extend_rules_fp8, pool, d, q, o, lse, qo_indptr, req_idx, prefix_len, extend_len,
+                  req_to_token, max_extend_len, sm_scale, rules, workspace, dev_status, stream)
+
+
+def _decode_rules(call, pool, d, q, o, lse, req_idx, seq_len, req_to_token, sm_scale, rules, workspace, dev_status, stream):
+    ref, ws_bytes = _rules_args(q, o, lse, (("req_idx", req_idx), ("seq_len", seq_len)), req_to_token, rules, workspace,
+                                dev_status, d)
+    B = req_idx.numel()
+    if q.shape[0] != B or seq_len.numel() != B:
+        raise ValueError("q must be [batch, num_q_heads, head_dim] and seq_len [batch]")
+    if B == 0:
+        return
+    _check(call(pool, _ptr(q), _ptr(o), _ptr(lse), q.shape[1], _ptr(req_idx), _ptr(seq_len), _ptr(req_to_token),
+                req_to_token.shape[1], B, ref, _ptr(workspace), ws_bytes, float(sm_scale), _ptr(dev_status),
+                _stream(stream)))
+
+
+def rx_attn_decode_rules(k_pool, v_pool, q, o, lse, req_idx, seq_len, req_to_token, sm_scale: float, rules: AttnRules,
+                         workspace, dev_status=None, stream=None, layer: int = 0) -> None:
+    """Decode attention (one token a request) with rules on the scores;
+    workspace: uint8, at least rx_attn_rules_workspace(0, batch, ...) bytes."""
+    pool, d = _bf16_pool(k_pool, v_pool, layer)
+    _decode_rules(_lib.rx_attn_decode_rules, pool, d, q, o, lse, req_idx, seq_len, req_to_token, sm_scale, rules,
+                  workspace, dev_status, stream)
+
+
+def rx_attn_decode_rules_fp8(k_pool, v_pool, k_scale: float, v_scale: float, q, o, lse, req_idx, seq_len, req_to_token,
+                             sm_scale: float, rules: AttnRules, workspace, dev_status=None, stream=None,
+                             layer: int = 0) -> None:
+    """rx_attn_decode_rules over uint8 E4M3 pools ([L,] S, Hkv, d) with per-pool scales."""
+    pool, d = _fp8_pool(k_pool, v_pool, k_scale, v_scale, layer)
+    _decode_rules(_lib.rx_attn_decode_rules_fp8, pool, d, q, o, lse, req_idx, seq_len, req_to_token, sm_scale, rules,
+                  workspace, dev_status, stream)
+
+
+def _axes_call(call, pool, dims, q, q_out, k_new, v_new, q_weight, k_weight, slots, pos, pair_axis, base, eps, dev_status,
+               stream):
+    torch = _torch()
+    S, hkv, dim, L = dims
+    n, hq, d, qs = _head_rows(q, "q")
+    new, v_row = _head_rows(k_new, "k_new"), _head_rows(v_new, "v_new")
+    _dev(q_out, torch.bfloat16, "q_out")
+    _dev(q_weight, torch.bfloat16, "q_weight")
+    _dev(k_weight, torch.bfloat16, "k_weight")
+    _dev(slots, torch.int32, "slots")
+    _dev(pos, torch.int32, "pos")
+    _dev(dev_status, torch.int32, "dev_status")
+    _here(q, "q")
+    if new[:3] != (slots.numel(), hkv, dim) or v_row[:3] != new[:3]:
+        raise ValueError("k_new/v_new must be [n, num_kv_heads, head_dim] and slots [n]")
+    if pos.dim() != 2 or pos.shape[1] != n:
+        raise ValueError("pos must be [axes, n]")
+    if n != new[0] or d != dim or q_out.shape != q.shape:
+        raise ValueError("q and q_out must be [n, num_q_heads, head_dim]")
+    if new[3] != v_row[3]:
+        raise ValueError("k_new and v_new must have the same row stride")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None and w.numel() != d:
+            raise ValueError(f"{name} must be [head_dim]")
+    if isinstance(pair_axis, torch.Tensor):
+        if pair_axis.is_cuda or pair_axis.dtype != torch.uint8 or not pair_axis.is_contiguous():
+            raise TypeError("pair_axis: expected a contiguous uint8 host tensor")
+        size, axis = pair_axis.numel(), pair_axis.data_ptr()
+    else:
+        pair_axis, axis = _np(pair_axis, np.uint8)
+        size = pair_axis.size
+    if size != d // 2:
+        raise ValueError("pair_axis must have head_dim / 2 entries")
+    _check(call(pool, _ptr(q), qs, _ptr(q_out), _ptr(k_new), _ptr(v_new), new[3], 0 if eps is None else 1, _ptr(q_weight),
+                _ptr(k_weight), _ptr(slots), _ptr(pos), n, pos.shape[0], axis, n, hq, float(base),
+                0.0 if eps is None else float(eps), _ptr(dev_status), _stream(stream)))
+
+
+def rx_qk_rope_axes_store(k_pool, v_pool, q, q_out, k_new, v_new, q_weight, k_weight, slots, pos, pair_axis, base: float,
+                          eps: Optional[float] = None, dev_status=None, stream=None, layer: int = 0) -> None:
+    """Rotation of every q and k head with positions on several axes (pos int32
+    [axes, n]; pair_axis: the axis of each of the head_dim / 2 pairs, a uint8
+    host array), after an RMS norm where eps is given (weights bf16 [d] or None),
+    q into q_out, K and V into the pool.  q, k_new, v_new as in
+    rx_qk_norm_rope_store."""
+    torch = _torch()
+    _dev(k_pool, torch.bfloat16, "k_pool")
+    _dev(v_pool, torch.bfloat16, "v_pool")
+    dims = _pool_dims(k_pool, v_pool, 0)
+    S, hkv, d, L = dims
+    pool = KVPool(k_pool.data_ptr(), v_pool.data_ptr(), S, hkv, d, L, int(layer))
+    _axes_call(_lib.rx_qk_rope_axes_store, ctypes.byref(pool), dims, q, q_out, k_new, v_new, q_weight, k_weight, slots, pos,
+               pair_axis, base, eps, dev_status, stream)
+
+
+def rx_qk_rope_axes_store_fp8(k_pool, v_pool, k_scale: float, v_scale: float, q, q_out, k_new, v_new, q_weight, k_weight,
+                              slots, pos, pair_axis, base: float, eps: Optional[float] = None, dev_status=None, stream=None,
+                              layer: int = 0) -> None:
+    """rx_qk_rope_axes_store into uint8 E4M3 pools ([L,] S, Hkv, d) with per-pool scales."""
+    pool, _ = _fp8_pool(k_pool, v_pool, k_scale, v_scale, layer)
+    _axes_call(_lib.rx_qk_rope_axes_store_fp8, pool, _pool_dims(k_pool, v_pool, 0), q, q_out, k_new, v_new, q_weight,
+               k_weight, slots, pos, pair_axis, base, eps, dev_status, stream)
+
+
+def rx_step_maps(req_idx, prefix_len, new_len, req_to_token, num_slots: int, qo_indptr, seq_len, pos, slots, pages=None,
+                 page_size: int = 0, dev_status=None, stream=None) -> None:
+    """The lists of a step from the requests' lengths: qo_indptr int32 [batch + 1],
+    seq_len int32 [batch] or None, pos and slots int32 [tokens].  pages int32
+    [requests, pages] of page_size slots each: slots come from them and are
+    written to req_to_token."""
+    i32 = _torch().int32
+    for t, name in ((req_idx, "req_idx"), (prefix_len, "prefix_len"), (new_len, "new_len"), (req_to_token, "req_to_token"),
+                    (qo_indptr, "qo_indptr"), (seq_len, "seq_len"), (pos, "pos"), (slots, "slots"), (pages, "pages"),
+                    (dev_status, "dev_status")):
+        _dev(t, i32, name)
+    _here(qo_indptr, "qo_indptr")
+    B, n = req_idx.numel(), pos.numel()
+    if prefix_len.numel() != B or new_len.numel() != B or qo_indptr.numel() != B + 1 or \
+            (seq_len is not None and seq_len.numel() != B) or slots.numel() != n:
+        raise ValueError("prefix_len, new_len and seq_len must be [batch], qo_indptr [batch + 1], pos and slots [tokens]")
+    if req_to_token.dim() != 2 or (pages is not None and (pages.dim() != 2 or pages.shape[0] != req_to_token.shape[0])):
+        raise ValueError("req_to_token must be [requests, stride] and pages [requests, pages]")
+    _check(_lib.rx_step_maps(_ptr(req_idx), _ptr(prefix_len), _ptr(new_len), B, _ptr(req_to_token), req_to_token.shape[1],
+                             _ptr(pages), 0 if pages is None else pages.shape[1], int(page_size), int(num_slots),
+                             _ptr(qo_indptr), _ptr(seq_len), _ptr(pos), _ptr(slots), n, _ptr(dev_status), _stream(stream)))

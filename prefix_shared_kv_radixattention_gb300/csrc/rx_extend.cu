@@ -49,6 +49,8 @@
 
 #include "rx_common.cuh"
 #include "rx_pipe.cuh"
+#include "rx_rules.cuh"
+#include "rx_split.h"
 
 namespace {
 
@@ -132,6 +134,9 @@ struct XParams {  // 64-byte aligned through its tensor maps
     float scale_log2;       // sm_scale log2(e), times K's scale for an FP8 pool
     float v_scale;          // V's scale for an FP8 pool (multiplies o); 1 otherwise
     int32_t *status;
+    // calls with rules on the scores (staged path)
+    rx::Rules rules;
+    const int32_t *stage_nf;  // [0]: some staged V was not finite; [1 + t]: some of the packed row tile t
 };
 
 struct Tile {
@@ -140,7 +145,9 @@ struct Tile {
     int64_t qbase;     // packed token index of row group 0
     int row0_pos;      // absolute position of row group 0
     int kv_end;        // keys [0, kv_end)
+    int ctx;           // the request's positions
     int ntiles;
+    int first;         // position tiles before the first one that a row sees (0 without rules)
     int stage_row0;    // staged path: first packed row of this request's own tiles
     int share_tiles;   // staged path: leading tiles read from another request's rows
     int share_row0;    // ... which start at this packed row
@@ -272,7 +279,7 @@ __device__ void producer(const XParams &p, const Tile &T, unsigned char *smem, u
 // 128-byte column block, each box kBN rows of one kv head.  Every packed
 // region is a whole number of kBN-row tiles with zeroed padding, so the boxes
 // never leave the request's region.
-template <int D>
+template <int D, bool RU>
 __device__ void tma_producer(const XParams &p, const Tile &T, unsigned char *smem, uint32_t sbase)
 {
     using L = XL<D>;
@@ -282,7 +289,8 @@ __device__ void tma_producer(const XParams &p, const Tile &T, unsigned char *sme
     for (int j = 0; j < T.ntiles; ++j) {
         const int st = j % kStages;
         // leading tiles shared with an earlier request come from its rows
-        const int row = j < T.share_tiles ? T.share_row0 + j * kBN : T.stage_row0 + (j - T.share_tiles) * kBN;
+        const int jt = RU ? T.first + j : j;
+        const int row = jt < T.share_tiles ? T.share_row0 + jt * kBN : T.stage_row0 + (jt - T.share_tiles) * kBN;
         bool stop = false;
 #pragma unroll
         for (int w = 0; w < 2; ++w) {  // K into its stage once S freed it, then V
@@ -388,7 +396,35 @@ __device__ void mma_issuer(const XParams &p, const Tile &T, unsigned char *smem,
 // softmax warps: one query row per thread
 // ---------------------------------------------------------------------------
 
+// With rules: the NaN and infinities of V at the positions lo .. hi - 1 that a
+// row sees, which staging dropped and noted for each tile, added to its o.
 template <int D>
+__device__ __noinline__ void add_not_finite(const XParams &p, const Tile &T, int lo, int hi, int64_t orow)
+{
+    for (int pos = lo; pos < hi; ++pos) {
+        const int jt = pos / kBN;
+        const int row = jt < T.share_tiles ? T.share_row0 + jt * kBN : T.stage_row0 + (jt - T.share_tiles) * kBN;
+        if (__ldg(p.stage_nf + 1 + row / kBN) == 0) {
+            pos = jt * kBN + kBN - 1;
+            continue;
+        }
+        const int64_t slot = __ldg(T.slots + pos);
+        if (slot < 0 || slot >= p.num_slots) continue;
+        const int64_t at = (slot * p.hkv + T.g) * D;
+        for (int i = 0; i < D; ++i) {
+            float v;
+            if (p.v8) {
+                const uint32_t h = rx::e4m3x2_to_f16x2(__ldg(p.v8 + at + i));
+                v = __half2float(__ushort_as_half((unsigned short)(h & 0xFFFFu)));
+            } else {
+                v = __bfloat162float(p.v_pool[at + i]);
+            }
+            if (!isfinite(v)) p.o[orow * D + i] = __float2bfloat16_rn(__bfloat162float(p.o[orow * D + i]) + v);
+        }
+    }
+}
+
+template <int D, bool RU>
 __device__ void softmax_rows(const XParams &p, const Tile &T, unsigned char *smem, uint32_t sbase,
                              uint32_t tmem)
 {
@@ -405,6 +441,13 @@ __device__ void softmax_rows(const XParams &p, const Tile &T, unsigned char *sme
     const uint32_t tO = tbase + 128;
     const int row_lim = T.row0_pos + row / p.G;   // keys at positions <= row_lim are visible
     const float sl2 = p.scale_log2;
+    // with rules: the positions [lo, hi) that the row sees, its head's slope
+    int lo = 0, hi = INT_MAX;
+    float slope = 0.f;
+    if (RU && row < T.M) {
+        rx::seen_range(p.rules, (int)T.qbase + row / p.G, row_lim, T.ctx, lo, hi);
+        if (p.rules.slope) slope = __ldg(p.rules.slope + (int64_t)T.g * p.G + row % p.G) * rx::kLog2e;
+    }
     {
         // this tile's Q rows (CTA row r: token r / G, q head g G + r % G) with
         // coalesced 16-byte copies by the tile's four warps, zeros past the
@@ -424,16 +467,16 @@ __device__ void softmax_rows(const XParams &p, const Tile &T, unsigned char *sme
         rx::fence_proxy_async_smem();
         rx::mbar_arrive(bar + 8 * (L::B_QFULL + t));
     }
-    float m_used = -INFINITY, l = 0.f;
+    float m_used = RU && p.rules.fixed ? p.rules.base : -INFINITY, l = 0.f;
     const uint32_t tS = tbase;  // S_t(j), then P_t(j) over its first kBN / 2 columns
     for (int j = 0; j < T.ntiles; ++j) {
         if (!warp_wait(bar + 8 * (L::B_SFULL + t), j & 1, abort_flag, p.status)) return;
         rx::tc_fence_after();
-        const int kbase = j * kBN;
+        const int kbase = (RU ? T.first + j : j) * kBN;
         // one answer per warp: the masked and unmasked passes below hold
         // different warp-collective tcgen05.ld instructions, so all lanes of
         // a warp must take the same one (the masked pass is exact for every row)
-        const bool need_mask = __any_sync(0xffffffffu, kbase + kBN - 1 > row_lim);
+        const bool need_mask = __any_sync(0xffffffffu, RU ? kbase < lo || kbase + kBN > hi : kbase + kBN - 1 > row_lim);
         // the tile's kBN scores of this row, loaded once (four loads in
         // flight) and kept in registers for the max and the exponentials;
         // the causal test only on tiles that cross the row's bound
@@ -442,15 +485,19 @@ __device__ void softmax_rows(const XParams &p, const Tile &T, unsigned char *sme
         for (int c = 0; c < kBN / 32; ++c)
             rx::tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * c));
         rx::tmem_wait_ld();
-        if (need_mask) {
+        float left = sl2;  // what the scores are still to be multiplied with
+        if constexpr (RU) {
+            left = rx::apply_rules(sv, p.rules, sl2, slope, row_lim - kbase);
+            if (need_mask) rx::hide(sv, kbase, lo, hi);
+        } else if (need_mask) {
 #pragma unroll
             for (int k = 0; k < kBN; ++k)
                 if (kbase + k > row_lim) sv[k] = __float_as_uint(-INFINITY);
         }
         // the row max: four running three-input maxima (few live registers
         // next to the kBN scores)
-        float mx;
-        {
+        float mx = -INFINITY;
+        if (!RU || !p.rules.fixed) {
             float a0 = -INFINITY, a1 = -INFINITY, a2 = -INFINITY, a3 = -INFINITY;
 #pragma unroll
             for (int k = 0; k < kBN / 8; ++k) {
@@ -461,8 +508,8 @@ __device__ void softmax_rows(const XParams &p, const Tile &T, unsigned char *sme
             }
             mx = rx::fmax3(fmaxf(a0, a1), a2, a3);
         }
-        const float m_new = fmaxf(m_used, mx * sl2);
-        const bool need = (m_used == -INFINITY) || (m_new > m_used + kRescale);
+        const float m_new = fmaxf(m_used, mx * left);
+        const bool need = (!RU || !p.rules.fixed) && ((m_used == -INFINITY) || (m_new > m_used + kRescale));
         const float alpha = (need && m_used != -INFINITY) ? rx::fast_exp2(m_used - m_new) : 1.f;
         if (need) {
             l *= alpha;
@@ -473,8 +520,8 @@ __device__ void softmax_rows(const XParams &p, const Tile &T, unsigned char *sme
         // sum in four packed accumulators.  (Measured: moving a share of the
         // exponentials to a polynomial on the FMA pipe is slower here, since
         // the softmax is bound by issue and the ALU pipe, not the exp unit.)
-        const float mu = (m_used == -INFINITY) ? 0.f : m_used;
-        const uint64_t scale2 = rx::f2(sl2, sl2), negm2 = rx::f2(-mu, -mu);
+        const float mu = (m_used == -INFINITY || (RU && p.rules.fixed)) ? 0.f : m_used;
+        const uint64_t scale2 = rx::f2(left, left), negm2 = rx::f2(-mu, -mu);
         uint64_t acc[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int c2 = 0; c2 < kBN / 64; ++c2) {
@@ -522,7 +569,7 @@ __device__ void softmax_rows(const XParams &p, const Tile &T, unsigned char *sme
     const bool valid = row < T.M;
     const int G = p.G;
     const int64_t orow = (T.qbase + row / G) * p.hq + (int64_t)T.g * G + row % G;
-    const float inv = p.v_scale / l;
+    const float inv = RU && l == 0.f ? 0.f : p.v_scale / l;
 #pragma unroll
     for (int c4 = 0; c4 < D / 32; ++c4) {
         uint32_t r[32];
@@ -541,10 +588,11 @@ __device__ void softmax_rows(const XParams &p, const Tile &T, unsigned char *sme
             }
         }
     }
-    if (valid && p.lse) p.lse[orow] = (m_used + log2f(l)) * rx::kLn2;
+    if (valid && p.lse) p.lse[orow] = RU && l == 0.f ? -INFINITY : (m_used + log2f(l)) * rx::kLn2;
+    if (RU && valid && __ldg(p.stage_nf)) add_not_finite<D>(p, T, lo, hi, orow);
 }
 
-template <int D, bool kStaged, bool F8 = false>
+template <int D, bool kStaged, bool F8 = false, bool RU = false>
 __global__ void __launch_bounds__(kStaged ? kStagedThreads : kThreads, 1)
     extend_kernel(const __grid_constant__ XParams p)
 {
@@ -584,13 +632,39 @@ __global__ void __launch_bounds__(kStaged ? kStagedThreads : kThreads, 1)
         T.stage_row0 = (int)p.stage_offs[b];
         T.share_tiles = p.stage_share[b];
         T.share_row0 = (int)p.stage_offs[p.stage_src[b]];
+        if constexpr (RU) {
+            // nothing before the window of a request's first new token is staged
+            const int f = rx::window_from(p.rules, (int)P) / kBN, src = p.stage_src[b];
+            T.share_row0 -= rx::window_from(p.rules, __ldg(p.prefix_len + src)) / kBN * kBN;
+            T.stage_row0 -= max(f - T.share_tiles, 0) * kBN;
+        }
     }
     T.M = ntok * p.G;
     T.nqt = T.M > kRows ? 2 : 1;
     T.qbase = (int64_t)__ldg(p.qo_indptr + b) + t0;
     T.row0_pos = (int)(P + t0);
     T.kv_end = (int)(P + t0 + ntok);
-    T.ntiles = (T.kv_end + kBN - 1) / kBN;
+    T.first = 0;
+    T.ctx = (int)(P + E);
+    if constexpr (RU) {
+        // what the CTA's tokens see together: positions from `least` up to `most`
+        __shared__ int least, most;
+        if (threadIdx.x == 0) {
+            least = INT_MAX;
+            most = T.kv_end;
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < ntok; i += blockDim.x) {
+            int lo, hi;
+            rx::seen_range(p.rules, (int)T.qbase + i, T.row0_pos + i, T.ctx, lo, hi);
+            atomicMin(&least, lo);
+            if (p.rules.see_to) atomicMax(&most, hi);
+        }
+        __syncthreads();
+        T.kv_end = most;
+        T.first = min(least, T.kv_end - 1) / kBN;  // one tile at least
+    }
+    T.ntiles = (T.kv_end + kBN - 1) / kBN - T.first;
     T.slots = p.rtt + (int64_t)__ldg(p.req_idx + b) * p.rtt_stride;
 
     const uint32_t bar = sbase + L::OFF_BAR;
@@ -622,13 +696,13 @@ __global__ void __launch_bounds__(kStaged ? kStagedThreads : kThreads, 1)
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::OFF_TMEM);
 
     if (warp < 8) {
-        softmax_rows<D>(p, T, smem, sbase, tmem);
+        softmax_rows<D, RU>(p, T, smem, sbase, tmem);
     } else {
         if (warp < mma_warp) {
             if (!kStaged) {
                 producer<D, F8>(p, T, smem, sbase);
             } else if (warp == kStagedProducerWarp) {
-                if ((threadIdx.x & 31) == 0) tma_producer<D>(p, T, smem, sbase);
+                if ((threadIdx.x & 31) == 0) tma_producer<D, RU>(p, T, smem, sbase);
                 __syncwarp();
             }
         } else {
@@ -651,6 +725,12 @@ __global__ void __launch_bounds__(kStaged ? kStagedThreads : kThreads, 1)
 
 // Packed rows of request b: its context (prefix + extend tokens) rounded up
 // to whole kBN-row tiles; none for lengths the attention kernel rejects.
+// With a window (INT_MAX: none) a request's tiles count from the first one that
+// its first new token sees.
+__device__ __forceinline__ int window_tile(int64_t P, int window)
+{
+    return P >= window ? (int)((P - window + 1) / kBN) : 0;
+}
 __device__ __forceinline__ int64_t staged_rows(const int32_t *prefix_len, const int32_t *extend_len, int b,
                                                int64_t rtt_stride)
 {
@@ -674,7 +754,7 @@ __global__ void __launch_bounds__(kBN) stage_share_kernel(const int32_t *__restr
                                                          const int32_t *__restrict__ req_idx,
                                                          const int32_t *__restrict__ prefix_len,
                                                          const int32_t *__restrict__ extend_len, int32_t *src,
-                                                         int32_t *share)
+                                                         int32_t *share, int window)
 {
     __shared__ int first, diff;
     const int b = blockIdx.x, t = threadIdx.x;
@@ -713,6 +793,11 @@ __global__ void __launch_bounds__(kBN) stage_share_kernel(const int32_t *__restr
         tiles = min(ntile, diff);
     }
     if (t == 0) {
+        // r has b's first tile, and they share tiles from there on
+        if (tiles > 0) {
+            const int f = window_tile(__ldg(prefix_len + b), window);
+            if (window_tile(__ldg(prefix_len + r), window) > f || tiles <= f) tiles = 0;
+        }
         src[b] = tiles > 0 ? r : b;
         share[b] = tiles;
     }
@@ -725,7 +810,8 @@ __global__ void __launch_bounds__(kBN) stage_share_kernel(const int32_t *__restr
 // anything.
 __global__ void __launch_bounds__(1024) ctx_offsets_kernel(const int32_t *prefix_len, const int32_t *extend_len,
                                                            const int32_t *share, int batch, int64_t rtt_stride,
-                                                           int64_t cap, int64_t *offs, int32_t *status)
+                                                           int64_t cap, int64_t *offs, int32_t *status, int window,
+                                                           int32_t *nf)
 {
     __shared__ int64_t warp_tot[32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -733,9 +819,13 @@ __global__ void __launch_bounds__(1024) ctx_offsets_kernel(const int32_t *prefix
     rx::pdl_wait();  // the share counts are written by the kernel before this one
     const int per = (batch + 1023) / 1024;
     const int b0 = threadIdx.x * per;
+    // rows of request b's own tiles: those neither shared nor before the window
+    auto own_rows = [&](int b) {
+        const int64_t rows = staged_rows(prefix_len, extend_len, b, rtt_stride);
+        return rows == 0 ? 0 : rows - (int64_t)max(share[b], window_tile(__ldg(prefix_len + b), window)) * kBN;
+    };
     int64_t local = 0;
-    for (int i = 0; i < per && b0 + i < batch; ++i)
-        local += staged_rows(prefix_len, extend_len, b0 + i, rtt_stride) - (int64_t)share[b0 + i] * kBN;
+    for (int i = 0; i < per && b0 + i < batch; ++i) local += own_rows(b0 + i);
     // inclusive scan over the block: within each warp, then over warp totals
     int64_t x = local;
 #pragma unroll
@@ -758,8 +848,11 @@ __global__ void __launch_bounds__(1024) ctx_offsets_kernel(const int32_t *prefix
     int64_t run = x - local + (warp > 0 ? warp_tot[warp - 1] : 0);  // exclusive
     for (int i = 0; i < per && b0 + i < batch; ++i) {
         offs[b0 + i] = run;
-        run += staged_rows(prefix_len, extend_len, b0 + i, rtt_stride) - (int64_t)share[b0 + i] * kBN;
+        run += own_rows(b0 + i);
     }
+    // with rules: no tile noted yet
+    if (nf && warp_tot[31] <= cap)
+        for (int64_t i = threadIdx.x; i <= warp_tot[31] / kBN; i += 1024) nf[i] = 0;
     if (threadIdx.x == 1023) {
         const int64_t total = warp_tot[31];
         offs[batch] = total;
@@ -774,13 +867,16 @@ __global__ void __launch_bounds__(1024) ctx_offsets_kernel(const int32_t *prefix
 // region is a multiple of kBN rows, so a block never straddles two requests.
 // F8: the pools hold E4M3 codes (a byte a value), widened to bf16 on the way
 // (their scales are applied by the attention kernel).
-template <bool F8>
+// RU: with rules on the scores, NaN and infinities of V become 0 here, since they
+// would reach rows that do not see them (0 times them is NaN), and their tile is
+// noted in nf (see add_not_finite).
+template <bool F8, bool RU>
 __global__ void __launch_bounds__(256) stage_rows_kernel(
     const void *__restrict__ k_pool, const void *__restrict__ v_pool, int64_t num_slots,
     const int32_t *__restrict__ rtt, int64_t rtt_stride, const int32_t *__restrict__ req_idx,
     const int32_t *__restrict__ prefix_len, const int32_t *__restrict__ extend_len,
     const int32_t *__restrict__ share, int batch, const int64_t *__restrict__ offs, int64_t cap,
-    bf16 *__restrict__ ks, bf16 *__restrict__ vs, int row_elems, int32_t *status)
+    bf16 *__restrict__ ks, bf16 *__restrict__ vs, int row_elems, int32_t *status, int window, int32_t *nf)
 {
     rx::pdl_launch_dependents();
     rx::pdl_wait();  // the packed-row offsets are written by the kernel before this one
@@ -802,7 +898,7 @@ __global__ void __launch_bounds__(256) stage_rows_kernel(
         // owns it
         const int b = lo;
         const int64_t ctx = (int64_t)__ldg(prefix_len + b) + __ldg(extend_len + b);
-        const int64_t pos0 = row0 - offs[b] + (int64_t)share[b] * kBN;
+        const int64_t pos0 = row0 - offs[b] + (int64_t)(RU ? max(share[b], window_tile(__ldg(prefix_len + b), window)) : share[b]) * kBN;
         int32_t my_slot = -1;
         if (lane < kStageBlock && pos0 + lane < ctx) {
             const int32_t sl = __ldg(rtt + (int64_t)__ldg(req_idx + b) * rtt_stride + pos0 + lane);
@@ -830,6 +926,12 @@ __global__ void __launch_bounds__(256) stage_rows_kernel(
                         vv = __ldg(reinterpret_cast<const uint4 *>(vsrc) + v);
                     }
                 }
+                if constexpr (RU) {
+                    if (rx::drop_not_finite(vv)) {
+                        nf[0] = 1;
+                        nf[1 + row0 / kBN] = 1;
+                    }
+                }
                 kdst[v] = kv;
                 vdst[v] = vv;
             }
@@ -852,14 +954,15 @@ int check_pool(const rx_kv_pool *pool)
 // rows and the packed V rows, [cap][kv heads][head_dim] bf16 each, every
 // part 256-byte aligned.
 struct StageLayout {
-    size_t off_src, off_share, off_k, off_v, bytes;
+    size_t off_src, off_share, off_k, off_v, off_nf, bytes;
 };
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 size_t stage_head(int32_t batch)
 {
     return align256((size_t)(batch + 1) * sizeof(int64_t)) + 2 * align256((size_t)batch * sizeof(int32_t));
 }
-StageLayout stage_layout(int64_t cap, int32_t batch, int64_t row_bytes)
+// with rules, also a word a tile for its V and one for all
+StageLayout stage_layout(int64_t cap, int32_t batch, int64_t row_bytes, bool rules)
 {
     StageLayout l;
     l.off_src = align256((size_t)(batch + 1) * sizeof(int64_t));
@@ -867,17 +970,19 @@ StageLayout stage_layout(int64_t cap, int32_t batch, int64_t row_bytes)
     l.off_k = stage_head(batch);
     const size_t region = align256((size_t)cap * (size_t)row_bytes);
     l.off_v = l.off_k + region;
-    l.bytes = l.off_v + region;
+    l.off_nf = l.off_v + region;
+    l.bytes = l.off_nf + (rules ? align256((size_t)(cap / kBN + 2) * sizeof(int32_t)) : 0);
     return l;
 }
 // largest row count a workspace of ws_bytes holds (TMA row coordinates are int32)
-int64_t stage_cap_for(size_t ws_bytes, int32_t batch, int64_t row_bytes)
+int64_t stage_cap_for(size_t ws_bytes, int32_t batch, int64_t row_bytes, bool rules)
 {
     const size_t head = stage_head(batch);
     if (ws_bytes <= head) return 0;
-    int64_t cap = (int64_t)((ws_bytes - head) / 2 / (size_t)row_bytes);
+    int64_t cap = rules ? (int64_t)((double)(ws_bytes - head) / (2.0 * row_bytes + 4.0 / kBN)) + 1
+                        : (int64_t)((ws_bytes - head) / 2 / (size_t)row_bytes);
     cap = cap < (int64_t)INT32_MAX - 2 * kBN ? cap : (int64_t)INT32_MAX - 2 * kBN;
-    while (cap > 0 && stage_layout(cap, batch, row_bytes).bytes > ws_bytes) --cap;
+    while (cap > 0 && stage_layout(cap, batch, row_bytes, rules).bytes > ws_bytes) --cap;
     return cap;
 }
 
@@ -937,19 +1042,19 @@ int launch_dependent(void (*kernel)(KArgs...), dim3 grid, unsigned block, size_t
     return RX_OK;
 }
 
-template <int D, bool kStaged, bool F8 = false>
+template <int D, bool kStaged, bool F8 = false, bool RU = false>
 int launch_extend(const XParams &p, dim3 grid, cudaStream_t st)
 {
     static bool configured = false;
     if (!configured) {
-        RX_CUDA_CHECK(cudaFuncSetAttribute(extend_kernel<D, kStaged, F8>,
+        RX_CUDA_CHECK(cudaFuncSetAttribute(extend_kernel<D, kStaged, F8, RU>,
                                            cudaFuncAttributeMaxDynamicSharedMemorySize, XL<D>::BYTES));
         configured = true;
     }
     // staged: a programmatic dependent of the staging copy
     if (kStaged)
-        return launch_dependent(extend_kernel<D, kStaged, F8>, grid, kStagedThreads, XL<D>::BYTES, st, p);
-    extend_kernel<D, kStaged, F8><<<grid, kThreads, XL<D>::BYTES, st>>>(p);
+        return launch_dependent(extend_kernel<D, kStaged, F8, RU>, grid, kStagedThreads, XL<D>::BYTES, st, p);
+    extend_kernel<D, kStaged, F8, RU><<<grid, kThreads, XL<D>::BYTES, st>>>(p);
     RX_CUDA_CHECK(cudaGetLastError());
     return RX_OK;
 }
@@ -960,21 +1065,25 @@ namespace {
 
 // One layer of the pool an extend call reads: bf16 rows, or E4M3 codes with
 // a scale per pool.
-struct ExtendPool {
-    const void *k, *v;
-    int64_t num_slots;
-    int hkv, D;
-    bool f8;
-    float k_scale, v_scale;
-};
+using ExtendPool = RxAttnPool;
+
+// A call with rules whose query rows make fewer CTAs than this (of 256 rows
+// each) shares the contexts among CTAs instead (rx_tree.cu).
+constexpr int kSplitBelow = 152;
+
+bool few_rows(int32_t hq, int32_t hkv, int32_t batch, int32_t max_len)
+{
+    const int64_t rows = (int64_t)max_len * (hq / hkv);
+    return max_len <= RX_SPLIT_MAX_LEN && (rows + kCtaRows - 1) / kCtaRows * hkv * batch < kSplitBelow;
+}
 
 // rx_attn_extend and rx_attn_extend_fp8 after their pool checks (`who`
-// names the entry point in messages).
+// names the entry point in messages), and with rules their forms that have them.
 int extend_call(const char *who, const ExtendPool &pool, const void *q, void *o, float *lse, int32_t hq,
                 const int32_t *qo_indptr, const int32_t *req_idx, const int32_t *prefix_len,
                 const int32_t *extend_len, const int32_t *rtt, int64_t rtt_stride, int32_t batch,
                 int32_t max_extend_len, void *workspace, size_t ws_bytes, float sm_scale, int32_t *dev_status,
-                void *stream)
+                void *stream, const rx_attn_rules *rules = nullptr)
 {
     if (!q || !o || !qo_indptr || !req_idx || !prefix_len || !extend_len || !rtt ||
         rtt_stride <= 0 || rtt_stride > INT32_MAX || batch < 0 || hq <= 0 || max_extend_len < 0 ||
@@ -991,7 +1100,15 @@ int extend_call(const char *who, const ExtendPool &pool, const void *q, void *o,
                             (int)pool_align + 1);
     if (workspace && (reinterpret_cast<uintptr_t>(workspace) & 255) != 0)
         return rx_set_error(RX_ERR_INVALID, "%s: workspace must be 256-byte aligned", who);
+    rx::Rules ru{};
+    if (rules) {
+        if (const int rc = rx::make_rules(who, rules, sm_scale * pool.k_scale * rx::kLog2e, ru)) return rc;
+        if (!workspace) return rx_set_error(RX_ERR_CAPACITY, "%s: no workspace", who);
+    }
     if (batch == 0 || max_extend_len == 0) return RX_OK;
+    if (rules && few_rows(hq, pool.hkv, batch, max_extend_len))
+        return rx_split_rules(who, pool, q, o, lse, hq, qo_indptr, req_idx, prefix_len, extend_len, rtt, rtt_stride, batch,
+                              max_extend_len, workspace, ws_bytes, sm_scale, rules, dev_status, stream);
     if (batch > 65535 || pool.hkv > 65535)
         return rx_set_error(RX_ERR_UNSUPPORTED, "%s: batch or kv heads above 65535", who);
     XParams p{};
@@ -1028,9 +1145,9 @@ int extend_call(const char *who, const ExtendPool &pool, const void *q, void *o,
 
     // staged path: offsets, packed copy of every context, then attention
     const int64_t row_bytes = (int64_t)p.hkv * D * (int64_t)sizeof(bf16);
-    const int64_t cap = stage_cap_for(ws_bytes, batch, row_bytes);
+    const int64_t cap = stage_cap_for(ws_bytes, batch, row_bytes, rules != nullptr);
     if (cap < kBN) return rx_set_error(RX_ERR_CAPACITY, "%s: workspace of %zu bytes too small", who, ws_bytes);
-    const StageLayout lay = stage_layout(cap, batch, row_bytes);
+    const StageLayout lay = stage_layout(cap, batch, row_bytes, rules != nullptr);
     int64_t *offs = static_cast<int64_t *>(workspace);
     bf16 *ks = reinterpret_cast<bf16 *>(static_cast<char *>(workspace) + lay.off_k);
     bf16 *vs = reinterpret_cast<bf16 *>(static_cast<char *>(workspace) + lay.off_v);
@@ -1042,21 +1159,27 @@ int extend_call(const char *who, const ExtendPool &pool, const void *q, void *o,
     p.stage_src = src;
     p.stage_share = share;
     p.stage_cap = cap;
+    p.rules = ru;
+    int32_t *nf = rules ? reinterpret_cast<int32_t *>(static_cast<char *>(workspace) + lay.off_nf) : nullptr;
+    p.stage_nf = nf;
+    const int window = rules ? ru.window : INT_MAX;
     int dev = 0, sms = 0;
     RX_CUDA_CHECK(cudaGetDevice(&dev));
     RX_CUDA_CHECK(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev));
-    stage_share_kernel<<<batch, kBN, 0, st>>>(rtt, rtt_stride, req_idx, prefix_len, extend_len, src, share);
+    stage_share_kernel<<<batch, kBN, 0, st>>>(rtt, rtt_stride, req_idx, prefix_len, extend_len, src, share, window);
     RX_CUDA_CHECK(cudaGetLastError());
     // the offsets, the copy and the attention kernel are each a programmatic
     // dependent of the kernel before: each waits on the device for what it reads
     if ((rc = launch_dependent(ctx_offsets_kernel, dim3(1), 1024, 0, st, prefix_len, extend_len,
-                               (const int32_t *)share, batch, rtt_stride, cap, offs, dev_status)) != RX_OK)
+                               (const int32_t *)share, batch, rtt_stride, cap, offs, dev_status, window, nf)) != RX_OK)
         return rc;
-    auto stage = pool.f8 ? stage_rows_kernel<true> : stage_rows_kernel<false>;
+    auto stage = rules ? (pool.f8 ? stage_rows_kernel<true, true> : stage_rows_kernel<false, true>)
+                       : (pool.f8 ? stage_rows_kernel<true, false> : stage_rows_kernel<false, false>);
     if ((rc = launch_dependent(stage, dim3(sms * 8), 256, 0, st, pool.k, pool.v, p.num_slots, rtt, rtt_stride,
                                req_idx, prefix_len, extend_len, (const int32_t *)share, batch,
-                               (const int64_t *)offs, cap, ks, vs, p.hkv * D, dev_status)) != RX_OK)
+                               (const int64_t *)offs, cap, ks, vs, p.hkv * D, dev_status, window, nf)) != RX_OK)
         return rc;
+    if (rules) return D == 128 ? launch_extend<128, true, false, true>(p, grid, st) : launch_extend<64, true, false, true>(p, grid, st);
     return D == 128 ? launch_extend<128, true>(p, grid, st) : launch_extend<64, true>(p, grid, st);
 }
 
@@ -1112,5 +1235,64 @@ extern "C" size_t rx_attn_extend_workspace(int64_t total_ctx_tokens, int32_t bat
         rx_set_error(RX_ERR_UNSUPPORTED, "rx_attn_extend_workspace: %lld context rows", (long long)cap);
         return 0;
     }
-    return stage_layout(cap < kBN ? kBN : cap, batch, (int64_t)num_kv_heads * head_dim * 2).bytes;
+    return stage_layout(cap < kBN ? kBN : cap, batch, (int64_t)num_kv_heads * head_dim * 2, false).bytes;
+}
+
+extern "C" int rx_attn_extend_rules(const rx_kv_pool *pool_in, const void *q, void *o, float *lse, int32_t hq,
+                                    const int32_t *qo_indptr, const int32_t *req_idx, const int32_t *prefix_len,
+                                    const int32_t *extend_len, const int32_t *rtt, int64_t rtt_stride, int32_t batch,
+                                    int32_t max_extend_len, const rx_attn_rules *rules, void *workspace, size_t ws_bytes,
+                                    float sm_scale, int32_t *dev_status, void *stream)
+{
+    rx_kv_pool layer_view;
+    if (const int rc = rx_pool_layer(pool_in, &layer_view, 0, "rx_attn_extend_rules")) return rc;
+    const rx_kv_pool *pool = pool_in ? &layer_view : nullptr;
+    if (const int rc = check_pool(pool)) return rc;
+    if (!rules) return rx_set_error(RX_ERR_INVALID, "rx_attn_extend_rules: no rules (rx_attn_extend is the call without them)");
+    const ExtendPool ep{pool->k, pool->v, pool->num_slots, pool->num_kv_heads, pool->head_dim, false, 1.f, 1.f};
+    return extend_call("rx_attn_extend_rules", ep, q, o, lse, hq, qo_indptr, req_idx, prefix_len, extend_len, rtt,
+                       rtt_stride, batch, max_extend_len, workspace, ws_bytes, sm_scale, dev_status, stream, rules);
+}
+
+extern "C" int rx_attn_extend_rules_fp8(const rx_kv_pool_fp8 *pool_in, const void *q, void *o, float *lse, int32_t hq,
+                                        const int32_t *qo_indptr, const int32_t *req_idx, const int32_t *prefix_len,
+                                        const int32_t *extend_len, const int32_t *rtt, int64_t rtt_stride, int32_t batch,
+                                        int32_t max_extend_len, const rx_attn_rules *rules, void *workspace,
+                                        size_t ws_bytes, float sm_scale, int32_t *dev_status, void *stream)
+{
+    rx_kv_pool_fp8 pool;
+    if (const int rc = rx_pool_layer(pool_in, &pool, 1, "rx_attn_extend_rules_fp8")) return rc;
+    if (!pool_in || !pool.k || !pool.v || pool.num_slots <= 0 || pool.num_kv_heads <= 0 || !(pool.k_scale > 0.f) ||
+        !(pool.v_scale > 0.f))
+        return rx_set_error(RX_ERR_INVALID, "rx_attn_extend_rules_fp8: invalid pool");
+    if (pool.head_dim != 64 && pool.head_dim != 128)
+        return rx_set_error(RX_ERR_UNSUPPORTED, "rx_attn_extend_rules_fp8: head_dim %d (supported: 64, 128)", pool.head_dim);
+    if (!rules)
+        return rx_set_error(RX_ERR_INVALID, "rx_attn_extend_rules_fp8: no rules (rx_attn_extend_fp8 is the call without them)");
+    if (rx_misaligned16(pool.k) || rx_misaligned16(pool.v))
+        return rx_set_error(RX_ERR_INVALID, "rx_attn_extend_rules_fp8: the pools must be 16-byte aligned");
+    const ExtendPool ep{pool.k, pool.v, pool.num_slots, pool.num_kv_heads, pool.head_dim, true, pool.k_scale, pool.v_scale};
+    return extend_call("rx_attn_extend_rules_fp8", ep, q, o, lse, hq, qo_indptr, req_idx, prefix_len, extend_len, rtt,
+                       rtt_stride, batch, max_extend_len, workspace, ws_bytes, sm_scale, dev_status, stream, rules);
+}
+
+extern "C" size_t rx_attn_rules_workspace(int64_t total_ctx_tokens, int32_t batch, int32_t hq, int32_t hkv,
+                                          int32_t head_dim, int32_t max_extend_len)
+{
+    if (total_ctx_tokens < 0 || batch <= 0 || batch > 65535 || hkv <= 0 || hkv > 8192 || hq <= 0 || hq % hkv != 0 ||
+        hq / hkv > kRows || max_extend_len < 1 || (head_dim != 64 && head_dim != 128)) {
+        rx_set_error(RX_ERR_INVALID, "rx_attn_rules_workspace: invalid argument");
+        return 0;
+    }
+    // calls of up to max_extend_len new tokens may take either way
+    const size_t split = rx_split_workspace(batch, hq, hkv, head_dim,
+                                            max_extend_len < RX_SPLIT_MAX_LEN ? max_extend_len : RX_SPLIT_MAX_LEN);
+    if (max_extend_len == 1 && total_ctx_tokens == 0) return split;
+    const int64_t cap = total_ctx_tokens + (int64_t)(2 * kBN - 1) * batch;  // rounded up to kBN rows, at a window's start too
+    if (cap > (int64_t)INT32_MAX - 2 * kBN) {
+        rx_set_error(RX_ERR_UNSUPPORTED, "rx_attn_rules_workspace: %lld context rows", (long long)cap);
+        return 0;
+    }
+    const size_t staged = stage_layout(cap < kBN ? kBN : cap, batch, (int64_t)hkv * head_dim * 2, true).bytes;
+    return split > staged ? split : staged;
 }

@@ -46,6 +46,19 @@ __device__ __forceinline__ uint32_t sw128(int r, int c, int blk)
     return (uint32_t)((c >> 3) * blk + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
+// Which halves of a word are NaN or infinite (bf16 pairs): 0xFFFF masks.
+__device__ __forceinline__ uint32_t not_finite(uint32_t w)
+{
+    constexpr uint32_t E = 0x7F80u;
+    return ((w & E) == E ? 0xFFFFu : 0u) | ((w & (E << 16)) == (E << 16) ? 0xFFFF0000u : 0u);
+}
+__device__ __forceinline__ bool drop_not_finite(uint4 &x)
+{
+    const uint32_t a = not_finite(x.x), b = not_finite(x.y), c = not_finite(x.z), d = not_finite(x.w);
+    x = make_uint4(x.x & ~a, x.y & ~b, x.z & ~c, x.w & ~d);
+    return (a | b | c | d) != 0u;
+}
+
 __device__ __forceinline__ float u2f(uint32_t u) { return __uint_as_float(u); }
 
 }  // namespace rx

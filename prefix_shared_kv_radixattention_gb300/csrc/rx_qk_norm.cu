@@ -60,6 +60,11 @@ struct NormParams {
     float k_scale, v_scale, k_inv, v_inv;  // the inverses correctly rounded
     int32_t *status;
     rx::RopeTab tab;
+    // positions on several axes (rx_qk_rope_axes_store): pair c of token i is
+    // turned by pos[axis[c] * pos_stride + i]
+    int64_t pos_stride;
+    int norm;  // 0: no norm
+    uint8_t axis[rx::kMaxHalf];
 };
 
 // Two fp32 values in one 64-bit register: this GPU's packed multiply-adds take
@@ -147,7 +152,8 @@ __device__ __forceinline__ float inverse_root(float v)
     return fmaf(.5f * r, fmaf(-low, r, __fmaf_rn(-p, r, 1.f)), r);
 }
 
-template <int D, bool F8>
+// AX: positions on several axes, the norm only where the call asks for it.
+template <int D, bool F8, bool AX>
 __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_store_kernel(const __grid_constant__ NormParams p)
 {
     constexpr int LPR = D / 16;             // lanes of one head
@@ -195,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_store_kernel(const _
 
     for (int i = threadIdx.x; i < ntok * HALF; i += kThreads) {
         const int t = i / HALF, c = i % HALF;
-        const int32_t pos = __ldg(p.pos + t0 + t);
+        const int32_t pos = __ldg(p.pos + (AX ? p.axis[c] * p.pos_stride : 0) + t0 + t);
         const uint32_t up = pos < 0 ? 0u - (uint32_t)pos : (uint32_t)pos;
         float sn, cn;
         rx::sincos_exact(p.tab, up, c, sn, cn);
@@ -234,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_store_kernel(const _
             if (t >= ntok) continue;
             const bool is_q = hh < p.hq, is_v = hh >= p.hq + p.hkv;
             if (!is_v) {
-                const float r = inverse_root(ss * (1.f / D) + p.eps);
+                const float r = AX && !p.norm ? 1.f : inverse_root(ss * (1.f / D) + p.eps);
                 const F2 rr(r, r), minus(-1.f, -1.f);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -261,7 +267,9 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_store_kernel(const _
             Chunk *dst = static_cast<Chunk *>(is_v ? p.v_pool : p.k_pool) + ((int64_t)slot * p.hkv + g) * (D / 8);
             if constexpr (F8) {
                 const float scale = is_v ? p.v_scale : p.k_scale, inv = is_v ? p.v_inv : p.k_inv;
-                const bool plain = scale >= 0x1p-60f && scale <= 0x1p60f && (is_v ? ss <= 0x1p80f : small);
+                // without a norm a rotated value is at most sqrt(2) times the head's largest
+                const bool plain = scale >= 0x1p-60f && scale <= 0x1p60f &&
+                                   (is_v ? ss <= 0x1p80f : AX && !p.norm ? ss <= 0x1p78f : small);
                 dst[gi] = codes(a, scale, inv, plain);
                 dst[LPR + gi] = codes(b, scale, inv, plain);
             } else {
@@ -281,10 +289,20 @@ struct Pool {
     float k_scale, v_scale;
 };
 
+// Positions on several axes, and whether there is a norm.
+struct Axes {
+    int64_t stride;
+    int n;
+    const uint8_t *pair;
+    int norm;
+};
+
 int norm_call(const char *who, const Pool &pool, const void *q, int64_t q_stride, void *q_out, const void *k_new,
               const void *v_new, int64_t kv_stride, const void *qw, const void *kw, const int32_t *slots,
-              const int32_t *pos, int64_t n, int32_t hq, double base, float eps, int32_t *dev_status, void *stream)
+              const int32_t *pos, int64_t n, int32_t hq, double base, float eps, int32_t *dev_status, void *stream,
+              const Axes *axes = nullptr)
 {
+    if (axes && !axes->norm) eps = 0.f;
     if (n < 0 || hq < 0 || !(eps >= 0.f) || eps > 3.4e38f ||
         (n > 0 && (!k_new || !v_new || !slots || !pos || (hq > 0 && (!q || !q_out)))))
         return rx_set_error(RX_ERR_INVALID, "%s: invalid argument", who);
@@ -304,6 +322,15 @@ int norm_call(const char *who, const Pool &pool, const void *q, int64_t q_stride
         return rx_set_error(RX_ERR_INVALID, "%s: q_out may be q only when q's rows are contiguous", who);
     if ((int64_t)hq + 2 * (int64_t)pool.hkv > 65535)
         return rx_set_error(RX_ERR_UNSUPPORTED, "%s: %d q heads and %d kv heads", who, hq, pool.hkv);
+    if (axes) {
+        if (axes->n < 1 || axes->n > 8)
+            return rx_set_error(RX_ERR_UNSUPPORTED, "%s: %d axes (1 to 8)", who, axes->n);
+        if (!axes->pair || (axes->n > 1 && axes->stride < n) || (!axes->norm && (qw || kw)))
+            return rx_set_error(RX_ERR_INVALID, "%s: pair_axis missing, pos_stride below n, or weights without a norm", who);
+        for (int c = 0; c < pool.D / 2; ++c)
+            if (axes->pair[c] >= axes->n)
+                return rx_set_error(RX_ERR_INVALID, "%s: pair %d on axis %d of %d", who, c, axes->pair[c], axes->n);
+    }
     if (n == 0) return RX_OK;
     // the frequency table of the last (head_dim, base) of this thread: a
     // model calls with one base, and 64 powers cost more host time than the launch
@@ -339,6 +366,11 @@ int norm_call(const char *who, const Pool &pool, const void *q, int64_t q_stride
     p.v_inv = 1.f / pool.v_scale;
     p.status = dev_status;
     p.tab = tab;
+    if (axes) {
+        p.pos_stride = axes->stride;
+        p.norm = axes->norm;
+        for (int c = 0; c < pool.D / 2; ++c) p.axis[c] = axes->pair[c];
+    }
     // tokens of a CTA: rows that fill its passes, fewer while that would leave
     // less than four CTAs an SM
     const int R = hq + 2 * pool.hkv, pass = kUnroll * kThreads / (pool.D / 16);
@@ -349,8 +381,12 @@ int norm_call(const char *who, const Pool &pool, const void *q, int64_t q_stride
     p.tok = (int)tok;
     const int64_t grid = (n + tok - 1) / tok;
     if (grid > INT32_MAX) return rx_set_error(RX_ERR_UNSUPPORTED, "%s: %lld tokens", who, (long long)n);
-    auto kernel = pool.D == 128 ? (pool.f8 ? qk_norm_rope_store_kernel<128, true> : qk_norm_rope_store_kernel<128, false>)
-                                : (pool.f8 ? qk_norm_rope_store_kernel<64, true> : qk_norm_rope_store_kernel<64, false>);
+    auto pick = [&](auto ax) {
+        constexpr bool AX = decltype(ax)::value;
+        return pool.D == 128 ? (pool.f8 ? qk_norm_rope_store_kernel<128, true, AX> : qk_norm_rope_store_kernel<128, false, AX>)
+                             : (pool.f8 ? qk_norm_rope_store_kernel<64, true, AX> : qk_norm_rope_store_kernel<64, false, AX>);
+    };
+    auto kernel = axes ? pick(std::true_type{}) : pick(std::false_type{});
     kernel<<<(unsigned)grid, kThreads, 0, (cudaStream_t)stream>>>(p);
     RX_CUDA_CHECK(cudaGetLastError());
     return RX_OK;
@@ -386,4 +422,38 @@ extern "C" int rx_qk_norm_rope_store_fp8(const rx_kv_pool_fp8 *pool_in, const vo
     const Pool pool{v.k, v.v, v.num_slots, v.num_kv_heads, v.head_dim, true, v.k_scale, v.v_scale};
     return norm_call("rx_qk_norm_rope_store_fp8", pool, q, q_stride, q_out, k_new, v_new, kv_stride, q_weight,
                      k_weight, slots, pos, n, num_q_heads, base, eps, dev_status, stream);
+}
+
+extern "C" int rx_qk_rope_axes_store(const rx_kv_pool *pool_in, const void *q, int64_t q_stride, void *q_out,
+                                     const void *k_new, const void *v_new, int64_t kv_stride, int32_t norm,
+                                     const void *q_weight, const void *k_weight, const int32_t *slots, const int32_t *pos,
+                                     int64_t pos_stride, int32_t num_axes, const uint8_t *pair_axis, int64_t n,
+                                     int32_t num_q_heads, double base, float eps, int32_t *dev_status, void *stream)
+{
+    rx_kv_pool v;
+    if (const int rc = rx_pool_layer(pool_in, &v, 0, "rx_qk_rope_axes_store")) return rc;
+    if (!pool_in || !v.k || !v.v || v.num_slots <= 0 || v.num_kv_heads <= 0)
+        return rx_set_error(RX_ERR_INVALID, "rx_qk_rope_axes_store: invalid pool");
+    const Pool pool{v.k, v.v, v.num_slots, v.num_kv_heads, v.head_dim, false, 1.f, 1.f};
+    const Axes axes{pos_stride, num_axes, pair_axis, norm};
+    return norm_call("rx_qk_rope_axes_store", pool, q, q_stride, q_out, k_new, v_new, kv_stride, q_weight, k_weight,
+                     slots, pos, n, num_q_heads, base, eps, dev_status, stream, &axes);
+}
+
+extern "C" int rx_qk_rope_axes_store_fp8(const rx_kv_pool_fp8 *pool_in, const void *q, int64_t q_stride, void *q_out,
+                                         const void *k_new, const void *v_new, int64_t kv_stride, int32_t norm,
+                                         const void *q_weight, const void *k_weight, const int32_t *slots,
+                                         const int32_t *pos, int64_t pos_stride, int32_t num_axes,
+                                         const uint8_t *pair_axis, int64_t n, int32_t num_q_heads, double base, float eps,
+                                         int32_t *dev_status, void *stream)
+{
+    rx_kv_pool_fp8 v;
+    if (const int rc = rx_pool_layer(pool_in, &v, 1, "rx_qk_rope_axes_store_fp8")) return rc;
+    if (!pool_in || !v.k || !v.v || v.num_slots <= 0 || v.num_kv_heads <= 0 || !(v.k_scale > 0.f) ||
+        !(v.v_scale > 0.f))
+        return rx_set_error(RX_ERR_INVALID, "rx_qk_rope_axes_store_fp8: invalid pool");
+    const Pool pool{v.k, v.v, v.num_slots, v.num_kv_heads, v.head_dim, true, v.k_scale, v.v_scale};
+    const Axes axes{pos_stride, num_axes, pair_axis, norm};
+    return norm_call("rx_qk_rope_axes_store_fp8", pool, q, q_stride, q_out, k_new, v_new, kv_stride, q_weight, k_weight,
+                     slots, pos, n, num_q_heads, base, eps, dev_status, stream, &axes);
 }

@@ -1,0 +1,133 @@
+// rx_rules.cuh -- rules on attention scores, shared by the kernels that apply
+// them (rx_extend.cu, rx_tree.cu): a tanh cap, a bias that falls with the
+// distance, and the positions a query token sees.
+//
+// A score s = sm_scale q . k of the query token at position p and the key at
+// position j becomes
+//     x = cap tanh(s / cap) - slope[h] |p - j|
+// where lo <= j < hi, and takes no part elsewhere.  In log2 units, with
+// E = 2^(2 log2(e) s / cap):
+//     log2(e) cap tanh(s / cap) = c2 - 2 c2 / (1 + E),   c2 = cap log2(e),
+// an exponential and a reciprocal of the special-function units a score; E of 0
+// or infinity gives -c2 and c2.  Its absolute error is c2 times a few 2^-23: for
+// a cap of 50 under 3e-5 log2 units, a weight's relative error under 2^-15,
+// where the weights are rounded to bf16 (2^-9) for the product with V.
+// (tanh.approx is off by 2^-11 of its value: 0.03 log2 units at that cap.)
+//
+// A cap bounds the scores, so the softmax needs no running maximum: with
+// |x| <= c2 and a key near enough in every row (no bias), the weights
+// 2^(x - m) with the one base m = min(c2, 100 - c2) neither overflow nor, for a
+// row's largest, fall below 2^-100; the maximum of a tile, the wait on it and
+// the rescaling of O all go.  That is done for c2 <= 72.2 (caps up to 50: the
+// largest weight is 2^45, and V may reach 2^57 before sums overflow).  Larger
+// caps and biased scores keep the running maximum.
+#pragma once
+
+#include "rx_common.cuh"
+
+namespace rx {
+
+struct Rules {
+    float c2;               // cap log2(e); 0: scores are not capped
+    float to_e;             // 2 / cap: E = 2^(s sl2 to_e)
+    float base;             // the weights' base, where it is fixed
+    int fixed;              // the base is fixed
+    int window;             // a token sees positions above p - window; INT_MAX: all
+    const float *slope;     // [q heads] or null
+    const int32_t *see_from;  // [query tokens] or null
+    const int32_t *see_to;    // [query tokens] or null
+};
+
+__device__ __forceinline__ float fast_rcp(float x)
+{
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// First position that a token at p sees by the window alone.
+__device__ __forceinline__ int window_from(const Rules &r, int p) { return p >= r.window ? p - r.window + 1 : 0; }
+
+// The positions [lo, hi) that query token `tok` (its row of see_from and
+// see_to) at position p sees, of a context of `ctx` positions.
+__device__ __forceinline__ void seen_range(const Rules &r, int tok, int p, int ctx, int &lo, int &hi)
+{
+    lo = window_from(r, p);
+    hi = p + 1;
+    if (r.see_from) lo = max(lo, __ldg(r.see_from + tok));
+    if (r.see_to) hi = max(hi, min(__ldg(r.see_to + tok), ctx));
+}
+
+// N scores q . k of consecutive keys, the first at position kbase, in place: to
+// log2 units (times sl2) with the cap and the bias, less the fixed base where
+// there is one.  dist = p - kbase; slope in log2 units a position.  Scores that
+// have neither cap nor bias stay as they are; the result is what the scores are
+// still to be multiplied with.
+template <int N>
+__device__ __forceinline__ float apply_rules(uint32_t (&sv)[N], const Rules &r, float sl2, float slope, int dist)
+{
+    if (r.c2 > 0.f) {
+        const float ke = fminf(sl2 * r.to_e, 0x1.fffffep127f), top = r.c2 - r.base;
+        const uint64_t ke2 = f2(ke, ke), one2 = f2(1.f, 1.f), minus2 = f2(-2.f * r.c2, -2.f * r.c2), top2 = f2(top, top);
+#pragma unroll
+        for (int k = 0; k < N / 2; ++k) {
+            float a, b;
+            f2_split(f2_mul(f2(__uint_as_float(sv[2 * k]), __uint_as_float(sv[2 * k + 1])), ke2), a, b);
+            f2_split(f2_add(f2(fast_exp2(a), fast_exp2(b)), one2), a, b);
+            f2_split(f2_fma(f2(fast_rcp(a), fast_rcp(b)), minus2, top2), a, b);
+            sv[2 * k] = __float_as_uint(a);
+            sv[2 * k + 1] = __float_as_uint(b);
+        }
+        if (!r.slope) return 1.f;
+    } else if (!r.slope) {
+        return sl2;
+    }
+    const float scale = r.c2 > 0.f ? 1.f : sl2, far = (float)dist;
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        sv[k] = __float_as_uint(fmaf(-slope, fabsf(far - (float)k), scale * __uint_as_float(sv[k])));
+    return 1.f;
+}
+
+// Scores of keys outside [lo, hi) to -infinity.
+template <int N>
+__device__ __forceinline__ void hide(uint32_t (&sv)[N], int kbase, int lo, int hi)
+{
+    const int from = lo - kbase, to = hi - kbase;
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        if (k < from || k >= to) sv[k] = 0xFF800000u;
+}
+
+// Checks a call's rules and fills in what the kernels take; `who` names the
+// entry point.  scale_log2: log2 units of a score.
+inline int make_rules(const char *who, const rx_attn_rules *in, float scale_log2, Rules &r)
+{
+    r = Rules{0.f, 0.f, 0.f, 0, INT32_MAX, nullptr, nullptr, nullptr};
+    if (!in) return rx_set_error(RX_ERR_INVALID, "%s: no rules (use the call without them)", who);
+    if (!(in->cap >= 0.f) || in->window < 0 || ((reinterpret_cast<uintptr_t>(in->slope) | reinterpret_cast<uintptr_t>(in->see_from) |
+                                                 reinterpret_cast<uintptr_t>(in->see_to)) & 3) != 0)
+        return rx_set_error(RX_ERR_INVALID, "%s: cap %g and window %d must not be negative, and the rules' arrays 4-byte aligned",
+                            who, in->cap, in->window);
+    // a hidden score is -infinity, and 0 times it would be NaN
+    if (!(scale_log2 >= 0x1p-126f && scale_log2 < INFINITY))
+        return rx_set_error(RX_ERR_INVALID, "%s: sm_scale (times K's scale) outside fp32's normal range", who);
+    r.slope = in->slope;
+    r.see_from = in->see_from;
+    r.see_to = in->see_to;
+    if (in->window > 0) r.window = in->window;
+    if (in->cap > 0.f) {
+        r.c2 = in->cap * kLog2e;
+        r.to_e = 2.f / in->cap;
+        const float ke = scale_log2 * r.to_e;
+        if (!(in->cap >= 1e-3f && in->cap <= 1e6f) || !(ke >= 0x1p-126f && ke < INFINITY))
+            return rx_set_error(RX_ERR_UNSUPPORTED, "%s: cap %g (from 1e-3 to 1e6)", who, in->cap);
+        if (r.c2 <= 72.2f && !in->slope) {
+            r.fixed = 1;
+            r.base = fminf(r.c2, 100.f - r.c2);
+        }
+    }
+    return RX_OK;
+}
+
+}  // namespace rx

@@ -57,10 +57,13 @@
 
 #include "rx_common.cuh"
 #include "rx_pipe.cuh"
+#include "rx_rules.cuh"
+#include "rx_split.h"
 
 namespace {
 
 using bf16 = __nv_bfloat16;
+using rx::drop_not_finite;
 using rx::sw128;
 using rx::u2f;
 using rx::wait_or_abort;
@@ -125,6 +128,10 @@ struct Seg {
     int nt;          // row tiles: 1 or 2
     int whole;       // every tile of the context: the result is final
     int last;        // the CTA's last segment
+    // with rules on the scores: the position tiles count from this one on; some
+    // row sees lo_min and what follows, every row what lies in [lo_max, its own
+    // position]
+    int first, lo_min, lo_max;
 };
 
 template <int D, bool F8>
@@ -184,6 +191,10 @@ struct TParams {
     float *part_l;      // [2 kCtas][128 nt] their log2-sum-exps
     struct Cut *cuts;   // [kCtas] what the merge has to do
     int32_t *status;
+    // calls with rules on the scores: chains only; extend_len or null, and
+    // without qo_indptr one token a request, prefix_len holding its context
+    rx::Rules rules;
+    const int32_t *extend_len;
 };
 
 // ---------------------------------------------------------------------------
@@ -197,18 +208,26 @@ struct Req {
     int row;          // of req_to_token
     int tok;          // its first query row
     int ntiles, nqt;  // 0 where there is nothing to do (no drafted token, or lengths out of range)
+    int first;        // with rules: tiles before the first one that a row sees
 
     __device__ __forceinline__ int64_t units() const { return (int64_t)ntiles * nqt; }
 };
 
+template <bool RU>
 __device__ __forceinline__ Req load_req(const TParams &p, int b, bool flag = false)
 {
     Req r;
-    r.tok = __ldg(p.qo_indptr + b);
-    r.T = __ldg(p.qo_indptr + b + 1) - r.tok;
-    r.P = __ldg(p.prefix_len + b);
+    if (RU && !p.qo_indptr) {
+        r.tok = b;
+        r.P = __ldg(p.prefix_len + b) - 1;
+        r.T = r.P == -1 ? 0 : 1;
+    } else {
+        r.tok = __ldg(p.qo_indptr + b);
+        r.T = RU ? __ldg(p.extend_len + b) : __ldg(p.qo_indptr + b + 1) - r.tok;
+        r.P = __ldg(p.prefix_len + b);
+    }
     r.row = __ldg(p.req_idx + b);
-    r.ntiles = r.nqt = 0;
+    r.ntiles = r.nqt = r.first = 0;
     if (r.T == 0) return r;
     if (r.T < 0 || r.T > p.max_tree || r.P < 0 || (int64_t)r.P + r.T > p.rtt_stride) {
         if (flag && p.status) atomicOr(p.status, RX_DEV_BAD_LEN);
@@ -216,6 +235,12 @@ __device__ __forceinline__ Req load_req(const TParams &p, int b, bool flag = fal
     }
     r.ntiles = (int)(((int64_t)r.P + r.T + kBN - 1) / kBN);
     r.nqt = (r.T + p.tb * p.nt - 1) / (p.tb * p.nt);
+    if (RU) {  // the window of the first token, or all that a request's one token sees; one tile at least
+        int lo = rx::window_from(p.rules, r.P);
+        if (r.T == 1 && p.rules.see_from) lo = max(lo, min(__ldg(p.rules.see_from + r.tok), r.P));
+        r.first = lo / kBN;
+        r.ntiles -= r.first;
+    }
     return r;
 }
 
@@ -236,7 +261,7 @@ struct __align__(16) Cut {
 
 // Exclusive prefix sums of the requests' units, `per` requests a thread, into
 // pre[0 .. threads]; returns the total.  Whole block.
-template <int THREADS>
+template <int THREADS, bool RU>
 __device__ int64_t scan_units(const TParams &p, int64_t *pre, int per, bool flag)
 {
     __shared__ int64_t warp_tot[THREADS / 32];
@@ -244,7 +269,7 @@ __device__ int64_t scan_units(const TParams &p, int64_t *pre, int per, bool flag
     int64_t sum = 0;
     for (int i = 0; i < per; ++i) {
         const int64_t b = (int64_t)threadIdx.x * per + i;
-        if (b < p.batch) sum += load_req(p, (int)b, flag).units();
+        if (b < p.batch) sum += load_req<RU>(p, (int)b, flag).units();
     }
     int64_t x = sum;
 #pragma unroll
@@ -267,7 +292,7 @@ __device__ int64_t scan_units(const TParams &p, int64_t *pre, int per, bool flag
 }
 
 // The place of unit u (0 <= u < hkv * per_head); r: its request.
-template <int THREADS>
+template <int THREADS, bool RU>
 __device__ Start locate(const TParams &p, const int64_t *pre, int per, int64_t per_head, int64_t u, Req &r)
 {
     Start c;
@@ -282,7 +307,7 @@ __device__ Start locate(const TParams &p, const int64_t *pre, int per, int64_t p
     }
     x -= pre[lo];
     c.b = lo * per;
-    for (r = load_req(p, c.b); x >= r.units(); r = load_req(p, c.b)) {
+    for (r = load_req<RU>(p, c.b); x >= r.units(); r = load_req<RU>(p, c.b)) {
         x -= r.units();
         ++c.b;
     }
@@ -299,7 +324,7 @@ __device__ __forceinline__ int64_t first_unit(int64_t total, int ctas, int c) { 
 // tree are among its tiles: under load a read of global memory takes
 // microseconds, which no other role then waits for.  The lanes hold the
 // lengths of 32 requests at a time.
-template <int D, bool F8>
+template <int D, bool F8, bool RU>
 __device__ void scheduler(const TParams &p, unsigned char *smem, uint32_t sbase)
 {
     using L = TL<D, F8>;
@@ -311,7 +336,7 @@ __device__ void scheduler(const TParams &p, unsigned char *smem, uint32_t sbase)
     Req mine;  // of request base + lane
     auto fill = [&]() {
         mine.ntiles = 0;
-        if (base + lane < p.batch) mine = load_req(p, base + lane);
+        if (base + lane < p.batch) mine = load_req<RU>(p, base + lane);
     };
     fill();
     Cut cut{0, 0, 0, 0};
@@ -335,8 +360,24 @@ __device__ void scheduler(const TParams &p, unsigned char *smem, uint32_t sbase)
         g.whole = g.j0 == 0 && g.j1 == ntiles;
         c.left -= g.j1 - g.j0;
         g.last = c.left <= 0;
+        g.first = g.lo_min = g.lo_max = 0;
+        if constexpr (RU) {
+            g.first = __shfl_sync(0xffffffffu, mine.first, l);
+            g.lo_min = rx::window_from(p.rules, g.P + g.node);
+            g.lo_max = rx::window_from(p.rules, g.P + g.node + g.ntok - 1);
+            if (p.rules.see_from) {
+                int least = INT_MAX, most = 0;
+                for (int i = lane; i < g.ntok; i += 32) {
+                    const int x = max(rx::window_from(p.rules, g.P + g.node + i), __ldg(p.rules.see_from + g.tok + i));
+                    least = min(least, x);
+                    most = max(most, x);
+                }
+                g.lo_min = __reduce_min_sync(0xffffffffu, least);
+                g.lo_max = __reduce_max_sync(0xffffffffu, most);
+            }
+        }
         if (lane == 0) *reinterpret_cast<Seg *>(smem + L::OFF_SEG + slot * 64) = g;
-        if (p.mask && g.T <= kMaskT && g.j1 * kBN > g.P) {
+        if (!RU && p.mask && g.T <= kMaskT && g.j1 * kBN > g.P) {
             const int W = (g.T + 31) / 32;
             const uint32_t dst = sbase + L::OFF_MASK + slot * (kMaskT * (kMaskT / 32) * 4);
             for (int i = lane; i < g.ntok * W; i += 32) {
@@ -386,14 +427,20 @@ __device__ void scheduler(const TParams &p, unsigned char *smem, uint32_t sbase)
 
 // The CTA's segment s for another role; false when a wait gave up.  The role
 // arrives on the segment's empty barrier once it needs it no more.
-template <typename L>
+template <typename L, bool RU = false>
 __device__ __forceinline__ bool get_seg(int s, Seg &g, unsigned char *smem, uint32_t sbase, int32_t *status)
 {
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
     if (!wait_or_abort(sbase + L::OFF_BAR + 8 * (L::B_SEGFULL + s % kSegs), (s / kSegs) & 1, abort_flag, status)) return false;
     const int4 *w = reinterpret_cast<const int4 *>(smem + L::OFF_SEG + (s % kSegs) * 64);
     const int4 a = w[0], b = w[1], c = w[2];
-    g = Seg{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w};
+    g = Seg{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w, 0, 0, 0};
+    if constexpr (RU) {
+        const int4 d = w[3];
+        g.first = d.x;
+        g.lo_min = d.y;
+        g.lo_max = d.z;
+    }
     return true;
 }
 template <typename L>
@@ -422,19 +469,6 @@ __device__ __forceinline__ uint32_t mask_word(const uint32_t *row, int words, in
 // producer warps
 // ---------------------------------------------------------------------------
 
-// Which halves of a word are NaN or infinite (bf16 pairs): 0xFFFF masks.
-__device__ __forceinline__ uint32_t not_finite(uint32_t w)
-{
-    constexpr uint32_t E = 0x7F80u;
-    return ((w & E) == E ? 0xFFFFu : 0u) | ((w & (E << 16)) == (E << 16) ? 0xFFFF0000u : 0u);
-}
-__device__ __forceinline__ bool drop_not_finite(uint4 &x)
-{
-    const uint32_t a = not_finite(x.x), b = not_finite(x.y), c = not_finite(x.z), d = not_finite(x.w);
-    x = make_uint4(x.x & ~a, x.y & ~b, x.z & ~c, x.w & ~d);
-    return (a | b | c | d) != 0u;
-}
-
 // Eight E4M3 codes as eight f16 (exact).
 __device__ __forceinline__ uint4 widen_f16(uint32_t lo, uint32_t hi)
 {
@@ -455,8 +489,10 @@ __device__ __forceinline__ uint4 widen_f16(uint32_t lo, uint32_t hi)
 //
 // V at drafted positions is looked at before it is handed over: a NaN or
 // infinity there would reach rows that do not see the position (0 * inf), so it
-// is dropped, noted, and added back to the rows that see it at the end.
-template <int D, bool F8, int NT, bool IS_V>
+// is dropped, noted, and added back to the rows that see it at the end.  With
+// rules on the scores that goes for the tiles that some row does not see all
+// of; positions that no row sees are not read at all.
+template <int D, bool F8, int NT, bool IS_V, bool RU>
 __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
 {
     using L = TL<D, F8>;
@@ -482,20 +518,27 @@ __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
         __device__ __forceinline__ int g() const { return meta & 0x1FFF; }
         __device__ __forceinline__ int rel() const { return ((meta >> 13) & 0x7FF) - lim; }  // first position, from the first drafted one
         __device__ __forceinline__ int seg() const { return meta >> 24; }
+
+        // with rules: the tile's first position, what some row sees, and whether
+        // every row sees all of it (see the V note above)
+        int at, lo;
+        bool all;
     };
     static_assert(kMaxTree < 2048 && kSegs <= 64, "the fields of meta");
     // the segment being handed out: its next tile, and how many it still has
     int s = -1, left = 0, lim = 0, meta = 0;
     bool last = false;
     const int32_t *slots = nullptr;  // of this lane's row in that tile
+    int at = 0, lo_min = 0, all_from = 0, all_to = 0;  // with rules
     // the next tile, with the loads of its slot ids
     auto take = [&](Tile &t) {
         t.slot = -1;
-        t.lim = t.meta = 0;
+        t.lim = t.meta = t.at = t.lo = 0;
+        t.all = true;
         if (left == 0) {
             if (last) return;
             Seg q;
-            if (!__all_sync(0xffffffffu, get_seg<L>(s + 1, q, smem, sbase, p.status))) {
+            if (!__all_sync(0xffffffffu, get_seg<L, RU>(s + 1, q, smem, sbase, p.status))) {
                 last = true;  // gave up
                 return;
             }
@@ -503,14 +546,24 @@ __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
             ++s;
             if (lane == 0) free_seg<L>(s, sbase);
             left = q.j1 - q.j0;
-            lim = q.P + q.T - q.j0 * kBN;
+            lim = q.P + q.T - (q.first + q.j0) * kBN;
+            at = (q.first + q.j0) * kBN;
+            lo_min = q.lo_min;
+            all_from = q.lo_max;
+            all_to = q.P + q.node + 1;
             meta = q.g | (q.T << 13) | ((s % kSegs) << 24);
             last = q.last;
-            slots = p.rtt + (int64_t)q.row * p.rtt_stride + (int64_t)q.j0 * kBN + r0 + lane;
+            slots = p.rtt + (int64_t)q.row * p.rtt_stride + (int64_t)(q.first + q.j0) * kBN + r0 + lane;
         }
         t.lim = lim;
         t.meta = meta;
-        if (lane < ROWS && r0 + lane < lim) t.slot = rx::ld_stream_b32(slots);
+        if constexpr (RU) {
+            t.at = at;
+            t.lo = lo_min - at;
+            t.all = at >= all_from && at + kBN <= all_to;
+            at += kBN;
+        }
+        if (lane < ROWS && r0 + lane < lim && (!RU || r0 + lane >= t.lo)) t.slot = rx::ld_stream_b32(slots);
         --left;
         lim -= kBN;
         slots += kBN;
@@ -518,7 +571,7 @@ __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
     // slots past the end or outside the pool (flagged) become -1
     auto check = [&](Tile &t) {
         if (t.slot >= 0 && (int64_t)t.slot < p.num_slots) return;
-        if (lane < ROWS && r0 + lane < t.lim && p.status) atomicOr(p.status, RX_DEV_BAD_SLOT);
+        if (lane < ROWS && r0 + lane < t.lim && (!RU || r0 + lane >= t.lo) && p.status) atomicOr(p.status, RX_DEV_BAD_SLOT);
         t.slot = -1;
     };
     auto source = [&](const Tile &t, int u, bool &ok) {
@@ -534,9 +587,10 @@ __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
             const int r = r0 + u / CH * RPI + sub, e = t.rel() + r;
             uint4 *at = reinterpret_cast<uint4 *>(smem + off + sw128(r, CH * ch + u % CH, L::BLK));
             uint4 x = *at;
-            if (e >= 0 && drop_not_finite(x)) {
+            if ((RU || e >= 0) && drop_not_finite(x)) {
                 *at = x;
-                atomicOr(reinterpret_cast<uint32_t *>(smem + L::OFF_NF) + t.seg() * 32 + (e >> 5), 1u << (e & 31));
+                // with rules the tile, not the position, is noted: all of them as one
+                atomicOr(reinterpret_cast<uint32_t *>(smem + L::OFF_NF) + t.seg() * 32 + (RU ? 0 : e >> 5), RU ? 1u : 1u << (e & 31));
             }
         }
     };
@@ -557,7 +611,7 @@ __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
                 const unsigned char *src = source(cur, u, ok);
                 rx::cp_async_16(sbase + off + sw128(r0 + u * RPI + sub, ch, L::BLK), src, ok ? 16 : 0);
             }
-            if (IS_V && cur.rel() + kBN > 0) {  // the tile has drafted positions
+            if (IS_V && (RU ? !cur.all : cur.rel() + kBN > 0)) {  // some rows do not see all of the tile
                 rx::cp_async_wait_all();
                 scrub(off, cur);
                 rx::fence_proxy_async_smem();
@@ -616,7 +670,7 @@ __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
             fetch(nxt, 1, buf);
             rx::cp_async_wait<2>();     // the second
             widen(off, 1, buf1);
-            if (IS_V && cur.rel() + kBN > 0) scrub(off, cur);  // the tile has drafted positions
+            if (IS_V && (RU ? !cur.all : cur.rel() + kBN > 0)) scrub(off, cur);  // some rows do not see all of the tile
             rx::fence_proxy_async_smem();
             rx::mbar_arrive(bar_full + 8 * st);
             check(nx2);
@@ -889,13 +943,43 @@ __device__ __noinline__ void add_not_finite(const TParams &p, const uint32_t *nf
         }
 }
 
+// With rules: those of V at positions from .. to - 1, all of them seen by the
+// row, that lie in tiles that some row of the segment does not see all of.
+template <int D, bool F8>
+__device__ __noinline__ void add_not_finite_rules(const TParams &p, const Seg &g, int from, int to, int64_t part, int64_t orow)
+{
+    const int32_t *slots = p.rtt + (int64_t)g.row * p.rtt_stride;
+    for (int pos = from; pos < to; ++pos) {
+        const int tile = pos / kBN * kBN;
+        if (tile >= g.lo_max && tile + kBN <= g.P + g.node + 1) {  // not looked at: the product has them
+            pos = tile + kBN - 1;
+            continue;
+        }
+        const int64_t slot = __ldg(slots + pos);
+        if (slot < 0 || slot >= p.num_slots) continue;
+        const int64_t at = (slot * p.hkv + g.g) * D;
+        for (int i = 0; i < D; ++i) {
+            float v;
+            if constexpr (F8) {
+                const uint32_t h = rx::e4m3x2_to_f16x2(__ldg(p.v + at + i));
+                v = __half2float(__ushort_as_half((unsigned short)(h & 0xFFFFu)));
+            } else {
+                v = __bfloat162float(reinterpret_cast<const bf16 *>(p.v)[at + i]);
+            }
+            if (isfinite(v)) continue;
+            if (part >= 0) p.part_o[part * D + i] += v;
+            else p.o[orow * D + i] = __float2bfloat16_rn(__bfloat162float(p.o[orow * D + i]) + v);
+        }
+    }
+}
+
 // What a thread keeps of its row of one row tile.
 struct RowState {
     float m, l;    // running maximum (log2 units) and sum
     float sl2;     // log2 units of a score
 };
 
-template <int D, bool F8, int NT>
+template <int D, bool F8, int NT, bool RU>
 __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sbase)
 {
     using L = TL<D, F8>;
@@ -910,7 +994,7 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
     int c = 0;                                         // the row tile's items so far
     for (int s = 0;; ++s) {
         Seg g;
-        if (!__all_sync(0xffffffffu, get_seg<L>(s, g, smem, sbase, p.status))) return;
+        if (!__all_sync(0xffffffffu, get_seg<L, RU>(s, g, smem, sbase, p.status))) return;
         if (NT == 2 && t >= g.nt) {  // the segment has one row tile
             __syncwarp();
             if ((row & 31) == 0) free_seg<L>(s, sbase);
@@ -923,6 +1007,18 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
                                                 : p.mask + (int64_t)g.tok * p.words;
         const int words = g.T <= kMaskT ? kMaskT / 32 : p.words;
         RowState a{-INFINITY, 0.f, p.scale_log2};
+        // with rules: the row's position, the positions that it sees, its slope
+        int at = 0, lo = 0, hi = 0;
+        float slope = 0.f;
+        if constexpr (RU) {
+            const int node = rt + t * p.tb;
+            at = g.P + g.node + node;
+            if (node < g.ntok && rt < p.tb) {
+                rx::seen_range(p.rules, g.tok + node, at, g.P + g.T, lo, hi);
+                if (p.rules.slope) slope = __ldg(p.rules.slope + (int64_t)g.g * p.G + rh) * rx::kLog2e;
+            }
+            if (p.rules.fixed) a.m = p.rules.base;
+        }
         for (int j = g.j0; j < g.j1; ++j, ++c) {
                 const int M = min(p.tb, g.ntok - t * p.tb) * p.G, node = rt + t * p.tb;
                 const bool valid = row < M, warp_on = (row & ~31) < M;
@@ -952,8 +1048,15 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
 #pragma unroll
                     for (int k = 0; k < kBN / 32; ++k) rx::tmem_ld32(tS + k * 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * k));
                     if (F8 && j == g.j0) a.sl2 = reinterpret_cast<const float *>(smem + L::OFF_QS)[(s % kRing) * kRows + row];
-                    const int kbase = j * kBN;
-                    if (kbase + kBN > g.P) {   // drafted positions, or past the last
+                    const int kbase = (RU ? g.first + j : j) * kBN;
+                    float left = a.sl2;  // what the scores are still to be multiplied with
+                    if constexpr (RU) {
+                        const bool all = __all_sync(0xffffffffu, !valid || (kbase >= lo && kbase + kBN <= hi));
+                        rx::tmem_wait_ld();
+                        release_s();
+                        left = rx::apply_rules(sv, p.rules, a.sl2, slope, at - kbase);
+                        if (!all) rx::hide(sv, kbase, lo, hi);
+                    } else if (kbase + kBN > g.P) {   // drafted positions, or past the last
                         const int off = kbase - g.P, w0 = off >> 5;
                         const uint32_t *mrow = masks && valid ? masks + (int64_t)node * words : nullptr;
                         uint32_t w[5];
@@ -972,8 +1075,8 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
                         rx::tmem_wait_ld();
                         release_s();
                     }
-                    float mx;
-                    {
+                    float mx = -INFINITY;
+                    if (!RU || !p.rules.fixed) {
                         float a0 = -INFINITY, a1 = -INFINITY, a2 = -INFINITY, a3 = -INFINITY;
 #pragma unroll
                         for (int k = 0; k < kBN / 8; ++k) {
@@ -984,16 +1087,16 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
                         }
                         mx = rx::fmax3(fmaxf(a0, a1), a2, a3);
                     }
-                    const float m_new = fmaxf(a.m, mx * a.sl2);
-                    const bool need = valid && (a.m == -INFINITY || m_new > a.m + kRescale);
+                    const float m_new = fmaxf(a.m, mx * left);
+                    const bool need = valid && (!RU || !p.rules.fixed) && (a.m == -INFINITY || m_new > a.m + kRescale);
                     const bool scale_o = need && a.m != -INFINITY;
                     const float alpha = scale_o ? rx::fast_exp2(a.m - m_new) : 1.f;
                     if (need) {
                         a.l *= alpha;
                         a.m = m_new;
                     }
-                    const float mu = a.m == -INFINITY ? 0.f : a.m;
-                    const uint64_t scale2 = rx::f2(a.sl2, a.sl2), negm2 = rx::f2(-mu, -mu);
+                    const float mu = a.m == -INFINITY || (RU && p.rules.fixed) ? 0.f : a.m;
+                    const uint64_t scale2 = rx::f2(left, left), negm2 = rx::f2(-mu, -mu);
                     uint64_t acc[4] = {0, 0, 0, 0};
                     if (!p_free()) return;
 #pragma unroll
@@ -1085,7 +1188,11 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
             }
             rx::tc_fence_before();
             rx::mbar_arrive(bar + 8 * (L::B_OEMPTY + t));
-            if (g.j1 * kBN > g.P) {
+            if constexpr (RU) {
+                if (nf[0] && valid)
+                    add_not_finite_rules<D, F8>(p, g, max(lo, (g.first + g.j0) * kBN), min(hi, (g.first + g.j1) * kBN),
+                                                g.whole ? -1 : prow, orow);
+            } else if (g.j1 * kBN > g.P) {
                 uint32_t any = 0;
                 for (int w = 0; w < (g.T + 31) / 32; ++w) any |= nf[w];
                 if (any && valid)
@@ -1099,7 +1206,7 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
     }
 }
 
-template <int D, bool F8, int NT>
+template <int D, bool F8, int NT, bool RU>
 __global__ void __launch_bounds__(Ro<NT>::THREADS, 1) tree_kernel(const __grid_constant__ TParams p)
 {
     using L = TL<D, F8>;
@@ -1143,7 +1250,7 @@ __global__ void __launch_bounds__(Ro<NT>::THREADS, 1) tree_kernel(const __grid_c
     for (int i = threadIdx.x; i < kSegs * 32; i += kThreads) reinterpret_cast<uint32_t *>(smem + L::OFF_NF)[i] = 0;
     int64_t *pre = reinterpret_cast<int64_t *>(smem + L::OFF_MASK);
     const int per = (p.batch + kThreads - 1) / kThreads;
-    const int64_t per_head = scan_units<kThreads>(p, pre, per, blockIdx.x == 0);
+    const int64_t per_head = scan_units<kThreads, RU>(p, pre, per, blockIdx.x == 0);
     const int64_t total = per_head * p.hkv;
     const int ctas = (int)min((int64_t)gridDim.x, total);
     if ((int)blockIdx.x >= ctas || total / ctas >= INT_MAX) {  // nothing to do, or lengths of no real pool
@@ -1157,7 +1264,7 @@ __global__ void __launch_bounds__(Ro<NT>::THREADS, 1) tree_kernel(const __grid_c
     if (threadIdx.x == 0) {
         const int64_t u0 = first_unit(total, ctas, blockIdx.x);
         Req r;
-        Start c = locate<kThreads>(p, pre, per, per_head, u0, r);
+        Start c = locate<kThreads, RU>(p, pre, per, per_head, u0, r);
         c.left = (int)(first_unit(total, ctas, blockIdx.x + 1) - u0);
         *reinterpret_cast<Start *>(smem + L::OFF_START) = c;
     }
@@ -1168,11 +1275,11 @@ __global__ void __launch_bounds__(Ro<NT>::THREADS, 1) tree_kernel(const __grid_c
 
     if (warp < W::SOFT) {
         rx::reg_inc<W::R_SOFT>();
-        softmax_rows<D, F8, NT>(p, smem, sbase);
+        softmax_rows<D, F8, NT, RU>(p, smem, sbase);
     } else if (warp < W::Q) {
         rx::reg_dec<W::R_REST>();
-        if (warp < W::SOFT + W::PROD) producer<D, F8, NT, false>(p, smem, sbase);
-        else producer<D, F8, NT, true>(p, smem, sbase);
+        if (warp < W::SOFT + W::PROD) producer<D, F8, NT, false, RU>(p, smem, sbase);
+        else producer<D, F8, NT, true, RU>(p, smem, sbase);
     } else {
         rx::reg_dec<W::R_REST>();
         if (warp == W::Q) {
@@ -1184,7 +1291,7 @@ __global__ void __launch_bounds__(Ro<NT>::THREADS, 1) tree_kernel(const __grid_c
             if ((threadIdx.x & 31) == 0) issue_pv<D, F8, NT>(p, smem, sbase);
             __syncwarp();
         } else if (warp == W::SCHED) {
-            scheduler<D, F8>(p, smem, sbase);
+            scheduler<D, F8, RU>(p, smem, sbase);
         }
     }
     rx::tc_fence_before();
@@ -1262,13 +1369,7 @@ size_t part_bytes(int32_t nt, int32_t head_dim) { return (size_t)2 * kCtas * nt 
 // The workspace has room for either.
 int row_tiles(int32_t hq, int32_t hkv, int32_t max_tree) { return (int64_t)max_tree > kRows / (hq / hkv) ? kMaxNt : 1; }
 
-struct TreePool {
-    const void *k, *v;
-    int64_t num_slots;
-    int hkv, D;
-    bool f8;
-    float k_scale, v_scale;
-};
+using TreePool = RxAttnPool;
 
 bool tree_shape_ok(int32_t batch, int32_t hq, int32_t hkv, int32_t D, int32_t max_tree)
 {
@@ -1278,21 +1379,21 @@ bool tree_shape_ok(int32_t batch, int32_t hq, int32_t hkv, int32_t D, int32_t ma
 
 // The registers that the kernel is launched with: the shares of the roles are
 // granted out of them, and a share that is not there would be waited for.
-template <int D, bool F8, int NT>
+template <int D, bool F8, int NT, bool RU>
 bool registers_ok()
 {
     cudaFuncAttributes a;
-    return cudaFuncGetAttributes(&a, tree_kernel<D, F8, NT>) == cudaSuccess && a.numRegs >= Ro<NT>::R_LAUNCH;
+    return cudaFuncGetAttributes(&a, tree_kernel<D, F8, NT, RU>) == cudaSuccess && a.numRegs >= Ro<NT>::R_LAUNCH;
 }
 
-template <int D, bool F8, int NT = 1>
+template <int D, bool F8, bool RU, int NT = 1>
 int launch(const TParams &p, cudaStream_t st)
 {
-    static const bool ok = registers_ok<D, F8, NT>();
+    static const bool ok = registers_ok<D, F8, NT, RU>();
     if (!ok) return rx_set_error(RX_ERR_UNSUPPORTED, "tree attention: the kernel was built with too few registers");
     // per device; cheap, and right whichever device is current
-    RX_CUDA_CHECK(cudaFuncSetAttribute(tree_kernel<D, F8, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, (TL<D, F8>::BYTES)));
-    tree_kernel<D, F8, NT><<<kCtas, Ro<NT>::THREADS, (TL<D, F8>::BYTES), st>>>(p);
+    RX_CUDA_CHECK(cudaFuncSetAttribute(tree_kernel<D, F8, NT, RU>, cudaFuncAttributeMaxDynamicSharedMemorySize, (TL<D, F8>::BYTES)));
+    tree_kernel<D, F8, NT, RU><<<kCtas, Ro<NT>::THREADS, (TL<D, F8>::BYTES), st>>>(p);
     RX_CUDA_CHECK(cudaGetLastError());
     // a programmatic dependent: it is launched meanwhile and waits on the device
     cudaLaunchConfig_t cfg = {};
@@ -1308,12 +1409,15 @@ int launch(const TParams &p, cudaStream_t st)
     return RX_OK;
 }
 
+// rx_attn_tree and its like after their pool checks.  rules: of the calls that
+// have them (chains; without qo_indptr one token a request), else null.
 int tree_call(const char *who, const TreePool &pool, const void *q, void *o, float *lse, int32_t hq,
               const int32_t *qo_indptr, const int32_t *req_idx, const int32_t *prefix_len, const uint32_t *mask,
               int32_t words, const int32_t *rtt, int64_t rtt_stride, int32_t batch, int32_t max_tree,
-              void *workspace, size_t ws_bytes, float sm_scale, int32_t *dev_status, void *stream)
+              void *workspace, size_t ws_bytes, float sm_scale, int32_t *dev_status, void *stream,
+              const rx_attn_rules *rules = nullptr, const int32_t *extend_len = nullptr)
 {
-    if (!q || !o || !qo_indptr || !req_idx || !prefix_len || !rtt || rtt_stride <= 0 || rtt_stride > INT32_MAX ||
+    if (!q || !o || (!qo_indptr && !rules) || !req_idx || !prefix_len || !rtt || rtt_stride <= 0 || rtt_stride > INT32_MAX ||
         batch < 0 || hq <= 0 || !(sm_scale > 0.f) || max_tree < 1)
         return rx_set_error(RX_ERR_INVALID, "%s: invalid argument", who);
     if (pool.D != 64 && pool.D != 128)
@@ -1337,8 +1441,11 @@ int tree_call(const char *who, const TreePool &pool, const void *q, void *o, flo
                             need);
     if ((reinterpret_cast<uintptr_t>(workspace) & 255) != 0)
         return rx_set_error(RX_ERR_INVALID, "%s: workspace must be 256-byte aligned", who);
-    if (batch == 0) return RX_OK;
     TParams p{};
+    if (rules)
+        if (const int rc = rx::make_rules(who, rules, scale_log2, p.rules)) return rc;
+    if (batch == 0) return RX_OK;
+    p.extend_len = extend_len;
     p.q = (const bf16 *)q;
     p.o = (bf16 *)o;
     p.lse = lse;
@@ -1366,9 +1473,15 @@ int tree_call(const char *who, const TreePool &pool, const void *q, void *o, flo
     p.part_l = (float *)((char *)workspace + part_bytes(p.nt, pool.D));
     p.cuts = (Cut *)(p.part_l + (size_t)2 * kCtas * p.nt * kRows);
     cudaStream_t st = (cudaStream_t)stream;
-    if (pool.D == 128)
-        return pool.f8 ? launch<128, true>(p, st) : p.nt == 1 ? launch<128, false>(p, st) : launch<128, false, kMaxNt>(p, st);
-    return pool.f8 ? launch<64, true>(p, st) : p.nt == 1 ? launch<64, false>(p, st) : launch<64, false, kMaxNt>(p, st);
+    auto run = [&](auto d, auto ru) {
+        constexpr int D = decltype(d)::value;
+        constexpr bool RU = decltype(ru)::value;
+        return pool.f8 ? launch<D, true, RU>(p, st) : p.nt == 1 ? launch<D, false, RU>(p, st) : launch<D, false, RU, kMaxNt>(p, st);
+    };
+    using std::integral_constant;
+    if (rules)
+        return pool.D == 128 ? run(integral_constant<int, 128>{}, std::true_type{}) : run(integral_constant<int, 64>{}, std::true_type{});
+    return pool.D == 128 ? run(integral_constant<int, 128>{}, std::false_type{}) : run(integral_constant<int, 64>{}, std::false_type{});
 }
 
 }  // namespace
@@ -1413,4 +1526,61 @@ extern "C" int rx_attn_tree_fp8(const rx_kv_pool_fp8 *pool_in, const void *q, vo
     const TreePool pool{v.k, v.v, v.num_slots, v.num_kv_heads, v.head_dim, true, v.k_scale, v.v_scale};
     return tree_call("rx_attn_tree_fp8", pool, q, o, lse, hq, qo_indptr, req_idx, prefix_len, mask, words, rtt,
                      rtt_stride, batch, max_tree, workspace, ws_bytes, sm_scale, dev_status, stream);
+}
+
+int rx_split_rules(const char *who, const RxAttnPool &pool, const void *q, void *o, float *lse, int32_t hq,
+                   const int32_t *qo_indptr, const int32_t *req_idx, const int32_t *prefix_len, const int32_t *extend_len,
+                   const int32_t *rtt, int64_t rtt_stride, int32_t batch, int32_t max_len, void *workspace, size_t ws_bytes,
+                   float sm_scale, const rx_attn_rules *rules, int32_t *dev_status, void *stream)
+{
+    return tree_call(who, pool, q, o, lse, hq, qo_indptr, req_idx, prefix_len, nullptr, 0, rtt, rtt_stride, batch, max_len,
+                     workspace, ws_bytes, sm_scale, dev_status, stream, rules, extend_len);
+}
+
+size_t rx_split_workspace(int32_t batch, int32_t hq, int32_t hkv, int32_t head_dim, int32_t max_len)
+{
+    return rx_attn_tree_workspace(batch, hq, hkv, head_dim, max_len);
+}
+
+namespace {
+
+// One token a request, after the pool's checks.
+int decode_rules(const char *who, const RxAttnPool &pool, const void *q, void *o, float *lse, int32_t hq,
+                 const int32_t *req_idx, const int32_t *seq_len, const int32_t *rtt, int64_t rtt_stride, int32_t batch,
+                 void *workspace, size_t ws_bytes, float sm_scale, const rx_attn_rules *rules, int32_t *dev_status, void *stream)
+{
+    if (!rules) return rx_set_error(RX_ERR_INVALID, "%s: no rules (rx_attn_decode is the call without them)", who);
+    if (rules->see_to) return rx_set_error(RX_ERR_INVALID, "%s: a last token sees nothing behind itself (see_to)", who);
+    return rx_split_rules(who, pool, q, o, lse, hq, nullptr, req_idx, seq_len, nullptr, rtt, rtt_stride, batch, 1, workspace,
+                          ws_bytes, sm_scale, rules, dev_status, stream);
+}
+
+}  // namespace
+
+extern "C" int rx_attn_decode_rules(const rx_kv_pool *pool_in, const void *q, void *o, float *lse, int32_t hq,
+                                    const int32_t *req_idx, const int32_t *seq_len, const int32_t *rtt, int64_t rtt_stride,
+                                    int32_t batch, const rx_attn_rules *rules, void *workspace, size_t ws_bytes,
+                                    float sm_scale, int32_t *dev_status, void *stream)
+{
+    rx_kv_pool v;
+    if (const int rc = rx_pool_layer(pool_in, &v, 0, "rx_attn_decode_rules")) return rc;
+    if (!pool_in || !v.k || !v.v || v.num_slots <= 0 || v.num_kv_heads <= 0)
+        return rx_set_error(RX_ERR_INVALID, "rx_attn_decode_rules: invalid pool");
+    const RxAttnPool pool{v.k, v.v, v.num_slots, v.num_kv_heads, v.head_dim, false, 1.f, 1.f};
+    return decode_rules("rx_attn_decode_rules", pool, q, o, lse, hq, req_idx, seq_len, rtt, rtt_stride, batch, workspace,
+                        ws_bytes, sm_scale, rules, dev_status, stream);
+}
+
+extern "C" int rx_attn_decode_rules_fp8(const rx_kv_pool_fp8 *pool_in, const void *q, void *o, float *lse, int32_t hq,
+                                        const int32_t *req_idx, const int32_t *seq_len, const int32_t *rtt,
+                                        int64_t rtt_stride, int32_t batch, const rx_attn_rules *rules, void *workspace,
+                                        size_t ws_bytes, float sm_scale, int32_t *dev_status, void *stream)
+{
+    rx_kv_pool_fp8 v;
+    if (const int rc = rx_pool_layer(pool_in, &v, 1, "rx_attn_decode_rules_fp8")) return rc;
+    if (!pool_in || !v.k || !v.v || v.num_slots <= 0 || v.num_kv_heads <= 0 || !(v.k_scale > 0.f) || !(v.v_scale > 0.f))
+        return rx_set_error(RX_ERR_INVALID, "rx_attn_decode_rules_fp8: invalid pool");
+    const RxAttnPool pool{v.k, v.v, v.num_slots, v.num_kv_heads, v.head_dim, true, v.k_scale, v.v_scale};
+    return decode_rules("rx_attn_decode_rules_fp8", pool, q, o, lse, hq, req_idx, seq_len, rtt, rtt_stride, batch, workspace,
+                        ws_bytes, sm_scale, rules, dev_status, stream);
 }
