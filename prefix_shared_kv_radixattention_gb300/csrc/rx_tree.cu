@@ -105,6 +105,17 @@ struct Tm {
     static __device__ __forceinline__ uint32_t s(int b) { return NT * 128 + (NT == 1 ? b * 128 : 0); }
     static __device__ __forceinline__ uint32_t p(int b) { return 384 + b * 64; }
 };
+// One token a request, up to 16 q heads a kv head (KEYS, see keys_softmax): S and
+// O transposed, two buffers of 16 columns each, P in shared memory: two buffers
+// of 16 rows of 128 weights, in rows of a query buffer that no query has
+constexpr int kKeyRows = 16;
+constexpr uint32_t kKeyTmemCols = 64;
+struct Kt {
+    static __device__ __forceinline__ uint32_t s(int b) { return b * 16; }
+    static __device__ __forceinline__ uint32_t o() { return 32; }
+    static __device__ __forceinline__ uint32_t p(int b) { return 4096 * (1 + b); }  // bytes behind OFF_Q
+    static constexpr int PBLK = kKeyRows * 128;                                     // of 64 weights of each row
+};
 // An item's S, P and product barriers and buffers: with one row tile the items
 // take turns at two; with two row tiles each has its own (but one S for both).
 // c: which item of its row tile it is.
@@ -157,7 +168,7 @@ struct TL {
                          B_VEMPTY = B_VFULL + kStages, B_QFULL = B_VEMPTY + kStages, B_QEMPTY = B_QFULL + QB,
                          B_SFULL = B_QEMPTY + QB, B_SEMPTY = B_SFULL + 2, B_PFULL = B_SEMPTY + 2, B_PVDONE = B_PFULL + 2,
                          B_OEMPTY = B_PVDONE + 2, B_SEGFULL = B_OEMPTY + 2, B_SEGEMPTY = B_SEGFULL + kSegs,
-                         B_FINAL = B_SEGEMPTY + kSegs, N_BAR = B_FINAL + 2;
+                         B_FINAL = B_SEGEMPTY + kSegs, B_TEAM = B_FINAL + 2, N_BAR = B_TEAM + 1;
     static constexpr int OFF_TMEM = OFF_BAR + N_BAR * 8;
     static constexpr int OFF_ABORT = OFF_TMEM + 8;
     static constexpr int OFF_START = OFF_ABORT + 8;                   // Start
@@ -838,7 +849,7 @@ __device__ __forceinline__ void for_items(const TParams &p, unsigned char *smem,
     }
 }
 
-template <int D, bool F8, int NT>
+template <int D, bool F8, int NT, bool KEYS>
 __device__ void issue_qk(const TParams &p, unsigned char *smem, uint32_t sbase)
 {
     using L = TL<D, F8>;
@@ -846,7 +857,8 @@ __device__ void issue_qk(const TParams &p, unsigned char *smem, uint32_t sbase)
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::OFF_TMEM);
     const uint32_t bar = sbase + L::OFF_BAR;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
-    constexpr uint32_t idesc = F8 ? rx::idesc_f16(kRows, kBN, false, false) : rx::idesc_bf16(kRows, kBN, false, false);
+    constexpr int N = KEYS ? kKeyRows : kBN;
+    constexpr uint32_t idesc = F8 ? rx::idesc_f16(kRows, N, false, false) : rx::idesc_bf16(kRows, N, false, false);
     auto wait = [&](int b, uint32_t parity) { return wait_or_abort(bar + 8 * b, parity, abort_flag, p.status); };
     const uint64_t dq = rx::sdesc_sw128(sbase + L::OFF_Q, 16, 1024);
     const uint64_t dk = rx::sdesc_sw128(sbase + L::OFF_K, 16, 1024);
@@ -869,7 +881,8 @@ __device__ void issue_qk(const TParams &p, unsigned char *smem, uint32_t sbase)
 #pragma unroll
         for (int kb = 0; kb < D / 16; ++kb) {
             const uint64_t off = (uint64_t)(((kb >> 2) * L::BLK + (kb & 3) * 32) >> 4);
-            rx::tc_mma(tmem + M::s(turn.b), dqs + off, dks + off, idesc, kb > 0);
+            if constexpr (KEYS) rx::tc_mma(tmem + Kt::s(turn.b), dks + off, dqs + off, idesc, kb > 0);
+            else rx::tc_mma(tmem + M::s(turn.b), dqs + off, dks + off, idesc, kb > 0);
         }
         rx::tc_commit(bar + 8 * (L::B_SFULL + turn.b));
         if (m.t1) rx::tc_commit(bar + 8 * (L::B_KEMPTY + st));
@@ -881,7 +894,7 @@ __device__ void issue_qk(const TParams &p, unsigned char *smem, uint32_t sbase)
     rx::drain_wait(bar + 8 * L::B_FINAL, 0, p.status);
 }
 
-template <int D, bool F8, int NT>
+template <int D, bool F8, int NT, bool KEYS>
 __device__ void issue_pv(const TParams &p, unsigned char *smem, uint32_t sbase)
 {
     using L = TL<D, F8>;
@@ -889,7 +902,7 @@ __device__ void issue_pv(const TParams &p, unsigned char *smem, uint32_t sbase)
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::OFF_TMEM);
     const uint32_t bar = sbase + L::OFF_BAR;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
-    constexpr uint32_t idesc = rx::idesc_bf16(kRows, D, false, true);
+    constexpr uint32_t idesc = KEYS ? rx::idesc_bf16(D, kKeyRows, true, false) : rx::idesc_bf16(kRows, D, false, true);
     auto wait = [&](int b, uint32_t parity) { return wait_or_abort(bar + 8 * b, parity, abort_flag, p.status); };
     const uint64_t dv = rx::sdesc_sw128(sbase + L::OFF_V, L::BLK, 1024);
     for_items<L, NT>(p, smem, sbase, [&](const Item &m) -> bool {
@@ -903,6 +916,11 @@ __device__ void issue_pv(const TParams &p, unsigned char *smem, uint32_t sbase)
         const uint64_t dvs = dv + (uint64_t)((st * L::NB * L::BLK) >> 4);
 #pragma unroll
         for (int ks = 0; ks < kBN / 16; ++ks)
+            if constexpr (KEYS)
+                rx::tc_mma(tmem + Kt::o(), dvs + (uint64_t)((ks * 16 * 128) >> 4),
+                           rx::sdesc_sw128(sbase + L::OFF_Q + Kt::p(turn.b) + (ks >> 2) * Kt::PBLK + (ks & 3) * 32, 16, 1024), idesc,
+                           (!m.first || ks > 0) ? 1u : 0u);
+            else
             rx::tc_mma_ts(tmem + M::o(m.t), tmem + M::p(turn.b) + ks * 8, dvs + (uint64_t)((ks * 16 * 128) >> 4), idesc,
                           (!m.first || ks > 0) ? 1u : 0u);
         rx::tc_commit(bar + 8 * (L::B_PVDONE + turn.b));
@@ -1206,7 +1224,205 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
     }
 }
 
-template <int D, bool F8, int NT, bool RU>
+// One token a request: S^T = K Q^T, a position of the tile a thread, and O^T =
+// V^T P^T.  The few query rows are the products' narrow side (N = 16), so a
+// thread has one weight a row to form where a row of a 128-row tile is 128
+// weights of one thread, the other 127 rows empty: a tile's softmax takes a few
+// hundred cycles, less than its bytes.  The weights go to the tensor core through shared memory (P^T is
+// the operand that has to lie there).  All threads hold the rows' running
+// maxima; a tile that has no score 2^8 above them (one vote of the four warps)
+// leaves them as they are, and with a fixed base there are none.
+template <int D, bool F8>
+__device__ void keys_softmax(const TParams &p, unsigned char *smem, uint32_t sbase)
+{
+    using L = TL<D, F8>;
+    static_assert(D == kRows, "a thread has one column of V");
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::OFF_TMEM);
+    const uint32_t bar = sbase + L::OFF_BAR;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
+    const int key = threadIdx.x, lane = key & 31, warp = key >> 5;   // = TMEM lane: position of the tile, column of V
+    const uint32_t lanes = (uint32_t)(key & ~31) << 16;
+    const int G = p.G;
+    // what the four warps tell one another, in turns of two buffers: a warp writes
+    // a turn's words again two turns later, when all have read them
+    constexpr int kTeam = 4 * kKeyRows;
+    float *words = reinterpret_cast<float *>(smem + L::OFF_MASK);    // no masks here
+    int turns = 0;
+    auto team_words = [&]() { return words + (turns & 1) * kTeam; };
+    auto team = [&]() {  // a bounded wait: a role that gave up elsewhere must not leave the others in a barrier
+        __syncwarp();
+        if (lane == 0) rx::mbar_arrive(bar + 8 * L::B_TEAM);
+        return warp_wait(bar + 8 * L::B_TEAM, turns++ & 1, abort_flag, p.status);
+    };
+    const bool fixed = p.rules.fixed;
+    // this thread's place in a row of P: row n's chunks are swizzled by n
+    const uint32_t p_at = L::OFF_Q + (key >> 6) * Kt::PBLK + (key & 7) * 2;
+    const int chunk = (key & 63) >> 3;
+    int c = 0;
+    for (int s = 0;; ++s) {
+        Seg g;
+        if (!__all_sync(0xffffffffu, get_seg<L, true>(s, g, smem, sbase, p.status))) return;
+        const int lo = g.lo_min, hi = g.P + 1;
+        float m[kKeyRows], l[kKeyRows], slope[kKeyRows];
+#pragma unroll
+        for (int n = 0; n < kKeyRows; ++n) {
+            m[n] = fixed ? p.rules.base : -INFINITY;
+            l[n] = 0.f;
+            slope[n] = p.rules.slope && n < G ? __ldg(p.rules.slope + g.g * G + n) * rx::kLog2e : 0.f;
+        }
+        const float *qs = reinterpret_cast<const float *>(smem + L::OFF_QS) + (s % kRing) * kRows;
+        for (int j = g.j0; j < g.j1; ++j, ++c) {
+            const int b = c & 1, phase = c >> 1;
+            if (!warp_wait(bar + 8 * (L::B_SFULL + b), phase & 1, abort_flag, p.status)) return;
+            rx::tc_fence_after();
+            uint32_t sv[kKeyRows];
+            rx::tmem_ld16(tmem + Kt::s(b) + lanes, sv);
+            rx::tmem_wait_ld();
+            rx::tc_fence_before();
+            rx::mbar_arrive(bar + 8 * (L::B_SEMPTY + b));
+            const int pos = (g.first + j) * kBN + key;
+            const bool seen = pos >= lo && pos < hi;
+            const float far = (float)(hi - 1 - pos);
+            float x[kKeyRows];
+            bool above = false;
+#pragma unroll
+            for (int n = 0; n < kKeyRows; ++n) {
+                if (n >= G) break;
+                const float sl2 = F8 ? qs[n] : p.scale_log2, q = u2f(sv[n]);
+                float y;
+                if (p.rules.c2 > 0.f) {
+                    const float e = rx::fast_exp2(q * fminf(sl2 * p.rules.to_e, 0x1.fffffep127f));
+                    y = fmaf(rx::fast_rcp(e + 1.f), -2.f * p.rules.c2, p.rules.c2 - p.rules.base);
+                } else {
+                    y = q * sl2;
+                }
+                x[n] = seen ? fmaf(-slope[n], far, y) : -INFINITY;
+                above |= x[n] > m[n] + kRescale;
+            }
+            // the product two before has read these columns of P
+            if (phase >= 1 && !warp_wait(bar + 8 * (L::B_PVDONE + b), (phase - 1) & 1, abort_flag, p.status)) return;
+            rx::tc_fence_after();
+            bool raise = false;
+            if (!fixed) {
+                float *v = team_words();
+                above = __any_sync(0xffffffffu, above);
+                if (lane == 0) v[warp] = above ? 1.f : 0.f;
+                if (!team()) return;
+                raise = v[0] + v[1] + v[2] + v[3] > 0.f;
+            }
+            if (raise) {
+                // new maxima: of each warp's positions, then of the four
+                float *red = team_words();
+                float alpha[kKeyRows];
+                bool scale_o = false;
+#pragma unroll
+                for (int n = 0; n < kKeyRows; ++n) {
+                    if (n >= G) break;
+                    float mx = x[n];
+#pragma unroll
+                    for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+                    if (lane == 0) red[warp * kKeyRows + n] = mx;
+                }
+                if (!team()) return;
+#pragma unroll
+                for (int n = 0; n < kKeyRows; ++n) {
+                    alpha[n] = 1.f;
+                    if (n >= G) continue;
+                    const float mx = fmaxf(fmaxf(red[n], red[kKeyRows + n]), fmaxf(red[2 * kKeyRows + n], red[3 * kKeyRows + n]));
+                    if (mx > m[n] + kRescale) {
+                        if (m[n] != -INFINITY) {
+                            alpha[n] = rx::fast_exp2(m[n] - mx);
+                            scale_o = true;
+                        }
+                        l[n] *= alpha[n];
+                        m[n] = mx;
+                    }
+                }
+                if (scale_o) {  // the same answer in all threads
+                    if (!warp_wait(bar + 8 * (L::B_PVDONE + ((c - 1) & 1)), ((c - 1) >> 1) & 1, abort_flag, p.status)) return;
+                    rx::tc_fence_after();
+                    uint32_t o[kKeyRows];
+                    rx::tmem_ld16(tmem + Kt::o() + lanes, o);
+                    rx::tmem_wait_ld();
+#pragma unroll
+                    for (int n = 0; n < kKeyRows; ++n) o[n] = __float_as_uint(u2f(o[n]) * alpha[n]);
+                    rx::tmem_st16(tmem + Kt::o() + lanes, o);
+                    rx::tmem_wait_st();
+                }
+            }
+#pragma unroll
+            for (int n = 0; n < kKeyRows; ++n) {
+                if (n >= G) break;
+                const float w = rx::fast_exp2(fixed || m[n] == -INFINITY ? x[n] : x[n] - m[n]);
+                l[n] += w;
+                // rounded to bf16 for the tensor core, its sum is not (as in softmax_rows)
+                *reinterpret_cast<__nv_bfloat16 *>(smem + p_at + Kt::p(b) + n * 128 + ((chunk ^ (n & 7)) << 4)) = __float2bfloat16_rn(w);
+            }
+            rx::fence_proxy_async_smem();
+            rx::tc_fence_before();
+            rx::mbar_arrive(bar + 8 * (L::B_PFULL + b));
+        }
+        // the rows' sums over all threads
+        float *red = team_words();
+#pragma unroll
+        for (int n = 0; n < kKeyRows; ++n) {
+            if (n >= G) break;
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) l[n] += __shfl_xor_sync(0xffffffffu, l[n], d);
+            if (lane == 0) red[warp * kKeyRows + n] = l[n];
+        }
+        if (!team()) return;
+        float tot[kKeyRows];
+#pragma unroll
+        for (int n = 0; n < kKeyRows; ++n)
+            tot[n] = n < G ? red[n] + red[kKeyRows + n] + red[2 * kKeyRows + n] + red[3 * kKeyRows + n] : 0.f;
+        if (!warp_wait(bar + 8 * (L::B_PVDONE + ((c - 1) & 1)), ((c - 1) >> 1) & 1, abort_flag, p.status)) return;
+        rx::tc_fence_after();
+        uint32_t o[kKeyRows];
+        rx::tmem_ld16(tmem + Kt::o() + lanes, o);
+        rx::tmem_wait_ld();
+        rx::tc_fence_before();
+        rx::mbar_arrive(bar + 8 * L::B_OEMPTY);
+        const uint32_t *nf = reinterpret_cast<const uint32_t *>(smem + L::OFF_NF) + (s % kSegs) * 32;
+        const int64_t orow = (int64_t)g.tok * p.hq + (int64_t)g.g * G;
+        const int64_t prow = (int64_t)(2 * blockIdx.x + (g.j0 == 0 ? 1 : 0)) * kRows;
+        float add = 0.f;  // NaN and infinities of V in this thread's column, dropped from the product
+        if (nf[0]) {
+            const int32_t *slots = p.rtt + (int64_t)g.row * p.rtt_stride;
+            for (int pos = max(lo, (g.first + g.j0) * kBN); pos < min(hi, (g.first + g.j1) * kBN); ++pos) {
+                const int tile = pos / kBN * kBN;
+                if (tile >= g.lo_max && tile + kBN <= hi) {  // not looked at: the product has them
+                    pos = tile + kBN - 1;
+                    continue;
+                }
+                const int64_t slot = __ldg(slots + pos);
+                if (slot < 0 || slot >= p.num_slots) continue;
+                const int64_t at = (slot * p.hkv + g.g) * D + key;
+                float v;
+                if constexpr (F8) v = __half2float(__ushort_as_half((unsigned short)(rx::e4m3x2_to_f16x2(__ldg(p.v + at)) & 0xFFFFu)));
+                else v = __bfloat162float(reinterpret_cast<const bf16 *>(p.v)[at]);
+                if (!isfinite(v)) add += v;
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < kKeyRows; ++n) {
+            if (n >= G) break;
+            const float v = tot[n] == 0.f ? 0.f : u2f(o[n]) * (p.v_scale / tot[n]) + add;
+            if (g.whole) p.o[(orow + n) * D + key] = __float2bfloat16_rn(v);
+            else p.part_o[(prow + n) * D + key] = v;
+            if (key == n) {
+                const float l2 = tot[n] == 0.f ? -INFINITY : m[n] + log2f(tot[n]);
+                if (!g.whole) p.part_l[prow + n] = l2;
+                else if (p.lse) p.lse[orow + n] = l2 * rx::kLn2;
+            }
+        }
+        __syncwarp();
+        if (lane == 0) free_seg<L>(s, sbase);
+        if (g.last) return;
+    }
+}
+
+template <int D, bool F8, int NT, bool RU, bool KEYS>
 __global__ void __launch_bounds__(Ro<NT>::THREADS, 1) tree_kernel(const __grid_constant__ TParams p)
 {
     using L = TL<D, F8>;
@@ -1244,6 +1460,7 @@ __global__ void __launch_bounds__(Ro<NT>::THREADS, 1) tree_kernel(const __grid_c
         }
         rx::mbar_init(bar + 8 * L::B_FINAL, 1);
         rx::mbar_init(bar + 8 * (L::B_FINAL + 1), 1);
+        rx::mbar_init(bar + 8 * L::B_TEAM, 4);  // the softmax warps of keys_softmax
         *reinterpret_cast<volatile int *>(smem + L::OFF_ABORT) = 0;
         rx::fence_mbar_init();
     }
@@ -1268,14 +1485,16 @@ __global__ void __launch_bounds__(Ro<NT>::THREADS, 1) tree_kernel(const __grid_c
         c.left = (int)(first_unit(total, ctas, blockIdx.x + 1) - u0);
         *reinterpret_cast<Start *>(smem + L::OFF_START) = c;
     }
-    if (warp == W::MMA) rx::tmem_alloc(sbase + L::OFF_TMEM, kTmemCols);
+    constexpr uint32_t kCols = KEYS ? kKeyTmemCols : kTmemCols;
+    if (warp == W::MMA) rx::tmem_alloc(sbase + L::OFF_TMEM, kCols);
     rx::tc_fence_before();
     __syncthreads();  // from here on the scan's room holds masks
     rx::tc_fence_after();
 
     if (warp < W::SOFT) {
         rx::reg_inc<W::R_SOFT>();
-        softmax_rows<D, F8, NT, RU>(p, smem, sbase);
+        if constexpr (KEYS) keys_softmax<D, F8>(p, smem, sbase);
+        else softmax_rows<D, F8, NT, RU>(p, smem, sbase);
     } else if (warp < W::Q) {
         rx::reg_dec<W::R_REST>();
         if (warp < W::SOFT + W::PROD) producer<D, F8, NT, false, RU>(p, smem, sbase);
@@ -1285,10 +1504,10 @@ __global__ void __launch_bounds__(Ro<NT>::THREADS, 1) tree_kernel(const __grid_c
         if (warp == W::Q) {
             query_loader<D, F8, NT>(p, smem, sbase);
         } else if (warp == W::MMA) {
-            if ((threadIdx.x & 31) == 0) issue_qk<D, F8, NT>(p, smem, sbase);
+            if ((threadIdx.x & 31) == 0) issue_qk<D, F8, NT, KEYS>(p, smem, sbase);
             __syncwarp();
         } else if (warp == W::PV) {
-            if ((threadIdx.x & 31) == 0) issue_pv<D, F8, NT>(p, smem, sbase);
+            if ((threadIdx.x & 31) == 0) issue_pv<D, F8, NT, KEYS>(p, smem, sbase);
             __syncwarp();
         } else if (warp == W::SCHED) {
             scheduler<D, F8, RU>(p, smem, sbase);
@@ -1298,7 +1517,7 @@ __global__ void __launch_bounds__(Ro<NT>::THREADS, 1) tree_kernel(const __grid_c
     __syncthreads();
     if (warp == W::MMA) {
         rx::tc_fence_after();
-        rx::tmem_dealloc(*reinterpret_cast<volatile uint32_t *>(smem + L::OFF_TMEM), kTmemCols);
+        rx::tmem_dealloc(*reinterpret_cast<volatile uint32_t *>(smem + L::OFF_TMEM), kCols);
     }
 }
 
@@ -1379,21 +1598,21 @@ bool tree_shape_ok(int32_t batch, int32_t hq, int32_t hkv, int32_t D, int32_t ma
 
 // The registers that the kernel is launched with: the shares of the roles are
 // granted out of them, and a share that is not there would be waited for.
-template <int D, bool F8, int NT, bool RU>
+template <int D, bool F8, int NT, bool RU, bool KEYS>
 bool registers_ok()
 {
     cudaFuncAttributes a;
-    return cudaFuncGetAttributes(&a, tree_kernel<D, F8, NT, RU>) == cudaSuccess && a.numRegs >= Ro<NT>::R_LAUNCH;
+    return cudaFuncGetAttributes(&a, tree_kernel<D, F8, NT, RU, KEYS>) == cudaSuccess && a.numRegs >= Ro<NT>::R_LAUNCH;
 }
 
-template <int D, bool F8, bool RU, int NT = 1>
+template <int D, bool F8, bool RU, int NT = 1, bool KEYS = false>
 int launch(const TParams &p, cudaStream_t st)
 {
-    static const bool ok = registers_ok<D, F8, NT, RU>();
+    static const bool ok = registers_ok<D, F8, NT, RU, KEYS>();
     if (!ok) return rx_set_error(RX_ERR_UNSUPPORTED, "tree attention: the kernel was built with too few registers");
     // per device; cheap, and right whichever device is current
-    RX_CUDA_CHECK(cudaFuncSetAttribute(tree_kernel<D, F8, NT, RU>, cudaFuncAttributeMaxDynamicSharedMemorySize, (TL<D, F8>::BYTES)));
-    tree_kernel<D, F8, NT, RU><<<kCtas, Ro<NT>::THREADS, (TL<D, F8>::BYTES), st>>>(p);
+    RX_CUDA_CHECK(cudaFuncSetAttribute(tree_kernel<D, F8, NT, RU, KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (TL<D, F8>::BYTES)));
+    tree_kernel<D, F8, NT, RU, KEYS><<<kCtas, Ro<NT>::THREADS, (TL<D, F8>::BYTES), st>>>(p);
     RX_CUDA_CHECK(cudaGetLastError());
     // a programmatic dependent: it is launched meanwhile and waits on the device
     cudaLaunchConfig_t cfg = {};
@@ -1479,6 +1698,10 @@ int tree_call(const char *who, const TreePool &pool, const void *q, void *o, flo
         return pool.f8 ? launch<D, true, RU>(p, st) : p.nt == 1 ? launch<D, false, RU>(p, st) : launch<D, false, RU, kMaxNt>(p, st);
     };
     using std::integral_constant;
+    // one token a request: the products with the positions as their wide side.
+    // It takes 16 rows, and a head_dim that fills the tensor core's 128 lanes.
+    if (rules && !qo_indptr && p.G <= kKeyRows && pool.D == kRows)
+        return pool.f8 ? launch<kRows, true, true, 1, true>(p, st) : launch<kRows, false, true, 1, true>(p, st);
     if (rules)
         return pool.D == 128 ? run(integral_constant<int, 128>{}, std::true_type{}) : run(integral_constant<int, 64>{}, std::true_type{});
     return pool.D == 128 ? run(integral_constant<int, 128>{}, std::false_type{}) : run(integral_constant<int, 64>{}, std::false_type{});
