@@ -289,7 +289,7 @@ __device__ void tma_producer(const XParams &p, const Tile &T, unsigned char *sme
     for (int j = 0; j < T.ntiles; ++j) {
         const int st = j % kStages;
         // leading tiles shared with an earlier request come from its rows
-        const int jt = RU ? T.first + j : j;
+        const int jt = RU ? T.first + T.ntiles - 1 - j : j;  // the nearest first, see softmax_rows
         const int row = jt < T.share_tiles ? T.share_row0 + jt * kBN : T.stage_row0 + (jt - T.share_tiles) * kBN;
         bool stop = false;
 #pragma unroll
@@ -472,7 +472,9 @@ __device__ void softmax_rows(const XParams &p, const Tile &T, unsigned char *sme
     for (int j = 0; j < T.ntiles; ++j) {
         if (!warp_wait(bar + 8 * (L::B_SFULL + t), j & 1, abort_flag, p.status)) return;
         rx::tc_fence_after();
-        const int kbase = (RU ? T.first + j : j) * kBN;
+        // with rules the nearest tile comes first: scores that fall with the
+        // distance would raise the running maximum at every tile otherwise
+        const int kbase = (RU ? T.first + T.ntiles - 1 - j : j) * kBN;
         // one answer per warp: the masked and unmasked passes below hold
         // different warp-collective tcgen05.ld instructions, so all lanes of
         // a warp must take the same one (the masked pass is exact for every row)

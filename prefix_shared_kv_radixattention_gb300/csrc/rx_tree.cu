@@ -82,7 +82,7 @@ constexpr int kCodeBufs = 3;         // FP8: half tiles of codes in flight, for 
 // The roles of the warps: for each row tile four softmax warps, one query row a
 // thread; producers for K and as many for V; one each that loads the query rows,
 // issues S = Q K^T, hands out the segments, issues the other product.
-template <int NT>
+template <int NT, bool KEYS = false>
 struct Ro {
     static constexpr int SOFT = 4 * NT, PROD = NT == 1 ? 8 : 4;
     static constexpr int ROWS = kBN / PROD;              // rows of a tile each producer warp gathers
@@ -90,11 +90,14 @@ struct Ro {
     static constexpr int THREADS = 32 * (Q + 4);
     // registers a thread, by role (a softmax thread holds a row's 128 scores):
     // 128 x 192 + 640 x 56 of the 768 x 80 launched; with two row tiles
-    // 256 x 168 + 384 x 48 of 640 x 96
-    static constexpr int R_SOFT = NT == 1 ? 192 : 168, R_REST = NT == 1 ? 56 : 48, R_LAUNCH = NT == 1 ? 80 : 96;
+    // 256 x 168 + 384 x 48 of 640 x 96; with a position a softmax thread
+    // 128 x 120 + 640 x 72 of 768 x 80
+    static constexpr int R_SOFT = KEYS ? 120 : NT == 1 ? 192 : 168, R_REST = KEYS ? 72 : NT == 1 ? 56 : 48,
+                         R_LAUNCH = NT == 1 ? 80 : 96;
     static_assert(32 * (SOFT * R_SOFT + (2 * PROD + 4) * R_REST) <= THREADS * R_LAUNCH,
                   "a share is granted out of the launched registers only");
     static_assert(THREADS * R_LAUNCH <= 65536, "registers of an SM");
+    static_assert(ROWS * PROD == kBN, "the producers' rows are a tile");
 };
 // TMEM: an O for each row tile, then S buffers (two; one beside two O), then
 // two P of 64 columns (16-bit pairs)
@@ -139,10 +142,15 @@ struct Seg {
     int nt;          // row tiles: 1 or 2
     int whole;       // every tile of the context: the result is final
     int last;        // the CTA's last segment
-    // with rules on the scores: the position tiles count from this one on; some
-    // row sees lo_min and what follows, every row what lies in [lo_max, its own
-    // position]
-    int first, lo_min, lo_max;
+    // with rules on the scores the position tiles count down from this one: a bias
+    // that falls with the distance lets scores rise along the context, and would
+    // raise the running maximum at every tile (long chat with slopes 593 us, 283
+    // without).  Some row sees lo_min and what follows, every row what lies in
+    // [lo_max, its own position]
+    int top, lo_min, lo_max;
+
+    template <bool RU>
+    __device__ __forceinline__ int tile(int j) const { return RU ? top - j : j; }
 };
 
 template <int D, bool F8>
@@ -371,9 +379,9 @@ __device__ void scheduler(const TParams &p, unsigned char *smem, uint32_t sbase)
         g.whole = g.j0 == 0 && g.j1 == ntiles;
         c.left -= g.j1 - g.j0;
         g.last = c.left <= 0;
-        g.first = g.lo_min = g.lo_max = 0;
+        g.top = g.lo_min = g.lo_max = 0;
         if constexpr (RU) {
-            g.first = __shfl_sync(0xffffffffu, mine.first, l);
+            g.top = __shfl_sync(0xffffffffu, mine.first, l) + ntiles - 1;
             g.lo_min = rx::window_from(p.rules, g.P + g.node);
             g.lo_max = rx::window_from(p.rules, g.P + g.node + g.ntok - 1);
             if (p.rules.see_from) {
@@ -448,7 +456,7 @@ __device__ __forceinline__ bool get_seg(int s, Seg &g, unsigned char *smem, uint
     g = Seg{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w, 0, 0, 0};
     if constexpr (RU) {
         const int4 d = w[3];
-        g.first = d.x;
+        g.top = d.x;
         g.lo_min = d.y;
         g.lo_max = d.z;
     }
@@ -557,14 +565,15 @@ __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
             ++s;
             if (lane == 0) free_seg<L>(s, sbase);
             left = q.j1 - q.j0;
-            lim = q.P + q.T - (q.first + q.j0) * kBN;
-            at = (q.first + q.j0) * kBN;
+            const int from = q.template tile<RU>(q.j0) * kBN;
+            lim = q.P + q.T - from;
+            if constexpr (RU) at = from;
             lo_min = q.lo_min;
             all_from = q.lo_max;
             all_to = q.P + q.node + 1;
             meta = q.g | (q.T << 13) | ((s % kSegs) << 24);
             last = q.last;
-            slots = p.rtt + (int64_t)q.row * p.rtt_stride + (int64_t)(q.first + q.j0) * kBN + r0 + lane;
+            slots = p.rtt + (int64_t)q.row * p.rtt_stride + (int64_t)from + r0 + lane;
         }
         t.lim = lim;
         t.meta = meta;
@@ -572,12 +581,12 @@ __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
             t.at = at;
             t.lo = lo_min - at;
             t.all = at >= all_from && at + kBN <= all_to;
-            at += kBN;
+            at -= kBN;
         }
         if (lane < ROWS && r0 + lane < lim && (!RU || r0 + lane >= t.lo)) t.slot = rx::ld_stream_b32(slots);
         --left;
-        lim -= kBN;
-        slots += kBN;
+        lim += RU ? kBN : -kBN;
+        slots += RU ? -kBN : kBN;
     };
     // slots past the end or outside the pool (flagged) become -1
     auto check = [&](Tile &t) {
@@ -1066,7 +1075,7 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
 #pragma unroll
                     for (int k = 0; k < kBN / 32; ++k) rx::tmem_ld32(tS + k * 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * k));
                     if (F8 && j == g.j0) a.sl2 = reinterpret_cast<const float *>(smem + L::OFF_QS)[(s % kRing) * kRows + row];
-                    const int kbase = (RU ? g.first + j : j) * kBN;
+                    const int kbase = g.template tile<RU>(j) * kBN;
                     float left = a.sl2;  // what the scores are still to be multiplied with
                     if constexpr (RU) {
                         const bool all = __all_sync(0xffffffffu, !valid || (kbase >= lo && kbase + kBN <= hi));
@@ -1208,7 +1217,7 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
             rx::mbar_arrive(bar + 8 * (L::B_OEMPTY + t));
             if constexpr (RU) {
                 if (nf[0] && valid)
-                    add_not_finite_rules<D, F8>(p, g, max(lo, (g.first + g.j0) * kBN), min(hi, (g.first + g.j1) * kBN),
+                    add_not_finite_rules<D, F8>(p, g, max(lo, g.template tile<RU>(g.j1 - 1) * kBN), min(hi, (g.template tile<RU>(g.j0) + 1) * kBN),
                                                 g.whole ? -1 : prow, orow);
             } else if (g.j1 * kBN > g.P) {
                 uint32_t any = 0;
@@ -1280,7 +1289,7 @@ __device__ void keys_softmax(const TParams &p, unsigned char *smem, uint32_t sba
             rx::tmem_wait_ld();
             rx::tc_fence_before();
             rx::mbar_arrive(bar + 8 * (L::B_SEMPTY + b));
-            const int pos = (g.first + j) * kBN + key;
+            const int pos = g.template tile<true>(j) * kBN + key;
             const bool seen = pos >= lo && pos < hi;
             const float far = (float)(hi - 1 - pos);
             float x[kKeyRows];
@@ -1389,7 +1398,7 @@ __device__ void keys_softmax(const TParams &p, unsigned char *smem, uint32_t sba
         float add = 0.f;  // NaN and infinities of V in this thread's column, dropped from the product
         if (nf[0]) {
             const int32_t *slots = p.rtt + (int64_t)g.row * p.rtt_stride;
-            for (int pos = max(lo, (g.first + g.j0) * kBN); pos < min(hi, (g.first + g.j1) * kBN); ++pos) {
+            for (int pos = max(lo, g.template tile<true>(g.j1 - 1) * kBN); pos < min(hi, (g.template tile<true>(g.j0) + 1) * kBN); ++pos) {
                 const int tile = pos / kBN * kBN;
                 if (tile >= g.lo_max && tile + kBN <= hi) {  // not looked at: the product has them
                     pos = tile + kBN - 1;
@@ -1426,7 +1435,7 @@ template <int D, bool F8, int NT, bool RU, bool KEYS>
 __global__ void __launch_bounds__(Ro<NT>::THREADS, 1) tree_kernel(const __grid_constant__ TParams p)
 {
     using L = TL<D, F8>;
-    using W = Ro<NT>;
+    using W = Ro<NT, KEYS>;
     constexpr int kThreads = W::THREADS;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     const uint32_t raw = rx::smem_u32(smem_raw);
@@ -1602,7 +1611,7 @@ template <int D, bool F8, int NT, bool RU, bool KEYS>
 bool registers_ok()
 {
     cudaFuncAttributes a;
-    return cudaFuncGetAttributes(&a, tree_kernel<D, F8, NT, RU, KEYS>) == cudaSuccess && a.numRegs >= Ro<NT>::R_LAUNCH;
+    return cudaFuncGetAttributes(&a, tree_kernel<D, F8, NT, RU, KEYS>) == cudaSuccess && a.numRegs >= Ro<NT, KEYS>::R_LAUNCH;
 }
 
 template <int D, bool F8, bool RU, int NT = 1, bool KEYS = false>
