@@ -109,15 +109,14 @@ struct Tm {
     static __device__ __forceinline__ uint32_t p(int b) { return 384 + b * 64; }
 };
 // One token a request, up to 16 q heads a kv head (KEYS, see keys_softmax): S and
-// O transposed, two buffers of 16 columns each, P in shared memory: two buffers
-// of 16 rows of 128 weights, in rows of a query buffer that no query has
+// O transposed, 16 columns each (S in two buffers), P in shared memory
 constexpr int kKeyRows = 16;
 constexpr uint32_t kKeyTmemCols = 64;
 struct Kt {
     static __device__ __forceinline__ uint32_t s(int b) { return b * 16; }
     static __device__ __forceinline__ uint32_t o() { return 32; }
-    static __device__ __forceinline__ uint32_t p(int b) { return 4096 * (1 + b); }  // bytes behind OFF_Q
-    static constexpr int PBLK = kKeyRows * 128;                                     // of 64 weights of each row
+    static constexpr int PBLK = kKeyRows * 128;                          // bytes of 64 weights of each row
+    static __device__ __forceinline__ uint32_t p(int b) { return b * 2 * PBLK; }  // of a buffer, behind OFF_P
 };
 // An item's S, P and product barriers and buffers: with one row tile the items
 // take turns at two; with two row tiles each has its own (but one S for both).
@@ -153,37 +152,44 @@ struct Seg {
     __device__ __forceinline__ int tile(int j) const { return RU ? top - j : j; }
 };
 
-template <int D, bool F8>
+template <int D, bool F8, bool KEYS = false>
 struct TL {
     static constexpr int NB = D / 64;             // 128-byte column blocks of a row
     static constexpr int BLK = kRows * 128;       // bytes of one column block of a tile
+    // the room that 16 query rows leave goes to what is in flight: a third stage
+    // of K and V, or a fourth half tile of codes
+    static constexpr int QBLK = KEYS ? kKeyRows * 128 : BLK;  // of a query buffer
+    static constexpr int ST = KEYS && !F8 ? 3 : kStages, CB = KEYS ? 4 : kCodeBufs;
     // query buffers: two for bf16 pools (of segments in turn, or of a segment's
     // row tiles); one for FP8 pools, whose codes need the room
     static constexpr int QB = F8 ? 1 : 2;
     static constexpr int CODE = F8 ? kBN * D / 2 : 0;  // bytes of half a tile of codes
     static constexpr int OFF_Q = 0;
-    static constexpr int OFF_K = OFF_Q + QB * NB * BLK;
-    static constexpr int OFF_V = OFF_K + kStages * NB * BLK;
-    static constexpr int OFF_CODE = OFF_V + kStages * NB * BLK;
-    static constexpr int OFF_NF = OFF_CODE + 2 * kCodeBufs * CODE;    // kSegs x 32 words
+    static constexpr int OFF_P = OFF_Q + QB * NB * QBLK;              // KEYS: two buffers of 16 rows of 128 weights
+    static constexpr int OFF_K = OFF_P + (KEYS ? 2 * 2 * QBLK : 0);
+    static constexpr int OFF_V = OFF_K + ST * NB * BLK;
+    static constexpr int OFF_CODE = OFF_V + ST * NB * BLK;
+    static constexpr int OFF_NF = OFF_CODE + 2 * CB * CODE;           // kSegs x 32 words
     static constexpr int OFF_QS = OFF_NF + kSegs * 32 * 4;            // kRing x 128 floats
     static constexpr int OFF_MASK = OFF_QS + kRing * kRows * 4;       // kSegs x 128 tokens x 4 words;
     static constexpr int MASK = kSegs * kMaskT * (kMaskT / 32) * 4;   //   before them, the scan of the lengths
     static_assert((Ro<1>::THREADS + 1) * 8 <= MASK && (Ro<2>::THREADS + 1) * 8 <= MASK, "room for the scan");
     static constexpr int OFF_SEG = OFF_MASK + MASK;
     static constexpr int OFF_BAR = OFF_SEG + kSegs * 64;
-    static constexpr int B_KFULL = 0, B_KEMPTY = B_KFULL + kStages, B_VFULL = B_KEMPTY + kStages,
-                         B_VEMPTY = B_VFULL + kStages, B_QFULL = B_VEMPTY + kStages, B_QEMPTY = B_QFULL + QB,
+    static constexpr int B_KFULL = 0, B_KEMPTY = B_KFULL + ST, B_VFULL = B_KEMPTY + ST,
+                         B_VEMPTY = B_VFULL + ST, B_QFULL = B_VEMPTY + ST, B_QEMPTY = B_QFULL + QB,
                          B_SFULL = B_QEMPTY + QB, B_SEMPTY = B_SFULL + 2, B_PFULL = B_SEMPTY + 2, B_PVDONE = B_PFULL + 2,
                          B_OEMPTY = B_PVDONE + 2, B_SEGFULL = B_OEMPTY + 2, B_SEGEMPTY = B_SEGFULL + kSegs,
-                         B_FINAL = B_SEGEMPTY + kSegs, B_TEAM = B_FINAL + 2, N_BAR = B_TEAM + 1;
+                         B_FINAL = B_SEGEMPTY + kSegs, N_BAR = B_FINAL + 2;
     static constexpr int OFF_TMEM = OFF_BAR + N_BAR * 8;
     static constexpr int OFF_ABORT = OFF_TMEM + 8;
     static constexpr int OFF_START = OFF_ABORT + 8;                   // Start
     static constexpr int BYTES = OFF_START + 32 + 1024;               // + room to align the base to 1024
 };
 static_assert(sizeof(Seg) <= 64, "room of a segment");
-static_assert(TL<128, false>::BYTES <= 226 * 1024 && TL<128, true>::BYTES <= 226 * 1024, "shared memory budget");
+static_assert(TL<128, false>::BYTES <= 226 * 1024 && TL<128, true>::BYTES <= 226 * 1024 &&
+              TL<128, false, true>::BYTES <= 226 * 1024 && TL<128, true, true>::BYTES <= 226 * 1024, "shared memory budget");
+static_assert(TL<128, false, true>::OFF_P % 1024 == 0 && TL<128, true, true>::OFF_K % 1024 == 0, "swizzle atoms");
 static_assert(TL<128, false>::OFF_MASK % 16 == 0 && TL<128, false>::OFF_BAR % 8 == 0, "alignment");
 
 struct TParams {
@@ -343,10 +349,10 @@ __device__ __forceinline__ int64_t first_unit(int64_t total, int ctas, int c) { 
 // tree are among its tiles: under load a read of global memory takes
 // microseconds, which no other role then waits for.  The lanes hold the
 // lengths of 32 requests at a time.
-template <int D, bool F8, bool RU>
+template <int D, bool F8, bool RU, bool KEYS>
 __device__ void scheduler(const TParams &p, unsigned char *smem, uint32_t sbase)
 {
-    using L = TL<D, F8>;
+    using L = TL<D, F8, KEYS>;
     const uint32_t bar = sbase + L::OFF_BAR;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
     const int lane = threadIdx.x & 31;
@@ -511,10 +517,10 @@ __device__ __forceinline__ uint4 widen_f16(uint32_t lo, uint32_t hi)
 // is dropped, noted, and added back to the rows that see it at the end.  With
 // rules on the scores that goes for the tiles that some row does not see all
 // of; positions that no row sees are not read at all.
-template <int D, bool F8, int NT, bool IS_V, bool RU>
+template <int D, bool F8, int NT, bool IS_V, bool RU, bool KEYS>
 __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
 {
-    using L = TL<D, F8>;
+    using L = TL<D, F8, KEYS>;
     constexpr int ROWS = Ro<NT>::ROWS;
     constexpr int EB = F8 ? 1 : 2;                    // bytes of a value
     constexpr int CPR = D * EB / 16;                  // 16-byte chunks of a row
@@ -620,11 +626,11 @@ __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
         take(cur);
         take(nxt);
         for (int n = 0; cur.lim > 0; ++n) {
-            const int st = n % kStages;
+            const int st = n % L::ST;
             take(nx2);
             check(cur);
             const uint32_t off = (IS_V ? L::OFF_V : L::OFF_K) + st * L::NB * L::BLK;
-            if (n >= kStages && !warp_wait(bar_empty + 8 * st, (n / kStages - 1) & 1, abort_flag, p.status)) break;
+            if (n >= L::ST && !warp_wait(bar_empty + 8 * st, (n / L::ST - 1) & 1, abort_flag, p.status)) break;
 #pragma unroll 2
             for (int u = 0; u < U; ++u) {
                 bool ok;
@@ -646,7 +652,7 @@ __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
     } else {
         constexpr int H = U / 2;  // instructions of half a tile
         // chunk u of half-tile buffer b: + b CODE + 512 u
-        const uint32_t mine = L::OFF_CODE + (IS_V ? kCodeBufs * L::CODE : 0) + (uint32_t)(pw * H * 32 + lane) * 16;
+        const uint32_t mine = L::OFF_CODE + (IS_V ? L::CB * L::CODE : 0) + (uint32_t)(pw * H * 32 + lane) * 16;
         auto fetch = [&](const Tile &t, int h, int buf) {
 #pragma unroll
             for (int u = 0; u < H; ++u) {
@@ -671,6 +677,39 @@ __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
                 *reinterpret_cast<uint4 *>(smem + off + sw128(r, 2 * ch + 1 - swap, L::BLK)) = swap ? a : b;
             }
         };
+        if constexpr (L::CB == 4) {  // two whole tiles in flight
+            Tile cur, nxt, nx2, nx3;
+            take(cur);
+            take(nxt);
+            take(nx2);
+            check(cur);
+            check(nxt);
+            fetch(cur, 0, 0);
+            fetch(cur, 1, 1);
+            fetch(nxt, 0, 2);
+            fetch(nxt, 1, 3);
+            for (int n = 0; cur.lim > 0; ++n) {
+                const int st = n % L::ST, buf = (n & 1) * 2;
+                const uint32_t off = (IS_V ? L::OFF_V : L::OFF_K) + st * L::NB * L::BLK;
+                take(nx3);
+                check(nx2);
+                rx::cp_async_wait<3>();  // the first half
+                if (n >= L::ST && !warp_wait(bar_empty + 8 * st, (n / L::ST - 1) & 1, abort_flag, p.status)) break;
+                widen(off, 0, buf);
+                fetch(nx2, 0, buf);
+                rx::cp_async_wait<3>();  // the second
+                widen(off, 1, buf + 1);
+                fetch(nx2, 1, buf + 1);
+                if (IS_V && !cur.all) scrub(off, cur);  // some rows do not see all of the tile
+                rx::fence_proxy_async_smem();
+                rx::mbar_arrive(bar_full + 8 * st);
+                cur = nxt;
+                nxt = nx2;
+                nx2 = nx3;
+            }
+            rx::cp_async_wait_all();
+            return;
+        }
         Tile cur, nxt, nx2;
         take(cur);
         take(nxt);
@@ -681,11 +720,11 @@ __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
         fetch(nxt, 0, 2);
         int buf = 0;  // of the tile's first half; three halves are in flight
         for (int n = 0; cur.lim > 0; ++n) {
-            const int st = n % kStages, buf1 = buf == 2 ? 0 : buf + 1, buf2 = buf1 == 2 ? 0 : buf1 + 1;
+            const int st = n % L::ST, buf1 = buf == 2 ? 0 : buf + 1, buf2 = buf1 == 2 ? 0 : buf1 + 1;
             const uint32_t off = (IS_V ? L::OFF_V : L::OFF_K) + st * L::NB * L::BLK;
             take(nx2);
             rx::cp_async_wait<2>();     // the first half
-            if (n >= kStages && !warp_wait(bar_empty + 8 * st, (n / kStages - 1) & 1, abort_flag, p.status)) break;
+            if (n >= L::ST && !warp_wait(bar_empty + 8 * st, (n / L::ST - 1) & 1, abort_flag, p.status)) break;
             widen(off, 0, buf);
             fetch(nxt, 1, buf);
             rx::cp_async_wait<2>();     // the second
@@ -716,10 +755,10 @@ __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
 //
 // Buffers: with one row tile a segment, of the segments in turn; with two, one
 // for each row tile.
-template <int D, bool F8, int NT>
+template <int D, bool F8, int NT, bool KEYS>
 __device__ void query_loader(const TParams &p, unsigned char *smem, uint32_t sbase)
 {
-    using L = TL<D, F8>;
+    using L = TL<D, F8, KEYS>;
     constexpr int CPR = D / 8, RPI = 32 / CPR;   // chunks of a row, rows of one instruction
     constexpr int UQ = 4;                        // FP8: instructions in flight
     const uint32_t bar = sbase + L::OFF_BAR;
@@ -738,7 +777,7 @@ __device__ void query_loader(const TParams &p, unsigned char *smem, uint32_t sba
             const int buf = NT == 1 ? s % L::QB : t, use = NT == 1 ? s / L::QB : uses[t]++;
             const int M = min(p.tb, g.ntok - t * p.tb) * p.G;
             if (use >= 1 && !(ok = warp_wait(bar + 8 * (L::B_QEMPTY + buf), (use - 1) & 1, abort_flag, p.status))) break;
-            const uint32_t dst = L::OFF_Q + buf * L::NB * L::BLK;
+            const uint32_t dst = L::OFF_Q + buf * L::NB * L::QBLK;
             // this lane's row, its drafted token's query row and its head
             int r = sub;
             const int step_t = RPI / p.G, step_h = RPI - step_t * p.G;
@@ -755,7 +794,7 @@ __device__ void query_loader(const TParams &p, unsigned char *smem, uint32_t sba
             };
             while (r - sub < M) {
                 if constexpr (!F8) {
-                    if (r < M) rx::cp_async_16(sbase + dst + sw128(r, ch, L::BLK), p.q + src, 16);
+                    if (r < M) rx::cp_async_16(sbase + dst + sw128(r, ch, L::QBLK), p.q + src, 16);
                     advance();
                 } else {
                     const int rbase = r;
@@ -782,7 +821,7 @@ __device__ void query_loader(const TParams &p, unsigned char *smem, uint32_t sba
                         for (int k = 0; k < 4; ++k)
                             y[k] = rx::pack_f16(__uint_as_float(w[k] << 16) * up, __uint_as_float(w[k] & 0xFFFF0000u) * up);
                         if (ru < M) {
-                            *reinterpret_cast<uint4 *>(smem + dst + sw128(ru, ch, L::BLK)) = make_uint4(y[0], y[1], y[2], y[3]);
+                            *reinterpret_cast<uint4 *>(smem + dst + sw128(ru, ch, L::QBLK)) = make_uint4(y[0], y[1], y[2], y[3]);
                             // never 0 or infinite: a masked place's score is
                             // -inf times it (a finite one is below 2^31)
                             if (ch == 0)
@@ -861,7 +900,7 @@ __device__ __forceinline__ void for_items(const TParams &p, unsigned char *smem,
 template <int D, bool F8, int NT, bool KEYS>
 __device__ void issue_qk(const TParams &p, unsigned char *smem, uint32_t sbase)
 {
-    using L = TL<D, F8>;
+    using L = TL<D, F8, KEYS>;
     using M = Tm<NT>;
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::OFF_TMEM);
     const uint32_t bar = sbase + L::OFF_BAR;
@@ -872,11 +911,11 @@ __device__ void issue_qk(const TParams &p, unsigned char *smem, uint32_t sbase)
     const uint64_t dq = rx::sdesc_sw128(sbase + L::OFF_Q, 16, 1024);
     const uint64_t dk = rx::sdesc_sw128(sbase + L::OFF_K, 16, 1024);
     for_items<L, NT>(p, smem, sbase, [&](const Item &m) -> bool {
-        const int st = m.n % kStages;
+        const int st = m.n % L::ST;
         const Turn<NT> turn(m.t, m.c);
         const int qb = NT == 1 ? m.seg % L::QB : m.t, quse = NT == 1 ? m.seg / L::QB : m.use;
         if (m.first && !wait(L::B_QFULL + qb, quse & 1)) return false;
-        if (m.t0 && !wait(L::B_KFULL + st, (m.n / kStages) & 1)) return false;
+        if (m.t0 && !wait(L::B_KFULL + st, (m.n / L::ST) & 1)) return false;
         // its S: of the item two before, or with one for both row tiles of the item before
         if constexpr (NT == 1) {
             if (m.c >= 2 && !wait(L::B_SEMPTY + turn.b, (turn.phase - 1) & 1)) return false;
@@ -886,11 +925,12 @@ __device__ void issue_qk(const TParams &p, unsigned char *smem, uint32_t sbase)
         rx::fence_proxy_async_smem();  // rows landed by cp.async -> async proxy
         rx::tc_fence_after();
         const uint64_t dks = dk + (uint64_t)((st * L::NB * L::BLK) >> 4);
-        const uint64_t dqs = dq + (uint64_t)((qb * L::NB * L::BLK) >> 4);
+        const uint64_t dqs = dq + (uint64_t)((qb * L::NB * L::QBLK) >> 4);
 #pragma unroll
         for (int kb = 0; kb < D / 16; ++kb) {
             const uint64_t off = (uint64_t)(((kb >> 2) * L::BLK + (kb & 3) * 32) >> 4);
-            if constexpr (KEYS) rx::tc_mma(tmem + Kt::s(turn.b), dks + off, dqs + off, idesc, kb > 0);
+            if constexpr (KEYS)
+                rx::tc_mma(tmem + Kt::s(turn.b), dks + off, dqs + (uint64_t)(((kb >> 2) * L::QBLK + (kb & 3) * 32) >> 4), idesc, kb > 0);
             else rx::tc_mma(tmem + M::s(turn.b), dqs + off, dks + off, idesc, kb > 0);
         }
         rx::tc_commit(bar + 8 * (L::B_SFULL + turn.b));
@@ -906,7 +946,7 @@ __device__ void issue_qk(const TParams &p, unsigned char *smem, uint32_t sbase)
 template <int D, bool F8, int NT, bool KEYS>
 __device__ void issue_pv(const TParams &p, unsigned char *smem, uint32_t sbase)
 {
-    using L = TL<D, F8>;
+    using L = TL<D, F8, KEYS>;
     using M = Tm<NT>;
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::OFF_TMEM);
     const uint32_t bar = sbase + L::OFF_BAR;
@@ -915,9 +955,9 @@ __device__ void issue_pv(const TParams &p, unsigned char *smem, uint32_t sbase)
     auto wait = [&](int b, uint32_t parity) { return wait_or_abort(bar + 8 * b, parity, abort_flag, p.status); };
     const uint64_t dv = rx::sdesc_sw128(sbase + L::OFF_V, L::BLK, 1024);
     for_items<L, NT>(p, smem, sbase, [&](const Item &m) -> bool {
-        const int st = m.n % kStages;
+        const int st = m.n % L::ST;
         const Turn<NT> turn(m.t, m.c);
-        if (m.t0 && !wait(L::B_VFULL + st, (m.n / kStages) & 1)) return false;
+        if (m.t0 && !wait(L::B_VFULL + st, (m.n / L::ST) & 1)) return false;
         if (m.first && m.use >= 1 && !wait(L::B_OEMPTY + m.t, (m.use - 1) & 1)) return false;
         if (!wait(L::B_PFULL + turn.b, turn.phase & 1)) return false;
         rx::fence_proxy_async_smem();  // V rows landed by cp.async
@@ -927,7 +967,7 @@ __device__ void issue_pv(const TParams &p, unsigned char *smem, uint32_t sbase)
         for (int ks = 0; ks < kBN / 16; ++ks)
             if constexpr (KEYS)
                 rx::tc_mma(tmem + Kt::o(), dvs + (uint64_t)((ks * 16 * 128) >> 4),
-                           rx::sdesc_sw128(sbase + L::OFF_Q + Kt::p(turn.b) + (ks >> 2) * Kt::PBLK + (ks & 3) * 32, 16, 1024), idesc,
+                           rx::sdesc_sw128(sbase + L::OFF_P + Kt::p(turn.b) + (ks >> 2) * Kt::PBLK + (ks & 3) * 32, 16, 1024), idesc,
                            (!m.first || ks > 0) ? 1u : 0u);
             else
             rx::tc_mma_ts(tmem + M::o(m.t), tmem + M::p(turn.b) + ks * 8, dvs + (uint64_t)((ks * 16 * 128) >> 4), idesc,
@@ -1244,7 +1284,7 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
 template <int D, bool F8>
 __device__ void keys_softmax(const TParams &p, unsigned char *smem, uint32_t sbase)
 {
-    using L = TL<D, F8>;
+    using L = TL<D, F8, true>;
     static_assert(D == kRows, "a thread has one column of V");
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::OFF_TMEM);
     const uint32_t bar = sbase + L::OFF_BAR;
@@ -1253,24 +1293,34 @@ __device__ void keys_softmax(const TParams &p, unsigned char *smem, uint32_t sba
     const uint32_t lanes = (uint32_t)(key & ~31) << 16;
     const int G = p.G;
     // what the four warps tell one another, in turns of two buffers: a warp writes
-    // a turn's words again two turns later, when all have read them
+    // a turn's words again two barriers later, when all have read them
     constexpr int kTeam = 4 * kKeyRows;
     float *words = reinterpret_cast<float *>(smem + L::OFF_MASK);    // no masks here
     int turns = 0;
     auto team_words = [&]() { return words + (turns & 1) * kTeam; };
-    auto team = [&]() {  // a bounded wait: a role that gave up elsewhere must not leave the others in a barrier
-        __syncwarp();
-        if (lane == 0) rx::mbar_arrive(bar + 8 * L::B_TEAM);
-        return warp_wait(bar + 8 * L::B_TEAM, turns++ & 1, abort_flag, p.status);
+    // The warps meet in a hardware barrier, which has no limit of its own.  Its
+    // limit is that of the waits before it: a warp whose wait gave up has raised
+    // the abort flag, arrives once more (leave) and returns, and the others look
+    // at the flag behind every barrier and return.
+    auto leave = [&]() { asm volatile("bar.arrive 1, %0;\n" ::"n"(kRows) : "memory"); };
+    auto team_or = [&](bool x, bool &any) {
+        any = rx::named_bar_or(1, kRows, x);
+        ++turns;
+        return *abort_flag == 0;
+    };
+    auto team = [&]() {
+        rx::named_bar_sync(1, kRows);
+        ++turns;
+        return *abort_flag == 0;
     };
     const bool fixed = p.rules.fixed;
     // this thread's place in a row of P: row n's chunks are swizzled by n
-    const uint32_t p_at = L::OFF_Q + (key >> 6) * Kt::PBLK + (key & 7) * 2;
+    const uint32_t p_at = L::OFF_P + (key >> 6) * Kt::PBLK + (key & 7) * 2;
     const int chunk = (key & 63) >> 3;
     int c = 0;
     for (int s = 0;; ++s) {
         Seg g;
-        if (!__all_sync(0xffffffffu, get_seg<L, true>(s, g, smem, sbase, p.status))) return;
+        if (!__all_sync(0xffffffffu, get_seg<L, true>(s, g, smem, sbase, p.status))) return leave();
         const int lo = g.lo_min, hi = g.P + 1;
         float m[kKeyRows], l[kKeyRows], slope[kKeyRows];
 #pragma unroll
@@ -1282,7 +1332,7 @@ __device__ void keys_softmax(const TParams &p, unsigned char *smem, uint32_t sba
         const float *qs = reinterpret_cast<const float *>(smem + L::OFF_QS) + (s % kRing) * kRows;
         for (int j = g.j0; j < g.j1; ++j, ++c) {
             const int b = c & 1, phase = c >> 1;
-            if (!warp_wait(bar + 8 * (L::B_SFULL + b), phase & 1, abort_flag, p.status)) return;
+            if (!warp_wait(bar + 8 * (L::B_SFULL + b), phase & 1, abort_flag, p.status)) return leave();
             rx::tc_fence_after();
             uint32_t sv[kKeyRows];
             rx::tmem_ld16(tmem + Kt::s(b) + lanes, sv);
@@ -1309,16 +1359,10 @@ __device__ void keys_softmax(const TParams &p, unsigned char *smem, uint32_t sba
                 above |= x[n] > m[n] + kRescale;
             }
             // the product two before has read these columns of P
-            if (phase >= 1 && !warp_wait(bar + 8 * (L::B_PVDONE + b), (phase - 1) & 1, abort_flag, p.status)) return;
+            if (phase >= 1 && !warp_wait(bar + 8 * (L::B_PVDONE + b), (phase - 1) & 1, abort_flag, p.status)) return leave();
             rx::tc_fence_after();
             bool raise = false;
-            if (!fixed) {
-                float *v = team_words();
-                above = __any_sync(0xffffffffu, above);
-                if (lane == 0) v[warp] = above ? 1.f : 0.f;
-                if (!team()) return;
-                raise = v[0] + v[1] + v[2] + v[3] > 0.f;
-            }
+            if (!fixed && !team_or(above, raise)) return;
             if (raise) {
                 // new maxima: of each warp's positions, then of the four
                 float *red = team_words();
@@ -1348,7 +1392,7 @@ __device__ void keys_softmax(const TParams &p, unsigned char *smem, uint32_t sba
                     }
                 }
                 if (scale_o) {  // the same answer in all threads
-                    if (!warp_wait(bar + 8 * (L::B_PVDONE + ((c - 1) & 1)), ((c - 1) >> 1) & 1, abort_flag, p.status)) return;
+                    if (!warp_wait(bar + 8 * (L::B_PVDONE + ((c - 1) & 1)), ((c - 1) >> 1) & 1, abort_flag, p.status)) return leave();
                     rx::tc_fence_after();
                     uint32_t o[kKeyRows];
                     rx::tmem_ld16(tmem + Kt::o() + lanes, o);
@@ -1385,7 +1429,7 @@ __device__ void keys_softmax(const TParams &p, unsigned char *smem, uint32_t sba
 #pragma unroll
         for (int n = 0; n < kKeyRows; ++n)
             tot[n] = n < G ? red[n] + red[kKeyRows + n] + red[2 * kKeyRows + n] + red[3 * kKeyRows + n] : 0.f;
-        if (!warp_wait(bar + 8 * (L::B_PVDONE + ((c - 1) & 1)), ((c - 1) >> 1) & 1, abort_flag, p.status)) return;
+        if (!warp_wait(bar + 8 * (L::B_PVDONE + ((c - 1) & 1)), ((c - 1) >> 1) & 1, abort_flag, p.status)) return leave();
         rx::tc_fence_after();
         uint32_t o[kKeyRows];
         rx::tmem_ld16(tmem + Kt::o() + lanes, o);
@@ -1434,7 +1478,7 @@ __device__ void keys_softmax(const TParams &p, unsigned char *smem, uint32_t sba
 template <int D, bool F8, int NT, bool RU, bool KEYS>
 __global__ void __launch_bounds__(Ro<NT>::THREADS, 1) tree_kernel(const __grid_constant__ TParams p)
 {
-    using L = TL<D, F8>;
+    using L = TL<D, F8, KEYS>;
     using W = Ro<NT, KEYS>;
     constexpr int kThreads = W::THREADS;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -1446,7 +1490,7 @@ __global__ void __launch_bounds__(Ro<NT>::THREADS, 1) tree_kernel(const __grid_c
     rx::pdl_launch_dependents();  // the merge kernel may launch and wait on the device
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kStages; ++i) {
+        for (int i = 0; i < L::ST; ++i) {
             rx::mbar_init(bar + 8 * (L::B_KFULL + i), 32 * W::PROD);
             rx::mbar_init(bar + 8 * (L::B_VFULL + i), 32 * W::PROD);
             rx::mbar_init(bar + 8 * (L::B_KEMPTY + i), 1);
@@ -1469,7 +1513,6 @@ __global__ void __launch_bounds__(Ro<NT>::THREADS, 1) tree_kernel(const __grid_c
         }
         rx::mbar_init(bar + 8 * L::B_FINAL, 1);
         rx::mbar_init(bar + 8 * (L::B_FINAL + 1), 1);
-        rx::mbar_init(bar + 8 * L::B_TEAM, 4);  // the softmax warps of keys_softmax
         *reinterpret_cast<volatile int *>(smem + L::OFF_ABORT) = 0;
         rx::fence_mbar_init();
     }
@@ -1506,12 +1549,12 @@ __global__ void __launch_bounds__(Ro<NT>::THREADS, 1) tree_kernel(const __grid_c
         else softmax_rows<D, F8, NT, RU>(p, smem, sbase);
     } else if (warp < W::Q) {
         rx::reg_dec<W::R_REST>();
-        if (warp < W::SOFT + W::PROD) producer<D, F8, NT, false, RU>(p, smem, sbase);
-        else producer<D, F8, NT, true, RU>(p, smem, sbase);
+        if (warp < W::SOFT + W::PROD) producer<D, F8, NT, false, RU, KEYS>(p, smem, sbase);
+        else producer<D, F8, NT, true, RU, KEYS>(p, smem, sbase);
     } else {
         rx::reg_dec<W::R_REST>();
         if (warp == W::Q) {
-            query_loader<D, F8, NT>(p, smem, sbase);
+            query_loader<D, F8, NT, KEYS>(p, smem, sbase);
         } else if (warp == W::MMA) {
             if ((threadIdx.x & 31) == 0) issue_qk<D, F8, NT, KEYS>(p, smem, sbase);
             __syncwarp();
@@ -1519,7 +1562,7 @@ __global__ void __launch_bounds__(Ro<NT>::THREADS, 1) tree_kernel(const __grid_c
             if ((threadIdx.x & 31) == 0) issue_pv<D, F8, NT, KEYS>(p, smem, sbase);
             __syncwarp();
         } else if (warp == W::SCHED) {
-            scheduler<D, F8, RU>(p, smem, sbase);
+            scheduler<D, F8, RU, KEYS>(p, smem, sbase);
         }
     }
     rx::tc_fence_before();
@@ -1620,8 +1663,8 @@ int launch(const TParams &p, cudaStream_t st)
     static const bool ok = registers_ok<D, F8, NT, RU, KEYS>();
     if (!ok) return rx_set_error(RX_ERR_UNSUPPORTED, "tree attention: the kernel was built with too few registers");
     // per device; cheap, and right whichever device is current
-    RX_CUDA_CHECK(cudaFuncSetAttribute(tree_kernel<D, F8, NT, RU, KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (TL<D, F8>::BYTES)));
-    tree_kernel<D, F8, NT, RU, KEYS><<<kCtas, Ro<NT>::THREADS, (TL<D, F8>::BYTES), st>>>(p);
+    RX_CUDA_CHECK(cudaFuncSetAttribute(tree_kernel<D, F8, NT, RU, KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (TL<D, F8, KEYS>::BYTES)));
+    tree_kernel<D, F8, NT, RU, KEYS><<<kCtas, Ro<NT>::THREADS, (TL<D, F8, KEYS>::BYTES), st>>>(p);
     RX_CUDA_CHECK(cudaGetLastError());
     // a programmatic dependent: it is launched meanwhile and waits on the device
     cudaLaunchConfig_t cfg = {};
