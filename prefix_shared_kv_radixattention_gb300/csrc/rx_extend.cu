@@ -79,6 +79,10 @@ constexpr int kThreads = 32 * 12;   // no register reallocation: every warp keep
 constexpr int kStagedThreads = 32 * 10;
 constexpr int kStagedProducerWarp = 8;
 constexpr int kStagedMmaWarp = 9;
+// with rules on the scores: 16 softmax warps
+constexpr int kRulesThreads = 32 * 18;
+constexpr int kRulesProducerWarp = 16;
+constexpr int kRulesMmaWarp = 17;
 constexpr int kStageBlock = 4;     // rows per copy unit of the staging kernel
 constexpr uint32_t kTmemCols = 512;  // per Q tile t: S (then P as bf16) [256t, +128), O [256t + 128, +128)
 constexpr float kRescale = 8.f;      // log2 units the running max may lag
@@ -103,8 +107,11 @@ struct XL {
     static constexpr int OFF_TMEM = OFF_BAR + N_BAR * 8;
     static constexpr int OFF_ABORT = OFF_TMEM + 8;
     static constexpr int BYTES = OFF_ABORT + 8 + 1024;  // + room to align the base to 1024
+    // with rules: what the two threads of a row tell one another, two turns
+    static constexpr int OFF_PAIR = (OFF_ABORT + 8 + 15) / 16 * 16;
+    static constexpr int RULES_BYTES = OFF_PAIR + 2 * 2 * kQT * kRows * 4 + 1024;
 };
-static_assert(XL<128>::BYTES <= 227 * 1024, "shared memory budget");
+static_assert(XL<128>::RULES_BYTES <= 227 * 1024, "shared memory budget");
 static_assert(XL<128>::OFF_BAR % 8 == 0 && XL<64>::OFF_BAR % 8 == 0, "mbarrier alignment");
 
 struct XParams {  // 64-byte aligned through its tensor maps
@@ -279,7 +286,7 @@ __device__ void producer(const XParams &p, const Tile &T, unsigned char *smem, u
 // 128-byte column block, each box kBN rows of one kv head.  Every packed
 // region is a whole number of kBN-row tiles with zeroed padding, so the boxes
 // never leave the request's region.
-template <int D, bool RU>
+template <int D, int RU>
 __device__ void tma_producer(const XParams &p, const Tile &T, unsigned char *smem, uint32_t sbase)
 {
     using L = XL<D>;
@@ -320,7 +327,7 @@ __device__ void tma_producer(const XParams &p, const Tile &T, unsigned char *sme
 // MMA thread
 // ---------------------------------------------------------------------------
 
-template <int D, bool kStaged>
+template <int D, bool kStaged, bool kHalves>
 __device__ void mma_issuer(const XParams &p, const Tile &T, unsigned char *smem, uint32_t sbase,
                            uint32_t tmem)
 {
@@ -367,10 +374,11 @@ __device__ void mma_issuer(const XParams &p, const Tile &T, unsigned char *smem,
         if (!kStaged) rx::fence_proxy_async_smem();  // V rows landed by cp.async
         rx::tc_fence_after();
         const uint64_t dvs = dv + (uint64_t)((st * L::NB * L::KBLK) >> 4);
-        // A = P_t(j) in TMEM: 16 keys per MMA = 8 columns of bf16 pairs
+        // A = P_t(j) in TMEM: 16 keys per MMA = 8 columns of bf16 pairs (kHalves:
+        // those of the second 64 keys over their own scores)
 #pragma unroll
         for (int ks = 0; ks < kBN / 16; ++ks)
-            rx::tc_mma_ts(tmem + t * 256 + 128, tmem + t * 256 + ks * 8, dvs + (uint64_t)((ks * 16 * 128) >> 4),
+            rx::tc_mma_ts(tmem + t * 256 + 128, tmem + t * 256 + ks * 8 + (kHalves && ks >= kBN / 32 ? kBN / 4 : 0), dvs + (uint64_t)((ks * 16 * 128) >> 4),
                           idesc_pv, (j > 0 || ks > 0) ? 1u : 0u);
         rx::tc_commit(bar + 8 * (L::B_PVDONE + t));
         if (t == T.nqt - 1) rx::tc_commit(bar + 8 * (L::B_VEMPTY + st));
@@ -397,9 +405,10 @@ __device__ void mma_issuer(const XParams &p, const Tile &T, unsigned char *smem,
 // ---------------------------------------------------------------------------
 
 // With rules: the NaN and infinities of V at the positions lo .. hi - 1 that a
-// row sees, which staging dropped and noted for each tile, added to its o.
+// row sees, which staging dropped and noted for each tile, added to the nc
+// columns of its o from c0 on.
 template <int D>
-__device__ __noinline__ void add_not_finite(const XParams &p, const Tile &T, int lo, int hi, int64_t orow)
+__device__ __noinline__ void add_not_finite(const XParams &p, const Tile &T, int lo, int hi, int64_t orow, int c0, int nc)
 {
     for (int pos = lo; pos < hi; ++pos) {
         const int jt = pos / kBN;
@@ -411,7 +420,7 @@ __device__ __noinline__ void add_not_finite(const XParams &p, const Tile &T, int
         const int64_t slot = __ldg(T.slots + pos);
         if (slot < 0 || slot >= p.num_slots) continue;
         const int64_t at = (slot * p.hkv + T.g) * D;
-        for (int i = 0; i < D; ++i) {
+        for (int i = c0; i < c0 + nc; ++i) {
             float v;
             if (p.v8) {
                 const uint32_t h = rx::e4m3x2_to_f16x2(__ldg(p.v8 + at + i));
@@ -424,7 +433,7 @@ __device__ __noinline__ void add_not_finite(const XParams &p, const Tile &T, int
     }
 }
 
-template <int D, bool RU>
+template <int D>
 __device__ void softmax_rows(const XParams &p, const Tile &T, unsigned char *smem, uint32_t sbase,
                              uint32_t tmem)
 {
@@ -441,13 +450,6 @@ __device__ void softmax_rows(const XParams &p, const Tile &T, unsigned char *sme
     const uint32_t tO = tbase + 128;
     const int row_lim = T.row0_pos + row / p.G;   // keys at positions <= row_lim are visible
     const float sl2 = p.scale_log2;
-    // with rules: the positions [lo, hi) that the row sees, its head's slope
-    int lo = 0, hi = INT_MAX;
-    float slope = 0.f;
-    if (RU && row < T.M) {
-        rx::seen_range(p.rules, (int)T.qbase + row / p.G, row_lim, T.ctx, lo, hi);
-        if (p.rules.slope) slope = __ldg(p.rules.slope + (int64_t)T.g * p.G + row % p.G) * rx::kLog2e;
-    }
     {
         // this tile's Q rows (CTA row r: token r / G, q head g G + r % G) with
         // coalesced 16-byte copies by the tile's four warps, zeros past the
@@ -467,18 +469,16 @@ __device__ void softmax_rows(const XParams &p, const Tile &T, unsigned char *sme
         rx::fence_proxy_async_smem();
         rx::mbar_arrive(bar + 8 * (L::B_QFULL + t));
     }
-    float m_used = RU && p.rules.fixed ? p.rules.base : -INFINITY, l = 0.f;
+    float m_used = -INFINITY, l = 0.f;
     const uint32_t tS = tbase;  // S_t(j), then P_t(j) over its first kBN / 2 columns
     for (int j = 0; j < T.ntiles; ++j) {
         if (!warp_wait(bar + 8 * (L::B_SFULL + t), j & 1, abort_flag, p.status)) return;
         rx::tc_fence_after();
-        // with rules the nearest tile comes first: scores that fall with the
-        // distance would raise the running maximum at every tile otherwise
-        const int kbase = (RU ? T.first + T.ntiles - 1 - j : j) * kBN;
+        const int kbase = j * kBN;
         // one answer per warp: the masked and unmasked passes below hold
         // different warp-collective tcgen05.ld instructions, so all lanes of
         // a warp must take the same one (the masked pass is exact for every row)
-        const bool need_mask = __any_sync(0xffffffffu, RU ? kbase < lo || kbase + kBN > hi : kbase + kBN - 1 > row_lim);
+        const bool need_mask = __any_sync(0xffffffffu, kbase + kBN - 1 > row_lim);
         // the tile's kBN scores of this row, loaded once (four loads in
         // flight) and kept in registers for the max and the exponentials;
         // the causal test only on tiles that cross the row's bound
@@ -487,19 +487,15 @@ __device__ void softmax_rows(const XParams &p, const Tile &T, unsigned char *sme
         for (int c = 0; c < kBN / 32; ++c)
             rx::tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * c));
         rx::tmem_wait_ld();
-        float left = sl2;  // what the scores are still to be multiplied with
-        if constexpr (RU) {
-            left = rx::apply_rules(sv, p.rules, sl2, slope, row_lim - kbase);
-            if (need_mask) rx::hide(sv, kbase, lo, hi);
-        } else if (need_mask) {
+        if (need_mask) {
 #pragma unroll
             for (int k = 0; k < kBN; ++k)
                 if (kbase + k > row_lim) sv[k] = __float_as_uint(-INFINITY);
         }
         // the row max: four running three-input maxima (few live registers
         // next to the kBN scores)
-        float mx = -INFINITY;
-        if (!RU || !p.rules.fixed) {
+        float mx;
+        {
             float a0 = -INFINITY, a1 = -INFINITY, a2 = -INFINITY, a3 = -INFINITY;
 #pragma unroll
             for (int k = 0; k < kBN / 8; ++k) {
@@ -510,8 +506,8 @@ __device__ void softmax_rows(const XParams &p, const Tile &T, unsigned char *sme
             }
             mx = rx::fmax3(fmaxf(a0, a1), a2, a3);
         }
-        const float m_new = fmaxf(m_used, mx * left);
-        const bool need = (!RU || !p.rules.fixed) && ((m_used == -INFINITY) || (m_new > m_used + kRescale));
+        const float m_new = fmaxf(m_used, mx * sl2);
+        const bool need = (m_used == -INFINITY) || (m_new > m_used + kRescale);
         const float alpha = (need && m_used != -INFINITY) ? rx::fast_exp2(m_used - m_new) : 1.f;
         if (need) {
             l *= alpha;
@@ -522,8 +518,8 @@ __device__ void softmax_rows(const XParams &p, const Tile &T, unsigned char *sme
         // sum in four packed accumulators.  (Measured: moving a share of the
         // exponentials to a polynomial on the FMA pipe is slower here, since
         // the softmax is bound by issue and the ALU pipe, not the exp unit.)
-        const float mu = (m_used == -INFINITY || (RU && p.rules.fixed)) ? 0.f : m_used;
-        const uint64_t scale2 = rx::f2(left, left), negm2 = rx::f2(-mu, -mu);
+        const float mu = (m_used == -INFINITY) ? 0.f : m_used;
+        const uint64_t scale2 = rx::f2(sl2, sl2), negm2 = rx::f2(-mu, -mu);
         uint64_t acc[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int c2 = 0; c2 < kBN / 64; ++c2) {
@@ -571,7 +567,7 @@ __device__ void softmax_rows(const XParams &p, const Tile &T, unsigned char *sme
     const bool valid = row < T.M;
     const int G = p.G;
     const int64_t orow = (T.qbase + row / G) * p.hq + (int64_t)T.g * G + row % G;
-    const float inv = RU && l == 0.f ? 0.f : p.v_scale / l;
+    const float inv = p.v_scale / l;
 #pragma unroll
     for (int c4 = 0; c4 < D / 32; ++c4) {
         uint32_t r[32];
@@ -590,12 +586,175 @@ __device__ void softmax_rows(const XParams &p, const Tile &T, unsigned char *sme
             }
         }
     }
-    if (valid && p.lse) p.lse[orow] = RU && l == 0.f ? -INFINITY : (m_used + log2f(l)) * rx::kLn2;
-    if (RU && valid && __ldg(p.stage_nf)) add_not_finite<D>(p, T, lo, hi, orow);
+    if (valid && p.lse) p.lse[orow] = (m_used + log2f(l)) * rx::kLn2;
 }
 
-template <int D, bool kStaged, bool F8 = false, bool RU = false>
-__global__ void __launch_bounds__(kStaged ? kStagedThreads : kThreads, 1)
+// With rules on the scores, 64 of a tile's 128 keys a thread: a row is shared by
+// two threads of two warps (16 softmax warps), since what bounds the kernel is how
+// long a tile's scores take on their way from S to P, and the cap makes that
+// longer.  A row's two halves agree on the maximum through shared memory, or,
+// with a fixed base, not at all until the end.  P_t lies over the first half of
+// each half's scores.
+//
+// The warps of a pair meet in a hardware barrier, which has no limit of its own.
+// Its limit is that of the waits before it: a warp whose wait gave up has raised
+// the abort flag, arrives once more (leave) and returns, and the other looks at the flag
+// behind every barrier and returns.
+template <int D, int KIND>
+__device__ void softmax_halves(const XParams &p, const Tile &T, unsigned char *smem, uint32_t sbase, uint32_t tmem)
+{
+    using L = XL<D>;
+    constexpr int HK = kBN / 2, HD = D / 2;       // keys and columns of O of a thread
+    const int warp = threadIdx.x >> 5;
+    const int t = warp >> 3, half = (warp >> 2) & 1;   // Q tile, half of its keys
+    if (t >= T.nqt) return;
+    const uint32_t bar = sbase + L::OFF_BAR;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
+    const int rl = threadIdx.x & (kRows - 1);     // row in the Q tile = TMEM lane
+    const int row = t * kRows + rl;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + t * 256 + lanes + half * HK, tO = tmem + t * 256 + 128 + lanes + half * HD;
+    const int row_pos = T.row0_pos + row / p.G;
+    const float sl2 = p.scale_log2;
+    // the positions [lo, hi) that the row sees, its head's slope
+    int lo = 0, hi = INT_MAX;
+    float slope = 0.f;
+    if (row < T.M) {
+        rx::seen_range(p.rules, (int)T.qbase + row / p.G, row_pos, T.ctx, lo, hi);
+        if (KIND == rx::kAnyRules && p.rules.slope) slope = __ldg(p.rules.slope + (int64_t)T.g * p.G + row % p.G) * rx::kLog2e;
+    }
+    {
+        // this tile's Q rows, as in softmax_rows
+        constexpr int CPR = D / 8;
+        const int G = p.G;
+        const uint32_t qd = sbase + L::OFF_Q + t * L::NB * L::QBLK;
+        for (int idx = threadIdx.x & (2 * kRows - 1); idx < kRows * CPR; idx += 2 * kRows) {
+            const int r = idx / CPR, c = idx % CPR;
+            const int qr = t * kRows + r;
+            const bool ok = qr < T.M;
+            const bf16 *src = ok ? p.q + ((T.qbase + qr / G) * p.hq + (int64_t)T.g * G + qr % G) * D + c * 8 : p.q;
+            rx::cp_async_16(qd + sw128(r, c, L::QBLK), src, ok ? 16 : 0);
+        }
+        rx::cp_async_commit();
+        rx::cp_async_wait<0>();
+        rx::fence_proxy_async_smem();
+        rx::mbar_arrive(bar + 8 * (L::B_QFULL + t));
+    }
+    // what the row's two threads tell one another: in turns of two buffers, each
+    // written again when the other thread has passed the barrier behind its reading
+    float *words = reinterpret_cast<float *>(smem + L::OFF_PAIR) + t * 2 * kRows + rl;
+    const int pair = 1 + t * 4 + (warp & 3);
+    auto leave = [&]() { asm volatile("bar.arrive %0, 64;\n" ::"r"(pair) : "memory"); };
+    auto swap = [&](float x, int turn, float &other) {
+        float *w = words + (turn & 1) * 2 * 2 * kRows;
+        w[half * kRows] = x;
+        rx::named_bar_sync(pair, 64);
+        other = w[(half ^ 1) * kRows];
+        return *abort_flag == 0;
+    };
+    float m_used = KIND == rx::kFixedCap ? p.rules.base : -INFINITY, l = 0.f;
+    for (int j = 0; j < T.ntiles; ++j) {
+        if (!warp_wait(bar + 8 * (L::B_SFULL + t), j & 1, abort_flag, p.status)) return leave();
+        rx::tc_fence_after();
+        // the nearest tile comes first: scores that fall with the distance would
+        // raise the running maximum at every tile otherwise
+        const int kbase = (T.first + T.ntiles - 1 - j) * kBN + half * HK;
+        const bool need_mask = __any_sync(0xffffffffu, kbase < lo || kbase + HK > hi);
+        uint32_t sv[HK];
+#pragma unroll
+        for (int c = 0; c < HK / 32; ++c) rx::tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * c));
+        rx::tmem_wait_ld();
+        const float left = rx::apply_rules<KIND>(sv, p.rules, sl2, slope, row_pos - kbase, p.rules.small > 0.f);
+        if (need_mask) rx::hide(sv, kbase, lo, hi);
+        bool need = false;
+        float alpha = 1.f;
+        if constexpr (KIND != rx::kFixedCap) {
+            float a0 = -INFINITY, a1 = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < HK / 4; ++k) {
+                a0 = rx::fmax3(a0, u2f(sv[4 * k]), u2f(sv[4 * k + 1]));
+                a1 = rx::fmax3(a1, u2f(sv[4 * k + 2]), u2f(sv[4 * k + 3]));
+            }
+            float mx = fmaxf(a0, a1), other;
+            if (!swap(mx, j, other)) return;
+            const float m_new = fmaxf(m_used, fmaxf(mx, other) * left);
+            need = (m_used == -INFINITY) || (m_new > m_used + kRescale);
+            if (need) {
+                alpha = m_used != -INFINITY ? rx::fast_exp2(m_used - m_new) : 1.f;
+                l *= alpha;
+                m_used = m_new;
+            }
+        }
+        // P = 2^(x - m) as bf16 pairs over the scores already read, 32 at a time
+        const float mu = (KIND == rx::kFixedCap || m_used == -INFINITY) ? 0.f : m_used;
+        const uint64_t scale2 = rx::f2(left, left), negm2 = rx::f2(-mu, -mu);
+        uint64_t acc[2] = {0, 0};
+#pragma unroll
+        for (int c2 = 0; c2 < HK / 32; ++c2) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                float x0 = u2f(sv[c2 * 32 + 2 * k]), x1 = u2f(sv[c2 * 32 + 2 * k + 1]);
+                if constexpr (KIND != rx::kFixedCap) rx::f2_split(rx::f2_fma(rx::f2(x0, x1), scale2, negm2), x0, x1);
+                const float e0 = rx::fast_exp2(x0), e1 = rx::fast_exp2(x1);  // -inf -> 0
+                acc[k & 1] = rx::f2_add(acc[k & 1], rx::f2(e0, e1));
+                pk[k] = rx::pack_bf16(e0, e1);
+            }
+            rx::tmem_st16(tS + c2 * 16, pk);
+        }
+        if (KIND != rx::kFixedCap && j > 0 && __any_sync(0xffffffffu, need)) {
+            // this half's columns of O (see softmax_rows)
+#pragma unroll
+            for (int c4 = 0; c4 < HD / 32; ++c4) {
+                uint32_t r[32];
+                rx::tmem_ld32(tO + c4 * 32, r);
+                rx::tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 32; ++k) r[k] = __float_as_uint(u2f(r[k]) * alpha);
+                rx::tmem_st32(tO + c4 * 32, r);
+            }
+        }
+        rx::tmem_wait_st();
+        {
+            float a0, a1;
+            rx::f2_split(rx::f2_add(acc[0], acc[1]), a0, a1);
+            l += a0 + a1;
+        }
+        rx::tc_fence_before();
+        rx::mbar_arrive(bar + 8 * (L::B_PFULL + t));
+    }
+    const int jl = T.ntiles - 1;
+    float other;
+    if (!swap(l, T.ntiles, other)) return;
+    // the same order in both threads: one result
+    l = half == 0 ? l + other : other + l;
+    if (!warp_wait(bar + 8 * (L::B_PVDONE + t), jl & 1, abort_flag, p.status)) return;
+    rx::tc_fence_after();
+    const bool valid = row < T.M;
+    const int G = p.G;
+    const int64_t orow = (T.qbase + row / G) * p.hq + (int64_t)T.g * G + row % G;
+    const float inv = l == 0.f ? 0.f : p.v_scale / l;
+#pragma unroll
+    for (int c4 = 0; c4 < HD / 32; ++c4) {
+        uint32_t r[32];
+        rx::tmem_ld32(tO + c4 * 32, r);
+        rx::tmem_wait_ld();
+        if (valid) {
+            uint4 *dst = reinterpret_cast<uint4 *>(p.o + orow * D + half * HD + c4 * 32);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                dst[q] = make_uint4(rx::pack_bf16(u2f(r[8 * q + 0]) * inv, u2f(r[8 * q + 1]) * inv),
+                                    rx::pack_bf16(u2f(r[8 * q + 2]) * inv, u2f(r[8 * q + 3]) * inv),
+                                    rx::pack_bf16(u2f(r[8 * q + 4]) * inv, u2f(r[8 * q + 5]) * inv),
+                                    rx::pack_bf16(u2f(r[8 * q + 6]) * inv, u2f(r[8 * q + 7]) * inv));
+        }
+    }
+    if (valid && half == 0 && p.lse) p.lse[orow] = l == 0.f ? -INFINITY : (m_used + log2f(l)) * rx::kLn2;
+    if (valid && __ldg(p.stage_nf)) add_not_finite<D>(p, T, lo, hi, orow, half * HD, HD);
+}
+
+template <int D, bool kStaged, bool F8 = false, int RU = rx::kNoRules>
+__global__ void __launch_bounds__(RU ? kRulesThreads : kStaged ? kStagedThreads : kThreads, 1)
     extend_kernel(const __grid_constant__ XParams p)
 {
     using L = XL<D>;
@@ -671,9 +830,10 @@ __global__ void __launch_bounds__(kStaged ? kStagedThreads : kThreads, 1)
 
     const uint32_t bar = sbase + L::OFF_BAR;
     const int warp = threadIdx.x >> 5;
-    constexpr int mma_warp = kStaged ? kStagedMmaWarp : kMmaWarp;
+    constexpr int mma_warp = RU ? kRulesMmaWarp : kStaged ? kStagedMmaWarp : kMmaWarp;
+    constexpr int softmax_warps = RU ? 16 : 8, row_threads = RU ? 256 : 128;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kQT; ++i) rx::mbar_init(bar + 8 * (L::B_QFULL + i), 128);  // softmax threads
+        for (int i = 0; i < kQT; ++i) rx::mbar_init(bar + 8 * (L::B_QFULL + i), row_threads);  // softmax threads
         for (int i = 0; i < kStages; ++i) {
             // gather path: every producer thread's copies; staged: the TMA thread's
             // arrival plus the boxes' bytes
@@ -684,7 +844,7 @@ __global__ void __launch_bounds__(kStaged ? kStagedThreads : kThreads, 1)
         }
         for (int i = 0; i < kQT; ++i) {
             rx::mbar_init(bar + 8 * (L::B_SFULL + i), 1);     // MMA commit
-            rx::mbar_init(bar + 8 * (L::B_PFULL + i), 128);   // the tile's softmax threads
+            rx::mbar_init(bar + 8 * (L::B_PFULL + i), row_threads);   // the tile's softmax threads
             rx::mbar_init(bar + 8 * (L::B_PVDONE + i), 1);    // MMA commit
         }
         rx::mbar_init(bar + 8 * L::B_FINAL, 1);
@@ -697,18 +857,19 @@ __global__ void __launch_bounds__(kStaged ? kStagedThreads : kThreads, 1)
     rx::tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::OFF_TMEM);
 
-    if (warp < 8) {
-        softmax_rows<D, RU>(p, T, smem, sbase, tmem);
+    if (warp < softmax_warps) {
+        if constexpr (RU) softmax_halves<D, RU>(p, T, smem, sbase, tmem);
+        else softmax_rows<D>(p, T, smem, sbase, tmem);
     } else {
         if (warp < mma_warp) {
             if (!kStaged) {
                 producer<D, F8>(p, T, smem, sbase);
-            } else if (warp == kStagedProducerWarp) {
+            } else if (warp == (RU ? kRulesProducerWarp : kStagedProducerWarp)) {
                 if ((threadIdx.x & 31) == 0) tma_producer<D, RU>(p, T, smem, sbase);
                 __syncwarp();
             }
         } else {
-            if ((threadIdx.x & 31) == 0) mma_issuer<D, kStaged>(p, T, smem, sbase, tmem);
+            if ((threadIdx.x & 31) == 0) mma_issuer<D, kStaged, RU != rx::kNoRules>(p, T, smem, sbase, tmem);
             __syncwarp();  // the whole warp reaches the exit barrier together
         }
     }
@@ -1044,19 +1205,20 @@ int launch_dependent(void (*kernel)(KArgs...), dim3 grid, unsigned block, size_t
     return RX_OK;
 }
 
-template <int D, bool kStaged, bool F8 = false, bool RU = false>
+template <int D, bool kStaged, bool F8 = false, int RU = rx::kNoRules>
 int launch_extend(const XParams &p, dim3 grid, cudaStream_t st)
 {
+    constexpr int kBytes = RU ? XL<D>::RULES_BYTES : XL<D>::BYTES;
     static bool configured = false;
     if (!configured) {
         RX_CUDA_CHECK(cudaFuncSetAttribute(extend_kernel<D, kStaged, F8, RU>,
-                                           cudaFuncAttributeMaxDynamicSharedMemorySize, XL<D>::BYTES));
+                                           cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes));
         configured = true;
     }
     // staged: a programmatic dependent of the staging copy
     if (kStaged)
-        return launch_dependent(extend_kernel<D, kStaged, F8, RU>, grid, kStagedThreads, XL<D>::BYTES, st, p);
-    extend_kernel<D, kStaged, F8, RU><<<grid, kThreads, XL<D>::BYTES, st>>>(p);
+        return launch_dependent(extend_kernel<D, kStaged, F8, RU>, grid, RU ? kRulesThreads : kStagedThreads, kBytes, st, p);
+    extend_kernel<D, kStaged, F8, RU><<<grid, kThreads, kBytes, st>>>(p);
     RX_CUDA_CHECK(cudaGetLastError());
     return RX_OK;
 }
@@ -1181,7 +1343,16 @@ int extend_call(const char *who, const ExtendPool &pool, const void *q, void *o,
                                req_idx, prefix_len, extend_len, (const int32_t *)share, batch,
                                (const int64_t *)offs, cap, ks, vs, p.hkv * D, dev_status, window, nf)) != RX_OK)
         return rc;
-    if (rules) return D == 128 ? launch_extend<128, true, false, true>(p, grid, st) : launch_extend<64, true, false, true>(p, grid, st);
+    if (rules) {
+        auto run = [&](auto kind) {
+            constexpr int K = decltype(kind)::value;
+            return D == 128 ? launch_extend<128, true, false, K>(p, grid, st) : launch_extend<64, true, false, K>(p, grid, st);
+        };
+        const int kind = rx::rules_kind(ru);
+        return kind == rx::kFixedCap ? run(std::integral_constant<int, rx::kFixedCap>{})
+               : kind == rx::kRange  ? run(std::integral_constant<int, rx::kRange>{})
+                                     : run(std::integral_constant<int, rx::kAnyRules>{});
+    }
     return D == 128 ? launch_extend<128, true>(p, grid, st) : launch_extend<64, true>(p, grid, st);
 }
 

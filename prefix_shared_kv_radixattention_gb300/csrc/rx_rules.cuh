@@ -8,8 +8,9 @@
 // where lo <= j < hi, and takes no part elsewhere.  In log2 units, with
 // E = 2^(2 log2(e) s / cap):
 //     log2(e) cap tanh(s / cap) = c2 - 2 c2 / (1 + E),   c2 = cap log2(e),
-// an exponential and a reciprocal of the special-function units a score; E of 0
-// or infinity gives -c2 and c2.  Its absolute error is c2 times a few 2^-23: for
+// an exponential and a reciprocal of the special-function units a score (E of 0
+// or infinity gives -c2 and c2), or, where every score of a warp's tile is within
+// the cap, a polynomial of degree 11 on the multiply-add units.  Its absolute error is c2 times a few 2^-23: for
 // a cap of 50 under 3e-5 log2 units, a weight's relative error under 2^-15,
 // where the weights are rounded to bf16 (2^-9) for the product with V.
 // (tanh.approx is off by 2^-11 of its value: 0.03 log2 units at that cap.)
@@ -23,6 +24,8 @@
 // caps and biased scores keep the running maximum.
 #pragma once
 
+#include <math.h>
+
 #include "rx_common.cuh"
 
 namespace rx {
@@ -32,6 +35,10 @@ struct Rules {
     float to_e;             // 2 / cap: E = 2^(s sl2 to_e)
     float base;             // the weights' base, where it is fixed
     int fixed;              // the base is fixed
+    // rows whose |q . k| all stay below `small` (0: none may) take the cap from a
+    // polynomial: c2 tanh(s / cap) = q.k (poly[0] + poly[1] (q.k)^2 + ...)
+    float small;
+    float poly[6];
     int window;             // a token sees positions above p - window; INT_MAX: all
     const float *slope;     // [q heads] or null
     const int32_t *see_from;  // [query tokens] or null
@@ -58,27 +65,62 @@ __device__ __forceinline__ void seen_range(const Rules &r, int tok, int p, int c
     if (r.see_to) hi = max(hi, min(__ldg(r.see_to + tok), ctx));
 }
 
+// What a kernel is built for: no cap and no bias; a cap with the fixed base;
+// whatever else.
+enum { kNoRules = 0, kRange = 1, kFixedCap = 2, kAnyRules = 3 };
+inline int rules_kind(const Rules &r) { return r.fixed ? kFixedCap : r.c2 > 0.f || r.slope ? kAnyRules : kRange; }
+
 // N scores q . k of consecutive keys, the first at position kbase, in place: to
 // log2 units (times sl2) with the cap and the bias, less the fixed base where
 // there is one.  dist = p - kbase; slope in log2 units a position.  Scores that
 // have neither cap nor bias stay as they are; the result is what the scores are
-// still to be multiplied with.
-template <int N>
-__device__ __forceinline__ float apply_rules(uint32_t (&sv)[N], const Rules &r, float sl2, float slope, int dist)
+// still to be multiplied with.  poly: the call's scores are all in the units of
+// r.poly.
+template <int KIND, int N>
+__device__ __forceinline__ float apply_rules(uint32_t (&sv)[N], const Rules &r, float sl2, float slope, int dist, bool poly)
 {
-    if (r.c2 > 0.f) {
-        const float ke = fminf(sl2 * r.to_e, 0x1.fffffep127f), top = r.c2 - r.base;
-        const uint64_t ke2 = f2(ke, ke), one2 = f2(1.f, 1.f), minus2 = f2(-2.f * r.c2, -2.f * r.c2), top2 = f2(top, top);
+    if constexpr (KIND == kRange) return sl2;
+    if (KIND == kFixedCap || r.c2 > 0.f) {
+        bool small = false;
+        if (poly) {
+            float a0 = 0.f, a1 = 0.f;
 #pragma unroll
-        for (int k = 0; k < N / 2; ++k) {
-            float a, b;
-            f2_split(f2_mul(f2(__uint_as_float(sv[2 * k]), __uint_as_float(sv[2 * k + 1])), ke2), a, b);
-            f2_split(f2_add(f2(fast_exp2(a), fast_exp2(b)), one2), a, b);
-            f2_split(f2_fma(f2(fast_rcp(a), fast_rcp(b)), minus2, top2), a, b);
-            sv[2 * k] = __float_as_uint(a);
-            sv[2 * k + 1] = __float_as_uint(b);
+            for (int k = 0; k < N / 4; ++k) {
+                a0 = fmax3(a0, fabsf(__uint_as_float(sv[4 * k])), fabsf(__uint_as_float(sv[4 * k + 1])));
+                a1 = fmax3(a1, fabsf(__uint_as_float(sv[4 * k + 2])), fabsf(__uint_as_float(sv[4 * k + 3])));
+            }
+            small = __all_sync(0xffffffffu, fmaxf(a0, a1) <= r.small);
         }
-        if (!r.slope) return 1.f;
+        if (small) {
+            uint64_t c[6];
+#pragma unroll
+            for (int i = 0; i < 6; ++i) c[i] = f2(r.poly[i], r.poly[i]);
+            const uint64_t base2 = f2(-r.base, -r.base);
+#pragma unroll
+            for (int k = 0; k < N / 2; ++k) {
+                const uint64_t s = f2(__uint_as_float(sv[2 * k]), __uint_as_float(sv[2 * k + 1])), z = f2_mul(s, s);
+                uint64_t y = f2_fma(c[5], z, c[4]);
+#pragma unroll
+                for (int i = 3; i >= 0; --i) y = f2_fma(y, z, c[i]);
+                float a, b;
+                f2_split(f2_fma(y, s, base2), a, b);
+                sv[2 * k] = __float_as_uint(a);
+                sv[2 * k + 1] = __float_as_uint(b);
+            }
+        } else {
+            const float ke = fminf(sl2 * r.to_e, 0x1.fffffep127f), top = r.c2 - r.base;
+            const uint64_t ke2 = f2(ke, ke), one2 = f2(1.f, 1.f), minus2 = f2(-2.f * r.c2, -2.f * r.c2), top2 = f2(top, top);
+#pragma unroll
+            for (int k = 0; k < N / 2; ++k) {
+                float a, b;
+                f2_split(f2_mul(f2(__uint_as_float(sv[2 * k]), __uint_as_float(sv[2 * k + 1])), ke2), a, b);
+                f2_split(f2_add(f2(fast_exp2(a), fast_exp2(b)), one2), a, b);
+                f2_split(f2_fma(f2(fast_rcp(a), fast_rcp(b)), minus2, top2), a, b);
+                sv[2 * k] = __float_as_uint(a);
+                sv[2 * k + 1] = __float_as_uint(b);
+            }
+        }
+        if (KIND == kFixedCap || !r.slope) return 1.f;
     } else if (!r.slope) {
         return sl2;
     }
@@ -103,7 +145,8 @@ __device__ __forceinline__ void hide(uint32_t (&sv)[N], int kbase, int lo, int h
 // entry point.  scale_log2: log2 units of a score.
 inline int make_rules(const char *who, const rx_attn_rules *in, float scale_log2, Rules &r)
 {
-    r = Rules{0.f, 0.f, 0.f, 0, INT32_MAX, nullptr, nullptr, nullptr};
+    r = Rules{};
+    r.window = INT32_MAX;
     if (!in) return rx_set_error(RX_ERR_INVALID, "%s: no rules (use the call without them)", who);
     if (!(in->cap >= 0.f) || in->window < 0 || ((reinterpret_cast<uintptr_t>(in->slope) | reinterpret_cast<uintptr_t>(in->see_from) |
                                                  reinterpret_cast<uintptr_t>(in->see_to)) & 3) != 0)
@@ -122,6 +165,17 @@ inline int make_rules(const char *who, const rx_attn_rules *in, float scale_log2
         const float ke = scale_log2 * r.to_e;
         if (!(in->cap >= 1e-3f && in->cap <= 1e6f) || !(ke >= 0x1p-126f && ke < INFINITY))
             return rx_set_error(RX_ERR_UNSUPPORTED, "%s: cap %g (from 1e-3 to 1e6)", who, in->cap);
+        // tanh y = y P(y^2) for |y| <= 1, off by at most 2.4e-7 (least maximum, found by reweighted least squares);
+        // y = k1 q . k
+        static const double P[6] = {0.999996854, -0.333240038, 0.132535251, -0.0509728597, 0.0161141767, -0.00283946378};
+        const double k1 = (double)scale_log2 / r.c2;
+        double c = (double)r.c2 * k1;
+        bool fits = 1. / k1 < 1e18;
+        for (int i = 0; i < 6; ++i, c *= k1 * k1) {
+            r.poly[i] = (float)(P[i] * c);
+            fits = fits && fabs(P[i] * c) > 1e-36 && fabs(P[i] * c) < 1e18;
+        }
+        r.small = fits ? (float)(1. / k1) : 0.f;
         if (r.c2 <= 72.2f && !in->slope) {
             r.fixed = 1;
             r.base = fminf(r.c2, 100.f - r.c2);
