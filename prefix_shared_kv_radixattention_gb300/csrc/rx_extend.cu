@@ -296,7 +296,7 @@ __device__ void tma_producer(const XParams &p, const Tile &T, unsigned char *sme
     for (int j = 0; j < T.ntiles; ++j) {
         const int st = j % kStages;
         // leading tiles shared with an earlier request come from its rows
-        const int jt = RU ? T.first + T.ntiles - 1 - j : j;  // the nearest first, see softmax_rows
+        const int jt = T.first + (RU == rx::kAnyRules ? T.ntiles - 1 - j : j);  // see softmax_halves
         const int row = jt < T.share_tiles ? T.share_row0 + jt * kBN : T.stage_row0 + (jt - T.share_tiles) * kBN;
         bool stop = false;
 #pragma unroll
@@ -656,15 +656,15 @@ __device__ void softmax_halves(const XParams &p, const Tile &T, unsigned char *s
     for (int j = 0; j < T.ntiles; ++j) {
         if (!warp_wait(bar + 8 * (L::B_SFULL + t), j & 1, abort_flag, p.status)) return leave();
         rx::tc_fence_after();
-        // the nearest tile comes first: scores that fall with the distance would
-        // raise the running maximum at every tile otherwise
-        const int kbase = (T.first + T.ntiles - 1 - j) * kBN + half * HK;
+        // with a bias the nearest tile comes first: scores that fall with the
+        // distance would raise the running maximum at every tile otherwise
+        const int kbase = (T.first + (KIND == rx::kAnyRules ? T.ntiles - 1 - j : j)) * kBN + half * HK;
         const bool need_mask = __any_sync(0xffffffffu, kbase < lo || kbase + HK > hi);
         uint32_t sv[HK];
 #pragma unroll
         for (int c = 0; c < HK / 32; ++c) rx::tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * c));
         rx::tmem_wait_ld();
-        const float left = rx::apply_rules<KIND>(sv, p.rules, sl2, slope, row_pos - kbase, p.rules.small > 0.f);
+        const float left = rx::apply_rules<KIND>(sv, p.rules, sl2, slope, row_pos - kbase);
         if (need_mask) rx::hide(sv, kbase, lo, hi);
         bool need = false;
         float alpha = 1.f;

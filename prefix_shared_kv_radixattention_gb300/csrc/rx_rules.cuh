@@ -35,10 +35,8 @@ struct Rules {
     float to_e;             // 2 / cap: E = 2^(s sl2 to_e)
     float base;             // the weights' base, where it is fixed
     int fixed;              // the base is fixed
-    // rows whose |q . k| all stay below `small` (0: none may) take the cap from a
-    // polynomial: c2 tanh(s / cap) = q.k (poly[0] + poly[1] (q.k)^2 + ...)
-    float small;
-    float poly[6];
+    float poly[6];          // c2 tanh y = y (poly[0] + poly[1] y^2 + ...), |y| <= 1
+    float to_y;             // y = s / cap from log2 units
     int window;             // a token sees positions above p - window; INT_MAX: all
     const float *slope;     // [q heads] or null
     const int32_t *see_from;  // [query tokens] or null
@@ -74,36 +72,32 @@ inline int rules_kind(const Rules &r) { return r.fixed ? kFixedCap : r.c2 > 0.f 
 // log2 units (times sl2) with the cap and the bias, less the fixed base where
 // there is one.  dist = p - kbase; slope in log2 units a position.  Scores that
 // have neither cap nor bias stay as they are; the result is what the scores are
-// still to be multiplied with.  poly: the call's scores are all in the units of
-// r.poly.
+// still to be multiplied with.
 template <int KIND, int N>
-__device__ __forceinline__ float apply_rules(uint32_t (&sv)[N], const Rules &r, float sl2, float slope, int dist, bool poly)
+__device__ __forceinline__ float apply_rules(uint32_t (&sv)[N], const Rules &r, float sl2, float slope, int dist)
 {
     if constexpr (KIND == kRange) return sl2;
     if (KIND == kFixedCap || r.c2 > 0.f) {
-        bool small = false;
-        if (poly) {
-            float a0 = 0.f, a1 = 0.f;
+        const float ky = fminf(sl2 * r.to_y, 0x1.fffffep127f);
+        float a0 = 0.f, a1 = 0.f;
 #pragma unroll
-            for (int k = 0; k < N / 4; ++k) {
-                a0 = fmax3(a0, fabsf(__uint_as_float(sv[4 * k])), fabsf(__uint_as_float(sv[4 * k + 1])));
-                a1 = fmax3(a1, fabsf(__uint_as_float(sv[4 * k + 2])), fabsf(__uint_as_float(sv[4 * k + 3])));
-            }
-            small = __all_sync(0xffffffffu, fmaxf(a0, a1) <= r.small);
+        for (int k = 0; k < N / 4; ++k) {
+            a0 = fmax3(a0, fabsf(__uint_as_float(sv[4 * k])), fabsf(__uint_as_float(sv[4 * k + 1])));
+            a1 = fmax3(a1, fabsf(__uint_as_float(sv[4 * k + 2])), fabsf(__uint_as_float(sv[4 * k + 3])));
         }
-        if (small) {
+        if (__all_sync(0xffffffffu, fmaxf(a0, a1) * ky <= 1.f)) {
             uint64_t c[6];
 #pragma unroll
             for (int i = 0; i < 6; ++i) c[i] = f2(r.poly[i], r.poly[i]);
-            const uint64_t base2 = f2(-r.base, -r.base);
+            const uint64_t base2 = f2(-r.base, -r.base), ky2 = f2(ky, ky);
 #pragma unroll
             for (int k = 0; k < N / 2; ++k) {
-                const uint64_t s = f2(__uint_as_float(sv[2 * k]), __uint_as_float(sv[2 * k + 1])), z = f2_mul(s, s);
-                uint64_t y = f2_fma(c[5], z, c[4]);
+                const uint64_t y = f2_mul(f2(__uint_as_float(sv[2 * k]), __uint_as_float(sv[2 * k + 1])), ky2), z = f2_mul(y, y);
+                uint64_t x = f2_fma(c[5], z, c[4]);
 #pragma unroll
-                for (int i = 3; i >= 0; --i) y = f2_fma(y, z, c[i]);
+                for (int i = 3; i >= 0; --i) x = f2_fma(x, z, c[i]);
                 float a, b;
-                f2_split(f2_fma(y, s, base2), a, b);
+                f2_split(f2_fma(x, y, base2), a, b);
                 sv[2 * k] = __float_as_uint(a);
                 sv[2 * k + 1] = __float_as_uint(b);
             }
@@ -165,17 +159,10 @@ inline int make_rules(const char *who, const rx_attn_rules *in, float scale_log2
         const float ke = scale_log2 * r.to_e;
         if (!(in->cap >= 1e-3f && in->cap <= 1e6f) || !(ke >= 0x1p-126f && ke < INFINITY))
             return rx_set_error(RX_ERR_UNSUPPORTED, "%s: cap %g (from 1e-3 to 1e6)", who, in->cap);
-        // tanh y = y P(y^2) for |y| <= 1, off by at most 2.4e-7 (least maximum, found by reweighted least squares);
-        // y = k1 q . k
-        static const double P[6] = {0.999996854, -0.333240038, 0.132535251, -0.0509728597, 0.0161141767, -0.00283946378};
-        const double k1 = (double)scale_log2 / r.c2;
-        double c = (double)r.c2 * k1;
-        bool fits = 1. / k1 < 1e18;
-        for (int i = 0; i < 6; ++i, c *= k1 * k1) {
-            r.poly[i] = (float)(P[i] * c);
-            fits = fits && fabs(P[i] * c) > 1e-36 && fabs(P[i] * c) < 1e18;
-        }
-        r.small = fits ? (float)(1. / k1) : 0.f;
+        // tanh y = y P(y^2) for |y| <= 1, off by at most 2.4e-7 (least maximum, found by reweighted least squares)
+        static const float P[6] = {0.999996854f, -0.333240038f, 0.132535251f, -0.0509728597f, 0.0161141767f, -0.00283946378f};
+        for (int i = 0; i < 6; ++i) r.poly[i] = P[i] * r.c2;
+        r.to_y = 1.f / r.c2;
         if (r.c2 <= 72.2f && !in->slope) {
             r.fixed = 1;
             r.base = fminf(r.c2, 100.f - r.c2);
