@@ -407,19 +407,21 @@ __device__ void mma_issuer(const XParams &p, const Tile &T, unsigned char *smem,
 // With rules: the NaN and infinities of V at the positions lo .. hi - 1 that a
 // row sees, which staging dropped and noted for each tile, added to the nc
 // columns of its o from c0 on.
+// (The tile's fields by value: one whose address is taken lives in memory, in every role.)
 template <int D>
-__device__ __noinline__ void add_not_finite(const XParams &p, const Tile &T, int lo, int hi, int64_t orow, int c0, int nc)
+__device__ __noinline__ void add_not_finite(const XParams &p, const int32_t *slots, int g, int share_tiles, int share_row0,
+                                            int stage_row0, int lo, int hi, int64_t orow, int c0, int nc)
 {
     for (int pos = lo; pos < hi; ++pos) {
         const int jt = pos / kBN;
-        const int row = jt < T.share_tiles ? T.share_row0 + jt * kBN : T.stage_row0 + (jt - T.share_tiles) * kBN;
+        const int row = jt < share_tiles ? share_row0 + jt * kBN : stage_row0 + (jt - share_tiles) * kBN;
         if (__ldg(p.stage_nf + 1 + row / kBN) == 0) {
             pos = jt * kBN + kBN - 1;
             continue;
         }
-        const int64_t slot = __ldg(T.slots + pos);
+        const int64_t slot = __ldg(slots + pos);
         if (slot < 0 || slot >= p.num_slots) continue;
-        const int64_t at = (slot * p.hkv + T.g) * D;
+        const int64_t at = (slot * p.hkv + g) * D;
         for (int i = c0; i < c0 + nc; ++i) {
             float v;
             if (p.v8) {
@@ -433,7 +435,9 @@ __device__ __noinline__ void add_not_finite(const XParams &p, const Tile &T, int
     }
 }
 
-template <int D>
+// RANGE: a row sees the positions [lo, hi) of its own (rules without a cap or a
+// bias), and may see none.
+template <int D, bool RANGE>
 __device__ void softmax_rows(const XParams &p, const Tile &T, unsigned char *smem, uint32_t sbase,
                              uint32_t tmem)
 {
@@ -450,6 +454,8 @@ __device__ void softmax_rows(const XParams &p, const Tile &T, unsigned char *sme
     const uint32_t tO = tbase + 128;
     const int row_lim = T.row0_pos + row / p.G;   // keys at positions <= row_lim are visible
     const float sl2 = p.scale_log2;
+    int lo = 0, hi = INT_MAX;
+    if (RANGE && row < T.M) rx::seen_range(p.rules, (int)T.qbase + row / p.G, row_lim, T.ctx, lo, hi);
     {
         // this tile's Q rows (CTA row r: token r / G, q head g G + r % G) with
         // coalesced 16-byte copies by the tile's four warps, zeros past the
@@ -474,11 +480,11 @@ __device__ void softmax_rows(const XParams &p, const Tile &T, unsigned char *sme
     for (int j = 0; j < T.ntiles; ++j) {
         if (!warp_wait(bar + 8 * (L::B_SFULL + t), j & 1, abort_flag, p.status)) return;
         rx::tc_fence_after();
-        const int kbase = j * kBN;
+        const int kbase = (RANGE ? T.first + j : j) * kBN;
         // one answer per warp: the masked and unmasked passes below hold
         // different warp-collective tcgen05.ld instructions, so all lanes of
         // a warp must take the same one (the masked pass is exact for every row)
-        const bool need_mask = __any_sync(0xffffffffu, kbase + kBN - 1 > row_lim);
+        const bool need_mask = __any_sync(0xffffffffu, RANGE ? kbase < lo || kbase + kBN > hi : kbase + kBN - 1 > row_lim);
         // the tile's kBN scores of this row, loaded once (four loads in
         // flight) and kept in registers for the max and the exponentials;
         // the causal test only on tiles that cross the row's bound
@@ -487,7 +493,9 @@ __device__ void softmax_rows(const XParams &p, const Tile &T, unsigned char *sme
         for (int c = 0; c < kBN / 32; ++c)
             rx::tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * c));
         rx::tmem_wait_ld();
-        if (need_mask) {
+        if (RANGE && need_mask) {
+            rx::hide(sv, kbase, lo, hi);
+        } else if (need_mask) {
 #pragma unroll
             for (int k = 0; k < kBN; ++k)
                 if (kbase + k > row_lim) sv[k] = __float_as_uint(-INFINITY);
@@ -567,7 +575,7 @@ __device__ void softmax_rows(const XParams &p, const Tile &T, unsigned char *sme
     const bool valid = row < T.M;
     const int G = p.G;
     const int64_t orow = (T.qbase + row / G) * p.hq + (int64_t)T.g * G + row % G;
-    const float inv = p.v_scale / l;
+    const float inv = RANGE && l == 0.f ? 0.f : p.v_scale / l;
 #pragma unroll
     for (int c4 = 0; c4 < D / 32; ++c4) {
         uint32_t r[32];
@@ -586,7 +594,8 @@ __device__ void softmax_rows(const XParams &p, const Tile &T, unsigned char *sme
             }
         }
     }
-    if (valid && p.lse) p.lse[orow] = (m_used + log2f(l)) * rx::kLn2;
+    if (valid && p.lse) p.lse[orow] = RANGE && l == 0.f ? -INFINITY : (m_used + log2f(l)) * rx::kLn2;
+    if (RANGE && valid && __ldg(p.stage_nf)) add_not_finite<D>(p, T.slots, T.g, T.share_tiles, T.share_row0, T.stage_row0, lo, hi, orow, 0, D);
 }
 
 // With rules on the scores, 64 of a tile's 128 keys a thread: a row is shared by
@@ -750,11 +759,11 @@ __device__ void softmax_halves(const XParams &p, const Tile &T, unsigned char *s
         }
     }
     if (valid && half == 0 && p.lse) p.lse[orow] = l == 0.f ? -INFINITY : (m_used + log2f(l)) * rx::kLn2;
-    if (valid && __ldg(p.stage_nf)) add_not_finite<D>(p, T, lo, hi, orow, half * HD, HD);
+    if (valid && __ldg(p.stage_nf)) add_not_finite<D>(p, T.slots, T.g, T.share_tiles, T.share_row0, T.stage_row0, lo, hi, orow, half * HD, HD);
 }
 
 template <int D, bool kStaged, bool F8 = false, int RU = rx::kNoRules>
-__global__ void __launch_bounds__(RU ? kRulesThreads : kStaged ? kStagedThreads : kThreads, 1)
+__global__ void __launch_bounds__(RU >= rx::kFixedCap ? kRulesThreads : kStaged ? kStagedThreads : kThreads, 1)
     extend_kernel(const __grid_constant__ XParams p)
 {
     using L = XL<D>;
@@ -809,20 +818,24 @@ __global__ void __launch_bounds__(RU ? kRulesThreads : kStaged ? kStagedThreads 
     T.ctx = (int)(P + E);
     if constexpr (RU) {
         // what the CTA's tokens see together: positions from `least` up to `most`
-        __shared__ int least, most;
-        if (threadIdx.x == 0) {
-            least = INT_MAX;
-            most = T.kv_end;
+        int least = rx::window_from(p.rules, T.row0_pos);
+        if (p.rules.see_from || p.rules.see_to) {
+            __shared__ int ends[2];
+            if (threadIdx.x == 0) {
+                ends[0] = INT_MAX;
+                ends[1] = T.kv_end;
+            }
+            __syncthreads();
+            for (int i = threadIdx.x; i < ntok; i += blockDim.x) {
+                int lo, hi;
+                rx::seen_range(p.rules, (int)T.qbase + i, T.row0_pos + i, T.ctx, lo, hi);
+                atomicMin(&ends[0], lo);
+                if (p.rules.see_to) atomicMax(&ends[1], hi);
+            }
+            __syncthreads();
+            least = ends[0];
+            T.kv_end = ends[1];
         }
-        __syncthreads();
-        for (int i = threadIdx.x; i < ntok; i += blockDim.x) {
-            int lo, hi;
-            rx::seen_range(p.rules, (int)T.qbase + i, T.row0_pos + i, T.ctx, lo, hi);
-            atomicMin(&least, lo);
-            if (p.rules.see_to) atomicMax(&most, hi);
-        }
-        __syncthreads();
-        T.kv_end = most;
         T.first = min(least, T.kv_end - 1) / kBN;  // one tile at least
     }
     T.ntiles = (T.kv_end + kBN - 1) / kBN - T.first;
@@ -830,8 +843,9 @@ __global__ void __launch_bounds__(RU ? kRulesThreads : kStaged ? kStagedThreads 
 
     const uint32_t bar = sbase + L::OFF_BAR;
     const int warp = threadIdx.x >> 5;
-    constexpr int mma_warp = RU ? kRulesMmaWarp : kStaged ? kStagedMmaWarp : kMmaWarp;
-    constexpr int softmax_warps = RU ? 16 : 8, row_threads = RU ? 256 : 128;
+    constexpr bool kHalves = RU >= rx::kFixedCap;  // two softmax threads a row
+    constexpr int mma_warp = kHalves ? kRulesMmaWarp : kStaged ? kStagedMmaWarp : kMmaWarp;
+    constexpr int softmax_warps = kHalves ? 16 : 8, row_threads = kHalves ? 256 : 128;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kQT; ++i) rx::mbar_init(bar + 8 * (L::B_QFULL + i), row_threads);  // softmax threads
         for (int i = 0; i < kStages; ++i) {
@@ -858,18 +872,18 @@ __global__ void __launch_bounds__(RU ? kRulesThreads : kStaged ? kStagedThreads 
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::OFF_TMEM);
 
     if (warp < softmax_warps) {
-        if constexpr (RU) softmax_halves<D, RU>(p, T, smem, sbase, tmem);
-        else softmax_rows<D>(p, T, smem, sbase, tmem);
+        if constexpr (kHalves) softmax_halves<D, RU>(p, T, smem, sbase, tmem);
+        else softmax_rows<D, RU == rx::kRange>(p, T, smem, sbase, tmem);
     } else {
         if (warp < mma_warp) {
             if (!kStaged) {
                 producer<D, F8>(p, T, smem, sbase);
-            } else if (warp == (RU ? kRulesProducerWarp : kStagedProducerWarp)) {
+            } else if (warp == (kHalves ? kRulesProducerWarp : kStagedProducerWarp)) {
                 if ((threadIdx.x & 31) == 0) tma_producer<D, RU>(p, T, smem, sbase);
                 __syncwarp();
             }
         } else {
-            if ((threadIdx.x & 31) == 0) mma_issuer<D, kStaged, RU != rx::kNoRules>(p, T, smem, sbase, tmem);
+            if ((threadIdx.x & 31) == 0) mma_issuer<D, kStaged, kHalves>(p, T, smem, sbase, tmem);
             __syncwarp();  // the whole warp reaches the exit barrier together
         }
     }
@@ -1208,7 +1222,7 @@ int launch_dependent(void (*kernel)(KArgs...), dim3 grid, unsigned block, size_t
 template <int D, bool kStaged, bool F8 = false, int RU = rx::kNoRules>
 int launch_extend(const XParams &p, dim3 grid, cudaStream_t st)
 {
-    constexpr int kBytes = RU ? XL<D>::RULES_BYTES : XL<D>::BYTES;
+    constexpr int kBytes = RU >= rx::kFixedCap ? XL<D>::RULES_BYTES : XL<D>::BYTES;
     static bool configured = false;
     if (!configured) {
         RX_CUDA_CHECK(cudaFuncSetAttribute(extend_kernel<D, kStaged, F8, RU>,
@@ -1217,7 +1231,7 @@ int launch_extend(const XParams &p, dim3 grid, cudaStream_t st)
     }
     // staged: a programmatic dependent of the staging copy
     if (kStaged)
-        return launch_dependent(extend_kernel<D, kStaged, F8, RU>, grid, RU ? kRulesThreads : kStagedThreads, kBytes, st, p);
+        return launch_dependent(extend_kernel<D, kStaged, F8, RU>, grid, RU >= rx::kFixedCap ? kRulesThreads : kStagedThreads, kBytes, st, p);
     extend_kernel<D, kStaged, F8, RU><<<grid, kThreads, kBytes, st>>>(p);
     RX_CUDA_CHECK(cudaGetLastError());
     return RX_OK;

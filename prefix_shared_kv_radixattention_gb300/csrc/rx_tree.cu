@@ -1011,20 +1011,22 @@ __device__ __noinline__ void add_not_finite(const TParams &p, const uint32_t *nf
 }
 
 // With rules: those of V at positions from .. to - 1, all of them seen by the
-// row, that lie in tiles that some row of the segment does not see all of.
+// row, that lie in tiles that some row of the segment (the first at first_pos)
+// does not see all of.
 template <int D, bool F8>
-__device__ __noinline__ void add_not_finite_rules(const TParams &p, const Seg &g, int from, int to, int64_t part, int64_t orow)
+__device__ __noinline__ void add_not_finite_rules(const TParams &p, int row, int g, int lo_max, int first_pos, int from, int to,
+                                                  int64_t part, int64_t orow)
 {
-    const int32_t *slots = p.rtt + (int64_t)g.row * p.rtt_stride;
+    const int32_t *slots = p.rtt + (int64_t)row * p.rtt_stride;
     for (int pos = from; pos < to; ++pos) {
         const int tile = pos / kBN * kBN;
-        if (tile >= g.lo_max && tile + kBN <= g.P + g.node + 1) {  // not looked at: the product has them
+        if (tile >= lo_max && tile + kBN <= first_pos + 1) {  // not looked at: the product has them
             pos = tile + kBN - 1;
             continue;
         }
         const int64_t slot = __ldg(slots + pos);
         if (slot < 0 || slot >= p.num_slots) continue;
-        const int64_t at = (slot * p.hkv + g.g) * D;
+        const int64_t at = (slot * p.hkv + g) * D;
         for (int i = 0; i < D; ++i) {
             float v;
             if constexpr (F8) {
@@ -1257,7 +1259,7 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
             rx::mbar_arrive(bar + 8 * (L::B_OEMPTY + t));
             if constexpr (RU) {
                 if (nf[0] && valid)
-                    add_not_finite_rules<D, F8>(p, g, max(lo, g.template tile<RU>(g.j1 - 1) * kBN), min(hi, (g.template tile<RU>(g.j0) + 1) * kBN),
+                    add_not_finite_rules<D, F8>(p, g.row, g.g, g.lo_max, g.P + g.node, max(lo, g.template tile<RU>(g.j1 - 1) * kBN), min(hi, (g.template tile<RU>(g.j0) + 1) * kBN),
                                                 g.whole ? -1 : prow, orow);
             } else if (g.j1 * kBN > g.P) {
                 uint32_t any = 0;
