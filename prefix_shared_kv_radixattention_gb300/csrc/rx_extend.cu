@@ -673,7 +673,7 @@ __device__ void softmax_halves(const XParams &p, const Tile &T, unsigned char *s
 #pragma unroll
         for (int c = 0; c < HK / 32; ++c) rx::tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * c));
         rx::tmem_wait_ld();
-        const float left = rx::apply_rules<KIND>(sv, p.rules, sl2, slope, row_pos - kbase);
+        const float left = rx::apply_rules<KIND, true>(sv, p.rules, sl2, slope, row_pos - kbase);
         if (need_mask) rx::hide(sv, kbase, lo, hi);
         bool need = false;
         float alpha = 1.f;

@@ -10,7 +10,8 @@
 //     log2(e) cap tanh(s / cap) = c2 - 2 c2 / (1 + E),   c2 = cap log2(e),
 // an exponential and a reciprocal of the special-function units a score (E of 0
 // or infinity gives -c2 and c2), or, where every score of a warp's tile is within
-// the cap, a polynomial of degree 11 on the multiply-add units.  Its absolute error is c2 times a few 2^-23: for
+// the cap, a polynomial of degree 11 on the multiply-add units, within half the
+// cap one of degree 7 (long chat extend, a cap of 50: CAPTIMES).  Its absolute error is c2 times a few 2^-23: for
 // a cap of 50 under 3e-5 log2 units, a weight's relative error under 2^-15,
 // where the weights are rounded to bf16 (2^-9) for the product with V.
 // (tanh.approx is off by 2^-11 of its value: 0.03 log2 units at that cap.)
@@ -37,6 +38,10 @@ struct Rules {
     int fixed;              // the base is fixed
     float poly[6];          // c2 tanh y = y (poly[0] + poly[1] y^2 + ...), |y| <= 1
     float to_y;             // y = s / cap from log2 units
+    // in units of the products x = q . k, |x| <= half the cap (0: out of fp32's
+    // range): c2 tanh = x (near[0] + near[1] x^2 + near[2] x^4 + near[3] x^6)
+    float half_cap;
+    float near[4];
     int window;             // a token sees positions above p - window; INT_MAX: all
     const float *slope;     // [q heads] or null
     const int32_t *see_from;  // [query tokens] or null
@@ -72,8 +77,8 @@ inline int rules_kind(const Rules &r) { return r.fixed ? kFixedCap : r.c2 > 0.f 
 // log2 units (times sl2) with the cap and the bias, less the fixed base where
 // there is one.  dist = p - kbase; slope in log2 units a position.  Scores that
 // have neither cap nor bias stay as they are; the result is what the scores are
-// still to be multiplied with.
-template <int KIND, int N>
+// still to be multiplied with.  SAME: sl2 is the call's, not the row's own.
+template <int KIND, bool SAME, int N>
 __device__ __forceinline__ float apply_rules(uint32_t (&sv)[N], const Rules &r, float sl2, float slope, int dist)
 {
     if constexpr (KIND == kRange) return sl2;
@@ -85,7 +90,24 @@ __device__ __forceinline__ float apply_rules(uint32_t (&sv)[N], const Rules &r, 
             a0 = fmax3(a0, fabsf(__uint_as_float(sv[4 * k])), fabsf(__uint_as_float(sv[4 * k + 1])));
             a1 = fmax3(a1, fabsf(__uint_as_float(sv[4 * k + 2])), fabsf(__uint_as_float(sv[4 * k + 3])));
         }
-        if (__all_sync(0xffffffffu, fmaxf(a0, a1) * ky <= 1.f)) {
+        const float most = fmaxf(a0, a1);
+        if (SAME && __all_sync(0xffffffffu, most <= r.half_cap)) {
+            uint64_t c[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c[i] = f2(r.near[i], r.near[i]);
+            const uint64_t base2 = f2(-r.base, -r.base);
+#pragma unroll
+            for (int k = 0; k < N / 2; ++k) {
+                const uint64_t s = f2(__uint_as_float(sv[2 * k]), __uint_as_float(sv[2 * k + 1])), z = f2_mul(s, s);
+                uint64_t x = f2_fma(c[3], z, c[2]);
+                x = f2_fma(x, z, c[1]);
+                x = f2_fma(x, z, c[0]);
+                float a, b;
+                f2_split(f2_fma(x, s, base2), a, b);
+                sv[2 * k] = __float_as_uint(a);
+                sv[2 * k + 1] = __float_as_uint(b);
+            }
+        } else if (__all_sync(0xffffffffu, most * ky <= 1.f)) {
             uint64_t c[6];
 #pragma unroll
             for (int i = 0; i < 6; ++i) c[i] = f2(r.poly[i], r.poly[i]);
@@ -163,6 +185,15 @@ inline int make_rules(const char *who, const rx_attn_rules *in, float scale_log2
         static const float P[6] = {0.999996854f, -0.333240038f, 0.132535251f, -0.0509728597f, 0.0161141767f, -0.00283946378f};
         for (int i = 0; i < 6; ++i) r.poly[i] = P[i] * r.c2;
         r.to_y = 1.f / r.c2;
+        // the same for |y| <= 1/2, off by at most 1.3e-7
+        static const double Q[4] = {0.999997676, -0.333206552, 0.131451454, -0.0433724766};
+        const double k1 = (double)scale_log2 / r.c2;
+        double c = (double)r.c2 * k1;
+        r.half_cap = (float)fmin(0.5 / k1, 1e18);
+        for (int i = 0; i < 4; ++i, c *= k1 * k1) {
+            r.near[i] = (float)(Q[i] * c);
+            if (!(fabs(Q[i] * c) > 1e-36 && fabs(Q[i] * c) < 1e18)) r.half_cap = 0.f;
+        }
         if (r.c2 <= 72.2f && !in->slope) {
             r.fixed = 1;
             r.base = fminf(r.c2, 100.f - r.c2);

@@ -1123,7 +1123,7 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
                         const bool all = __all_sync(0xffffffffu, !valid || (kbase >= lo && kbase + kBN <= hi));
                         rx::tmem_wait_ld();
                         release_s();
-                        left = rx::apply_rules<rx::kAnyRules>(sv, p.rules, a.sl2, slope, at - kbase);
+                        left = rx::apply_rules<rx::kAnyRules, !F8>(sv, p.rules, a.sl2, slope, at - kbase);
                         if (!all) rx::hide(sv, kbase, lo, hi);
                     } else if (kbase + kBN > g.P) {   // drafted positions, or past the last
                         const int off = kbase - g.P, w0 = off >> 5;
