@@ -156,10 +156,10 @@ template <int D, bool F8, bool KEYS = false>
 struct TL {
     static constexpr int NB = D / 64;             // 128-byte column blocks of a row
     static constexpr int BLK = kRows * 128;       // bytes of one column block of a tile
-    // the room that 16 query rows leave goes to what is in flight: a third stage
-    // of K and V, or a fourth half tile of codes
+    // the room that 16 query rows leave goes to a third stage of K and V (a fourth
+    // half tile of codes made windowed E4M3 decode slower, 193 against 176 us)
     static constexpr int QBLK = KEYS ? kKeyRows * 128 : BLK;  // of a query buffer
-    static constexpr int ST = KEYS && !F8 ? 3 : kStages, CB = KEYS ? 4 : kCodeBufs;
+    static constexpr int ST = KEYS && !F8 ? 3 : kStages;
     // query buffers: two for bf16 pools (of segments in turn, or of a segment's
     // row tiles); one for FP8 pools, whose codes need the room
     static constexpr int QB = F8 ? 1 : 2;
@@ -169,7 +169,7 @@ struct TL {
     static constexpr int OFF_K = OFF_P + (KEYS ? 2 * 2 * QBLK : 0);
     static constexpr int OFF_V = OFF_K + ST * NB * BLK;
     static constexpr int OFF_CODE = OFF_V + ST * NB * BLK;
-    static constexpr int OFF_NF = OFF_CODE + 2 * CB * CODE;           // kSegs x 32 words
+    static constexpr int OFF_NF = OFF_CODE + 2 * kCodeBufs * CODE;           // kSegs x 32 words
     static constexpr int OFF_QS = OFF_NF + kSegs * 32 * 4;            // kRing x 128 floats
     static constexpr int OFF_MASK = OFF_QS + kRing * kRows * 4;       // kSegs x 128 tokens x 4 words;
     static constexpr int MASK = kSegs * kMaskT * (kMaskT / 32) * 4;   //   before them, the scan of the lengths
@@ -652,7 +652,7 @@ __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
     } else {
         constexpr int H = U / 2;  // instructions of half a tile
         // chunk u of half-tile buffer b: + b CODE + 512 u
-        const uint32_t mine = L::OFF_CODE + (IS_V ? L::CB * L::CODE : 0) + (uint32_t)(pw * H * 32 + lane) * 16;
+        const uint32_t mine = L::OFF_CODE + (IS_V ? kCodeBufs * L::CODE : 0) + (uint32_t)(pw * H * 32 + lane) * 16;
         auto fetch = [&](const Tile &t, int h, int buf) {
 #pragma unroll
             for (int u = 0; u < H; ++u) {
@@ -677,39 +677,6 @@ __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
                 *reinterpret_cast<uint4 *>(smem + off + sw128(r, 2 * ch + 1 - swap, L::BLK)) = swap ? a : b;
             }
         };
-        if constexpr (L::CB == 4) {  // two whole tiles in flight
-            Tile cur, nxt, nx2, nx3;
-            take(cur);
-            take(nxt);
-            take(nx2);
-            check(cur);
-            check(nxt);
-            fetch(cur, 0, 0);
-            fetch(cur, 1, 1);
-            fetch(nxt, 0, 2);
-            fetch(nxt, 1, 3);
-            for (int n = 0; cur.lim > 0; ++n) {
-                const int st = n % L::ST, buf = (n & 1) * 2;
-                const uint32_t off = (IS_V ? L::OFF_V : L::OFF_K) + st * L::NB * L::BLK;
-                take(nx3);
-                check(nx2);
-                rx::cp_async_wait<3>();  // the first half
-                if (n >= L::ST && !warp_wait(bar_empty + 8 * st, (n / L::ST - 1) & 1, abort_flag, p.status)) break;
-                widen(off, 0, buf);
-                fetch(nx2, 0, buf);
-                rx::cp_async_wait<3>();  // the second
-                widen(off, 1, buf + 1);
-                fetch(nx2, 1, buf + 1);
-                if (IS_V && !cur.all) scrub(off, cur);  // some rows do not see all of the tile
-                rx::fence_proxy_async_smem();
-                rx::mbar_arrive(bar_full + 8 * st);
-                cur = nxt;
-                nxt = nx2;
-                nx2 = nx3;
-            }
-            rx::cp_async_wait_all();
-            return;
-        }
         Tile cur, nxt, nx2;
         take(cur);
         take(nxt);
@@ -1323,6 +1290,11 @@ __device__ void keys_softmax(const TParams &p, unsigned char *smem, uint32_t sba
     for (int s = 0;; ++s) {
         Seg g;
         if (!__all_sync(0xffffffffu, get_seg<L, true>(s, g, smem, sbase, p.status))) return leave();
+        // the same in all lanes, and known to be: loops whose bounds come out of
+        // shared memory are compiled as if lanes could part (windowed E4M3 190, 176 us)
+#pragma unroll
+        for (int k = 0; k < (int)(sizeof(Seg) / 4); ++k)
+            reinterpret_cast<int *>(&g)[k] = __shfl_sync(0xffffffffu, reinterpret_cast<int *>(&g)[k], 0);
         const int lo = g.lo_min, hi = g.P + 1;
         float m[kKeyRows], l[kKeyRows], slope[kKeyRows];
 #pragma unroll
