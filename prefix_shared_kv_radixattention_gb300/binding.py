@@ -1072,6 +1072,21 @@ def _here(t, name):
         raise ValueError(f"{name}: must be on the current CUDA device")
 
 
+def _checked(dtype, named):
+    """_dev for several tensors of one type: these calls are made a layer, and a
+    function call a tensor is a fifth of one on a small batch."""
+    try:
+        for _, t in named:
+            if t is not None and not (t.dtype is dtype and t.is_cuda and t.is_contiguous()):
+                break
+        else:
+            return
+    except AttributeError:
+        pass
+    for name, t in named:
+        _dev(t, dtype, name)
+
+
 class AttnRules:
     """What the calls with rules apply to the scores (rx_attn_rules): cap > 0
     caps them (cap * tanh(s / cap)), window > 0 bounds how far back a token sees,
@@ -1114,53 +1129,51 @@ def rx_attn_rules_workspace(total_ctx_tokens: int, batch: int, num_q_heads: int,
 
 def _rules_args(q, o, lse, lists, req_to_token, rules, workspace, dev_status, head_dim):
     torch = _torch()
-    i32 = torch.int32
-    _dev(q, torch.bfloat16, "q")
-    _dev(o, torch.bfloat16, "o")
+    _checked(torch.bfloat16, (("q", q), ("o", o)))
+    _checked(torch.int32, (*lists, ("req_to_token", req_to_token), ("dev_status", dev_status)))
     _dev(lse, torch.float32, "lse")
-    for name, t in lists:
-        _dev(t, i32, name)
-    _dev(req_to_token, i32, "req_to_token")
     _dev(workspace, torch.uint8, "workspace")
-    _dev(dev_status, i32, "dev_status")
     _here(q, "q")
     if not isinstance(rules, AttnRules):
         raise TypeError("rules: expected an AttnRules")
-    if q.dim() != 3 or q.shape != o.shape or q.shape[2] != head_dim:
+    shape = q.shape
+    if len(shape) != 3 or shape != o.shape or shape[2] != head_dim:
         raise ValueError("q and o must be [tokens, num_q_heads, head_dim], head_dim that of the pools")
-    if lse is not None and lse.shape != q.shape[:2]:
+    n, h, _ = shape
+    if lse is not None and lse.shape != (n, h):
         raise ValueError("lse must be [tokens, num_q_heads]")
     if req_to_token.dim() != 2:
         raise ValueError("req_to_token must be [requests, stride]")
-    return rules._check(q.shape[0], q.shape[1]), 0 if workspace is None else workspace.numel()
+    return rules._check(n, h), 0 if workspace is None else workspace.numel(), n, h
 
 
 def _bf16_pool(k_pool, v_pool, layer):
-    pool = make_pool(k_pool, v_pool, layer)
-    return ctypes.byref(pool), pool.head_dim
+    _checked(_torch().bfloat16, (("k_pool", k_pool), ("v_pool", v_pool)))
+    S, hkv, d, L = _pool_dims(k_pool, v_pool, layer)
+    return ctypes.byref(KVPool(k_pool.data_ptr(), v_pool.data_ptr(), S, hkv, d, L, int(layer))), (S, hkv, d, L)
 
 
 def _fp8_pool(k_pool, v_pool, k_scale, v_scale, layer):
-    torch = _torch()
-    _dev(k_pool, torch.uint8, "k_pool")
-    _dev(v_pool, torch.uint8, "v_pool")
+    _checked(_torch().uint8, (("k_pool", k_pool), ("v_pool", v_pool)))
     S, hkv, d, L = _pool_dims(k_pool, v_pool, layer)
     return ctypes.byref(KVPoolFp8(k_pool.data_ptr(), v_pool.data_ptr(), S, hkv, d, float(k_scale), float(v_scale), L,
-                                  int(layer))), d
+                                  int(layer))), (S, hkv, d, L)
 
 
 def _extend_rules(call, pool, d, q, o, lse, qo_indptr, req_idx, prefix_len, extend_len, req_to_token, max_extend_len,
                   sm_scale, rules, workspace, dev_status, stream):
-    ref, ws_bytes = _rules_args(q, o, lse, (("qo_indptr", qo_indptr), ("req_idx", req_idx), ("prefix_len", prefix_len),
-                                            ("extend_len", extend_len)), req_to_token, rules, workspace, dev_status, d)
+    ref, ws_bytes, n, h = _rules_args(q, o, lse, (("qo_indptr", qo_indptr), ("req_idx", req_idx), ("prefix_len", prefix_len),
+                                                  ("extend_len", extend_len)), req_to_token, rules, workspace, dev_status, d)
     B = req_idx.numel()
     if qo_indptr.numel() != B + 1 or prefix_len.numel() != B or extend_len.numel() != B:
         raise ValueError("qo_indptr must be [batch + 1], prefix_len and extend_len [batch]")
-    if B == 0 or q.shape[0] == 0:
+    if B == 0 or n == 0:
         return  # empty tensors have no address; there is nothing to do
-    _check(call(pool, _ptr(q), _ptr(o), _ptr(lse), q.shape[1], _ptr(qo_indptr), _ptr(req_idx), _ptr(prefix_len),
-                _ptr(extend_len), _ptr(req_to_token), req_to_token.shape[1], B, int(max_extend_len), ref, _ptr(workspace),
-                ws_bytes, float(sm_scale), _ptr(dev_status), _stream(stream)))
+    rc = call(pool, q.data_ptr(), o.data_ptr(), _ptr(lse), h, qo_indptr.data_ptr(), req_idx.data_ptr(), prefix_len.data_ptr(),
+              extend_len.data_ptr(), req_to_token.data_ptr(), req_to_token.shape[1], B, int(max_extend_len), ref, _ptr(workspace),
+              ws_bytes, float(sm_scale), _ptr(dev_status), _stream(stream))
+    if rc:
+        _check(rc)
 
 
 def rx_attn_extend_rules(k_pool, v_pool, q, o, lse, qo_indptr, req_idx, prefix_len, extend_len, req_to_token,
@@ -1169,7 +1182,7 @@ def rx_attn_extend_rules(k_pool, v_pool, q, o, lse, qo_indptr, req_idx, prefix_l
     """rx_attn_extend with rules on the scores; workspace: uint8, at least
     rx_attn_rules_workspace(...) bytes.  Without query tokens (no rows of q) or
     requests the call does nothing."""
-    pool, d = _bf16_pool(k_pool, v_pool, layer)
+    pool, (_, _, d, _) = _bf16_pool(k_pool, v_pool, layer)
     _extend_rules(_lib.rx_attn_extend_rules, pool, d, q, o, lse, qo_indptr, req_idx, prefix_len, extend_len, req_to_token,
                   max_extend_len, sm_scale, rules, workspace, dev_status, stream)
 
@@ -1178,29 +1191,30 @@ def rx_attn_extend_rules_fp8(k_pool, v_pool, k_scale: float, v_scale: float, q, 
                              extend_len, req_to_token, max_extend_len: int, sm_scale: float, rules: AttnRules, workspace,
                              dev_status=None, stream=None, layer: int = 0) -> None:
     """rx_attn_extend_rules over uint8 E4M3 pools ([L,] S, Hkv, d) with per-pool scales."""
-    pool, d = _fp8_pool(k_pool, v_pool, k_scale, v_scale, layer)
+    pool, (_, _, d, _) = _fp8_pool(k_pool, v_pool, k_scale, v_scale, layer)
     _extend_rules(_lib.rx_attn_extend_rules_fp8, pool, d, q, o, lse, qo_indptr, req_idx, prefix_len, extend_len,
                   req_to_token, max_extend_len, sm_scale, rules, workspace, dev_status, stream)
 
 
 def _decode_rules(call, pool, d, q, o, lse, req_idx, seq_len, req_to_token, sm_scale, rules, workspace, dev_status, stream):
-    ref, ws_bytes = _rules_args(q, o, lse, (("req_idx", req_idx), ("seq_len", seq_len)), req_to_token, rules, workspace,
-                                dev_status, d)
+    ref, ws_bytes, n, h = _rules_args(q, o, lse, (("req_idx", req_idx), ("seq_len", seq_len)), req_to_token, rules, workspace,
+                                      dev_status, d)
     B = req_idx.numel()
-    if q.shape[0] != B or seq_len.numel() != B:
+    if n != B or seq_len.numel() != B:
         raise ValueError("q must be [batch, num_q_heads, head_dim] and seq_len [batch]")
     if B == 0:
         return
-    _check(call(pool, _ptr(q), _ptr(o), _ptr(lse), q.shape[1], _ptr(req_idx), _ptr(seq_len), _ptr(req_to_token),
-                req_to_token.shape[1], B, ref, _ptr(workspace), ws_bytes, float(sm_scale), _ptr(dev_status),
-                _stream(stream)))
+    rc = call(pool, q.data_ptr(), o.data_ptr(), _ptr(lse), h, req_idx.data_ptr(), seq_len.data_ptr(), req_to_token.data_ptr(),
+              req_to_token.shape[1], B, ref, _ptr(workspace), ws_bytes, float(sm_scale), _ptr(dev_status), _stream(stream))
+    if rc:
+        _check(rc)
 
 
 def rx_attn_decode_rules(k_pool, v_pool, q, o, lse, req_idx, seq_len, req_to_token, sm_scale: float, rules: AttnRules,
                          workspace, dev_status=None, stream=None, layer: int = 0) -> None:
     """Decode attention (one token a request) with rules on the scores;
     workspace: uint8, at least rx_attn_rules_workspace(0, batch, ...) bytes."""
-    pool, d = _bf16_pool(k_pool, v_pool, layer)
+    pool, (_, _, d, _) = _bf16_pool(k_pool, v_pool, layer)
     _decode_rules(_lib.rx_attn_decode_rules, pool, d, q, o, lse, req_idx, seq_len, req_to_token, sm_scale, rules,
                   workspace, dev_status, stream)
 
@@ -1209,7 +1223,7 @@ def rx_attn_decode_rules_fp8(k_pool, v_pool, k_scale: float, v_scale: float, q, 
                              sm_scale: float, rules: AttnRules, workspace, dev_status=None, stream=None,
                              layer: int = 0) -> None:
     """rx_attn_decode_rules over uint8 E4M3 pools ([L,] S, Hkv, d) with per-pool scales."""
-    pool, d = _fp8_pool(k_pool, v_pool, k_scale, v_scale, layer)
+    pool, (_, _, d, _) = _fp8_pool(k_pool, v_pool, k_scale, v_scale, layer)
     _decode_rules(_lib.rx_attn_decode_rules_fp8, pool, d, q, o, lse, req_idx, seq_len, req_to_token, sm_scale, rules,
                   workspace, dev_status, stream)
 
@@ -1220,12 +1234,8 @@ def _axes_call(call, pool, dims, q, q_out, k_new, v_new, q_weight, k_weight, slo
     S, hkv, dim, L = dims
     n, hq, d, qs = _head_rows(q, "q")
     new, v_row = _head_rows(k_new, "k_new"), _head_rows(v_new, "v_new")
-    _dev(q_out, torch.bfloat16, "q_out")
-    _dev(q_weight, torch.bfloat16, "q_weight")
-    _dev(k_weight, torch.bfloat16, "k_weight")
-    _dev(slots, torch.int32, "slots")
-    _dev(pos, torch.int32, "pos")
-    _dev(dev_status, torch.int32, "dev_status")
+    _checked(torch.bfloat16, (("q_out", q_out), ("q_weight", q_weight), ("k_weight", k_weight)))
+    _checked(torch.int32, (("slots", slots), ("pos", pos), ("dev_status", dev_status)))
     _here(q, "q")
     if new[:3] != (slots.numel(), hkv, dim) or v_row[:3] != new[:3]:
         raise ValueError("k_new/v_new must be [n, num_kv_heads, head_dim] and slots [n]")
@@ -1247,9 +1257,11 @@ def _axes_call(call, pool, dims, q, q_out, k_new, v_new, q_weight, k_weight, slo
         size = pair_axis.size
     if size != d // 2:
         raise ValueError("pair_axis must have head_dim / 2 entries")
-    _check(call(pool, _ptr(q), qs, _ptr(q_out), _ptr(k_new), _ptr(v_new), new[3], 0 if eps is None else 1, _ptr(q_weight),
-                _ptr(k_weight), _ptr(slots), _ptr(pos), n, pos.shape[0], axis, n, hq, float(base),
-                0.0 if eps is None else float(eps), _ptr(dev_status), _stream(stream)))
+    rc = call(pool, q.data_ptr(), qs, q_out.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), new[3], 0 if eps is None else 1,
+              _ptr(q_weight), _ptr(k_weight), slots.data_ptr(), pos.data_ptr(), n, pos.shape[0], axis, n, hq, float(base),
+              0.0 if eps is None else float(eps), _ptr(dev_status), _stream(stream))
+    if rc:
+        _check(rc)
 
 
 def rx_qk_rope_axes_store(k_pool, v_pool, q, q_out, k_new, v_new, q_weight, k_weight, slots, pos, pair_axis, base: float,
@@ -1259,13 +1271,8 @@ def rx_qk_rope_axes_store(k_pool, v_pool, q, q_out, k_new, v_new, q_weight, k_we
     host array), after an RMS norm where eps is given (weights bf16 [d] or None),
     q into q_out, K and V into the pool.  q, k_new, v_new as in
     rx_qk_norm_rope_store."""
-    torch = _torch()
-    _dev(k_pool, torch.bfloat16, "k_pool")
-    _dev(v_pool, torch.bfloat16, "v_pool")
-    dims = _pool_dims(k_pool, v_pool, 0)
-    S, hkv, d, L = dims
-    pool = KVPool(k_pool.data_ptr(), v_pool.data_ptr(), S, hkv, d, L, int(layer))
-    _axes_call(_lib.rx_qk_rope_axes_store, ctypes.byref(pool), dims, q, q_out, k_new, v_new, q_weight, k_weight, slots, pos,
+    pool, dims = _bf16_pool(k_pool, v_pool, layer)
+    _axes_call(_lib.rx_qk_rope_axes_store, pool, dims, q, q_out, k_new, v_new, q_weight, k_weight, slots, pos,
                pair_axis, base, eps, dev_status, stream)
 
 
@@ -1273,8 +1280,8 @@ def rx_qk_rope_axes_store_fp8(k_pool, v_pool, k_scale: float, v_scale: float, q,
                               slots, pos, pair_axis, base: float, eps: Optional[float] = None, dev_status=None, stream=None,
                               layer: int = 0) -> None:
     """rx_qk_rope_axes_store into uint8 E4M3 pools ([L,] S, Hkv, d) with per-pool scales."""
-    pool, _ = _fp8_pool(k_pool, v_pool, k_scale, v_scale, layer)
-    _axes_call(_lib.rx_qk_rope_axes_store_fp8, pool, _pool_dims(k_pool, v_pool, 0), q, q_out, k_new, v_new, q_weight,
+    pool, dims = _fp8_pool(k_pool, v_pool, k_scale, v_scale, layer)
+    _axes_call(_lib.rx_qk_rope_axes_store_fp8, pool, dims, q, q_out, k_new, v_new, q_weight,
                k_weight, slots, pos, pair_axis, base, eps, dev_status, stream)
 
 
@@ -1284,11 +1291,9 @@ def rx_step_maps(req_idx, prefix_len, new_len, req_to_token, num_slots: int, qo_
     seq_len int32 [batch] or None, pos and slots int32 [tokens].  pages int32
     [requests, pages] of page_size slots each: slots come from them and are
     written to req_to_token."""
-    i32 = _torch().int32
-    for t, name in ((req_idx, "req_idx"), (prefix_len, "prefix_len"), (new_len, "new_len"), (req_to_token, "req_to_token"),
-                    (qo_indptr, "qo_indptr"), (seq_len, "seq_len"), (pos, "pos"), (slots, "slots"), (pages, "pages"),
-                    (dev_status, "dev_status")):
-        _dev(t, i32, name)
+    _checked(_torch().int32, (("req_idx", req_idx), ("prefix_len", prefix_len), ("new_len", new_len),
+                              ("req_to_token", req_to_token), ("qo_indptr", qo_indptr), ("seq_len", seq_len), ("pos", pos),
+                              ("slots", slots), ("pages", pages), ("dev_status", dev_status)))
     _here(qo_indptr, "qo_indptr")
     B, n = req_idx.numel(), pos.numel()
     if prefix_len.numel() != B or new_len.numel() != B or qo_indptr.numel() != B + 1 or \
@@ -1296,6 +1301,9 @@ def rx_step_maps(req_idx, prefix_len, new_len, req_to_token, num_slots: int, qo_
         raise ValueError("prefix_len, new_len and seq_len must be [batch], qo_indptr [batch + 1], pos and slots [tokens]")
     if req_to_token.dim() != 2 or (pages is not None and (pages.dim() != 2 or pages.shape[0] != req_to_token.shape[0])):
         raise ValueError("req_to_token must be [requests, stride] and pages [requests, pages]")
-    _check(_lib.rx_step_maps(_ptr(req_idx), _ptr(prefix_len), _ptr(new_len), B, _ptr(req_to_token), req_to_token.shape[1],
-                             _ptr(pages), 0 if pages is None else pages.shape[1], int(page_size), int(num_slots),
-                             _ptr(qo_indptr), _ptr(seq_len), _ptr(pos), _ptr(slots), n, _ptr(dev_status), _stream(stream)))
+    rc = _lib.rx_step_maps(req_idx.data_ptr(), prefix_len.data_ptr(), new_len.data_ptr(), B, req_to_token.data_ptr(),
+                           req_to_token.shape[1], _ptr(pages), 0 if pages is None else pages.shape[1], int(page_size), int(num_slots),
+                           qo_indptr.data_ptr(), _ptr(seq_len), pos.data_ptr(), slots.data_ptr(), n, _ptr(dev_status),
+                           _stream(stream))
+    if rc:
+        _check(rc)

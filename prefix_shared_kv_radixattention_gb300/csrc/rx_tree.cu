@@ -285,16 +285,19 @@ struct __align__(16) Cut {
 };
 
 // Exclusive prefix sums of the requests' units, `per` requests a thread, into
-// pre[0 .. threads]; returns the total.  Whole block.
+// pre[0 .. threads]; returns the total.  mine: the thread's last request.  Whole block.
 template <int THREADS, bool RU>
-__device__ int64_t scan_units(const TParams &p, int64_t *pre, int per, bool flag)
+__device__ int64_t scan_units(const TParams &p, int64_t *pre, int per, bool flag, Req &mine)
 {
     __shared__ int64_t warp_tot[THREADS / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int64_t sum = 0;
     for (int i = 0; i < per; ++i) {
         const int64_t b = (int64_t)threadIdx.x * per + i;
-        if (b < p.batch) sum += load_req<RU>(p, (int)b, flag).units();
+        if (b < p.batch) {
+            mine = load_req<RU>(p, (int)b, flag);
+            sum += mine.units();
+        }
     }
     int64_t x = sum;
 #pragma unroll
@@ -316,29 +319,27 @@ __device__ int64_t scan_units(const TParams &p, int64_t *pre, int per, bool flag
     return total;
 }
 
-// The place of unit u (0 <= u < hkv * per_head); r: its request.
-template <int THREADS, bool RU>
-__device__ Start locate(const TParams &p, const int64_t *pre, int per, int64_t per_head, int64_t u, Req &r)
+// The place of unit u (0 <= u < hkv * per_head), found by the thread whose
+// requests hold it; false in the others.  mine: that of a thread with one request.
+template <bool RU>
+__device__ bool locate(const TParams &p, const int64_t *pre, int per, int64_t per_head, int64_t u, const Req &mine, Start &c)
 {
-    Start c;
     c.left = 0;
     c.total = per_head * p.hkv;
     c.g = (int)(u / per_head);
     int64_t x = u - c.g * per_head;
-    int lo = 0, hi = THREADS - 1;  // the thread whose requests hold unit x
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (pre[mid] <= x) lo = mid; else hi = mid - 1;
-    }
-    x -= pre[lo];
-    c.b = lo * per;
-    for (r = load_req<RU>(p, c.b); x >= r.units(); r = load_req<RU>(p, c.b)) {
-        x -= r.units();
-        ++c.b;
-    }
+    if (pre[threadIdx.x] > x || pre[threadIdx.x + 1] <= x) return false;
+    x -= pre[threadIdx.x];
+    c.b = (int)threadIdx.x * per;
+    Req r = mine;
+    if (per > 1)
+        for (r = load_req<RU>(p, c.b); x >= r.units(); r = load_req<RU>(p, c.b)) {
+            x -= r.units();
+            ++c.b;
+        }
     c.qt = (int)(x / r.ntiles);
     c.j = (int)(x - (int64_t)c.qt * r.ntiles);
-    return c;
+    return true;
 }
 
 // First unit of CTA c out of `ctas` (no more CTAs than units: none is empty).
@@ -1493,7 +1494,8 @@ __global__ void __launch_bounds__(Ro<NT>::THREADS, 1) tree_kernel(const __grid_c
     for (int i = threadIdx.x; i < kSegs * 32; i += kThreads) reinterpret_cast<uint32_t *>(smem + L::OFF_NF)[i] = 0;
     int64_t *pre = reinterpret_cast<int64_t *>(smem + L::OFF_MASK);
     const int per = (p.batch + kThreads - 1) / kThreads;
-    const int64_t per_head = scan_units<kThreads, RU>(p, pre, per, blockIdx.x == 0);
+    Req mine{};
+    const int64_t per_head = scan_units<kThreads, RU>(p, pre, per, blockIdx.x == 0, mine);
     const int64_t total = per_head * p.hkv;
     const int ctas = (int)min((int64_t)gridDim.x, total);
     if ((int)blockIdx.x >= ctas || total / ctas >= INT_MAX) {  // nothing to do, or lengths of no real pool
@@ -1504,12 +1506,13 @@ __global__ void __launch_bounds__(Ro<NT>::THREADS, 1) tree_kernel(const __grid_c
         return;
     }
     static_assert(sizeof(Start) <= 32, "the start's room");
-    if (threadIdx.x == 0) {
+    {
         const int64_t u0 = first_unit(total, ctas, blockIdx.x);
-        Req r;
-        Start c = locate<kThreads, RU>(p, pre, per, per_head, u0, r);
-        c.left = (int)(first_unit(total, ctas, blockIdx.x + 1) - u0);
-        *reinterpret_cast<Start *>(smem + L::OFF_START) = c;
+        Start c;
+        if (locate<RU>(p, pre, per, per_head, u0, mine, c)) {
+            c.left = (int)(first_unit(total, ctas, blockIdx.x + 1) - u0);
+            *reinterpret_cast<Start *>(smem + L::OFF_START) = c;
+        }
     }
     constexpr uint32_t kCols = KEYS ? kKeyTmemCols : kTmemCols;
     if (warp == W::MMA) rx::tmem_alloc(sbase + L::OFF_TMEM, kCols);
@@ -1636,8 +1639,12 @@ int launch(const TParams &p, cudaStream_t st)
 {
     static const bool ok = registers_ok<D, F8, NT, RU, KEYS>();
     if (!ok) return rx_set_error(RX_ERR_UNSUPPORTED, "tree attention: the kernel was built with too few registers");
-    // per device; cheap, and right whichever device is current
-    RX_CUDA_CHECK(cudaFuncSetAttribute(tree_kernel<D, F8, NT, RU, KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (TL<D, F8, KEYS>::BYTES)));
+    // per device, whichever is current
+    static thread_local int set_on = -1;
+    int dev = 0;
+    RX_CUDA_CHECK(cudaGetDevice(&dev));
+    if (dev != set_on) RX_CUDA_CHECK(cudaFuncSetAttribute(tree_kernel<D, F8, NT, RU, KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (TL<D, F8, KEYS>::BYTES)));
+    set_on = dev;
     tree_kernel<D, F8, NT, RU, KEYS><<<kCtas, Ro<NT>::THREADS, (TL<D, F8, KEYS>::BYTES), st>>>(p);
     RX_CUDA_CHECK(cudaGetLastError());
     // a programmatic dependent: it is launched meanwhile and waits on the device
