@@ -1242,14 +1242,20 @@ namespace {
 // a scale per pool.
 using ExtendPool = RxAttnPool;
 
-// A call with rules whose query rows make fewer CTAs than this (of 256 rows
-// each) shares the contexts among CTAs instead (rx_tree.cu).
-constexpr int kSplitBelow = 152;
-
-bool few_rows(int32_t hq, int32_t hkv, int32_t batch, int32_t max_len)
+// A call with rules that shares the contexts among CTAs (rx_rules.cu) instead of
+// copying them first: one with few query rows a kv head and request, for which
+// every position is read once or twice either way, or one that would leave SMs
+// without a CTA.  Measured, time shared / time copied, bf16: up to 512 rows 0.16 to
+// 0.87 (one case 1.02); 1,024 and 2,048 rows 0.40 to 1.09 with 32 or 64 CTAs, 0.77
+// to 1.28 with 128, 0.9 to 1.7 with more; 4,096 rows and more 1.1 to 2.6.  E4M3,
+// of which every row tile of 128 gathers and widens the positions for itself: up to
+// 128 rows 0.19 to 1.21 (most below 0.9); 256 and 512 rows 0.35 to 1.16 with up to
+// 32 CTAs, 1.2 to 1.9 with more; more rows 0.85 to 3.2.
+bool few_rows(int32_t hq, int32_t hkv, int32_t batch, int32_t max_len, bool f8)
 {
-    const int64_t rows = (int64_t)max_len * (hq / hkv);
-    return max_len <= RX_SPLIT_MAX_LEN && (rows + kCtaRows - 1) / kCtaRows * hkv * batch < kSplitBelow;
+    const int64_t rows = (int64_t)max_len * (hq / hkv), ctas = (rows + kCtaRows - 1) / kCtaRows * hkv * batch;
+    if (max_len > RX_SPLIT_MAX_LEN) return false;
+    return f8 ? rows <= 128 || (rows <= 512 && ctas <= 32) : rows <= 512 || ctas < 96;
 }
 
 // rx_attn_extend and rx_attn_extend_fp8 after their pool checks (`who`
@@ -1281,7 +1287,7 @@ int extend_call(const char *who, const ExtendPool &pool, const void *q, void *o,
         if (!workspace) return rx_set_error(RX_ERR_CAPACITY, "%s: no workspace", who);
     }
     if (batch == 0 || max_extend_len == 0) return RX_OK;
-    if (rules && few_rows(hq, pool.hkv, batch, max_extend_len))
+    if (rules && few_rows(hq, pool.hkv, batch, max_extend_len, pool.f8))
         return rx_split_rules(who, pool, q, o, lse, hq, qo_indptr, req_idx, prefix_len, extend_len, rtt, rtt_stride, batch,
                               max_extend_len, workspace, ws_bytes, sm_scale, rules, dev_status, stream);
     if (batch > 65535 || pool.hkv > 65535)

@@ -10,9 +10,10 @@
 //     log2(e) cap tanh(s / cap) = c2 - 2 c2 / (1 + E),   c2 = cap log2(e),
 // an exponential and a reciprocal of the special-function units a score (E of 0
 // or infinity gives -c2 and c2), or, where every score of a warp's tile is within
-// the cap, a polynomial of degree 11 on the multiply-add units, within half the
-// cap one of degree 7 (long chat extend, a cap of 50: CAPTIMES).  Its absolute error is c2 times a few 2^-23: for
-// a cap of 50 under 3e-5 log2 units, a weight's relative error under 2^-15,
+// the cap, a polynomial of degree 13 on the multiply-add units, within 3/8 of the
+// cap one of degree 7: the special-function units are what a tile waits for
+// otherwise.  Its absolute error is c2 times a few 2^-23 (2^-25 and 2^-26):
+// for a cap of 50 under 3e-5 log2 units, a weight's relative error under 2^-15,
 // where the weights are rounded to bf16 (2^-9) for the product with V.
 // (tanh.approx is off by 2^-11 of its value: 0.03 log2 units at that cap.)
 //
@@ -36,11 +37,11 @@ struct Rules {
     float to_e;             // 2 / cap: E = 2^(s sl2 to_e)
     float base;             // the weights' base, where it is fixed
     int fixed;              // the base is fixed
-    float poly[6];          // c2 tanh y = y (poly[0] + poly[1] y^2 + ...), |y| <= 1
+    float poly[7];          // c2 tanh y = y (poly[0] + poly[1] y^2 + ...), |y| <= 1
     float to_y;             // y = s / cap from log2 units
-    // in units of the products x = q . k, |x| <= half the cap (0: out of fp32's
-    // range): c2 tanh = x (near[0] + near[1] x^2 + near[2] x^4 + near[3] x^6)
-    float half_cap;
+    // in units of the products x = q . k, for |x| up to near_to, 3/8 of the cap (0:
+    // out of fp32's range): c2 tanh = x (near[0] + near[1] x^2 + ... + near[3] x^6)
+    float near_to;
     float near[4];
     int window;             // a token sees positions above p - window; INT_MAX: all
     const float *slope;     // [q heads] or null
@@ -91,7 +92,7 @@ __device__ __forceinline__ float apply_rules(uint32_t (&sv)[N], const Rules &r, 
             a1 = fmax3(a1, fabsf(__uint_as_float(sv[4 * k + 2])), fabsf(__uint_as_float(sv[4 * k + 3])));
         }
         const float most = fmaxf(a0, a1);
-        if (SAME && __all_sync(0xffffffffu, most <= r.half_cap)) {
+        if (SAME && __all_sync(0xffffffffu, most <= r.near_to)) {
             uint64_t c[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) c[i] = f2(r.near[i], r.near[i]);
@@ -108,16 +109,16 @@ __device__ __forceinline__ float apply_rules(uint32_t (&sv)[N], const Rules &r, 
                 sv[2 * k + 1] = __float_as_uint(b);
             }
         } else if (__all_sync(0xffffffffu, most * ky <= 1.f)) {
-            uint64_t c[6];
+            uint64_t c[7];
 #pragma unroll
-            for (int i = 0; i < 6; ++i) c[i] = f2(r.poly[i], r.poly[i]);
+            for (int i = 0; i < 7; ++i) c[i] = f2(r.poly[i], r.poly[i]);
             const uint64_t base2 = f2(-r.base, -r.base), ky2 = f2(ky, ky);
 #pragma unroll
             for (int k = 0; k < N / 2; ++k) {
                 const uint64_t y = f2_mul(f2(__uint_as_float(sv[2 * k]), __uint_as_float(sv[2 * k + 1])), ky2), z = f2_mul(y, y);
-                uint64_t x = f2_fma(c[5], z, c[4]);
+                uint64_t x = f2_fma(c[6], z, c[5]);
 #pragma unroll
-                for (int i = 3; i >= 0; --i) x = f2_fma(x, z, c[i]);
+                for (int i = 4; i >= 0; --i) x = f2_fma(x, z, c[i]);
                 float a, b;
                 f2_split(f2_fma(x, y, base2), a, b);
                 sv[2 * k] = __float_as_uint(a);
@@ -181,18 +182,19 @@ inline int make_rules(const char *who, const rx_attn_rules *in, float scale_log2
         const float ke = scale_log2 * r.to_e;
         if (!(in->cap >= 1e-3f && in->cap <= 1e6f) || !(ke >= 0x1p-126f && ke < INFINITY))
             return rx_set_error(RX_ERR_UNSUPPORTED, "%s: cap %g (from 1e-3 to 1e6)", who, in->cap);
-        // tanh y = y P(y^2) for |y| <= 1, off by at most 2.4e-7 (least maximum, found by reweighted least squares)
-        static const float P[6] = {0.999996854f, -0.333240038f, 0.132535251f, -0.0509728597f, 0.0161141767f, -0.00283946378f};
-        for (int i = 0; i < 6; ++i) r.poly[i] = P[i] * r.c2;
+        // tanh y = y P(y^2) for |y| <= 1, off by at most 2.0e-8 (least maximum, found by reweighted least squares;
+        // degree 11, off by 2.4e-7, left a log-sum-exp off by 1e-6 of itself)
+        static const float P[7] = {0.999999693f, -0.333321293f, 0.133195837f, -0.0532658349f, 0.0199732818f, -0.00595127971f, 0.000963771925f};
+        for (int i = 0; i < 7; ++i) r.poly[i] = P[i] * r.c2;
         r.to_y = 1.f / r.c2;
-        // the same for |y| <= 1/2, off by at most 1.3e-7
-        static const double Q[4] = {0.999997676, -0.333206552, 0.131451454, -0.0433724766};
+        // the same for |y| <= 3/8, off by at most 9.6e-9
+        static const double Q[4] = {0.99999974, -0.333308399, 0.132683921, -0.0476184644};
         const double k1 = (double)scale_log2 / r.c2;
         double c = (double)r.c2 * k1;
-        r.half_cap = (float)fmin(0.5 / k1, 1e18);
+        r.near_to = (float)fmin(0.375 / k1, 1e18);
         for (int i = 0; i < 4; ++i, c *= k1 * k1) {
             r.near[i] = (float)(Q[i] * c);
-            if (!(fabs(Q[i] * c) > 1e-36 && fabs(Q[i] * c) < 1e18)) r.half_cap = 0.f;
+            if (!(fabs(Q[i] * c) > 2e-38 && fabs(Q[i] * c) < 1e18)) r.near_to = 0.f;
         }
         if (r.c2 <= 72.2f && !in->slope) {
             r.fixed = 1;
