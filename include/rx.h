@@ -697,9 +697,10 @@ size_t rx_attn_tree_workspace(int32_t batch, int32_t num_q_heads, int32_t num_kv
  *
  * Scores, sums and the output's accumulator are fp32; the weights are rounded to
  * bf16 for the product with V (off by at most 2^-8 sum p |V|) and o once more,
- * as in rx_attn_extend and rx_attn_tree.  The cap's tanh comes from the
- * hardware's exponential and reciprocal: off by a few 2^-23 cap.  With a cap of
- * up to 50 and no slopes, V values above 2^57 may overflow o.
+ * as in rx_attn_extend and rx_attn_tree.  A capped score is off by at most 2^-21
+ * of itself and 2^-25 of the cap, next to scores beyond the cap by a few 2^-23 of
+ * the cap.  With a cap of up to 50 and no slopes, V values above 2^57 may overflow
+ * o.
  *
  * What a token does not see takes no part in its result, whatever K and V hold
  * there (NaN and infinities among it).  Positions that no token of a request

@@ -606,9 +606,10 @@ __device__ void softmax_rows(const XParams &p, const Tile &T, unsigned char *sme
 // each half's scores.
 //
 // The warps of a pair meet in a hardware barrier, which has no limit of its own.
-// Its limit is that of the waits before it: a warp whose wait gave up has raised
-// the abort flag, arrives once more (leave) and returns, and the other looks at the flag
-// behind every barrier and returns.
+// Its limit is that of the waits before it: the abort flag is looked at behind
+// every barrier too, and whoever returns early, for whichever reason, arrives once
+// more (leave).  So the other is released from the next barrier, if it still goes
+// there, and finds the flag behind it.
 template <int D, int KIND>
 __device__ void softmax_halves(const XParams &p, const Tile &T, unsigned char *smem, uint32_t sbase, uint32_t tmem)
 {
@@ -659,7 +660,7 @@ __device__ void softmax_halves(const XParams &p, const Tile &T, unsigned char *s
         w[half * kRows] = x;
         rx::named_bar_sync(pair, 64);
         other = w[(half ^ 1) * kRows];
-        return *abort_flag == 0;
+        return __all_sync(0xffffffffu, *abort_flag == 0);
     };
     float m_used = KIND == rx::kFixedCap ? p.rules.base : -INFINITY, l = 0.f;
     for (int j = 0; j < T.ntiles; ++j) {
@@ -673,7 +674,7 @@ __device__ void softmax_halves(const XParams &p, const Tile &T, unsigned char *s
 #pragma unroll
         for (int c = 0; c < HK / 32; ++c) rx::tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * c));
         rx::tmem_wait_ld();
-        const float left = rx::apply_rules<KIND, true>(sv, p.rules, sl2, slope, row_pos - kbase);
+        const float left = rx::apply_rules<KIND, true>(sv, p.rules, sl2, slope, row_pos - kbase, row < T.M);
         if (need_mask) rx::hide(sv, kbase, lo, hi);
         bool need = false;
         float alpha = 1.f;
@@ -685,7 +686,7 @@ __device__ void softmax_halves(const XParams &p, const Tile &T, unsigned char *s
                 a1 = rx::fmax3(a1, u2f(sv[4 * k + 2]), u2f(sv[4 * k + 3]));
             }
             float mx = fmaxf(a0, a1), other;
-            if (!swap(mx, j, other)) return;
+            if (!swap(mx, j, other)) return leave();
             const float m_new = fmaxf(m_used, fmaxf(mx, other) * left);
             need = (m_used == -INFINITY) || (m_new > m_used + kRescale);
             if (need) {
@@ -734,7 +735,7 @@ __device__ void softmax_halves(const XParams &p, const Tile &T, unsigned char *s
     }
     const int jl = T.ntiles - 1;
     float other;
-    if (!swap(l, T.ntiles, other)) return;
+    if (!swap(l, T.ntiles, other)) return leave();
     // the same order in both threads: one result
     l = half == 0 ? l + other : other + l;
     if (!warp_wait(bar + 8 * (L::B_PVDONE + t), jl & 1, abort_flag, p.status)) return;
@@ -1220,11 +1221,14 @@ template <int D, bool kStaged, bool F8 = false, int RU = rx::kNoRules>
 int launch_extend(const XParams &p, dim3 grid, cudaStream_t st)
 {
     constexpr int kBytes = RU >= rx::kFixedCap ? XL<D>::RULES_BYTES : XL<D>::BYTES;
-    static bool configured = false;
-    if (!configured) {
+    // per device, whichever is current
+    static thread_local int set_on = -1;
+    int dev = 0;
+    RX_CUDA_CHECK(cudaGetDevice(&dev));
+    if (dev != set_on) {
         RX_CUDA_CHECK(cudaFuncSetAttribute(extend_kernel<D, kStaged, F8, RU>,
                                            cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes));
-        configured = true;
+        set_on = dev;
     }
     // staged: a programmatic dependent of the staging copy
     if (kStaged)

@@ -1,5 +1,5 @@
 // rx_pipe.cuh -- bounded waits and the swizzled tile layout shared by the
-// tensor-core attention kernels (rx_extend.cu, rx_tree.cu).
+// tensor-core attention kernels (rx_extend.cu, rx_tree.cuh).
 #pragma once
 
 #include "rx_common.cuh"

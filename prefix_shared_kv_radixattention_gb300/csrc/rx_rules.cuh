@@ -1,5 +1,5 @@
 // rx_rules.cuh -- rules on attention scores, shared by the kernels that apply
-// them (rx_extend.cu, rx_tree.cu): a tanh cap, a bias that falls with the
+// them (rx_extend.cu, rx_tree.cuh): a tanh cap, a bias that falls with the
 // distance, and the positions a query token sees.
 //
 // A score s = sm_scale q . k of the query token at position p and the key at
@@ -12,9 +12,10 @@
 // or infinity gives -c2 and c2), or, where every score of a warp's tile is within
 // the cap, a polynomial of degree 13 on the multiply-add units, within 3/8 of the
 // cap one of degree 7: the special-function units are what a tile waits for
-// otherwise.  Its absolute error is c2 times a few 2^-23 (2^-25 and 2^-26):
-// for a cap of 50 under 3e-5 log2 units, a weight's relative error under 2^-15,
-// where the weights are rounded to bf16 (2^-9) for the product with V.
+// otherwise.  The first way is off by c2 times a few 2^-23 (a cap of 50: under 3e-5
+// log2 units, a weight's relative error under 2^-15, where the weights are rounded
+// to bf16 for the product with V), the polynomials by 2^-25 and 2^-26 of c2 and
+// never more than 2^-21 of the score, so that a large cap costs nothing.
 // (tanh.approx is off by 2^-11 of its value: 0.03 log2 units at that cap.)
 //
 // A cap bounds the scores, so the softmax needs no running maximum: with
@@ -78,9 +79,10 @@ inline int rules_kind(const Rules &r) { return r.fixed ? kFixedCap : r.c2 > 0.f 
 // log2 units (times sl2) with the cap and the bias, less the fixed base where
 // there is one.  dist = p - kbase; slope in log2 units a position.  Scores that
 // have neither cap nor bias stay as they are; the result is what the scores are
-// still to be multiplied with.  SAME: sl2 is the call's, not the row's own.
+// still to be multiplied with.  SAME: sl2 is the call's, not the row's own; valid:
+// the row is one (others hold anything).
 template <int KIND, bool SAME, int N>
-__device__ __forceinline__ float apply_rules(uint32_t (&sv)[N], const Rules &r, float sl2, float slope, int dist)
+__device__ __forceinline__ float apply_rules(uint32_t (&sv)[N], const Rules &r, float sl2, float slope, int dist, bool valid)
 {
     if constexpr (KIND == kRange) return sl2;
     if (KIND == kFixedCap || r.c2 > 0.f) {
@@ -91,7 +93,7 @@ __device__ __forceinline__ float apply_rules(uint32_t (&sv)[N], const Rules &r, 
             a0 = fmax3(a0, fabsf(__uint_as_float(sv[4 * k])), fabsf(__uint_as_float(sv[4 * k + 1])));
             a1 = fmax3(a1, fabsf(__uint_as_float(sv[4 * k + 2])), fabsf(__uint_as_float(sv[4 * k + 3])));
         }
-        const float most = fmaxf(a0, a1);
+        const float most = valid ? fmaxf(a0, a1) : 0.f;
         if (SAME && __all_sync(0xffffffffu, most <= r.near_to)) {
             uint64_t c[4];
 #pragma unroll

@@ -1,5 +1,5 @@
 // rx_split.h -- attention with rules on the scores by the kernels that share a
-// context among CTAs (rx_tree.cu), for rx_attn_decode_rules and, where a call
+// context among CTAs (rx_rules.cu), for rx_attn_decode_rules and, where a call
 // has few query rows, rx_attn_extend_rules.
 #pragma once
 

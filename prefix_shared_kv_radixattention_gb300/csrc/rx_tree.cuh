@@ -1103,7 +1103,7 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
                         const bool all = __all_sync(0xffffffffu, !valid || (kbase >= lo && kbase + kBN <= hi));
                         rx::tmem_wait_ld();
                         release_s();
-                        left = rx::apply_rules<RU, !F8>(sv, p.rules, a.sl2, slope, at - kbase);
+                        left = rx::apply_rules<RU, !F8>(sv, p.rules, a.sl2, slope, at - kbase, valid);
                         if (!all) rx::hide(sv, kbase, lo, hi);
                     } else if (kbase + kBN > g.P) {   // drafted positions, or past the last
                         const int off = kbase - g.P, w0 = off >> 5;
@@ -1281,19 +1281,15 @@ __device__ void keys_softmax(const TParams &p, unsigned char *smem, uint32_t sba
     int turns = 0;
     auto team_words = [&]() { return words + (turns & 1) * kTeam; };
     // The warps meet in a hardware barrier, which has no limit of its own.  Its
-    // limit is that of the waits before it: a warp whose wait gave up has raised
-    // the abort flag, arrives once more (leave) and returns, and the others look
-    // at the flag behind every barrier and return.
+    // limit is that of the waits before it: the abort flag is looked at behind every
+    // barrier too, and whoever returns early, for whichever reason, arrives once
+    // more (leave).  So the others are released from the next barrier, if they still
+    // go there, and find the flag behind it.
     auto leave = [&]() { asm volatile("bar.arrive 1, %0;\n" ::"n"(kRows) : "memory"); };
-    auto team_or = [&](bool x, bool &any) {
-        any = rx::named_bar_or(1, kRows, x);
-        ++turns;
-        return *abort_flag == 0;
-    };
     auto team = [&]() {
         rx::named_bar_sync(1, kRows);
         ++turns;
-        return *abort_flag == 0;
+        return __all_sync(0xffffffffu, *abort_flag == 0);
     };
     const bool fixed = p.rules.fixed;
     // this thread's place in a row of P: row n's chunks are swizzled by n
@@ -1325,27 +1321,52 @@ __device__ void keys_softmax(const TParams &p, unsigned char *smem, uint32_t sba
             const int pos = g.template tile<rx::kAnyRules>(j) * kBN + key;
             const bool seen = pos >= lo && pos < hi;
             const float far = (float)(hi - 1 - pos);
-            float x[kKeyRows];
+            float x[kKeyRows];  // in log2 units
+            float most = 0.f;
+#pragma unroll
+            for (int n = 0; n < kKeyRows; ++n) {
+                if (n >= G) break;
+                x[n] = u2f(sv[n]) * (F8 ? qs[n] : p.scale_log2);
+                most = fmaxf(most, seen ? fabsf(x[n]) : 0.f);
+            }
+            if (p.rules.c2 > 0.f) {  // as in apply_rules
+                if (__all_sync(0xffffffffu, most <= p.rules.c2)) {
+#pragma unroll
+                    for (int n = 0; n < kKeyRows; ++n) {
+                        if (n >= G) break;
+                        const float y = x[n] * p.rules.to_y, z = y * y;
+                        float v = fmaf(p.rules.poly[6], z, p.rules.poly[5]);
+#pragma unroll
+                        for (int i = 4; i >= 0; --i) v = fmaf(v, z, p.rules.poly[i]);
+                        x[n] = fmaf(v, y, -p.rules.base);
+                    }
+                } else {
+#pragma unroll
+                    for (int n = 0; n < kKeyRows; ++n) {
+                        if (n >= G) break;
+                        const float e = rx::fast_exp2(x[n] * p.rules.to_e);
+                        x[n] = fmaf(rx::fast_rcp(e + 1.f), -2.f * p.rules.c2, p.rules.c2 - p.rules.base);
+                    }
+                }
+            }
             bool above = false;
 #pragma unroll
             for (int n = 0; n < kKeyRows; ++n) {
                 if (n >= G) break;
-                const float sl2 = F8 ? qs[n] : p.scale_log2, q = u2f(sv[n]);
-                float y;
-                if (p.rules.c2 > 0.f) {
-                    const float e = rx::fast_exp2(q * fminf(sl2 * p.rules.to_e, 0x1.fffffep127f));
-                    y = fmaf(rx::fast_rcp(e + 1.f), -2.f * p.rules.c2, p.rules.c2 - p.rules.base);
-                } else {
-                    y = q * sl2;
-                }
-                x[n] = seen ? fmaf(-slope[n], far, y) : -INFINITY;
+                x[n] = seen ? fmaf(-slope[n], far, x[n]) : -INFINITY;
                 above |= x[n] > m[n] + kRescale;
             }
             // the product two before has read these columns of P
             if (phase >= 1 && !warp_wait(bar + 8 * (L::B_PVDONE + b), (phase - 1) & 1, abort_flag, p.status)) return leave();
             rx::tc_fence_after();
             bool raise = false;
-            if (!fixed && !team_or(above, raise)) return;
+            if (!fixed) {
+                float *v = team_words();
+                above = __any_sync(0xffffffffu, above);
+                if (lane == 0) v[warp] = above ? 1.f : 0.f;
+                if (!team()) return leave();
+                raise = v[0] + v[1] + v[2] + v[3] > 0.f;
+            }
             if (raise) {
                 // new maxima: of each warp's positions, then of the four
                 float *red = team_words();
@@ -1359,7 +1380,7 @@ __device__ void keys_softmax(const TParams &p, unsigned char *smem, uint32_t sba
                     for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
                     if (lane == 0) red[warp * kKeyRows + n] = mx;
                 }
-                if (!team()) return;
+                if (!team()) return leave();
 #pragma unroll
                 for (int n = 0; n < kKeyRows; ++n) {
                     alpha[n] = 1.f;
@@ -1407,7 +1428,7 @@ __device__ void keys_softmax(const TParams &p, unsigned char *smem, uint32_t sba
             for (int d = 16; d > 0; d >>= 1) l[n] += __shfl_xor_sync(0xffffffffu, l[n], d);
             if (lane == 0) red[warp * kKeyRows + n] = l[n];
         }
-        if (!team()) return;
+        if (!team()) return leave();
         float tot[kKeyRows];
 #pragma unroll
         for (int n = 0; n < kKeyRows; ++n)

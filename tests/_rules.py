@@ -61,17 +61,19 @@ class RulesBatch:
                              self.window, self.slopes, self.see_from, self.see_to)
 
 
-def check(o, lse, r, b, what=""):
+def check(o, lse, r, b, what="", cap=None):
     """Bounds of the attention with rules.  o: the softmax weights are rounded to
     bf16 before P V (2^-8 of sum p |v|) and the result once more (2^-8 of |o|).
     The scores are fp32 sums of d exact products, off by at most d 2^-24 sum |q
     k| scale; with spread s of the queries that sum is under 0.8 s sqrt(d) times
     1.5: under 3e-4 s for d up to 128.  A cap adds under 4 2^-23 cap log2(e) log2
     units: 1e-6 cap; a bias is rounded to 2^-24 of scores that count, under 64:
-    1e-5.  Each moves every weight by at most that, twice with the sum."""
+    1e-5.  Each moves every weight by at most that, twice with the sum.  cap: where
+    every score is far within the cap its share is 2^-21 of a score, under 64 (and
+    2^-25 of the cap): less than 1e-6 of 30 whatever the cap."""
     ro, rl, ra = r
     s = max(1.0, float(np.abs(b.q).max()) / 4.0)
-    off = 2 * (3e-4 * s + 1e-6 * b.cap + 1e-5)
+    off = 2 * (3e-4 * s + 1e-6 * (b.cap if cap is None else cap) + 1e-5)
     bound = HALF_STEP * np.abs(ro) + (HALF_STEP * (1 + HALF_STEP) + off) * ra + 1e-30
     err = np.abs(np.asarray(o, np.float64) - ro)
     assert not np.isnan(o).any(), f"{what}: NaN"

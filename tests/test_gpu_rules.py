@@ -159,6 +159,29 @@ def test_decode_over_many_ctas(f8):
     Run(b, f8).check("decode")
 
 
+@pytest.mark.parametrize("path", ["split", "staged", "decode"])
+@pytest.mark.parametrize("rules", [dict(cap=2.0, spread=12.0), dict(cap=50.0, spread=40.0), dict(cap=80.0, spread=60.0),
+                                   dict(cap=1e-3)], ids=str)
+def test_scores_far_beyond_the_cap(rules, path):
+    """Scores of every size against the cap: within it, around it, many times it."""
+    new = [1, 1, 1] if path == "decode" else [40, 70, 3]
+    for heads, f8 in ((HEADS[0], False), (HEADS[1], False), (HEADS[1], True)):
+        b = RulesBatch(27, *heads, [100, 3, 260], new, **rules)
+        b.q[::2] *= np.float32(0.02)                                   # rows with small scores next to rows with large ones
+        Run(b, f8).check("decode" if path == "decode" else "extend", STAGED if path == "staged" else None)
+
+
+@pytest.mark.parametrize("path", ["split", "staged", "decode"])
+@pytest.mark.parametrize("cap", [1e3, 1e6])
+def test_large_caps_cost_nothing(cap, path):
+    new = [1, 1] if path == "decode" else [40, 7]
+    for heads, f8 in ((HEADS[0], False), (HEADS[1], False), (HEADS[1], True)):
+        b = RulesBatch(28, *heads, [100, 260], new, cap=cap)
+        run = Run(b, f8)
+        o, lse = run("decode" if path == "decode" else "extend", STAGED if path == "staged" else None)
+        _rules.check(o, lse, b.oracle(run.q64, run.k64, run.v64), b, cap=30.0)
+
+
 def test_without_lse():
     b = RulesBatch(17, 8, 2, 64, [100], [9], cap=50.0)
     Run(b).check(with_lse=False)
@@ -173,13 +196,14 @@ def test_layers(path):
         Run(b, f8, layers=3, layer=2).check(max_len=STAGED if path == "staged" else None)
 
 
+@pytest.mark.parametrize("heads", [(4, 2, 64), (8, 2, 128)], ids=str)
 @pytest.mark.parametrize("f8", [False, True], ids=["bf16", "fp8"])
 @pytest.mark.parametrize("path", ["split", "staged", "decode"])
 @pytest.mark.parametrize("rules", [dict(window=70), dict(mask="docs"), dict(cap=50.0, window=70)], ids=str)
-def test_not_finite_where_a_token_does_not_see(rules, path, f8):
+def test_not_finite_where_a_token_does_not_see(rules, path, f8, heads):
     """NaN and infinities of K and V reach the tokens that see their position, and no other."""
     new = [1, 1] if path == "decode" else [60, 12]
-    b = RulesBatch(19, 4, 2, 64, [300, 90], new, **{**rules, **({"mask": ""} if path == "decode" else {})})
+    b = RulesBatch(19, *heads, [300, 90], new, **{**rules, **({"mask": ""} if path == "decode" else {})})
     if path == "decode" and "mask" in rules:
         b.see_from = np.array([280, 40], np.int32)
     at = [(0, 231), (0, 240), (0, 20), (0, 299), (0, 300 + new[0] - 1), (1, 30)]   # (request, position)
@@ -208,7 +232,7 @@ def test_not_finite_where_a_token_does_not_see(rules, path, f8):
                 assert np.isnan(o[row]).all() and np.isnan(lse[row]).all()
                 o[row], lse[row] = ref_o[row], ref_l[row]
                 hit = set()
-            for h in (2, 3):                            # the heads of kv head 1
+            for h in range(heads[0] // 2, heads[0]):    # the heads of kv head 1
                 got = o[row, h, 5]
                 if hit:
                     want_nan = any(np.isnan(x) for x in hit) or len(hit) > 1
