@@ -17,7 +17,10 @@ int go(const TParams &p, const TreePool &pool, cudaStream_t st)
     // It takes 16 rows, and a head_dim that fills the tensor core's 128 lanes.
     // (Long chat, a cap of 50: 258 us, with the rows as the wide side 403; few-shot
     // with slopes 174, 406.)
-    if (!p.qo_indptr && p.G <= kKeyRows && pool.D == kRows)
+    // It takes the cap from the exponential and the reciprocal alone (the
+    // polynomials beside them: windowed E4M3 208 us, without 170), whose error grows
+    // with the cap: up to 150 a log-sum-exp is off by less than 1e-6 of itself.
+    if (!p.qo_indptr && p.G <= kKeyRows && pool.D == kRows && p.rules.c2 <= 150.f * rx::kLog2e)
         return pool.f8 ? launch<kRows, true, rx::kAnyRules, 1, true>(p, st) : launch<kRows, false, rx::kAnyRules, 1, true>(p, st);
     switch (rx::rules_kind(p.rules)) {
     case rx::kFixedCap: return go_kind<rx::kFixedCap>(p, pool, st);

@@ -1274,22 +1274,26 @@ __device__ void keys_softmax(const TParams &p, unsigned char *smem, uint32_t sba
     const int key = threadIdx.x, lane = key & 31, warp = key >> 5;   // = TMEM lane: position of the tile, column of V
     const uint32_t lanes = (uint32_t)(key & ~31) << 16;
     const int G = p.G;
-    // what the four warps tell one another, in turns of two buffers: a warp writes
-    // a turn's words again two barriers later, when all have read them
-    constexpr int kTeam = 4 * kKeyRows;
+    // What the four warps tell one another, in turns of two buffers: a warp writes
+    // a turn's words again two barriers later, when all have read them.  The
+    // barriers have no limit of their own, so no warp leaves alone: one whose wait
+    // gave up (its limit is that of the waits) goes on to where the words are
+    // exchanged, and all four return there together.
+    constexpr int kTeam = 4 * kKeyRows + 4;
     float *words = reinterpret_cast<float *>(smem + L::OFF_MASK);    // no masks here
     int turns = 0;
+    bool dead = false;
     auto team_words = [&]() { return words + (turns & 1) * kTeam; };
-    // The warps meet in a hardware barrier, which has no limit of its own.  Its
-    // limit is that of the waits before it: the abort flag is looked at behind every
-    // barrier too, and whoever returns early, for whichever reason, arrives once
-    // more (leave).  So the others are released from the next barrier, if they still
-    // go there, and find the flag behind it.
-    auto leave = [&]() { asm volatile("bar.arrive 1, %0;\n" ::"n"(kRows) : "memory"); };
-    auto team = [&]() {
-        rx::named_bar_sync(1, kRows);
+    auto exchange = [&]() -> bool {  // false: some warp's wait gave up
+        float *w = team_words() + 4 * kKeyRows;
+        if (lane == 0) w[warp] = dead ? 1.f : 0.f;
+        rx::named_bar_sync(2, kRows);
         ++turns;
-        return __all_sync(0xffffffffu, *abort_flag == 0);
+        return w[0] + w[1] + w[2] + w[3] == 0.f;
+    };
+    auto wait = [&](int b, uint32_t parity) {
+        if (!warp_wait(bar + 8 * b, parity, abort_flag, p.status)) dead = true;
+        rx::tc_fence_after();
     };
     const bool fixed = p.rules.fixed;
     // this thread's place in a row of P: row n's chunks are swizzled by n
@@ -1298,7 +1302,12 @@ __device__ void keys_softmax(const TParams &p, unsigned char *smem, uint32_t sba
     int c = 0;
     for (int s = 0;; ++s) {
         Seg g;
-        if (!__all_sync(0xffffffffu, get_seg<L, rx::kAnyRules>(s, g, smem, sbase, p.status))) return leave();
+        if (!__all_sync(0xffffffffu, get_seg<L, rx::kAnyRules>(s, g, smem, sbase, p.status))) {
+            dead = true;  // the others' next exchange: a raise, or with a fixed base their segment's end
+            if (!fixed) rx::named_bar_or(1, kRows, true);
+            exchange();
+            return;
+        }
         same_in_all_lanes(g);
         const int lo = g.lo_min, hi = g.P + 1;
         float m[kKeyRows], l[kKeyRows], slope[kKeyRows];
@@ -1311,8 +1320,7 @@ __device__ void keys_softmax(const TParams &p, unsigned char *smem, uint32_t sba
         const float *qs = reinterpret_cast<const float *>(smem + L::OFF_QS) + (s % kRing) * kRows;
         for (int j = g.j0; j < g.j1; ++j, ++c) {
             const int b = c & 1, phase = c >> 1;
-            if (!warp_wait(bar + 8 * (L::B_SFULL + b), phase & 1, abort_flag, p.status)) return leave();
-            rx::tc_fence_after();
+            wait(L::B_SFULL + b, phase & 1);
             uint32_t sv[kKeyRows];
             rx::tmem_ld16(tmem + Kt::s(b) + lanes, sv);
             rx::tmem_wait_ld();
@@ -1321,53 +1329,25 @@ __device__ void keys_softmax(const TParams &p, unsigned char *smem, uint32_t sba
             const int pos = g.template tile<rx::kAnyRules>(j) * kBN + key;
             const bool seen = pos >= lo && pos < hi;
             const float far = (float)(hi - 1 - pos);
-            float x[kKeyRows];  // in log2 units
-            float most = 0.f;
-#pragma unroll
-            for (int n = 0; n < kKeyRows; ++n) {
-                if (n >= G) break;
-                x[n] = u2f(sv[n]) * (F8 ? qs[n] : p.scale_log2);
-                most = fmaxf(most, seen ? fabsf(x[n]) : 0.f);
-            }
-            if (p.rules.c2 > 0.f) {  // as in apply_rules
-                if (__all_sync(0xffffffffu, most <= p.rules.c2)) {
-#pragma unroll
-                    for (int n = 0; n < kKeyRows; ++n) {
-                        if (n >= G) break;
-                        const float y = x[n] * p.rules.to_y, z = y * y;
-                        float v = fmaf(p.rules.poly[6], z, p.rules.poly[5]);
-#pragma unroll
-                        for (int i = 4; i >= 0; --i) v = fmaf(v, z, p.rules.poly[i]);
-                        x[n] = fmaf(v, y, -p.rules.base);
-                    }
-                } else {
-#pragma unroll
-                    for (int n = 0; n < kKeyRows; ++n) {
-                        if (n >= G) break;
-                        const float e = rx::fast_exp2(x[n] * p.rules.to_e);
-                        x[n] = fmaf(rx::fast_rcp(e + 1.f), -2.f * p.rules.c2, p.rules.c2 - p.rules.base);
-                    }
-                }
-            }
+            float x[kKeyRows];
             bool above = false;
 #pragma unroll
             for (int n = 0; n < kKeyRows; ++n) {
                 if (n >= G) break;
-                x[n] = seen ? fmaf(-slope[n], far, x[n]) : -INFINITY;
+                const float sl2 = F8 ? qs[n] : p.scale_log2, q = u2f(sv[n]);
+                float y;
+                if (p.rules.c2 > 0.f) {
+                    const float e = rx::fast_exp2(q * fminf(sl2 * p.rules.to_e, 0x1.fffffep127f));
+                    y = fmaf(rx::fast_rcp(e + 1.f), -2.f * p.rules.c2, p.rules.c2 - p.rules.base);
+                } else {
+                    y = q * sl2;
+                }
+                x[n] = seen ? fmaf(-slope[n], far, y) : -INFINITY;
                 above |= x[n] > m[n] + kRescale;
             }
             // the product two before has read these columns of P
-            if (phase >= 1 && !warp_wait(bar + 8 * (L::B_PVDONE + b), (phase - 1) & 1, abort_flag, p.status)) return leave();
-            rx::tc_fence_after();
-            bool raise = false;
-            if (!fixed) {
-                float *v = team_words();
-                above = __any_sync(0xffffffffu, above);
-                if (lane == 0) v[warp] = above ? 1.f : 0.f;
-                if (!team()) return leave();
-                raise = v[0] + v[1] + v[2] + v[3] > 0.f;
-            }
-            if (raise) {
+            if (phase >= 1) wait(L::B_PVDONE + b, (phase - 1) & 1);
+            if (!fixed && rx::named_bar_or(1, kRows, above || dead)) {
                 // new maxima: of each warp's positions, then of the four
                 float *red = team_words();
                 float alpha[kKeyRows];
@@ -1380,7 +1360,7 @@ __device__ void keys_softmax(const TParams &p, unsigned char *smem, uint32_t sba
                     for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
                     if (lane == 0) red[warp * kKeyRows + n] = mx;
                 }
-                if (!team()) return leave();
+                if (!exchange()) return;
 #pragma unroll
                 for (int n = 0; n < kKeyRows; ++n) {
                     alpha[n] = 1.f;
@@ -1396,8 +1376,7 @@ __device__ void keys_softmax(const TParams &p, unsigned char *smem, uint32_t sba
                     }
                 }
                 if (scale_o) {  // the same answer in all threads
-                    if (!warp_wait(bar + 8 * (L::B_PVDONE + ((c - 1) & 1)), ((c - 1) >> 1) & 1, abort_flag, p.status)) return leave();
-                    rx::tc_fence_after();
+                    wait(L::B_PVDONE + ((c - 1) & 1), ((c - 1) >> 1) & 1);
                     uint32_t o[kKeyRows];
                     rx::tmem_ld16(tmem + Kt::o() + lanes, o);
                     rx::tmem_wait_ld();
@@ -1428,13 +1407,12 @@ __device__ void keys_softmax(const TParams &p, unsigned char *smem, uint32_t sba
             for (int d = 16; d > 0; d >>= 1) l[n] += __shfl_xor_sync(0xffffffffu, l[n], d);
             if (lane == 0) red[warp * kKeyRows + n] = l[n];
         }
-        if (!team()) return leave();
+        if (!exchange()) return;
         float tot[kKeyRows];
 #pragma unroll
         for (int n = 0; n < kKeyRows; ++n)
             tot[n] = n < G ? red[n] + red[kKeyRows + n] + red[2 * kKeyRows + n] + red[3 * kKeyRows + n] : 0.f;
-        if (!warp_wait(bar + 8 * (L::B_PVDONE + ((c - 1) & 1)), ((c - 1) >> 1) & 1, abort_flag, p.status)) return leave();
-        rx::tc_fence_after();
+        wait(L::B_PVDONE + ((c - 1) & 1), ((c - 1) >> 1) & 1);
         uint32_t o[kKeyRows];
         rx::tmem_ld16(tmem + Kt::o() + lanes, o);
         rx::tmem_wait_ld();
