@@ -33,7 +33,11 @@
  *   - the verification step of drafted tokens: norm of each q and k head with
  *     the rotation and the scatter (rx_qk_norm_rope_store), attention of a
  *     tree of drafted tokens (rx_tree_mask_build, rx_attn_tree), and
- *     penalties, biases and grammar masks on the logits (rx_logits_process).
+ *     penalties, biases and grammar masks on the logits (rx_logits_process);
+ *   - an attention step of models that read images or cap, window or bias their
+ *     scores: the lists of a step (rx_step_maps), rotation with positions on
+ *     several axes and store (rx_qk_rope_axes_store), attention with rules on
+ *     the scores (rx_attn_extend_rules, rx_attn_decode_rules).
  *
  * Attention definition (all attention entry points).  For a query row of
  * request b at absolute position p, q-head h, with G = num_q_heads /
@@ -698,8 +702,8 @@ size_t rx_attn_tree_workspace(int32_t batch, int32_t num_q_heads, int32_t num_kv
  * Scores, sums and the output's accumulator are fp32; the weights are rounded to
  * bf16 for the product with V (off by at most 2^-8 sum p |V|) and o once more,
  * as in rx_attn_extend and rx_attn_tree.  A capped score is off by at most 2^-21
- * of itself and 2^-25 of the cap, next to scores beyond the cap by a few 2^-23 of
- * the cap.  With a cap of up to 50 and no slopes, V values above 2^57 may overflow
+ * of itself and 2^-25 of the cap; next to scores beyond the cap, and in
+ * rx_attn_decode_rules with caps up to 150, by a few 2^-23 of the cap.  With a cap of up to 50 and no slopes, V values above 2^57 may overflow
  * o.
  *
  * What a token does not see takes no part in its result, whatever K and V hold

@@ -26,6 +26,10 @@
 // thread in flight at four CTAs an SM; four rows and two CTAs take 115 and
 // 28 us, one row and four 117 and 23.  Rows that do not fill a CTA's passes
 // (two tokens of 80 rows on passes of 128) took 156 us.
+//
+// With positions on several axes (rx_qk_rope_axes_store) only the angles differ: a
+// pair's position comes from its axis.  16,384 tokens of 64/8 heads on three axes
+// and the norm take 110 us.
 #include <numeric>
 #include <type_traits>
 
