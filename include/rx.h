@@ -707,10 +707,10 @@ size_t rx_attn_tree_workspace(int32_t batch, int32_t num_q_heads, int32_t num_kv
  * o.
  *
  * What a token does not see takes no part in its result, whatever K and V hold
- * there (NaN and infinities among it).  Positions that no token of a request
- * sees may be read or not: their slot ids must be in the pool or are flagged if
- * they are read (a window's call skips whole tiles of 128 positions before it,
- * and rx_attn_decode_rules reads no position before its token's lo). */
+ * there (NaN and infinities among it).  Positions before the window of a request's
+ * first new token are not read, nor in rx_attn_decode_rules those before its
+ * token's lo: their slot ids may be anything.  Other positions that no token sees
+ * may be read or not, and a slot id outside the pool is flagged if it is. */
 typedef struct {
     float cap;                /* > 0 (1e-3 to 1e6): scores are capped; 0: they are not        */
     int32_t window;           /* > 0: positions a token sees, itself among them; 0: all of them */

@@ -383,8 +383,8 @@ __device__ void mma_issuer(const XParams &p, const Tile &T, unsigned char *smem,
         // those of the second 64 keys over their own scores)
 #pragma unroll
         for (int ks = 0; ks < kBN / 16; ++ks)
-            rx::tc_mma_ts(tmem + t * 256 + 128, tmem + t * 256 + ks * 8 + (kHalves && ks >= kBN / 32 ? kBN / 4 : 0), dvs + (uint64_t)((ks * 16 * 128) >> 4),
-                          idesc_pv, (j > 0 || ks > 0) ? 1u : 0u);
+            rx::tc_mma_ts(tmem + t * 256 + 128, tmem + t * 256 + ks * 8 + (kHalves && ks >= kBN / 32 ? kBN / 4 : 0),
+                          dvs + (uint64_t)((ks * 16 * 128) >> 4), idesc_pv, (j > 0 || ks > 0) ? 1u : 0u);
         rx::tc_commit(bar + 8 * (L::B_PVDONE + t));
         if (t == T.nqt - 1) rx::tc_commit(bar + 8 * (L::B_VEMPTY + st));
         return true;
@@ -600,15 +600,16 @@ __device__ void softmax_rows(const XParams &p, const Tile &T, unsigned char *sme
         }
     }
     if (valid && p.lse) p.lse[orow] = RANGE && l == 0.f ? -INFINITY : (m_used + log2f(l)) * rx::kLn2;
-    if (RANGE && valid && __ldg(p.stage_nf)) add_not_finite<D>(p, T.slots, T.g, T.share_tiles, T.share_row0, T.stage_row0, lo, hi, orow, 0, D);
+    if (RANGE && valid && __ldg(p.stage_nf))
+        add_not_finite<D>(p, T.slots, T.g, T.share_tiles, T.share_row0, T.stage_row0, lo, hi, orow, 0, D);
 }
 
 // With rules on the scores, 64 of a tile's 128 keys a thread: a row is shared by
 // two threads of two warps (16 softmax warps), since what bounds the kernel is how
 // long a tile's scores take on their way from S to P, and the cap makes that
-// longer (a cap of 50, one thread a row: 1,962 us, two 1,745).  A row's two halves agree on the maximum through shared memory, or,
-// with a fixed base, not at all until the end.  P_t lies over the first half of
-// each half's scores.
+// longer (a cap of 50, one thread a row: 1,962 us, two 1,745).  A row's two halves
+// agree on the maximum through shared memory, or, with a fixed base, not at all
+// until the end.  P_t lies over the first half of each half's scores.
 //
 // The warps of a pair meet in a hardware barrier, which has no limit of its own.
 // Its limit is that of the waits before it: the abort flag is looked at behind
@@ -765,7 +766,8 @@ __device__ void softmax_halves(const XParams &p, const Tile &T, unsigned char *s
         }
     }
     if (valid && half == 0 && p.lse) p.lse[orow] = l == 0.f ? -INFINITY : (m_used + log2f(l)) * rx::kLn2;
-    if (valid && __ldg(p.stage_nf)) add_not_finite<D>(p, T.slots, T.g, T.share_tiles, T.share_row0, T.stage_row0, lo, hi, orow, half * HD, HD);
+    if (valid && __ldg(p.stage_nf))
+        add_not_finite<D>(p, T.slots, T.g, T.share_tiles, T.share_row0, T.stage_row0, lo, hi, orow, half * HD, HD);
 }
 
 template <int D, bool kStaged, bool F8 = false, int RU = rx::kNoRules>
@@ -905,12 +907,10 @@ __global__ void __launch_bounds__(RU >= rx::kFixedCap ? kRulesThreads : kStaged 
 
 // Packed rows of request b: its context (prefix + extend tokens) rounded up
 // to whole kBN-row tiles; none for lengths the attention kernel rejects.
-// With a window (INT_MAX: none) a request's tiles count from the first one that
-// its first new token sees.
-__device__ __forceinline__ int window_tile(int64_t P, int window)
-{
-    return P >= window ? (int)((P - window + 1) / kBN) : 0;
-}
+// With a window (INT_MAX: none) a request's first new token sees positions from
+// window_start on; nothing before it is read, and its tiles count from that one's.
+__device__ __forceinline__ int window_start(int64_t P, int window) { return P >= window ? (int)(P - window + 1) : 0; }
+__device__ __forceinline__ int window_tile(int64_t P, int window) { return window_start(P, window) / kBN; }
 __device__ __forceinline__ int64_t staged_rows(const int32_t *prefix_len, const int32_t *extend_len, int b,
                                                int64_t rtt_stride)
 {
@@ -973,10 +973,10 @@ __global__ void __launch_bounds__(kBN) stage_share_kernel(const int32_t *__restr
         tiles = min(ntile, diff);
     }
     if (t == 0) {
-        // r has b's first tile, and they share tiles from there on
+        // r has all that b sees of its first tile, and they share tiles from there on
         if (tiles > 0) {
-            const int f = window_tile(__ldg(prefix_len + b), window);
-            if (window_tile(__ldg(prefix_len + r), window) > f || tiles <= f) tiles = 0;
+            const int from = window_start(__ldg(prefix_len + b), window);
+            if (window_start(__ldg(prefix_len + r), window) > from || tiles <= from / kBN) tiles = 0;
         }
         src[b] = tiles > 0 ? r : b;
         share[b] = tiles;
@@ -1080,7 +1080,7 @@ __global__ void __launch_bounds__(256) stage_rows_kernel(
         const int64_t ctx = (int64_t)__ldg(prefix_len + b) + __ldg(extend_len + b);
         const int64_t pos0 = row0 - offs[b] + (int64_t)(RU ? max(share[b], window_tile(__ldg(prefix_len + b), window)) : share[b]) * kBN;
         int32_t my_slot = -1;
-        if (lane < kStageBlock && pos0 + lane < ctx) {
+        if (lane < kStageBlock && pos0 + lane < ctx && (!RU || pos0 + lane >= window_start(__ldg(prefix_len + b), window))) {
             const int32_t sl = __ldg(rtt + (int64_t)__ldg(req_idx + b) * rtt_stride + pos0 + lane);
             if (sl >= 0 && (int64_t)sl < num_slots) my_slot = sl;
             else if (status) atomicOr(status, RX_DEV_BAD_SLOT);

@@ -73,6 +73,7 @@ using rx::wait_or_abort;
 using rx::warp_wait;
 
 constexpr int kMaxTree = 1024;
+static_assert(RX_SPLIT_MAX_LEN == kMaxTree, "new tokens of a request");
 constexpr int kCtas = 152;           // CTAs of a call: one an SM
 constexpr int kRows = 128;           // query rows of a row tile (MMA M)
 constexpr int kMaxNt = 2;            // row tiles that share a K/V tile

@@ -261,6 +261,25 @@ def test_bad_slots_and_lengths(path):
     assert np.isnan(o[:10]).all() and not np.isnan(o[10:]).any()       # left as they were
 
 
+@pytest.mark.parametrize("f8", [False, True], ids=["bf16", "fp8"])
+@pytest.mark.parametrize("path", ["split", "staged", "decode"])
+def test_slots_before_the_window_may_be_anything(path, f8):
+    new = [1, 1, 1] if path == "decode" else [60, 12, 30]
+    for heads in ((4, 2, 64), (8, 2, 128)):
+        b = RulesBatch(29, *heads, [300, 90, 260], new, window=70, cap=50.0, shared=280)
+        for r in range(3):
+            b.rtt[b.req_idx[r], :max(0, int(b.prefix_len[r]) - 69)] = (-1, b.num_slots, -(2 ** 31))[r]
+        Run(b, f8).check("decode" if path == "decode" else "extend", STAGED if path == "staged" else None)
+
+
+@pytest.mark.parametrize("window", [100, 130, 150, 200])
+def test_shared_tiles_with_windows_that_begin_apart(window):
+    """Requests that share their text, the windows' starts inside one tile and across tiles, in either order."""
+    for prefixes in ([400, 380, 390, 130], [380, 400, 130, 390]):
+        b = RulesBatch(30, 4, 2, 64, prefixes, [20, 33, 5, 9], window=window, shared=384)
+        Run(b).check(max_len=STAGED)
+
+
 def test_decode_leaves_out_requests_without_a_context():
     from prefix_shared_kv_radixattention_gb300 import binding as rx
     b = RulesBatch(22, 4, 2, 64, [99, 20, 30], [1, 1, 1], cap=50.0)
