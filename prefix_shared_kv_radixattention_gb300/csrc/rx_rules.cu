@@ -11,6 +11,12 @@ int go_kind(const TParams &p, const TreePool &pool, cudaStream_t st)
     return pool.D == 128 ? launch_of<RU, 128>(p, pool, st) : launch_of<RU, 64>(p, pool, st);
 }
 
+template <int GN>
+int go_keys(const TParams &p, const TreePool &pool, cudaStream_t st)
+{
+    return pool.f8 ? launch<kRows, true, rx::kAnyRules, 1, true, GN>(p, st) : launch<kRows, false, rx::kAnyRules, 1, true, GN>(p, st);
+}
+
 int go(const TParams &p, const TreePool &pool, cudaStream_t st)
 {
     // one token a request: the products with the positions as their wide side.
@@ -21,7 +27,7 @@ int go(const TParams &p, const TreePool &pool, cudaStream_t st)
     // polynomials beside them: windowed E4M3 208 us, without 170), whose error grows
     // with the cap: up to 150 a log-sum-exp is off by less than 1e-6 of itself.
     if (!p.qo_indptr && p.G <= kKeyRows && pool.D == kRows && p.rules.c2 <= 150.f * rx::kLog2e)
-        return pool.f8 ? launch<kRows, true, rx::kAnyRules, 1, true>(p, st) : launch<kRows, false, rx::kAnyRules, 1, true>(p, st);
+        return p.G <= 8 ? go_keys<8>(p, pool, st) : go_keys<kKeyRows>(p, pool, st);
     switch (rx::rules_kind(p.rules)) {
     case rx::kFixedCap: return go_kind<rx::kFixedCap>(p, pool, st);
     case rx::kRange: return go_kind<rx::kRange>(p, pool, st);

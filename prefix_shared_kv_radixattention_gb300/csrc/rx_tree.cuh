@@ -1026,6 +1026,7 @@ __device__ __noinline__ void add_not_finite_rules(const TParams &p, int row, int
 // What a thread keeps of its row of one row tile.
 struct RowState {
     float m, l;    // running maximum (log2 units) and sum
+    float lr;      // with rules: the sum of the rounded weights, by which the result is divided (see keys_softmax)
     float sl2;     // log2 units of a score
 };
 
@@ -1056,7 +1057,7 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
                                 : g.T <= kMaskT ? reinterpret_cast<const uint32_t *>(smem + L::OFF_MASK) + (s % kSegs) * (kMaskT * (kMaskT / 32))
                                                 : p.mask + (int64_t)g.tok * p.words;
         const int words = g.T <= kMaskT ? kMaskT / 32 : p.words;
-        RowState a{-INFINITY, 0.f, p.scale_log2};
+        RowState a{-INFINITY, 0.f, 0.f, p.scale_log2};
         // with rules: the row's position, the positions that it sees, its slope
         int at = 0, lo = 0, hi = 0;
         float slope = 0.f;
@@ -1143,11 +1144,12 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
                     const float alpha = scale_o ? rx::fast_exp2(a.m - m_new) : 1.f;
                     if (need) {
                         a.l *= alpha;
+                        if (RU) a.lr *= alpha;
                         a.m = m_new;
                     }
                     const float mu = a.m == -INFINITY || RU == rx::kFixedCap ? 0.f : a.m;
                     const uint64_t scale2 = rx::f2(left, left), negm2 = rx::f2(-mu, -mu);
-                    uint64_t acc[4] = {0, 0, 0, 0};
+                    uint64_t acc[4] = {0, 0, 0, 0}, rounded = 0;
                     if (!p_free()) return;
 #pragma unroll
                     for (int k = 0; k < kBN / 64; ++k) {
@@ -1163,12 +1165,17 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
                             // three more bits of weights near the largest, but none of
                             // those 17 nats below it, which a long context adds up
                             pk[e] = rx::pack_bf16(e0, e1);
+                            if constexpr (RU) rounded = rx::f2_add(rounded, rx::f2(u2f(pk[e] << 16), u2f(pk[e] & 0xFFFF0000u)));
                         }
                         rx::tmem_st32(tP + k * 32, pk);
                     }
                     float a0, a1;
                     rx::f2_split(rx::f2_add(rx::f2_add(acc[0], acc[1]), rx::f2_add(acc[2], acc[3])), a0, a1);
                     a.l += a0 + a1;
+                    if constexpr (RU) {
+                        rx::f2_split(rounded, a0, a1);
+                        a.lr += a0 + a1;
+                    }
                     if (__any_sync(0xffffffffu, scale_o)) {
                         // the row tile's product before has to be complete; that
                         // of the item two before is
@@ -1199,7 +1206,7 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
             const uint32_t tO = tmem + TM::o(t) + lanes;
             if (!warp_wait(bar + 8 * (L::B_PVDONE + end.b), end.phase & 1, abort_flag, p.status)) return;
             rx::tc_fence_after();
-            const float inv = a.l == 0.f ? 0.f : p.v_scale / a.l;
+            const float div = RU ? a.lr : a.l, inv = div == 0.f ? 0.f : p.v_scale / div;
             const int64_t orow = (int64_t)(g.tok + node) * p.hq + (int64_t)g.g * p.G + rh;
             const int64_t prow = ((int64_t)(2 * blockIdx.x + (g.j0 == 0 ? 1 : 0)) * NT + t) * kRows + row;
             if (warp_on) {
@@ -1267,7 +1274,8 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
 // the operand that has to lie there).  All threads hold the rows' running
 // maxima; a tile that has no score 2^8 above them (one vote of the four warps)
 // leaves them as they are, and with a fixed base there are none.
-template <int D, bool F8>
+// GN: q heads of a kv head, at most (8 leaves half the registers of 16, and half the code).
+template <int D, bool F8, int GN>
 __device__ void keys_softmax(const TParams &p, unsigned char *smem, uint32_t sbase)
 {
     using L = TL<D, F8, true>;
@@ -1314,11 +1322,11 @@ __device__ void keys_softmax(const TParams &p, unsigned char *smem, uint32_t sba
         }
         same_in_all_lanes(g);
         const int lo = g.lo_min, hi = g.P + 1;
-        float m[kKeyRows], l[kKeyRows], slope[kKeyRows];
+        float m[GN], l[GN], lr[GN], slope[GN];  // lr: of the rounded weights
 #pragma unroll
-        for (int n = 0; n < kKeyRows; ++n) {
+        for (int n = 0; n < GN; ++n) {
             m[n] = fixed ? p.rules.base : -INFINITY;
-            l[n] = 0.f;
+            l[n] = lr[n] = 0.f;
             slope[n] = p.rules.slope && n < G ? __ldg(p.rules.slope + g.g * G + n) * rx::kLog2e : 0.f;
         }
         const float *qs = reinterpret_cast<const float *>(smem + L::OFF_QS) + (s % kRing) * kRows;
@@ -1333,10 +1341,10 @@ __device__ void keys_softmax(const TParams &p, unsigned char *smem, uint32_t sba
             const int pos = g.template tile<rx::kAnyRules>(j) * kBN + key;
             const bool seen = pos >= lo && pos < hi;
             const float far = (float)(hi - 1 - pos);
-            float x[kKeyRows];
+            float x[GN];
             bool above = false;
 #pragma unroll
-            for (int n = 0; n < kKeyRows; ++n) {
+            for (int n = 0; n < GN; ++n) {
                 if (n >= G) break;
                 const float sl2 = F8 ? qs[n] : p.scale_log2, q = u2f(sv[n]);
                 float y;
@@ -1354,10 +1362,10 @@ __device__ void keys_softmax(const TParams &p, unsigned char *smem, uint32_t sba
             if (!fixed && rx::named_bar_or(1, kRows, above || dead)) {
                 // new maxima: of each warp's positions, then of the four
                 float *red = team_words();
-                float alpha[kKeyRows];
+                float alpha[GN];
                 bool scale_o = false;
 #pragma unroll
-                for (int n = 0; n < kKeyRows; ++n) {
+                for (int n = 0; n < GN; ++n) {
                     if (n >= G) break;
                     float mx = x[n];
 #pragma unroll
@@ -1366,7 +1374,7 @@ __device__ void keys_softmax(const TParams &p, unsigned char *smem, uint32_t sba
                 }
                 if (!exchange()) return;
 #pragma unroll
-                for (int n = 0; n < kKeyRows; ++n) {
+                for (int n = 0; n < GN; ++n) {
                     alpha[n] = 1.f;
                     if (n >= G) continue;
                     const float mx = fmaxf(fmaxf(red[n], red[kKeyRows + n]), fmaxf(red[2 * kKeyRows + n], red[3 * kKeyRows + n]));
@@ -1376,6 +1384,7 @@ __device__ void keys_softmax(const TParams &p, unsigned char *smem, uint32_t sba
                             scale_o = true;
                         }
                         l[n] *= alpha[n];
+                        lr[n] *= alpha[n];
                         m[n] = mx;
                     }
                 }
@@ -1385,37 +1394,48 @@ __device__ void keys_softmax(const TParams &p, unsigned char *smem, uint32_t sba
                     rx::tmem_ld16(tmem + Kt::o() + lanes, o);
                     rx::tmem_wait_ld();
 #pragma unroll
-                    for (int n = 0; n < kKeyRows; ++n) o[n] = __float_as_uint(u2f(o[n]) * alpha[n]);
+                    for (int n = 0; n < GN; ++n) o[n] = __float_as_uint(u2f(o[n]) * alpha[n]);
                     rx::tmem_st16(tmem + Kt::o() + lanes, o);
                     rx::tmem_wait_st();
                 }
             }
 #pragma unroll
-            for (int n = 0; n < kKeyRows; ++n) {
+            for (int n = 0; n < GN; ++n) {
                 if (n >= G) break;
                 const float w = rx::fast_exp2(fixed || m[n] == -INFINITY ? x[n] : x[n] - m[n]);
+                // rounded to bf16 for the tensor core.  The result is divided by the sum of
+                // what was rounded, so that a weight's rounding moves it only as far as
+                // its V is from the result (few keys with most of the weight: error to
+                // 64 bits 2.6e-3 without, where the result's own rounding is 1.7e-3); the
+                // log-sum-exp takes the sum of the weights themselves
+                const __nv_bfloat16 r = __float2bfloat16_rn(w);
                 l[n] += w;
-                // rounded to bf16 for the tensor core, its sum is not (as in softmax_rows)
-                *reinterpret_cast<__nv_bfloat16 *>(smem + p_at + Kt::p(b) + n * 128 + ((chunk ^ (n & 7)) << 4)) = __float2bfloat16_rn(w);
+                lr[n] += __bfloat162float(r);
+                *reinterpret_cast<__nv_bfloat16 *>(smem + p_at + Kt::p(b) + n * 128 + ((chunk ^ (n & 7)) << 4)) = r;
             }
             rx::fence_proxy_async_smem();
             rx::tc_fence_before();
             rx::mbar_arrive(bar + 8 * (L::B_PFULL + b));
         }
-        // the rows' sums over all threads
-        float *red = team_words();
+        // the rows' sums over all threads, then those of the rounded weights
+        float tot[GN], div[GN];
 #pragma unroll
-        for (int n = 0; n < kKeyRows; ++n) {
-            if (n >= G) break;
+        for (int k = 0; k < 2; ++k) {
+            float *red = team_words();
 #pragma unroll
-            for (int d = 16; d > 0; d >>= 1) l[n] += __shfl_xor_sync(0xffffffffu, l[n], d);
-            if (lane == 0) red[warp * kKeyRows + n] = l[n];
+            for (int n = 0; n < GN; ++n) {
+                if (n >= G) break;
+                float x = k == 0 ? l[n] : lr[n];
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+                if (lane == 0) red[warp * kKeyRows + n] = x;
+            }
+            if (!exchange()) return;
+#pragma unroll
+            for (int n = 0; n < GN; ++n)
+                (k == 0 ? tot : div)[n] =
+                    n < G ? red[n] + red[kKeyRows + n] + red[2 * kKeyRows + n] + red[3 * kKeyRows + n] : 0.f;
         }
-        if (!exchange()) return;
-        float tot[kKeyRows];
-#pragma unroll
-        for (int n = 0; n < kKeyRows; ++n)
-            tot[n] = n < G ? red[n] + red[kKeyRows + n] + red[2 * kKeyRows + n] + red[3 * kKeyRows + n] : 0.f;
         wait(L::B_PVDONE + ((c - 1) & 1), ((c - 1) >> 1) & 1);
         uint32_t o[kKeyRows];
         rx::tmem_ld16(tmem + Kt::o() + lanes, o);
@@ -1444,9 +1464,9 @@ __device__ void keys_softmax(const TParams &p, unsigned char *smem, uint32_t sba
             }
         }
 #pragma unroll
-        for (int n = 0; n < kKeyRows; ++n) {
+        for (int n = 0; n < GN; ++n) {
             if (n >= G) break;
-            const float v = tot[n] == 0.f ? 0.f : u2f(o[n]) * (p.v_scale / tot[n]) + add;
+            const float v = div[n] == 0.f ? 0.f : u2f(o[n]) * (p.v_scale / div[n]) + add;
             if (g.whole) p.o[(orow + n) * D + key] = __float2bfloat16_rn(v);
             else p.part_o[(prow + n) * D + key] = v;
             if (key == n) {
@@ -1461,7 +1481,7 @@ __device__ void keys_softmax(const TParams &p, unsigned char *smem, uint32_t sba
     }
 }
 
-template <int D, bool F8, int NT, int RU, bool KEYS>
+template <int D, bool F8, int NT, int RU, bool KEYS, int GN>
 __global__ void __launch_bounds__(Ro<NT>::THREADS, 1) tree_kernel(const __grid_constant__ TParams p)
 {
     using L = TL<D, F8, KEYS>;
@@ -1533,7 +1553,7 @@ __global__ void __launch_bounds__(Ro<NT>::THREADS, 1) tree_kernel(const __grid_c
 
     if (warp < W::SOFT) {
         rx::reg_inc<W::R_SOFT>();
-        if constexpr (KEYS) keys_softmax<D, F8>(p, smem, sbase);
+        if constexpr (KEYS) keys_softmax<D, F8, GN>(p, smem, sbase);
         else softmax_rows<D, F8, NT, RU>(p, smem, sbase);
     } else if (warp < W::Q) {
         rx::reg_dec<W::R_REST>();
@@ -1638,25 +1658,25 @@ bool tree_shape_ok(int32_t batch, int32_t hq, int32_t hkv, int32_t D, int32_t ma
 
 // The registers that the kernel is launched with: the shares of the roles are
 // granted out of them, and a share that is not there would be waited for.
-template <int D, bool F8, int NT, int RU, bool KEYS>
+template <int D, bool F8, int NT, int RU, bool KEYS, int GN>
 bool registers_ok()
 {
     cudaFuncAttributes a;
-    return cudaFuncGetAttributes(&a, tree_kernel<D, F8, NT, RU, KEYS>) == cudaSuccess && a.numRegs >= Ro<NT, KEYS>::R_LAUNCH;
+    return cudaFuncGetAttributes(&a, tree_kernel<D, F8, NT, RU, KEYS, GN>) == cudaSuccess && a.numRegs >= Ro<NT, KEYS>::R_LAUNCH;
 }
 
-template <int D, bool F8, int RU, int NT = 1, bool KEYS = false>
+template <int D, bool F8, int RU, int NT = 1, bool KEYS = false, int GN = 0>
 int launch(const TParams &p, cudaStream_t st)
 {
-    static const bool ok = registers_ok<D, F8, NT, RU, KEYS>();
+    static const bool ok = registers_ok<D, F8, NT, RU, KEYS, GN>();
     if (!ok) return rx_set_error(RX_ERR_UNSUPPORTED, "tree attention: the kernel was built with too few registers");
     // per device, whichever is current
     static thread_local int set_on = -1;
     int dev = 0;
     RX_CUDA_CHECK(cudaGetDevice(&dev));
-    if (dev != set_on) RX_CUDA_CHECK(cudaFuncSetAttribute(tree_kernel<D, F8, NT, RU, KEYS>, cudaFuncAttributeMaxDynamicSharedMemorySize, (TL<D, F8, KEYS>::BYTES)));
+    if (dev != set_on) RX_CUDA_CHECK(cudaFuncSetAttribute(tree_kernel<D, F8, NT, RU, KEYS, GN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (TL<D, F8, KEYS>::BYTES)));
     set_on = dev;
-    tree_kernel<D, F8, NT, RU, KEYS><<<kCtas, Ro<NT>::THREADS, (TL<D, F8, KEYS>::BYTES), st>>>(p);
+    tree_kernel<D, F8, NT, RU, KEYS, GN><<<kCtas, Ro<NT>::THREADS, (TL<D, F8, KEYS>::BYTES), st>>>(p);
     RX_CUDA_CHECK(cudaGetLastError());
     // a programmatic dependent: it is launched meanwhile and waits on the device
     cudaLaunchConfig_t cfg = {};
