@@ -700,8 +700,10 @@ size_t rx_attn_tree_workspace(int32_t batch, int32_t num_q_heads, int32_t num_kv
  * the window bounds only what lies behind the token.
  *
  * Scores, sums and the output's accumulator are fp32; the weights are rounded to
- * bf16 for the product with V (off by at most 2^-8 sum p |V|) and o once more,
- * as in rx_attn_extend and rx_attn_tree.  A capped score is off by at most 2^-21
+ * bf16 for the product with V and o once more, as in rx_attn_extend and
+ * rx_attn_tree (calls with few query rows divide o by the sum of the rounded
+ * weights, lse is always that of the weights themselves): the rounded weights move
+ * o by at most 2^-8 sum p |V - o|, or 2^-8 sum p |V|.  A capped score is off by at most 2^-21
  * of itself and 2^-25 of the cap; next to scores beyond the cap, and in
  * rx_attn_decode_rules with caps up to 150, by a few 2^-23 of the cap.  With a cap of up to 50 and no slopes, V values above 2^57 may overflow
  * o.

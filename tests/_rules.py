@@ -63,7 +63,9 @@ class RulesBatch:
 
 def check(o, lse, r, b, what="", cap=None):
     """Bounds of the attention with rules.  o: the softmax weights are rounded to
-    bf16 before P V (2^-8 of sum p |v|) and the result once more (2^-8 of |o|).
+    bf16 before P V (2^-8 of sum p |v|; divided by the sum of the rounded weights,
+    sum p (1 + e) v / sum p (1 + e) is off from o by at most max |e| sum p |v - o|, under
+    2^-8 (sum p |v| + |o|)) and the result once more (2^-8 of |o|).
     The scores are fp32 sums of d exact products, off by at most d 2^-24 sum |q
     k| scale; with spread s of the queries that sum is under 0.8 s sqrt(d) times
     1.5: under 3e-4 s for d up to 128.  A cap adds under 4 2^-23 cap log2(e) log2
@@ -74,7 +76,7 @@ def check(o, lse, r, b, what="", cap=None):
     ro, rl, ra = r
     s = max(1.0, float(np.abs(b.q).max()) / 4.0)
     off = 2 * (3e-4 * s + 1e-6 * (b.cap if cap is None else cap) + 1e-5)
-    bound = HALF_STEP * np.abs(ro) + (HALF_STEP * (1 + HALF_STEP) + off) * ra + 1e-30
+    bound = 2 * HALF_STEP * np.abs(ro) + (HALF_STEP * (1 + HALF_STEP) + off) * ra + 1e-30
     err = np.abs(np.asarray(o, np.float64) - ro)
     assert not np.isnan(o).any(), f"{what}: NaN"
     worst = (err / bound).max() if err.size else 0.0
