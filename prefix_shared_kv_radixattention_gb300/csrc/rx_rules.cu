@@ -21,7 +21,7 @@ int go(const TParams &p, const TreePool &pool, cudaStream_t st)
 {
     // one token a request: the products with the positions as their wide side.
     // It takes 16 rows, and a head_dim that fills the tensor core's 128 lanes.
-    // (Long chat, a cap of 50: 258 us, with the rows as the wide side 403; few-shot
+    // (Long chat, a cap of 50: 255 us, with the rows as the wide side 403; few-shot
     // with slopes 162, 406.)
     // It takes the cap from the exponential and the reciprocal alone (the
     // polynomials beside them: windowed E4M3 208 us, without 170), whose error grows

@@ -945,14 +945,16 @@ __device__ void issue_pv(const TParams &p, unsigned char *smem, uint32_t sbase)
         rx::tc_fence_after();
         const uint64_t dvs = dv + (uint64_t)((st * L::NB * L::BLK) >> 4);
 #pragma unroll
-        for (int ks = 0; ks < kBN / 16; ++ks)
+        for (int ks = 0; ks < kBN / 16; ++ks) {
+            const uint64_t v = dvs + (uint64_t)((ks * 16 * 128) >> 4);
+            const uint32_t more = !m.first || ks > 0;
             if constexpr (KEYS)
-                rx::tc_mma(tmem + Kt::o(), dvs + (uint64_t)((ks * 16 * 128) >> 4),
-                           rx::sdesc_sw128(sbase + L::OFF_P + Kt::p(turn.b) + (ks >> 2) * Kt::PBLK + (ks & 3) * 32, 16, 1024), idesc,
-                           (!m.first || ks > 0) ? 1u : 0u);
+                rx::tc_mma(tmem + Kt::o(), v,
+                           rx::sdesc_sw128(sbase + L::OFF_P + Kt::p(turn.b) + (ks >> 2) * Kt::PBLK + (ks & 3) * 32, 16, 1024),
+                           idesc, more);
             else
-            rx::tc_mma_ts(tmem + M::o(m.t), tmem + M::p(turn.b) + ks * 8, dvs + (uint64_t)((ks * 16 * 128) >> 4), idesc,
-                          (!m.first || ks > 0) ? 1u : 0u);
+                rx::tc_mma_ts(tmem + M::o(m.t), tmem + M::p(turn.b) + ks * 8, v, idesc, more);
+        }
         rx::tc_commit(bar + 8 * (L::B_PVDONE + turn.b));
         if (m.t1) rx::tc_commit(bar + 8 * (L::B_VEMPTY + st));
         return true;
