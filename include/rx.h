@@ -399,7 +399,8 @@ int rx_qk_norm_rope_store_fp8(const rx_kv_pool_fp8 *pool, const void *q, int64_t
  *       device int32 [batch]; req_to_token: device int32, row stride
  *       rtt_stride;
  *   max_extend_len: host bound on extend_len[b] (sizes the grid; larger
- *       device values are an error that leaves rows unwritten);
+ *       device values are an error that leaves rows unwritten, and so is an
+ *       extend_len[b] above qo_indptr[b+1] - qo_indptr[b]: RX_DEV_BAD_LEN);
  *   workspace, ws_bytes: NULL / 0, or device memory of at least
  *       rx_attn_extend_workspace(...) bytes, 256-byte aligned, owned by the
  *       caller and not used by anything else until the call's work on
@@ -818,7 +819,8 @@ int rx_qk_rope_axes_store_fp8(const rx_kv_pool_fp8 *pool, const void *q, int64_t
  * A negative length, or one past rtt_stride (or the pages' positions), sets
  * RX_DEV_BAD_LEN and counts as a request without new tokens, seq_len 0.  More
  * new tokens than max_tokens set RX_DEV_BAD_LEN: qo_indptr ends at max_tokens
- * and the tokens behind it are left out.  A slot or page outside the pool sets
+ * and the tokens behind it are left out (the extend calls leave out a request
+ * that has fewer rows there than new tokens).  A slot or page outside the pool sets
  * RX_DEV_BAD_SLOT and its slot is -1 (in req_to_token too). */
 int rx_step_maps(const int32_t *req_idx, const int32_t *prefix_len, const int32_t *new_len, int32_t batch,
                  int32_t *req_to_token, int64_t rtt_stride, const int32_t *pages, int64_t pages_stride, int32_t page_size,

@@ -246,19 +246,24 @@ template <int RU>
 __device__ __forceinline__ Req load_req(const TParams &p, int b, bool flag = false)
 {
     Req r;
+    [[maybe_unused]] int rows = 1;  // with rules: rows of q and o that are the request's
     if (RU && !p.qo_indptr) {
         r.tok = b;
         r.P = __ldg(p.prefix_len + b) - 1;
         r.T = r.P == -1 ? 0 : 1;
     } else {
         r.tok = __ldg(p.qo_indptr + b);
-        r.T = RU ? __ldg(p.extend_len + b) : __ldg(p.qo_indptr + b + 1) - r.tok;
+        r.T = __ldg(p.qo_indptr + b + 1) - r.tok;
+        if constexpr (RU) {
+            rows = r.T;
+            r.T = __ldg(p.extend_len + b);
+        }
         r.P = __ldg(p.prefix_len + b);
     }
     r.row = __ldg(p.req_idx + b);
     r.ntiles = r.nqt = r.first = 0;
     if (r.T == 0) return r;
-    if (r.T < 0 || r.T > p.max_tree || r.P < 0 || (int64_t)r.P + r.T > p.rtt_stride) {
+    if (r.T < 0 || r.T > p.max_tree || (RU && r.T > rows) || r.P < 0 || (int64_t)r.P + r.T > p.rtt_stride) {
         if (flag && p.status) atomicOr(p.status, RX_DEV_BAD_LEN);
         return r;
     }
