@@ -1066,21 +1066,24 @@ def rx_logits_process(rules: LogitsRules, logits, out, dev_status=None, stream=N
 # ---------------------------------------------------------------------------
 
 
-def _here(t, name):
+def _here(named):
     """The launch goes to the current device: its tensors have to be there."""
-    if t.get_device() != _torch()._C._cuda_getDevice():
-        raise ValueError(f"{name}: must be on the current CUDA device")
+    device = _torch()._C._cuda_getDevice()
+    for name, t in named:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"{name}: must be on the current CUDA device")
 
 
 def _checked(dtype, named):
-    """_dev for several tensors of one type: these calls are made a layer, and a
-    function call a tensor is a fifth of one on a small batch."""
+    """_dev for several tensors of one type, and that they are on the current
+    device: these calls are made a layer, and a function call a tensor is a fifth
+    of one on a small batch."""
     try:
         for _, t in named:
             if t is not None and not (t.dtype is dtype and t.is_cuda and t.is_contiguous()):
                 break
         else:
-            return
+            return _here(named)
     except AttributeError:
         pass
     for name, t in named:
@@ -1108,6 +1111,7 @@ class AttnRules:
         self._ref = ctypes.byref(self.struct)
 
     def _check(self, tokens: int, heads: int):
+        _here((("slopes", self.slopes), ("see_from", self.see_from), ("see_to", self.see_to)))
         if self.slopes is not None and self.slopes.numel() != heads:
             raise ValueError("AttnRules: slopes must have an entry for each q head")
         for t in (self.see_from, self.see_to):
@@ -1133,7 +1137,7 @@ def _rules_args(q, o, lse, lists, req_to_token, rules, workspace, dev_status, he
     _checked(torch.int32, (*lists, ("req_to_token", req_to_token), ("dev_status", dev_status)))
     _dev(lse, torch.float32, "lse")
     _dev(workspace, torch.uint8, "workspace")
-    _here(q, "q")
+    _here((("lse", lse), ("workspace", workspace)))
     if not isinstance(rules, AttnRules):
         raise TypeError("rules: expected an AttnRules")
     shape = q.shape
@@ -1236,7 +1240,7 @@ def _axes_call(call, pool, dims, q, q_out, k_new, v_new, q_weight, k_weight, slo
     new, v_row = _head_rows(k_new, "k_new"), _head_rows(v_new, "v_new")
     _checked(torch.bfloat16, (("q_out", q_out), ("q_weight", q_weight), ("k_weight", k_weight)))
     _checked(torch.int32, (("slots", slots), ("pos", pos), ("dev_status", dev_status)))
-    _here(q, "q")
+    _here((("q", q), ("k_new", k_new), ("v_new", v_new)))
     if new[:3] != (slots.numel(), hkv, dim) or v_row[:3] != new[:3]:
         raise ValueError("k_new/v_new must be [n, num_kv_heads, head_dim] and slots [n]")
     if pos.dim() != 2 or pos.shape[1] != n:
@@ -1294,7 +1298,6 @@ def rx_step_maps(req_idx, prefix_len, new_len, req_to_token, num_slots: int, qo_
     _checked(_torch().int32, (("req_idx", req_idx), ("prefix_len", prefix_len), ("new_len", new_len),
                               ("req_to_token", req_to_token), ("qo_indptr", qo_indptr), ("seq_len", seq_len), ("pos", pos),
                               ("slots", slots), ("pages", pages), ("dev_status", dev_status)))
-    _here(qo_indptr, "qo_indptr")
     B, n = req_idx.numel(), pos.numel()
     if prefix_len.numel() != B or new_len.numel() != B or qo_indptr.numel() != B + 1 or \
             (seq_len is not None and seq_len.numel() != B) or slots.numel() != n:
