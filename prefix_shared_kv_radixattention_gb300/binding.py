@@ -1232,6 +1232,20 @@ def rx_attn_decode_rules_fp8(k_pool, v_pool, k_scale: float, v_scale: float, q, 
                   workspace, dev_status, stream)
 
 
+def _pair_axis(pair_axis):
+    """The array to keep alive, its address, its entries."""
+    torch = _torch()
+    if isinstance(pair_axis, torch.Tensor):
+        if pair_axis.is_cuda or pair_axis.dtype != torch.uint8 or not pair_axis.is_contiguous():
+            raise TypeError("pair_axis: expected a contiguous uint8 host tensor")
+        return pair_axis, pair_axis.data_ptr(), pair_axis.numel()
+    given = np.asarray(pair_axis)
+    if given.dtype != np.uint8 and not ((given >= 0) & (given <= 255) & (given == np.floor(given))).all():
+        raise ValueError("pair_axis: entries must be whole numbers of 0 .. 255")  # the cast would wrap or cut them
+    axis, address = _np(given, np.uint8)
+    return axis, address, axis.size
+
+
 def _axes_call(call, pool, dims, q, q_out, k_new, v_new, q_weight, k_weight, slots, pos, pair_axis, base, eps, dev_status,
                stream):
     torch = _torch()
@@ -1252,13 +1266,7 @@ def _axes_call(call, pool, dims, q, q_out, k_new, v_new, q_weight, k_weight, slo
     for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
         if w is not None and w.numel() != d:
             raise ValueError(f"{name} must be [head_dim]")
-    if isinstance(pair_axis, torch.Tensor):
-        if pair_axis.is_cuda or pair_axis.dtype != torch.uint8 or not pair_axis.is_contiguous():
-            raise TypeError("pair_axis: expected a contiguous uint8 host tensor")
-        size, axis = pair_axis.numel(), pair_axis.data_ptr()
-    else:
-        pair_axis, axis = _np(pair_axis, np.uint8)
-        size = pair_axis.size
+    pair_axis, axis, size = _pair_axis(pair_axis)
     if size != d // 2:
         raise ValueError("pair_axis must have head_dim / 2 entries")
     rc = call(pool, q.data_ptr(), qs, q_out.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), new[3], 0 if eps is None else 1,

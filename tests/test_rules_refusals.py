@@ -170,3 +170,13 @@ def test_pair_axis_has_an_entry_a_pair():
     x = torch.zeros(3, 4, 64, dtype=torch.bfloat16)
     with pytest.raises(TypeError):
         rx.rx_qk_rope_axes_store(x, x, x, x, x, x, None, None, None, None, np.zeros(32, np.uint8), 1e4)
+
+
+@pytest.mark.parametrize("bad", [256, -1, 1.5, float("nan"), 1 << 40])
+def test_pair_axis_is_not_cut_to_a_byte(bad):
+    for make in (list, np.array):
+        with pytest.raises(ValueError):
+            rx._pair_axis(make([0] * 31 + [bad]))
+    for good in ([0, 1, 255], np.array([0, 1, 255]), np.array([0., 1., 255.]), np.array([0, 1, 255], np.uint8)):
+        axis, _, size = rx._pair_axis(good)
+        assert axis.dtype == np.uint8 and axis.tolist() == [0, 1, 255] and size == 3
