@@ -710,7 +710,10 @@ size_t rx_attn_tree_workspace(int32_t batch, int32_t num_q_heads, int32_t num_kv
  * o.
  *
  * What a token does not see takes no part in its result, whatever K and V hold
- * there (NaN and infinities among it).  Positions before the window of a request's
+ * there (NaN and infinities among it).  One thing it may share with the tokens
+ * next to it: which form of the cap is computed goes by the largest score that any
+ * of up to 32 rows (tokens times heads of a kv head) sees in a part of the context,
+ * and the forms differ within the bounds above.  Positions before the window of a request's
  * first new token are not read, nor in rx_attn_decode_rules those before its
  * token's lo: their slot ids may be anything.  Other positions that no token sees
  * may be read or not, and a slot id outside the pool is flagged if it is. */

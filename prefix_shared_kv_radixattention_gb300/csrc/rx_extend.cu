@@ -499,7 +499,7 @@ __device__ void softmax_rows(const XParams &p, const Tile &T, unsigned char *sme
             rx::tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * c));
         rx::tmem_wait_ld();
         if (RANGE && need_mask) {
-            rx::hide(sv, kbase, lo, hi);
+            rx::hide<0xFF800000u>(sv, lo - kbase, hi - kbase);
         } else if (need_mask) {
 #pragma unroll
             for (int k = 0; k < kBN; ++k)
@@ -680,8 +680,8 @@ __device__ void softmax_halves(const XParams &p, const Tile &T, unsigned char *s
 #pragma unroll
         for (int c = 0; c < HK / 32; ++c) rx::tmem_ld32(tS + c * 32, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * c));
         rx::tmem_wait_ld();
-        const float left = rx::apply_rules<KIND, true>(sv, p.rules, sl2, slope, row_pos - kbase, row < T.M);
-        if (need_mask) rx::hide(sv, kbase, lo, hi);
+        const float left = rx::apply_rules<KIND, true>(sv, p.rules, sl2, slope, row_pos - kbase, row < T.M, need_mask, lo - kbase, hi - kbase);
+        if (need_mask) rx::hide<0xFF800000u>(sv, lo - kbase, hi - kbase);
         bool need = false;
         float alpha = 1.f;
         if constexpr (KIND != rx::kFixedCap) {

@@ -1112,8 +1112,8 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
                         const bool all = __all_sync(0xffffffffu, !valid || (kbase >= lo && kbase + kBN <= hi));
                         rx::tmem_wait_ld();
                         release_s();
-                        left = rx::apply_rules<RU, !F8>(sv, p.rules, a.sl2, slope, at - kbase, valid);
-                        if (!all) rx::hide(sv, kbase, lo, hi);
+                        left = rx::apply_rules<RU, !F8>(sv, p.rules, a.sl2, slope, at - kbase, valid, !all, lo - kbase, hi - kbase);
+                        if (!all) rx::hide<0xFF800000u>(sv, lo - kbase, hi - kbase);
                     } else if (kbase + kBN > g.P) {   // drafted positions, or past the last
                         const int off = kbase - g.P, w0 = off >> 5;
                         const uint32_t *mrow = masks && valid ? masks + (int64_t)node * words : nullptr;
