@@ -704,10 +704,13 @@ size_t rx_attn_tree_workspace(int32_t batch, int32_t num_q_heads, int32_t num_kv
  * bf16 for the product with V and o once more, as in rx_attn_extend and
  * rx_attn_tree (calls with few query rows divide o by the sum of the rounded
  * weights, lse is always that of the weights themselves): the rounded weights move
- * o by at most 2^-8 sum p |V - o|, or 2^-8 sum p |V|.  A capped score is off by at most 2^-21
- * of itself and 2^-25 of the cap; next to scores beyond the cap, and in
- * rx_attn_decode_rules with caps up to 150, by a few 2^-23 of the cap.  With a cap of up to 50 and no slopes, V values above 2^57 may overflow
- * o.
+ * o by at most 2^-8 sum p |V - o|, or 2^-8 sum p |V|.  Past the rounding of q . k
+ * itself a capped score is off by at most 2^-21 of itself and 2^-24 of the cap; next
+ * to scores beyond the cap, and in rx_attn_decode_rules with caps up to 150, by at
+ * most 5 * 2^-23 of the cap.  With a cap of up to 50 and no slopes the weights
+ * before their sum divides them lie between 2^-100 and 2^45: V values above 2^57
+ * may overflow o, and where all of a row's scores are near minus the cap, V values
+ * below 2^-26 lose bits in products under fp32's normal range.
  *
  * What a token does not see takes no part in its result, whatever K and V hold
  * there (NaN and infinities among it).  One thing it may share with the tokens

@@ -14,8 +14,10 @@
 // 3/8 of the cap one of degree 7: the special-function units are what a tile waits for
 // otherwise.  The first way is off by c2 times a few 2^-23 (a cap of 50: under 3e-5
 // log2 units, a weight's relative error under 2^-15, where the weights are rounded
-// to bf16 for the product with V), the polynomials by 2^-25 and 2^-26 of c2 and
-// never more than 2^-21 of the score, so that a large cap costs nothing.
+// to bf16 for the product with V), the polynomials' fits by 2^-25 and 2^-26 of c2 and
+// what fp32 makes of them by no more than 2^-21 of the score, so that a large cap
+// costs nothing; a fixed base (below) takes another 2^-18 log2 units, half a step of
+// x - m, or 2^-24 of c2.
 // (tanh.approx is off by 2^-11 of its value: 0.03 log2 units at that cap.)
 //
 // A cap bounds the scores, so the softmax needs no running maximum: with
@@ -214,12 +216,12 @@ inline int make_rules(const char *who, const rx_attn_rules *in, float scale_log2
         const float ke = scale_log2 * r.to_e;
         if (!(in->cap >= 1e-3f && in->cap <= 1e6f) || !(ke >= 0x1p-126f && ke < INFINITY))
             return rx_set_error(RX_ERR_UNSUPPORTED, "%s: cap %g (from 1e-3 to 1e6)", who, in->cap);
-        // tanh y = y P(y^2) for |y| <= 1, off by at most 2.0e-8 (least maximum, found by reweighted least squares;
-        // degree 11, off by 2.4e-7, left a log-sum-exp off by 1e-6 of itself)
+        // tanh y = y P(y^2) for |y| <= 1, off by at most 2.6e-8 as rounded here (least maximum, found by
+        // reweighted least squares, 2.0e-8 before the rounding; degree 11, off by 2.4e-7, left a log-sum-exp off by 1e-6 of itself)
         static const float P[7] = {0.999999693f, -0.333321293f, 0.133195837f, -0.0532658349f, 0.0199732818f, -0.00595127971f, 0.000963771925f};
         for (int i = 0; i < 7; ++i) r.poly[i] = P[i] * r.c2;
         r.to_y = 1.f / r.c2;
-        // the same for |y| <= 3/8, off by at most 9.6e-9
+        // the same for |y| <= 3/8, off by at most 1.1e-8
         static const double Q[4] = {0.99999974, -0.333308399, 0.132683921, -0.0476184644};
         const double k1 = (double)scale_log2 / r.c2;
         double c = (double)r.c2 * k1;
