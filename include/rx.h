@@ -716,10 +716,10 @@ size_t rx_attn_tree_workspace(int32_t batch, int32_t num_q_heads, int32_t num_kv
  * there (NaN and infinities among it).  One thing it may share with the tokens
  * next to it: which form of the cap is computed goes by the largest score that any
  * of up to 32 rows (tokens times heads of a kv head) sees in a part of the context,
- * and the forms differ within the bounds above.  Positions before the window of a request's
- * first new token are not read, nor in rx_attn_decode_rules those before its
- * token's lo: their slot ids may be anything.  Other positions that no token sees
- * may be read or not, and a slot id outside the pool is flagged if it is. */
+ * and the forms differ within the bounds above.  Positions before the window of a
+ * request's first new token are not read, nor in rx_attn_decode_rules those before
+ * its token's lo: their slot ids may be anything.  Other positions that no token
+ * sees may be read or not, and a slot id outside the pool is flagged if it is. */
 typedef struct {
     float cap;                /* > 0 (1e-3 to 1e6): scores are capped; 0: they are not        */
     int32_t window;           /* > 0: positions a token sees, itself among them; 0: all of them */
@@ -827,7 +827,8 @@ int rx_qk_rope_axes_store_fp8(const rx_kv_pool_fp8 *pool, const void *q, int64_t
  * new tokens than max_tokens set RX_DEV_BAD_LEN: qo_indptr ends at max_tokens
  * and the tokens behind it are left out (the extend calls leave out a request
  * that has fewer rows there than new tokens).  A slot or page outside the pool sets
- * RX_DEV_BAD_SLOT and its slot is -1 (in req_to_token too). */
+ * RX_DEV_BAD_SLOT and its slot is -1 (with pages in req_to_token too; without
+ * them req_to_token is only read). */
 int rx_step_maps(const int32_t *req_idx, const int32_t *prefix_len, const int32_t *new_len, int32_t batch,
                  int32_t *req_to_token, int64_t rtt_stride, const int32_t *pages, int64_t pages_stride, int32_t page_size,
                  int64_t num_slots, int32_t *qo_indptr, int32_t *seq_len, int32_t *pos, int32_t *slots, int64_t max_tokens,
