@@ -1257,17 +1257,25 @@ using ExtendPool = RxAttnPool;
 // A call with rules that shares the contexts among CTAs (rx_rules.cu) instead of
 // copying them first: one with few query rows a kv head and request, for which
 // every position is read once or twice either way, or one that would leave SMs
-// without a CTA.  Measured, time shared / time copied, bf16: up to 512 rows 0.16 to
-// 0.87 (one case 1.02); 1,024 and 2,048 rows 0.40 to 1.09 with 32 or 64 CTAs, 0.77
-// to 1.28 with 128, 0.9 to 1.7 with more; 4,096 rows and more 1.1 to 2.6.  E4M3,
-// of which every row tile of 128 gathers and widens the positions for itself: up to
-// 128 rows 0.19 to 1.21 (most below 0.9); 256 and 512 rows 0.35 to 1.16 with up to
-// 32 CTAs, 1.2 to 1.9 with more; more rows 0.85 to 3.2.
+// without a CTA, which then walks a long context alone.  The lengths are not known
+// here.  Measured, time shared / time copied (geometric mean, least and most of
+// contexts of 1,024 to 16,384, prefixes of one request's and shared by four, 1 to 32
+// kv heads, a cap):
+//   bf16   up to 128 rows  0.15 to 1.07 at every number of CTAs
+//          256             up to 64 CTAs 0.7 (0.20 to 1.06), up to 512 0.9 (0.64 to 1.38)
+//          512 to 2,048    17 to 32 CTAs 0.7 (0.41 to 1.09), 33 to 64 0.9 (0.57 to 1.25), more 1.1 to 1.5 (0.77 to 1.61)
+//          4,096 to 16,384 up to 32 CTAs 0.75 (0.44 to 1.18), 64 and more 1.2 (1.04 to 1.34)
+//   E4M3, of which every row tile of 128 gathers and widens the positions for itself:
+//          up to 64        33 to 64 CTAs 0.8 (0.50 to 1.06), 65 to 128 1.05 (0.72 to 1.52), more 1.2 (0.90 to 1.74)
+//          128             17 to 32 CTAs 0.9 (0.46 to 1.61), 33 to 64 1.1 (0.60 to 1.67), more 1.4 (0.97 to 1.95)
+//          256 to 4,096    up to 16 CTAs 0.9 (0.38 to 1.66), 17 to 32 1.25 (0.76 to 1.76), more 1.5 to 3.6
+// A window of 1,024 makes the copy cheap: 0.6 to 1.0 with bf16 and up to 256 rows, 0.9 to 2.1 with E4M3.
 bool few_rows(int32_t hq, int32_t hkv, int32_t batch, int32_t max_len, bool f8)
 {
     const int64_t rows = (int64_t)max_len * (hq / hkv), ctas = (rows + kCtaRows - 1) / kCtaRows * hkv * batch;
     if (max_len > RX_SPLIT_MAX_LEN) return false;
-    return f8 ? rows <= 128 || (rows <= 512 && ctas <= 32) : rows <= 512 || ctas < 96;
+    if (f8) return rows <= 4096 && ctas <= (rows <= 64 ? 64 : rows <= 128 ? 32 : 16);
+    return rows <= 256 || ctas <= (rows <= 2048 ? 64 : 32);
 }
 
 // rx_attn_extend and rx_attn_extend_fp8 after their pool checks (`who`

@@ -180,3 +180,35 @@ def test_pair_axis_is_not_cut_to_a_byte(bad):
     for good in ([0, 1, 255], np.array([0, 1, 255]), np.array([0., 1., 255.]), np.array([0, 1, 255], np.uint8)):
         axis, _, size = rx._pair_axis(good)
         assert axis.dtype == np.uint8 and axis.tolist() == [0, 1, 255] and size == 3
+
+
+def _shared(f8, hq, hkv, batch, max_len):
+    """Whether rx_attn_extend_rules shares the contexts among CTAs (else it copies them): the two refuse a workspace of
+    one byte in words of their own."""
+    lib, kw = rx.library(), dict(BASE, d=128, hkv=hkv)
+    pool = _pools(kw)[1 if f8 else 0]
+    rules = rx.AttnRulesStruct(50.0, 0, None, None, None)
+    call = lib.rx_attn_extend_rules_fp8 if f8 else lib.rx_attn_extend_rules
+    rc = call(ctypes.byref(pool), P(FAKE), P(FAKE), None, hq, P(FAKE), P(FAKE), P(FAKE), P(FAKE), P(FAKE), 100, batch, max_len,
+              ctypes.byref(rules), P(FAKE), 1, 0.125, None, None)
+    assert rc == rx.RX_ERR_CAPACITY
+    words = rx.last_error()
+    assert words.endswith("needed") != words.endswith("too small"), words
+    return words.endswith("needed")
+
+
+@pytest.mark.parametrize("f8,hq,hkv,batch,max_len,shared", [
+    # few rows, any number of requests
+    (False, 32, 8, 512, 16, True), (False, 32, 8, 64, 64, True), (False, 32, 8, 1, 64, True),
+    # many rows: only where few CTAs would be left with long contexts
+    (False, 64, 8, 4, 64, True), (False, 64, 8, 5, 64, False), (False, 32, 8, 8, 128, False), (False, 64, 8, 1, 256, True),
+    # few kv heads: 4,096 rows and more at 64 CTAs and more take up to a third longer when shared
+    (False, 8, 1, 1, 512, True), (False, 8, 1, 2, 512, True), (False, 8, 1, 5, 512, False), (False, 16, 1, 1, 1024, False),
+    (False, 16, 2, 1, 1024, False), (False, 8, 2, 5, 512, False), (False, 8, 1, 5, 256, True), (False, 16, 1, 1, 512, True),
+    (False, 8, 1, 1, 1025, False),
+    # E4M3: every row tile gathers for itself
+    (True, 32, 8, 8, 16, True), (True, 32, 8, 9, 16, False), (True, 64, 8, 4, 16, True), (True, 64, 8, 8, 16, False),
+    (True, 32, 8, 2, 64, True), (True, 32, 8, 4, 64, False), (True, 8, 1, 16, 64, False), (True, 8, 1, 4, 64, True),
+    (True, 8, 1, 1, 512, True), (True, 16, 1, 1, 512, False)])
+def test_which_calls_share_their_contexts(f8, hq, hkv, batch, max_len, shared):
+    assert _shared(f8, hq, hkv, batch, max_len) == shared
