@@ -246,7 +246,6 @@ template <int RU>
 __device__ __forceinline__ Req load_req(const TParams &p, int b, bool flag = false)
 {
     Req r;
-    [[maybe_unused]] int rows = 1;  // with rules: rows of q and o that are the request's
     if (RU && !p.qo_indptr) {
         r.tok = b;
         r.P = __ldg(p.prefix_len + b) - 1;
@@ -254,16 +253,16 @@ __device__ __forceinline__ Req load_req(const TParams &p, int b, bool flag = fal
     } else {
         r.tok = __ldg(p.qo_indptr + b);
         r.T = __ldg(p.qo_indptr + b + 1) - r.tok;
-        if constexpr (RU) {
-            rows = r.T;
-            r.T = __ldg(p.extend_len + b);
+        if constexpr (RU) {  // more new tokens than rows of q and o: a length out of range
+            const int E = __ldg(p.extend_len + b);
+            r.T = E <= r.T ? E : -1;
         }
         r.P = __ldg(p.prefix_len + b);
     }
     r.row = __ldg(p.req_idx + b);
     r.ntiles = r.nqt = r.first = 0;
     if (r.T == 0) return r;
-    if (r.T < 0 || r.T > p.max_tree || (RU && r.T > rows) || r.P < 0 || (int64_t)r.P + r.T > p.rtt_stride) {
+    if (r.T < 0 || r.T > p.max_tree || r.P < 0 || (int64_t)r.P + r.T > p.rtt_stride) {
         if (flag && p.status) atomicOr(p.status, RX_DEV_BAD_LEN);
         return r;
     }
@@ -554,7 +553,16 @@ __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
     const int sub = lane / CPR, ch = lane % CPR;
     const int row_bytes = p.hkv * D * EB;             // at most 2^21 (the heads are bounded)
 
-    struct Tile {
+    // What the calls with rules keep of a tile besides: its first position, what some
+    // row sees, and whether every row sees all of it (see the V note above).  Drafted
+    // trees do without (with the fields, though unused, few-shot trees took 224 us in
+    // place of 219).
+    struct Rest {
+        int at, lo;
+        bool all;
+    };
+    struct None {};
+    struct Tile : std::conditional_t<RU != 0, Rest, None> {
         int32_t slot;  // lane l < ROWS: slot of row r0 + l, in flight until check() looks at it
         int lim;       // positions of the request from the tile's first on; 0: no tile
         int meta;      // kv head, T, segment mod kSegs: bits 0, 13 and 24 on
@@ -563,22 +571,24 @@ __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
         __device__ __forceinline__ int rel() const { return ((meta >> 13) & 0x7FF) - lim; }  // first position, from the first drafted one
         __device__ __forceinline__ int seg() const { return meta >> 24; }
 
-        // with rules: the tile's first position, what some row sees, and whether
-        // every row sees all of it (see the V note above)
-        int at, lo;
-        bool all;
     };
     static_assert(kMaxTree < 2048 && kSegs <= 64, "the fields of meta");
     // the segment being handed out: its next tile, and how many it still has
     int s = -1, left = 0, lim = 0, meta = 0;
     bool last = false;
     const int32_t *slots = nullptr;  // of this lane's row in that tile
-    int at = 0, lo_min = 0, all_from = 0, all_to = 0;  // with rules
+    struct Next {  // with rules: of the segment's next tile
+        int at = 0, lo_min = 0, all_from = 0, all_to = 0;
+    };
+    std::conditional_t<RU != 0, Next, None> next;
     // the next tile, with the loads of its slot ids
     auto take = [&](Tile &t) {
         t.slot = -1;
-        t.lim = t.meta = t.at = t.lo = 0;
-        t.all = true;
+        t.lim = t.meta = 0;
+        if constexpr (RU) {
+            t.at = t.lo = 0;
+            t.all = true;
+        }
         if (left == 0) {
             if (last) return;
             Seg q;
@@ -590,33 +600,43 @@ __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
             ++s;
             if (lane == 0) free_seg<L>(s, sbase);
             left = q.j1 - q.j0;
-            const int from = q.template tile<RU>(q.j0) * kBN;
-            lim = q.P + q.T - from;
-            if constexpr (RU) at = from;
-            lo_min = q.lo_min;
-            all_from = q.lo_max;
-            all_to = q.P + q.node + 1;
+            lim = q.P + q.T - q.template tile<RU>(q.j0) * kBN;
+            if constexpr (RU) {
+                next.at = q.template tile<RU>(q.j0) * kBN;
+                next.lo_min = q.lo_min;
+                next.all_from = q.lo_max;
+                next.all_to = q.P + q.node + 1;
+            }
             meta = q.g | (q.T << 13) | ((s % kSegs) << 24);
             last = q.last;
-            slots = p.rtt + (int64_t)q.row * p.rtt_stride + (int64_t)from + r0 + lane;
+            slots = p.rtt + (int64_t)q.row * p.rtt_stride + (int64_t)q.template tile<RU>(q.j0) * kBN + r0 + lane;
         }
         t.lim = lim;
         t.meta = meta;
         if constexpr (RU) {
-            t.at = at;
-            t.lo = lo_min - at;
-            t.all = at >= all_from && at + kBN <= all_to;
-            at -= kBN;
+            t.at = next.at;
+            t.lo = next.lo_min - next.at;
+            t.all = next.at >= next.all_from && next.at + kBN <= next.all_to;
+            next.at -= kBN;
         }
-        if (lane < ROWS && r0 + lane < lim && (!RU || r0 + lane >= t.lo)) t.slot = rx::ld_stream_b32(slots);
+        bool there = lane < ROWS && r0 + lane < lim;
+        if constexpr (RU) there = there && r0 + lane >= t.lo;
+        if (there) t.slot = rx::ld_stream_b32(slots);
         --left;
-        lim += RU ? kBN : -kBN;
-        slots += RU ? -kBN : kBN;
+        if constexpr (RU) {
+            lim += kBN;
+            slots -= kBN;
+        } else {
+            lim -= kBN;
+            slots += kBN;
+        }
     };
     // slots past the end or outside the pool (flagged) become -1
     auto check = [&](Tile &t) {
         if (t.slot >= 0 && (int64_t)t.slot < p.num_slots) return;
-        if (lane < ROWS && r0 + lane < t.lim && (!RU || r0 + lane >= t.lo) && p.status) atomicOr(p.status, RX_DEV_BAD_SLOT);
+        bool there = lane < ROWS && r0 + lane < t.lim;
+        if constexpr (RU) there = there && r0 + lane >= t.lo;
+        if (there && p.status) atomicOr(p.status, RX_DEV_BAD_SLOT);
         t.slot = -1;
     };
     auto source = [&](const Tile &t, int u, bool &ok) {
@@ -632,10 +652,14 @@ __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
             const int r = r0 + u / CH * RPI + sub, e = t.rel() + r;
             uint4 *at = reinterpret_cast<uint4 *>(smem + off + sw128(r, CH * ch + u % CH, L::BLK));
             uint4 x = *at;
-            if ((RU || e >= 0) && drop_not_finite(x)) {
+            if constexpr (RU) {  // the tile, not the position, is noted: all of them as one
+                if (drop_not_finite(x)) {
+                    *at = x;
+                    atomicOr(reinterpret_cast<uint32_t *>(smem + L::OFF_NF) + t.seg() * 32, 1u);
+                }
+            } else if (e >= 0 && drop_not_finite(x)) {
                 *at = x;
-                // with rules the tile, not the position, is noted: all of them as one
-                atomicOr(reinterpret_cast<uint32_t *>(smem + L::OFF_NF) + t.seg() * 32 + (RU ? 0 : e >> 5), RU ? 1u : 1u << (e & 31));
+                atomicOr(reinterpret_cast<uint32_t *>(smem + L::OFF_NF) + t.seg() * 32 + (e >> 5), 1u << (e & 31));
             }
         }
     };
@@ -656,7 +680,10 @@ __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
                 const unsigned char *src = source(cur, u, ok);
                 rx::cp_async_16(sbase + off + sw128(r0 + u * RPI + sub, ch, L::BLK), src, ok ? 16 : 0);
             }
-            if (IS_V && (RU ? !cur.all : cur.rel() + kBN > 0)) {  // some rows do not see all of the tile
+            bool part = IS_V;  // some rows do not see all of the tile
+            if constexpr (RU) part = part && !cur.all;
+            else part = part && cur.rel() + kBN > 0;
+            if (part) {
                 rx::cp_async_wait_all();
                 scrub(off, cur);
                 rx::fence_proxy_async_smem();
@@ -715,7 +742,10 @@ __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
             fetch(nxt, 1, buf);
             rx::cp_async_wait<2>();     // the second
             widen(off, 1, buf1);
-            if (IS_V && (RU ? !cur.all : cur.rel() + kBN > 0)) scrub(off, cur);  // some rows do not see all of the tile
+            bool part = IS_V;  // some rows do not see all of the tile
+            if constexpr (RU) part = part && !cur.all;
+            else part = part && cur.rel() + kBN > 0;
+            if (part) scrub(off, cur);
             rx::fence_proxy_async_smem();
             rx::mbar_arrive(bar_full + 8 * st);
             check(nx2);
