@@ -791,7 +791,7 @@ __global__ void __launch_bounds__(RU >= rx::kFixedCap ? kRulesThreads : kStaged 
     T.g = blockIdx.y;
     const int tb = kCtaRows / p.G;
     const int E = __ldg(p.extend_len + b);
-    const int64_t row0 = __ldg(p.qo_indptr + b), rows = __ldg(p.qo_indptr + b + 1) - row0;
+    const int row0 = __ldg(p.qo_indptr + b), rows = __ldg(p.qo_indptr + b + 1) - row0;
     // past max_extend_len, or past the request's own rows of q and o (lists that
     // were cut, as rx_step_maps cuts them, would have it read and write behind both)
     if (E > (int)gridDim.x * tb || E > rows) {
@@ -822,7 +822,7 @@ __global__ void __launch_bounds__(RU >= rx::kFixedCap ? kRulesThreads : kStaged 
     }
     T.M = ntok * p.G;
     T.nqt = T.M > kRows ? 2 : 1;
-    T.qbase = row0 + t0;
+    T.qbase = (int64_t)row0 + t0;
     T.row0_pos = (int)(P + t0);
     T.kv_end = (int)(P + t0 + ntok);
     T.first = 0;
