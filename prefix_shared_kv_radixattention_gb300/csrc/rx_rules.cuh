@@ -116,23 +116,26 @@ __device__ __forceinline__ float apply_rules(uint32_t (&sv)[N], const Rules &r, 
     if (KIND == kFixedCap || r.c2 > 0.f) {
         const float ky = fminf(sl2 * r.to_y, 0x1.fffffep127f);
         float a0 = 0.f, a1 = 0.f;
-        // with 64 keys a thread the hidden ones are written over, with 128 passed by
-        // (long chat, a cap of 50, 1,445 us in place of 1,476; 64 tokens on 8,192, a
-        // cap of 30, 103 us in place of 109)
-        if (N <= 64 && masked) hide<0u>(sv, from, to);
-        if (N > 64 && masked) {
+        // hidden scores are written over, or the maximum is taken again over the others
+        // (long chat, a cap of 50, 1,437 us and 1,476; a cap of 60, 1,870 and 1,833; 64 tokens
+        // on 8,192, a cap of 30, with 128 keys a thread, 109 and 102)
+        constexpr bool kOver = KIND == kFixedCap && N <= 64;
+        if (kOver && masked) hide<0u>(sv, from, to);
+#pragma unroll
+        for (int k = 0; k < N / 4; ++k) {
+            a0 = fmax3(a0, fabsf(__uint_as_float(sv[4 * k])), fabsf(__uint_as_float(sv[4 * k + 1])));
+            a1 = fmax3(a1, fabsf(__uint_as_float(sv[4 * k + 2])), fabsf(__uint_as_float(sv[4 * k + 3])));
+        }
+        if (!kOver && masked) {
+            a0 = a1 = 0.f;
 #pragma unroll
             for (int i = 0; i < N / 32; ++i) {
                 const uint32_t seen = among(from - 32 * i, to - 32 * i);
 #pragma unroll
-                for (int k = 0; k < 32; ++k)
+                for (int k = 0; k < 32; k += 2) {
                     if ((seen >> k) & 1u) a0 = fmaxf(a0, fabsf(__uint_as_float(sv[32 * i + k])));
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < N / 4; ++k) {
-                a0 = fmax3(a0, fabsf(__uint_as_float(sv[4 * k])), fabsf(__uint_as_float(sv[4 * k + 1])));
-                a1 = fmax3(a1, fabsf(__uint_as_float(sv[4 * k + 2])), fabsf(__uint_as_float(sv[4 * k + 3])));
+                    if ((seen >> k) & 2u) a1 = fmaxf(a1, fabsf(__uint_as_float(sv[32 * i + k + 1])));
+                }
             }
         }
         const float most = valid ? fmaxf(a0, a1) : 0.f;
