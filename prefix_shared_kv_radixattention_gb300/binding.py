@@ -415,13 +415,13 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream(stream):
+def _stream(stream, device=None):
     if stream is not None:
         return stream.cuda_stream
     # the current stream's handle without the Python object around it, which
     # takes 3 us to make: a sixth of a call on a small batch
     c = _torch()._C
-    return c._cuda_getCurrentRawStream(c._cuda_getDevice())
+    return c._cuda_getCurrentRawStream(c._cuda_getDevice() if device is None else device)
 
 
 def _pool_dims(k_pool, v_pool, layer: int):
@@ -1066,28 +1066,33 @@ def rx_logits_process(rules: LogitsRules, logits, out, dev_status=None, stream=N
 # ---------------------------------------------------------------------------
 
 
-def _here(named):
-    """The launch goes to the current device: its tensors have to be there."""
-    device = _torch()._C._cuda_getDevice()
-    for name, t in named:
-        if t is not None and t.get_device() != device:
-            raise ValueError(f"{name}: must be on the current CUDA device")
+def _current() -> int:
+    """The device that a launch goes to (-2: there is none)."""
+    try:
+        return _torch()._C._cuda_getDevice()
+    except RuntimeError:
+        return -2
 
 
-def _checked(dtype, named):
-    """_dev for several tensors of one type, and that they are on the current
-    device: these calls are made a layer, and a function call a tensor is a fifth
+def _elsewhere(name):
+    return ValueError(f"{name}: must be on the current CUDA device")
+
+
+def _checked(dtype, named, here):
+    """_dev for several tensors of one type, and that they are on the device
+    `here`: these calls are made a layer, and a function call a tensor is a fifth
     of one on a small batch."""
     try:
         for _, t in named:
-            if t is not None and not (t.dtype is dtype and t.is_cuda and t.is_contiguous()):
+            if t is not None and not (t.dtype is dtype and t.get_device() == here and t.is_contiguous()):
                 break
         else:
-            return _here(named)
+            return
     except AttributeError:
         pass
     for name, t in named:
-        _dev(t, dtype, name)
+        if _dev(t, dtype, name) is not None and t.get_device() != here:
+            raise _elsewhere(name)
 
 
 class AttnRules:
@@ -1109,9 +1114,12 @@ class AttnRules:
         self.slopes, self.see_from, self.see_to = slopes, see_from, see_to
         self.struct = AttnRulesStruct(self.cap, self.window, _ptr(slopes), _ptr(see_from), _ptr(see_to))
         self._ref = ctypes.byref(self.struct)
+        self._devices = {t.get_device() for t in (slopes, see_from, see_to) if t is not None}
 
-    def _check(self, tokens: int, heads: int):
-        _here((("slopes", self.slopes), ("see_from", self.see_from), ("see_to", self.see_to)))
+    def _check(self, tokens: int, heads: int, here: int):
+        for device in self._devices:
+            if device != here:
+                raise _elsewhere("AttnRules")
         if self.slopes is not None and self.slopes.numel() != heads:
             raise ValueError("AttnRules: slopes must have an entry for each q head")
         for t in (self.see_from, self.see_to):
@@ -1131,13 +1139,12 @@ def rx_attn_rules_workspace(total_ctx_tokens: int, batch: int, num_q_heads: int,
     return int(n)
 
 
-def _rules_args(q, o, lse, lists, req_to_token, rules, workspace, dev_status, head_dim):
+def _rules_args(q, o, lse, lists, req_to_token, rules, workspace, dev_status, head_dim, here):
     torch = _torch()
-    _checked(torch.bfloat16, (("q", q), ("o", o)))
-    _checked(torch.int32, (*lists, ("req_to_token", req_to_token), ("dev_status", dev_status)))
-    _dev(lse, torch.float32, "lse")
-    _dev(workspace, torch.uint8, "workspace")
-    _here((("lse", lse), ("workspace", workspace)))
+    _checked(torch.bfloat16, (("q", q), ("o", o)), here)
+    _checked(torch.int32, (*lists, ("req_to_token", req_to_token), ("dev_status", dev_status)), here)
+    _checked(torch.float32, (("lse", lse),), here)
+    _checked(torch.uint8, (("workspace", workspace),), here)
     if not isinstance(rules, AttnRules):
         raise TypeError("rules: expected an AttnRules")
     shape = q.shape
@@ -1148,26 +1155,26 @@ def _rules_args(q, o, lse, lists, req_to_token, rules, workspace, dev_status, he
         raise ValueError("lse must be [tokens, num_q_heads]")
     if req_to_token.dim() != 2:
         raise ValueError("req_to_token must be [requests, stride]")
-    return rules._check(n, h), 0 if workspace is None else workspace.numel(), n, h
+    return rules._check(n, h, here), 0 if workspace is None else workspace.numel(), n, h
 
 
-def _bf16_pool(k_pool, v_pool, layer):
-    _checked(_torch().bfloat16, (("k_pool", k_pool), ("v_pool", v_pool)))
+def _bf16_pool(k_pool, v_pool, layer, here):
+    _checked(_torch().bfloat16, (("k_pool", k_pool), ("v_pool", v_pool)), here)
     S, hkv, d, L = _pool_dims(k_pool, v_pool, layer)
     return ctypes.byref(KVPool(k_pool.data_ptr(), v_pool.data_ptr(), S, hkv, d, L, int(layer))), (S, hkv, d, L)
 
 
-def _fp8_pool(k_pool, v_pool, k_scale, v_scale, layer):
-    _checked(_torch().uint8, (("k_pool", k_pool), ("v_pool", v_pool)))
+def _fp8_pool(k_pool, v_pool, k_scale, v_scale, layer, here):
+    _checked(_torch().uint8, (("k_pool", k_pool), ("v_pool", v_pool)), here)
     S, hkv, d, L = _pool_dims(k_pool, v_pool, layer)
     return ctypes.byref(KVPoolFp8(k_pool.data_ptr(), v_pool.data_ptr(), S, hkv, d, float(k_scale), float(v_scale), L,
                                   int(layer))), (S, hkv, d, L)
 
 
-def _extend_rules(call, pool, d, q, o, lse, qo_indptr, req_idx, prefix_len, extend_len, req_to_token, max_extend_len,
+def _extend_rules(call, pool, d, here, q, o, lse, qo_indptr, req_idx, prefix_len, extend_len, req_to_token, max_extend_len,
                   sm_scale, rules, workspace, dev_status, stream):
     ref, ws_bytes, n, h = _rules_args(q, o, lse, (("qo_indptr", qo_indptr), ("req_idx", req_idx), ("prefix_len", prefix_len),
-                                                  ("extend_len", extend_len)), req_to_token, rules, workspace, dev_status, d)
+                                                  ("extend_len", extend_len)), req_to_token, rules, workspace, dev_status, d, here)
     B = req_idx.numel()
     if qo_indptr.numel() != B + 1 or prefix_len.numel() != B or extend_len.numel() != B:
         raise ValueError("qo_indptr must be [batch + 1], prefix_len and extend_len [batch]")
@@ -1175,7 +1182,7 @@ def _extend_rules(call, pool, d, q, o, lse, qo_indptr, req_idx, prefix_len, exte
         return  # empty tensors have no address; there is nothing to do
     rc = call(pool, q.data_ptr(), o.data_ptr(), _ptr(lse), h, qo_indptr.data_ptr(), req_idx.data_ptr(), prefix_len.data_ptr(),
               extend_len.data_ptr(), req_to_token.data_ptr(), req_to_token.shape[1], B, int(max_extend_len), ref, _ptr(workspace),
-              ws_bytes, float(sm_scale), _ptr(dev_status), _stream(stream))
+              ws_bytes, float(sm_scale), _ptr(dev_status), _stream(stream, here))
     if rc:
         _check(rc)
 
@@ -1186,8 +1193,9 @@ def rx_attn_extend_rules(k_pool, v_pool, q, o, lse, qo_indptr, req_idx, prefix_l
     """rx_attn_extend with rules on the scores; workspace: uint8, at least
     rx_attn_rules_workspace(...) bytes.  Without query tokens (no rows of q) or
     requests the call does nothing."""
-    pool, (_, _, d, _) = _bf16_pool(k_pool, v_pool, layer)
-    _extend_rules(_lib.rx_attn_extend_rules, pool, d, q, o, lse, qo_indptr, req_idx, prefix_len, extend_len, req_to_token,
+    here = _current()
+    pool, (_, _, d, _) = _bf16_pool(k_pool, v_pool, layer, here)
+    _extend_rules(_lib.rx_attn_extend_rules, pool, d, here, q, o, lse, qo_indptr, req_idx, prefix_len, extend_len, req_to_token,
                   max_extend_len, sm_scale, rules, workspace, dev_status, stream)
 
 
@@ -1195,21 +1203,22 @@ def rx_attn_extend_rules_fp8(k_pool, v_pool, k_scale: float, v_scale: float, q, 
                              extend_len, req_to_token, max_extend_len: int, sm_scale: float, rules: AttnRules, workspace,
                              dev_status=None, stream=None, layer: int = 0) -> None:
     """rx_attn_extend_rules over uint8 E4M3 pools ([L,] S, Hkv, d) with per-pool scales."""
-    pool, (_, _, d, _) = _fp8_pool(k_pool, v_pool, k_scale, v_scale, layer)
-    _extend_rules(_lib.rx_attn_extend_rules_fp8, pool, d, q, o, lse, qo_indptr, req_idx, prefix_len, extend_len,
+    here = _current()
+    pool, (_, _, d, _) = _fp8_pool(k_pool, v_pool, k_scale, v_scale, layer, here)
+    _extend_rules(_lib.rx_attn_extend_rules_fp8, pool, d, here, q, o, lse, qo_indptr, req_idx, prefix_len, extend_len,
                   req_to_token, max_extend_len, sm_scale, rules, workspace, dev_status, stream)
 
 
-def _decode_rules(call, pool, d, q, o, lse, req_idx, seq_len, req_to_token, sm_scale, rules, workspace, dev_status, stream):
+def _decode_rules(call, pool, d, here, q, o, lse, req_idx, seq_len, req_to_token, sm_scale, rules, workspace, dev_status, stream):
     ref, ws_bytes, n, h = _rules_args(q, o, lse, (("req_idx", req_idx), ("seq_len", seq_len)), req_to_token, rules, workspace,
-                                      dev_status, d)
+                                      dev_status, d, here)
     B = req_idx.numel()
     if n != B or seq_len.numel() != B:
         raise ValueError("q must be [batch, num_q_heads, head_dim] and seq_len [batch]")
     if B == 0:
         return
     rc = call(pool, q.data_ptr(), o.data_ptr(), _ptr(lse), h, req_idx.data_ptr(), seq_len.data_ptr(), req_to_token.data_ptr(),
-              req_to_token.shape[1], B, ref, _ptr(workspace), ws_bytes, float(sm_scale), _ptr(dev_status), _stream(stream))
+              req_to_token.shape[1], B, ref, _ptr(workspace), ws_bytes, float(sm_scale), _ptr(dev_status), _stream(stream, here))
     if rc:
         _check(rc)
 
@@ -1218,8 +1227,9 @@ def rx_attn_decode_rules(k_pool, v_pool, q, o, lse, req_idx, seq_len, req_to_tok
                          workspace, dev_status=None, stream=None, layer: int = 0) -> None:
     """Decode attention (one token a request) with rules on the scores;
     workspace: uint8, at least rx_attn_rules_workspace(0, batch, ...) bytes."""
-    pool, (_, _, d, _) = _bf16_pool(k_pool, v_pool, layer)
-    _decode_rules(_lib.rx_attn_decode_rules, pool, d, q, o, lse, req_idx, seq_len, req_to_token, sm_scale, rules,
+    here = _current()
+    pool, (_, _, d, _) = _bf16_pool(k_pool, v_pool, layer, here)
+    _decode_rules(_lib.rx_attn_decode_rules, pool, d, here, q, o, lse, req_idx, seq_len, req_to_token, sm_scale, rules,
                   workspace, dev_status, stream)
 
 
@@ -1227,8 +1237,9 @@ def rx_attn_decode_rules_fp8(k_pool, v_pool, k_scale: float, v_scale: float, q, 
                              sm_scale: float, rules: AttnRules, workspace, dev_status=None, stream=None,
                              layer: int = 0) -> None:
     """rx_attn_decode_rules over uint8 E4M3 pools ([L,] S, Hkv, d) with per-pool scales."""
-    pool, (_, _, d, _) = _fp8_pool(k_pool, v_pool, k_scale, v_scale, layer)
-    _decode_rules(_lib.rx_attn_decode_rules_fp8, pool, d, q, o, lse, req_idx, seq_len, req_to_token, sm_scale, rules,
+    here = _current()
+    pool, (_, _, d, _) = _fp8_pool(k_pool, v_pool, k_scale, v_scale, layer, here)
+    _decode_rules(_lib.rx_attn_decode_rules_fp8, pool, d, here, q, o, lse, req_idx, seq_len, req_to_token, sm_scale, rules,
                   workspace, dev_status, stream)
 
 
@@ -1246,15 +1257,17 @@ def _pair_axis(pair_axis):
     return axis, address, axis.size
 
 
-def _axes_call(call, pool, dims, q, q_out, k_new, v_new, q_weight, k_weight, slots, pos, pair_axis, base, eps, dev_status,
+def _axes_call(call, pool, dims, here, q, q_out, k_new, v_new, q_weight, k_weight, slots, pos, pair_axis, base, eps, dev_status,
                stream):
     torch = _torch()
     S, hkv, dim, L = dims
     n, hq, d, qs = _head_rows(q, "q")
     new, v_row = _head_rows(k_new, "k_new"), _head_rows(v_new, "v_new")
-    _checked(torch.bfloat16, (("q_out", q_out), ("q_weight", q_weight), ("k_weight", k_weight)))
-    _checked(torch.int32, (("slots", slots), ("pos", pos), ("dev_status", dev_status)))
-    _here((("q", q), ("k_new", k_new), ("v_new", v_new)))
+    _checked(torch.bfloat16, (("q_out", q_out), ("q_weight", q_weight), ("k_weight", k_weight)), here)
+    _checked(torch.int32, (("slots", slots), ("pos", pos), ("dev_status", dev_status)), here)
+    for t, name in ((q, "q"), (k_new, "k_new"), (v_new, "v_new")):
+        if t.get_device() != here:
+            raise _elsewhere(name)
     if new[:3] != (slots.numel(), hkv, dim) or v_row[:3] != new[:3]:
         raise ValueError("k_new/v_new must be [n, num_kv_heads, head_dim] and slots [n]")
     if pos.dim() != 2 or pos.shape[1] != n:
@@ -1271,7 +1284,7 @@ def _axes_call(call, pool, dims, q, q_out, k_new, v_new, q_weight, k_weight, slo
         raise ValueError("pair_axis must have head_dim / 2 entries")
     rc = call(pool, q.data_ptr(), qs, q_out.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), new[3], 0 if eps is None else 1,
               _ptr(q_weight), _ptr(k_weight), slots.data_ptr(), pos.data_ptr(), n, pos.shape[0], axis, n, hq, float(base),
-              0.0 if eps is None else float(eps), _ptr(dev_status), _stream(stream))
+              0.0 if eps is None else float(eps), _ptr(dev_status), _stream(stream, here))
     if rc:
         _check(rc)
 
@@ -1283,8 +1296,9 @@ def rx_qk_rope_axes_store(k_pool, v_pool, q, q_out, k_new, v_new, q_weight, k_we
     host array), after an RMS norm where eps is given (weights bf16 [d] or None),
     q into q_out, K and V into the pool.  q, k_new, v_new as in
     rx_qk_norm_rope_store."""
-    pool, dims = _bf16_pool(k_pool, v_pool, layer)
-    _axes_call(_lib.rx_qk_rope_axes_store, pool, dims, q, q_out, k_new, v_new, q_weight, k_weight, slots, pos,
+    here = _current()
+    pool, dims = _bf16_pool(k_pool, v_pool, layer, here)
+    _axes_call(_lib.rx_qk_rope_axes_store, pool, dims, here, q, q_out, k_new, v_new, q_weight, k_weight, slots, pos,
                pair_axis, base, eps, dev_status, stream)
 
 
@@ -1292,8 +1306,9 @@ def rx_qk_rope_axes_store_fp8(k_pool, v_pool, k_scale: float, v_scale: float, q,
                               slots, pos, pair_axis, base: float, eps: Optional[float] = None, dev_status=None, stream=None,
                               layer: int = 0) -> None:
     """rx_qk_rope_axes_store into uint8 E4M3 pools ([L,] S, Hkv, d) with per-pool scales."""
-    pool, dims = _fp8_pool(k_pool, v_pool, k_scale, v_scale, layer)
-    _axes_call(_lib.rx_qk_rope_axes_store_fp8, pool, dims, q, q_out, k_new, v_new, q_weight,
+    here = _current()
+    pool, dims = _fp8_pool(k_pool, v_pool, k_scale, v_scale, layer, here)
+    _axes_call(_lib.rx_qk_rope_axes_store_fp8, pool, dims, here, q, q_out, k_new, v_new, q_weight,
                k_weight, slots, pos, pair_axis, base, eps, dev_status, stream)
 
 
@@ -1303,9 +1318,10 @@ def rx_step_maps(req_idx, prefix_len, new_len, req_to_token, num_slots: int, qo_
     seq_len int32 [batch] or None, pos and slots int32 [tokens].  pages int32
     [requests, pages] of page_size slots each: slots come from them and are
     written to req_to_token."""
+    here = _current()
     _checked(_torch().int32, (("req_idx", req_idx), ("prefix_len", prefix_len), ("new_len", new_len),
                               ("req_to_token", req_to_token), ("qo_indptr", qo_indptr), ("seq_len", seq_len), ("pos", pos),
-                              ("slots", slots), ("pages", pages), ("dev_status", dev_status)))
+                              ("slots", slots), ("pages", pages), ("dev_status", dev_status)), here)
     B, n = req_idx.numel(), pos.numel()
     if prefix_len.numel() != B or new_len.numel() != B or qo_indptr.numel() != B + 1 or \
             (seq_len is not None and seq_len.numel() != B) or slots.numel() != n:
@@ -1315,6 +1331,6 @@ def rx_step_maps(req_idx, prefix_len, new_len, req_to_token, num_slots: int, qo_
     rc = _lib.rx_step_maps(req_idx.data_ptr(), prefix_len.data_ptr(), new_len.data_ptr(), B, req_to_token.data_ptr(),
                            req_to_token.shape[1], _ptr(pages), 0 if pages is None else pages.shape[1], int(page_size), int(num_slots),
                            qo_indptr.data_ptr(), _ptr(seq_len), pos.data_ptr(), slots.data_ptr(), n, _ptr(dev_status),
-                           _stream(stream))
+                           _stream(stream, here))
     if rc:
         _check(rc)

@@ -23,7 +23,7 @@ def on_device_0(monkeypatch):
     for name in ("rx_attn_extend_rules", "rx_attn_extend_rules_fp8", "rx_attn_decode_rules", "rx_attn_decode_rules_fp8",
                  "rx_qk_rope_axes_store", "rx_qk_rope_axes_store_fp8", "rx_step_maps"):
         monkeypatch.setattr(rx._lib, name, launch)
-    monkeypatch.setattr(rx, "_stream", lambda s: 0)
+    monkeypatch.setattr(rx, "_stream", lambda *a: 0)
     with fake.FakeTensorMode():
         yield Called
 
