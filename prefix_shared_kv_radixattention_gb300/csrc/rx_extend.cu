@@ -38,7 +38,7 @@
 // With rules on the scores (rx_attn_extend_rules, rx_rules.cuh; always staged) a
 // CTA goes over the tiles that its tokens see, and with a cap or a bias two threads
 // share a row (softmax_halves).  16 requests of up to 1,024 tokens on 4,096, 64/8
-// heads of 128: 1,433 us with a cap of 50, 1,392 with ranges alone, 1,325 causal; the
+// heads of 128: 1,427 us with a cap of 50, 1,380 with ranges alone, 1,325 causal; the
 // same bound in all three: a tile's way from S through the softmax to P and back.
 // Every mbarrier wait is bounded in time: a wait that gives up sets
 // RX_DEV_TIMEOUT and raises an abort flag; every role then runs to the common

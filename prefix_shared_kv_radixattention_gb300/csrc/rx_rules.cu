@@ -21,10 +21,10 @@ int go(const TParams &p, const TreePool &pool, cudaStream_t st)
 {
     // one token a request: the products with the positions as their wide side.
     // It takes 16 rows, and a head_dim that fills the tensor core's 128 lanes.
-    // (Long chat, a cap of 50: 255 us, with the rows as the wide side 403; few-shot
-    // with slopes 162, 406.)
+    // (Long chat, a cap of 50: 254 us, with the rows as the wide side 403; few-shot
+    // with slopes 163, 406.)
     // It takes the cap from the exponential and the reciprocal alone (the
-    // polynomials beside them: windowed E4M3 208 us, without 170), whose error grows
+    // polynomials beside them: windowed E4M3 208 us, without 170 then), whose error grows
     // with the cap: up to 150 a log-sum-exp is off by less than 1e-6 of itself.
     if (!p.qo_indptr && p.G <= kKeyRows && pool.D == kRows && p.rules.c2 <= 150.f * rx::kLog2e)
         return p.G <= 8 ? go_keys<8>(p, pool, st) : go_keys<kKeyRows>(p, pool, st);

@@ -555,8 +555,8 @@ __device__ void producer(const TParams &p, unsigned char *smem, uint32_t sbase)
 
     // What the calls with rules keep of a tile besides: its first position, what some
     // row sees, and whether every row sees all of it (see the V note above).  Drafted
-    // trees do without (with the fields, though unused, few-shot trees took 224 us in
-    // place of 219).
+    // trees do without (with the fields, though unused, few-shot trees took 219 us in
+    // place of 215).
     struct Rest {
         int at, lo;
         bool all;
@@ -1305,8 +1305,8 @@ __device__ void softmax_rows(const TParams &p, unsigned char *smem, uint32_t sba
 // thread has one weight a row to form where a row of a 128-row tile is 128
 // weights of one thread, the other 127 rows empty: a tile's softmax takes a few
 // hundred cycles, less than its bytes (64 requests of up to 1,281, 32/32 heads, with
-// slopes: 162 us, 0.92 of the copy rate; 16 of up to 32,768, 64/8, a cap of 50: 255 us,
-// 0.93; over E4M3 pools, 64 with a window of 4,096, 181 us, bound by V's producers).
+// slopes: 163 us, 0.91 of the copy rate; 16 of up to 32,768, 64/8, a cap of 50: 254 us,
+// 0.93; over E4M3 pools, 64 with a window of 4,096, 180 us, bound by V's producers).
 // The weights go to the tensor core through shared memory (P^T is
 // the operand that has to lie there).  All threads hold the rows' running
 // maxima; a tile that has no score 2^8 above them (one vote of the four warps)
