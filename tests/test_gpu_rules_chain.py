@@ -5,7 +5,6 @@ import numpy as np
 import pytest
 
 from oracle import fp8
-from prefix_shared_kv_radixattention_gb300 import inputs
 from tests._chain import BASE, CAP, D, HKV, HQ, PAGE, Chain
 from tests.test_gpu_draft_norm import _check_bf16, _check_codes
 
